@@ -166,7 +166,7 @@ def prepare(case, seed):
     B, Hk, Hv, dk, dv = (case[n] for n in ("B", "Hk", "Hv", "dk", "dv"))
     s["factor"] = dk ** -0.5
     if case["op"] == "step":
-        q, k, v, g, beta = _rule_values(case, (B, Hk, dk), (B, Hk and Hv, dv), (B, Hv), r)
+        q, k, v, g, beta = _rule_values(case, (B, Hk, dk), (B, Hv, dv), (B, Hv), r)
         s.update(q=q, k=k, v=v, g=g, beta=beta)
         s["S"] = 0.3 * r((case["pool"], Hv, dv, dk))
         order = torch.randperm(case["pool"], generator=gen, device=DEV)[:B]
