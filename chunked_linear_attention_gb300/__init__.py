@@ -34,7 +34,8 @@ EXPORTED = (
     "ttt_set_wait_limit_ns", "ttt_selftest_gemm", "ttt_launch_count", "ttt_profile_start",
     "ttt_profile_stop", "linattn_chunked_forward_noalloc", "ttt_layer_host_workspace_size",
     "ttt_layer_forward_host", "ttt_selftest_withhold_release", "linattn_rule_workspace_size",
-    "linattn_chunked_forward_rule",
+    "linattn_chunked_forward_rule", "delta_rule_workspace_size", "delta_rule_chunked_forward",
+    "delta_rule_step", "block_norm_forward",
 )
 
 
@@ -51,6 +52,11 @@ FORM_RECURRENT = 1
 FORM_PARALLEL = 2
 
 
+GATE_NONE = 0
+GATE_SILU = 1
+GATE_SIGMOID = 2
+
+
 class UpdateRule(ctypes.Structure):
     """Mirror of ``ttt_update_rule``."""
     _fields_ = [("l2norm", ctypes.c_int), ("muon_steps", ctypes.c_int),
@@ -65,6 +71,18 @@ class LinattnRule(ctypes.Structure):
     _fields_ = [("alpha", ctypes.c_void_p), ("lr", ctypes.c_void_p), ("M0", ctypes.c_void_p),
                 ("M_final", ctypes.c_void_p), ("muon_steps", ctypes.c_int),
                 ("ns_a", ctypes.c_float), ("ns_b", ctypes.c_float), ("ns_c", ctypes.c_float)]
+
+
+class DeltaRuleLayout(ctypes.Structure):
+    """Mirror of ``delta_rule_layout``: (batch, head, token) strides of q, k, v, g, beta, out."""
+    _fields_ = [("strides", ctypes.c_longlong * 18)]
+
+
+class BlockNormStrides(ctypes.Structure):
+    """Mirror of ``block_norm_strides``."""
+    _fields_ = [("y", ctypes.c_longlong), ("gate", ctypes.c_longlong),
+                ("residual", ctypes.c_longlong), ("out", ctypes.c_longlong),
+                ("h", ctypes.c_longlong)]
 
 
 def update_rule(l2norm=True, muon_steps=0, momentum_beta=0.0, ns_coef=MUON_COEF,
@@ -119,6 +137,18 @@ def _declare(lib):
     lib.linattn_chunked_forward_noalloc.restype = i
     lib.linattn_chunked_forward_noalloc.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i,
                                                     vp, vp, vp, vp]
+    f32, ll = ctypes.c_float, ctypes.c_longlong
+    lib.delta_rule_workspace_size.restype = sz
+    lib.delta_rule_workspace_size.argtypes = [i] * 8
+    lib.delta_rule_chunked_forward.restype = i
+    lib.delta_rule_chunked_forward.argtypes = [vp] * 7 + [i] * 8 + [
+        f32, ctypes.POINTER(DeltaRuleLayout), vp, vp, vp, sz, vp]
+    lib.delta_rule_step.restype = i
+    lib.delta_rule_step.argtypes = [vp] * 7 + [i] * 7 + [
+        f32, ctypes.POINTER(DeltaRuleLayout), vp, vp]
+    lib.block_norm_forward.restype = i
+    lib.block_norm_forward.argtypes = [vp] * 6 + [ll] + [i] * 5 + [
+        f32, ctypes.POINTER(BlockNormStrides), vp, vp, vp]
     lib.ttt_selftest_withhold_release.restype = None
     lib.ttt_selftest_withhold_release.argtypes = [i]
     lib.ttt_launch_count.restype = ctypes.c_ulonglong
@@ -405,6 +435,246 @@ def linattn_chunked_forward_noalloc(q, k, v, eta, chunk: int, mask_mode: int,
     del keep
     _check(rc, "linattn_chunked_forward_noalloc")
     return out, S_final
+
+
+def _shape(t, shape, what):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _same(t, dtype, dev, what):
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{what} must be on {dev}, got {t.device}")
+
+
+def _last_contiguous(t, what):
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what} must be contiguous in its last dimension")
+
+
+class _On:
+    """Makes `dev` current, and `stream` when one is given (so that outputs and
+    workspace belong to the stream that uses them); gives the stream's handle."""
+
+    def __init__(self, dev, stream):
+        if dev.type != "cuda":
+            raise ValueError("tensors passed to the CUDA path must be on a CUDA device")
+        self.dev, self.stream, self.inner = dev, stream, None
+
+    def __enter__(self):
+        if self.stream is not None:
+            self.inner = torch.cuda.stream(self.stream)
+        elif self.dev.index != torch.cuda.current_device():
+            self.inner = torch.cuda.device(self.dev)
+        if self.inner is not None:
+            self.inner.__enter__()
+        s = torch.cuda.current_stream(self.dev) if self.stream is None else self.stream
+        return ctypes.c_void_p(s.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.inner is not None:
+            self.inner.__exit__(*exc)
+
+
+def _rule_heads(q, k, v, g, beta, tokens):
+    """Checks the inputs of a delta-rule call; tokens: () or (N,)."""
+    B, Hk, dk = q.shape[0], q.shape[1], q.shape[-1]
+    Hv, dv = v.shape[1], v.shape[-1]
+    _shape(q, (B, Hk) + tokens + (dk,), "q")
+    _shape(k, (B, Hk) + tokens + (dk,), "k")
+    _shape(v, (B, Hv) + tokens + (dv,), "v")
+    for t, what in ((g, "g"), (beta, "beta")):
+        _shape(t, (B, Hv) + tokens, what)
+        _same(t, torch.float32, q.device, what)
+    for t, what in ((k, "k"), (v, "v")):
+        _same(t, q.dtype, q.device, what)
+    for t, what in ((q, "q"), (k, "k"), (v, "v")):
+        _last_contiguous(t, what)
+    return B, Hk, Hv, dk, dv
+
+
+def delta_rule_workspace_size(B, Hk, Hv, N, d_k, d_v, n_seq, io_dtype) -> int:
+    return library().delta_rule_workspace_size(B, Hk, Hv, N, d_k, d_v, n_seq, io_dtype)
+
+
+def delta_rule_chunked_forward(q, k, v, g, beta, S0: Optional[torch.Tensor] = None,
+                               seq_starts: Optional[torch.Tensor] = None,
+                               scale: Optional[float] = None,
+                               out: Optional[torch.Tensor] = None,
+                               S_final: Optional[torch.Tensor] = None,
+                               workspace: Optional[torch.Tensor] = None, stream=None):
+    """The gated delta rule over whole sequences (see
+    ``delta_rule_chunked_forward`` in include/ttt_delta.h).
+
+    q, k [B, Hk, N, d_k] and v [B, Hv, N, d_v], bf16 or fp32, any strides with
+    the last dimension contiguous; g (log decay), beta [B, Hv, N] fp32.
+    seq_starts: int32 [n_seq + 1] on the same device for sequences packed
+    along the token axis (B = 1).  scale: d_k ** -0.5 when None.  S0 and
+    S_final [n_seq or B, Hv, d_v, d_k] fp32.  Without ``out``, the outputs are
+    stored in v's order of dimensions.  Returns (out [B, Hv, N, d_v], S_final).
+    """
+    lib = library()
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q and v must have four dimensions")
+    N = q.shape[2]
+    B, Hk, Hv, dk, dv = _rule_heads(q, k, v, g, beta, (N,))
+    io, dev = _io_dtype(q), q.device
+    n_seq = B
+    if seq_starts is not None:
+        _same(seq_starts, torch.int32, dev, "seq_starts")
+        if seq_starts.dim() != 1 or seq_starts.numel() < 2 or not seq_starts.is_contiguous():
+            raise ValueError("seq_starts must be a contiguous vector of n_seq + 1 entries")
+        if B != 1:
+            raise ValueError("seq_starts needs B = 1")
+        n_seq = seq_starts.numel() - 1
+    state = (n_seq, Hv, dv, dk)
+    with _On(dev, stream) as handle:
+        if out is None:
+            out = torch.empty_like(v)   # v's strides where they are dense, else row-major
+        else:
+            _shape(out, (B, Hv, N, dv), "out")
+            _same(out, q.dtype, dev, "out")
+            _last_contiguous(out, "out")
+        if S_final is None:
+            S_final = torch.empty(state, device=dev, dtype=torch.float32)
+        for t, what in ((S0, "S0"), (S_final, "S_final")):
+            if t is not None:
+                _shape(t, state, what)
+                _same(t, torch.float32, dev, what)
+        need = lib.delta_rule_workspace_size(B, Hk, Hv, N, dk, dv, n_seq, io)
+        if workspace is None:
+            workspace = torch.empty(max(need, 256), device=dev, dtype=torch.uint8)
+        elif workspace.device != dev:
+            raise ValueError(f"workspace must be on {dev}")
+        lay = DeltaRuleLayout((ctypes.c_longlong * 18)(
+            *q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *g.stride(), *beta.stride(),
+            *out.stride()[:3]))
+        rc = lib.delta_rule_chunked_forward(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(S0),
+            None if seq_starts is None else seq_starts.data_ptr(), n_seq, B, Hk, Hv, N, dk, dv, io,
+            dk ** -0.5 if scale is None else float(scale), ctypes.byref(lay), out.data_ptr(),
+            _ptr(S_final), _ptr(workspace), workspace.numel() * workspace.element_size(), handle)
+    _check(rc, "delta_rule_chunked_forward")
+    return out, S_final
+
+
+def delta_rule_step(q, k, v, g, beta, state, slots: Optional[torch.Tensor] = None,
+                    scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                    stream=None):
+    """The gated delta rule for one token of each of B sequences, on a pool of
+    states that is updated in place (see ``delta_rule_step`` in
+    include/ttt_delta.h).
+
+    q, k [B, Hk, d_k], v [B, Hv, d_v], bf16 or fp32, last dimension
+    contiguous; g, beta [B, Hv] fp32; state [n_slots, Hv, d_v, d_k] fp32;
+    slots int32 [B] (negative: an idle row) or None.  Returns out [B, Hv, d_v].
+    """
+    lib = library()
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q and v must have three dimensions")
+    B, Hk, Hv, dk, dv = _rule_heads(q, k, v, g, beta, ())
+    io, dev = _io_dtype(q), q.device
+    _same(state, torch.float32, dev, "state")
+    if state.dim() != 4:
+        raise ValueError("state must have four dimensions")
+    _shape(state, (state.shape[0], Hv, dv, dk), "state")
+    if slots is not None:
+        _same(slots, torch.int32, dev, "slots")
+        _shape(slots, (B,), "slots")
+        if not slots.is_contiguous():
+            raise ValueError("slots must be contiguous")
+    with _On(dev, stream) as handle:
+        if out is None:
+            out = torch.empty((B, Hv, dv), device=dev, dtype=q.dtype)
+        else:
+            _shape(out, (B, Hv, dv), "out")
+            _same(out, q.dtype, dev, "out")
+            _last_contiguous(out, "out")
+        lay = DeltaRuleLayout((ctypes.c_longlong * 18)(
+            *q.stride()[:2], 0, *k.stride()[:2], 0, *v.stride()[:2], 0, *g.stride(), 0,
+            *beta.stride(), 0, *out.stride()[:2], 0))
+        rc = lib.delta_rule_step(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(state),
+            None if slots is None else slots.data_ptr(), state.shape[0], B, Hk, Hv, dk, dv, io,
+            dk ** -0.5 if scale is None else float(scale), ctypes.byref(lay), out.data_ptr(),
+            handle)
+    _check(rc, "delta_rule_step")
+    return out
+
+
+def _rows(t, rows, D, what):
+    """Row stride of a [..., D] tensor whose leading dimensions run on as one."""
+    if t.shape[-1] != D or t.numel() != rows * D:
+        raise ValueError(f"{what} must hold {rows} rows of {D}, got shape {tuple(t.shape)}")
+    _last_contiguous(t, what)
+    if t.is_contiguous():
+        return D
+    stride, size = None, 1
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != stride * size:
+            raise ValueError(f"the rows of {what} must be equally far apart")
+        size *= n
+    return D if stride is None else stride
+
+
+def block_norm_forward(y, w: Optional[torch.Tensor] = None,
+                       gate: Optional[torch.Tensor] = None, gate_act: int = GATE_NONE,
+                       residual: Optional[torch.Tensor] = None,
+                       scale: Optional[torch.Tensor] = None,
+                       w_next: Optional[torch.Tensor] = None, group: Optional[int] = None,
+                       eps: float = 1e-6, out_dtype: Optional[torch.dtype] = None,
+                       out: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                       stream=None):
+    """The norms around a block with its gate, residual scale and residual sum
+    (see ``block_norm_forward`` in include/ttt_delta.h).
+
+    y, gate [..., D] bf16 or fp32; residual [..., D] and out in ``out_dtype``
+    (residual's type, or y's); w [group] (its length sets the group), scale
+    and w_next [D] fp32.  Returns (out, h); h is None without ``w_next``.
+    """
+    lib = library()
+    dev, D = y.device, y.shape[-1]
+    io = _io_dtype(y)
+    if D == 0 or y.numel() == 0:
+        raise ValueError("y must not be empty")
+    rows = y.numel() // D
+    if out_dtype is None:
+        out_dtype = (residual if residual is not None else out if out is not None else y).dtype
+    if group is None:
+        group = D if w is None else w.numel()
+    for t, n, what in ((w, group, "w"), (scale, D, "scale"), (w_next, D, "w_next")):
+        if t is not None:
+            _same(t, torch.float32, dev, what)
+            _shape(t, (n,), what)
+    with _On(dev, stream) as handle:
+        if out is None:
+            out = torch.empty(y.shape, device=dev, dtype=out_dtype)
+        if w_next is None:
+            if h is not None:
+                raise ValueError("h needs w_next")
+        elif h is None:
+            h = torch.empty(y.shape, device=dev, dtype=y.dtype)
+        st = [0, 0, 0, 0, 0]
+        for i, (t, dt, what) in enumerate(((y, y.dtype, "y"), (gate, y.dtype, "gate"),
+                                           (residual, out_dtype, "residual"),
+                                           (out, out_dtype, "out"), (h, y.dtype, "h"))):
+            if t is not None:
+                _same(t, dt, dev, what)
+                st[i] = _rows(t, rows, D, what)
+        rc = lib.block_norm_forward(
+            y.data_ptr(), _ptr(w), None if gate is None else gate.data_ptr(),
+            None if residual is None else residual.data_ptr(), _ptr(scale), _ptr(w_next), rows, D,
+            group, io, _io_dtype(out), int(gate_act), float(eps),
+            ctypes.byref(BlockNormStrides(*st)), out.data_ptr(),
+            None if h is None else h.data_ptr(), handle)
+    _check(rc, "block_norm_forward")
+    return out, h
 
 
 def device_status(stream=None) -> int:

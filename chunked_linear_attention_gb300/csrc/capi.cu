@@ -6,6 +6,7 @@
 
 #include "ttt.h"
 #include "ttt_selftest.h"
+#include "capi_util.h"
 #include "layer.h"
 #include "linattn_fused.h"
 
@@ -138,6 +139,11 @@ bool host_pinned(const void* p) {
 }
 
 }  // namespace
+
+namespace ttt {
+int* capi_status_ptr() { return status_ptr(); }
+unsigned long long capi_wait_limit_ns() { return g_wait_limit_ns; }
+}  // namespace ttt
 
 extern "C" {
 
