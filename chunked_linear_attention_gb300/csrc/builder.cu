@@ -55,6 +55,18 @@ bool MapCache::get(const TensorRef& t, int box_rows, CUtensorMap* out) {
   return true;
 }
 
+bool encode_bf16_4d(CUtensorMap* out, const void* ptr, const unsigned long long (&dims)[4],
+                    const unsigned long long (&strides)[3], const unsigned (&box)[4]) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+  const cuuint64_t st[3] = {strides[0], strides[1], strides[2]};
+  const cuuint32_t bx[4] = {box[0], box[1], box[2], box[3]}, es[4] = {1, 1, 1, 1};
+  return fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), d, st, bx, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool MapCache::get_blocked(const TensorRef& t, int box_rows, int nblk, CUtensorMap* out) {
   for (const Entry& e : entries_)
     if (e.ptr == t.ptr && e.bf16 == t.bf16 && e.rows == t.rows && e.inner == t.inner &&

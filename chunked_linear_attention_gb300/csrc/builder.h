@@ -44,6 +44,11 @@ class MapCache {
   std::vector<Entry> entries_;
 };
 
+// TMA map of a 4-D bf16 tensor (innermost dimension contiguous; `strides`: the
+// other dimensions', in bytes) with boxes one 128-byte swizzle row wide.
+bool encode_bf16_4d(CUtensorMap* out, const void* ptr, const unsigned long long (&dims)[4],
+                    const unsigned long long (&strides)[3], const unsigned (&box)[4]);
+
 class LaunchBuilder {
  public:
   LaunchBuilder(bool tensor_cores, MapCache* cache, int* status, unsigned long long wait_ns);

@@ -88,7 +88,8 @@ int delta_rule_chunked_forward(const void* q, const void* k, const void* v, cons
   a.status = st;
   a.wait_ns = ttt::capi_wait_limit_ns();
   a.stream = reinterpret_cast<cudaStream_t>(stream);
-  return ttt::delta_rule_recurrent(a);
+  rc = ttt::delta_rule_chunk_launch(a);
+  return rc == 1 ? ttt::delta_rule_recurrent(a) : rc;
 }
 
 int delta_rule_step(const void* q, const void* k, const void* v, const float* g,

@@ -48,6 +48,10 @@ struct DeltaStepArgs {
 // Token by token in fp32: every type, size and stride.  Returns a ttt_status.
 int delta_rule_recurrent(const DeltaArgs& a);
 
+// Chunks of 64 tokens on the tensor cores (bf16, d_k <= 128, aligned strides).
+// Returns 1 where it does not apply, else a ttt_status.
+int delta_rule_chunk_launch(const DeltaArgs& a);
+
 int delta_rule_step_launch(const DeltaStepArgs& a);
 
 struct BlockNormArgs {

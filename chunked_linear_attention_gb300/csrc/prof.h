@@ -25,6 +25,7 @@ enum ProfTag : int {
   PT_APPLY_PROJ,
   PT_APPLY_OUT,
   PT_FEATURIZE,
+  PT_DELTA_CHUNK,
   PT_DELTA_RECURRENT,
   PT_DELTA_STEP,
   PT_BLOCK_NORM,
