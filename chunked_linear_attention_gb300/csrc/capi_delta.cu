@@ -47,7 +47,9 @@ extern "C" {
 size_t delta_rule_workspace_size(int B, int Hk, int Hv, int N, int d_k, int d_v, int n_seq,
                                  int io_dtype) {
   if (check_rule(B, Hk, Hv, N, d_k, d_v, n_seq, io_dtype) != TTT_OK) return 0;
-  return 256;
+  const size_t need =
+      io_dtype == TTT_BF16 ? ttt::delta_rule_chunk_workspace(B, Hv, N, d_k, d_v, n_seq) : 0;
+  return need < 256 ? 256 : need;
 }
 
 int delta_rule_chunked_forward(const void* q, const void* k, const void* v, const float* g,

@@ -1,0 +1,154 @@
+// What the tensor-core kernels of the gated delta rule share: the records that
+// one writes and the other reads, and small device helpers.
+#pragma once
+
+#include <cuda.h>
+
+#include "common.cuh"
+#include "delta_rule.h"
+
+namespace ttt {
+
+constexpr int kC = 64;       // tokens per chunk
+constexpr int kBlk = 8192;   // 64 rows of 64 bf16, 128-byte swizzled
+
+// Record of one (chunk, value head): four 64 x 64 bf16 tiles as the MMAs read
+// them (rows i, columns j, 128-byte swizzled): T diag(beta) hi and lo,
+// scale D o Q K^T hi and lo.
+constexpr int kRecBytes = 4 * kBlk;
+
+struct RecScal {
+  float neg[kC];   // -exp(G_i)
+  float er[kC];    // exp(G_63 - G_j)
+  float eall;      // exp(G_63)
+  float pad[3];
+};
+static_assert(sizeof(RecScal) % 16 == 0, "bulk copies move 16 bytes");
+
+// Token range of a sequence, and the number of its first chunk's records.  For
+// packed sequences both come from a plan that one block makes beforehand.
+struct SeqPlan {
+  int t0, len, chunk0, pad;
+};
+
+// Segment j of n of a sequence: the chunks that one CTA walks (seq < 0: no
+// segment at this place).
+struct SegPlan {
+  int seq, j, n, pad;
+};
+
+__host__ __device__ __forceinline__ int n_chunks(int len) { return (len + kC - 1) / kC; }
+
+__device__ __forceinline__ SeqPlan seq_plan(const SeqPlan* plan, int seq, int N) {
+  if (plan) return plan[seq];
+  SeqPlan s;
+  s.t0 = 0;
+  s.len = N;
+  s.chunk0 = seq * n_chunks(N);
+  s.pad = 0;
+  return s;
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                            int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}"
+               : "=r"(r));
+  return r != 0;
+}
+
+// Bounded wait of a whole warp; after one that ran out (ok false) the caller's
+// waits return at once, and it runs to its end.
+__device__ __forceinline__ void wait_w(bool& ok, uint64_t* bar, uint32_t parity, int* status,
+                                       unsigned long long lim) {
+  if (!ok || __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
+  unsigned long long since = 0;
+  while (!__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, 1000000u))) {
+    const unsigned long long now = global_ns();
+    if (since == 0) since = now;
+    if (__any_sync(0xffffffffu, now - since > lim)) {
+      report_status(status, kStatusTimeout);
+      ok = false;
+      return;
+    }
+  }
+}
+
+// Two fp32 values in one 64-bit register, for the packed fp32 instructions.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pack2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(F2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) {
+  F2 r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// (a, b) as a pair of packed bf16 pairs: a ~ hi.x + lo.x, b ~ hi.y + lo.y, each
+// off by at most 2^-17 of its value.
+__device__ __forceinline__ void split2(F2 v, uint32_t& hi, uint32_t& lo) {
+  float a, b;
+  unpack2(v, a, b);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  const F2 r = sub2(v, pack2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)));
+  unpack2(r, a, b);
+  const __nv_bfloat162 l = __floats2bfloat162_rn(a, b);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ---------------------------------------------------------------- host side
+// [B, H, N, d] bf16 with the given strides as a map of 64 x 64 boxes; false
+// where TMA cannot take it.
+bool delta_map(CUtensorMap* m, const void* ptr, const delta_rule_stride& s, int B, int H, int N,
+               int d);
+
+struct PrepParams {
+  CUtensorMap q, k;
+  const float* g;
+  const float* beta;
+  const SeqPlan* plan;     // or NULL
+  int n_seq;
+  int Hk, Hv, N;
+  delta_rule_stride sg, sb;
+  float scale;
+  uint8_t* rec;            // [chunk][Hv] records
+  RecScal* scal;           // [chunk][Hv]
+  int* status;
+  unsigned long long wait_ns;
+};
+
+// The records of every chunk; `chunks` is the number of chunk places.
+cudaError_t launch_delta_prep(const PrepParams& p, int chunks, cudaStream_t stream);
+
+}  // namespace ttt

@@ -25,13 +25,14 @@ const char* kTagName[PT_COUNT] = {
     "init", "gemm.proj", "gemm.grad", "gemm.ns_gram", "gemm.ns_poly", "gemm.ns_step",
     "norm", "lin.scale", "gemm.lin_partial", "lin.prefix", "gemm.lin_out", "gemm.selftest", "muon.cluster",
     "muon.half", "lin.fused", "gemm.apply_proj", "gemm.apply_out", "gemm.featurize",
-    "delta.chunk", "delta.recurrent", "delta.step", "block.norm"};
+    "delta.plan", "delta.prep", "delta.carry", "delta.join", "delta.chunk", "delta.recurrent", "delta.step", "block.norm"};
 const char* kTagKernel[PT_COUNT] = {
     "init_layer_kernel", "umma_gemm_kernel", "umma_gemm_kernel", "umma_gemm_kernel",
     "umma_gemm_kernel", "umma_gemm_kernel", "update_normalize_kernel", "scale_rows_kernel",
     "umma_gemm_kernel", "linattn_prefix_kernel", "umma_gemm_kernel", "umma_gemm_kernel",
     "ns_cluster_kernel", "ns_half_kernel", "linattn_fused_kernel",
-    "umma_gemm_kernel", "umma_gemm_kernel", "umma_gemm_kernel", "delta_chunk_kernel",
+    "umma_gemm_kernel", "umma_gemm_kernel", "umma_gemm_kernel", "delta_plan_kernel",
+    "delta_prep_kernel", "delta_scan_kernel", "delta_join_kernel", "delta_scan_kernel",
     "delta_recurrent_kernel", "delta_step_kernel", "block_norm_kernel"};
 
 }  // namespace

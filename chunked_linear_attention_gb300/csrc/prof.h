@@ -25,6 +25,10 @@ enum ProfTag : int {
   PT_APPLY_PROJ,
   PT_APPLY_OUT,
   PT_FEATURIZE,
+  PT_DELTA_PLAN,
+  PT_DELTA_PREP,
+  PT_DELTA_CARRY,
+  PT_DELTA_JOIN,
   PT_DELTA_CHUNK,
   PT_DELTA_RECURRENT,
   PT_DELTA_STEP,
