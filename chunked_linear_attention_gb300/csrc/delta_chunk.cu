@@ -24,13 +24,15 @@
 // v = 0) are computed for all segments at once, the start states follow by
 // S_{j+1} = S_j P_j + L_j, and all segments run at once.
 //
-// Roles (512 threads, one CTA per SM, persistent over (segment, head, d_v tile)):
+// Roles (768 threads, one CTA per SM, persistent over (segment, head, d_v tile)):
 //   warp 0      TMA: q, k, v in three stages, the chunk's records in two.
 //   warp 1      all MMAs.
 //   warp 2      zeroes the rows behind a sequence's end, so that other
 //               sequences' values cannot reach it.
-//   warps 4-11  the chain S -> K S^T -> X -> S.
-//   warps 12-15 the outputs.
+//   warps 4-19  the chain S -> K S^T -> X -> S: warp w has rows 32 (w % 4) .. and a
+//               quarter of the columns (conversions are bound by instruction
+//               latency with fewer warps).
+//   warps 20-23 the outputs.
 #include <mutex>
 
 #include "builder.h"
@@ -52,8 +54,9 @@ struct Bars {
   uint32_t tmem;
 };
 
+constexpr int kOutBytes = 4 * 64 * 64;
 constexpr int kSmem = kStages * kStageBytes + 2 * kRecBytes + 2 * (int)sizeof(RecScal) +
-                      (int)sizeof(Bars) + 1024;
+                      kOutBytes + (int)sizeof(Bars) + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 // TMEM columns
@@ -83,6 +86,7 @@ struct ScanParams {
   int Hk, Hv, N, dk, dv, tiles, items;
   int seg_chunks, seg_n;   // chunks per segment; segments per sequence (not packed)
   float scale;
+  int wide_out;            // rows of out can be stored 16 bytes at a time
 };
 
 struct Item {
@@ -163,48 +167,64 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// 32 tokens' values of a row, each times f[token], as pairs at TMEM columns taddr
-// (16 of hi, 16 of lo).
-__device__ __forceinline__ void put_scaled(uint32_t taddr, const float (&x)[32], const float* f) {
+// 16 tokens' values of a row, each times f[token], as pairs at TMEM columns taddr
+// (8 of hi, 8 of lo: the operand of one MMA each).
+__device__ __forceinline__ void put_scaled(uint32_t taddr, const float (&x)[16], const float* f) {
+  uint32_t hi[8], lo[8];
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    uint32_t hi[8], lo[8];
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(f + 16 * b + 2 * e);
-      const int c = 16 * b + 2 * e;
-      split2(mul2(w.x, pack2(x[c], x[c + 1])), hi[e], lo[e]);
-      split2(mul2(w.y, pack2(x[c + 2], x[c + 3])), hi[e + 1], lo[e + 1]);
-    }
-    tmem_st8(taddr + 8 * b, hi);
-    tmem_st8(taddr + 16 + 8 * b, lo);
+  for (int e = 0; e < 8; e += 2) {
+    const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(f + 2 * e);
+    split2(mul2(w.x, pack2(x[2 * e], x[2 * e + 1])), hi[e], lo[e]);
+    split2(mul2(w.y, pack2(x[2 * e + 2], x[2 * e + 3])), hi[e + 1], lo[e + 1]);
   }
+  tmem_st8(taddr, hi);
+  tmem_st8(taddr + 8, lo);
 }
 
 // The same without a factor.
-__device__ __forceinline__ void put_pairs(uint32_t taddr, const float (&x)[32]) {
+__device__ __forceinline__ void put_pairs(uint32_t taddr, const float (&x)[16]) {
+  uint32_t hi[8], lo[8];
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    uint32_t hi[8], lo[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      split2(pack2(x[16 * b + 2 * e], x[16 * b + 2 * e + 1]), hi[e], lo[e]);
-    tmem_st8(taddr + 8 * b, hi);
-    tmem_st8(taddr + 16 + 8 * b, lo);
-  }
+  for (int e = 0; e < 8; ++e) split2(pack2(x[2 * e], x[2 * e + 1]), hi[e], lo[e]);
+  tmem_st8(taddr, hi);
+  tmem_st8(taddr + 8, lo);
+}
+
+// 16 TMEM lanes by 16 columns: v[4 b + 2 r + c] is lane lane / 4 + 8 r, column
+// 8 b + 2 (lane % 4) + c.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                 "=f"(v[6]), "=f"(v[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_frag(float (&v)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                 "+f"(v[6]), "+f"(v[7])
+               :
+               : "memory");
+}
+// Four 8 x 8 matrices of 16-bit elements, stored transposed; lane i gives the
+// address of row i % 8 (of the stored form) of matrix i / 8.
+__device__ __forceinline__ void stmatrix4_t(uint32_t saddr, const uint32_t (&w)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr),
+               "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+               : "memory");
 }
 
 // ---------------------------------------------------------------- the kernel
 // CARRY: the end states L and P of the segments, without outputs.
 template <bool CARRY>
-__global__ void __launch_bounds__(CARRY ? 384 : 512, 1)
+__global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
     delta_scan_kernel(const __grid_constant__ ScanParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* rec = smem + kStages * kStageBytes;
   RecScal* scal = reinterpret_cast<RecScal*>(rec + 2 * kRecBytes);
-  Bars* B = reinterpret_cast<Bars*>(scal + 2);
+  uint8_t* obuf = reinterpret_cast<uint8_t*>(scal + 2);   // outputs on their way
+  Bars* B = reinterpret_cast<Bars*>(obuf + kOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -215,15 +235,15 @@ __global__ void __launch_bounds__(CARRY ? 384 : 512, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&B->rec_full[b], 1);
-      mbar_init(&B->rec_free[b], 1 + 8 + (CARRY ? 0 : 4));
+      mbar_init(&B->rec_free[b], 1 + 16 + (CARRY ? 0 : 4));
     }
     mbar_init(&B->ks_full, 1);
-    mbar_init(&B->y_ready, 8);
+    mbar_init(&B->y_ready, 16);
     mbar_init(&B->x_full, 1);
-    mbar_init(&B->xs_ready, 8);
+    mbar_init(&B->xs_ready, 16);
     mbar_init(&B->ds_full, 1);
-    mbar_init(&B->x_ready, 8);
-    mbar_init(&B->s_ready, 8);
+    mbar_init(&B->x_ready, 16);
+    mbar_init(&B->s_ready, 16);
     mbar_init(&B->o_full, 1);
     mbar_init(&B->o_free, 4);
     fence_mbar_init();
@@ -241,7 +261,7 @@ __global__ void __launch_bounds__(CARRY ? 384 : 512, 1)
   };
 
   if (warp < 4) {
-    regs_dec<64>();
+    regs_dec<CARRY ? 64 : 56>();
     if (warp == 0) {
       int n = 0;
       for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
@@ -331,8 +351,8 @@ __global__ void __launch_bounds__(CARRY ? 384 : 512, 1)
           if (el) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t y = tmem + kKS + (k >> 1) * 32 + (k & 1) * 8;
-              umma_ts(tmem + kX, y + 16, th + k * 2, id64, has_v || k != 0);
+              const uint32_t y = tmem + kKS + k * 16;
+              umma_ts(tmem + kX, y + 8, th + k * 2, id64, has_v || k != 0);
               umma_ts(tmem + kX, y, tl + k * 2, id64, 1);
               umma_ts(tmem + kX, y, th + k * 2, id64, 1);
             }
@@ -359,8 +379,8 @@ __global__ void __launch_bounds__(CARRY ? 384 : 512, 1)
             const uint64_t km = smem_desc_sw128(st + kBlk, 2 * kBlk, 1024);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t x = tmem + kX + (k >> 1) * 32 + (k & 1) * 8;
-              umma_ts(tmem + kDS, x + 16, km + k * 128, id128, k != 0);
+              const uint32_t x = tmem + kX + k * 16;
+              umma_ts(tmem + kDS, x + 8, km + k * 128, id128, k != 0);
               umma_ts(tmem + kDS, x, km + k * 128, id128, 1);
             }
             umma_commit(&B->ds_full);
@@ -377,8 +397,8 @@ __global__ void __launch_bounds__(CARRY ? 384 : 512, 1)
               const uint64_t pL = smem_desc_sw128(rb + 3 * kBlk, 16, 1024);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const uint32_t x = tmem + kXu + (k >> 1) * 32 + (k & 1) * 8;
-                umma_ts(tmem + kO, x + 16, pH + k * 2, id64, k != 0);
+                const uint32_t x = tmem + kXu + k * 16;
+                umma_ts(tmem + kO, x + 8, pH + k * 2, id64, k != 0);
                 umma_ts(tmem + kO, x, pL + k * 2, id64, 1);
                 umma_ts(tmem + kO, x, pH + k * 2, id64, 1);
               }
@@ -414,40 +434,40 @@ __global__ void __launch_bounds__(CARRY ? 384 : 512, 1)
         }
       }
     }
-  } else if (warp < 12) {
-    // ---- the chain: rows 32 q4 + lane, half of the columns
-    regs_inc<168>();
-    const int q4 = warp & 3, half = (warp - 4) >> 2;
+  } else if (warp < 20) {
+    // ---- the chain: rows 32 q4 + lane, a quarter of the columns
+    regs_inc<CARRY ? 104 : 88>();
+    const int q4 = warp & 3, part = (warp - 4) >> 2;
     const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
     int n = 0;
     for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
       const Item it = get_item<CARRY>(p, i);
       const int nc = n_chunks(it.len);
       const int row = 128 * it.tile + 32 * q4 + lane;
-      const long long so = (long long)row * p.dk + 64 * half;
-      F2 S[32];
+      const long long so = (long long)row * p.dk + 32 * part;
+      F2 S[16];
 #pragma unroll
-      for (int c = 0; c < 64; c += 4) {
+      for (int c = 0; c < 32; c += 4) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (it.from && row < p.dv && 64 * half + c < p.dk)
+        if (it.from && row < p.dv && 32 * part + c < p.dk)
           x = *reinterpret_cast<const float4*>(it.from + so + c);
         S[c / 2] = pack2(x.x, x.y);
         S[c / 2 + 1] = pack2(x.z, x.w);
       }
       if (CARRY && it.unit) {
-        const int d = row - 64 * half;   // this row's column of the unit matrix
+        const int d = row - 32 * part;   // this row's column of the unit matrix
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
+        for (int c = 0; c < 16; ++c)
           S[c] = pack2(d == 2 * c ? 1.f : 0.f, d == 2 * c + 1 ? 1.f : 0.f);
       }
       auto put_S = [&]() {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < 2; ++b) {
           uint32_t hi[8], lo[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) split2(S[8 * b + e], hi[e], lo[e]);
-          tmem_st8(tl + kSh + 32 * half + 8 * b, hi);
-          tmem_st8(tl + kSh + 64 + 32 * half + 8 * b, lo);
+          tmem_st8(tl + kSh + 16 * part + 8 * b, hi);
+          tmem_st8(tl + kSh + 64 + 16 * part + 8 * b, lo);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -458,22 +478,22 @@ __global__ void __launch_bounds__(CARRY ? 384 : 512, 1)
       for (int c = 0; c < nc; ++c, ++n) {
         const uint32_t ph = n & 1;
         const RecScal& sc = scal[ph];
-        float x[32];
+        float x[16];
         wait(&B->rec_full[ph], (n >> 1) & 1);
         wait(&B->ks_full, ph);
         tc_fence_after();
-        tmem_ld32(tl + kKS + 32 * half, x);
-        tmem_wait32(x);
-        put_scaled(tl + kKS + 32 * half, x, &sc.neg[32 * half]);
+        tmem_ld16_nowait(tl + kKS + 16 * part, x);
+        tmem_wait_bind(x);
+        put_scaled(tl + kKS + 16 * part, x, &sc.neg[16 * part]);
         tmem_wait_st();
         tc_fence_before();
         arrive(&B->y_ready);
 
         wait(&B->x_full, ph);
         tc_fence_after();
-        tmem_ld32(tl + kX + 32 * half, x);
-        tmem_wait32(x);
-        put_scaled(tl + kX + 32 * half, x, &sc.er[32 * half]);
+        tmem_ld16_nowait(tl + kX + 16 * part, x);
+        tmem_wait_bind(x);
+        put_scaled(tl + kX + 16 * part, x, &sc.er[16 * part]);
         tmem_wait_st();
         tc_fence_before();
         arrive(&B->xs_ready);
@@ -482,7 +502,7 @@ __global__ void __launch_bounds__(CARRY ? 384 : 512, 1)
         if (!CARRY) {
           if (n > 0) wait(&B->o_full, ph ^ 1);   // P X of the chunk before has read X
           tc_fence_after();
-          put_pairs(tl + kXu + 32 * half, x);
+          put_pairs(tl + kXu + 16 * part, x);
           tmem_wait_st();
           tc_fence_before();
           arrive(&B->x_ready);
@@ -492,65 +512,93 @@ __global__ void __launch_bounds__(CARRY ? 384 : 512, 1)
         tc_fence_after();
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          tmem_ld32(tl + kDS + 64 * half + 32 * b, x);
-          tmem_wait32(x);
+          tmem_ld16_nowait(tl + kDS + 32 * part + 16 * b, x);
+          tmem_wait_bind(x);
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            S[16 * b + e] = fma2(eall, S[16 * b + e], pack2(x[2 * e], x[2 * e + 1]));
+          for (int e = 0; e < 8; ++e)
+            S[8 * b + e] = fma2(eall, S[8 * b + e], pack2(x[2 * e], x[2 * e + 1]));
         }
         if (c + 1 < nc) put_S();
       }
       if (ok && it.to && row < it.rows) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 4)
-          if (64 * half + c < p.dk)
+        for (int c = 0; c < 32; c += 4)
+          if (32 * part + c < p.dk)
             *reinterpret_cast<ulonglong2*>(it.to + so + c) =
                 make_ulonglong2(S[c / 2], S[c / 2 + 1]);
       }
     }
   } else if (!CARRY) {
     // ---- outputs
-    regs_dec<104>();
+    regs_dec<72>();
     const int q4 = warp & 3;
     const float nscale = -p.scale;
+    const F2 nscale2 = pack2(nscale, nscale);
     const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
+    // this warp's 64 tokens x 32 rows of d_v, 64 bytes a token, the 16-byte pieces
+    // of a token exchanged by its number
+    uint8_t* ob = obuf + q4 * 4096;
+    const uint32_t obs = smem_u32(ob);
     int n = 0;
     for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
       const Item it = get_item<CARRY>(p, i);
       const int nc = n_chunks(it.len);
-      const int col = 128 * it.tile + 32 * q4 + lane;
+      const int col = 128 * it.tile + 32 * q4;
       __nv_bfloat16* out = p.out + it.batch * p.so.batch + it.h * p.so.head +
                            it.t0 * p.so.token + col;
+#pragma unroll 1
       for (int c = 0; c < nc; ++c, ++n) {
         const RecScal& sc = scal[n & 1];
         wait(&B->rec_full[n & 1], (n >> 1) & 1);
         wait(&B->o_full, n & 1);
         tc_fence_after();
-        int valid = ok && col < p.dv ? min(kC, it.len - c * kC) : 0;
-#pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-          float x[16], y[16];
-          tmem_ld16_nowait(tl + kQS + 16 * b, x);
-          tmem_ld16_nowait(tl + kO + 16 * b, y);
-          const float4* neg4 = reinterpret_cast<const float4*>(&sc.neg[16 * b]);
-          float w[16];
+#pragma unroll 2
+        for (int b = 0; b < 8; ++b) {   // 16 rows (b & 1) by 16 tokens (b >> 1)
+          float x[8], y[8];
+          const uint32_t ta = tl + ((uint32_t)(16 * (b & 1)) << 16) + 16 * (b >> 1);
+          tmem_ld_frag(ta + kQS, x);
+          tmem_ld_frag(ta + kO, y);
+          uint32_t w[4];
+          F2 f[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 f = neg4[e];
-            w[4 * e] = f.x; w[4 * e + 1] = f.y; w[4 * e + 2] = f.z; w[4 * e + 3] = f.w;
-          }
-          tmem_wait_bind(x);
-          tmem_wait_bind(y);
+          for (int t = 0; t < 2; ++t)
+            f[t] = mul2(nscale2, *reinterpret_cast<const F2*>(
+                                     &sc.neg[16 * (b >> 1) + 8 * t + 2 * (lane & 3)]));
+          tmem_wait_frag(x);
+          tmem_wait_frag(y);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (e < valid) *out = __float2bfloat16_rn(fmaf(nscale * w[e], x[e], y[e]));
-            out += p.so.token;
+          for (int e = 0; e < 4; ++e) {   // tokens 8 (e >> 1) .., rows 8 (e & 1) ..
+            const F2 o = fma2(f[e >> 1], pack2(x[2 * e], x[2 * e + 1]), pack2(y[2 * e], y[2 * e + 1]));
+            float o0, o1;
+            unpack2(o, o0, o1);
+            const __nv_bfloat162 r = __floats2bfloat162_rn(o0, o1);
+            w[e] = *reinterpret_cast<const uint32_t*>(&r);
           }
-          valid -= 16;
+          const int t = 16 * (b >> 1) + 8 * (lane >> 4) + (lane & 7);
+          const int piece = 2 * (b & 1) + ((lane >> 3) & 1);
+          stmatrix4_t(obs + t * 64 + ((piece ^ ((t >> 1) & 3)) << 4), w);
         }
         tc_fence_before();
         arrive(&B->o_free);
         arrive(&B->rec_free[n & 1]);
+        const int valid = ok ? min(kC, it.len - c * kC) : 0;
+        if (p.wide_out) {
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            const int t = 8 * b + (lane >> 2), piece = lane & 3;
+            const uint4 w = lds128(obs + t * 64 + ((piece ^ ((t >> 1) & 3)) << 4));
+            if (t < valid && col + 8 * piece < p.dv)
+              *reinterpret_cast<uint4*>(out + (long long)(c * kC + t) * p.so.token + 8 * piece) = w;
+          }
+        } else {
+#pragma unroll 1
+          for (int t = 0; t < valid; ++t) {
+            const __nv_bfloat16 o = *reinterpret_cast<const __nv_bfloat16*>(
+                ob + t * 64 + (((lane >> 3) ^ ((t >> 1) & 3)) << 4) + 2 * (lane & 7));
+            if (col + lane < p.dv) out[(long long)(c * kC + t) * p.so.token + lane] = o;
+          }
+        }
+        __syncwarp();
       }
     }
   }
@@ -623,23 +671,41 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 // ---------------------------------------------------------------- start states of the segments
-// S_{j+1} = S_j P_j + L_j for one (sequence, head): a CTA takes kJoinRows rows.
-constexpr int kJoinRows = 8, kJoinThreads = 128;
+// S_{j+1} = S_j P_j + L_j, in fp32: a CTA takes R rows of the state of one
+// (sequence, head) through all segments.  P_j comes into shared memory by bulk
+// copies a segment ahead (64 KB: the product itself is short, so the latency and
+// the L2 rate of these loads are what it waits for); each of the eight warps
+// takes an eighth of the summation index and 4 columns per lane, the eight
+// partial sums are added in a fixed order.
+constexpr int kJoinThreads = 256;
 
 struct JoinParams {
   const SegPlan* segs;
-  int seg_places, seg_n;
+  int seg_n;
   const float* S0;
   const float* L;
   const float* P;
   float* Sseg;
+  int* status;
+  unsigned long long wait_ns;
   int Hv, dk, dv, row_tiles;
 };
 
-__global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_constant__ JoinParams p) {
-  __shared__ float S[kJoinRows][128];
-  const int tile = blockIdx.x % p.row_tiles, sh = blockIdx.x / p.row_tiles;
-  const int h = sh % p.Hv, first = sh / p.Hv;   // first: a segment's place
+template <int R>
+struct JoinShared {
+  float P[2][128 * 128];
+  float part[8][R][128];
+  float S[R][128];
+  uint64_t full[2];
+};
+
+template <int R>
+__global__ void __launch_bounds__(kJoinThreads, 1)
+    delta_join_kernel(const __grid_constant__ JoinParams p) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  JoinShared<R>& sh = *reinterpret_cast<JoinShared<R>*>(smem_raw);
+  const int tile = blockIdx.x % p.row_tiles, x = blockIdx.x / p.row_tiles;
+  const int h = x % p.Hv, first = x / p.Hv;   // first: a segment's place (or a sequence)
   SegPlan sg;
   if (p.segs) {
     sg = p.segs[first];
@@ -650,39 +716,90 @@ __global__ void __launch_bounds__(kJoinThreads) delta_join_kernel(const __grid_c
   }
   if (sg.n < 2) return;
   const int seg0 = p.segs ? first : first * p.seg_n;
-  const int row0 = tile * kJoinRows, nr = min(kJoinRows, p.dv - row0);
-  const long long one = (long long)p.dv * p.dk;
-  const int k = threadIdx.x;
-  float acc[kJoinRows];
-#pragma unroll
-  for (int r = 0; r < kJoinRows; ++r) {
-    acc[r] = 0.f;
-    if (p.S0 && r < nr && k < p.dk)
-      acc[r] = p.S0[((long long)sg.seq * p.Hv + h) * one + (long long)(row0 + r) * p.dk + k];
-  }
-  for (int j = 0; j + 1 < sg.n; ++j) {
-    const long long x = (long long)(seg0 + j) * p.Hv + h;
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kJoinRows; ++r) S[r][k] = acc[r];
-    __syncthreads();
-    const float* P = p.P + x * p.dk * p.dk;
-    const float* L = p.L + x * one + (long long)row0 * p.dk;
-    if (k < p.dk) {
-#pragma unroll
-      for (int r = 0; r < kJoinRows; ++r) acc[r] = r < nr ? L[r * p.dk + k] : 0.f;
-#pragma unroll 8
-      for (int m = 0; m < p.dk; ++m) {
-        const float pm = P[(long long)m * p.dk + k];
-#pragma unroll
-        for (int r = 0; r < kJoinRows; ++r) acc[r] = fmaf(S[r][m], pm, acc[r]);
-      }
-      float* to = p.Sseg + (x + p.Hv) * one + (long long)row0 * p.dk;
-#pragma unroll
-      for (int r = 0; r < kJoinRows; ++r)
-        if (r < nr) to[r * p.dk + k] = acc[r];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row0 = tile * R;
+  const long long one = (long long)p.dv * p.dk, pp = (long long)p.dk * p.dk;
+  const uint32_t pbytes = (uint32_t)pp * 4;
+  bool ok = true;
+  if (tid == 0) {
+    mbar_init(&sh.full[0], 1);
+    mbar_init(&sh.full[1], 1);
+    fence_mbar_init();
+    for (int j = 0; j < 2 && j + 1 < sg.n; ++j) {
+      mbar_arrive_expect_tx(&sh.full[j], pbytes);
+      bulk_load_g2s(sh.P[j], p.P + ((long long)(seg0 + j) * p.Hv + h) * pp, pbytes, &sh.full[j]);
     }
   }
+  // this thread's outputs: column col, rows r0 .. r0 + R / 2
+  const int col = tid & 127, r0 = (tid >> 7) * (R / 2);
+#pragma unroll
+  for (int r = 0; r < R / 2; ++r) {
+    const int row = row0 + r0 + r;
+    sh.S[r0 + r][col] =
+        p.S0 && row < p.dv && col < p.dk
+            ? p.S0[((long long)sg.seq * p.Hv + h) * one + (long long)row * p.dk + col]
+            : 0.f;
+  }
+  __syncthreads();
+  const int m_per = p.dk / 8, m0 = warp * m_per, c4 = 4 * lane;
+  for (int j = 0; j + 1 < sg.n; ++j) {
+    const long long sgh = (long long)(seg0 + j) * p.Hv + h;
+    float l[R / 2];
+#pragma unroll
+    for (int r = 0; r < R / 2; ++r) {
+      const int row = row0 + r0 + r;
+      l[r] = row < p.dv && col < p.dk ? p.L[sgh * one + (long long)row * p.dk + col] : 0.f;
+    }
+    wait_w(ok, &sh.full[j & 1], (j >> 1) & 1, p.status, p.wait_ns);
+    F2 acc[R][2];
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[r][0] = acc[r][1] = 0;
+    if (c4 < p.dk) {
+      const float* P = sh.P[j & 1] + m0 * p.dk + c4;
+#pragma unroll 2
+      for (int m = 0; m < m_per; ++m, P += p.dk) {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(P);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float s = sh.S[r][m0 + m];
+          const F2 s2 = pack2(s, s);
+          acc[r][0] = fma2(s2, w.x, acc[r][0]);
+          acc[r][1] = fma2(s2, w.y, acc[r][1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      *reinterpret_cast<ulonglong2*>(&sh.part[warp][r][c4]) = make_ulonglong2(acc[r][0], acc[r][1]);
+    __syncthreads();
+    if (tid == 0 && j + 3 < sg.n) {   // everyone is done with P_j
+      fence_proxy_async_smem();
+      mbar_arrive_expect_tx(&sh.full[j & 1], pbytes);
+      bulk_load_g2s(sh.P[j & 1], p.P + (sgh + 2 * p.Hv) * pp, pbytes, &sh.full[j & 1]);
+    }
+    float* to = p.Sseg + (sgh + p.Hv) * one;
+#pragma unroll
+    for (int r = 0; r < R / 2; ++r) {
+      float s = l[r];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) s += sh.part[w][r0 + r][col];
+      sh.S[r0 + r][col] = s;
+      const int row = row0 + r0 + r;
+      if (ok && row < p.dv && col < p.dk) to[(long long)row * p.dk + col] = s;
+    }
+    __syncthreads();
+  }
+}
+
+template <int R>
+cudaError_t launch_join(JoinParams j, long long heads, cudaStream_t stream) {
+  auto kern = delta_join_kernel<R>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)sizeof(JoinShared<R>));
+  if (e != cudaSuccess) return e;
+  j.row_tiles = (j.dv + R - 1) / R;
+  kern<<<(unsigned)(heads * j.row_tiles), kJoinThreads, sizeof(JoinShared<R>), stream>>>(j);
+  return cudaGetLastError();
 }
 
 int g_ready[64] = {0};   // 0 unknown, 1 usable, 2 not usable
@@ -832,6 +949,8 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
   p.seg_chunks = pl.seg_chunks;
   p.seg_n = pl.seg_n;
   p.scale = a.scale;
+  p.wide_out = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.lay.out.batch % 8 == 0 &&
+               a.lay.out.head % 8 == 0 && a.lay.out.token % 8 == 0;
 
   const double tok = (double)a.B * a.N;
   if (packed) {
@@ -846,30 +965,34 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
       p.items = pl.seg_places * a.Hv * (p.tiles + 1);
       ProfScope ps(PT_DELTA_CARRY, a.stream, 5.0 * tok * a.Hv * a.dk * (a.dv + a.dk),
                    tok * 2.0 * (a.Hk * a.dk + a.Hv * a.dv));
-      delta_scan_kernel<true><<<p.items < sms ? p.items : sms, 384, kSmem, a.stream>>>(p);
+      delta_scan_kernel<true><<<p.items < sms ? p.items : sms, 640, kSmem, a.stream>>>(p);
       if (cudaGetLastError() != cudaSuccess) return TTT_ERR_CUDA;
     }
     JoinParams j;
     j.segs = segs;
-    j.seg_places = pl.seg_places;
     j.seg_n = pl.seg_n;
     j.S0 = a.S0;
     j.L = p.L;
     j.P = p.P;
     j.Sseg = Sseg;
+    j.status = a.status;
+    j.wait_ns = a.wait_ns;
     j.Hv = a.Hv; j.dk = a.dk; j.dv = a.dv;
-    j.row_tiles = (a.dv + kJoinRows - 1) / kJoinRows;
     const double states = (double)pl.seg_places * a.Hv * a.dk;
     ProfScope ps(PT_DELTA_JOIN, a.stream, 2.0 * states * a.dk * a.dv,
                  4.0 * states * (a.dk + 2 * a.dv));
-    const int firsts = packed ? pl.seg_places : a.B;
-    delta_join_kernel<<<(unsigned)(firsts * a.Hv * j.row_tiles), kJoinThreads, 0, a.stream>>>(j);
-    if (cudaGetLastError() != cudaSuccess) return TTT_ERR_CUDA;
+    // rows per CTA: as many as leave a CTA to every SM (one fits)
+    const long long heads = (long long)(packed ? pl.seg_places : a.B) * a.Hv;
+    const long long rows = (long long)a.n_seq * a.Hv * a.dv;
+    const cudaError_t e = rows >= 16 * 128   ? launch_join<16>(j, heads, a.stream)
+                          : rows >= 8 * 128 ? launch_join<8>(j, heads, a.stream)
+                                            : launch_join<4>(j, heads, a.stream);
+    if (e != cudaSuccess) return TTT_ERR_CUDA;
   }
   p.items = pl.seg_places * a.Hv * p.tiles;
   ProfScope ps(PT_DELTA_CHUNK, a.stream, 7.0 * tok * a.Hv * a.dk * a.dv,
                tok * 4.0 * (a.Hk * a.dk + a.Hv * a.dv));
-  delta_scan_kernel<false><<<p.items < sms ? p.items : sms, 512, kSmem, a.stream>>>(p);
+  delta_scan_kernel<false><<<p.items < sms ? p.items : sms, 768, kSmem, a.stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 

@@ -27,6 +27,7 @@ namespace {
 // other, rows of 16 floats 20 apart (so that the fragments' and the rows'
 // accesses spread over the banks).
 constexpr int kRowF = 20, kBlockF = 16 * kRowF;
+static_assert(10 * kBlockF * 4 <= 2 * kBlk, "scratch");
 
 __device__ __forceinline__ int block_at(int I, int J) { return (I * (I + 1) / 2 + J) * kBlockF; }
 
@@ -92,7 +93,6 @@ constexpr int kPThreads = 128;
 constexpr uint32_t kPCols = 64;
 
 struct PrepShared {
-  float M[10 * kBlockF];
   float beta[kC];
   float gl[kC];    // running sum of g log2(e) inside each block of 16
   float el[kC];    // exp2(blk - gl): decay from token j to the end of its block
@@ -113,7 +113,7 @@ __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
-__global__ void __launch_bounds__(kPThreads, 4)
+__global__ void __launch_bounds__(kPThreads, 6)
     delta_prep_kernel(const __grid_constant__ PrepParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tile =
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kPThreads, 4)
 
   const int half = warp & 1, row = half * 32 + lane, I = row >> 4;
   const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-  float* M = sh.M;
+  float* M = reinterpret_cast<float*>(tile);   // over the room of T's tiles
 #pragma unroll 1
   for (int hg = 0; hg < group; ++hg) {
     const int h = hk * group + hg;
@@ -372,13 +372,12 @@ __global__ void __launch_bounds__(kPThreads, 4)
       block_put<2>(o, r, -1.f, lane);
     }
     __syncthreads();
-    {   // T diag(beta) as a pair: half a row per thread
+    {   // T diag(beta) as a pair, over the scratch: half a row per thread
       const int i = tid >> 1, hf = tid & 1, IB = i >> 4;
-      const uint32_t trow = smem_u32(tile) + i * 128;
+      float x[32];
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const int J = 2 * hf + b;
-        float x[16];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -391,18 +390,20 @@ __global__ void __launch_bounds__(kPThreads, 4)
             v.z = j + 2 <= i ? v.z * be.z : 0.f;
             v.w = j + 3 <= i ? v.w * be.w : 0.f;
           }
-          *reinterpret_cast<float4*>(&x[4 * e]) = v;
+          *reinterpret_cast<float4*>(&x[16 * b + 4 * e]) = v;
         }
+      }
+      __syncthreads();
+      const uint32_t trow = smem_u32(tile) + i * 128;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t hi[4], lo[4];
+      for (int q = 0; q < 4; ++q) {
+        uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            split2(pack2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1]), hi[e], lo[e]);
-          const uint32_t o = trow + (((4 * hf + 2 * b + q) ^ (i & 7)) << 4);
-          sts128(o, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-          sts128(o + kBlk, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-        }
+        for (int e = 0; e < 4; ++e)
+          split2(pack2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1]), hi[e], lo[e]);
+        const uint32_t o = trow + (((4 * hf + q) ^ (i & 7)) << 4);
+        sts128(o, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        sts128(o + kBlk, make_uint4(lo[0], lo[1], lo[2], lo[3]));
       }
     }
     fence_proxy_async_smem();
