@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -73,18 +74,6 @@ class LinattnRule(ctypes.Structure):
                 ("ns_a", ctypes.c_float), ("ns_b", ctypes.c_float), ("ns_c", ctypes.c_float)]
 
 
-class DeltaRuleLayout(ctypes.Structure):
-    """Mirror of ``delta_rule_layout``: (batch, head, token) strides of q, k, v, g, beta, out."""
-    _fields_ = [("strides", ctypes.c_longlong * 18)]
-
-
-class BlockNormStrides(ctypes.Structure):
-    """Mirror of ``block_norm_strides``."""
-    _fields_ = [("y", ctypes.c_longlong), ("gate", ctypes.c_longlong),
-                ("residual", ctypes.c_longlong), ("out", ctypes.c_longlong),
-                ("h", ctypes.c_longlong)]
-
-
 def update_rule(l2norm=True, muon_steps=0, momentum_beta=0.0, ns_coef=MUON_COEF,
                 last_layer_only=False, inner_steps=1, form=FORM_AUTO) -> UpdateRule:
     a, b, c = ns_coef
@@ -137,18 +126,18 @@ def _declare(lib):
     lib.linattn_chunked_forward_noalloc.restype = i
     lib.linattn_chunked_forward_noalloc.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i,
                                                     vp, vp, vp, vp]
-    f32, ll = ctypes.c_float, ctypes.c_longlong
+    f32, ll = ctypes.c_float, ctypes.c_longlong   # strides: packed bytes (c_char_p)
     lib.delta_rule_workspace_size.restype = sz
     lib.delta_rule_workspace_size.argtypes = [i] * 8
     lib.delta_rule_chunked_forward.restype = i
     lib.delta_rule_chunked_forward.argtypes = [vp] * 7 + [i] * 8 + [
-        f32, ctypes.POINTER(DeltaRuleLayout), vp, vp, vp, sz, vp]
+        f32, ctypes.c_char_p, vp, vp, vp, sz, vp]
     lib.delta_rule_step.restype = i
     lib.delta_rule_step.argtypes = [vp] * 7 + [i] * 7 + [
-        f32, ctypes.POINTER(DeltaRuleLayout), vp, vp]
+        f32, ctypes.c_char_p, vp, vp]
     lib.block_norm_forward.restype = i
     lib.block_norm_forward.argtypes = [vp] * 6 + [ll] + [i] * 5 + [
-        f32, ctypes.POINTER(BlockNormStrides), vp, vp, vp]
+        f32, ctypes.c_char_p, vp, vp, vp]
     lib.ttt_selftest_withhold_release.restype = None
     lib.ttt_selftest_withhold_release.argtypes = [i]
     lib.ttt_launch_count.restype = ctypes.c_ulonglong
@@ -437,62 +426,44 @@ def linattn_chunked_forward_noalloc(q, k, v, eta, chunk: int, mask_mode: int,
     return out, S_final
 
 
-def _shape(t, shape, what):
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
+# The delta-rule and norm calls are made once per layer and decoded token, so
+# their bindings keep the host's share short: strides travel as packed bytes,
+# and the stream is looked up by device index.
+_pack_layout = struct.Struct("18q").pack
+_pack_norm_strides = struct.Struct("5q").pack
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _same(t, dtype, dev, what):
+def _elsewhere(dev, stream):
+    """None where `dev` is current and no stream is given; else a context that
+    makes them so (outputs and workspace then belong to the stream that uses
+    them)."""
+    if dev.type != "cuda":
+        raise ValueError("tensors passed to the CUDA path must be on a CUDA device")
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"the stream must be on {dev}")
+        return torch.cuda.stream(stream)
+    if dev.index != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return None
+
+
+def _want(t, shape, dtype, dev, what):
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{what} must be on {dev}, got {t.device}")
 
 
-def _last_contiguous(t, what):
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+def _strides(t, what):
+    """Strides of a tensor whose last dimension is contiguous."""
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{what} must be contiguous in its last dimension")
-
-
-class _On:
-    """Makes `dev` current, and `stream` when one is given (so that outputs and
-    workspace belong to the stream that uses them); gives the stream's handle."""
-
-    def __init__(self, dev, stream):
-        if dev.type != "cuda":
-            raise ValueError("tensors passed to the CUDA path must be on a CUDA device")
-        self.dev, self.stream, self.inner = dev, stream, None
-
-    def __enter__(self):
-        if self.stream is not None:
-            self.inner = torch.cuda.stream(self.stream)
-        elif self.dev.index != torch.cuda.current_device():
-            self.inner = torch.cuda.device(self.dev)
-        if self.inner is not None:
-            self.inner.__enter__()
-        s = torch.cuda.current_stream(self.dev) if self.stream is None else self.stream
-        return ctypes.c_void_p(s.cuda_stream)
-
-    def __exit__(self, *exc):
-        if self.inner is not None:
-            self.inner.__exit__(*exc)
-
-
-def _rule_heads(q, k, v, g, beta, tokens):
-    """Checks the inputs of a delta-rule call; tokens: () or (N,)."""
-    B, Hk, dk = q.shape[0], q.shape[1], q.shape[-1]
-    Hv, dv = v.shape[1], v.shape[-1]
-    _shape(q, (B, Hk) + tokens + (dk,), "q")
-    _shape(k, (B, Hk) + tokens + (dk,), "k")
-    _shape(v, (B, Hv) + tokens + (dv,), "v")
-    for t, what in ((g, "g"), (beta, "beta")):
-        _shape(t, (B, Hv) + tokens, what)
-        _same(t, torch.float32, q.device, what)
-    for t, what in ((k, "k"), (v, "v")):
-        _same(t, q.dtype, q.device, what)
-    for t, what in ((q, "q"), (k, "k"), (v, "v")):
-        _last_contiguous(t, what)
-    return B, Hk, Hv, dk, dv
+    return st
 
 
 def delta_rule_workspace_size(B, Hk, Hv, N, d_k, d_v, n_seq, io_dtype) -> int:
@@ -515,47 +486,54 @@ def delta_rule_chunked_forward(q, k, v, g, beta, S0: Optional[torch.Tensor] = No
     S_final [n_seq or B, Hv, d_v, d_k] fp32.  Without ``out``, the outputs are
     stored in v's order of dimensions.  Returns (out [B, Hv, N, d_v], S_final).
     """
-    lib = library()
+    dev = q.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return delta_rule_chunked_forward(q, k, v, g, beta, S0, seq_starts, scale, out,
+                                              S_final, workspace)
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q and v must have four dimensions")
-    N = q.shape[2]
-    B, Hk, Hv, dk, dv = _rule_heads(q, k, v, g, beta, (N,))
-    io, dev = _io_dtype(q), q.device
+    B, Hk, N, dk = q.shape
+    Hv, dv = v.shape[1], v.shape[3]
+    dt, io, f32 = q.dtype, _io_dtype(q), torch.float32
+    _want(k, (B, Hk, N, dk), dt, dev, "k")
+    _want(v, (B, Hv, N, dv), dt, dev, "v")
+    _want(g, (B, Hv, N), f32, dev, "g")
+    _want(beta, (B, Hv, N), f32, dev, "beta")
     n_seq = B
     if seq_starts is not None:
-        _same(seq_starts, torch.int32, dev, "seq_starts")
-        if seq_starts.dim() != 1 or seq_starts.numel() < 2 or not seq_starts.is_contiguous():
-            raise ValueError("seq_starts must be a contiguous vector of n_seq + 1 entries")
         if B != 1:
             raise ValueError("seq_starts needs B = 1")
         n_seq = seq_starts.numel() - 1
+        if n_seq < 1 or not seq_starts.is_contiguous():
+            raise ValueError("seq_starts must be a contiguous vector of n_seq + 1 entries")
+        _want(seq_starts, (n_seq + 1,), torch.int32, dev, "seq_starts")
+    lib = library()
+    if out is None:
+        out = torch.empty_like(v)   # v's strides where they are dense, else row-major
+    else:
+        _want(out, (B, Hv, N, dv), dt, dev, "out")
     state = (n_seq, Hv, dv, dk)
-    with _On(dev, stream) as handle:
-        if out is None:
-            out = torch.empty_like(v)   # v's strides where they are dense, else row-major
-        else:
-            _shape(out, (B, Hv, N, dv), "out")
-            _same(out, q.dtype, dev, "out")
-            _last_contiguous(out, "out")
-        if S_final is None:
-            S_final = torch.empty(state, device=dev, dtype=torch.float32)
-        for t, what in ((S0, "S0"), (S_final, "S_final")):
-            if t is not None:
-                _shape(t, state, what)
-                _same(t, torch.float32, dev, what)
+    if S_final is None:
+        S_final = torch.empty(state, device=dev, dtype=f32)
+    else:
+        _want(S_final, state, f32, dev, "S_final")
+    if S0 is not None:
+        _want(S0, state, f32, dev, "S0")
+    if workspace is None:
         need = lib.delta_rule_workspace_size(B, Hk, Hv, N, dk, dv, n_seq, io)
-        if workspace is None:
-            workspace = torch.empty(max(need, 256), device=dev, dtype=torch.uint8)
-        elif workspace.device != dev:
-            raise ValueError(f"workspace must be on {dev}")
-        lay = DeltaRuleLayout((ctypes.c_longlong * 18)(
-            *q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *g.stride(), *beta.stride(),
-            *out.stride()[:3]))
-        rc = lib.delta_rule_chunked_forward(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(S0),
-            None if seq_starts is None else seq_starts.data_ptr(), n_seq, B, Hk, Hv, N, dk, dv, io,
-            dk ** -0.5 if scale is None else float(scale), ctypes.byref(lay), out.data_ptr(),
-            _ptr(S_final), _ptr(workspace), workspace.numel() * workspace.element_size(), handle)
+        workspace = torch.empty(need or 256, device=dev, dtype=torch.uint8)
+    elif workspace.device != dev:
+        raise ValueError(f"workspace must be on {dev}")
+    rc = lib.delta_rule_chunked_forward(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(S0),
+        None if seq_starts is None else seq_starts.data_ptr(), n_seq, B, Hk, Hv, N, dk, dv, io,
+        dk ** -0.5 if scale is None else scale,
+        _pack_layout(*_strides(q, "q")[:3], *_strides(k, "k")[:3], *_strides(v, "v")[:3],
+                     *g.stride(), *beta.stride(), *_strides(out, "out")[:3]),
+        out.data_ptr(), _ptr(S_final), _ptr(workspace), workspace.nbytes,
+        _raw_stream(dev.index))
     _check(rc, "delta_rule_chunked_forward")
     return out, S_final
 
@@ -571,48 +549,52 @@ def delta_rule_step(q, k, v, g, beta, state, slots: Optional[torch.Tensor] = Non
     contiguous; g, beta [B, Hv] fp32; state [n_slots, Hv, d_v, d_k] fp32;
     slots int32 [B] (negative: an idle row) or None.  Returns out [B, Hv, d_v].
     """
-    lib = library()
-    if q.dim() != 3 or v.dim() != 3:
-        raise ValueError("q and v must have three dimensions")
-    B, Hk, Hv, dk, dv = _rule_heads(q, k, v, g, beta, ())
-    io, dev = _io_dtype(q), q.device
-    _same(state, torch.float32, dev, "state")
-    if state.dim() != 4:
-        raise ValueError("state must have four dimensions")
-    _shape(state, (state.shape[0], Hv, dv, dk), "state")
+    dev = q.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return delta_rule_step(q, k, v, g, beta, state, slots, scale, out)
+    if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
+        raise ValueError("q and v must have three dimensions, state four")
+    B, Hk, dk = q.shape
+    Hv, dv = v.shape[1], v.shape[2]
+    dt, io, f32 = q.dtype, _io_dtype(q), torch.float32
+    _want(k, (B, Hk, dk), dt, dev, "k")
+    _want(v, (B, Hv, dv), dt, dev, "v")
+    _want(g, (B, Hv), f32, dev, "g")
+    _want(beta, (B, Hv), f32, dev, "beta")
+    n_slots = state.shape[0]
+    _want(state, (n_slots, Hv, dv, dk), f32, dev, "state")
     if slots is not None:
-        _same(slots, torch.int32, dev, "slots")
-        _shape(slots, (B,), "slots")
+        _want(slots, (B,), torch.int32, dev, "slots")
         if not slots.is_contiguous():
             raise ValueError("slots must be contiguous")
-    with _On(dev, stream) as handle:
-        if out is None:
-            out = torch.empty((B, Hv, dv), device=dev, dtype=q.dtype)
-        else:
-            _shape(out, (B, Hv, dv), "out")
-            _same(out, q.dtype, dev, "out")
-            _last_contiguous(out, "out")
-        lay = DeltaRuleLayout((ctypes.c_longlong * 18)(
-            *q.stride()[:2], 0, *k.stride()[:2], 0, *v.stride()[:2], 0, *g.stride(), 0,
-            *beta.stride(), 0, *out.stride()[:2], 0))
-        rc = lib.delta_rule_step(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(state),
-            None if slots is None else slots.data_ptr(), state.shape[0], B, Hk, Hv, dk, dv, io,
-            dk ** -0.5 if scale is None else float(scale), ctypes.byref(lay), out.data_ptr(),
-            handle)
+    if out is None:
+        out = torch.empty((B, Hv, dv), device=dev, dtype=dt)
+    else:
+        _want(out, (B, Hv, dv), dt, dev, "out")
+    rc = library().delta_rule_step(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(state),
+        None if slots is None else slots.data_ptr(), n_slots, B, Hk, Hv, dk, dv, io,
+        dk ** -0.5 if scale is None else scale,
+        _pack_layout(*_strides(q, "q")[:2], 0, *_strides(k, "k")[:2], 0, *_strides(v, "v")[:2], 0,
+                     *g.stride(), 0, *beta.stride(), 0, *_strides(out, "out")[:2], 0),
+        out.data_ptr(), _raw_stream(dev.index))
     _check(rc, "delta_rule_step")
     return out
 
 
-def _rows(t, rows, D, what):
+def _rows(t, rows, D, dtype, dev, what):
     """Row stride of a [..., D] tensor whose leading dimensions run on as one."""
+    if t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{what} must be {dtype} on {dev}, got {t.dtype} on {t.device}")
     if t.shape[-1] != D or t.numel() != rows * D:
         raise ValueError(f"{what} must hold {rows} rows of {D}, got shape {tuple(t.shape)}")
-    _last_contiguous(t, what)
     if t.is_contiguous():
         return D
+    strides = _strides(t, what)
     stride, size = None, 1
-    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for n, st in zip(reversed(t.shape[:-1]), reversed(strides[:-1])):
         if n == 1:
             continue
         if stride is None:
@@ -638,41 +620,43 @@ def block_norm_forward(y, w: Optional[torch.Tensor] = None,
     (residual's type, or y's); w [group] (its length sets the group), scale
     and w_next [D] fp32.  Returns (out, h); h is None without ``w_next``.
     """
-    lib = library()
-    dev, D = y.device, y.shape[-1]
-    io = _io_dtype(y)
-    if D == 0 or y.numel() == 0:
+    dev = y.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return block_norm_forward(y, w, gate, gate_act, residual, scale, w_next, group, eps,
+                                      out_dtype, out, h)
+    D, n, dt, io, f32 = y.shape[-1], y.numel(), y.dtype, _io_dtype(y), torch.float32
+    if n == 0:
         raise ValueError("y must not be empty")
-    rows = y.numel() // D
+    rows = n // D
     if out_dtype is None:
         out_dtype = (residual if residual is not None else out if out is not None else y).dtype
     if group is None:
         group = D if w is None else w.numel()
-    for t, n, what in ((w, group, "w"), (scale, D, "scale"), (w_next, D, "w_next")):
-        if t is not None:
-            _same(t, torch.float32, dev, what)
-            _shape(t, (n,), what)
-    with _On(dev, stream) as handle:
-        if out is None:
-            out = torch.empty(y.shape, device=dev, dtype=out_dtype)
-        if w_next is None:
-            if h is not None:
-                raise ValueError("h needs w_next")
-        elif h is None:
-            h = torch.empty(y.shape, device=dev, dtype=y.dtype)
-        st = [0, 0, 0, 0, 0]
-        for i, (t, dt, what) in enumerate(((y, y.dtype, "y"), (gate, y.dtype, "gate"),
-                                           (residual, out_dtype, "residual"),
-                                           (out, out_dtype, "out"), (h, y.dtype, "h"))):
-            if t is not None:
-                _same(t, dt, dev, what)
-                st[i] = _rows(t, rows, D, what)
-        rc = lib.block_norm_forward(
-            y.data_ptr(), _ptr(w), None if gate is None else gate.data_ptr(),
-            None if residual is None else residual.data_ptr(), _ptr(scale), _ptr(w_next), rows, D,
-            group, io, _io_dtype(out), int(gate_act), float(eps),
-            ctypes.byref(BlockNormStrides(*st)), out.data_ptr(),
-            None if h is None else h.data_ptr(), handle)
+    if w is not None:
+        _want(w, (group,), f32, dev, "w")
+    if scale is not None:
+        _want(scale, (D,), f32, dev, "scale")
+    if w_next is not None:
+        _want(w_next, (D,), f32, dev, "w_next")
+        if h is None:
+            h = torch.empty(y.shape, device=dev, dtype=dt)
+    elif h is not None:
+        raise ValueError("h needs w_next")
+    if out is None:
+        out = torch.empty(y.shape, device=dev, dtype=out_dtype)
+    rc = library().block_norm_forward(
+        y.data_ptr(), _ptr(w), None if gate is None else gate.data_ptr(),
+        None if residual is None else residual.data_ptr(), _ptr(scale), _ptr(w_next), rows, D,
+        group, io, _io_dtype(out), gate_act, eps,
+        _pack_norm_strides(
+            _rows(y, rows, D, dt, dev, "y"),
+            0 if gate is None else _rows(gate, rows, D, dt, dev, "gate"),
+            0 if residual is None else _rows(residual, rows, D, out_dtype, dev, "residual"),
+            _rows(out, rows, D, out_dtype, dev, "out"),
+            0 if h is None else _rows(h, rows, D, dt, dev, "h")),
+        out.data_ptr(), None if h is None else h.data_ptr(), _raw_stream(dev.index))
     _check(rc, "block_norm_forward")
     return out, h
 

@@ -793,12 +793,9 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
 
 template <int R>
 cudaError_t launch_join(JoinParams j, long long heads, cudaStream_t stream) {
-  auto kern = delta_join_kernel<R>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)sizeof(JoinShared<R>));
-  if (e != cudaSuccess) return e;
   j.row_tiles = (j.dv + R - 1) / R;
-  kern<<<(unsigned)(heads * j.row_tiles), kJoinThreads, sizeof(JoinShared<R>), stream>>>(j);
+  delta_join_kernel<R>
+      <<<(unsigned)(heads * j.row_tiles), kJoinThreads, sizeof(JoinShared<R>), stream>>>(j);
   return cudaGetLastError();
 }
 
@@ -813,10 +810,15 @@ int prepare() {
   std::lock_guard<std::mutex> lk(g_mu);
   if (g_ready[dev] == 0) {
     g_ready[dev] = 2;
-    if (cudaFuncSetAttribute(delta_scan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmem) == cudaSuccess &&
-        cudaFuncSetAttribute(delta_scan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmem) == cudaSuccess &&
+    auto room = [](auto kern, size_t bytes) {
+      return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
+             cudaSuccess;
+    };
+    if (room(delta_scan_kernel<false>, kSmem) && room(delta_scan_kernel<true>, kSmem) &&
+        room(delta_join_kernel<4>, sizeof(JoinShared<4>)) &&
+        room(delta_join_kernel<8>, sizeof(JoinShared<8>)) &&
+        room(delta_join_kernel<16>, sizeof(JoinShared<16>)) &&
+        prepare_delta_prep() == cudaSuccess &&
         cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
       g_ready[dev] = 1;
     cudaGetLastError();

@@ -432,10 +432,11 @@ __global__ void __launch_bounds__(kPThreads, 6)
 
 }  // namespace
 
+cudaError_t prepare_delta_prep() {
+  return cudaFuncSetAttribute(delta_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem);
+}
+
 cudaError_t launch_delta_prep(const PrepParams& p, int chunks, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(delta_prep_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem);
-  if (e != cudaSuccess) return e;
   const double rec = (double)chunks * p.Hv;
   ProfScope ps(PT_DELTA_PREP, stream, 2.0 * 128 * 64 * 128 * (double)chunks * p.Hk,
                rec * (kRecBytes + sizeof(RecScal)) + 32768.0 * chunks * p.Hk);

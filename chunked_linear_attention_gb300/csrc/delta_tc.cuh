@@ -148,6 +148,8 @@ struct PrepParams {
   unsigned long long wait_ns;
 };
 
+// One-time kernel attributes of the current device.
+cudaError_t prepare_delta_prep();
 // The records of every chunk; `chunks` is the number of chunk places.
 cudaError_t launch_delta_prep(const PrepParams& p, int chunks, cudaStream_t stream);
 

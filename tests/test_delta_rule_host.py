@@ -1,6 +1,6 @@
 """Host-side checks of the delta-rule and norm entry points (no GPU): bad
 arguments are refused with the documented codes before the device is touched."""
-import ctypes
+import struct
 
 import pytest
 import torch
@@ -23,7 +23,7 @@ def rule(cla, B=1, Hk=1, Hv=2, N=64, dk=64, dv=64, n_seq=None, io=1, scale=1.0, 
     need = lib.delta_rule_workspace_size(B, Hk, Hv, N, dk, dv, n_seq, io)
     return lib.delta_rule_chunked_forward(
         q, k, v, g, b, s0 if S0 else None, st if packed else None, n_seq, B, Hk, Hv, N, dk, dv,
-        io, scale, ctypes.byref(lay) if lay is not None else None, out, sf, wsp,
+        io, scale, lay, out, sf, wsp,
         max(need, 256) if ws is None else ws, None)
 
 
@@ -32,7 +32,7 @@ def layout(cla, **change):
         2 * 64 * 64, 64 * 64, 64]
     for at, x in change.items():
         s[int(at[1:])] = x
-    return cla.DeltaRuleLayout((ctypes.c_longlong * 18)(*s))
+    return struct.pack("18q", *s)
 
 
 def test_rule_refusals(cla):
@@ -95,7 +95,7 @@ def norm(cla, rows=4, D=64, group=64, io=1, st=1, act=0, eps=1e-6, gate=False, n
     h = nxt if h is None else h
     return cla.library().block_norm_forward(
         y, w, z if gate else None, x, a, wn if nxt else None, rows, D, group, io, st, act, eps,
-        ctypes.byref(strides) if strides is not None else None, out, hh if h else None, None)
+        strides, out, hh if h else None, None)
 
 
 def test_norm_refusals(cla):
@@ -111,9 +111,8 @@ def test_norm_refusals(cla):
         assert norm(cla, **bad) == TTT_ERR_ARG, bad
     assert norm(cla, D=32768, group=32768) == TTT_ERR_UNSUPPORTED
     assert norm(cla, off=(0,)) == TTT_ERR_ALIGN
-    S = cla.BlockNormStrides
-    assert norm(cla, strides=S(64, 0, 64, 32, 0)) == TTT_ERR_ARG     # rows of out overlap
-    assert norm(cla, strides=S(-64, 0, 64, 64, 0)) == TTT_ERR_ARG
+    assert norm(cla, strides=struct.pack("5q", 64, 0, 64, 32, 0)) == TTT_ERR_ARG     # rows of out overlap
+    assert norm(cla, strides=struct.pack("5q", -64, 0, 64, 64, 0)) == TTT_ERR_ARG
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-device path")
