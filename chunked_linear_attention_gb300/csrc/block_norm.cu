@@ -3,13 +3,18 @@
 //   n = y / sqrt(mean_group(y^2) + eps) w;  r = residual + scale n act(gate);
 //   h = r / sqrt(mean_row(r^2) + eps) w_next
 //
-// One CTA per row; a thread owns VPT pieces of VEC neighbouring elements, keeps
-// them in registers as fp32 between the two means and the stores, so every
-// tensor moves once and the kernel is bound by HBM.  A group's mean: the
-// squares are summed within a piece, by a butterfly over the P lanes that the
-// group's pieces fill in whole (P = the largest power of two that divides the
-// group's pieces, at most 32), and the group's few remaining partial sums
-// through shared memory, always in the same order.
+// A thread owns VPT pieces of VEC neighbouring elements, the same ones in every
+// row that its CTA takes, so the weights are read once; the next row's loads are
+// issued before the present row's arithmetic.  A row stays in registers as fp32
+// between the two means and the stores: every tensor moves once, and the bound is
+// HBM.  A group's mean: the squares are summed within a piece, by a butterfly over
+// the P lanes that the group's pieces fill in whole (P = the largest power of two
+// that divides the group's pieces, at most 32), and the group's few remaining
+// partial sums through shared memory, always in the same order.
+//
+// One row per CTA, with the weights read anew for each, took 197 us for 65536
+// rows of 1536 with four gated groups (3.1 TB/s): its instructions, and not HBM,
+// were the bound.
 #include "common.cuh"
 #include "delta_rule.h"
 #include "prof.h"
@@ -17,6 +22,11 @@
 namespace ttt {
 
 namespace {
+
+// Threads of a CTA: 256 where a thread has one piece (three CTAs per SM and their
+// loads in flight), else up to 512.
+constexpr int max_threads(int vpt) { return vpt == 1 ? 256 : 512; }
+constexpr int min_ctas(int vpt) { return vpt == 1 ? 3 : 1; }
 
 struct NormParams {
   const void* y;
@@ -27,36 +37,56 @@ struct NormParams {
   const float* w_next;
   void* out;
   void* h;
+  long long rows;
   int D, group, act;
   int pieces;        // D / VEC
   int gpieces;       // group / VEC
   int P;             // lanes of a group's butterfly
+  int nt;            // threads per row
   float eps;
   block_norm_strides st;
 };
 
+// VEC elements as they are loaded.
 template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, float (&x)[VEC]) {
-  if constexpr (VEC == 8 && sizeof(T) == 2) {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+struct Raw {
+  T x[VEC];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) x[i] = p[i];
+  }
+  __device__ __forceinline__ void get(float (&f)[VEC]) const {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = to_f<T>(x[i]);
+  }
+};
+template <>
+struct Raw<__nv_bfloat16, 8> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    u = __ldcs(reinterpret_cast<const uint4*>(p));
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
-  } else if constexpr (VEC == 8) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 f = __ldcs(reinterpret_cast<const float4*>(p) + i);
-      x[4 * i] = f.x; x[4 * i + 1] = f.y; x[4 * i + 2] = f.z; x[4 * i + 3] = f.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) x[i] = to_f<T>(p[i]);
   }
-}
+};
+template <>
+struct Raw<float, 8> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+};
 
 template <typename T, int VEC>
 __device__ __forceinline__ void store_vec(T* p, const float (&x)[VEC]) {
@@ -79,130 +109,205 @@ __device__ __forceinline__ void store_vec(T* p, const float (&x)[VEC]) {
   }
 }
 
-// Weights: read by every row, so kept in the caches.
+// A weight's elements, or ones.
 template <int VEC>
-__device__ __forceinline__ void load_w(const float* p, float (&x)[VEC]) {
-  if constexpr (VEC == 8) {
+__device__ __forceinline__ void load_w(const float* p, bool there, float (&x)[VEC]) {
+  if (!there) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) x[i] = 1.f;
+  } else if constexpr (VEC == 8) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(p) + i);
+      const float4 f = reinterpret_cast<const float4*>(p)[i];
       x[4 * i] = f.x; x[4 * i + 1] = f.y; x[4 * i + 2] = f.z; x[4 * i + 3] = f.w;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) x[i] = __ldg(p + i);
+    for (int i = 0; i < VEC; ++i) x[i] = p[i];
   }
 }
 
-template <typename T, typename TS, int VEC, int VPT>
-__global__ void __launch_bounds__(1024) block_norm_kernel(const __grid_constant__ NormParams p) {
-  extern __shared__ float part[];   // [pieces / P] group partials, then [32] row partials
-  const long long row = blockIdx.x;
-  const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31;
-  const T* y = static_cast<const T*>(p.y) + row * p.st.y;
-  const T* z = static_cast<const T*>(p.gate) + row * p.st.gate;
-  const TS* x = static_cast<const TS*>(p.residual) + row * p.st.residual;
-  float m[VPT][VEC], gate[VPT][VEC], res[VPT][VEC];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = (i * nt + tid) * VEC;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) m[i][j] = gate[i][j] = res[i][j] = 0.f;
-    if (c < p.D) {
-      load_vec<T, VEC>(y + c, m[i]);
-      if (p.act) load_vec<T, VEC>(z + c, gate[i]);
-      if (p.residual) load_vec<TS, VEC>(x + c, res[i]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) ss = fmaf(m[i][j], m[i][j], ss);
-    for (int o = p.P >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const int piece = i * nt + tid;
-    if (piece < p.pieces && (piece & (p.P - 1)) == 0) part[piece / p.P] = ss;
-  }
-  __syncthreads();
+// sigmoid(x) from the hardware exponential and reciprocal (2^-22 each; the
+// exponent's own rounding adds |x| 2^-24): the exact division would cost more
+// than the loads.  Saturates to 0 and 1.
+__device__ __forceinline__ float sigmoid_fast(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
+
+// PARTS: which of gate (4), residual (2) and next norm (1) are there; -1: the
+// call says (wide or unaligned rows, which need no variant for each).
+template <typename T, typename TS, int VEC, int VPT, int PARTS>
+__global__ void __launch_bounds__(max_threads(VPT), min_ctas(VPT))
+    block_norm_kernel(const __grid_constant__ NormParams p) {
+  const bool GATE = PARTS < 0 ? p.gate != nullptr : (PARTS & 4) != 0;
+  const bool RES = PARTS < 0 ? p.residual != nullptr : (PARTS & 2) != 0;
+  const bool NEXT = PARTS < 0 ? p.h != nullptr : (PARTS & 1) != 0;
+  // for each row of the CTA: [2][pieces / P] group partials, [2][nt / 32] row partials
+  extern __shared__ float smem[];
+  const int ty = threadIdx.x / p.nt, tid = threadIdx.x - ty * p.nt, ny = blockDim.x / p.nt;
+  const int warp = tid >> 5, lane = tid & 31, nw = p.nt >> 5, np = p.pieces / p.P;
+  float* part = smem + ty * 2 * (np + nw);
+  float* rpart = part + 2 * np;
   const int per = p.gpieces / p.P;   // partials of a group
-  float rr = 0.f;
+  const float inv_g = 1.f / (float)p.group, inv_d = 1.f / (float)p.D;
+  int col[VPT], first[VPT], slot[VPT];   // slot: of the group partial this thread writes, or -1
+  float w[VPT][VEC], wn[VPT][VEC];   // w: times the residual scale
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int piece = i * nt + tid, c = piece * VEC;
-    if (c < p.D) {
-      const int grp = piece / p.gpieces;
-      float ss = 0.f;
-      for (int j = 0; j < per; ++j) ss += part[grp * per + j];
-      const float inv = rsqrtf(ss / (float)p.group + p.eps);
-      float w[VEC];
-      if (p.w) {
-        load_w<VEC>(p.w + (c - grp * p.group), w);
+    const int piece = i * p.nt + tid, grp = piece / p.gpieces;
+    col[i] = piece * VEC;
+    first[i] = grp * per;
+    slot[i] = piece < p.pieces && piece % p.P == 0 ? piece / p.P : -1;
+    const bool in = col[i] < p.D;
+    float a[VEC];
+    load_w<VEC>(p.w + (col[i] - grp * p.group), in && p.w, w[i]);
+    load_w<VEC>(p.scale + col[i], in && p.scale, a);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) m[i][j] *= inv * w[j];
-      } else {
+    for (int j = 0; j < VEC; ++j) w[i][j] *= a[j];
+    if (NEXT) load_w<VEC>(p.w_next + col[i], in, wn[i]);
+  }
+  // rows move by whole CTAs: pointers advance, nothing is multiplied per row
+  long long row = (long long)blockIdx.x * ny + ty;
+  const long long step = (long long)gridDim.x * ny;
+  const T* py = static_cast<const T*>(p.y) + row * p.st.y;
+  const T* pz = static_cast<const T*>(p.gate) + row * p.st.gate;
+  const TS* px = static_cast<const TS*>(p.residual) + row * p.st.residual;
+  TS* po = static_cast<TS*>(p.out) + row * p.st.out;
+  T* ph = static_cast<T*>(p.h) + row * p.st.h;
+  const long long sy = step * p.st.y, sz = step * p.st.gate, sx = step * p.st.residual;
+  const long long so = step * p.st.out, shh = step * p.st.h;
+  Raw<T, VEC> ry[VPT], rz[VPT];
+  Raw<TS, VEC> rx[VPT];
+  auto load = [&]() {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) m[i][j] *= inv;
+    for (int i = 0; i < VPT; ++i)
+      if (col[i] < p.D) {
+        ry[i].load(py + col[i]);
+        if (GATE) rz[i].load(pz + col[i]);
+        if (RES) rx[i].load(px + col[i]);
       }
-      if (p.act) {
+    py += sy;
+    if (GATE) pz += sz;
+    if (RES) px += sx;
+  };
+  if (row < p.rows) load();
+  int buf = 0;
+  for (long long r0 = (long long)blockIdx.x * ny; r0 < p.rows; r0 += step, row += step, buf ^= 1) {
+    const bool live = row < p.rows;   // the CTA's rows meet at its barriers
+    float m[VPT][VEC], z[VPT][VEC], x[VPT][VEC];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float sg = sigmoid_precise(gate[i][j]);
-          m[i][j] *= p.act == BLOCK_GATE_SILU ? gate[i][j] * sg : sg;
+    for (int i = 0; i < VPT; ++i) {
+      ry[i].get(m[i]);
+      if (GATE) rz[i].get(z[i]);
+      if (RES) rx[i].get(x[i]);
+    }
+    if (row + step < p.rows) load();
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      float ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) ss = fmaf(m[i][j], m[i][j], ss);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        if (o < p.P) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (slot[i] >= 0) part[buf * np + slot[i]] = ss;
+    }
+    __syncthreads();
+    float rr = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      if (!live || col[i] >= p.D) continue;
+      float ss = 0.f;
+      for (int j = 0; j < per; ++j) ss += part[buf * np + first[i] + j];
+      const float inv = rsqrtf(fmaf(ss, inv_g, p.eps));
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) m[i][j] *= inv * w[i][j];
+      if (GATE) {
+        if (p.act == BLOCK_GATE_SILU) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) m[i][j] *= z[i][j] * sigmoid_fast(z[i][j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) m[i][j] *= sigmoid_fast(z[i][j]);
         }
       }
-      if (p.scale) {
-        load_w<VEC>(p.scale + c, w);
+      if (RES) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) m[i][j] *= w[j];
+        for (int j = 0; j < VEC; ++j) m[i][j] += x[i][j];
       }
+      if (NEXT) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        m[i][j] += res[i][j];
-        rr = fmaf(m[i][j], m[i][j], rr);
+        for (int j = 0; j < VEC; ++j) rr = fmaf(m[i][j], m[i][j], rr);
       }
-      store_vec<TS, VEC>(static_cast<TS*>(p.out) + row * p.st.out + c, m[i]);
+      store_vec<TS, VEC>(po + col[i], m[i]);
     }
-  }
-  if (!p.w_next) return;
-  float* rpart = part + p.pieces / p.P;
+    po += so;
+    if (NEXT) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) rr += __shfl_xor_sync(0xffffffffu, rr, o);
-  if (lane == 0) rpart[warp] = rr;
-  __syncthreads();
-  float tot = 0.f;
-  for (int j = 0; j < (nt >> 5); ++j) tot += rpart[j];
-  const float inv = rsqrtf(tot / (float)p.D + p.eps);
+      for (int o = 16; o > 0; o >>= 1) rr += __shfl_xor_sync(0xffffffffu, rr, o);
+      if (lane == 0) rpart[buf * nw + warp] = rr;
+      __syncthreads();
+      float tot = 0.f;
+      for (int j = 0; j < nw; ++j) tot += rpart[buf * nw + j];
+      const float inv = rsqrtf(fmaf(tot, inv_d, p.eps));
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = (i * nt + tid) * VEC;
-    if (c < p.D) {
-      float w[VEC];
-      load_w<VEC>(p.w_next + c, w);
+      for (int i = 0; i < VPT; ++i) {
+        if (!live || col[i] >= p.D) continue;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) m[i][j] *= inv * w[j];
-      store_vec<T, VEC>(static_cast<T*>(p.h) + row * p.st.h + c, m[i]);
+        for (int j = 0; j < VEC; ++j) m[i][j] *= inv * wn[i][j];
+        store_vec<T, VEC>(ph + col[i], m[i]);
+      }
+      ph += shh;
     }
   }
 }
 
-template <typename T, typename TS, int VEC, int VPT>
-int launch_norm(const BlockNormArgs& a, NormParams p) {
+template <typename T, typename TS, int VEC, int VPT, int PARTS>
+int launch_parts(const BlockNormArgs& a, NormParams p) {
+  auto kern = block_norm_kernel<T, TS, VEC, VPT, PARTS>;
+  static const int regs = [&] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
+  }();
+  if (regs == 0) return TTT_ERR_CUDA;
   p.pieces = a.D / VEC;
   p.gpieces = a.group / VEC;
   p.P = 1;
   while (p.P < 32 && p.gpieces % (2 * p.P) == 0) p.P *= 2;
-  const int nt = ((p.pieces + VPT - 1) / VPT + 31) / 32 * 32;
-  const int smem = (p.pieces / p.P + 32) * 4;
-  auto kern = block_norm_kernel<T, TS, VEC, VPT>;
+  p.nt = ((p.pieces + VPT - 1) / VPT + 31) / 32 * 32;
+  // rows per CTA: up to 256 threads; CTAs: what the SMs hold of them at once, so
+  // that all run to the end together
+  const int ny = p.nt >= 256 ? 1 : 256 / p.nt, threads = p.nt * ny;
+  const int smem = ny * 2 * (p.pieces / p.P + p.nt / 32) * 4;
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return TTT_ERR_CUDA;
+  int per_sm = 65536 / ((regs + 7) / 8 * 8 * threads);
+  per_sm = per_sm < 1 ? 1 : per_sm > 2048 / threads ? 2048 / threads : per_sm;
   const double n = (double)a.rows * a.D;
   ProfScope ps(PT_BLOCK_NORM, a.stream, 0.0,
                n * (sizeof(T) * (1 + (a.gate ? 1 : 0) + (a.h ? 1 : 0)) +
                     sizeof(TS) * (1 + (a.residual ? 1 : 0))));
-  kern<<<(unsigned)a.rows, nt, smem, a.stream>>>(p);
+  const long long ctas = (a.rows + ny - 1) / ny, most = 152ll * per_sm;
+  kern<<<(unsigned)(ctas < most ? ctas : most), threads, smem, a.stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+}
+
+template <typename T, typename TS>
+int launch_narrow(const BlockNormArgs& a, const NormParams& p) {
+  switch ((a.gate ? 4 : 0) | (a.residual ? 2 : 0) | (a.h ? 1 : 0)) {
+    case 0: return launch_parts<T, TS, 8, 1, 0>(a, p);
+    case 1: return launch_parts<T, TS, 8, 1, 1>(a, p);
+    case 2: return launch_parts<T, TS, 8, 1, 2>(a, p);
+    case 3: return launch_parts<T, TS, 8, 1, 3>(a, p);
+    case 4: return launch_parts<T, TS, 8, 1, 4>(a, p);
+    case 5: return launch_parts<T, TS, 8, 1, 5>(a, p);
+    case 6: return launch_parts<T, TS, 8, 1, 6>(a, p);
+    default: return launch_parts<T, TS, 8, 1, 7>(a, p);
+  }
 }
 
 template <typename T, typename TS>
@@ -213,12 +318,11 @@ int norm_t(const BlockNormArgs& a, const NormParams& p) {
                     a.st.y % 8 == 0 && a.st.gate % 8 == 0 && a.st.residual % 8 == 0 &&
                     a.st.out % 8 == 0 && a.st.h % 8 == 0;
   if (wide) {
-    if (a.D <= 8192) return launch_norm<T, TS, 8, 1>(a, p);
-    return launch_norm<T, TS, 8, 2>(a, p);
+    if (a.D <= 8 * 256) return launch_narrow<T, TS>(a, p);
+    return launch_parts<T, TS, 8, 4, -1>(a, p);
   }
-  if (a.D <= 1024) return launch_norm<T, TS, 1, 1>(a, p);
-  if (a.D <= 4096) return launch_norm<T, TS, 1, 4>(a, p);
-  return launch_norm<T, TS, 1, 16>(a, p);
+  if (a.D <= 4 * 512) return launch_parts<T, TS, 1, 4, -1>(a, p);
+  return launch_parts<T, TS, 1, 32, -1>(a, p);
 }
 
 }  // namespace
@@ -227,6 +331,7 @@ int block_norm_launch(const BlockNormArgs& a) {
   NormParams p{};
   p.y = a.y; p.w = a.w; p.gate = a.gate; p.residual = a.residual;
   p.scale = a.scale; p.w_next = a.w_next; p.out = a.out; p.h = a.h;
+  p.rows = a.rows;
   p.D = a.D; p.group = a.group; p.act = a.act; p.eps = a.eps;
   p.st = a.st;
   using B = __nv_bfloat16;
