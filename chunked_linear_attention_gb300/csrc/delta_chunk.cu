@@ -91,49 +91,46 @@ struct ScanParams {
 
 struct Item {
   int h, tile, batch, t0, len, chunk0;
-  int unit;                // carry pass: the unit matrix's rows, v = 0
   const float* from;       // start state [dv][dk] of this head, or NULL
   float* to;               // end state, or NULL
-  int rows;                // rows of the state
 };
 
-template <bool CARRY>
-__device__ __forceinline__ Item get_item(const ScanParams& p, int i) {
-  const int tiles = p.tiles + (CARRY ? 1 : 0);
-  Item it;
-  it.tile = i % tiles;
-  const int sh = i / tiles, seg = sh / p.Hv;
-  it.h = sh % p.Hv;
+__device__ __forceinline__ SegPlan get_segment(const ScanParams& p, int seg) {
+  if (p.segs) return p.segs[seg];
   SegPlan sg;
-  if (p.segs) {
-    sg = p.segs[seg];
-  } else {
-    sg.seq = seg / p.seg_n;
-    sg.j = seg % p.seg_n;
-    sg.n = p.seg_n;
-  }
-  const bool last = sg.j == sg.n - 1;
-  it.unit = CARRY && it.tile == p.tiles;
-  it.rows = it.unit ? p.dk : p.dv;
+  sg.seq = seg / p.seg_n;
+  sg.j = seg % p.seg_n;
+  sg.n = p.seg_n;
+  sg.pad = 0;
+  return sg;
+}
+
+// The tokens of a segment, in an item.
+__device__ __forceinline__ void set_range(const ScanParams& p, const SegPlan& sg, Item& it) {
+  const SeqPlan sp = seq_plan(p.plan, sg.seq, p.N);
+  const int before = sg.j * p.seg_chunks;
+  it.batch = p.plan ? 0 : sg.seq;
+  it.t0 = sp.t0 + before * kC;
+  it.len = sg.j == sg.n - 1 ? sp.len - before * kC : p.seg_chunks * kC;
+  it.chunk0 = sp.chunk0 + before;
+}
+
+__device__ __forceinline__ Item get_item(const ScanParams& p, int i) {
+  Item it;
+  it.tile = i % p.tiles;
+  const int sh = i / p.tiles, seg = sh / p.Hv;
+  it.h = sh % p.Hv;
   it.from = nullptr;
   it.to = nullptr;
   it.batch = it.t0 = it.len = it.chunk0 = 0;
-  if (sg.seq < 0 || (CARRY && last)) return it;
-  const SeqPlan sp = seq_plan(p.plan, sg.seq, p.N);
-  it.batch = p.plan ? 0 : sg.seq;
-  it.t0 = sp.t0 + sg.j * p.seg_chunks * kC;
-  it.len = last ? sp.len - sg.j * p.seg_chunks * kC : p.seg_chunks * kC;
-  it.chunk0 = sp.chunk0 + sg.j * p.seg_chunks;
-  const long long one = (long long)p.dv * p.dk, sgh = (long long)seg * p.Hv + it.h;
+  const SegPlan sg = get_segment(p, seg);
+  if (sg.seq < 0) return it;
+  set_range(p, sg, it);
+  const long long one = (long long)p.dv * p.dk;
   const long long sqh = (long long)sg.seq * p.Hv + it.h;
-  if (CARRY) {
-    it.to = it.unit ? p.P + sgh * p.dk * p.dk : p.L + sgh * one;
-    if (it.unit) it.tile = 0;
-  } else {
-    if (sg.j > 0) it.from = p.Sseg + sgh * one;
-    else if (p.S0) it.from = p.S0 + sqh * one;
-    if (last && p.S_final) it.to = p.S_final + sqh * one;
-  }
+  if (sg.j > 0) it.from = p.Sseg + ((long long)seg * p.Hv + it.h) * one;
+  else if (p.S0) it.from = p.S0 + sqh * one;
+  if (sg.j == sg.n - 1 && p.S_final) it.to = p.S_final + sqh * one;
   return it;
 }
 
@@ -214,9 +211,7 @@ __device__ __forceinline__ void stmatrix4_t(uint32_t saddr, const uint32_t (&w)[
 }
 
 // ---------------------------------------------------------------- the kernel
-// CARRY: the end states L and P of the segments, without outputs.
-template <bool CARRY>
-__global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
+__global__ void __launch_bounds__(768, 1)
     delta_scan_kernel(const __grid_constant__ ScanParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem =
@@ -235,7 +230,7 @@ __global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&B->rec_full[b], 1);
-      mbar_init(&B->rec_free[b], 1 + 16 + (CARRY ? 0 : 4));
+      mbar_init(&B->rec_free[b], 1 + 16 + 4);
     }
     mbar_init(&B->ks_full, 1);
     mbar_init(&B->y_ready, 16);
@@ -261,11 +256,11 @@ __global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
   };
 
   if (warp < 4) {
-    regs_dec<CARRY ? 64 : 56>();
+    regs_dec<56>();
     if (warp == 0) {
       int n = 0;
       for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
-        const Item it = get_item<CARRY>(p, i);
+        const Item it = get_item(p, i);
         const int hk = it.h / (p.Hv / p.Hk), nc = n_chunks(it.len);
         for (int c = 0; c < nc && ok; ++c, ++n) {
           const int s = n % kStages, r = n & 1;
@@ -274,23 +269,21 @@ __global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
           if (lane == 0) {
             uint8_t* st = smem + s * kStageBytes;
             const int t = it.t0 + c * kC;
-            mbar_arrive_expect_tx(&B->full[s], (2 + (CARRY ? 0 : 2) + (it.unit ? 0 : 2)) * kBlk);
+            mbar_arrive_expect_tx(&B->full[s], 6 * kBlk);
             for (int b = 0; b < 2; ++b) {
               tma_load_4d(st + (2 * b + 1) * kBlk, &p.k, 64 * b, t, hk, it.batch, &B->full[s]);
-              if (!CARRY) tma_load_4d(st + 2 * b * kBlk, &p.q, 64 * b, t, hk, it.batch, &B->full[s]);
+              tma_load_4d(st + 2 * b * kBlk, &p.q, 64 * b, t, hk, it.batch, &B->full[s]);
             }
-            if (!it.unit)
-              for (int b = 0; b < 2; ++b)
-                tma_load_4d(st + (4 + b) * kBlk, &p.v, 128 * it.tile + 64 * b, t, it.h, it.batch,
-                            &B->full[s]);
+            for (int b = 0; b < 2; ++b)
+              tma_load_4d(st + (4 + b) * kBlk, &p.v, 128 * it.tile + 64 * b, t, it.h, it.batch,
+                          &B->full[s]);
           }
           __syncwarp();
           wait(&B->rec_free[r], ((n >> 1) & 1) ^ 1);
           if (lane == 0 && ok) {
             const long long x = (long long)(it.chunk0 + c) * p.Hv + it.h;
-            constexpr uint32_t bytes = CARRY ? kRecBytes / 2 : kRecBytes;
-            mbar_arrive_expect_tx(&B->rec_full[r], bytes + sizeof(RecScal));
-            bulk_load_g2s(rec + r * kRecBytes, p.rec + x * kRecBytes, bytes, &B->rec_full[r]);
+            mbar_arrive_expect_tx(&B->rec_full[r], kRecBytes + sizeof(RecScal));
+            bulk_load_g2s(rec + r * kRecBytes, p.rec + x * kRecBytes, kRecBytes, &B->rec_full[r]);
             bulk_load_g2s(scal + r, p.scal + x, sizeof(RecScal), &B->rec_full[r]);
           }
           __syncwarp();
@@ -310,9 +303,8 @@ __global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
       const uint32_t id128 = idesc_bf16_f32(128, 0, 1);      // B = K^T, MN-major
       int n = 0;
       for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
-        const Item it = get_item<CARRY>(p, i);
+        const Item it = get_item(p, i);
         const int nc = n_chunks(it.len);
-        const bool has_v = !it.unit;
         for (int c = 0; c < nc && ok; ++c, ++n) {
           const uint32_t st = base + (n % kStages) * kStageBytes;
           const uint32_t rb = recb + (n & 1) * kRecBytes;
@@ -324,7 +316,7 @@ __global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
           wait(&B->rec_full[ph], (n >> 1) & 1);
           if (n > 0) wait(&B->ds_full, ph ^ 1);
           tc_fence_after();
-          if (el && has_v) {
+          if (el) {
             const uint64_t vd = smem_desc_sw128(st + 4 * kBlk, kBlk, 1024);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -352,7 +344,7 @@ __global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t y = tmem + kKS + k * 16;
-              umma_ts(tmem + kX, y + 8, th + k * 2, id64, has_v || k != 0);
+              umma_ts(tmem + kX, y + 8, th + k * 2, id64, 1);
               umma_ts(tmem + kX, y, tl + k * 2, id64, 1);
               umma_ts(tmem + kX, y, th + k * 2, id64, 1);
             }
@@ -360,18 +352,16 @@ __global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
           }
           __syncwarp();
           // S Q^T
-          if (!CARRY) {
-            wait(&B->o_free, ph ^ 1);
-            tc_fence_after();
-            if (el) {
-              const uint64_t qd = smem_desc_sw128(st, 16, 1024);
+          wait(&B->o_free, ph ^ 1);
+          tc_fence_after();
+          if (el) {
+            const uint64_t qd = smem_desc_sw128(st, 16, 1024);
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
-                umma_ts(tmem + kQS, tmem + kSh + (k >> 3) * 64 + (k & 7) * 8,
-                        qd + ((k >> 2) & 1) * (2 * kBlk / 16) + (k & 3) * 2, id64, k != 0);
-            }
-            __syncwarp();
+            for (int k = 0; k < 16; ++k)
+              umma_ts(tmem + kQS, tmem + kSh + (k >> 3) * 64 + (k & 7) * 8,
+                      qd + ((k >> 2) & 1) * (2 * kBlk / 16) + (k & 3) * 2, id64, k != 0);
           }
+          __syncwarp();
           // X^T K
           wait(&B->xs_ready, ph);
           tc_fence_after();
@@ -385,28 +375,25 @@ __global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
             }
             umma_commit(&B->ds_full);
             umma_commit(&B->empty[n % kStages]);
-            if (CARRY) umma_commit(&B->rec_free[ph]);
           }
           __syncwarp();
           // P X
-          if (!CARRY) {
-            wait(&B->x_ready, ph);
-            tc_fence_after();
-            if (el) {
-              const uint64_t pH = smem_desc_sw128(rb + 2 * kBlk, 16, 1024);
-              const uint64_t pL = smem_desc_sw128(rb + 3 * kBlk, 16, 1024);
+          wait(&B->x_ready, ph);
+          tc_fence_after();
+          if (el) {
+            const uint64_t pH = smem_desc_sw128(rb + 2 * kBlk, 16, 1024);
+            const uint64_t pL = smem_desc_sw128(rb + 3 * kBlk, 16, 1024);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t x = tmem + kXu + k * 16;
-                umma_ts(tmem + kO, x + 8, pH + k * 2, id64, k != 0);
-                umma_ts(tmem + kO, x, pL + k * 2, id64, 1);
-                umma_ts(tmem + kO, x, pH + k * 2, id64, 1);
-              }
-              umma_commit(&B->o_full);
-              umma_commit(&B->rec_free[ph]);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t x = tmem + kXu + k * 16;
+              umma_ts(tmem + kO, x + 8, pH + k * 2, id64, k != 0);
+              umma_ts(tmem + kO, x, pL + k * 2, id64, 1);
+              umma_ts(tmem + kO, x, pH + k * 2, id64, 1);
             }
-            __syncwarp();
+            umma_commit(&B->o_full);
+            umma_commit(&B->rec_free[ph]);
           }
+          __syncwarp();
         }
       }
       if (n > 0) {   // every arrival on this CTA's barriers has landed before it ends
@@ -416,7 +403,7 @@ __global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
     } else if (warp == 2) {
       int n = 0;
       for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
-        const Item it = get_item<CARRY>(p, i);
+        const Item it = get_item(p, i);
         const int nc = n_chunks(it.len);
         for (int c = 0; c < nc; ++c, ++n) {
           const int s = n % kStages;
@@ -436,12 +423,12 @@ __global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
     }
   } else if (warp < 20) {
     // ---- the chain: rows 32 q4 + lane, a quarter of the columns
-    regs_inc<CARRY ? 104 : 88>();
+    regs_inc<88>();
     const int q4 = warp & 3, part = (warp - 4) >> 2;
     const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
     int n = 0;
     for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
-      const Item it = get_item<CARRY>(p, i);
+      const Item it = get_item(p, i);
       const int nc = n_chunks(it.len);
       const int row = 128 * it.tile + 32 * q4 + lane;
       const long long so = (long long)row * p.dk + 32 * part;
@@ -453,12 +440,6 @@ __global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
           x = *reinterpret_cast<const float4*>(it.from + so + c);
         S[c / 2] = pack2(x.x, x.y);
         S[c / 2 + 1] = pack2(x.z, x.w);
-      }
-      if (CARRY && it.unit) {
-        const int d = row - 32 * part;   // this row's column of the unit matrix
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-          S[c] = pack2(d == 2 * c ? 1.f : 0.f, d == 2 * c + 1 ? 1.f : 0.f);
       }
       auto put_S = [&]() {
 #pragma unroll
@@ -499,14 +480,12 @@ __global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
         arrive(&B->xs_ready);
         const F2 eall = pack2(sc.eall, sc.eall);
         arrive(&B->rec_free[ph]);
-        if (!CARRY) {
-          if (n > 0) wait(&B->o_full, ph ^ 1);   // P X of the chunk before has read X
-          tc_fence_after();
-          put_pairs(tl + kXu + 16 * part, x);
-          tmem_wait_st();
-          tc_fence_before();
-          arrive(&B->x_ready);
-        }
+        if (n > 0) wait(&B->o_full, ph ^ 1);   // P X of the chunk before has read X
+        tc_fence_after();
+        put_pairs(tl + kXu + 16 * part, x);
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(&B->x_ready);
 
         wait(&B->ds_full, ph);
         tc_fence_after();
@@ -520,7 +499,7 @@ __global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
         }
         if (c + 1 < nc) put_S();
       }
-      if (ok && it.to && row < it.rows) {
+      if (ok && it.to && row < p.dv) {
 #pragma unroll
         for (int c = 0; c < 32; c += 4)
           if (32 * part + c < p.dk)
@@ -528,7 +507,7 @@ __global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
                 make_ulonglong2(S[c / 2], S[c / 2 + 1]);
       }
     }
-  } else if (!CARRY) {
+  } else {
     // ---- outputs
     regs_dec<72>();
     const int q4 = warp & 3;
@@ -541,7 +520,7 @@ __global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
     const uint32_t obs = smem_u32(ob);
     int n = 0;
     for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
-      const Item it = get_item<CARRY>(p, i);
+      const Item it = get_item(p, i);
       const int nc = n_chunks(it.len);
       const int col = 128 * it.tile + 32 * q4;
       __nv_bfloat16* out = p.out + it.batch * p.so.batch + it.h * p.so.head +
@@ -599,6 +578,326 @@ __global__ void __launch_bounds__(CARRY ? 640 : 768, 1)
           }
         }
         __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- L and P of the segments
+// The chain without outputs, for two units at once: a unit is 128 rows of L (start
+// state zero) or the rows of P (start state the unit matrix, v = 0).  The units of
+// a (segment, head) share k and T, and while one unit's products run, the other's
+// results are converted: the chain's steps wait on one another, so a single one
+// leaves the tensor cores idle two thirds of the time (4160 cycles a chunk for
+// one, 2 x 128 rows in about the same time for two).
+//
+// 256 TMEM columns per unit: S as pairs and later X^T K in the same 128 (S itself
+// is in registers, and its pairs are used up by then; both take 16 columns per 16
+// of d_k), S K^T and its pairs in 64, X and its pairs in 64.
+// Warps 4-11 and 12-19 are the units' chains: rows 32 (w % 4) .., half of the columns.
+constexpr int kCarryStages = 4;
+constexpr int kCarryBytes = 6 * kBlk;   // K0 K1 V0 V1, T hi, T lo
+constexpr uint32_t kUnitCols = 256, kUA = 128, kUX = 192;
+
+struct CarryBars {
+  uint64_t full[kCarryStages], ready[kCarryStages], empty[kCarryStages];
+  uint64_t ks_full[2], y_ready[2], x_full[2], xs_ready[2], ds_full[2], s_ready[2];
+  uint32_t tmem;
+};
+constexpr int kCarrySmem = kCarryStages * (kCarryBytes + (int)sizeof(RecScal)) +
+                           (int)sizeof(CarryBars) + 1024;
+static_assert(kCarrySmem <= 227 * 1024, "shared memory");
+
+// Unit 0: a tile of L; unit 1: P, beside the first tile.
+struct CarryItem {
+  Item it;
+  long long sgh;           // (segment, head)
+};
+
+__device__ __forceinline__ CarryItem get_carry(const ScanParams& p, int i) {
+  CarryItem c;
+  c.it.tile = i % p.tiles;
+  const int sh = i / p.tiles, seg = sh / p.Hv;
+  c.it.h = sh % p.Hv;
+  c.it.len = 0;
+  c.sgh = (long long)seg * p.Hv + c.it.h;
+  const SegPlan sg = get_segment(p, seg);
+  if (sg.seq >= 0 && sg.j < sg.n - 1) set_range(p, sg, c.it);
+  return c;
+}
+
+__global__ void __launch_bounds__(640, 1)
+    delta_carry_kernel(const __grid_constant__ ScanParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  RecScal* scal = reinterpret_cast<RecScal*>(smem + kCarryStages * kCarryBytes);
+  CarryBars* B = reinterpret_cast<CarryBars*>(scal + kCarryStages);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kCarryStages; ++s) {
+      mbar_init(&B->full[s], 1);
+      mbar_init(&B->ready[s], 1);
+      mbar_init(&B->empty[s], 1 + 16);
+    }
+    for (int u = 0; u < 2; ++u) {
+      mbar_init(&B->ks_full[u], 1);
+      mbar_init(&B->y_ready[u], 8);
+      mbar_init(&B->x_full[u], 1);
+      mbar_init(&B->xs_ready[u], 8);
+      mbar_init(&B->ds_full[u], 1);
+      mbar_init(&B->s_ready[u], 8);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(&B->tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B->tmem;
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { wait_w(ok, bar, parity, p.status, p.wait_ns); };
+  auto arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+
+  if (warp < 4) {
+    regs_dec<64>();
+    if (warp == 0) {
+      int n = 0;
+      for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+        const CarryItem ci = get_carry(p, i);
+        const int hk = ci.it.h / (p.Hv / p.Hk), nc = n_chunks(ci.it.len);
+        for (int c = 0; c < nc && ok; ++c, ++n) {
+          const int s = n % kCarryStages;
+          wait(&B->empty[s], ((n / kCarryStages) & 1) ^ 1);
+          if (!ok) break;
+          if (lane == 0) {
+            uint8_t* st = smem + s * kCarryBytes;
+            const int t = ci.it.t0 + c * kC;
+            const long long x = (long long)(ci.it.chunk0 + c) * p.Hv + ci.it.h;
+            mbar_arrive_expect_tx(&B->full[s], kCarryBytes + sizeof(RecScal));
+            for (int b = 0; b < 2; ++b)
+              tma_load_4d(st + b * kBlk, &p.k, 64 * b, t, hk, ci.it.batch, &B->full[s]);
+            for (int b = 0; b < 2; ++b)
+              tma_load_4d(st + (2 + b) * kBlk, &p.v, 128 * ci.it.tile + 64 * b, t, ci.it.h,
+                          ci.it.batch, &B->full[s]);
+            bulk_load_g2s(st + 4 * kBlk, p.rec + x * kRecBytes, 2 * kBlk, &B->full[s]);
+            bulk_load_g2s(scal + s, p.scal + x, sizeof(RecScal), &B->full[s]);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok)   // copies still on their way into this CTA's shared memory
+        for (int m = n > kCarryStages ? n - kCarryStages : 0; m < n; ++m)
+          mbar_wait_w(&B->full[m % kCarryStages], (m / kCarryStages) & 1, p.status, p.wait_ns);
+    } else if (warp == 1) {
+      const bool el = elect_lane();
+      const uint32_t base = smem_u32(smem);
+      const uint32_t id64 = idesc_bf16_f32(64, 0, 0);
+      const uint32_t id64m = idesc_bf16_f32(64, 1, 0);
+      const uint32_t id128 = idesc_bf16_f32(128, 0, 1);
+      int n = 0;
+      uint32_t nu1 = 0;   // chunks of unit 1
+      for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+        const CarryItem ci = get_carry(p, i);
+        const int nc = n_chunks(ci.it.len), units = ci.it.tile == 0 ? 2 : 1;
+        for (int c = 0; c < nc && ok; ++c, ++n) {
+          const int s = n % kCarryStages;
+          const uint32_t st = base + s * kCarryBytes;
+          const uint64_t th = smem_desc_sw128(st + 4 * kBlk, 16, 1024);
+          const uint64_t tl = smem_desc_sw128(st + 5 * kBlk, 16, 1024);
+          const uint32_t ph[2] = {(uint32_t)n & 1, nu1 & 1};
+          wait(&B->ready[s], (n / kCarryStages) & 1);
+          // T V, once the chunk before is done with X's columns
+          if (n > 0) wait(&B->ds_full[0], ph[0] ^ 1);
+          tc_fence_after();
+          if (el) {
+            const uint64_t vd = smem_desc_sw128(st + 2 * kBlk, kBlk, 1024);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              umma_bf16(tmem + kUX, vd + k * 128, tl + k * 2, id64m, k != 0);
+              umma_bf16(tmem + kUX, vd + k * 128, th + k * 2, id64m, 1);
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {   // S K^T
+            if (u >= units) break;
+            const uint32_t d = tmem + u * kUnitCols;
+            wait(&B->s_ready[u], ph[u]);
+            tc_fence_after();
+            if (el) {
+              const uint64_t kd = smem_desc_sw128(st, 16, 1024);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint64_t b = kd + (k >> 2) * (kBlk / 16) + (k & 3) * 2;
+                umma_ts(d + kUA, d + 16 * k + 8, b, id64, k != 0);
+                umma_ts(d + kUA, d + 16 * k, b, id64, 1);
+              }
+              umma_commit(&B->ks_full[u]);
+            }
+            __syncwarp();
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {   // X += T (-e^G K S^T)
+            if (u >= units) break;
+            const uint32_t d = tmem + u * kUnitCols;
+            wait(&B->y_ready[u], ph[u]);
+            tc_fence_after();
+            if (el) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t y = d + kUA + 16 * k;
+                umma_ts(d + kUX, y + 8, th + k * 2, id64, u == 0 || k != 0);
+                umma_ts(d + kUX, y, tl + k * 2, id64, 1);
+                umma_ts(d + kUX, y, th + k * 2, id64, 1);
+              }
+              umma_commit(&B->x_full[u]);
+            }
+            __syncwarp();
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {   // X^T K
+            if (u >= units) break;
+            const uint32_t d = tmem + u * kUnitCols;
+            wait(&B->xs_ready[u], ph[u]);
+            tc_fence_after();
+            if (el) {
+              const uint64_t km = smem_desc_sw128(st, kBlk, 1024);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t x = d + kUX + 16 * k;
+                umma_ts(d, x + 8, km + k * 128, id128, k != 0);
+                umma_ts(d, x, km + k * 128, id128, 1);
+              }
+              umma_commit(&B->ds_full[u]);
+              if (u == units - 1) umma_commit(&B->empty[s]);
+            }
+            __syncwarp();
+          }
+          if (units == 2) ++nu1;
+        }
+      }
+      if (n > 0)   // every arrival on this CTA's barriers has landed before it ends
+        wait(&B->empty[(n - 1) % kCarryStages], ((n - 1) / kCarryStages) & 1);
+    } else if (warp == 2) {
+      int n = 0;
+      for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
+        const CarryItem ci = get_carry(p, i);
+        const int nc = n_chunks(ci.it.len);
+        // (segments before a sequence's last one hold whole chunks: nothing to zero)
+        for (int c = 0; c < nc; ++c, ++n) {
+          wait(&B->full[n % kCarryStages], (n / kCarryStages) & 1);
+          arrive(&B->ready[n % kCarryStages]);
+        }
+      }
+    }
+  } else {
+    regs_inc<104>();
+    const int q4 = warp & 3, half = ((warp - 4) >> 2) & 1, u = (warp - 4) >> 3;
+    const uint32_t d = tmem + u * kUnitCols + ((uint32_t)(q4 * 32) << 16);
+    int n = 0;
+    uint32_t m = 0;   // chunks of this unit
+    for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
+      const CarryItem ci = get_carry(p, i);
+      const int nc = n_chunks(ci.it.len);
+      if (nc == 0) continue;
+      if (u == 1 && ci.it.tile != 0) {   // no unit here: pass the stages on
+        for (int c = 0; c < nc; ++c, ++n) {
+          wait(&B->ready[n % kCarryStages], (n / kCarryStages) & 1);
+          arrive(&B->empty[n % kCarryStages]);
+        }
+        continue;
+      }
+      const bool is_p = u == 1;
+      const int row = 32 * q4 + lane;
+      F2 S[32];
+      {
+        const int one = is_p ? row - 64 * half : -1;   // this row's column of the unit matrix
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          S[c] = pack2(one == 2 * c ? 1.f : 0.f, one == 2 * c + 1 ? 1.f : 0.f);
+      }
+      auto put_S = [&]() {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) split2(S[8 * b + e], hi[e], lo[e]);
+          tmem_st8(d + 64 * half + 16 * b, hi);
+          tmem_st8(d + 64 * half + 16 * b + 8, lo);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(&B->s_ready[u]);
+      };
+      put_S();
+#pragma unroll 1
+      for (int c = 0; c < nc; ++c, ++n, ++m) {
+        const int s = n % kCarryStages;
+        const uint32_t ph = m & 1;
+        const RecScal& sc = scal[s];
+        wait(&B->ready[s], (n / kCarryStages) & 1);
+        wait(&B->ks_full[u], ph);
+        tc_fence_after();
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const uint32_t a = d + kUA + 32 * half + 16 * b;
+          float x[16];
+          tmem_ld16_nowait(a, x);
+          tmem_wait_bind(x);
+          put_scaled(a, x, &sc.neg[32 * half + 16 * b]);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(&B->y_ready[u]);
+
+        wait(&B->x_full[u], ph);
+        tc_fence_after();
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const uint32_t a = d + kUX + 32 * half + 16 * b;
+          float x[16];
+          tmem_ld16_nowait(a, x);
+          tmem_wait_bind(x);
+          put_scaled(a, x, &sc.er[32 * half + 16 * b]);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(&B->xs_ready[u]);
+        const F2 eall = pack2(sc.eall, sc.eall);
+        arrive(&B->empty[s]);
+
+        wait(&B->ds_full[u], ph);
+        tc_fence_after();
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          float x[16];
+          tmem_ld16_nowait(d + 64 * half + 16 * b, x);
+          tmem_wait_bind(x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            S[8 * b + e] = fma2(eall, S[8 * b + e], pack2(x[2 * e], x[2 * e + 1]));
+        }
+        if (c + 1 < nc) put_S();
+      }
+      const int grow = is_p ? row : 128 * ci.it.tile + row, rows = is_p ? p.dk : p.dv;
+      float* to = is_p ? p.P + ci.sgh * p.dk * p.dk : p.L + ci.sgh * p.dv * p.dk;
+      if (ok && grow < rows) {
+#pragma unroll
+        for (int c = 0; c < 64; c += 4)
+          if (64 * half + c < p.dk)
+            *reinterpret_cast<ulonglong2*>(to + (long long)grow * p.dk + 64 * half + c) =
+                make_ulonglong2(S[c / 2], S[c / 2 + 1]);
       }
     }
   }
@@ -814,7 +1113,7 @@ int prepare() {
       return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
              cudaSuccess;
     };
-    if (room(delta_scan_kernel<false>, kSmem) && room(delta_scan_kernel<true>, kSmem) &&
+    if (room(delta_scan_kernel, kSmem) && room(delta_carry_kernel, kCarrySmem) &&
         room(delta_join_kernel<4>, sizeof(JoinShared<4>)) &&
         room(delta_join_kernel<8>, sizeof(JoinShared<8>)) &&
         room(delta_join_kernel<16>, sizeof(JoinShared<16>)) &&
@@ -849,7 +1148,7 @@ Plan make_plan(int B, int Hv, int N, int dk, int dv, int n_seq, bool packed) {
   for (int n = 1; n <= 64 && n <= nc; ++n) {
     const int lc = (nc + n - 1) / n;
     const long long out = (units * tiles * n + kSms - 1) / kSms * lc;
-    const long long carry = n > 1 ? (units * (tiles + 1) * (n - 1) + kSms - 1) / kSms * lc + n : 0;
+    const long long carry = n > 1 ? (units * tiles * (n - 1) + kSms - 1) / kSms * lc + n : 0;
     if (n == 1 || out + carry < best) {
       best = out + carry;
       p.seg_n = n;
@@ -964,10 +1263,10 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
   if (launch_delta_prep(r, pl.chunks, a.stream) != cudaSuccess) return TTT_ERR_CUDA;
   if (pl.split) {
     {
-      p.items = pl.seg_places * a.Hv * (p.tiles + 1);
+      p.items = pl.seg_places * a.Hv * p.tiles;
       ProfScope ps(PT_DELTA_CARRY, a.stream, 5.0 * tok * a.Hv * a.dk * (a.dv + a.dk),
                    tok * 2.0 * (a.Hk * a.dk + a.Hv * a.dv));
-      delta_scan_kernel<true><<<p.items < sms ? p.items : sms, 640, kSmem, a.stream>>>(p);
+      delta_carry_kernel<<<p.items < sms ? p.items : sms, 640, kCarrySmem, a.stream>>>(p);
       if (cudaGetLastError() != cudaSuccess) return TTT_ERR_CUDA;
     }
     JoinParams j;
@@ -994,7 +1293,7 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
   p.items = pl.seg_places * a.Hv * p.tiles;
   ProfScope ps(PT_DELTA_CHUNK, a.stream, 7.0 * tok * a.Hv * a.dk * a.dv,
                tok * 4.0 * (a.Hk * a.dk + a.Hv * a.dv));
-  delta_scan_kernel<false><<<p.items < sms ? p.items : sms, 768, kSmem, a.stream>>>(p);
+  delta_scan_kernel<<<p.items < sms ? p.items : sms, 768, kSmem, a.stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 

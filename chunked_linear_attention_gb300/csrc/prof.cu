@@ -32,7 +32,7 @@ const char* kTagKernel[PT_COUNT] = {
     "umma_gemm_kernel", "linattn_prefix_kernel", "umma_gemm_kernel", "umma_gemm_kernel",
     "ns_cluster_kernel", "ns_half_kernel", "linattn_fused_kernel",
     "umma_gemm_kernel", "umma_gemm_kernel", "umma_gemm_kernel", "delta_plan_kernel",
-    "delta_prep_kernel", "delta_scan_kernel", "delta_join_kernel", "delta_scan_kernel",
+    "delta_prep_kernel", "delta_carry_kernel", "delta_join_kernel", "delta_scan_kernel",
     "delta_recurrent_kernel", "delta_step_kernel", "block_norm_kernel"};
 
 }  // namespace
