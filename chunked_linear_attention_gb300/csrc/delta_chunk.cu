@@ -24,15 +24,14 @@
 // v = 0) are computed for all segments at once, the start states follow by
 // S_{j+1} = S_j P_j + L_j, and all segments run at once.
 //
-// Roles (768 threads, one CTA per SM, persistent over (segment, head, d_v tile)):
+// Roles (512 threads, one CTA per SM, persistent over (segment, head, d_v tile)):
 //   warp 0      TMA: q, k, v in three stages, the chunk's records in two.
 //   warp 1      all MMAs.
 //   warp 2      zeroes the rows behind a sequence's end, so that other
 //               sequences' values cannot reach it.
-//   warps 4-19  the chain S -> K S^T -> X -> S: warp w has rows 32 (w % 4) .. and a
-//               quarter of the columns (conversions are bound by instruction
-//               latency with fewer warps).
-//   warps 20-23 the outputs.
+//   warps 4-11  the chain S -> K S^T -> X -> S: warp w has rows 32 (w % 4) .. and half
+//               of the columns, and hands them to the MMAs 16 at a time.
+//   warps 12-15 the outputs.
 #include <mutex>
 
 #include "builder.h"
@@ -49,7 +48,8 @@ constexpr int kStageBytes = 6 * kBlk;   // Q0 K0 Q1 K1 V0 V1 (column blocks of 6
 struct Bars {
   uint64_t full[kStages], ready[kStages], empty[kStages];
   uint64_t rec_full[2], rec_free[2];
-  uint64_t ks_full, y_ready, x_full, xs_ready, ds_full, x_ready, s_ready;
+  uint64_t ks_full, x_full, ds_full, x_ready;
+  uint64_t y_ready[2], xs_ready[2], s_ready[4];
   uint64_t o_full, o_free;
   uint32_t tmem;
 };
@@ -64,27 +64,32 @@ constexpr uint32_t kXu = 0;      // 64: X as a pair
 constexpr uint32_t kQS = 64;     // 64: S Q^T
 constexpr uint32_t kKS = 128;    // 64: S K^T, then its pair in the same columns
 constexpr uint32_t kDS = 128;    // 128: X^T K (after K S^T is used up)
-constexpr uint32_t kSh = 256;    // 64 + 64: S, hi and lo
+constexpr uint32_t kSh = 256;    // 128: S, for each 16 of d_k 8 columns of hi and 8 of lo
 constexpr uint32_t kX = 384;     // 64: X, then e^{G_63 - G} X as a pair
 constexpr uint32_t kO = 448;     // 64: P X
+
+constexpr int kPBytes = 65536;
+constexpr int kStateFloats = 128 * 128;   // a tile of the state between the kernels
 
 struct ScanParams {
   CUtensorMap q, k, v;
   const SeqPlan* plan;     // packed sequences, or NULL
-  const SegPlan* segs;     // likewise
+  const SegPlan* segs;     // likewise, as are
+  const int* order;        // the segments' places, a sequence's last ones at the end,
+  const int* counts;       // and how many are not a last one, all, and sequences of several
   const uint8_t* rec;
   const RecScal* scal;
   const float* S0;
-  const float* Sseg;       // start states of the segments behind the first
+  const float* Sseg;       // [segment][Hv][tile] start states of the segments behind the first
   float* S_final;
-  float* L;                // [segment][Hv][dv][dk] (the carry pass)
-  float* P;                // [segment][Hv][dk][dk]
+  float* L;                // [segment][Hv][tile] (the carry pass)
+  uint8_t* P;              // [segment][Hv]: 128 x 128 pairs, as the join's operand tiles
   __nv_bfloat16* out;
   int* status;
   unsigned long long wait_ns;
   delta_rule_stride so;
-  int Hk, Hv, N, dk, dv, tiles, items;
-  int seg_chunks, seg_n;   // chunks per segment; segments per sequence (not packed)
+  int Hk, Hv, N, dk, dv, tiles;
+  int seqs, seg_chunks, seg_n;   // chunks per segment; segments per sequence (not packed)
   float scale;
   int wide_out;            // rows of out can be stored 16 bytes at a time
 };
@@ -92,17 +97,36 @@ struct ScanParams {
 struct Item {
   int h, tile, batch, t0, len, chunk0;
   const float* from;       // start state [dv][dk] of this head, or NULL
+  const float* from_tile;  // or a tile as the join left it
   float* to;               // end state, or NULL
 };
 
-__device__ __forceinline__ SegPlan get_segment(const ScanParams& p, int seg) {
-  if (p.segs) return p.segs[seg];
+// The k-th segment: whole ones first, so that a round of the SMs is of one length;
+// the last ones of the sequences (of any length) behind them.
+__device__ __forceinline__ SegPlan get_segment(const ScanParams& p, int k, int& place) {
+  if (p.segs) {
+    place = p.order[k];
+    return p.segs[place];
+  }
+  const int whole = p.seqs * (p.seg_n - 1);
   SegPlan sg;
-  sg.seq = seg / p.seg_n;
-  sg.j = seg % p.seg_n;
   sg.n = p.seg_n;
   sg.pad = 0;
+  if (k < whole) {
+    sg.seq = k / (p.seg_n - 1);
+    sg.j = k - sg.seq * (p.seg_n - 1);
+  } else {
+    sg.seq = k - whole;
+    sg.j = p.seg_n - 1;
+  }
+  place = sg.seq * p.seg_n + sg.j;
   return sg;
+}
+
+// Items of the carry pass (no last segments) and of the outputs' pass.
+__device__ __forceinline__ int n_items(const ScanParams& p, bool carry) {
+  const int n = p.counts ? p.counts[carry ? 0 : 1] : carry ? p.seqs * (p.seg_n - 1) : p.seqs * p.seg_n;
+  return n * p.Hv * p.tiles;
 }
 
 // The tokens of a segment, in an item.
@@ -118,17 +142,18 @@ __device__ __forceinline__ void set_range(const ScanParams& p, const SegPlan& sg
 __device__ __forceinline__ Item get_item(const ScanParams& p, int i) {
   Item it;
   it.tile = i % p.tiles;
-  const int sh = i / p.tiles, seg = sh / p.Hv;
+  const int sh = i / p.tiles;
   it.h = sh % p.Hv;
-  it.from = nullptr;
-  it.to = nullptr;
-  it.batch = it.t0 = it.len = it.chunk0 = 0;
-  const SegPlan sg = get_segment(p, seg);
-  if (sg.seq < 0) return it;
+  int place;
+  const SegPlan sg = get_segment(p, sh / p.Hv, place);
   set_range(p, sg, it);
+  it.from = it.from_tile = nullptr;
+  it.to = nullptr;
   const long long one = (long long)p.dv * p.dk;
   const long long sqh = (long long)sg.seq * p.Hv + it.h;
-  if (sg.j > 0) it.from = p.Sseg + ((long long)seg * p.Hv + it.h) * one;
+  if (sg.j > 0)
+    it.from_tile =
+        p.Sseg + (((long long)place * p.Hv + it.h) * p.tiles + it.tile) * kStateFloats;
   else if (p.S0) it.from = p.S0 + sqh * one;
   if (sg.j == sg.n - 1 && p.S_final) it.to = p.S_final + sqh * one;
   return it;
@@ -162,6 +187,33 @@ __device__ __forceinline__ void regs_inc() {
 template <int R>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// A 128 x 128 state between the kernels, in the order of the threads that hold it
+// (row 32 q4 + lane, 64 columns from 64 half, four at a time): a warp's access is
+// 512 bytes in one piece, where rows of d_k numbers would be 32 pieces of 16 bytes
+// (the join step took 5 us that way).  The float4 of columns 4 c ..:
+__device__ __forceinline__ long long state_at(int q4, int half, int c, int lane) {
+  return ((q4 * 2 + half) * 16 + c) * 32 + lane;
+}
+
+__device__ __forceinline__ void load_state(const float* tile, int q4, int half, int lane,
+                                           F2 (&S)[32]) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    const ulonglong2 w =
+        reinterpret_cast<const ulonglong2*>(tile)[state_at(q4, half, c, lane)];
+    S[2 * c] = w.x;
+    S[2 * c + 1] = w.y;
+  }
+}
+
+__device__ __forceinline__ void store_state(float* tile, int q4, int half, int lane,
+                                            const F2 (&S)[32]) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    reinterpret_cast<ulonglong2*>(tile)[state_at(q4, half, c, lane)] =
+        make_ulonglong2(S[2 * c], S[2 * c + 1]);
 }
 
 // 16 tokens' values of a row, each times f[token], as pairs at TMEM columns taddr
@@ -211,7 +263,7 @@ __device__ __forceinline__ void stmatrix4_t(uint32_t saddr, const uint32_t (&w)[
 }
 
 // ---------------------------------------------------------------- the kernel
-__global__ void __launch_bounds__(768, 1)
+__global__ void __launch_bounds__(512, 1)
     delta_scan_kernel(const __grid_constant__ ScanParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem =
@@ -221,6 +273,7 @@ __global__ void __launch_bounds__(768, 1)
   uint8_t* obuf = reinterpret_cast<uint8_t*>(scal + 2);   // outputs on their way
   Bars* B = reinterpret_cast<Bars*>(obuf + kOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int items = n_items(p, false);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -230,15 +283,17 @@ __global__ void __launch_bounds__(768, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&B->rec_full[b], 1);
-      mbar_init(&B->rec_free[b], 1 + 16 + 4);
+      mbar_init(&B->rec_free[b], 1 + 8 + 4);
     }
     mbar_init(&B->ks_full, 1);
-    mbar_init(&B->y_ready, 16);
     mbar_init(&B->x_full, 1);
-    mbar_init(&B->xs_ready, 16);
     mbar_init(&B->ds_full, 1);
-    mbar_init(&B->x_ready, 16);
-    mbar_init(&B->s_ready, 16);
+    mbar_init(&B->x_ready, 8);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&B->y_ready[b], 8);
+      mbar_init(&B->xs_ready[b], 8);
+    }
+    for (int b = 0; b < 4; ++b) mbar_init(&B->s_ready[b], 8);
     mbar_init(&B->o_full, 1);
     mbar_init(&B->o_free, 4);
     fence_mbar_init();
@@ -256,10 +311,10 @@ __global__ void __launch_bounds__(768, 1)
   };
 
   if (warp < 4) {
-    regs_dec<56>();
+    regs_dec<64>();
     if (warp == 0) {
       int n = 0;
-      for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
         const Item it = get_item(p, i);
         const int hk = it.h / (p.Hv / p.Hk), nc = n_chunks(it.len);
         for (int c = 0; c < nc && ok; ++c, ++n) {
@@ -302,7 +357,7 @@ __global__ void __launch_bounds__(768, 1)
       const uint32_t id64m = idesc_bf16_f32(64, 1, 0);       // A = V^T, MN-major
       const uint32_t id128 = idesc_bf16_f32(128, 0, 1);      // B = K^T, MN-major
       int n = 0;
-      for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
         const Item it = get_item(p, i);
         const int nc = n_chunks(it.len);
         for (int c = 0; c < nc && ok; ++c, ++n) {
@@ -326,31 +381,40 @@ __global__ void __launch_bounds__(768, 1)
           }
           __syncwarp();
           // S K^T
-          wait(&B->s_ready, ph);
-          tc_fence_after();
-          if (el) {
-            const uint64_t kd = smem_desc_sw128(st + kBlk, 16, 1024);
+          const uint64_t kd = smem_desc_sw128(st + kBlk, 16, 1024);
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              umma_ts(tmem + kKS, tmem + kSh + (k >> 3) * 64 + (k & 7) * 8,
-                      kd + ((k >> 2) & 1) * (2 * kBlk / 16) + (k & 3) * 2, id64, k != 0);
-            umma_commit(&B->ks_full);
-          }
-          __syncwarp();
-          // X += T (-e^G K S^T)
-          wait(&B->y_ready, ph);
-          tc_fence_after();
-          if (el) {
+          for (int b = 0; b < 4; ++b) {   // 16 of each half of d_k at a time
+            wait(&B->s_ready[b], ph);
+            tc_fence_after();
+            if (el) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t y = tmem + kKS + k * 16;
-              umma_ts(tmem + kX, y + 8, th + k * 2, id64, 1);
-              umma_ts(tmem + kX, y, tl + k * 2, id64, 1);
-              umma_ts(tmem + kX, y, th + k * 2, id64, 1);
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t a = tmem + kSh + 64 * h + 16 * b;
+                const uint64_t kb = kd + h * (2 * kBlk / 16) + b * 2;
+                umma_ts(tmem + kKS, a + 8, kb, id64, b + h != 0);
+                umma_ts(tmem + kKS, a, kb, id64, 1);
+              }
+              if (b == 3) umma_commit(&B->ks_full);
             }
-            umma_commit(&B->x_full);
+            __syncwarp();
           }
-          __syncwarp();
+          // X += T (-e^G K S^T)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {   // 16 of each half of the tokens at a time
+            wait(&B->y_ready[b], ph);
+            tc_fence_after();
+            if (el) {
+#pragma unroll
+              for (int k = b; k < 4; k += 2) {
+                const uint32_t y = tmem + kKS + k * 16;
+                umma_ts(tmem + kX, y + 8, th + k * 2, id64, 1);
+                umma_ts(tmem + kX, y, tl + k * 2, id64, 1);
+                umma_ts(tmem + kX, y, th + k * 2, id64, 1);
+              }
+              if (b == 1) umma_commit(&B->x_full);
+            }
+            __syncwarp();
+          }
           // S Q^T
           wait(&B->o_free, ph ^ 1);
           tc_fence_after();
@@ -358,25 +422,30 @@ __global__ void __launch_bounds__(768, 1)
             const uint64_t qd = smem_desc_sw128(st, 16, 1024);
 #pragma unroll
             for (int k = 0; k < 16; ++k)
-              umma_ts(tmem + kQS, tmem + kSh + (k >> 3) * 64 + (k & 7) * 8,
-                      qd + ((k >> 2) & 1) * (2 * kBlk / 16) + (k & 3) * 2, id64, k != 0);
+              umma_ts(tmem + kQS, tmem + kSh + (k >> 1) * 16 + (k & 1) * 8,
+                      qd + (k >> 3) * (2 * kBlk / 16) + ((k >> 1) & 3) * 2, id64, k != 0);
           }
           __syncwarp();
           // X^T K
-          wait(&B->xs_ready, ph);
-          tc_fence_after();
-          if (el) {
-            const uint64_t km = smem_desc_sw128(st + kBlk, 2 * kBlk, 1024);
+          const uint64_t km = smem_desc_sw128(st + kBlk, 2 * kBlk, 1024);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t x = tmem + kX + k * 16;
-              umma_ts(tmem + kDS, x + 8, km + k * 128, id128, k != 0);
-              umma_ts(tmem + kDS, x, km + k * 128, id128, 1);
+          for (int b = 0; b < 2; ++b) {
+            wait(&B->xs_ready[b], ph);
+            tc_fence_after();
+            if (el) {
+#pragma unroll
+              for (int k = b; k < 4; k += 2) {
+                const uint32_t x = tmem + kX + k * 16;
+                umma_ts(tmem + kDS, x + 8, km + k * 128, id128, k != 0);
+                umma_ts(tmem + kDS, x, km + k * 128, id128, 1);
+              }
+              if (b == 1) {
+                umma_commit(&B->ds_full);
+                umma_commit(&B->empty[n % kStages]);
+              }
             }
-            umma_commit(&B->ds_full);
-            umma_commit(&B->empty[n % kStages]);
+            __syncwarp();
           }
-          __syncwarp();
           // P X
           wait(&B->x_ready, ph);
           tc_fence_after();
@@ -402,7 +471,7 @@ __global__ void __launch_bounds__(768, 1)
       }
     } else if (warp == 2) {
       int n = 0;
-      for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
+      for (int i = blockIdx.x; i < items; i += gridDim.x) {
         const Item it = get_item(p, i);
         const int nc = n_chunks(it.len);
         for (int c = 0; c < nc; ++c, ++n) {
@@ -421,68 +490,81 @@ __global__ void __launch_bounds__(768, 1)
         }
       }
     }
-  } else if (warp < 20) {
-    // ---- the chain: rows 32 q4 + lane, a quarter of the columns
-    regs_inc<88>();
-    const int q4 = warp & 3, part = (warp - 4) >> 2;
+  } else if (warp < 12) {
+    // ---- the chain: rows 32 q4 + lane, half of the columns
+    regs_inc<168>();
+    const int q4 = warp & 3, half = (warp - 4) >> 2;
     const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
     int n = 0;
-    for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
+    for (int i = blockIdx.x; i < items; i += gridDim.x) {
       const Item it = get_item(p, i);
       const int nc = n_chunks(it.len);
       const int row = 128 * it.tile + 32 * q4 + lane;
-      const long long so = (long long)row * p.dk + 32 * part;
-      F2 S[16];
+      const long long so = (long long)row * p.dk + 64 * half;
+      F2 S[32];
+      if (it.from_tile) {
+        load_state(it.from_tile, q4, half, lane, S);
+      } else {
 #pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (it.from && row < p.dv && 32 * part + c < p.dk)
-          x = *reinterpret_cast<const float4*>(it.from + so + c);
-        S[c / 2] = pack2(x.x, x.y);
-        S[c / 2 + 1] = pack2(x.z, x.w);
+        for (int c = 0; c < 64; c += 4) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (it.from && row < p.dv && 64 * half + c < p.dk)
+            x = *reinterpret_cast<const float4*>(it.from + so + c);
+          S[c / 2] = pack2(x.x, x.y);
+          S[c / 2 + 1] = pack2(x.z, x.w);
+        }
       }
       auto put_S = [&]() {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < 4; ++b) {
           uint32_t hi[8], lo[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) split2(S[8 * b + e], hi[e], lo[e]);
-          tmem_st8(tl + kSh + 16 * part + 8 * b, hi);
-          tmem_st8(tl + kSh + 64 + 16 * part + 8 * b, lo);
+          tmem_st8(tl + kSh + 64 * half + 16 * b, hi);
+          tmem_st8(tl + kSh + 64 * half + 16 * b + 8, lo);
+          tmem_wait_st();
+          tc_fence_before();
+          arrive(&B->s_ready[b]);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        arrive(&B->s_ready);
       };
       if (nc > 0) put_S();
 #pragma unroll 1
       for (int c = 0; c < nc; ++c, ++n) {
         const uint32_t ph = n & 1;
         const RecScal& sc = scal[ph];
-        float x[16];
+        float x[2][16];
         wait(&B->rec_full[ph], (n >> 1) & 1);
         wait(&B->ks_full, ph);
         tc_fence_after();
-        tmem_ld16_nowait(tl + kKS + 16 * part, x);
-        tmem_wait_bind(x);
-        put_scaled(tl + kKS + 16 * part, x, &sc.neg[16 * part]);
-        tmem_wait_st();
-        tc_fence_before();
-        arrive(&B->y_ready);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const uint32_t a = tl + kKS + 32 * half + 16 * b;
+          tmem_ld16_nowait(a, x[b]);
+          tmem_wait_bind(x[b]);
+          put_scaled(a, x[b], &sc.neg[32 * half + 16 * b]);
+          tmem_wait_st();
+          tc_fence_before();
+          arrive(&B->y_ready[b]);
+        }
 
         wait(&B->x_full, ph);
         tc_fence_after();
-        tmem_ld16_nowait(tl + kX + 16 * part, x);
-        tmem_wait_bind(x);
-        put_scaled(tl + kX + 16 * part, x, &sc.er[16 * part]);
-        tmem_wait_st();
-        tc_fence_before();
-        arrive(&B->xs_ready);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const uint32_t a = tl + kX + 32 * half + 16 * b;
+          tmem_ld16_nowait(a, x[b]);
+          tmem_wait_bind(x[b]);
+          put_scaled(a, x[b], &sc.er[32 * half + 16 * b]);
+          tmem_wait_st();
+          tc_fence_before();
+          arrive(&B->xs_ready[b]);
+        }
         const F2 eall = pack2(sc.eall, sc.eall);
         arrive(&B->rec_free[ph]);
         if (n > 0) wait(&B->o_full, ph ^ 1);   // P X of the chunk before has read X
         tc_fence_after();
-        put_pairs(tl + kXu + 16 * part, x);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) put_pairs(tl + kXu + 32 * half + 16 * b, x[b]);
         tmem_wait_st();
         tc_fence_before();
         arrive(&B->x_ready);
@@ -490,26 +572,26 @@ __global__ void __launch_bounds__(768, 1)
         wait(&B->ds_full, ph);
         tc_fence_after();
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          tmem_ld16_nowait(tl + kDS + 32 * part + 16 * b, x);
-          tmem_wait_bind(x);
+        for (int b = 0; b < 4; ++b) {
+          tmem_ld16_nowait(tl + kDS + 64 * half + 16 * b, x[0]);
+          tmem_wait_bind(x[0]);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            S[8 * b + e] = fma2(eall, S[8 * b + e], pack2(x[2 * e], x[2 * e + 1]));
+            S[8 * b + e] = fma2(eall, S[8 * b + e], pack2(x[0][2 * e], x[0][2 * e + 1]));
         }
         if (c + 1 < nc) put_S();
       }
       if (ok && it.to && row < p.dv) {
 #pragma unroll
-        for (int c = 0; c < 32; c += 4)
-          if (32 * part + c < p.dk)
+        for (int c = 0; c < 64; c += 4)
+          if (64 * half + c < p.dk)
             *reinterpret_cast<ulonglong2*>(it.to + so + c) =
                 make_ulonglong2(S[c / 2], S[c / 2 + 1]);
       }
     }
   } else {
     // ---- outputs
-    regs_dec<72>();
+    regs_dec<104>();
     const int q4 = warp & 3;
     const float nscale = -p.scale;
     const F2 nscale2 = pack2(nscale, nscale);
@@ -519,7 +601,7 @@ __global__ void __launch_bounds__(768, 1)
     uint8_t* ob = obuf + q4 * 4096;
     const uint32_t obs = smem_u32(ob);
     int n = 0;
-    for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
+    for (int i = blockIdx.x; i < items; i += gridDim.x) {
       const Item it = get_item(p, i);
       const int nc = n_chunks(it.len);
       const int col = 128 * it.tile + 32 * q4;
@@ -623,12 +705,12 @@ struct CarryItem {
 __device__ __forceinline__ CarryItem get_carry(const ScanParams& p, int i) {
   CarryItem c;
   c.it.tile = i % p.tiles;
-  const int sh = i / p.tiles, seg = sh / p.Hv;
+  const int sh = i / p.tiles;
   c.it.h = sh % p.Hv;
-  c.it.len = 0;
-  c.sgh = (long long)seg * p.Hv + c.it.h;
-  const SegPlan sg = get_segment(p, seg);
-  if (sg.seq >= 0 && sg.j < sg.n - 1) set_range(p, sg, c.it);
+  int place;
+  const SegPlan sg = get_segment(p, sh / p.Hv, place);
+  set_range(p, sg, c.it);
+  c.sgh = (long long)place * p.Hv + c.it.h;
   return c;
 }
 
@@ -640,6 +722,7 @@ __global__ void __launch_bounds__(640, 1)
   RecScal* scal = reinterpret_cast<RecScal*>(smem + kCarryStages * kCarryBytes);
   CarryBars* B = reinterpret_cast<CarryBars*>(scal + kCarryStages);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int items = n_items(p, true);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kCarryStages; ++s) {
@@ -673,7 +756,7 @@ __global__ void __launch_bounds__(640, 1)
     regs_dec<64>();
     if (warp == 0) {
       int n = 0;
-      for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
         const CarryItem ci = get_carry(p, i);
         const int hk = ci.it.h / (p.Hv / p.Hk), nc = n_chunks(ci.it.len);
         for (int c = 0; c < nc && ok; ++c, ++n) {
@@ -707,7 +790,7 @@ __global__ void __launch_bounds__(640, 1)
       const uint32_t id128 = idesc_bf16_f32(128, 0, 1);
       int n = 0;
       uint32_t nu1 = 0;   // chunks of unit 1
-      for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
         const CarryItem ci = get_carry(p, i);
         const int nc = n_chunks(ci.it.len), units = ci.it.tile == 0 ? 2 : 1;
         for (int c = 0; c < nc && ok; ++c, ++n) {
@@ -791,7 +874,7 @@ __global__ void __launch_bounds__(640, 1)
         wait(&B->empty[(n - 1) % kCarryStages], ((n - 1) / kCarryStages) & 1);
     } else if (warp == 2) {
       int n = 0;
-      for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
+      for (int i = blockIdx.x; i < items; i += gridDim.x) {
         const CarryItem ci = get_carry(p, i);
         const int nc = n_chunks(ci.it.len);
         // (segments before a sequence's last one hold whole chunks: nothing to zero)
@@ -807,10 +890,9 @@ __global__ void __launch_bounds__(640, 1)
     const uint32_t d = tmem + u * kUnitCols + ((uint32_t)(q4 * 32) << 16);
     int n = 0;
     uint32_t m = 0;   // chunks of this unit
-    for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
+    for (int i = blockIdx.x; i < items; i += gridDim.x) {
       const CarryItem ci = get_carry(p, i);
       const int nc = n_chunks(ci.it.len);
-      if (nc == 0) continue;
       if (u == 1 && ci.it.tile != 0) {   // no unit here: pass the stages on
         for (int c = 0; c < nc; ++c, ++n) {
           wait(&B->ready[n % kCarryStages], (n / kCarryStages) & 1);
@@ -890,14 +972,20 @@ __global__ void __launch_bounds__(640, 1)
         }
         if (c + 1 < nc) put_S();
       }
-      const int grow = is_p ? row : 128 * ci.it.tile + row, rows = is_p ? p.dk : p.dv;
-      float* to = is_p ? p.P + ci.sgh * p.dk * p.dk : p.L + ci.sgh * p.dv * p.dk;
-      if (ok && grow < rows) {
+      if (!ok) continue;
+      if (is_p) {   // row of the join's operand tiles: 64 columns a block, hi then lo
+        uint8_t* to = p.P + ci.sgh * kPBytes + half * 16384 + row * 128;
 #pragma unroll
-        for (int c = 0; c < 64; c += 4)
-          if (64 * half + c < p.dk)
-            *reinterpret_cast<ulonglong2*>(to + (long long)grow * p.dk + 64 * half + c) =
-                make_ulonglong2(S[c / 2], S[c / 2 + 1]);
+        for (int c = 0; c < 8; ++c) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split2(S[4 * c + e], hi[e], lo[e]);
+          const int o = (c ^ (row & 7)) << 4;
+          *reinterpret_cast<uint4*>(to + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(to + kPBytes / 2 + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      } else {
+        store_state(p.L + (ci.sgh * p.tiles + ci.it.tile) * kStateFloats, q4, half, lane, S);
       }
     }
   }
@@ -935,9 +1023,10 @@ __device__ __forceinline__ int block_before(int x, int* part, int& total) {
 
 __global__ void __launch_bounds__(kPlanThreads)
     delta_plan_kernel(const int* starts, int n_seq, int N, int chunks, int seg_chunks,
-                      int seg_places, SeqPlan* plan, SegPlan* segs, int* status) {
+                      int seg_places, SeqPlan* plan, SegPlan* segs, int* order, int* joins,
+                      int* counts, int* status) {
   __shared__ int part[kPlanThreads / 32];
-  int chunk0 = 0, seg0 = 0;
+  int chunk0 = 0, seg0 = 0, join0 = 0;
   for (int s0 = 0; s0 < n_seq; s0 += kPlanThreads) {
     const int s = s0 + (int)threadIdx.x;
     int t0 = 0, len = 0, nc = 0, ns = 0;
@@ -952,150 +1041,302 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     int tc, ts;
     const int cb = chunk0 + block_before(nc, part, tc);
+    // bounds that ascend fit always; sequences that overlap (bad bounds between
+    // them) may hold more chunks than there are places: those stay empty
+    const bool fits = cb + nc <= chunks;
+    if (!fits) {
+      len = 0;
+      ns = 1;
+    }
     const int sb = seg0 + block_before(ns, part, ts);
+    int tj;
+    const int jb = join0 + block_before(ns > 1 ? 1 : 0, part, tj);
+    if (ns > 1) joins[jb] = sb;   // the place of its first segment
+    join0 += tj;
     if (s < n_seq) {
-      // ascending bounds fit always; sequences that overlap (bad bounds around
-      // them) may hold more chunks than there are places: those stay empty
-      const bool fits = cb + nc <= chunks && sb + ns <= seg_places;
-      plan[s] = SeqPlan{t0, fits ? len : 0, fits ? cb : 0, 0};
-      for (int j = 0; j < ns; ++j)
-        if (sb + j < seg_places)
-          segs[sb + j] = fits ? SegPlan{s, j, ns, 0} : SegPlan{j == 0 ? s : -1, 0, 1, 0};
+      plan[s] = SeqPlan{t0, len, fits ? cb : 0, 0};
+      for (int j = 0; j < ns; ++j) {
+        segs[sb + j] = SegPlan{s, j, ns, 0};
+        if (j + 1 < ns) order[sb - s + j] = sb + j;   // s last ones are before it
+      }
     }
     chunk0 += tc;
     seg0 += ts;
   }
+  // the last segments, behind the whole ones
+  __syncthreads();
+  const int whole = seg0 - n_seq;
+  for (int i = (int)threadIdx.x; i < seg0; i += kPlanThreads) {
+    const SegPlan sg = segs[i];
+    if (sg.j == sg.n - 1) order[whole + sg.seq] = i;
+  }
   for (int i = seg0 + (int)threadIdx.x; i < seg_places; i += kPlanThreads)
     segs[i] = SegPlan{-1, 0, 1, 0};
+  if (threadIdx.x == 0) {
+    counts[0] = whole;
+    counts[1] = seg0;
+    counts[2] = join0;
+  }
 }
 
 // ---------------------------------------------------------------- start states of the segments
-// S_{j+1} = S_j P_j + L_j, in fp32: a CTA takes R rows of the state of one
-// (sequence, head) through all segments.  P_j comes into shared memory by bulk
-// copies a segment ahead (64 KB: the product itself is short, so the latency and
-// the L2 rate of these loads are what it waits for); each of the eight warps
-// takes an eighth of the summation index and 4 columns per lane, the eight
-// partial sums are added in a fixed order.
-constexpr int kJoinThreads = 256;
+// S_{j+1} = S_j P_j + L_j: a CTA takes 128 rows of the state of one (sequence, head)
+// through all segments, S as pairs in TMEM, P_j as pairs from the carry pass (64 KB
+// by bulk copy, the next one on its way), three products, L_j added in fp32.
+// Warps 0-7: rows 32 (w % 4) .., half of the columns; warp 8: copies and MMAs.
+// A step takes one SM 2.7 us, its 192 KB of L, P and S; in fp32 on the CUDA cores it
+// took 16 of them 2.5 us.
+constexpr int kJoinThreads = 288;
+constexpr int kJoinSmem = 2 * kPBytes + 256 + 1024;
+
+struct JoinBars {
+  uint64_t full[2], s_ready, d_full;
+  uint32_t tmem;
+};
 
 struct JoinParams {
   const SegPlan* segs;
-  int seg_n;
+  const int* joins;
+  const int* counts;
+  int seqs, seg_n;
   const float* S0;
   const float* L;
-  const float* P;
+  const uint8_t* P;
   float* Sseg;
   int* status;
   unsigned long long wait_ns;
-  int Hv, dk, dv, row_tiles;
+  int Hv, dk, dv, tiles;
 };
 
+__global__ void __launch_bounds__(kJoinThreads, 1)
+    delta_join_kernel(const __grid_constant__ JoinParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  JoinBars* B = reinterpret_cast<JoinBars*>(smem + 2 * kPBytes);
+  const int tile = blockIdx.x % p.tiles, x = blockIdx.x / p.tiles;
+  const int h = x % p.Hv, k = x / p.Hv;
+  if (k >= (p.counts ? p.counts[2] : p.seqs)) return;
+  const int seg0 = p.segs ? p.joins[k] : k * p.seg_n;
+  const int seq = p.segs ? p.segs[seg0].seq : k, n = p.segs ? p.segs[seg0].n : p.seg_n;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(&B->full[0], 1);
+    mbar_init(&B->full[1], 1);
+    mbar_init(&B->s_ready, 8);
+    mbar_init(&B->d_full, 1);
+    fence_mbar_init();
+  }
+  if (warp == 8) tmem_alloc(&B->tmem, 256);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B->tmem;   // 128 columns of S's pairs, 128 of the product
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { wait_w(ok, bar, parity, p.status, p.wait_ns); };
+  if (warp == 8) {
+    const bool el = elect_lane();
+    const uint32_t id = idesc_bf16_f32(128, 0, 1);   // B = P, MN-major
+    auto load = [&](int j) {
+      mbar_arrive_expect_tx(&B->full[j & 1], kPBytes);
+      bulk_load_g2s(smem + (j & 1) * kPBytes, p.P + ((long long)(seg0 + j) * p.Hv + h) * kPBytes,
+                    kPBytes, &B->full[j & 1]);
+    };
+    int loaded = 0;
+    for (; loaded < 2 && loaded + 1 < n; ++loaded)
+      if (el) load(loaded);
+    int j = 0;
+    for (; j + 1 < n && ok; ++j) {
+      const uint32_t pb = smem_u32(smem) + (j & 1) * kPBytes;
+      wait(&B->full[j & 1], (j >> 1) & 1);
+      wait(&B->s_ready, j & 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (el) {
+        const uint64_t ph = smem_desc_sw128(pb, 16384, 1024);
+        const uint64_t pl = smem_desc_sw128(pb + kPBytes / 2, 16384, 1024);
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          umma_ts(tmem + 128, tmem + 16 * m + 8, ph + m * 128, id, m != 0);
+          umma_ts(tmem + 128, tmem + 16 * m, pl + m * 128, id, 1);
+          umma_ts(tmem + 128, tmem + 16 * m, ph + m * 128, id, 1);
+        }
+        umma_commit(&B->d_full);
+      }
+      __syncwarp();
+      wait(&B->d_full, j & 1);
+      if (ok && loaded + 1 < n) {
+        if (el) load(loaded);
+        ++loaded;
+      }
+      __syncwarp();
+    }
+    if (!ok)   // copies still on their way into this CTA's shared memory
+      for (; j < loaded; ++j) mbar_wait_w(&B->full[j & 1], (j >> 1) & 1, p.status, p.wait_ns);
+  } else {
+    const int q4 = warp & 3, half = warp >> 2;
+    const int row = 128 * tile + 32 * q4 + lane;
+    const uint32_t t = tmem + ((uint32_t)(q4 * 32) << 16) + 64 * half;
+    F2 S[32];
+#pragma unroll
+    for (int c = 0; c < 64; c += 4) {
+      ulonglong2 w = make_ulonglong2(0, 0);
+      if (p.S0 && row < p.dv && 64 * half + c < p.dk)
+        w = *reinterpret_cast<const ulonglong2*>(
+            p.S0 + (((long long)seq * p.Hv + h) * p.dv + row) * p.dk + 64 * half + c);
+      S[c / 2] = w.x;
+      S[c / 2 + 1] = w.y;
+    }
+    for (int j = 0; j + 1 < n; ++j) {
+      const long long sgh = (long long)(seg0 + j) * p.Hv + h;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) split2(S[8 * b + e], hi[e], lo[e]);
+        tmem_st8(t + 16 * b, hi);
+        tmem_st8(t + 16 * b + 8, lo);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B->s_ready);
+      load_state(p.L + (sgh * p.tiles + tile) * kStateFloats, q4, half, lane, S);
+      wait(&B->d_full, j & 1);
+      tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        float d[16];
+        tmem_ld16_nowait(t + 128 + 16 * b, d);
+        tmem_wait_bind(d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) S[8 * b + e] = add2(S[8 * b + e], pack2(d[2 * e], d[2 * e + 1]));
+      }
+      if (ok)
+        store_state(p.Sseg + ((sgh + p.Hv) * p.tiles + tile) * kStateFloats, q4, half, lane, S);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+// The same for few heads, in fp32 on the CUDA cores: a CTA takes R rows, so that a
+// head's step is spread over 128 / R SMs (one SM moves the 192 KB of a step above in
+// 2.7 us; here a step takes 1.0 us with R = 4, its 64 KB of P).  Each of the eight
+// warps takes sixteen rows of P and 4 columns per lane; the eight partial sums are
+// added in a fixed order.
+constexpr int kRowsThreads = 256;
+
 template <int R>
-struct JoinShared {
-  float P[2][128 * 128];
+struct RowsShared {
+  uint8_t P[2][kPBytes];
   float part[8][R][128];
   float S[R][128];
   uint64_t full[2];
 };
 
 template <int R>
-__global__ void __launch_bounds__(kJoinThreads, 1)
-    delta_join_kernel(const __grid_constant__ JoinParams p) {
+__global__ void __launch_bounds__(kRowsThreads, 1)
+    delta_join_rows_kernel(const __grid_constant__ JoinParams p) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  JoinShared<R>& sh = *reinterpret_cast<JoinShared<R>*>(smem_raw);
-  const int tile = blockIdx.x % p.row_tiles, x = blockIdx.x / p.row_tiles;
-  const int h = x % p.Hv, first = x / p.Hv;   // first: a segment's place (or a sequence)
-  SegPlan sg;
-  if (p.segs) {
-    sg = p.segs[first];
-    if (sg.seq < 0 || sg.j != 0) return;
-  } else {
-    sg.seq = first;
-    sg.n = p.seg_n;
-  }
-  if (sg.n < 2) return;
-  const int seg0 = p.segs ? first : first * p.seg_n;
+  RowsShared<R>& sh = *reinterpret_cast<RowsShared<R>*>(smem_raw);
+  constexpr int kParts = 128 / R;
+  const int row0 = R * (blockIdx.x % kParts), x = blockIdx.x / kParts;
+  const int tile = x % p.tiles, h = x / p.tiles % p.Hv, seq = x / p.tiles / p.Hv;
+  const int n = p.seg_n, seg0 = seq * n;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int row0 = tile * R;
-  const long long one = (long long)p.dv * p.dk, pp = (long long)p.dk * p.dk;
-  const uint32_t pbytes = (uint32_t)pp * 4;
   bool ok = true;
+  auto load = [&](int j) {
+    mbar_arrive_expect_tx(&sh.full[j & 1], kPBytes);
+    bulk_load_g2s(sh.P[j & 1], p.P + ((long long)(seg0 + j) * p.Hv + h) * kPBytes, kPBytes,
+                  &sh.full[j & 1]);
+  };
   if (tid == 0) {
     mbar_init(&sh.full[0], 1);
     mbar_init(&sh.full[1], 1);
     fence_mbar_init();
-    for (int j = 0; j < 2 && j + 1 < sg.n; ++j) {
-      mbar_arrive_expect_tx(&sh.full[j], pbytes);
-      bulk_load_g2s(sh.P[j], p.P + ((long long)(seg0 + j) * p.Hv + h) * pp, pbytes, &sh.full[j]);
-    }
+    for (int j = 0; j < 2 && j + 1 < n; ++j) load(j);
   }
   // this thread's outputs: column col, rows r0 .. r0 + R / 2
   const int col = tid & 127, r0 = (tid >> 7) * (R / 2);
+  int at[R / 2];
 #pragma unroll
   for (int r = 0; r < R / 2; ++r) {
-    const int row = row0 + r0 + r;
+    const int row = row0 + r0 + r, grow = 128 * tile + row;
+    at[r] = (int)state_at(row >> 5, col >> 6, (col & 63) >> 2, row & 31) * 4 + (col & 3);
     sh.S[r0 + r][col] =
-        p.S0 && row < p.dv && col < p.dk
-            ? p.S0[((long long)sg.seq * p.Hv + h) * one + (long long)row * p.dk + col]
+        p.S0 && grow < p.dv && col < p.dk
+            ? p.S0[(((long long)seq * p.Hv + h) * p.dv + grow) * p.dk + col]
             : 0.f;
   }
   __syncthreads();
-  const int m_per = p.dk / 8, m0 = warp * m_per, c4 = 4 * lane;
-  for (int j = 0; j + 1 < sg.n; ++j) {
+  const int half = lane >> 4;   // of P's column blocks; 4 columns from 4 (lane & 15) in it
+  for (int j = 0; j + 1 < n; ++j) {
     const long long sgh = (long long)(seg0 + j) * p.Hv + h;
+    const float* L = p.L + (sgh * p.tiles + tile) * kStateFloats;
     float l[R / 2];
 #pragma unroll
-    for (int r = 0; r < R / 2; ++r) {
-      const int row = row0 + r0 + r;
-      l[r] = row < p.dv && col < p.dk ? p.L[sgh * one + (long long)row * p.dk + col] : 0.f;
-    }
+    for (int r = 0; r < R / 2; ++r) l[r] = L[at[r]];
     wait_w(ok, &sh.full[j & 1], (j >> 1) & 1, p.status, p.wait_ns);
     F2 acc[R][2];
 #pragma unroll
     for (int r = 0; r < R; ++r) acc[r][0] = acc[r][1] = 0;
-    if (c4 < p.dk) {
-      const float* P = sh.P[j & 1] + m0 * p.dk + c4;
-#pragma unroll 2
-      for (int m = 0; m < m_per; ++m, P += p.dk) {
-        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(P);
+    const uint8_t* P = sh.P[j & 1] + half * 16384 + (lane & 1) * 8;
+#pragma unroll 1
+    for (int m = 16 * warp; m < 16 * warp + 16; m += 4) {
+      F2 w[4][2];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float s = sh.S[r][m0 + m];
-          const F2 s2 = pack2(s, s);
-          acc[r][0] = fma2(s2, w.x, acc[r][0]);
-          acc[r][1] = fma2(s2, w.y, acc[r][1]);
+      for (int e = 0; e < 4; ++e) {
+        const int o = (m + e) * 128 + ((((lane & 15) >> 1) ^ ((m + e) & 7)) << 4);
+        const uint2 hi = *reinterpret_cast<const uint2*>(P + o);
+        const uint2 lo = *reinterpret_cast<const uint2*>(P + kPBytes / 2 + o);
+        w[e][0] = add2(pack2(__uint_as_float(hi.x << 16), __uint_as_float(hi.x & 0xffff0000u)),
+                       pack2(__uint_as_float(lo.x << 16), __uint_as_float(lo.x & 0xffff0000u)));
+        w[e][1] = add2(pack2(__uint_as_float(hi.y << 16), __uint_as_float(hi.y & 0xffff0000u)),
+                       pack2(__uint_as_float(lo.y << 16), __uint_as_float(lo.y & 0xffff0000u)));
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float4 s4 = *reinterpret_cast<const float4*>(&sh.S[r][m]);
+        const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const F2 s2 = pack2(s[e], s[e]);
+          acc[r][0] = fma2(s2, w[e][0], acc[r][0]);
+          acc[r][1] = fma2(s2, w[e][1], acc[r][1]);
         }
       }
     }
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      *reinterpret_cast<ulonglong2*>(&sh.part[warp][r][c4]) = make_ulonglong2(acc[r][0], acc[r][1]);
+      *reinterpret_cast<ulonglong2*>(&sh.part[warp][r][4 * lane]) =
+          make_ulonglong2(acc[r][0], acc[r][1]);
     __syncthreads();
-    if (tid == 0 && j + 3 < sg.n) {   // everyone is done with P_j
+    if (tid == 0 && j + 3 < n) {   // everyone is done with P_j
       fence_proxy_async_smem();
-      mbar_arrive_expect_tx(&sh.full[j & 1], pbytes);
-      bulk_load_g2s(sh.P[j & 1], p.P + (sgh + 2 * p.Hv) * pp, pbytes, &sh.full[j & 1]);
+      load(j + 2);
     }
-    float* to = p.Sseg + (sgh + p.Hv) * one;
+    float* to = p.Sseg + ((sgh + p.Hv) * p.tiles + tile) * kStateFloats;
 #pragma unroll
     for (int r = 0; r < R / 2; ++r) {
       float s = l[r];
 #pragma unroll
       for (int w = 0; w < 8; ++w) s += sh.part[w][r0 + r][col];
       sh.S[r0 + r][col] = s;
-      const int row = row0 + r0 + r;
-      if (ok && row < p.dv && col < p.dk) to[(long long)row * p.dk + col] = s;
+      if (ok) to[at[r]] = s;
     }
     __syncthreads();
   }
 }
 
 template <int R>
-cudaError_t launch_join(JoinParams j, long long heads, cudaStream_t stream) {
-  j.row_tiles = (j.dv + R - 1) / R;
-  delta_join_kernel<R>
-      <<<(unsigned)(heads * j.row_tiles), kJoinThreads, sizeof(JoinShared<R>), stream>>>(j);
-  return cudaGetLastError();
+void launch_rows(const JoinParams& j, cudaStream_t stream) {
+  delta_join_rows_kernel<R>
+      <<<j.seqs * j.Hv * j.tiles * (128 / R), kRowsThreads, sizeof(RowsShared<R>), stream>>>(j);
 }
 
 int g_ready[64] = {0};   // 0 unknown, 1 usable, 2 not usable
@@ -1114,9 +1355,9 @@ int prepare() {
              cudaSuccess;
     };
     if (room(delta_scan_kernel, kSmem) && room(delta_carry_kernel, kCarrySmem) &&
-        room(delta_join_kernel<4>, sizeof(JoinShared<4>)) &&
-        room(delta_join_kernel<8>, sizeof(JoinShared<8>)) &&
-        room(delta_join_kernel<16>, sizeof(JoinShared<16>)) &&
+        room(delta_join_kernel, kJoinSmem) &&
+        room(delta_join_rows_kernel<4>, sizeof(RowsShared<4>)) &&
+        room(delta_join_rows_kernel<8>, sizeof(RowsShared<8>)) &&
         prepare_delta_prep() == cudaSuccess &&
         cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
       g_ready[dev] = 1;
@@ -1132,7 +1373,7 @@ struct Plan {
   int chunks;        // places of records per head
   int seg_chunks, seg_n, seg_places;
   bool split;
-  size_t plan, segs, scal, rec, L, P, Sseg, total;
+  size_t plan, segs, lists, scal, rec, L, P, Sseg, total;
 };
 
 Plan make_plan(int B, int Hv, int N, int dk, int dv, int n_seq, bool packed) {
@@ -1140,18 +1381,29 @@ Plan make_plan(int B, int Hv, int N, int dk, int dv, int n_seq, bool packed) {
   const int tiles = (dv + 127) / 128;
   const int nc = n_chunks(N);
   p.chunks = packed ? N / kC + n_seq : B * nc;
-  // segments of a sequence: the steps that a CTA walks in the two passes
-  long long best = 0;
-  p.seg_n = 1;
+  // Chunks per segment, from the times of a step on one SM (measured, in us): 2.65
+  // with outputs, 3.05 for L and P, each item about one step more; a join step 1.0
+  // by rows and 2.7 by tiles, and 10 to begin.
+  const long long units = (long long)(packed ? 1 : B) * Hv * tiles;
+  const double join = !packed && units * 16 <= kSms ? 1.0 : 2.7;
+  double best = 0.0;
   p.seg_chunks = nc;
-  const long long units = (long long)(packed ? 1 : B) * Hv;
-  for (int n = 1; n <= 64 && n <= nc; ++n) {
+  for (int n = 1; n <= 128 && n <= nc; ++n) {
     const int lc = (nc + n - 1) / n;
-    const long long out = (units * tiles * n + kSms - 1) / kSms * lc;
-    const long long carry = n > 1 ? (units * tiles * (n - 1) + kSms - 1) / kSms * lc + n : 0;
-    if (n == 1 || out + carry < best) {
-      best = out + carry;
-      p.seg_n = n;
+    double t;
+    if (!packed) {   // sequences of one length: whole rounds of the SMs
+      t = 2.65 * (double)((units * n + kSms - 1) / kSms) * (lc + 1);
+      if (n > 1)
+        t += 3.05 * (double)((units * (n - 1) + kSms - 1) / kSms) * (lc + 1) + join * (n - 1) + 10.0;
+    } else {   // lengths unknown: an even share and one segment; the longest of n_seq
+      const double share = (double)units * nc / kSms;
+      const double longest = n_seq > 4 ? 4.0 * nc / n_seq : nc;
+      const double pieces = longest / lc;
+      t = 2.65 * (share + share / lc + (longest < lc ? longest : lc));
+      if (pieces > 1.0) t += 3.05 * (share + share / lc + lc) + join * pieces + 10.0;
+    }
+    if (n == 1 || t < best) {
+      best = t;
       p.seg_chunks = lc;
     }
   }
@@ -1166,12 +1418,13 @@ Plan make_plan(int B, int Hv, int N, int dk, int dv, int n_seq, bool packed) {
   };
   p.plan = take(packed ? (size_t)n_seq * sizeof(SeqPlan) : 0);
   p.segs = take(packed ? (size_t)p.seg_places * sizeof(SegPlan) : 0);
+  p.lists = take(packed ? ((size_t)p.seg_places + n_seq + 4) * sizeof(int) : 0);
   p.scal = take((size_t)p.chunks * Hv * sizeof(RecScal));
   p.rec = take((size_t)p.chunks * Hv * kRecBytes);
   const size_t sh = p.split ? (size_t)p.seg_places * Hv : 0;
-  p.L = take(sh * dv * dk * 4);
-  p.P = take(sh * dk * dk * 4);
-  p.Sseg = take(sh * dv * dk * 4);
+  p.L = take(sh * tiles * kStateFloats * 4);
+  p.P = take(sh * kPBytes);
+  p.Sseg = take(sh * tiles * kStateFloats * 4);
   p.total = off;
   return p;
 }
@@ -1233,12 +1486,18 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
 
   p.plan = plan;
   p.segs = segs;
+  int* counts = packed ? reinterpret_cast<int*>(ws + pl.lists) : nullptr;
+  int* joins = packed ? counts + 4 : nullptr;
+  int* order = packed ? joins + a.n_seq : nullptr;
+  p.counts = counts;
+  p.order = order;
+  p.seqs = a.n_seq;
   p.rec = r.rec;
   p.scal = r.scal;
   p.S0 = a.S0;
   p.S_final = a.S_final;
   p.L = reinterpret_cast<float*>(ws + pl.L);
-  p.P = reinterpret_cast<float*>(ws + pl.P);
+  p.P = reinterpret_cast<uint8_t*>(ws + pl.P);
   float* Sseg = reinterpret_cast<float*>(ws + pl.Sseg);
   p.Sseg = Sseg;
   p.out = static_cast<__nv_bfloat16*>(a.out);
@@ -1257,20 +1516,24 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
   if (packed) {
     ProfScope ps(PT_DELTA_PLAN, a.stream, 0.0, 20.0 * a.n_seq);
     delta_plan_kernel<<<1, kPlanThreads, 0, a.stream>>>(a.seq_starts, a.n_seq, a.N, pl.chunks,
-                                                        pl.seg_chunks, pl.seg_places, plan, segs, a.status);
+                                                        pl.seg_chunks, pl.seg_places, plan, segs,
+                                                        order, joins, counts, a.status);
     if (cudaGetLastError() != cudaSuccess) return TTT_ERR_CUDA;
   }
   if (launch_delta_prep(r, pl.chunks, a.stream) != cudaSuccess) return TTT_ERR_CUDA;
   if (pl.split) {
     {
-      p.items = pl.seg_places * a.Hv * p.tiles;
+      const int items = (packed ? pl.seg_places : a.B * (pl.seg_n - 1)) * a.Hv * p.tiles;
       ProfScope ps(PT_DELTA_CARRY, a.stream, 5.0 * tok * a.Hv * a.dk * (a.dv + a.dk),
                    tok * 2.0 * (a.Hk * a.dk + a.Hv * a.dv));
-      delta_carry_kernel<<<p.items < sms ? p.items : sms, 640, kCarrySmem, a.stream>>>(p);
+      delta_carry_kernel<<<items < sms ? items : sms, 640, kCarrySmem, a.stream>>>(p);
       if (cudaGetLastError() != cudaSuccess) return TTT_ERR_CUDA;
     }
     JoinParams j;
     j.segs = segs;
+    j.joins = joins;
+    j.counts = counts;
+    j.seqs = a.n_seq;
     j.seg_n = pl.seg_n;
     j.S0 = a.S0;
     j.L = p.L;
@@ -1279,21 +1542,21 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
     j.status = a.status;
     j.wait_ns = a.wait_ns;
     j.Hv = a.Hv; j.dk = a.dk; j.dv = a.dv;
+    j.tiles = p.tiles;
     const double states = (double)pl.seg_places * a.Hv * a.dk;
     ProfScope ps(PT_DELTA_JOIN, a.stream, 2.0 * states * a.dk * a.dv,
                  4.0 * states * (a.dk + 2 * a.dv));
-    // rows per CTA: as many as leave a CTA to every SM (one fits)
-    const long long heads = (long long)(packed ? pl.seg_places : a.B) * a.Hv;
-    const long long rows = (long long)a.n_seq * a.Hv * a.dv;
-    const cudaError_t e = rows >= 16 * 128   ? launch_join<16>(j, heads, a.stream)
-                          : rows >= 8 * 128 ? launch_join<8>(j, heads, a.stream)
-                                            : launch_join<4>(j, heads, a.stream);
-    if (e != cudaSuccess) return TTT_ERR_CUDA;
+    // by rows where that still fits the card at once
+    const long long tiles = (long long)a.n_seq * a.Hv * p.tiles;
+    if (!packed && tiles * 32 <= sms) launch_rows<4>(j, a.stream);
+    else if (!packed && tiles * 16 <= sms) launch_rows<8>(j, a.stream);
+    else delta_join_kernel<<<(unsigned)tiles, kJoinThreads, kJoinSmem, a.stream>>>(j);
+    if (cudaGetLastError() != cudaSuccess) return TTT_ERR_CUDA;
   }
-  p.items = pl.seg_places * a.Hv * p.tiles;
+  const int items = pl.seg_places * a.Hv * p.tiles;
   ProfScope ps(PT_DELTA_CHUNK, a.stream, 7.0 * tok * a.Hv * a.dk * a.dv,
                tok * 4.0 * (a.Hk * a.dk + a.Hv * a.dv));
-  delta_scan_kernel<<<p.items < sms ? p.items : sms, 768, kSmem, a.stream>>>(p);
+  delta_scan_kernel<<<items < sms ? items : sms, 512, kSmem, a.stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 
