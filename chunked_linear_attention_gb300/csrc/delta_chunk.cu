@@ -47,15 +47,15 @@ constexpr int kStageBytes = 6 * kBlk;   // Q0 K0 Q1 K1 V0 V1 (column blocks of 6
 
 struct Bars {
   uint64_t full[kStages], ready[kStages], empty[kStages];
-  uint64_t rec_full[2], rec_free[2];
+  uint64_t t_full[2], t_free[2], p_full[2], p_free[2];
   uint64_t ks_full, x_full, ds_full, x_ready;
   uint64_t y_ready[2], xs_ready[2], s_ready[4];
   uint64_t o_full, o_free;
   uint32_t tmem;
 };
 
-constexpr int kOutBytes = 4 * 64 * 64;
-constexpr int kSmem = kStages * kStageBytes + 2 * kRecBytes + 2 * (int)sizeof(RecScal) +
+constexpr int kOutBytes = 4 * 32 * 64;
+constexpr int kSmem = kStages * kStageBytes + 2 * kRecBytes + 4 * (int)sizeof(RecScal) +
                       kOutBytes + (int)sizeof(Bars) + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(512, 1)
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* rec = smem + kStages * kStageBytes;
   RecScal* scal = reinterpret_cast<RecScal*>(rec + 2 * kRecBytes);
-  uint8_t* obuf = reinterpret_cast<uint8_t*>(scal + 2);   // outputs on their way
+  uint8_t* obuf = reinterpret_cast<uint8_t*>(scal + 4);   // outputs on their way
   Bars* B = reinterpret_cast<Bars*>(obuf + kOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int items = n_items(p, false);
@@ -282,8 +282,10 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(&B->empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&B->rec_full[b], 1);
-      mbar_init(&B->rec_free[b], 1 + 8 + 4);
+      mbar_init(&B->t_full[b], 1);
+      mbar_init(&B->t_free[b], 1);
+      mbar_init(&B->p_full[b], 1);
+      mbar_init(&B->p_free[b], 1);
     }
     mbar_init(&B->ks_full, 1);
     mbar_init(&B->x_full, 1);
@@ -314,13 +316,13 @@ __global__ void __launch_bounds__(512, 1)
     regs_dec<64>();
     if (warp == 0) {
       int n = 0;
-      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+      for (int i = blockIdx.x; i < items && (ok = together(ok)); i += gridDim.x) {
         const Item it = get_item(p, i);
         const int hk = it.h / (p.Hv / p.Hk), nc = n_chunks(it.len);
-        for (int c = 0; c < nc && ok; ++c, ++n) {
+        for (int c = 0; c < nc && (ok = together(ok)); ++c, ++n) {
           const int s = n % kStages, r = n & 1;
           wait(&B->empty[s], ((n / kStages) & 1) ^ 1);
-          if (!ok) break;
+          if (!(ok = together(ok))) break;
           if (lane == 0) {
             uint8_t* st = smem + s * kStageBytes;
             const int t = it.t0 + c * kC;
@@ -334,21 +336,34 @@ __global__ void __launch_bounds__(512, 1)
                           &B->full[s]);
           }
           __syncwarp();
-          wait(&B->rec_free[r], ((n >> 1) & 1) ^ 1);
+          // T's two tiles are used up long before the chunk's outputs: a record's
+          // halves come and go on their own (together, the next T came too late and
+          // a step took 900 cycles longer).  The factors' four places need no
+          // barrier: at T(n) the outputs of chunk n - 4 have been read.
+          const long long x = (long long)(it.chunk0 + c) * p.Hv + it.h;
+          wait(&B->t_free[r], ((n >> 1) & 1) ^ 1);
           if (lane == 0 && ok) {
-            const long long x = (long long)(it.chunk0 + c) * p.Hv + it.h;
-            mbar_arrive_expect_tx(&B->rec_full[r], kRecBytes + sizeof(RecScal));
-            bulk_load_g2s(rec + r * kRecBytes, p.rec + x * kRecBytes, kRecBytes, &B->rec_full[r]);
-            bulk_load_g2s(scal + r, p.scal + x, sizeof(RecScal), &B->rec_full[r]);
+            mbar_arrive_expect_tx(&B->t_full[r], kRecBytes / 2 + sizeof(RecScal));
+            bulk_load_g2s(rec + r * kRecBytes, p.rec + x * kRecBytes, kRecBytes / 2, &B->t_full[r]);
+            bulk_load_g2s(scal + (n & 3), p.scal + x, sizeof(RecScal), &B->t_full[r]);
+          }
+          __syncwarp();
+          wait(&B->p_free[r], ((n >> 1) & 1) ^ 1);
+          if (lane == 0 && ok) {
+            mbar_arrive_expect_tx(&B->p_full[r], kRecBytes / 2);
+            bulk_load_g2s(rec + r * kRecBytes + kRecBytes / 2, p.rec + x * kRecBytes + kRecBytes / 2,
+                          kRecBytes / 2, &B->p_full[r]);
           }
           __syncwarp();
         }
       }
-      if (!ok) {   // copies still on their way into this CTA's shared memory
+      if (!together(ok)) {   // copies still on their way into this CTA's shared memory
         for (int m = n > kStages ? n - kStages : 0; m < n; ++m)
           mbar_wait_w(&B->full[m % kStages], (m / kStages) & 1, p.status, p.wait_ns);
-        for (int m = n > 2 ? n - 2 : 0; m < n; ++m)
-          mbar_wait_w(&B->rec_full[m & 1], (m >> 1) & 1, p.status, p.wait_ns);
+        for (int m = n > 2 ? n - 2 : 0; m < n; ++m) {
+          mbar_wait_w(&B->t_full[m & 1], (m >> 1) & 1, p.status, p.wait_ns);
+          mbar_wait_w(&B->p_full[m & 1], (m >> 1) & 1, p.status, p.wait_ns);
+        }
       }
     } else if (warp == 1) {
       const bool el = elect_lane();
@@ -357,10 +372,10 @@ __global__ void __launch_bounds__(512, 1)
       const uint32_t id64m = idesc_bf16_f32(64, 1, 0);       // A = V^T, MN-major
       const uint32_t id128 = idesc_bf16_f32(128, 0, 1);      // B = K^T, MN-major
       int n = 0;
-      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+      for (int i = blockIdx.x; i < items && (ok = together(ok)); i += gridDim.x) {
         const Item it = get_item(p, i);
         const int nc = n_chunks(it.len);
-        for (int c = 0; c < nc && ok; ++c, ++n) {
+        for (int c = 0; c < nc && (ok = together(ok)); ++c, ++n) {
           const uint32_t st = base + (n % kStages) * kStageBytes;
           const uint32_t rb = recb + (n & 1) * kRecBytes;
           const uint32_t ph = n & 1;
@@ -368,7 +383,7 @@ __global__ void __launch_bounds__(512, 1)
           const uint64_t tl = smem_desc_sw128(rb + kBlk, 16, 1024);
           // T V, once the chunk before is done with X's columns
           wait(&B->ready[n % kStages], (n / kStages) & 1);
-          wait(&B->rec_full[ph], (n >> 1) & 1);
+          wait(&B->t_full[ph], (n >> 1) & 1);
           if (n > 0) wait(&B->ds_full, ph ^ 1);
           tc_fence_after();
           if (el) {
@@ -411,7 +426,10 @@ __global__ void __launch_bounds__(512, 1)
                 umma_ts(tmem + kX, y, tl + k * 2, id64, 1);
                 umma_ts(tmem + kX, y, th + k * 2, id64, 1);
               }
-              if (b == 1) umma_commit(&B->x_full);
+              if (b == 1) {
+                umma_commit(&B->x_full);
+                umma_commit(&B->t_free[ph]);
+              }
             }
             __syncwarp();
           }
@@ -448,6 +466,7 @@ __global__ void __launch_bounds__(512, 1)
           }
           // P X
           wait(&B->x_ready, ph);
+          wait(&B->p_full[ph], (n >> 1) & 1);
           tc_fence_after();
           if (el) {
             const uint64_t pH = smem_desc_sw128(rb + 2 * kBlk, 16, 1024);
@@ -460,14 +479,16 @@ __global__ void __launch_bounds__(512, 1)
               umma_ts(tmem + kO, x, pH + k * 2, id64, 1);
             }
             umma_commit(&B->o_full);
-            umma_commit(&B->rec_free[ph]);
+            umma_commit(&B->p_free[ph]);
           }
           __syncwarp();
         }
       }
+      ok = together(ok);
       if (n > 0) {   // every arrival on this CTA's barriers has landed before it ends
         wait(&B->empty[(n - 1) % kStages], ((n - 1) / kStages) & 1);
-        wait(&B->rec_free[(n - 1) & 1], ((n - 1) >> 1) & 1);
+        wait(&B->t_free[(n - 1) & 1], ((n - 1) >> 1) & 1);
+        wait(&B->p_free[(n - 1) & 1], ((n - 1) >> 1) & 1);
       }
     } else if (warp == 2) {
       int n = 0;
@@ -531,9 +552,9 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll 1
       for (int c = 0; c < nc; ++c, ++n) {
         const uint32_t ph = n & 1;
-        const RecScal& sc = scal[ph];
+        const RecScal& sc = scal[n & 3];
         float x[2][16];
-        wait(&B->rec_full[ph], (n >> 1) & 1);
+        wait(&B->t_full[ph], (n >> 1) & 1);
         wait(&B->ks_full, ph);
         tc_fence_after();
 #pragma unroll
@@ -560,7 +581,6 @@ __global__ void __launch_bounds__(512, 1)
           arrive(&B->xs_ready[b]);
         }
         const F2 eall = pack2(sc.eall, sc.eall);
-        arrive(&B->rec_free[ph]);
         if (n > 0) wait(&B->o_full, ph ^ 1);   // P X of the chunk before has read X
         tc_fence_after();
 #pragma unroll
@@ -596,9 +616,9 @@ __global__ void __launch_bounds__(512, 1)
     const float nscale = -p.scale;
     const F2 nscale2 = pack2(nscale, nscale);
     const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
-    // this warp's 64 tokens x 32 rows of d_v, 64 bytes a token, the 16-byte pieces
+    // this warp's 32 tokens x 32 rows of d_v, 64 bytes a token, the 16-byte pieces
     // of a token exchanged by its number
-    uint8_t* ob = obuf + q4 * 4096;
+    uint8_t* ob = obuf + q4 * 2048;
     const uint32_t obs = smem_u32(ob);
     int n = 0;
     for (int i = blockIdx.x; i < items; i += gridDim.x) {
@@ -609,57 +629,67 @@ __global__ void __launch_bounds__(512, 1)
                            it.t0 * p.so.token + col;
 #pragma unroll 1
       for (int c = 0; c < nc; ++c, ++n) {
-        const RecScal& sc = scal[n & 1];
-        wait(&B->rec_full[n & 1], (n >> 1) & 1);
+        const RecScal& sc = scal[n & 3];
         wait(&B->o_full, n & 1);
         tc_fence_after();
-#pragma unroll 2
-        for (int b = 0; b < 8; ++b) {   // 16 rows (b & 1) by 16 tokens (b >> 1)
-          float x[8], y[8];
-          const uint32_t ta = tl + ((uint32_t)(16 * (b & 1)) << 16) + 16 * (b >> 1);
-          tmem_ld_frag(ta + kQS, x);
-          tmem_ld_frag(ta + kO, y);
-          uint32_t w[4];
-          F2 f[2];
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            f[t] = mul2(nscale2, *reinterpret_cast<const F2*>(
-                                     &sc.neg[16 * (b >> 1) + 8 * t + 2 * (lane & 3)]));
-          tmem_wait_frag(x);
-          tmem_wait_frag(y);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {   // tokens 8 (e >> 1) .., rows 8 (e & 1) ..
-            const F2 o = fma2(f[e >> 1], pack2(x[2 * e], x[2 * e + 1]), pack2(y[2 * e], y[2 * e + 1]));
-            float o0, o1;
-            unpack2(o, o0, o1);
-            const __nv_bfloat162 r = __floats2bfloat162_rn(o0, o1);
-            w[e] = *reinterpret_cast<const uint32_t*>(&r);
-          }
-          const int t = 16 * (b >> 1) + 8 * (lane >> 4) + (lane & 7);
-          const int piece = 2 * (b & 1) + ((lane >> 3) & 1);
-          stmatrix4_t(obs + t * 64 + ((piece ^ ((t >> 1) & 3)) << 4), w);
-        }
-        tc_fence_before();
-        arrive(&B->o_free);
-        arrive(&B->rec_free[n & 1]);
         const int valid = ok ? min(kC, it.len - c * kC) : 0;
-        if (p.wide_out) {
-#pragma unroll
-          for (int b = 0; b < 8; ++b) {
-            const int t = 8 * b + (lane >> 2), piece = lane & 3;
-            const uint4 w = lds128(obs + t * 64 + ((piece ^ ((t >> 1) & 3)) << 4));
-            if (t < valid && col + 8 * piece < p.dv)
-              *reinterpret_cast<uint4*>(out + (long long)(c * kC + t) * p.so.token + 8 * piece) = w;
-          }
-        } else {
 #pragma unroll 1
-          for (int t = 0; t < valid; ++t) {
-            const __nv_bfloat16 o = *reinterpret_cast<const __nv_bfloat16*>(
-                ob + t * 64 + (((lane >> 3) ^ ((t >> 1) & 3)) << 4) + 2 * (lane & 7));
-            if (col + lane < p.dv) out[(long long)(c * kC + t) * p.so.token + lane] = o;
+        for (int th = 0; th < 2; ++th) {   // 32 tokens at a time
+#pragma unroll 2
+          for (int b = 0; b < 4; ++b) {    // 16 rows (b & 1) by 16 tokens (b >> 1)
+            float x[8], y[8];
+            const int t0 = 32 * th + 16 * (b >> 1);
+            const uint32_t ta = tl + ((uint32_t)(16 * (b & 1)) << 16) + t0;
+            tmem_ld_frag(ta + kQS, x);
+            tmem_ld_frag(ta + kO, y);
+            uint32_t w[4];
+            F2 f[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              f[t] = mul2(nscale2,
+                          *reinterpret_cast<const F2*>(&sc.neg[t0 + 8 * t + 2 * (lane & 3)]));
+            tmem_wait_frag(x);
+            tmem_wait_frag(y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {   // tokens 8 (e >> 1) .., rows 8 (e & 1) ..
+              const F2 o =
+                  fma2(f[e >> 1], pack2(x[2 * e], x[2 * e + 1]), pack2(y[2 * e], y[2 * e + 1]));
+              float o0, o1;
+              unpack2(o, o0, o1);
+              const __nv_bfloat162 r = __floats2bfloat162_rn(o0, o1);
+              w[e] = *reinterpret_cast<const uint32_t*>(&r);
+            }
+            const int t = 16 * (b >> 1) + 8 * (lane >> 4) + (lane & 7);
+            const int piece = 2 * (b & 1) + ((lane >> 3) & 1);
+            stmatrix4_t(obs + t * 64 + ((piece ^ ((t >> 1) & 3)) << 4), w);
           }
+          if (th == 1) {
+            tc_fence_before();
+            arrive(&B->o_free);
+          } else {
+            __syncwarp();
+          }
+          __nv_bfloat16* dst = out + (long long)(c * kC + 32 * th) * p.so.token;
+          const int here = valid - 32 * th;
+          if (p.wide_out) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const int t = 8 * b + (lane >> 2), piece = lane & 3;
+              const uint4 w = lds128(obs + t * 64 + ((piece ^ ((t >> 1) & 3)) << 4));
+              if (t < here && col + 8 * piece < p.dv)
+                *reinterpret_cast<uint4*>(dst + (long long)t * p.so.token + 8 * piece) = w;
+            }
+          } else {
+            const int last = here < 32 ? here : 32;
+#pragma unroll 1
+            for (int t = 0; t < last; ++t) {
+              const __nv_bfloat16 o = *reinterpret_cast<const __nv_bfloat16*>(
+                  ob + t * 64 + (((lane >> 3) ^ ((t >> 1) & 3)) << 4) + 2 * (lane & 7));
+              if (col + lane < p.dv) dst[(long long)t * p.so.token + lane] = o;
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
     }
   }
@@ -756,13 +786,13 @@ __global__ void __launch_bounds__(640, 1)
     regs_dec<64>();
     if (warp == 0) {
       int n = 0;
-      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+      for (int i = blockIdx.x; i < items && (ok = together(ok)); i += gridDim.x) {
         const CarryItem ci = get_carry(p, i);
         const int hk = ci.it.h / (p.Hv / p.Hk), nc = n_chunks(ci.it.len);
-        for (int c = 0; c < nc && ok; ++c, ++n) {
+        for (int c = 0; c < nc; ++c, ++n) {
           const int s = n % kCarryStages;
           wait(&B->empty[s], ((n / kCarryStages) & 1) ^ 1);
-          if (!ok) break;
+          if (!(ok = together(ok))) break;
           if (lane == 0) {
             uint8_t* st = smem + s * kCarryBytes;
             const int t = ci.it.t0 + c * kC;
@@ -779,7 +809,7 @@ __global__ void __launch_bounds__(640, 1)
           __syncwarp();
         }
       }
-      if (!ok)   // copies still on their way into this CTA's shared memory
+      if (!together(ok))   // copies still on their way into this CTA's shared memory
         for (int m = n > kCarryStages ? n - kCarryStages : 0; m < n; ++m)
           mbar_wait_w(&B->full[m % kCarryStages], (m / kCarryStages) & 1, p.status, p.wait_ns);
     } else if (warp == 1) {
@@ -790,10 +820,10 @@ __global__ void __launch_bounds__(640, 1)
       const uint32_t id128 = idesc_bf16_f32(128, 0, 1);
       int n = 0;
       uint32_t nu1 = 0;   // chunks of unit 1
-      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+      for (int i = blockIdx.x; i < items && (ok = together(ok)); i += gridDim.x) {
         const CarryItem ci = get_carry(p, i);
         const int nc = n_chunks(ci.it.len), units = ci.it.tile == 0 ? 2 : 1;
-        for (int c = 0; c < nc && ok; ++c, ++n) {
+        for (int c = 0; c < nc && (ok = together(ok)); ++c, ++n) {
           const int s = n % kCarryStages;
           const uint32_t st = base + s * kCarryBytes;
           const uint64_t th = smem_desc_sw128(st + 4 * kBlk, 16, 1024);
@@ -870,6 +900,7 @@ __global__ void __launch_bounds__(640, 1)
           if (units == 2) ++nu1;
         }
       }
+      ok = together(ok);
       if (n > 0)   // every arrival on this CTA's barriers has landed before it ends
         wait(&B->empty[(n - 1) % kCarryStages], ((n - 1) / kCarryStages) & 1);
     } else if (warp == 2) {
@@ -1150,7 +1181,7 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
       const uint32_t pb = smem_u32(smem) + (j & 1) * kPBytes;
       wait(&B->full[j & 1], (j >> 1) & 1);
       wait(&B->s_ready, j & 1);
-      if (!ok) break;
+      if (!(ok = together(ok))) break;
       tc_fence_after();
       if (el) {
         const uint64_t ph = smem_desc_sw128(pb, 16384, 1024);
@@ -1165,6 +1196,7 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
       }
       __syncwarp();
       wait(&B->d_full, j & 1);
+      ok = together(ok);
       if (ok && loaded + 1 < n) {
         if (el) load(loaded);
         ++loaded;

@@ -65,22 +65,26 @@ __device__ __forceinline__ bool elect_lane() {
   return r != 0;
 }
 
-// Bounded wait of a whole warp; after one that ran out (ok false) the caller's
-// waits return at once, and it runs to its end.
+// Bounded wait, by every lane for itself (a vote after each wait would double its
+// 45 cycles, and a chunk's chain holds a dozen of them in turn).  After one that ran
+// out (ok false) a lane's waits return at once and the role runs to its end without
+// storing; loops bring `ok` together once an iteration (together()), before
+// anything that the whole warp must do together depends on it.
 __device__ __forceinline__ void wait_w(bool& ok, uint64_t* bar, uint32_t parity, int* status,
                                        unsigned long long lim) {
-  if (!ok || __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
+  if (!ok || mbar_try_wait(bar, parity)) return;
   unsigned long long since = 0;
-  while (!__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, 1000000u))) {
+  while (!mbar_try_wait_sleep(bar, parity, 1000000u)) {
     const unsigned long long now = global_ns();
     if (since == 0) since = now;
-    if (__any_sync(0xffffffffu, now - since > lim)) {
+    if (now - since > lim) {
       report_status(status, kStatusTimeout);
       ok = false;
       return;
     }
   }
 }
+__device__ __forceinline__ bool together(bool ok) { return __all_sync(0xffffffffu, ok); }
 
 // Two fp32 values in one 64-bit register, for the packed fp32 instructions.
 using F2 = unsigned long long;
