@@ -381,21 +381,8 @@ __global__ void __launch_bounds__(512, 1)
           const uint32_t ph = n & 1;
           const uint64_t th = smem_desc_sw128(rb, 16, 1024);
           const uint64_t tl = smem_desc_sw128(rb + kBlk, 16, 1024);
-          // T V, once the chunk before is done with X's columns
-          wait(&B->ready[n % kStages], (n / kStages) & 1);
-          wait(&B->t_full[ph], (n >> 1) & 1);
-          if (n > 0) wait(&B->ds_full, ph ^ 1);
-          tc_fence_after();
-          if (el) {
-            const uint64_t vd = smem_desc_sw128(st + 4 * kBlk, kBlk, 1024);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              umma_bf16(tmem + kX, vd + k * 128, tl + k * 2, id64m, k != 0);
-              umma_bf16(tmem + kX, vd + k * 128, th + k * 2, id64m, 1);
-            }
-          }
-          __syncwarp();
           // S K^T
+          wait(&B->ready[n % kStages], (n / kStages) & 1);
           const uint64_t kd = smem_desc_sw128(st + kBlk, 16, 1024);
 #pragma unroll
           for (int b = 0; b < 4; ++b) {   // 16 of each half of d_k at a time
@@ -413,6 +400,19 @@ __global__ void __launch_bounds__(512, 1)
             }
             __syncwarp();
           }
+          // T V, while S K^T is converted (the pairs of S that the chain has made say
+          // that the chunk before is done with X's columns)
+          wait(&B->t_full[ph], (n >> 1) & 1);
+          tc_fence_after();
+          if (el) {
+            const uint64_t vd = smem_desc_sw128(st + 4 * kBlk, kBlk, 1024);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              umma_bf16(tmem + kX, vd + k * 128, tl + k * 2, id64m, k != 0);
+              umma_bf16(tmem + kX, vd + k * 128, th + k * 2, id64m, 1);
+            }
+          }
+          __syncwarp();
           // X += T (-e^G K S^T)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {   // 16 of each half of the tokens at a time
@@ -830,7 +830,8 @@ __global__ void __launch_bounds__(640, 1)
           const uint64_t tl = smem_desc_sw128(st + 5 * kBlk, 16, 1024);
           const uint32_t ph[2] = {(uint32_t)n & 1, nu1 & 1};
           wait(&B->ready[s], (n / kCarryStages) & 1);
-          // T V, once the chunk before is done with X's columns
+          // T V, once the chunk before is done with X's columns (behind S K^T, as in the
+          // outputs' pass, it is slower here: the other unit's products wait then)
           if (n > 0) wait(&B->ds_full[0], ph[0] ^ 1);
           tc_fence_after();
           if (el) {
