@@ -216,6 +216,33 @@ __device__ __forceinline__ void store_state(float* tile, int q4, int half, int l
         make_ulonglong2(S[2 * c], S[2 * c + 1]);
 }
 
+// 64 columns of one row of a user's state (rows of dk numbers, dk a multiple of 8),
+// 32 bytes at a time; columns from dk on are zero.
+__device__ __forceinline__ void load_row(const float* from, int cols, F2 (&S)[32]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (8 * c < cols) ldg256(from + 8 * c, w);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      S[4 * c + e] = pack2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
+  }
+}
+__device__ __forceinline__ void store_row(float* to, int cols, const F2 (&S)[32]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float a, b;
+      unpack2(S[4 * c + e], a, b);
+      w[2 * e] = __float_as_uint(a);
+      w[2 * e + 1] = __float_as_uint(b);
+    }
+    if (8 * c < cols) stg256(to + 8 * c, w);
+  }
+}
+
 // 16 tokens' values of a row, each times f[token], as pairs at TMEM columns taddr
 // (8 of hi, 8 of lo: the operand of one MMA each).
 __device__ __forceinline__ void put_scaled(uint32_t taddr, const float (&x)[16], const float* f) {
@@ -526,14 +553,7 @@ __global__ void __launch_bounds__(512, 1)
       if (it.from_tile) {
         load_state(it.from_tile, q4, half, lane, S);
       } else {
-#pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (it.from && row < p.dv && 64 * half + c < p.dk)
-            x = *reinterpret_cast<const float4*>(it.from + so + c);
-          S[c / 2] = pack2(x.x, x.y);
-          S[c / 2 + 1] = pack2(x.z, x.w);
-        }
+        load_row(it.from + so, it.from && row < p.dv ? p.dk - 64 * half : 0, S);
       }
       auto put_S = [&]() {
 #pragma unroll
@@ -601,13 +621,7 @@ __global__ void __launch_bounds__(512, 1)
         }
         if (c + 1 < nc) put_S();
       }
-      if (ok && it.to && row < p.dv) {
-#pragma unroll
-        for (int c = 0; c < 64; c += 4)
-          if (64 * half + c < p.dk)
-            *reinterpret_cast<ulonglong2*>(it.to + so + c) =
-                make_ulonglong2(S[c / 2], S[c / 2 + 1]);
-      }
+      if (ok && it.to && row < p.dv) store_row(it.to + so, p.dk - 64 * half, S);
     }
   } else {
     // ---- outputs
@@ -1210,16 +1224,15 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
     const int q4 = warp & 3, half = warp >> 2;
     const int row = 128 * tile + 32 * q4 + lane;
     const uint32_t t = tmem + ((uint32_t)(q4 * 32) << 16) + 64 * half;
-    F2 S[32];
-#pragma unroll
-    for (int c = 0; c < 64; c += 4) {
-      ulonglong2 w = make_ulonglong2(0, 0);
-      if (p.S0 && row < p.dv && 64 * half + c < p.dk)
-        w = *reinterpret_cast<const ulonglong2*>(
-            p.S0 + (((long long)seq * p.Hv + h) * p.dv + row) * p.dk + 64 * half + c);
-      S[c / 2] = w.x;
-      S[c / 2 + 1] = w.y;
-    }
+    F2 S[32], L[32];   // L: a step ahead
+    load_row(p.S0 + (((long long)seq * p.Hv + h) * p.dv + row) * p.dk + 64 * half,
+             p.S0 && row < p.dv ? p.dk - 64 * half : 0, S);
+    auto load_L = [&](int j) {
+      load_state(p.L + (((long long)(seg0 + j) * p.Hv + h) * p.tiles + tile) * kStateFloats, q4, half,
+                 lane, L);
+    };
+    load_L(0);
+#pragma unroll 1
     for (int j = 0; j + 1 < n; ++j) {
       const long long sgh = (long long)(seg0 + j) * p.Hv + h;
 #pragma unroll
@@ -1234,7 +1247,6 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&B->s_ready);
-      load_state(p.L + (sgh * p.tiles + tile) * kStateFloats, q4, half, lane, S);
       wait(&B->d_full, j & 1);
       tc_fence_after();
 #pragma unroll
@@ -1243,8 +1255,9 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
         tmem_ld16_nowait(t + 128 + 16 * b, d);
         tmem_wait_bind(d);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) S[8 * b + e] = add2(S[8 * b + e], pack2(d[2 * e], d[2 * e + 1]));
+        for (int e = 0; e < 8; ++e) S[8 * b + e] = add2(L[8 * b + e], pack2(d[2 * e], d[2 * e + 1]));
       }
+      if (j + 2 < n) load_L(j + 1);
       if (ok)
         store_state(p.Sseg + ((sgh + p.Hv) * p.tiles + tile) * kStateFloats, q4, half, lane, S);
     }
@@ -1414,27 +1427,33 @@ Plan make_plan(int B, int Hv, int N, int dk, int dv, int n_seq, bool packed) {
   const int tiles = (dv + 127) / 128;
   const int nc = n_chunks(N);
   p.chunks = packed ? N / kC + n_seq : B * nc;
-  // Chunks per segment, from the times of a step on one SM (measured, in us): 2.65
-  // with outputs, 3.05 for L and P, each item about one step more; a join step 1.0
-  // by rows and 2.7 by tiles, and 10 to begin.
+  // Chunks per segment, from measured times in us: a step with outputs 2.25 and one
+  // of L and P 2.65, on one SM; beginnings 10 and 12; a join step 1.0 with four rows
+  // per CTA, 1.8 with eight, 2.0 by tiles, and 5 to begin.
   const long long units = (long long)(packed ? 1 : B) * Hv * tiles;
-  const double join = !packed && units * 16 <= kSms ? 1.0 : 2.7;
+  const double join = packed || units * 16 > kSms ? 2.0 : units * 32 > kSms ? 1.8 : 1.0;
+  auto rounds = [](double items) { return (double)(long long)((items + kSms - 1) / kSms); };
   double best = 0.0;
   p.seg_chunks = nc;
   for (int n = 1; n <= 128 && n <= nc; ++n) {
     const int lc = (nc + n - 1) / n;
-    double t;
+    double t, hops = n - 1;
     if (!packed) {   // sequences of one length: whole rounds of the SMs
-      t = 2.65 * (double)((units * n + kSms - 1) / kSms) * (lc + 1);
-      if (n > 1)
-        t += 3.05 * (double)((units * (n - 1) + kSms - 1) / kSms) * (lc + 1) + join * (n - 1) + 10.0;
-    } else {   // lengths unknown: an even share and one segment; the longest of n_seq
-      const double share = (double)units * nc / kSms;
+      t = 10.0 + 2.25 * rounds((double)units * n) * (lc + 1);
+      if (n > 1) t += 12.0 + 2.65 * rounds((double)units * (n - 1)) * (lc + 1);
+    } else {
+      // lengths unknown: of n_seq sequences half a segment is left over each, and the
+      // longest is about four times the mean
       const double longest = n_seq > 4 ? 4.0 * nc / n_seq : nc;
-      const double pieces = longest / lc;
-      t = 2.65 * (share + share / lc + (longest < lc ? longest : lc));
-      if (pieces > 1.0) t += 3.05 * (share + share / lc + lc) + join * pieces + 10.0;
+      double whole = (double)nc / lc - 0.5 * n_seq;
+      hops = longest / lc;
+      if (whole < hops) whole = hops;
+      if (hops < 1.0) whole = 0.0;
+      const double left = longest < lc ? longest : 0.75 * lc + 1.5;
+      t = 10.0 + 2.25 * (rounds(units * whole) * (lc + 1) + rounds((double)units * n_seq) * left);
+      if (whole > 0.0) t += 12.0 + 2.65 * rounds(units * whole) * (lc + 1);
     }
+    if (hops >= 1.0) t += 5.0 + join * hops;
     if (n == 1 || t < best) {
       best = t;
       p.seg_chunks = lc;
