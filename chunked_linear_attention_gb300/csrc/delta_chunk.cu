@@ -1130,8 +1130,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 // through all segments, S as pairs in TMEM, P_j as pairs from the carry pass (64 KB
 // by bulk copy, the next one on its way), three products, L_j added in fp32.
 // Warps 0-7: rows 32 (w % 4) .., half of the columns; warp 8: copies and MMAs.
-// A step takes one SM 2.7 us, its 192 KB of L, P and S; in fp32 on the CUDA cores it
-// took 16 of them 2.5 us.
+// (A step in fp32 on the CUDA cores took 16 SMs 2.5 us.)
 constexpr int kJoinThreads = 288;
 constexpr int kJoinSmem = 2 * kPBytes + 256 + 1024;
 
@@ -1224,17 +1223,12 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
     const int q4 = warp & 3, half = warp >> 2;
     const int row = 128 * tile + 32 * q4 + lane;
     const uint32_t t = tmem + ((uint32_t)(q4 * 32) << 16) + 64 * half;
-    F2 S[32], L[32];   // L: a step ahead
+    F2 S[32], L[32];
     load_row(p.S0 + (((long long)seq * p.Hv + h) * p.dv + row) * p.dk + 64 * half,
              p.S0 && row < p.dv ? p.dk - 64 * half : 0, S);
-    auto load_L = [&](int j) {
-      load_state(p.L + (((long long)(seg0 + j) * p.Hv + h) * p.tiles + tile) * kStateFloats, q4, half,
-                 lane, L);
-    };
-    load_L(0);
+    auto place = [&](int j) { return (((long long)(seg0 + j) * p.Hv + h) * p.tiles + tile) * kStateFloats; };
 #pragma unroll 1
     for (int j = 0; j + 1 < n; ++j) {
-      const long long sgh = (long long)(seg0 + j) * p.Hv + h;
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         uint32_t hi[8], lo[8];
@@ -1247,6 +1241,9 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&B->s_ready);
+      // beside the product: its 128 KB through the load-store units take as long
+      load_state(p.L + place(j), q4, half, lane, L);
+      if (ok && j > 0) store_state(p.Sseg + place(j), q4, half, lane, S);
       wait(&B->d_full, j & 1);
       tc_fence_after();
 #pragma unroll
@@ -1257,10 +1254,8 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
 #pragma unroll
         for (int e = 0; e < 8; ++e) S[8 * b + e] = add2(L[8 * b + e], pack2(d[2 * e], d[2 * e + 1]));
       }
-      if (j + 2 < n) load_L(j + 1);
-      if (ok)
-        store_state(p.Sseg + ((sgh + p.Hv) * p.tiles + tile) * kStateFloats, q4, half, lane, S);
     }
+    if (ok) store_state(p.Sseg + place(n - 1), q4, half, lane, S);
   }
   tc_fence_before();
   __syncthreads();
@@ -1271,8 +1266,8 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
 }
 
 // The same for few heads, in fp32 on the CUDA cores: a CTA takes R rows, so that a
-// head's step is spread over 128 / R SMs (one SM moves the 192 KB of a step above in
-// 2.7 us; here a step takes 1.0 us with R = 4, its 64 KB of P).  Each of the eight
+// head's step is spread over 128 / R SMs (one SM moves 192 KB in a step above; here a
+// step takes 1.0 us with R = 4, its 64 KB of P).  Each of the eight
 // warps takes sixteen rows of P and 4 columns per lane; the eight partial sums are
 // added in a fixed order.
 constexpr int kRowsThreads = 256;
