@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(512, 1)
   uint8_t* obuf = reinterpret_cast<uint8_t*>(scal + 4);   // outputs on their way
   Bars* B = reinterpret_cast<Bars*>(obuf + kOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int items = n_items(p, false);
+  pdl_launch_dependents();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -332,6 +332,8 @@ __global__ void __launch_bounds__(512, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B->tmem;
+  pdl_wait();
+  const int items = n_items(p, false);
   bool ok = true;   // after a wait that ran out: no more waiting, run to the end
   auto wait = [&](uint64_t* bar, uint32_t parity) { wait_w(ok, bar, parity, p.status, p.wait_ns); };
   auto arrive = [&](uint64_t* bar) {
@@ -766,7 +768,7 @@ __global__ void __launch_bounds__(640, 1)
   RecScal* scal = reinterpret_cast<RecScal*>(smem + kCarryStages * kCarryBytes);
   CarryBars* B = reinterpret_cast<CarryBars*>(scal + kCarryStages);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int items = n_items(p, true);
+  pdl_launch_dependents();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kCarryStages; ++s) {
@@ -789,6 +791,8 @@ __global__ void __launch_bounds__(640, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B->tmem;
+  pdl_wait();
+  const int items = n_items(p, true);
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) { wait_w(ok, bar, parity, p.status, p.wait_ns); };
   auto arrive = [&](uint64_t* bar) {
@@ -1072,6 +1076,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                       int seg_places, SeqPlan* plan, SegPlan* segs, int* order, int* joins,
                       int* counts, int* status) {
   __shared__ int part[kPlanThreads / 32];
+  pdl_launch_dependents();
   int chunk0 = 0, seg0 = 0, join0 = 0;
   for (int s0 = 0; s0 < n_seq; s0 += kPlanThreads) {
     const int s = s0 + (int)threadIdx.x;
@@ -1161,6 +1166,8 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
   JoinBars* B = reinterpret_cast<JoinBars*>(smem + 2 * kPBytes);
   const int tile = blockIdx.x % p.tiles, x = blockIdx.x / p.tiles;
   const int h = x % p.Hv, k = x / p.Hv;
+  pdl_launch_dependents();
+  pdl_wait();
   if (k >= (p.counts ? p.counts[2] : p.seqs)) return;
   const int seg0 = p.segs ? p.joins[k] : k * p.seg_n;
   const int seq = p.segs ? p.segs[seg0].seq : k, n = p.segs ? p.segs[seg0].n : p.seg_n;
@@ -1290,6 +1297,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   const int tile = x % p.tiles, h = x / p.tiles % p.Hv, seq = x / p.tiles / p.Hv;
   const int n = p.seg_n, seg0 = seq * n;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch_dependents();
+  pdl_wait();
   bool ok = true;
   auto load = [&](int j) {
     mbar_arrive_expect_tx(&sh.full[j & 1], kPBytes);
@@ -1375,9 +1384,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 }
 
 template <int R>
-void launch_rows(const JoinParams& j, cudaStream_t stream) {
-  delta_join_rows_kernel<R>
-      <<<j.seqs * j.Hv * j.tiles * (128 / R), kRowsThreads, sizeof(RowsShared<R>), stream>>>(j);
+cudaError_t launch_rows(const JoinParams& j, cudaStream_t stream) {
+  return launch_behind(delta_join_rows_kernel<R>, j.seqs * j.Hv * j.tiles * (128 / R), kRowsThreads,
+                       sizeof(RowsShared<R>), stream, j);
 }
 
 int g_ready[64] = {0};   // 0 unknown, 1 usable, 2 not usable
@@ -1573,8 +1582,9 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
       const int items = (packed ? pl.seg_places : a.B * (pl.seg_n - 1)) * a.Hv * p.tiles;
       ProfScope ps(PT_DELTA_CARRY, a.stream, 5.0 * tok * a.Hv * a.dk * (a.dv + a.dk),
                    tok * 2.0 * (a.Hk * a.dk + a.Hv * a.dv));
-      delta_carry_kernel<<<items < sms ? items : sms, 640, kCarrySmem, a.stream>>>(p);
-      if (cudaGetLastError() != cudaSuccess) return TTT_ERR_CUDA;
+      if (launch_behind(delta_carry_kernel, items < sms ? items : sms, 640, kCarrySmem, a.stream, p) !=
+          cudaSuccess)
+        return TTT_ERR_CUDA;
     }
     JoinParams j;
     j.segs = segs;
@@ -1595,16 +1605,20 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
                  4.0 * states * (a.dk + 2 * a.dv));
     // by rows where that still fits the card at once
     const long long tiles = (long long)a.n_seq * a.Hv * p.tiles;
-    if (!packed && tiles * 32 <= sms) launch_rows<4>(j, a.stream);
-    else if (!packed && tiles * 16 <= sms) launch_rows<8>(j, a.stream);
-    else delta_join_kernel<<<(unsigned)tiles, kJoinThreads, kJoinSmem, a.stream>>>(j);
-    if (cudaGetLastError() != cudaSuccess) return TTT_ERR_CUDA;
+    const cudaError_t e =
+        !packed && tiles * 32 <= sms   ? launch_rows<4>(j, a.stream)
+        : !packed && tiles * 16 <= sms ? launch_rows<8>(j, a.stream)
+                                       : launch_behind(delta_join_kernel, (unsigned)tiles, kJoinThreads,
+                                                       kJoinSmem, a.stream, j);
+    if (e != cudaSuccess) return TTT_ERR_CUDA;
   }
   const int items = pl.seg_places * a.Hv * p.tiles;
   ProfScope ps(PT_DELTA_CHUNK, a.stream, 7.0 * tok * a.Hv * a.dk * a.dv,
                tok * 4.0 * (a.Hk * a.dk + a.Hv * a.dv));
-  delta_scan_kernel<<<items < sms ? items : sms, 512, kSmem, a.stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+  return launch_behind(delta_scan_kernel, items < sms ? items : sms, 512, kSmem, a.stream, p) ==
+                 cudaSuccess
+             ? TTT_OK
+             : TTT_ERR_CUDA;
 }
 
 }  // namespace ttt

@@ -121,6 +121,8 @@ __global__ void __launch_bounds__(kPThreads, 6)
   PrepShared& sh = *reinterpret_cast<PrepShared*>(tile + 4 * kBlk);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hk = blockIdx.x % p.Hk, place = blockIdx.x / p.Hk;
+  pdl_launch_dependents();
+  if (p.plan) pdl_wait();   // the plan is the kernel before
   // the chunk at this place
   int seq, c;
   if (p.plan) {   // last sequence whose first chunk is not behind the place
@@ -440,6 +442,8 @@ cudaError_t launch_delta_prep(const PrepParams& p, int chunks, cudaStream_t stre
   const double rec = (double)chunks * p.Hv;
   ProfScope ps(PT_DELTA_PREP, stream, 2.0 * 128 * 64 * 128 * (double)chunks * p.Hk,
                rec * (kRecBytes + sizeof(RecScal)) + 32768.0 * chunks * p.Hk);
+  if (p.plan)
+    return launch_behind(delta_prep_kernel, (unsigned)(chunks * p.Hk), kPThreads, kPSmem, stream, p);
   delta_prep_kernel<<<(unsigned)(chunks * p.Hk), kPThreads, kPSmem, stream>>>(p);
   return cudaGetLastError();
 }

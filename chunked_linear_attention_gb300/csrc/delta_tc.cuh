@@ -137,6 +137,25 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // ---------------------------------------------------------------- host side
+// Launch that may begin while the kernel before it in the stream still runs: its
+// prologue (barriers, TMEM, tensor maps) overlaps that kernel's end.  The kernel
+// calls pdl_wait() before it touches memory.
+template <typename P>
+cudaError_t launch_behind(void (*kern)(P), unsigned grid, unsigned block, size_t smem,
+                          cudaStream_t stream, const P& params) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, params);
+}
+
 // [B, H, N, d] bf16 with the given strides as a map of 64 x 64 boxes; false
 // where TMA cannot take it.
 bool delta_map(CUtensorMap* m, const void* ptr, const delta_rule_stride& s, int B, int H, int N,
