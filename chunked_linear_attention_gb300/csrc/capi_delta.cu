@@ -17,7 +17,8 @@ int check_rule(int B, int Hk, int Hv, int N, int dk, int dv, int n_seq, int io) 
   if (B != 1 && n_seq != B) return TTT_ERR_SHAPE;
   if (io != TTT_F32 && io != TTT_BF16) return TTT_ERR_ARG;
   if (dk > 512 || dv > 1024) return TTT_ERR_UNSUPPORTED;
-  if ((long long)n_seq * Hv > (1 << 20)) return TTT_ERR_UNSUPPORTED;
+  if ((long long)n_seq * Hv > (1 << 20) || (long long)B * Hv * N > (1LL << 31) - 1)
+    return TTT_ERR_UNSUPPORTED;
   return TTT_OK;
 }
 

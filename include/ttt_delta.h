@@ -60,7 +60,9 @@ size_t delta_rule_workspace_size(int B, int Hk, int Hv, int N, int d_k, int d_v,
  *               may be 0.  Tokens of no sequence are not read and their rows
  *               of out are not written.  Entries that are not ascending or not
  *               within 0..N make their sequence empty and set TTT_ERR_ARG in
- *               the device status word (ttt_device_status).
+ *               the device status word (ttt_device_status); other sequences
+ *               that overlap around such entries have undefined results
+ *               (nothing outside the tensors is touched).
  *   scale       factor of the outputs (d_k^-1/2 is usual).
  *   layout      HOST pointer or NULL.
  *   out         [B, Hv, N, d_v] in io_dtype.  May not overlap an input.
@@ -71,11 +73,14 @@ size_t delta_rule_workspace_size(int B, int Hk, int Hv, int N, int d_k, int d_v,
  *               not shared with a concurrent call.
  *
  * io_dtype TTT_BF16 with d_k <= 128, d_k and d_v multiples of 8, and q, k, v
- * 16-byte aligned with strides that are multiples of 8 elements runs chunks of
- * 64 tokens on the tensor cores, every intermediate held as a pair of bf16
- * numbers (16 bits of significand) with fp32 sums and state; all other calls
- * run token by token in fp32.  Supported: d_k <= 512, d_v <= 1024, and
- * B * Hv and n_seq * Hv at most 2^20.
+ * 16-byte aligned with strides that are multiples of 8 elements (and not 0)
+ * runs chunks of 64 tokens on the tensor cores, every intermediate held as a
+ * pair of bf16 numbers (16 bits of significand) with fp32 sums and state; there
+ * a NaN or infinity in a token's v may also reach the outputs of the up to 63
+ * tokens before it in its chunk.  All other calls run token by token in fp32.
+ * Decays below exp(-104) count as exp(-104) (zero in fp32).
+ * Supported: d_k <= 512, d_v <= 1024, n_seq * Hv at most 2^20, and
+ * B * Hv * N below 2^31.
  * S0 and S_final must be 16-byte aligned. */
 int delta_rule_chunked_forward(const void* q, const void* k, const void* v, const float* g,
                                const float* beta, const float* S0, const int* seq_starts,

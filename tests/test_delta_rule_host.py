@@ -46,6 +46,7 @@ def test_rule_refusals(cla):
     assert rule(cla, dk=513) == TTT_ERR_UNSUPPORTED
     assert rule(cla, dv=1025) == TTT_ERR_UNSUPPORTED
     assert rule(cla, n_seq=1 << 20, packed=True) == TTT_ERR_UNSUPPORTED
+    assert rule(cla, N=1 << 30) == TTT_ERR_UNSUPPORTED
     assert rule(cla, off=(5,)) == TTT_ERR_ALIGN          # S0
     assert rule(cla, off=(8,)) == TTT_ERR_ALIGN          # S_final
     assert rule(cla, off=(3,)) == TTT_ERR_ALIGN          # g: 4-byte

@@ -234,6 +234,59 @@ def test_long_sequences_split_over_the_card():
     check(cla, run(cla, t, S0, starts), oracle(t, S0, starts), torch.bfloat16)
 
 
+SPLITS = [
+    # B, Hk, Hv, N, dk, dv: four, eight and sixteen heads take the join's three
+    # forms; two tiles of d_v, and head sizes below the tile's
+    (1, 2, 4, 2000, 128, 128),
+    (1, 2, 8, 1500, 128, 128),
+    (1, 4, 16, 1400, 64, 128),
+    (2, 2, 2, 1300, 128, 256),
+    (1, 3, 6, 1290, 96, 72),
+]
+
+
+@pytest.mark.parametrize("size", SPLITS, ids=str)
+def test_segments(size):
+    """Sequences that are cut into segments: start states and outputs across
+    the joins, weak forgetting so that they matter."""
+    cla = lib()
+    B, Hk, Hv, N, dk, dv = size
+    t = inputs(40, *size, torch.bfloat16, 0.01)
+    S0 = torch.randn(B, Hv, dv, dk, generator=torch.Generator().manual_seed(41)) * 0.3
+    ref = oracle(t, S0)
+    run(cla, t, S0)
+    cla.profile_start()
+    got = run(cla, t, S0)
+    kinds = {e["name"] for e in cla.profile_stop()}
+    assert {"delta.prep", "delta.carry", "delta.join", "delta.chunk"} <= kinds
+    check(cla, got, ref, torch.bfloat16)
+
+
+def test_many_packed_sequences():
+    """More sequences than the plan's block has threads, one of them long."""
+    cla = lib()
+    gen = torch.Generator().manual_seed(42)
+    lens = torch.randint(0, 40, (300,), generator=gen).tolist()
+    lens[77], lens[299] = 1500, 65
+    starts = [0] + torch.tensor(lens).cumsum(0).tolist()
+    t = inputs(43, 1, 1, 2, starts[-1] + 3, 128, 128, torch.bfloat16, 0.05)
+    S0 = torch.randn(300, 2, 128, 128, generator=gen) * 0.3
+    check(cla, run(cla, t, S0, starts), oracle(t, S0, starts), torch.bfloat16)
+
+
+def test_zero_length_axis_edges_and_one_token_sequences():
+    """A packed batch of single tokens, and one in which every sequence is
+    empty: outputs untouched, states unchanged."""
+    cla = lib()
+    t = inputs(44, 1, 2, 2, 9, 128, 128, torch.bfloat16)
+    S0 = torch.randn(9, 2, 128, 128, generator=torch.Generator().manual_seed(45))
+    check(cla, run(cla, t, S0, list(range(10))), oracle(t, S0, list(range(10))), torch.bfloat16)
+    out = torch.full((1, 2, 9, 128), 3.0, dtype=torch.bfloat16, device=DEV)
+    o, S = run(cla, t, S0[:4], [5, 5, 5, 5, 5], out=out)
+    assert_status_ok(cla)
+    assert (o == 3.0).all() and torch.equal(S.cpu(), S0[:4])
+
+
 def test_same_call_twice_gives_the_same_bits():
     cla = lib()
     t = inputs(15, 2, 1, 2, 1000, 128, 128, torch.bfloat16)
