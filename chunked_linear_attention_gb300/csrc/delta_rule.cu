@@ -95,38 +95,59 @@ __global__ void __launch_bounds__(256) delta_recurrent_kernel(const __grid_const
   const int row0 = tile * ROWS;
   const int ntile = (len + TT - 1) / TT;
 
-  auto load = [&](int it, int buf) {               // by the loader warps
-    for (int j = warp - kRecWarps; j < TT; j += kRecWarps) {
-      const int t = it * TT + j;
-      if (t >= len) break;
-      float* d = stage + (buf * TT + j) * TOK;
+  // by the loader warps: all of a warp's tokens are on their way before the first
+  // is put down (one after the other, a tile waited for four trips to memory)
+  constexpr int TPW = TT / kRecWarps, KE = W / 32, VE = (ROWS + 31) / 32;
+  auto load = [&](int it, int buf) {
+    float kv[TPW][KE], qv[TPW][KE], vv[TPW][VE], gv[TPW], bv[TPW];
+#pragma unroll
+    for (int x = 0; x < TPW; ++x) {
+      const int t = it * TT + x * kRecWarps + warp - kRecWarps;
+      const bool in = t < len;
+#pragma unroll
+      for (int e = 0; e < KE; ++e) {
+        const int c = 32 * e + lane;
+        kv[x][e] = in && c < p.dk ? to_f<T>(k[t * p.lay.k.token + c]) : 0.f;
+        qv[x][e] = in && c < p.dk ? to_f<T>(q[t * p.lay.q.token + c]) : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const int c = 32 * e + lane;
+        vv[x][e] = in && c < ROWS && row0 + c < p.dv ? to_f<T>(v[t * p.lay.v.token + row0 + c]) : 0.f;
+      }
+      gv[x] = in ? g[t * p.lay.g.token] : 0.f;
+      bv[x] = in ? be[t * p.lay.beta.token] : 0.f;
+    }
+#pragma unroll
+    for (int x = 0; x < TPW; ++x) {
+      float* d = stage + (buf * TT + x * kRecWarps + warp - kRecWarps) * TOK;
       float kq = 0.f;
-      for (int c = lane; c < W; c += 32) {
-        const float kv = c < p.dk ? to_f<T>(k[t * p.lay.k.token + c]) : 0.f;
-        const float qv = c < p.dk ? to_f<T>(q[t * p.lay.q.token + c]) : 0.f;
-        d[c] = kv;
-        d[W + c] = qv;
-        kq = fmaf(kv, qv, kq);
+#pragma unroll
+      for (int e = 0; e < KE; ++e) {
+        d[32 * e + lane] = kv[x][e];
+        d[W + 32 * e + lane] = qv[x][e];
+        kq = fmaf(kv[x][e], qv[x][e], kq);
       }
-      for (int c = lane; c < ROWS; c += 32)
-        d[2 * W + c] = row0 + c < p.dv ? to_f<T>(v[t * p.lay.v.token + row0 + c]) : 0.f;
+#pragma unroll
+      for (int e = 0; e < VE; ++e)
+        if (32 * e + lane < ROWS) d[2 * W + 32 * e + lane] = vv[x][e];
       kq = sum_lanes<32>(kq);
-      if (lane == 0) {
-        d[2 * W + ROWS] = expf(g[t * p.lay.g.token]);
-        d[2 * W + ROWS + 1] = be[t * p.lay.beta.token];
-        d[2 * W + ROWS + 2] = kq;
-      }
+      if (lane == 0)
+        *reinterpret_cast<float4*>(d + 2 * W + ROWS) = make_float4(expf(gv[x]), bv[x], kq, 0.f);
     }
   };
 
   const int l = lane % L;
   float S[R][E];
   int row[R];
+  bool mine[R];   // this lane stores the row's outputs
+  T* op = out + row0 + warp * R * (32 / L) + lane / L;
   const long long sbase = (long long)sh * p.dv * p.dk;
   if (warp < kRecWarps) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       row[r] = (warp * R + r) * (32 / L) + lane / L;
+      mine[r] = l == 0 && row0 + row[r] < p.dv;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int c = elem<L>(l, e);
@@ -145,34 +166,55 @@ __global__ void __launch_bounds__(256) delta_recurrent_kernel(const __grid_const
       if (it + 1 < ntile) load(it + 1, buf ^ 1);
     } else {
       const int n = min(TT, len - it * TT);
-      for (int j = 0; j < n; ++j) {
-        const float* d = stage + (buf * TT + j) * TOK;
-        float kk[E], qq[E];
+      // a token's operands are read while the one before it is worked on
+      float kk[E], qq[E], vv[R];
+      float4 f;
+      const float* d = stage + buf * TT * TOK;
+      auto fetch = [&]() {
 #pragma unroll
         for (int e = 0; e < E; e += 4) {
-          *reinterpret_cast<float4*>(&kk[e]) =
-              *reinterpret_cast<const float4*>(d + elem<L>(l, e));
+          *reinterpret_cast<float4*>(&kk[e]) = *reinterpret_cast<const float4*>(d + elem<L>(l, e));
           *reinterpret_cast<float4*>(&qq[e]) =
               *reinterpret_cast<const float4*>(d + W + elem<L>(l, e));
         }
-        const float a = d[2 * W + ROWS], b = d[2 * W + ROWS + 1], kq = d[2 * W + ROWS + 2];
+#pragma unroll
+        for (int r = 0; r < R; ++r) vv[r] = d[2 * W + row[r]];
+        f = *reinterpret_cast<const float4*>(d + 2 * W + ROWS);   // decay, beta, k . q
+        d += TOK;
+      };
+      fetch();
+#pragma unroll 2
+      for (int j = 0; j < n; ++j) {
+        float k0[E], v0[R], sk[R], sq[R];
+        const float4 f0 = f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          float sk = 0.f, sq = 0.f;
+          v0[r] = vv[r];
+          float a[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f};   // short chains
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            sk = fmaf(S[r][e], kk[e], sk);
-            sq = fmaf(S[r][e], qq[e], sq);
+            a[e & 3] = fmaf(S[r][e], kk[e], a[e & 3]);
+            c[e & 3] = fmaf(S[r][e], qq[e], c[e & 3]);
           }
-          sk = sum_lanes<L>(sk);
-          sq = sum_lanes<L>(sq);
-          const float u = b * (d[2 * W + row[r]] - a * sk);
-#pragma unroll
-          for (int e = 0; e < E; ++e) S[r][e] = fmaf(u, kk[e], a * S[r][e]);
-          if (l == 0 && row0 + row[r] < p.dv)
-            out[(long long)(it * TT + j) * p.lay.out.token + row0 + row[r]] =
-                from_f<T>(p.scale * fmaf(u, kq, a * sq));
+          sk[r] = (a[0] + a[1]) + (a[2] + a[3]);
+          sq[r] = (c[0] + c[1]) + (c[2] + c[3]);
         }
+#pragma unroll
+        for (int e = 0; e < E; ++e) k0[e] = kk[e];
+        if (j + 1 < n) fetch();
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          sk[r] = sum_lanes<L>(sk[r]);
+          sq[r] = sum_lanes<L>(sq[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float u = f0.y * (v0[r] - f0.x * sk[r]);
+#pragma unroll
+          for (int e = 0; e < E; ++e) S[r][e] = fmaf(u, k0[e], f0.x * S[r][e]);
+          if (mine[r]) op[32 / L * r] = from_f<T>(p.scale * fmaf(u, f0.z, f0.x * sq[r]));
+        }
+        op += p.lay.out.token;
       }
     }
     __syncthreads();
