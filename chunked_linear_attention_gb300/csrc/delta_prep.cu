@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(kPThreads, 6)
     }
   }
   if (warp == 1) tmem_alloc(&sh.tmem, kPCols);
-  // this head's g and beta: warp 0, tokens lane and lane + 32
+  // this head's g and beta: warp 3 (beside warp 0's wait for the tiles), tokens lane
+  // and lane + 32
   float gv[2] = {0.f, 0.f}, bv[2] = {0.f, 0.f};
   auto load_gates = [&](int h) {
     const float* g = p.g + batch * p.sg.batch + h * p.sg.head + t0 * p.sg.token;
@@ -169,12 +170,12 @@ __global__ void __launch_bounds__(kPThreads, 6)
       bv[e] = t < valid ? be[t * p.sb.token] : 0.f;
     }
   };
-  if (warp == 0) load_gates(hk * group);
+  if (warp == 3) load_gates(hk * group);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  wait_w(ok, &sh.full, 0, p.status, p.wait_ns);
+  if (warp == 0 || valid < kC) wait_w(ok, &sh.full, 0, p.status, p.wait_ns);
   if (valid < kC) {   // rows behind the sequence's end: other tokens, or none
     const int pieces = (kC - valid) * 8;
     for (int b = 0; b < 4; ++b)
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(kPThreads, 6)
 #pragma unroll 1
   for (int hg = 0; hg < group; ++hg) {
     const int h = hk * group + hg;
-    if (warp == 0) {
+    if (warp == 3) {
       constexpr float kLog2e = 1.4426950408889634f;
       float gl[2], tot[2];
 #pragma unroll
