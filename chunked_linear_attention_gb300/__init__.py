@@ -432,30 +432,28 @@ def linattn_chunked_forward_noalloc(q, k, v, eta, chunk: int, mask_mode: int,
 _pack_layout = struct.Struct("18q").pack
 _pack_norm_strides = struct.Struct("5q").pack
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_BF16, _F32 = torch.bfloat16, torch.float32
 
 
 def _elsewhere(dev, stream):
-    """None where `dev` is current and no stream is given; else a context that
-    makes them so (outputs and workspace then belong to the stream that uses
-    them)."""
-    if dev.type != "cuda":
-        raise ValueError("tensors passed to the CUDA path must be on a CUDA device")
+    """A context that makes `dev` current and `stream` too where one is given
+    (outputs and workspace then belong to the stream that uses them)."""
     if stream is not None:
         if stream.device != dev:
             raise ValueError(f"the stream must be on {dev}")
         return torch.cuda.stream(stream)
-    if dev.index != torch.cuda.current_device():
-        return torch.cuda.device(dev)
-    return None
+    return torch.cuda.device(dev)
 
 
 def _want(t, shape, dtype, dev, what):
+    if t.shape == shape and t.dtype is dtype and t.device == dev:
+        return
     if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{what} must be on {dev}, got {t.device}")
+    raise ValueError(f"{what} must be on {dev}, got {t.device}")
 
 
 def _strides(t, what):
@@ -487,16 +485,17 @@ def delta_rule_chunked_forward(q, k, v, g, beta, S0: Optional[torch.Tensor] = No
     stored in v's order of dimensions.  Returns (out [B, Hv, N, d_v], S_final).
     """
     dev = q.device
-    ctx = _elsewhere(dev, stream)
-    if ctx is not None:
-        with ctx:
+    if dev.type != "cuda":
+        raise ValueError("tensors passed to the CUDA path must be on a CUDA device")
+    if stream is not None or dev.index != _current_device():
+        with _elsewhere(dev, stream):
             return delta_rule_chunked_forward(q, k, v, g, beta, S0, seq_starts, scale, out,
                                               S_final, workspace)
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q and v must have four dimensions")
     B, Hk, N, dk = q.shape
     Hv, dv = v.shape[1], v.shape[3]
-    dt, io, f32 = q.dtype, _io_dtype(q), torch.float32
+    dt, io, f32 = q.dtype, _io_dtype(q), _F32
     _want(k, (B, Hk, N, dk), dt, dev, "k")
     _want(v, (B, Hv, N, dv), dt, dev, "v")
     _want(g, (B, Hv, N), f32, dev, "g")
@@ -509,7 +508,7 @@ def delta_rule_chunked_forward(q, k, v, g, beta, S0: Optional[torch.Tensor] = No
         if n_seq < 1 or not seq_starts.is_contiguous():
             raise ValueError("seq_starts must be a contiguous vector of n_seq + 1 entries")
         _want(seq_starts, (n_seq + 1,), torch.int32, dev, "seq_starts")
-    lib = library()
+    lib = _lib or library()
     if out is None:
         out = torch.empty_like(v)   # v's strides where they are dense, else row-major
     else:
@@ -524,17 +523,18 @@ def delta_rule_chunked_forward(q, k, v, g, beta, S0: Optional[torch.Tensor] = No
     if workspace is None:
         need = lib.delta_rule_workspace_size(B, Hk, Hv, N, dk, dv, n_seq, io)
         workspace = torch.empty(need or 256, device=dev, dtype=torch.uint8)
-    elif workspace.device != dev:
-        raise ValueError(f"workspace must be on {dev}")
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
     rc = lib.delta_rule_chunked_forward(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(S0),
         None if seq_starts is None else seq_starts.data_ptr(), n_seq, B, Hk, Hv, N, dk, dv, io,
         dk ** -0.5 if scale is None else scale,
         _pack_layout(*_strides(q, "q")[:3], *_strides(k, "k")[:3], *_strides(v, "v")[:3],
                      *g.stride(), *beta.stride(), *_strides(out, "out")[:3]),
-        out.data_ptr(), _ptr(S_final), _ptr(workspace), workspace.nbytes,
+        out.data_ptr(), _ptr(S_final), workspace.data_ptr(), workspace.nbytes,
         _raw_stream(dev.index))
-    _check(rc, "delta_rule_chunked_forward")
+    if rc:
+        _check(rc, "delta_rule_chunked_forward")
     return out, S_final
 
 
@@ -550,15 +550,16 @@ def delta_rule_step(q, k, v, g, beta, state, slots: Optional[torch.Tensor] = Non
     slots int32 [B] (negative: an idle row) or None.  Returns out [B, Hv, d_v].
     """
     dev = q.device
-    ctx = _elsewhere(dev, stream)
-    if ctx is not None:
-        with ctx:
+    if dev.type != "cuda":
+        raise ValueError("tensors passed to the CUDA path must be on a CUDA device")
+    if stream is not None or dev.index != _current_device():
+        with _elsewhere(dev, stream):
             return delta_rule_step(q, k, v, g, beta, state, slots, scale, out)
     if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
         raise ValueError("q and v must have three dimensions, state four")
     B, Hk, dk = q.shape
     Hv, dv = v.shape[1], v.shape[2]
-    dt, io, f32 = q.dtype, _io_dtype(q), torch.float32
+    dt, io, f32 = q.dtype, _io_dtype(q), _F32
     _want(k, (B, Hk, dk), dt, dev, "k")
     _want(v, (B, Hv, dv), dt, dev, "v")
     _want(g, (B, Hv), f32, dev, "g")
@@ -573,14 +574,15 @@ def delta_rule_step(q, k, v, g, beta, state, slots: Optional[torch.Tensor] = Non
         out = torch.empty((B, Hv, dv), device=dev, dtype=dt)
     else:
         _want(out, (B, Hv, dv), dt, dev, "out")
-    rc = library().delta_rule_step(
+    rc = (_lib or library()).delta_rule_step(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(state),
         None if slots is None else slots.data_ptr(), n_slots, B, Hk, Hv, dk, dv, io,
         dk ** -0.5 if scale is None else scale,
         _pack_layout(*_strides(q, "q")[:2], 0, *_strides(k, "k")[:2], 0, *_strides(v, "v")[:2], 0,
                      *g.stride(), 0, *beta.stride(), 0, *_strides(out, "out")[:2], 0),
         out.data_ptr(), _raw_stream(dev.index))
-    _check(rc, "delta_rule_step")
+    if rc:
+        _check(rc, "delta_rule_step")
     return out
 
 
@@ -621,12 +623,13 @@ def block_norm_forward(y, w: Optional[torch.Tensor] = None,
     and w_next [D] fp32.  Returns (out, h); h is None without ``w_next``.
     """
     dev = y.device
-    ctx = _elsewhere(dev, stream)
-    if ctx is not None:
-        with ctx:
+    if dev.type != "cuda":
+        raise ValueError("tensors passed to the CUDA path must be on a CUDA device")
+    if stream is not None or dev.index != _current_device():
+        with _elsewhere(dev, stream):
             return block_norm_forward(y, w, gate, gate_act, residual, scale, w_next, group, eps,
                                       out_dtype, out, h)
-    D, n, dt, io, f32 = y.shape[-1], y.numel(), y.dtype, _io_dtype(y), torch.float32
+    D, n, dt, io, f32 = y.shape[-1], y.numel(), y.dtype, _io_dtype(y), _F32
     if n == 0:
         raise ValueError("y must not be empty")
     rows = n // D
@@ -646,7 +649,7 @@ def block_norm_forward(y, w: Optional[torch.Tensor] = None,
         raise ValueError("h needs w_next")
     if out is None:
         out = torch.empty(y.shape, device=dev, dtype=out_dtype)
-    rc = library().block_norm_forward(
+    rc = (_lib or library()).block_norm_forward(
         y.data_ptr(), _ptr(w), None if gate is None else gate.data_ptr(),
         None if residual is None else residual.data_ptr(), _ptr(scale), _ptr(w_next), rows, D,
         group, io, _io_dtype(out), gate_act, eps,
@@ -657,7 +660,8 @@ def block_norm_forward(y, w: Optional[torch.Tensor] = None,
             _rows(out, rows, D, out_dtype, dev, "out"),
             0 if h is None else _rows(h, rows, D, dt, dev, "h")),
         out.data_ptr(), None if h is None else h.data_ptr(), _raw_stream(dev.index))
-    _check(rc, "block_norm_forward")
+    if rc:
+        _check(rc, "block_norm_forward")
     return out, h
 
 
