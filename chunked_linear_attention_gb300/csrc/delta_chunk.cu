@@ -176,6 +176,11 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* w) {
                "r"(w[7])
                : "memory");
 }
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&w)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -255,6 +260,24 @@ __device__ __forceinline__ void put_scaled(uint32_t taddr, const float (&x)[16],
   }
   tmem_st8(taddr, hi);
   tmem_st8(taddr + 8, lo);
+}
+
+// put_scaled with half of the registers at a time.
+__device__ __forceinline__ void put_scaled_lean(uint32_t taddr, const float (&x)[16],
+                                                const float* f) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(f + 8 * h + 2 * e);
+      const int c = 8 * h + 2 * e;
+      split2(mul2(w.x, pack2(x[c], x[c + 1])), hi[e], lo[e]);
+      split2(mul2(w.y, pack2(x[c + 2], x[c + 3])), hi[e + 1], lo[e + 1]);
+    }
+    tmem_st4(taddr + 4 * h, hi);
+    tmem_st4(taddr + 8 + 4 * h, lo);
+  }
 }
 
 // The same without a factor.
@@ -467,7 +490,7 @@ __global__ void __launch_bounds__(512, 1)
           tc_fence_after();
           if (el) {
             const uint64_t qd = smem_desc_sw128(st, 16, 1024);
-#pragma unroll
+#pragma unroll 4
             for (int k = 0; k < 16; ++k)
               umma_ts(tmem + kQS, tmem + kSh + (k >> 1) * 16 + (k & 1) * 8,
                       qd + (k >> 3) * (2 * kBlk / 16) + ((k >> 1) & 3) * 2, id64, k != 0);
@@ -570,10 +593,10 @@ __global__ void __launch_bounds__(512, 1)
           arrive(&B->s_ready[b]);
         }
       };
-      if (nc > 0) put_S();
 #pragma unroll 1
       for (int c = 0; c < nc; ++c, ++n) {
         const uint32_t ph = n & 1;
+        put_S();
         const RecScal& sc = scal[n & 3];
         float x[2][16];
         wait(&B->t_full[ph], (n >> 1) & 1);
@@ -621,7 +644,6 @@ __global__ void __launch_bounds__(512, 1)
           for (int e = 0; e < 8; ++e)
             S[8 * b + e] = fma2(eall, S[8 * b + e], pack2(x[0][2 * e], x[0][2 * e + 1]));
         }
-        if (c + 1 < nc) put_S();
       }
       if (ok && it.to && row < p.dv) store_row(it.to + so, p.dk - 64 * half, S);
     }
@@ -961,12 +983,12 @@ __global__ void __launch_bounds__(640, 1)
       }
       auto put_S = [&]() {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t hi[8], lo[8];
+        for (int b = 0; b < 8; ++b) {
+          uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) split2(S[8 * b + e], hi[e], lo[e]);
-          tmem_st8(d + 64 * half + 16 * b, hi);
-          tmem_st8(d + 64 * half + 16 * b + 8, lo);
+          for (int e = 0; e < 4; ++e) split2(S[4 * b + e], hi[e], lo[e]);
+          tmem_st4(d + 64 * half + 16 * (b >> 1) + 4 * (b & 1), hi);
+          tmem_st4(d + 64 * half + 16 * (b >> 1) + 8 + 4 * (b & 1), lo);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -987,7 +1009,7 @@ __global__ void __launch_bounds__(640, 1)
           float x[16];
           tmem_ld16_nowait(a, x);
           tmem_wait_bind(x);
-          put_scaled(a, x, &sc.neg[32 * half + 16 * b]);
+          put_scaled_lean(a, x, &sc.neg[32 * half + 16 * b]);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -1001,7 +1023,7 @@ __global__ void __launch_bounds__(640, 1)
           float x[16];
           tmem_ld16_nowait(a, x);
           tmem_wait_bind(x);
-          put_scaled(a, x, &sc.er[32 * half + 16 * b]);
+          put_scaled_lean(a, x, &sc.er[32 * half + 16 * b]);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -1514,6 +1536,10 @@ size_t delta_rule_chunk_workspace(int B, int Hv, int N, int dk, int dv, int n_se
 
 int delta_rule_chunk_launch(const DeltaArgs& a) {
   if (!a.bf16 || a.dk > 128) return 1;
+  // A few tokens of a few heads are done sooner token by token, in one launch (16
+  // heads: 32 tokens 14.4 us, here 16.4; 48 tokens 16.4 and 16.5; 64 tokens 20.5 and
+  // 16.4; with more CTAs than SMs it is slower from 16 tokens on).
+  if (a.N <= 40 && (long long)a.n_seq * a.Hv * ((a.dv + 15) / 16) <= kSms) return 1;
   PrepParams r;
   ScanParams p;
   if (!delta_map(&p.q, a.q, a.lay.q, a.B, a.Hk, a.N, a.dk) ||

@@ -77,7 +77,8 @@ size_t delta_rule_workspace_size(int B, int Hk, int Hv, int N, int d_k, int d_v,
  * runs chunks of 64 tokens on the tensor cores, every intermediate held as a
  * pair of bf16 numbers (16 bits of significand) with fp32 sums and state; there
  * a NaN or infinity in a token's v may also reach the outputs of the up to 63
- * tokens before it in its chunk.  All other calls run token by token in fp32.
+ * tokens before it in its chunk.  All other calls, and ones of a few tokens,
+ * run token by token in fp32.
  * Decays below exp(-104) count as exp(-104) (zero in fp32).
  * Supported: d_k <= 512, d_v <= 1024, n_seq * Hv at most 2^20, and
  * B * Hv * N below 2^31.
