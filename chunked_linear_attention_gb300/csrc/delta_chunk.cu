@@ -1136,12 +1136,28 @@ __global__ void __launch_bounds__(kPlanThreads)
     chunk0 += tc;
     seg0 += ts;
   }
-  // the last segments, behind the whole ones
-  __syncthreads();
+  // The last segments, behind the whole ones, long ones first: each CTA takes every
+  // 152nd item, and the short ones fill up the rounds.  (Order among equals does not
+  // matter to any result.)
+  __shared__ int count[kPlanThreads], base[kPlanThreads];
+  count[threadIdx.x] = 0;
+  __syncthreads();   // segs and plan are written
   const int whole = seg0 - n_seq;
+  auto bin = [&](const SegPlan& sg) {   // by chunks, the most in bin 0
+    const int left = n_chunks(plan[sg.seq].len) - sg.j * seg_chunks;
+    return kPlanThreads - 1 - min(left, kPlanThreads - 1);
+  };
   for (int i = (int)threadIdx.x; i < seg0; i += kPlanThreads) {
     const SegPlan sg = segs[i];
-    if (sg.j == sg.n - 1) order[whole + sg.seq] = i;
+    if (sg.j == sg.n - 1) atomicAdd(&count[bin(sg)], 1);
+  }
+  __syncthreads();
+  int all;
+  base[threadIdx.x] = block_before(count[threadIdx.x], part, all);
+  __syncthreads();
+  for (int i = (int)threadIdx.x; i < seg0; i += kPlanThreads) {
+    const SegPlan sg = segs[i];
+    if (sg.j == sg.n - 1) order[whole + atomicAdd(&base[bin(sg)], 1)] = i;
   }
   for (int i = seg0 + (int)threadIdx.x; i < seg_places; i += kPlanThreads)
     segs[i] = SegPlan{-1, 0, 1, 0};
