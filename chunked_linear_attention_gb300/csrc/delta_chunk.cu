@@ -222,12 +222,26 @@ __device__ __forceinline__ void store_state(float* tile, int q4, int half, int l
 }
 
 // 64 columns of one row of a user's state (rows of dk numbers, dk a multiple of 8),
-// 32 bytes at a time; columns from dk on are zero.
+// 32 bytes at a time (16 where the tensor begins in the middle of 32); columns from
+// dk on are zero.
+__device__ __forceinline__ bool at_32(const void* p) {
+  return (reinterpret_cast<uintptr_t>(p) & 31) == 0;
+}
 __device__ __forceinline__ void load_row(const float* from, int cols, F2 (&S)[32]) {
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (8 * c < cols) ldg256(from + 8 * c, w);
+    if (8 * c < cols) {
+      if (at_32(from)) {
+        ldg256(from + 8 * c, w);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint4 x = reinterpret_cast<const uint4*>(from)[2 * c + e];
+          w[4 * e] = x.x; w[4 * e + 1] = x.y; w[4 * e + 2] = x.z; w[4 * e + 3] = x.w;
+        }
+      }
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       S[4 * c + e] = pack2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
@@ -244,7 +258,16 @@ __device__ __forceinline__ void store_row(float* to, int cols, const F2 (&S)[32]
       w[2 * e] = __float_as_uint(a);
       w[2 * e + 1] = __float_as_uint(b);
     }
-    if (8 * c < cols) stg256(to + 8 * c, w);
+    if (8 * c < cols) {
+      if (at_32(to)) {
+        stg256(to + 8 * c, w);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          reinterpret_cast<uint4*>(to)[2 * c + e] =
+              make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+      }
+    }
   }
 }
 

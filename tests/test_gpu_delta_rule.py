@@ -262,6 +262,22 @@ def test_segments(size):
     check(cla, got, ref, torch.bfloat16)
 
 
+@pytest.mark.parametrize("dk,dv", [(128, 128), (72, 40)])
+def test_states_that_begin_in_the_middle_of_32_bytes(dk, dv):
+    """Initial and final states 16 bytes behind an allocation's start."""
+    cla = lib()
+    t = inputs(46, 1, 1, 2, 200, dk, dv, torch.bfloat16)
+    S0 = torch.randn(1, 2, dv, dk, generator=torch.Generator().manual_seed(47)) * 0.3
+    n = S0.numel()
+    room = torch.full((2, n + 8), 5.0, device=DEV)
+    first, last = (r[4:4 + n].view(1, 2, dv, dk) for r in room)
+    first.copy_(S0)
+    assert first.data_ptr() % 32 == 16
+    got = run(cla, t, first, S_final=last)
+    check(cla, got, oracle(t, S0), torch.bfloat16)
+    assert (room[:, :4] == 5.0).all() and (room[:, 4 + n:] == 5.0).all()
+
+
 def test_many_packed_sequences():
     """More sequences than the plan's block has threads, one of them long."""
     cla = lib()
