@@ -80,7 +80,7 @@ struct ScanParams {
   const uint8_t* rec;
   const RecScal* scal;
   const float* S0;
-  const float* Sseg;       // [segment][Hv][tile] start states of the segments behind the first
+  const float* Sseg;       // [segment][Hv][tile] start states of the segments
   float* S_final;
   float* L;                // [segment][Hv][tile] (the carry pass)
   uint8_t* P;              // [segment][Hv]: 128 x 128 pairs, as the join's operand tiles
@@ -151,7 +151,9 @@ __device__ __forceinline__ Item get_item(const ScanParams& p, int i) {
   it.to = nullptr;
   const long long one = (long long)p.dv * p.dk;
   const long long sqh = (long long)sg.seq * p.Hv + it.h;
-  if (sg.j > 0)
+  // a sequence of several segments has its S0 from the join too: S_final may be S0,
+  // and the last segment's CTA may be done before the first one's has begun
+  if (sg.n > 1 && (sg.j > 0 || p.S0))
     it.from_tile =
         p.Sseg + (((long long)place * p.Hv + it.h) * p.tiles + it.tile) * kStateFloats;
   else if (p.S0) it.from = p.S0 + sqh * one;
@@ -1311,7 +1313,7 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
       if (lane == 0) mbar_arrive(&B->s_ready);
       // beside the product: its 128 KB through the load-store units take as long
       load_state(p.L + place(j), q4, half, lane, L);
-      if (ok && j > 0) store_state(p.Sseg + place(j), q4, half, lane, S);
+      if (ok && (j > 0 || p.S0)) store_state(p.Sseg + place(j), q4, half, lane, S);
       wait(&B->d_full, j & 1);
       tc_fence_after();
 #pragma unroll
@@ -1379,10 +1381,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   for (int r = 0; r < R / 2; ++r) {
     const int row = row0 + r0 + r, grow = 128 * tile + row;
     at[r] = (int)state_at(row >> 5, col >> 6, (col & 63) >> 2, row & 31) * 4 + (col & 3);
-    sh.S[r0 + r][col] =
-        p.S0 && grow < p.dv && col < p.dk
-            ? p.S0[(((long long)seq * p.Hv + h) * p.dv + grow) * p.dk + col]
-            : 0.f;
+    const float s = p.S0 && grow < p.dv && col < p.dk
+                        ? p.S0[(((long long)seq * p.Hv + h) * p.dv + grow) * p.dk + col]
+                        : 0.f;
+    sh.S[r0 + r][col] = s;
+    if (p.S0)
+      p.Sseg[(((long long)seg0 * p.Hv + h) * p.tiles + tile) * kStateFloats + at[r]] = s;
   }
   __syncthreads();
   const int half = lane >> 4;   // of P's column blocks; 4 columns from 4 (lane & 15) in it

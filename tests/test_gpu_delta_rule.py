@@ -260,6 +260,14 @@ def test_segments(size):
     kinds = {e["name"] for e in cla.profile_stop()}
     assert {"delta.prep", "delta.carry", "delta.join", "delta.chunk"} <= kinds
     check(cla, got, ref, torch.bfloat16)
+    # the states in place, over a call that keeps the card busy on another stream
+    S, busy = S0.to(DEV), torch.cuda.Stream()
+    dev = [x.to(DEV) for x in t]
+    torch.cuda.synchronize()
+    other = cla.delta_rule_chunked_forward(*dev, stream=busy)
+    o, S = cla.delta_rule_chunked_forward(*dev, S0=S, S_final=S)
+    torch.cuda.synchronize()
+    assert torch.equal(o, got[0]) and torch.equal(S, got[1]) and other is not None
 
 
 @pytest.mark.parametrize("dk,dv", [(128, 128), (72, 40)])
