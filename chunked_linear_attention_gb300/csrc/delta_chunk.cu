@@ -1098,18 +1098,19 @@ __global__ void __launch_bounds__(640, 1)
 constexpr int kPlanThreads = 256;
 
 // Sum of x over the block's threads before this one; `total` over all.
-__device__ __forceinline__ int block_before(int x, int* part, int& total) {
+template <typename I>
+__device__ __forceinline__ I block_before(I x, I* part, I& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int s = x;
+  I s = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, s, o);
+    const I y = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += y;
   }
   __syncthreads();
   if (lane == 31) part[warp] = s;
   __syncthreads();
-  int before = 0;
+  I before = 0;
   total = 0;
   for (int w = 0; w < kPlanThreads / 32; ++w) {
     if (w < warp) before += part[w];
@@ -1123,8 +1124,11 @@ __global__ void __launch_bounds__(kPlanThreads)
                       int seg_places, SeqPlan* plan, SegPlan* segs, int* order, int* joins,
                       int* counts, int* status) {
   __shared__ int part[kPlanThreads / 32];
+  __shared__ long long wide_part[kPlanThreads / 32];
   pdl_launch_dependents();
-  int chunk0 = 0, seg0 = 0, join0 = 0;
+  // (sequences that overlap may hold more chunks together than an int can count)
+  long long chunk0 = 0;
+  int seg0 = 0, join0 = 0;
   for (int s0 = 0; s0 < n_seq; s0 += kPlanThreads) {
     const int s = s0 + (int)threadIdx.x;
     int t0 = 0, len = 0, nc = 0, ns = 0;
@@ -1137,12 +1141,13 @@ __global__ void __launch_bounds__(kPlanThreads)
       nc = n_chunks(len);
       ns = max(1, (nc + seg_chunks - 1) / seg_chunks);
     }
-    int tc, ts;
-    const int cb = chunk0 + block_before(nc, part, tc);
+    long long tc;
+    int ts;
+    const long long cb = chunk0 + block_before<long long>(nc, wide_part, tc);
     // bounds that ascend fit always; sequences that overlap (bad bounds between
     // them) may hold more chunks than there are places: those stay empty
     const bool fits = cb + nc <= chunks;
-    if (!fits) {
+    if (!fits && s < n_seq) {
       len = 0;
       ns = 1;
     }
@@ -1152,7 +1157,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (ns > 1) joins[jb] = sb;   // the place of its first segment
     join0 += tj;
     if (s < n_seq) {
-      plan[s] = SeqPlan{t0, len, fits ? cb : 0, 0};
+      plan[s] = SeqPlan{t0, len, fits ? (int)cb : 0, 0};
       for (int j = 0; j < ns; ++j) {
         segs[sb + j] = SegPlan{s, j, ns, 0};
         if (j + 1 < ns) order[sb - s + j] = sb + j;   // s last ones are before it

@@ -37,7 +37,9 @@ struct SegPlan {
   int seq, j, n, pad;
 };
 
-__host__ __device__ __forceinline__ int n_chunks(int len) { return (len + kC - 1) / kC; }
+__host__ __device__ __forceinline__ int n_chunks(int len) {
+  return len / kC + (len % kC != 0);   // len + 63 may pass 31 bits
+}
 
 __device__ __forceinline__ SeqPlan seq_plan(const SeqPlan* plan, int seq, int N) {
   if (plan) return plan[seq];

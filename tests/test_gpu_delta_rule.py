@@ -186,6 +186,24 @@ def test_bad_bounds_are_reported():
                 assert rel_l2(f64(S[s:s + 1]), ref[1]) <= STATE_BF16
 
 
+def test_overlapping_bounds_stay_inside_the_tensors():
+    """Bounds that go back and forth describe more chunks than the token axis
+    holds: the descending ones are empty, the call reports and ends, and
+    nothing around the outputs and states is touched."""
+    cla = lib()
+    N, n = 1000, 10
+    t = inputs(48, 1, 1, 1, N, 128, 128, torch.bfloat16)
+    S0 = torch.randn(n, 1, 128, 128, generator=torch.Generator().manual_seed(49))
+    room = torch.full((1, 1, N + 2, 128), 3.0, dtype=torch.bfloat16, device=DEV)
+    states = torch.full((n + 2, 1, 128, 128), 4.0, device=DEV)
+    run(cla, t, S0, [0, N] * 5 + [0], out=room[:, :, 1:-1], S_final=states[1:-1])
+    assert cla.device_status() == TTT_ERR_ARG
+    assert (room[:, :, 0] == 3.0).all() and (room[:, :, -1] == 3.0).all()
+    assert (states[0] == 4.0).all() and (states[-1] == 4.0).all()
+    for s in range(1, n, 2):
+        assert torch.equal(states[1 + s].cpu(), S0[s])
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 def test_layouts(dtype):
     """Strided views: slices of one projection, a wider head dimension, odd
