@@ -50,7 +50,7 @@ struct Bars {
   uint64_t t_full[2], t_free[2], p_full[2], p_free[2];
   uint64_t ks_full, x_full, ds_full, x_ready;
   uint64_t y_ready[2], xs_ready[2], s_ready[4];
-  uint64_t o_full, o_free;
+  uint64_t o_full, o_free, done;
   uint32_t tmem;
 };
 
@@ -185,6 +185,15 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&w)[4])
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// After a wait that ran out: the MMAs that this warp has issued are waited for
+// before their TMEM is given back.
+__device__ __forceinline__ void drain_mmas(uint64_t* bar, bool el, int* status,
+                                           unsigned long long lim) {
+  if (el) umma_commit(bar);
+  __syncwarp();
+  mbar_wait_w(bar, 0, status, lim);
 }
 
 template <int R>
@@ -373,6 +382,7 @@ __global__ void __launch_bounds__(512, 1)
     for (int b = 0; b < 4; ++b) mbar_init(&B->s_ready[b], 8);
     mbar_init(&B->o_full, 1);
     mbar_init(&B->o_free, 4);
+    mbar_init(&B->done, 1);
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(&B->tmem, 512);
@@ -414,8 +424,7 @@ __global__ void __launch_bounds__(512, 1)
           }
           __syncwarp();
           // T's two tiles are used up long before the chunk's outputs: a record's
-          // halves come and go on their own (together, the next T came too late and
-          // a step took 900 cycles longer).  The factors' four places need no
+          // halves come and go on their own.  The factors' four places need no
           // barrier: at T(n) the outputs of chunk n - 4 have been read.
           const long long x = (long long)(it.chunk0 + c) * p.Hv + it.h;
           wait(&B->t_free[r], ((n >> 1) & 1) ^ 1);
@@ -567,6 +576,7 @@ __global__ void __launch_bounds__(512, 1)
         wait(&B->t_free[(n - 1) & 1], ((n - 1) >> 1) & 1);
         wait(&B->p_free[(n - 1) & 1], ((n - 1) >> 1) & 1);
       }
+      if (!together(ok)) drain_mmas(&B->done, el, p.status, p.wait_ns);
     } else if (warp == 2) {
       int n = 0;
       for (int i = blockIdx.x; i < items; i += gridDim.x) {
@@ -783,6 +793,7 @@ constexpr uint32_t kUnitCols = 256, kUA = 128, kUX = 192;
 struct CarryBars {
   uint64_t full[kCarryStages], ready[kCarryStages], empty[kCarryStages];
   uint64_t ks_full[2], y_ready[2], x_full[2], xs_ready[2], ds_full[2], s_ready[2];
+  uint64_t done;
   uint32_t tmem;
 };
 constexpr int kCarrySmem = kCarryStages * (kCarryBytes + (int)sizeof(RecScal)) +
@@ -831,6 +842,7 @@ __global__ void __launch_bounds__(640, 1)
       mbar_init(&B->ds_full[u], 1);
       mbar_init(&B->s_ready[u], 8);
     }
+    mbar_init(&B->done, 1);
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(&B->tmem, 512);
@@ -969,6 +981,7 @@ __global__ void __launch_bounds__(640, 1)
       ok = together(ok);
       if (n > 0)   // every arrival on this CTA's barriers has landed before it ends
         wait(&B->empty[(n - 1) % kCarryStages], ((n - 1) / kCarryStages) & 1);
+      if (!together(ok)) drain_mmas(&B->done, el, p.status, p.wait_ns);
     } else if (warp == 2) {
       int n = 0;
       for (int i = blockIdx.x; i < items; i += gridDim.x) {
@@ -1395,12 +1408,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   }
   __syncthreads();
   const int half = lane >> 4;   // of P's column blocks; 4 columns from 4 (lane & 15) in it
+  int waited = 0;
   for (int j = 0; j + 1 < n; ++j) {
     const long long sgh = (long long)(seg0 + j) * p.Hv + h;
     const float* L = p.L + (sgh * p.tiles + tile) * kStateFloats;
     float l[R / 2];
 #pragma unroll
     for (int r = 0; r < R / 2; ++r) l[r] = L[at[r]];
+    if (ok) waited = j;
     wait_w(ok, &sh.full[j & 1], (j >> 1) & 1, p.status, p.wait_ns);
     F2 acc[R][2];
 #pragma unroll
@@ -1436,7 +1451,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       *reinterpret_cast<ulonglong2*>(&sh.part[warp][r][4 * lane]) =
           make_ulonglong2(acc[r][0], acc[r][1]);
     __syncthreads();
-    if (tid == 0 && j + 3 < n) {   // everyone is done with P_j
+    if (tid == 0 && j + 3 < n && ok) {   // everyone is done with P_j
       fence_proxy_async_smem();
       load(j + 2);
     }
@@ -1451,6 +1466,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     }
     __syncthreads();
   }
+  if (tid == 0 && !ok)   // copies still on their way into this CTA's shared memory
+    for (int j = waited; j < waited + 2 && j + 1 < n; ++j)
+      mbar_wait(&sh.full[j & 1], (j >> 1) & 1, p.status, p.wait_ns);
 }
 
 template <int R>

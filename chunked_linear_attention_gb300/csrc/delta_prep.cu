@@ -421,9 +421,11 @@ __global__ void __launch_bounds__(kPThreads, 6)
     __syncthreads();
   }
   if (tid == 0) bulk_wait_all();
-  if (!ok) {   // the loads may still be on their way into this CTA's shared memory
+  if (!ok) {   // the loads and the products may still be on their way
     ok = true;
     wait_w(ok, &sh.full, 0, p.status, p.wait_ns);
+    ok = true;
+    wait_w(ok, &sh.done, 0, p.status, p.wait_ns);
   }
   tc_fence_before();
   __syncthreads();
