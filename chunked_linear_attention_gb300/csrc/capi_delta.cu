@@ -1,7 +1,9 @@
 // The extern "C" boundary of ttt_delta.h: argument validation on the host,
 // before anything is enqueued, and dispatch.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <utility>
 
 #include "capi_util.h"
 #include "delta_rule.h"
@@ -31,14 +33,27 @@ delta_rule_layout dense_layout(long long Hk, long long Hv, long long N, long lon
   return L;
 }
 
-// Strides an output may have: no two elements in one place along an axis.
-bool layout_ok(const delta_rule_layout& L, int B, int Hv, int N) {
+// Strides a call may have: none negative, and no two rows of the output on one
+// another (from the closest axis to the farthest, each begins behind the one before).
+bool layout_ok(const delta_rule_layout& L, int B, int Hv, int N, int dv) {
   const delta_rule_stride* s[] = {&L.q, &L.k, &L.v, &L.g, &L.beta, &L.out};
   for (const delta_rule_stride* x : s)
     if (x->batch < 0 || x->head < 0 || x->token < 0) return false;
-  if ((B > 1 && L.out.batch == 0) || (Hv > 1 && L.out.head == 0) || (N > 1 && L.out.token == 0))
-    return false;
+  std::pair<long long, int> ax[3] = {{L.out.batch, B}, {L.out.head, Hv}, {L.out.token, N}};
+  std::sort(ax, ax + 3);
+  long long end = dv;
+  for (const auto& a : ax) {
+    if (a.second == 1) continue;
+    if (a.first < end || a.first > (1LL << 61) / a.second) return false;
+    end += a.first * (a.second - 1);
+  }
   return true;
+}
+
+// A tensor written over another one row by row: the same rows, or another tensor.
+bool rows_match(const void* to, long long sto, const void* from, long long sfrom, bool same_type,
+                long long rows) {
+  return to != from || (same_type && (rows == 1 || sto == sfrom));
 }
 
 }  // namespace
@@ -66,7 +81,8 @@ int delta_rule_chunked_forward(const void* q, const void* k, const void* v, cons
   if (seq_starts && B != 1) return TTT_ERR_SHAPE;
   if (!std::isfinite(scale)) return TTT_ERR_ARG;
   const delta_rule_layout L = layout ? *layout : dense_layout(Hk, Hv, N, d_k, d_v);
-  if (!layout_ok(L, B, Hv, N)) return TTT_ERR_ARG;
+  if (!layout_ok(L, B, Hv, N, d_v)) return TTT_ERR_ARG;
+  if (out == q || out == k || out == v) return TTT_ERR_ARG;
   const unsigned es = io_dtype == TTT_BF16 ? 2 : 4;
   if (!capi_aligned(q, es) || !capi_aligned(k, es) || !capi_aligned(v, es) ||
       !capi_aligned(out, es) || !capi_aligned(g, 4) || !capi_aligned(beta, 4) ||
@@ -105,7 +121,8 @@ int delta_rule_step(const void* q, const void* k, const void* v, const float* g,
   if (n_slots <= 0 || (!slots && n_slots < B)) return TTT_ERR_SHAPE;
   if (!std::isfinite(scale)) return TTT_ERR_ARG;
   const delta_rule_layout L = layout ? *layout : dense_layout(Hk, Hv, 1, d_k, d_v);
-  if (!layout_ok(L, B, Hv, 1)) return TTT_ERR_ARG;
+  if (!layout_ok(L, B, Hv, 1, d_v)) return TTT_ERR_ARG;
+  if (out == q || out == k || out == v || out == state) return TTT_ERR_ARG;
   const unsigned es = io_dtype == TTT_BF16 ? 2 : 4;
   if (!capi_aligned(q, es) || !capi_aligned(k, es) || !capi_aligned(v, es) ||
       !capi_aligned(out, es) || !capi_aligned(g, 4) || !capi_aligned(beta, 4) ||
@@ -146,6 +163,12 @@ int block_norm_forward(const void* y, const float* w, const void* gate, const vo
   // rows of a tensor may not overlap (inputs may repeat one row: stride 0)
   if (a.st.y < 0 || a.st.gate < 0 || a.st.residual < 0 || (rows > 1 && a.st.out < D) ||
       (h && rows > 1 && a.st.h < D))
+    return TTT_ERR_ARG;
+  const bool one_type = io_dtype == stream_dtype;
+  if (!rows_match(out, a.st.out, y, a.st.y, one_type, rows) ||
+      !rows_match(out, a.st.out, residual, a.st.residual, true, rows) ||
+      !rows_match(out, a.st.out, gate, a.st.gate, one_type, rows) || out == h ||
+      (h && (h == y || h == residual || h == gate)))
     return TTT_ERR_ARG;
   const unsigned es = io_dtype == TTT_BF16 ? 2 : 4, ss = stream_dtype == TTT_BF16 ? 2 : 4;
   if (!capi_aligned(y, es) || !capi_aligned(gate, es) || !capi_aligned(h, es) ||

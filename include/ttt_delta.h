@@ -65,7 +65,8 @@ size_t delta_rule_workspace_size(int B, int Hk, int Hv, int N, int d_k, int d_v,
  *               (nothing outside the tensors is touched).
  *   scale       factor of the outputs (d_k^-1/2 is usual).
  *   layout      HOST pointer or NULL.
- *   out         [B, Hv, N, d_v] in io_dtype.  May not overlap an input.
+ *   out         [B, Hv, N, d_v] in io_dtype.  May not overlap an input, nor
+ *               its rows one another.
  *   S_final     fp32 [n_seq, Hv, d_v, d_k], the states after each sequence's
  *               last token (S0, or zeros, for an empty one), or NULL.  May be
  *               S0 itself.
@@ -76,8 +77,8 @@ size_t delta_rule_workspace_size(int B, int Hk, int Hv, int N, int d_k, int d_v,
  * 16-byte aligned with strides that are multiples of 8 elements (and not 0)
  * runs chunks of 64 tokens on the tensor cores, every intermediate held as a
  * pair of bf16 numbers (16 bits of significand) with fp32 sums and state; there
- * a NaN or infinity in a token's v may also reach the outputs of the up to 63
- * tokens before it in its chunk.  All other calls, and ones of a few tokens,
+ * a NaN or infinity in a token's k, v, g or beta may also reach the outputs of
+ * the up to 63 tokens before it in its chunk.  All other calls, and ones of a few tokens,
  * run token by token in fp32.
  * Decays below exp(-104) count as exp(-104) (zero in fp32).
  * Supported: d_k <= 512, d_v <= 1024, n_seq * Hv at most 2^20, and
@@ -102,6 +103,7 @@ int delta_rule_chunked_forward(const void* q, const void* k, const void* v, cons
  *               earlier row of the call already uses, is treated as idle and
  *               sets TTT_ERR_ARG in the device status word.
  *   layout      HOST pointer or NULL; the token strides are not used.
+ *   out         overlaps no other tensor.
  *
  * Computed in fp32 for both I/O types.  Supported: d_k <= 512, d_v <= 1024,
  * B * Hv <= 2^20.  state must be 16-byte aligned. */
@@ -138,9 +140,11 @@ typedef struct {
  *   residual    [rows, D] in stream_dtype, or NULL (0).
  *   scale       fp32 [D] residual scale, or NULL (1).
  *   out         [rows, D] in stream_dtype; may be `residual`, and may be y
- *               where the two types are the same.
+ *               or gate where the two types are the same (with the same row
+ *               stride).
  *   w_next      fp32 [D] weight of the norm before the next block, or NULL.
- *   h           [rows, D] in io_dtype; given exactly when w_next is.
+ *   h           [rows, D] in io_dtype; given exactly when w_next is.  Overlaps
+ *               no other tensor.
  *
  * Computed in fp32.  Any D up to 16384; rows from 1.  Tensors whose pointers
  * are 16-byte aligned, with D, group and the row strides multiples of 8, are

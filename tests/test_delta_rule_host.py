@@ -1,5 +1,6 @@
 """Host-side checks of the delta-rule and norm entry points (no GPU): bad
 arguments are refused with the documented codes before the device is touched."""
+import itertools
 import struct
 
 import pytest
@@ -13,9 +14,10 @@ __all__ = ["cla"]
 
 
 def rule(cla, B=1, Hk=1, Hv=2, N=64, dk=64, dv=64, n_seq=None, io=1, scale=1.0, packed=False,
-         lay=None, nulls=(), ws=None, off=(), S0=True):
+         lay=None, nulls=(), ws=None, off=(), S0=True, out=7):
     n_seq = B if n_seq is None else n_seq
     p = [fake(0x100000 * (i + 1) + (2 if i in off else 0)) for i in range(10)]
+    p[7] = p[out]
     for i in nulls:
         p[i] = None
     q, k, v, g, b, s0, st, out, sf, wsp = p
@@ -55,6 +57,10 @@ def test_rule_refusals(cla):
     assert rule(cla, nulls=(9,)) == TTT_ERR_WORKSPACE
     assert rule(cla, lay=layout(cla, _2=-64)) == TTT_ERR_ARG
     assert rule(cla, lay=layout(cla, _17=0)) == TTT_ERR_ARG   # out rows on one another
+    assert rule(cla, lay=layout(cla, _17=63)) == TTT_ERR_ARG
+    assert rule(cla, lay=layout(cla, _16=63 * 64)) == TTT_ERR_ARG
+    for i in (0, 1, 2):
+        assert rule(cla, out=i) == TTT_ERR_ARG
 
 
 def test_rule_workspace_size(cla):
@@ -88,8 +94,10 @@ def test_step_refusals(cla):
 
 
 def norm(cla, rows=4, D=64, group=64, io=1, st=1, act=0, eps=1e-6, gate=False, nxt=False, h=None,
-         strides=None, nulls=(), off=()):
+         strides=None, nulls=(), off=(), over=None):
     p = [fake(0x100000 * (i + 1) + (1 if i in off else 0)) for i in range(8)]
+    if over:
+        p[over[0]] = p[over[1]]
     for i in nulls:
         p[i] = None
     y, w, z, x, a, wn, out, hh = p
@@ -114,6 +122,25 @@ def test_norm_refusals(cla):
     assert norm(cla, off=(0,)) == TTT_ERR_ALIGN
     assert norm(cla, strides=struct.pack("5q", 64, 0, 64, 32, 0)) == TTT_ERR_ARG     # rows of out overlap
     assert norm(cla, strides=struct.pack("5q", -64, 0, 64, 64, 0)) == TTT_ERR_ARG
+    # out over another tensor's rows: only over the same ones, of the same type
+    assert norm(cla, over=(6, 3), strides=struct.pack("5q", 64, 0, 0, 64, 0)) == TTT_ERR_ARG
+    assert norm(cla, over=(6, 0), strides=struct.pack("5q", 128, 0, 64, 64, 0)) == TTT_ERR_ARG
+    assert norm(cla, over=(6, 0), st=0) == TTT_ERR_ARG
+    for i in (0, 2, 3, 6):
+        assert norm(cla, gate=True, act=1, nxt=True, over=(7, i)) == TTT_ERR_ARG
+
+
+def test_layouts_of_the_outputs(cla):
+    """Every order of the axes passes the checks (and gets as far as the
+    workspace's, which is the last before the device)."""
+    for b, h, n in itertools.permutations(range(3)):
+        size = (3, 2, 64)
+        order = sorted(zip((b, h, n), range(3)))
+        st, at = [0, 0, 0], 64
+        for _, ax in order:
+            st[ax], at = at, at * size[ax]
+        lay = struct.pack("18q", *[64 * 64 * 2, 64 * 64, 64] * 3, *[128, 64, 1] * 2, *st)
+        assert rule(cla, B=3, lay=lay, ws=8) == TTT_ERR_WORKSPACE
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-device path")
