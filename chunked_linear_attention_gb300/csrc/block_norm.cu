@@ -12,9 +12,12 @@
 // that divides the group's pieces, at most 32), and the group's few remaining
 // partial sums through shared memory, always in the same order.
 //
-// One row per CTA, with the weights read anew for each, took 197 us for 65536
-// rows of 1536 with four gated groups (3.1 TB/s): its instructions, and not HBM,
-// were the bound.
+// Measured: 65536 rows of 1536 with four gated groups, bf16, 104 us (5.8 TB/s, 86%
+// of a measured copy; one row per CTA, with the weights read anew for each, took
+// 197: its instructions, and not HBM, were the bound); 20011 rows of 1536 with gate,
+// fp32 residual and both norms 69 us (6.2 TB/s); a single row 4 us.  Longer rows
+// reach 3.6 to 4.9 TB/s (fewer CTAs per SM to run past each other's barriers), ones
+// of unaligned length 1.0 to 1.4 (an element per access, and issue is the bound).
 #include "common.cuh"
 #include "delta_rule.h"
 #include "prof.h"
@@ -23,10 +26,19 @@ namespace ttt {
 
 namespace {
 
-// Threads of a CTA: 256 where a thread has one piece (three CTAs per SM and their
-// loads in flight), else up to 512.
-constexpr int max_threads(int vpt) { return vpt == 1 ? 256 : 512; }
-constexpr int min_ctas(int vpt) { return vpt == 1 ? 3 : 1; }
+// Threads of a CTA, at most: 256 for rows of up to 2048 elements, a piece per thread
+// (three CTAs per SM and their loads in flight); 768 for longer ones, 512 with two
+// pieces or (unaligned rows of up to 2048) four elements each; 1024 where a thread
+// cannot hold the weights and the next row.
+template <int VEC, int VPT, int PARTS, bool KEEP>
+constexpr int kMaxThreads = !KEEP ? 1024 : VEC == 1 || VPT > 1 ? 512 : PARTS >= 0 ? 256 : 768;
+template <int PARTS>
+constexpr int kMinCtas = PARTS >= 0 ? 3 : 1;
+
+// Partial sums of a group up to which every thread adds them up for itself; of more
+// a warp makes one first (21831 rows of 1537, one group: 337 us; with the 1537 added up
+// by every thread 6.1 ms).
+constexpr int kFew = 16;
 
 struct NormParams {
   const void* y;
@@ -139,8 +151,8 @@ __device__ __forceinline__ float sigmoid_fast(float x) {
 
 // PARTS: which of gate (4), residual (2) and next norm (1) are there; -1: the
 // call says (wide or unaligned rows, which need no variant for each).
-template <typename T, typename TS, int VEC, int VPT, int PARTS>
-__global__ void __launch_bounds__(max_threads(VPT), min_ctas(VPT))
+template <typename T, typename TS, int VEC, int VPT, int PARTS, bool KEEP>
+__global__ void __launch_bounds__(kMaxThreads<VEC, VPT, PARTS, KEEP>, kMinCtas<PARTS>)
     block_norm_kernel(const __grid_constant__ NormParams p) {
   const bool GATE = PARTS < 0 ? p.gate != nullptr : (PARTS & 4) != 0;
   const bool RES = PARTS < 0 ? p.residual != nullptr : (PARTS & 2) != 0;
@@ -152,59 +164,110 @@ __global__ void __launch_bounds__(max_threads(VPT), min_ctas(VPT))
   float* part = smem + ty * 2 * (np + nw);
   float* rpart = part + 2 * np;
   const int per = p.gpieces / p.P;   // partials of a group
+  const bool many = PARTS < 0 && per > kFew;
   const float inv_g = 1.f / (float)p.group, inv_d = 1.f / (float)p.D;
-  int col[VPT], first[VPT], slot[VPT];   // slot: of the group partial this thread writes, or -1
-  float w[VPT][VEC], wn[VPT][VEC];   // w: times the residual scale
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int piece = i * p.nt + tid, grp = piece / p.gpieces;
-    col[i] = piece * VEC;
-    first[i] = grp * per;
-    slot[i] = piece < p.pieces && piece % p.P == 0 ? piece / p.P : -1;
-    const bool in = col[i] < p.D;
+  // Piece i of this thread: its first column, that in its group, its group's first
+  // partial sum, and the partial sum that it writes itself (or -1).
+  struct Piece {
+    int col, wcol, first, slot;
+  };
+  int me = tid;
+  auto place = [&](int i) {
+    const int piece = i * p.nt + me, grp = piece / p.gpieces;
+    Piece c;
+    c.col = piece * VEC;
+    c.wcol = c.col - grp * p.group;
+    c.first = grp * per;
+    c.slot = piece < p.pieces && piece % p.P == 0 ? piece / p.P : -1;
+    return c;
+  };
+  auto weights = [&](const Piece& c, float (&x)[VEC]) {
+    const bool in = c.col < p.D;
     float a[VEC];
-    load_w<VEC>(p.w + (col[i] - grp * p.group), in && p.w, w[i]);
-    load_w<VEC>(p.scale + col[i], in && p.scale, a);
+    load_w<VEC>(p.w + c.wcol, in && p.w, x);
+    load_w<VEC>(p.scale + c.col, in && p.scale, a);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) w[i][j] *= a[j];
-    if (NEXT) load_w<VEC>(p.w_next + col[i], in, wn[i]);
+    for (int j = 0; j < VEC; ++j) x[j] *= a[j];
+  };
+  // Weights are read once, and the next row ahead, where the registers hold both;
+  // else the weights come from the caches row by row, gate and residual G pieces at
+  // a time when they are needed, and the CTA's many threads hide the loads (all of
+  // it held, 700 bytes a thread were spilled).
+  constexpr int G = KEEP ? VPT : VEC == 1 ? 4 : 1;
+  static_assert(VPT % G == 0, "whole groups");
+  float w[KEEP ? VPT : 1][VEC], wn[KEEP ? VPT : 1][VEC];   // w: times the residual scale
+  Piece held[KEEP ? VPT : 1];
+  auto at = [&](int i) { return KEEP ? held[KEEP ? i : 0] : place(i); };
+  auto col = [&](int i) { return KEEP ? held[KEEP ? i : 0].col : (i * p.nt + me) * VEC; };
+  if (KEEP) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      held[KEEP ? i : 0] = place(i);
+      weights(held[KEEP ? i : 0], w[KEEP ? i : 0]);
+      if (NEXT) load_w<VEC>(p.w_next + col(i), col(i) < p.D, wn[KEEP ? i : 0]);
+    }
   }
-  // rows move by whole CTAs: pointers advance, nothing is multiplied per row
+  // rows move by whole CTAs: pointers advance, nothing is multiplied per row (short
+  // of registers: multiplied)
   long long row = (long long)blockIdx.x * ny + ty;
   const long long step = (long long)gridDim.x * ny;
-  const T* py = static_cast<const T*>(p.y) + row * p.st.y;
-  const T* pz = static_cast<const T*>(p.gate) + row * p.st.gate;
-  const TS* px = static_cast<const TS*>(p.residual) + row * p.st.residual;
-  TS* po = static_cast<TS*>(p.out) + row * p.st.out;
-  T* ph = static_cast<T*>(p.h) + row * p.st.h;
+  const T *py, *pz;
+  const TS* px;
+  TS* po;
+  T* ph;
+  auto point = [&]() {
+    py = static_cast<const T*>(p.y) + row * p.st.y;
+    pz = static_cast<const T*>(p.gate) + row * p.st.gate;
+    px = static_cast<const TS*>(p.residual) + row * p.st.residual;
+    po = static_cast<TS*>(p.out) + row * p.st.out;
+    ph = static_cast<T*>(p.h) + row * p.st.h;
+  };
+  point();
   const long long sy = step * p.st.y, sz = step * p.st.gate, sx = step * p.st.residual;
   const long long so = step * p.st.out, shh = step * p.st.h;
-  Raw<T, VEC> ry[VPT], rz[VPT];
-  Raw<TS, VEC> rx[VPT];
-  auto load = [&]() {
+  Raw<T, VEC> ry[VPT], rz[G];
+  Raw<TS, VEC> rx[G];
+  auto load_y = [&]() {
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
-      if (col[i] < p.D) {
-        ry[i].load(py + col[i]);
-        if (GATE) rz[i].load(pz + col[i]);
-        if (RES) rx[i].load(px + col[i]);
+      if (col(i) < p.D) ry[i].load(py + col(i));
+  };
+  auto load_zx = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+      if (col(i0 + i) < p.D) {
+        if (GATE) rz[i].load(pz + col(i0 + i));
+        if (RES) rx[i].load(px + col(i0 + i));
       }
+  };
+  auto load = [&]() {
+    load_y();
+    load_zx(0);
     py += sy;
     if (GATE) pz += sz;
     if (RES) px += sx;
   };
-  if (row < p.rows) load();
+  if (KEEP && row < p.rows) load();
   int buf = 0;
   for (long long r0 = (long long)blockIdx.x * ny; r0 < p.rows; r0 += step, row += step, buf ^= 1) {
     const bool live = row < p.rows;   // the CTA's rows meet at its barriers
-    float m[VPT][VEC], z[VPT][VEC], x[VPT][VEC];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      ry[i].get(m[i]);
-      if (GATE) rz[i].get(z[i]);
-      if (RES) rx[i].get(x[i]);
+    float m[VPT][VEC], z[G][VEC], x[G][VEC];
+    if (!KEEP) {
+      asm volatile("" : "+r"(me));   // places and pointers anew in each row: no room to hold them
+      point();
+      if (live) load_y();
     }
-    if (row + step < p.rows) load();
+    auto get_zx = [&]() {
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        if (GATE) rz[i].get(z[i]);
+        if (RES) rx[i].get(x[i]);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) ry[i].get(m[i]);
+    if (KEEP) get_zx();
+    if (KEEP && row + step < p.rows) load();
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       float ss = 0.f;
@@ -213,38 +276,69 @@ __global__ void __launch_bounds__(max_threads(VPT), min_ctas(VPT))
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
         if (o < p.P) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (slot[i] >= 0) part[buf * np + slot[i]] = ss;
+      const int slot = at(i).slot;
+      if (slot >= 0) part[buf * np + slot] = ss;
     }
     __syncthreads();
+    if (many) {   // a warp per group; its sum takes the place of its first partial
+      for (int g = warp; g * per < np; g += nw) {
+        float* q = part + buf * np + g * per;
+        float s4[4] = {0.f, 0.f, 0.f, 0.f};   // of at most 16384 terms, 128 each
+        for (int j = lane; j < per; j += 128) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j + 32 * e < per) s4[e] += q[j + 32 * e];
+        }
+        float ss = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        __syncwarp();
+        if (lane == 0) q[0] = ss;
+      }
+      __syncthreads();
+    }
     float rr = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      if (!live || col[i] >= p.D) continue;
+      if (!live) continue;
+      if (!KEEP && i % G == 0) {
+        load_zx(i);
+        get_zx();
+      }
+      const Piece c = at(i);
+      if (c.col >= p.D) continue;
       float ss = 0.f;
-      for (int j = 0; j < per; ++j) ss += part[buf * np + first[i] + j];
+      for (int j = 0; j < (many ? 1 : per); ++j) ss += part[buf * np + c.first + j];
       const float inv = rsqrtf(fmaf(ss, inv_g, p.eps));
+      float f[VEC];
+      if (KEEP) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) m[i][j] *= inv * w[i][j];
+        for (int j = 0; j < VEC; ++j) f[j] = w[KEEP ? i : 0][j];
+      } else {
+        weights(c, f);
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) m[i][j] *= inv * f[j];
       if (GATE) {
         if (p.act == BLOCK_GATE_SILU) {
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) m[i][j] *= z[i][j] * sigmoid_fast(z[i][j]);
+          for (int j = 0; j < VEC; ++j) m[i][j] *= z[i % G][j] * sigmoid_fast(z[i % G][j]);
         } else {
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) m[i][j] *= sigmoid_fast(z[i][j]);
+          for (int j = 0; j < VEC; ++j) m[i][j] *= sigmoid_fast(z[i % G][j]);
         }
       }
       if (RES) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) m[i][j] += x[i][j];
+        for (int j = 0; j < VEC; ++j) m[i][j] += x[i % G][j];
       }
       if (NEXT) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) rr = fmaf(m[i][j], m[i][j], rr);
       }
-      store_vec<TS, VEC>(po + col[i], m[i]);
+      store_vec<TS, VEC>(po + c.col, m[i]);
     }
-    po += so;
+    if (KEEP) po += so;
     if (NEXT) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) rr += __shfl_xor_sync(0xffffffffu, rr, o);
@@ -255,19 +349,26 @@ __global__ void __launch_bounds__(max_threads(VPT), min_ctas(VPT))
       const float inv = rsqrtf(fmaf(tot, inv_d, p.eps));
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        if (!live || col[i] >= p.D) continue;
+        if (!live || col(i) >= p.D) continue;
+        float f[VEC];
+        if (KEEP) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) m[i][j] *= inv * wn[i][j];
-        store_vec<T, VEC>(ph + col[i], m[i]);
+          for (int j = 0; j < VEC; ++j) f[j] = wn[KEEP ? i : 0][j];
+        } else {
+          load_w<VEC>(p.w_next + col(i), true, f);
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) m[i][j] *= inv * f[j];
+        store_vec<T, VEC>(ph + col(i), m[i]);
       }
-      ph += shh;
+      if (KEEP) ph += shh;
     }
   }
 }
 
-template <typename T, typename TS, int VEC, int VPT, int PARTS>
+template <typename T, typename TS, int VEC, int VPT, int PARTS, bool KEEP>
 int launch_parts(const BlockNormArgs& a, NormParams p) {
-  auto kern = block_norm_kernel<T, TS, VEC, VPT, PARTS>;
+  auto kern = block_norm_kernel<T, TS, VEC, VPT, PARTS, KEEP>;
   static const int regs = [&] {
     cudaFuncAttributes at;
     return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
@@ -299,14 +400,14 @@ int launch_parts(const BlockNormArgs& a, NormParams p) {
 template <typename T, typename TS>
 int launch_narrow(const BlockNormArgs& a, const NormParams& p) {
   switch ((a.gate ? 4 : 0) | (a.residual ? 2 : 0) | (a.h ? 1 : 0)) {
-    case 0: return launch_parts<T, TS, 8, 1, 0>(a, p);
-    case 1: return launch_parts<T, TS, 8, 1, 1>(a, p);
-    case 2: return launch_parts<T, TS, 8, 1, 2>(a, p);
-    case 3: return launch_parts<T, TS, 8, 1, 3>(a, p);
-    case 4: return launch_parts<T, TS, 8, 1, 4>(a, p);
-    case 5: return launch_parts<T, TS, 8, 1, 5>(a, p);
-    case 6: return launch_parts<T, TS, 8, 1, 6>(a, p);
-    default: return launch_parts<T, TS, 8, 1, 7>(a, p);
+    case 0: return launch_parts<T, TS, 8, 1, 0, true>(a, p);
+    case 1: return launch_parts<T, TS, 8, 1, 1, true>(a, p);
+    case 2: return launch_parts<T, TS, 8, 1, 2, true>(a, p);
+    case 3: return launch_parts<T, TS, 8, 1, 3, true>(a, p);
+    case 4: return launch_parts<T, TS, 8, 1, 4, true>(a, p);
+    case 5: return launch_parts<T, TS, 8, 1, 5, true>(a, p);
+    case 6: return launch_parts<T, TS, 8, 1, 6, true>(a, p);
+    default: return launch_parts<T, TS, 8, 1, 7, true>(a, p);
   }
 }
 
@@ -318,11 +419,20 @@ int norm_t(const BlockNormArgs& a, const NormParams& p) {
                     a.st.y % 8 == 0 && a.st.gate % 8 == 0 && a.st.residual % 8 == 0 &&
                     a.st.out % 8 == 0 && a.st.h % 8 == 0;
   if (wide) {
-    if (a.D <= 8 * 256) return launch_narrow<T, TS>(a, p);
-    return launch_parts<T, TS, 8, 4, -1>(a, p);
+    int pieces = a.group / 8;   // of a group, and of a butterfly's sum: see launch_parts
+    for (int i = 0; i < 5 && pieces % 2 == 0; ++i) pieces /= 2;
+    if (a.D <= 8 * 256 && pieces <= kFew) return launch_narrow<T, TS>(a, p);
+    if (a.D <= 8 * 256) return launch_parts<T, TS, 8, 1, -1, true>(a, p);
+    // two pieces a thread where two CTAs of them fit an SM (rows of 4096 in bf16, two
+    // norms, gate and residual: 77 us for 8192 rows, 97 with one piece; of 6144, one
+    // CTA, 115 against 104), and where little is held ahead
+    if (a.D <= 8 * 512 || (a.D <= 8 * 1024 && sizeof(T) + sizeof(TS) == 4))
+      return launch_parts<T, TS, 8, 2, -1, true>(a, p);
+    if (a.D <= 8 * 768) return launch_parts<T, TS, 8, 1, -1, true>(a, p);
+    return launch_parts<T, TS, 8, 2, -1, false>(a, p);
   }
-  if (a.D <= 4 * 512) return launch_parts<T, TS, 1, 4, -1>(a, p);
-  return launch_parts<T, TS, 1, 32, -1>(a, p);
+  if (a.D <= 4 * 512) return launch_parts<T, TS, 1, 4, -1, true>(a, p);
+  return launch_parts<T, TS, 1, 16, -1, false>(a, p);
 }
 
 }  // namespace

@@ -67,6 +67,19 @@ def test_sizes(rows, D, group, io, st):
         check(got, want(t, group), io, st)
 
 
+@pytest.mark.parametrize("io,st", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)], ids=str)
+@pytest.mark.parametrize("rows,D,group", [
+    (3, 2040, 2040), (400, 1537, 1537), (2, 4095, 4095), (2, 4096, 4096), (700, 4096, 128),
+    (2, 6144, 6144), (300, 8192, 8192), (200, 8200, 1640), (2, 6000, 24), (170, 16384, 16384),
+    (160, 16383, 16383)], ids=str)
+def test_groups_of_many_partial_sums_and_long_rows(rows, D, group, io, st):
+    """Groups whose elements halve few times (many partial sums), and the
+    forms of rows above 2048, with several rows per block."""
+    cla = lib()
+    t = make(6, rows, D, group, io, st, 1, True, True, True)
+    check(cla.block_norm_forward(**on(t), out_dtype=st), want(t, group), io, st)
+
+
 def test_every_choice_of_parts():
     cla = lib()
     for act, residual, scale, nxt in itertools.product((0, 1, 2), *[(False, True)] * 3):
