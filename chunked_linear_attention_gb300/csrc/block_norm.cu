@@ -16,8 +16,8 @@
 // of a measured copy; one row per CTA, with the weights read anew for each, took
 // 197: its instructions, and not HBM, were the bound); 20011 rows of 1536 with gate,
 // fp32 residual and both norms 69 us (6.2 TB/s); a single row 4 us.  Longer rows
-// reach 3.6 to 4.9 TB/s (fewer CTAs per SM to run past each other's barriers), ones
-// of unaligned length 1.0 to 1.4 (an element per access, and issue is the bound).
+// reach 3.6 to 4.8 TB/s (fewer CTAs per SM to run past each other's barriers), ones
+// of unaligned length 1.2 to 1.6 (an element per access, and issue is the bound).
 #include "common.cuh"
 #include "delta_rule.h"
 #include "prof.h"
@@ -32,12 +32,16 @@ namespace {
 // cannot hold the weights and the next row.
 template <int VEC, int VPT, int PARTS, bool KEEP>
 constexpr int kMaxThreads = !KEEP ? 1024 : VEC == 1 || VPT > 1 ? 512 : PARTS >= 0 ? 256 : 768;
-template <int PARTS>
-constexpr int kMinCtas = PARTS >= 0 ? 3 : 1;
+// CTAs per SM to leave registers for: four where at most gate or residual is there
+// besides y, all bf16 (four gated groups of 1536: 103 us, with three 112).
+template <int PARTS, int BYTES>
+constexpr int kMinCtas = PARTS < 0                                             ? 1
+                         : BYTES == 4 && (PARTS == 0 || PARTS == 2 || PARTS == 4) ? 4
+                                                                               : 3;
 
 // Partial sums of a group up to which every thread adds them up for itself; of more
-// a warp makes one first (21831 rows of 1537, one group: 337 us; with the 1537 added up
-// by every thread 6.1 ms).
+// a warp makes one first (21816 rows of 1538 in two groups 366 us; rows of 1537 whose
+// partial sums every thread added up took 6.1 ms).
 constexpr int kFew = 16;
 
 struct NormParams {
@@ -55,6 +59,7 @@ struct NormParams {
   int gpieces;       // group / VEC
   int P;             // lanes of a group's butterfly
   int nt;            // threads per row
+  int np;            // places of the groups' partial sums
   float eps;
   block_norm_strides st;
 };
@@ -152,7 +157,7 @@ __device__ __forceinline__ float sigmoid_fast(float x) {
 // PARTS: which of gate (4), residual (2) and next norm (1) are there; -1: the
 // call says (wide or unaligned rows, which need no variant for each).
 template <typename T, typename TS, int VEC, int VPT, int PARTS, bool KEEP>
-__global__ void __launch_bounds__(kMaxThreads<VEC, VPT, PARTS, KEEP>, kMinCtas<PARTS>)
+__global__ void __launch_bounds__(kMaxThreads<VEC, VPT, PARTS, KEEP>, kMinCtas<PARTS, sizeof(T) + sizeof(TS)>)
     block_norm_kernel(const __grid_constant__ NormParams p) {
   const bool GATE = PARTS < 0 ? p.gate != nullptr : (PARTS & 4) != 0;
   const bool RES = PARTS < 0 ? p.residual != nullptr : (PARTS & 2) != 0;
@@ -160,11 +165,13 @@ __global__ void __launch_bounds__(kMaxThreads<VEC, VPT, PARTS, KEEP>, kMinCtas<P
   // for each row of the CTA: [2][pieces / P] group partials, [2][nt / 32] row partials
   extern __shared__ float smem[];
   const int ty = threadIdx.x / p.nt, tid = threadIdx.x - ty * p.nt, ny = blockDim.x / p.nt;
-  const int warp = tid >> 5, lane = tid & 31, nw = p.nt >> 5, np = p.pieces / p.P;
+  const int warp = tid >> 5, lane = tid & 31, nw = p.nt >> 5, np = p.np;
   float* part = smem + ty * 2 * (np + nw);
   float* rpart = part + 2 * np;
-  const int per = p.gpieces / p.P;   // partials of a group
-  const bool many = PARTS < 0 && per > kFew;
+  // one group: each warp makes a partial sum, whatever the group's length
+  const bool one = PARTS < 0 && p.gpieces == p.pieces;
+  const int per = one ? nw : p.gpieces / p.P;   // partials of a group
+  const bool many = PARTS < 0 && !one && per > kFew;
   const float inv_g = 1.f / (float)p.group, inv_d = 1.f / (float)p.D;
   // Piece i of this thread: its first column, that in its group, its group's first
   // partial sum, and the partial sum that it writes itself (or -1).
@@ -268,20 +275,30 @@ __global__ void __launch_bounds__(kMaxThreads<VEC, VPT, PARTS, KEEP>, kMinCtas<P
     for (int i = 0; i < VPT; ++i) ry[i].get(m[i]);
     if (KEEP) get_zx();
     if (KEEP && row + step < p.rows) load();
+    float all = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       float ss = 0.f;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) ss = fmaf(m[i][j], m[i][j], ss);
+      if (one) {
+        all += col(i) < p.D ? ss : 0.f;
+        continue;
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
         if (o < p.P) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       const int slot = at(i).slot;
       if (slot >= 0) part[buf * np + slot] = ss;
     }
+    if (one) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      if (lane == 0) part[buf * np + warp] = all;
+    }
     __syncthreads();
     if (many) {   // a warp per group; its sum takes the place of its first partial
-      for (int g = warp; g * per < np; g += nw) {
+      for (int g = warp; g * p.gpieces < p.pieces; g += nw) {
         float* q = part + buf * np + g * per;
         float s4[4] = {0.f, 0.f, 0.f, 0.f};   // of at most 16384 terms, 128 each
         for (int j = lane; j < per; j += 128) {
@@ -382,7 +399,8 @@ int launch_parts(const BlockNormArgs& a, NormParams p) {
   // rows per CTA: up to 256 threads; CTAs: what the SMs hold of them at once, so
   // that all run to the end together
   const int ny = p.nt >= 256 ? 1 : 256 / p.nt, threads = p.nt * ny;
-  const int smem = ny * 2 * (p.pieces / p.P + p.nt / 32) * 4;
+  p.np = p.pieces / p.P > p.nt / 32 ? p.pieces / p.P : p.nt / 32;
+  const int smem = ny * 2 * (p.np + p.nt / 32) * 4;
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return TTT_ERR_CUDA;
