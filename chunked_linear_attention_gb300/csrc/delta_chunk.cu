@@ -24,6 +24,14 @@
 // v = 0) are computed for all segments at once, the start states follow by
 // S_{j+1} = S_j P_j + L_j, and all segments run at once.
 //
+// What bounds it: a chunk's four products follow one another (S K^T, X, X^T K, and
+// the state's next pairs), with a conversion by the warps between any two.  A step
+// takes 2.25 us, of which the tensor pipe works 47% (2690 cycles of products, in
+// pairs); one more order of products to fill the gaps (two MMA warps, other
+// hand-overs) was slower.  B 4, H 4, 8192 tokens, d 128: 149 us (prep 34, L and P
+// 55, join 24, outputs 47, their ends overlapping), token by token 1.7 ms; one
+// sequence of 131072 tokens, 4 heads: 434 us (103, 158, 45, 139).
+//
 // Roles (512 threads, one CTA per SM, persistent over (segment, head, d_v tile)):
 //   warp 0      TMA: q, k, v in three stages, the chunk's records in two.
 //   warp 1      all MMAs.
@@ -778,9 +786,9 @@ __global__ void __launch_bounds__(512, 1)
 // The chain without outputs, for two units at once: a unit is 128 rows of L (start
 // state zero) or the rows of P (start state the unit matrix, v = 0).  The units of
 // a (segment, head) share k and T, and while one unit's products run, the other's
-// results are converted: the chain's steps wait on one another, so a single one
-// leaves the tensor cores idle two thirds of the time (4160 cycles a chunk for
-// one, 2 x 128 rows in about the same time for two).
+// results are converted: the chain's steps wait on one another, and a single one
+// leaves the tensor cores idle most of the time (a chunk of two units takes 2.65 us,
+// one of one unit with outputs 2.25).
 //
 // 256 TMEM columns per unit: S as pairs and later X^T K in the same 128 (S itself
 // is in registers, and its pairs are used up by then; both take 16 columns per 16

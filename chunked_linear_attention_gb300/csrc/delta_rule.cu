@@ -44,9 +44,14 @@ __device__ __forceinline__ void seq_range(const int* starts, int s, int N, int* 
 }
 
 // ------------------------------------------------------------ whole sequences
-// One CTA: 16 R rows of one (sequence, head): four warps compute, four more
-// bring the next TT tokens' k, q, v (as fp32), decay, beta and k . q into the
-// other half of the shared memory.
+// One CTA: 16 rows of one (sequence, head): four warps compute, four more bring
+// the next TT tokens' k, q, v (as fp32), decay, beta and k . q into the other half
+// of the shared memory.  Bound by the chain of a token (two dot products, a
+// butterfly, the update), hidden in part by the other CTA of the SM: in fp32 B 4,
+// H 4, 8192 tokens take 1.66 ms at d 128 (0.20 us a token, 16 CTAs' rows of 16
+// fill 128 SMs), 256 tokens of one head 34 us at d 32 and 58 at d 128.  With d_k of
+// 256, two CTAs per SM (128 registers) take 1.0 ms for 2048 tokens and one 1.34; of
+// 512, four rows a thread 1.2 ms for 512 tokens (0.6 us a token) and two 1.5.
 constexpr int kRecWarps = 4;
 
 struct RecParams {
@@ -66,7 +71,8 @@ struct RecParams {
 };
 
 template <typename T, int L, int E, int R, int TT>
-__global__ void __launch_bounds__(256) delta_recurrent_kernel(const __grid_constant__ RecParams p) {
+__global__ void __launch_bounds__(256, R < 4 ? 2 : 1)
+    delta_recurrent_kernel(const __grid_constant__ RecParams p) {
   constexpr int W = L * E;                         // padded d_k
   constexpr int ROWS = kRecWarps * (32 / L) * R;   // rows of this CTA
   constexpr int TOK = 2 * W + ROWS + 4;            // floats per staged token
@@ -276,7 +282,10 @@ struct StepParams {
 constexpr int kStepThreads = 128;
 
 // One CTA: 4 (32 / L) R rows of one (row of the batch, head).  The state is
-// read and written once, each thread's R E elements all in flight together.
+// read and written once, each thread's R E elements all in flight together; the
+// bound is HBM (the states' bytes twice).  Heads of 128 x 128: 256 rows of 32
+// heads 179 us (6.0 TB/s, 90% of a measured copy), 56 rows of 16 heads 24.6 us
+// (4.8 TB/s: beginning and end are a part of it), one row of 4 heads 4 us.
 template <typename T, int L, int E, int R, bool VEC>
 __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(
     const __grid_constant__ StepParams p) {
