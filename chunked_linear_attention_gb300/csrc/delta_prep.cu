@@ -266,68 +266,80 @@ __global__ void __launch_bounds__(kPThreads, 6)
     const uint32_t prow = smem_u32(tile) + 2 * kBlk + row * 128;
 #pragma unroll 1
     for (int J = 3; J >= 0; --J) {
-      float x[16];
-      if (J <= 2 * half + 1) {
-        tmem_ld16_nowait(tmem + lane_off + 16 * J, x);
-        float f = 0.f;
-        if (J < I) {
-          f = mul * ex2(decay);
-          decay += sh.blk[J];
-        }
-        const float4* gl4 = reinterpret_cast<const float4*>(&sh.gl[16 * J]);
-        const float4* el4 = reinterpret_cast<const float4*>(&sh.el[16 * J]);
-        float d[16];
+      if (J > 2 * half + 1) {   // behind the diagonal for all of the warp
+        if (warp < 2) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 w = el4[e];
-          d[4 * e] = f * w.x; d[4 * e + 1] = f * w.y;
-          d[4 * e + 2] = f * w.z; d[4 * e + 3] = f * w.w;
+          for (int b = 0; b < 2; ++b) {
+            const uint32_t o = prow + (((2 * J + b) ^ (row & 7)) << 4);
+            sts128(o, make_uint4(0, 0, 0, 0));
+            sts128(o + kBlk, make_uint4(0, 0, 0, 0));
+          }
         }
-        if (J >= 2 * half) {   // lanes with their diagonal here, or (J > I) nothing
-          const int last = row - 16 * J;   // last column of the row's part
+        continue;
+      }
+      float x[16];
+      F2 y[8];
+      tmem_ld16_nowait(tmem + lane_off + 16 * J, x);
+      float f = 0.f;
+      if (J < I) {
+        f = mul * ex2(decay);
+        decay += sh.blk[J];
+      }
+      const F2 f2 = pack2(f, f);
+      const ulonglong2* el2 = reinterpret_cast<const ulonglong2*>(&sh.el[16 * J]);
+      F2 d[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const ulonglong2 w = el2[e];
+        d[2 * e] = mul2(f2, w.x);
+        d[2 * e + 1] = mul2(f2, w.y);
+      }
+      if (J >= 2 * half) {   // lanes with their diagonal here, or (J > I) nothing
+        const float4* gl4 = reinterpret_cast<const float4*>(&sh.gl[16 * J]);
+        const int last = row - 16 * J;   // last column of the row's part
+        if (J >= I) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float4 w = gl4[e];
-            if (J >= I) {
-              d[4 * e] = mul * ex2(gli - w.x); d[4 * e + 1] = mul * ex2(gli - w.y);
-              d[4 * e + 2] = mul * ex2(gli - w.z); d[4 * e + 3] = mul * ex2(gli - w.w);
-            }
+            d[2 * e] = pack2(mul * ex2(gli - w.x), mul * ex2(gli - w.y));
+            d[2 * e + 1] = pack2(mul * ex2(gli - w.z), mul * ex2(gli - w.w));
           }
-          tmem_wait_bind(x);
-          // a product behind the diagonal may be anything: no 0 * inf
+        }
+        tmem_wait_bind(x);
+        // a product behind the diagonal may be anything, and so may its decay
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = e <= last ? x[e] * d[e] : 0.f;
-        } else {
-          tmem_wait_bind(x);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] *= d[e];
+        for (int e = 0; e < 8; ++e) {
+          float a, b;
+          unpack2(mul2(pack2(x[2 * e], x[2 * e + 1]), d[e]), a, b);
+          y[e] = pack2(2 * e <= last ? a : 0.f, 2 * e + 1 <= last ? b : 0.f);
         }
       } else {
+        tmem_wait_bind(x);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = 0.f;
+        for (int e = 0; e < 8; ++e) y[e] = mul2(pack2(x[2 * e], x[2 * e + 1]), d[e]);
       }
       if (warp < 2) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            split2(pack2(x[8 * b + 2 * e], x[8 * b + 2 * e + 1]), hi[e], lo[e]);
+          for (int e = 0; e < 4; ++e) split2(y[4 * b + e], hi[e], lo[e]);
           const uint32_t o = prow + (((2 * J + b) ^ (row & 7)) << 4);
           sts128(o, make_uint4(hi[0], hi[1], hi[2], hi[3]));
           sts128(o + kBlk, make_uint4(lo[0], lo[1], lo[2], lo[3]));
         }
       } else if (J <= I) {
-        float4* m = reinterpret_cast<float4*>(M + block_at(I, J) + (row & 15) * kRowF);
+        ulonglong2* m = reinterpret_cast<ulonglong2*>(M + block_at(I, J) + (row & 15) * kRowF);
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-          m[b] = make_float4(x[4 * b], x[4 * b + 1], x[4 * b + 2], x[4 * b + 3]);
+        for (int b = 0; b < 4; ++b) m[b] = make_ulonglong2(y[2 * b], y[2 * b + 1]);
       }
     }
-    __syncthreads();
-    {   // T of this warp's diagonal block, column lane & 15 in registers
-      const int col = lane & 15;
-      float* m = M + block_at(warp, warp);
+    // T of the diagonal blocks, by the warps that have just written them (two blocks
+    // each, a column per lane), while the others are at P's pairs
+    if (warp >= 2) {
+      __syncwarp();
+      const int col = lane & 15, blk = 2 * half + (lane >> 4);
+      float* m = M + block_at(blk, blk);
       float x[16];
       x[0] = col == 0 ? 1.f : 0.f;
 #pragma unroll
@@ -346,10 +358,8 @@ __global__ void __launch_bounds__(kPThreads, 6)
         x[i] = v0 + v1;
       }
       __syncwarp();
-      if (lane < 16) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m[i * kRowF + col] = x[i];
-      }
+      for (int i = 0; i < 16; ++i) m[i * kRowF + col] = x[i];
     }
     __syncthreads();
     {   // T_10 and T_32: two warps each, eight columns a warp; W = T_11 A_10 first
@@ -382,17 +392,19 @@ __global__ void __launch_bounds__(kPThreads, 6)
       block_put<2>(o, r, -1.f, lane);
     }
     __syncthreads();
-    {   // T diag(beta) as a pair, over the scratch: half a row per thread
-      const int i = tid >> 1, hf = tid & 1, IB = i >> 4;
-      float x[32];
+    {   // T diag(beta) as a pair, over the scratch: the warp's 16 rows, two blocks of
+        // 16 columns at a time (the first two are all that the upper rows have)
+      const int r = lane & 15, i = 16 * warp + r, hf = lane >> 4;
+      F2 x[2][8];
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const int J = 2 * hf + b;
+        const int J = 2 * b + hf;
+        if (2 * b > warp) break;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (J <= IB) {
-            v = *reinterpret_cast<const float4*>(M + block_at(IB, J) + (i & 15) * kRowF + 4 * e);
+          if (J <= warp) {
+            v = *reinterpret_cast<const float4*>(M + block_at(warp, J) + r * kRowF + 4 * e);
             const float4 be = *reinterpret_cast<const float4*>(&sh.beta[16 * J + 4 * e]);
             const int j = 16 * J + 4 * e;
             v.x = j <= i ? v.x * be.x : 0.f;
@@ -400,20 +412,25 @@ __global__ void __launch_bounds__(kPThreads, 6)
             v.z = j + 2 <= i ? v.z * be.z : 0.f;
             v.w = j + 3 <= i ? v.w * be.w : 0.f;
           }
-          *reinterpret_cast<float4*>(&x[16 * b + 4 * e]) = v;
+          x[b][2 * e] = pack2(v.x, v.y);
+          x[b][2 * e + 1] = pack2(v.z, v.w);
         }
       }
       __syncthreads();
       const uint32_t trow = smem_u32(tile) + i * 128;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t hi[4], lo[4];
+      for (int b = 0; b < 2; ++b) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          split2(pack2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1]), hi[e], lo[e]);
-        const uint32_t o = trow + (((4 * hf + q) ^ (i & 7)) << 4);
-        sts128(o, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        sts128(o + kBlk, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        for (int q = 0; q < 2; ++q) {
+          uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+          if (2 * b <= warp) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split2(x[b][4 * q + e], hi[e], lo[e]);
+          }
+          const uint32_t o = trow + (((4 * b + 2 * hf + q) ^ (i & 7)) << 4);
+          sts128(o, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          sts128(o + kBlk, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        }
       }
     }
     fence_proxy_async_smem();
