@@ -28,9 +28,9 @@
 // the state's next pairs), with a conversion by the warps between any two.  A step
 // takes 2.25 us, of which the tensor pipe works 47% (2690 cycles of products, in
 // pairs); one more order of products to fill the gaps (two MMA warps, other
-// hand-overs) was slower.  B 4, H 4, 8192 tokens, d 128: 149 us (prep 34, L and P
+// hand-overs) was slower.  B 4, H 4, 8192 tokens, d 128: 149 us (prep 32, L and P
 // 55, join 24, outputs 47, their ends overlapping), token by token 1.7 ms; one
-// sequence of 131072 tokens, 4 heads: 434 us (103, 158, 45, 139).
+// sequence of 131072 tokens, 4 heads: 431 us (97, 156, 46, 139).
 //
 // Roles (512 threads, one CTA per SM, persistent over (segment, head, d_v tile)):
 //   warp 0      TMA: q, k, v in three stages, the chunk's records in two.
@@ -221,34 +221,41 @@ __device__ __forceinline__ long long state_at(int q4, int half, int c, int lane)
   return ((q4 * 2 + half) * 16 + c) * 32 + lane;
 }
 
+// (C float4 of a row from column 4 C half on: half a row of 8 C columns)
+template <int C>
 __device__ __forceinline__ void load_state(const float* tile, int q4, int half, int lane,
-                                           F2 (&S)[32]) {
+                                           F2 (&S)[2 * C]) {
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
+  for (int c = 0; c < C; ++c) {
+    const int x = C * half + c;
     const ulonglong2 w =
-        reinterpret_cast<const ulonglong2*>(tile)[state_at(q4, half, c, lane)];
+        reinterpret_cast<const ulonglong2*>(tile)[state_at(q4, x >> 4, x & 15, lane)];
     S[2 * c] = w.x;
     S[2 * c + 1] = w.y;
   }
 }
 
+template <int C>
 __device__ __forceinline__ void store_state(float* tile, int q4, int half, int lane,
-                                            const F2 (&S)[32]) {
+                                            const F2 (&S)[2 * C]) {
 #pragma unroll
-  for (int c = 0; c < 16; ++c)
-    reinterpret_cast<ulonglong2*>(tile)[state_at(q4, half, c, lane)] =
+  for (int c = 0; c < C; ++c) {
+    const int x = C * half + c;
+    reinterpret_cast<ulonglong2*>(tile)[state_at(q4, x >> 4, x & 15, lane)] =
         make_ulonglong2(S[2 * c], S[2 * c + 1]);
+  }
 }
 
-// 64 columns of one row of a user's state (rows of dk numbers, dk a multiple of 8),
+// 4 C columns of one row of a user's state (rows of dk numbers, dk a multiple of 8),
 // 32 bytes at a time (16 where the tensor begins in the middle of 32); columns from
 // dk on are zero.
 __device__ __forceinline__ bool at_32(const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & 31) == 0;
 }
-__device__ __forceinline__ void load_row(const float* from, int cols, F2 (&S)[32]) {
+template <int C>
+__device__ __forceinline__ void load_row(const float* from, int cols, F2 (&S)[2 * C]) {
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
+  for (int c = 0; c < C / 2; ++c) {
     uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (8 * c < cols) {
       if (at_32(from)) {
@@ -266,9 +273,10 @@ __device__ __forceinline__ void load_row(const float* from, int cols, F2 (&S)[32
       S[4 * c + e] = pack2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
   }
 }
-__device__ __forceinline__ void store_row(float* to, int cols, const F2 (&S)[32]) {
+template <int C>
+__device__ __forceinline__ void store_row(float* to, int cols, const F2 (&S)[2 * C]) {
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
+  for (int c = 0; c < C / 2; ++c) {
     uint32_t w[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -355,8 +363,13 @@ __device__ __forceinline__ void stmatrix4_t(uint32_t saddr, const uint32_t (&w)[
 }
 
 // ---------------------------------------------------------------- the kernel
+// DK: 128, or 64 for d_k up to 64: a step's state, its pairs and its products with k and
+// q are half as many columns (B 2, 32 heads of d 64, 4096 tokens: 132 us, with 128
+// columns 153; the carry pass of 4 heads, 131072 tokens: 128 and 154).
+template <int DK>
 __global__ void __launch_bounds__(512, 1)
     delta_scan_kernel(const __grid_constant__ ScanParams p) {
+  constexpr int HC = DK / 2, NB = HC / 16, QK = DK / 64;   // columns of half a row; in 16s; blocks
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -387,7 +400,7 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(&B->y_ready[b], 8);
       mbar_init(&B->xs_ready[b], 8);
     }
-    for (int b = 0; b < 4; ++b) mbar_init(&B->s_ready[b], 8);
+    for (int b = 0; b < NB; ++b) mbar_init(&B->s_ready[b], 8);
     mbar_init(&B->o_full, 1);
     mbar_init(&B->o_free, 4);
     mbar_init(&B->done, 1);
@@ -421,8 +434,8 @@ __global__ void __launch_bounds__(512, 1)
           if (lane == 0) {
             uint8_t* st = smem + s * kStageBytes;
             const int t = it.t0 + c * kC;
-            mbar_arrive_expect_tx(&B->full[s], 6 * kBlk);
-            for (int b = 0; b < 2; ++b) {
+            mbar_arrive_expect_tx(&B->full[s], (2 * QK + 2) * kBlk);
+            for (int b = 0; b < QK; ++b) {
               tma_load_4d(st + (2 * b + 1) * kBlk, &p.k, 64 * b, t, hk, it.batch, &B->full[s]);
               tma_load_4d(st + 2 * b * kBlk, &p.q, 64 * b, t, hk, it.batch, &B->full[s]);
             }
@@ -464,7 +477,7 @@ __global__ void __launch_bounds__(512, 1)
       const uint32_t base = smem_u32(smem), recb = smem_u32(rec);
       const uint32_t id64 = idesc_bf16_f32(64, 0, 0);        // both K-major
       const uint32_t id64m = idesc_bf16_f32(64, 1, 0);       // A = V^T, MN-major
-      const uint32_t id128 = idesc_bf16_f32(128, 0, 1);      // B = K^T, MN-major
+      const uint32_t idk = idesc_bf16_f32(DK, 0, 1);         // B = K^T, MN-major
       int n = 0;
       for (int i = blockIdx.x; i < items && (ok = together(ok)); i += gridDim.x) {
         const Item it = get_item(p, i);
@@ -479,18 +492,18 @@ __global__ void __launch_bounds__(512, 1)
           wait(&B->ready[n % kStages], (n / kStages) & 1);
           const uint64_t kd = smem_desc_sw128(st + kBlk, 16, 1024);
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {   // 16 of each half of d_k at a time
+          for (int b = 0; b < NB; ++b) {   // 16 of each half of d_k at a time
             wait(&B->s_ready[b], ph);
             tc_fence_after();
             if (el) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint32_t a = tmem + kSh + 64 * h + 16 * b;
-                const uint64_t kb = kd + h * (2 * kBlk / 16) + b * 2;
+                const uint32_t a = tmem + kSh + HC * h + 16 * b;
+                const uint64_t kb = kd + (DK == 128 ? h * (2 * kBlk / 16) : h * 4) + b * 2;
                 umma_ts(tmem + kKS, a + 8, kb, id64, b + h != 0);
                 umma_ts(tmem + kKS, a, kb, id64, 1);
               }
-              if (b == 3) umma_commit(&B->ks_full);
+              if (b == NB - 1) umma_commit(&B->ks_full);
             }
             __syncwarp();
           }
@@ -533,7 +546,7 @@ __global__ void __launch_bounds__(512, 1)
           if (el) {
             const uint64_t qd = smem_desc_sw128(st, 16, 1024);
 #pragma unroll 4
-            for (int k = 0; k < 16; ++k)
+            for (int k = 0; k < DK / 8; ++k)
               umma_ts(tmem + kQS, tmem + kSh + (k >> 1) * 16 + (k & 1) * 8,
                       qd + (k >> 3) * (2 * kBlk / 16) + ((k >> 1) & 3) * 2, id64, k != 0);
           }
@@ -548,8 +561,8 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
               for (int k = b; k < 4; k += 2) {
                 const uint32_t x = tmem + kX + k * 16;
-                umma_ts(tmem + kDS, x + 8, km + k * 128, id128, k != 0);
-                umma_ts(tmem + kDS, x, km + k * 128, id128, 1);
+                umma_ts(tmem + kDS, x + 8, km + k * 128, idk, k != 0);
+                umma_ts(tmem + kDS, x, km + k * 128, idk, 1);
               }
               if (b == 1) {
                 umma_commit(&B->ds_full);
@@ -598,7 +611,7 @@ __global__ void __launch_bounds__(512, 1)
             const uint32_t st = smem_u32(smem + s * kStageBytes) + valid * 128;
             const int pieces = (kC - valid) * 8;
             for (int b = 0; b < 6; ++b)
-              for (int x = lane; x < pieces; x += 32)
+              for (int x = lane; x < pieces && (b < 2 * QK || b >= 4); x += 32)
                 sts128(st + b * kBlk + x * 16, make_uint4(0, 0, 0, 0));
             fence_proxy_async_smem();
           }
@@ -616,21 +629,21 @@ __global__ void __launch_bounds__(512, 1)
       const Item it = get_item(p, i);
       const int nc = n_chunks(it.len);
       const int row = 128 * it.tile + 32 * q4 + lane;
-      const long long so = (long long)row * p.dk + 64 * half;
-      F2 S[32];
+      const long long so = (long long)row * p.dk + HC * half;
+      F2 S[HC / 2];
       if (it.from_tile) {
-        load_state(it.from_tile, q4, half, lane, S);
+        load_state<HC / 4>(it.from_tile, q4, half, lane, S);
       } else {
-        load_row(it.from + so, it.from && row < p.dv ? p.dk - 64 * half : 0, S);
+        load_row<HC / 4>(it.from + so, it.from && row < p.dv ? p.dk - HC * half : 0, S);
       }
       auto put_S = [&]() {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < NB; ++b) {
           uint32_t hi[8], lo[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) split2(S[8 * b + e], hi[e], lo[e]);
-          tmem_st8(tl + kSh + 64 * half + 16 * b, hi);
-          tmem_st8(tl + kSh + 64 * half + 16 * b + 8, lo);
+          tmem_st8(tl + kSh + HC * half + 16 * b, hi);
+          tmem_st8(tl + kSh + HC * half + 16 * b + 8, lo);
           tmem_wait_st();
           tc_fence_before();
           arrive(&B->s_ready[b]);
@@ -680,15 +693,15 @@ __global__ void __launch_bounds__(512, 1)
         wait(&B->ds_full, ph);
         tc_fence_after();
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          tmem_ld16_nowait(tl + kDS + 64 * half + 16 * b, x[0]);
+        for (int b = 0; b < NB; ++b) {
+          tmem_ld16_nowait(tl + kDS + HC * half + 16 * b, x[0]);
           tmem_wait_bind(x[0]);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             S[8 * b + e] = fma2(eall, S[8 * b + e], pack2(x[0][2 * e], x[0][2 * e + 1]));
         }
       }
-      if (ok && it.to && row < p.dv) store_row(it.to + so, p.dk - 64 * half, S);
+      if (ok && it.to && row < p.dv) store_row<HC / 4>(it.to + so, p.dk - HC * half, S);
     }
   } else {
     // ---- outputs
@@ -826,8 +839,10 @@ __device__ __forceinline__ CarryItem get_carry(const ScanParams& p, int i) {
   return c;
 }
 
+template <int DK>
 __global__ void __launch_bounds__(640, 1)
     delta_carry_kernel(const __grid_constant__ ScanParams p) {
+  constexpr int HC = DK / 2, QK = DK / 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -882,8 +897,8 @@ __global__ void __launch_bounds__(640, 1)
             uint8_t* st = smem + s * kCarryBytes;
             const int t = ci.it.t0 + c * kC;
             const long long x = (long long)(ci.it.chunk0 + c) * p.Hv + ci.it.h;
-            mbar_arrive_expect_tx(&B->full[s], kCarryBytes + sizeof(RecScal));
-            for (int b = 0; b < 2; ++b)
+            mbar_arrive_expect_tx(&B->full[s], (4 + QK) * kBlk + sizeof(RecScal));
+            for (int b = 0; b < QK; ++b)
               tma_load_4d(st + b * kBlk, &p.k, 64 * b, t, hk, ci.it.batch, &B->full[s]);
             for (int b = 0; b < 2; ++b)
               tma_load_4d(st + (2 + b) * kBlk, &p.v, 128 * ci.it.tile + 64 * b, t, ci.it.h,
@@ -902,7 +917,7 @@ __global__ void __launch_bounds__(640, 1)
       const uint32_t base = smem_u32(smem);
       const uint32_t id64 = idesc_bf16_f32(64, 0, 0);
       const uint32_t id64m = idesc_bf16_f32(64, 1, 0);
-      const uint32_t id128 = idesc_bf16_f32(128, 0, 1);
+      const uint32_t idk = idesc_bf16_f32(DK, 0, 1);
       int n = 0;
       uint32_t nu1 = 0;   // chunks of unit 1
       for (int i = blockIdx.x; i < items && (ok = together(ok)); i += gridDim.x) {
@@ -937,7 +952,7 @@ __global__ void __launch_bounds__(640, 1)
             if (el) {
               const uint64_t kd = smem_desc_sw128(st, 16, 1024);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
+              for (int k = 0; k < DK / 16; ++k) {
                 const uint64_t b = kd + (k >> 2) * (kBlk / 16) + (k & 3) * 2;
                 umma_ts(d + kUA, d + 16 * k + 8, b, id64, k != 0);
                 umma_ts(d + kUA, d + 16 * k, b, id64, 1);
@@ -975,8 +990,8 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const uint32_t x = d + kUX + 16 * k;
-                umma_ts(d, x + 8, km + k * 128, id128, k != 0);
-                umma_ts(d, x, km + k * 128, id128, 1);
+                umma_ts(d, x + 8, km + k * 128, idk, k != 0);
+                umma_ts(d, x, km + k * 128, idk, 1);
               }
               umma_commit(&B->ds_full[u]);
               if (u == units - 1) umma_commit(&B->empty[s]);
@@ -1020,21 +1035,21 @@ __global__ void __launch_bounds__(640, 1)
       }
       const bool is_p = u == 1;
       const int row = 32 * q4 + lane;
-      F2 S[32];
+      F2 S[HC / 2];
       {
-        const int one = is_p ? row - 64 * half : -1;   // this row's column of the unit matrix
+        const int one = is_p ? row - HC * half : -1;   // this row's column of the unit matrix
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
+        for (int c = 0; c < HC / 2; ++c)
           S[c] = pack2(one == 2 * c ? 1.f : 0.f, one == 2 * c + 1 ? 1.f : 0.f);
       }
       auto put_S = [&]() {
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
+        for (int b = 0; b < HC / 8; ++b) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) split2(S[4 * b + e], hi[e], lo[e]);
-          tmem_st4(d + 64 * half + 16 * (b >> 1) + 4 * (b & 1), hi);
-          tmem_st4(d + 64 * half + 16 * (b >> 1) + 8 + 4 * (b & 1), lo);
+          tmem_st4(d + HC * half + 16 * (b >> 1) + 4 * (b & 1), hi);
+          tmem_st4(d + HC * half + 16 * (b >> 1) + 8 + 4 * (b & 1), lo);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -1080,9 +1095,9 @@ __global__ void __launch_bounds__(640, 1)
         wait(&B->ds_full[u], ph);
         tc_fence_after();
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < HC / 16; ++b) {
           float x[16];
-          tmem_ld16_nowait(d + 64 * half + 16 * b, x);
+          tmem_ld16_nowait(d + HC * half + 16 * b, x);
           tmem_wait_bind(x);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
@@ -1091,19 +1106,31 @@ __global__ void __launch_bounds__(640, 1)
         if (c + 1 < nc) put_S();
       }
       if (!ok) continue;
+      // (d_k up to 64: what the join reads behind column 64 is zero)
       if (is_p) {   // row of the join's operand tiles: 64 columns a block, hi then lo
-        uint8_t* to = p.P + ci.sgh * kPBytes + half * 16384 + row * 128;
+        uint8_t* to = p.P + ci.sgh * kPBytes + row * 128;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < HC / 8; ++c) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) split2(S[4 * c + e], hi[e], lo[e]);
-          const int o = (c ^ (row & 7)) << 4;
+          const int x = HC / 8 * half + c;
+          const int o = (x >> 3) * 16384 + (((x & 7) ^ (row & 7)) << 4);
           *reinterpret_cast<uint4*>(to + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4*>(to + kPBytes / 2 + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          if (DK == 64) {
+            *reinterpret_cast<uint4*>(to + 16384 + o) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(to + kPBytes / 2 + 16384 + o) = make_uint4(0, 0, 0, 0);
+          }
         }
       } else {
-        store_state(p.L + (ci.sgh * p.tiles + ci.it.tile) * kStateFloats, q4, half, lane, S);
+        float* to = p.L + (ci.sgh * p.tiles + ci.it.tile) * kStateFloats;
+        store_state<HC / 4>(to, q4, half, lane, S);
+        if (DK == 64) {
+#pragma unroll
+          for (int c = 0; c < HC / 2; ++c) S[c] = 0;
+          store_state<HC / 4>(to, q4, 2 + half, lane, S);
+        }
       }
     }
   }
@@ -1320,7 +1347,7 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
     const int row = 128 * tile + 32 * q4 + lane;
     const uint32_t t = tmem + ((uint32_t)(q4 * 32) << 16) + 64 * half;
     F2 S[32], L[32];
-    load_row(p.S0 + (((long long)seq * p.Hv + h) * p.dv + row) * p.dk + 64 * half,
+    load_row<16>(p.S0 + (((long long)seq * p.Hv + h) * p.dv + row) * p.dk + 64 * half,
              p.S0 && row < p.dv ? p.dk - 64 * half : 0, S);
     auto place = [&](int j) { return (((long long)(seg0 + j) * p.Hv + h) * p.tiles + tile) * kStateFloats; };
 #pragma unroll 1
@@ -1338,8 +1365,8 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&B->s_ready);
       // beside the product: its 128 KB through the load-store units take as long
-      load_state(p.L + place(j), q4, half, lane, L);
-      if (ok && (j > 0 || p.S0)) store_state(p.Sseg + place(j), q4, half, lane, S);
+      load_state<16>(p.L + place(j), q4, half, lane, L);
+      if (ok && (j > 0 || p.S0)) store_state<16>(p.Sseg + place(j), q4, half, lane, S);
       wait(&B->d_full, j & 1);
       tc_fence_after();
 #pragma unroll
@@ -1351,7 +1378,7 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
         for (int e = 0; e < 8; ++e) S[8 * b + e] = add2(L[8 * b + e], pack2(d[2 * e], d[2 * e + 1]));
       }
     }
-    if (ok) store_state(p.Sseg + place(n - 1), q4, half, lane, S);
+    if (ok) store_state<16>(p.Sseg + place(n - 1), q4, half, lane, S);
   }
   tc_fence_before();
   __syncthreads();
@@ -1500,7 +1527,8 @@ int prepare() {
       return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
              cudaSuccess;
     };
-    if (room(delta_scan_kernel, kSmem) && room(delta_carry_kernel, kCarrySmem) &&
+    if (room(delta_scan_kernel<64>, kSmem) && room(delta_scan_kernel<128>, kSmem) &&
+        room(delta_carry_kernel<64>, kCarrySmem) && room(delta_carry_kernel<128>, kCarrySmem) &&
         room(delta_join_kernel, kJoinSmem) &&
         room(delta_join_rows_kernel<4>, sizeof(RowsShared<4>)) &&
         room(delta_join_rows_kernel<8>, sizeof(RowsShared<8>)) &&
@@ -1632,7 +1660,7 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
   r.g = a.g; r.beta = a.beta;
   r.plan = plan;
   r.n_seq = a.n_seq;
-  r.Hk = a.Hk; r.Hv = a.Hv; r.N = a.N;
+  r.Hk = a.Hk; r.Hv = a.Hv; r.N = a.N; r.dk = a.dk;
   r.sg = a.lay.g; r.sb = a.lay.beta;
   r.scale = a.scale;
   r.rec = reinterpret_cast<uint8_t*>(ws + pl.rec);
@@ -1682,7 +1710,7 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
       const int items = (packed ? pl.seg_places : a.B * (pl.seg_n - 1)) * a.Hv * p.tiles;
       ProfScope ps(PT_DELTA_CARRY, a.stream, 5.0 * tok * a.Hv * a.dk * (a.dv + a.dk),
                    tok * 2.0 * (a.Hk * a.dk + a.Hv * a.dv));
-      if (launch_behind(delta_carry_kernel, items < sms ? items : sms, 640, kCarrySmem, a.stream, p) !=
+      if (launch_behind(a.dk > 64 ? delta_carry_kernel<128> : delta_carry_kernel<64>, items < sms ? items : sms, 640, kCarrySmem, a.stream, p) !=
           cudaSuccess)
         return TTT_ERR_CUDA;
     }
@@ -1715,7 +1743,7 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
   const int items = pl.seg_places * a.Hv * p.tiles;
   ProfScope ps(PT_DELTA_CHUNK, a.stream, 7.0 * tok * a.Hv * a.dk * a.dv,
                tok * 4.0 * (a.Hk * a.dk + a.Hv * a.dv));
-  return launch_behind(delta_scan_kernel, items < sms ? items : sms, 512, kSmem, a.stream, p) ==
+  return launch_behind(a.dk > 64 ? delta_scan_kernel<128> : delta_scan_kernel<64>, items < sms ? items : sms, 512, kSmem, a.stream, p) ==
                  cudaSuccess
              ? TTT_OK
              : TTT_ERR_CUDA;

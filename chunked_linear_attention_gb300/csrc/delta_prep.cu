@@ -17,9 +17,9 @@
 // most 1 where g <= 0.
 //
 // Bound by instruction issue and shared memory (issue 48%, l1tex 68%, DRAM 37%): the
-// decays, the substitution and the pairs cost about 7500 warp instructions per
-// record.  2048 records (B 4, H 4, 8192 tokens) take 33.5 us, 8192 (131072 tokens of
-// 4 heads) 103 us, against 80 for the bytes.  Six CTAs per SM, so that one's
+// decays, the substitution and the pairs cost about 7000 warp instructions per
+// record.  2048 records (B 4, H 4, 8192 tokens) take 32 us, 8192 (131072 tokens of 4
+// heads) 97 us, against 80 for the bytes.  Six CTAs per SM, so that one's
 // substitution runs beside another's products; T's tiles lie over the scratch, and
 // the record over q and k, to make room for them.
 #include "delta_tc.cuh"
@@ -157,8 +157,9 @@ __global__ void __launch_bounds__(kPThreads, 6)
     mbar_init(&sh.full, 1);
     mbar_init(&sh.done, 1);
     fence_mbar_init();
-    mbar_arrive_expect_tx(&sh.full, 4 * kBlk);
-    for (int b = 0; b < 2; ++b) {
+    const int blocks = p.dk > 64 ? 2 : 1;
+    mbar_arrive_expect_tx(&sh.full, 2 * blocks * kBlk);
+    for (int b = 0; b < blocks; ++b) {
       tma_load_4d(tile + 2 * b * kBlk, &p.q, 64 * b, t0, hk, batch, &sh.full);
       tma_load_4d(tile + (2 * b + 1) * kBlk, &p.k, 64 * b, t0, hk, batch, &sh.full);
     }
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(kPThreads, 6)
     if (elect_lane()) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
+        if (k == 4 && p.dk <= 64) break;
         const uint32_t o = (k >> 2) * (2 * kBlk / 16) + (k & 3) * 2;
         umma_bf16(tmem, a + o, b + o, id, k != 0);
       }

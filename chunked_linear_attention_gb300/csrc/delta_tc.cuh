@@ -169,7 +169,7 @@ struct PrepParams {
   const float* beta;
   const SeqPlan* plan;     // or NULL
   int n_seq;
-  int Hk, Hv, N;
+  int Hk, Hv, N, dk;
   delta_rule_stride sg, sb;
   float scale;
   uint8_t* rec;            // [chunk][Hv] records

@@ -260,6 +260,8 @@ SPLITS = [
     (1, 4, 16, 1400, 64, 128),
     (2, 2, 2, 1300, 128, 256),
     (1, 3, 6, 1290, 96, 72),
+    (1, 2, 4, 1500, 64, 64),
+    (1, 1, 8, 1300, 40, 136),
 ]
 
 
@@ -304,15 +306,16 @@ def test_states_that_begin_in_the_middle_of_32_bytes(dk, dv):
     assert (room[:, :4] == 5.0).all() and (room[:, 4 + n:] == 5.0).all()
 
 
-def test_many_packed_sequences():
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_packed_sequences(d):
     """More sequences than the plan's block has threads, one of them long."""
     cla = lib()
     gen = torch.Generator().manual_seed(42)
     lens = torch.randint(0, 40, (300,), generator=gen).tolist()
     lens[77], lens[299] = 1500, 65
     starts = [0] + torch.tensor(lens).cumsum(0).tolist()
-    t = inputs(43, 1, 1, 2, starts[-1] + 3, 128, 128, torch.bfloat16, 0.05)
-    S0 = torch.randn(300, 2, 128, 128, generator=gen) * 0.3
+    t = inputs(43, 1, 1, 2, starts[-1] + 3, d, d, torch.bfloat16, 0.05)
+    S0 = torch.randn(300, 2, d, d, generator=gen) * 0.3
     check(cla, run(cla, t, S0, starts), oracle(t, S0, starts), torch.bfloat16)
 
 
