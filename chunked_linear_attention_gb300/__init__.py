@@ -456,6 +456,16 @@ def _want(t, shape, dtype, dev, what):
     raise ValueError(f"{what} must be on {dev}, got {t.device}")
 
 
+def _dense(t, shape, dtype, dev, what):
+    """Address of a contiguous tensor of this shape, or None for None."""
+    if t is None:
+        return None
+    _want(t, shape, dtype, dev, what)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
 def _strides(t, what):
     """Strides of a tensor whose last dimension is contiguous."""
     st = t.stride()
@@ -515,23 +525,21 @@ def delta_rule_chunked_forward(q, k, v, g, beta, S0: Optional[torch.Tensor] = No
         _want(out, (B, Hv, N, dv), dt, dev, "out")
     state = (n_seq, Hv, dv, dk)
     if S_final is None:
-        S_final = torch.empty(state, device=dev, dtype=f32)
-    else:
-        _want(S_final, state, f32, dev, "S_final")
-    if S0 is not None:
-        _want(S0, state, f32, dev, "S0")
+        S_final = g.new_empty(state)
     if workspace is None:
         need = lib.delta_rule_workspace_size(B, Hk, Hv, N, dk, dv, n_seq, io)
         workspace = torch.empty(need or 256, device=dev, dtype=torch.uint8)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {dev}")
     rc = lib.delta_rule_chunked_forward(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(S0),
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+        _dense(S0, state, f32, dev, "S0"),
         None if seq_starts is None else seq_starts.data_ptr(), n_seq, B, Hk, Hv, N, dk, dv, io,
         dk ** -0.5 if scale is None else scale,
         _pack_layout(*_strides(q, "q")[:3], *_strides(k, "k")[:3], *_strides(v, "v")[:3],
                      *g.stride(), *beta.stride(), *_strides(out, "out")[:3]),
-        out.data_ptr(), _ptr(S_final), workspace.data_ptr(), workspace.nbytes,
+        out.data_ptr(), _dense(S_final, state, f32, dev, "S_final"), workspace.data_ptr(),
+        workspace.nbytes,
         _raw_stream(dev.index))
     if rc:
         _check(rc, "delta_rule_chunked_forward")
@@ -565,18 +573,14 @@ def delta_rule_step(q, k, v, g, beta, state, slots: Optional[torch.Tensor] = Non
     _want(g, (B, Hv), f32, dev, "g")
     _want(beta, (B, Hv), f32, dev, "beta")
     n_slots = state.shape[0]
-    _want(state, (n_slots, Hv, dv, dk), f32, dev, "state")
-    if slots is not None:
-        _want(slots, (B,), torch.int32, dev, "slots")
-        if not slots.is_contiguous():
-            raise ValueError("slots must be contiguous")
     if out is None:
-        out = torch.empty((B, Hv, dv), device=dev, dtype=dt)
+        out = torch.empty_like(v)   # half the host time of torch.empty with a device
     else:
         _want(out, (B, Hv, dv), dt, dev, "out")
     rc = (_lib or library()).delta_rule_step(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(state),
-        None if slots is None else slots.data_ptr(), n_slots, B, Hk, Hv, dk, dv, io,
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+        _dense(state, (n_slots, Hv, dv, dk), f32, dev, "state"),
+        _dense(slots, (B,), torch.int32, dev, "slots"), n_slots, B, Hk, Hv, dk, dv, io,
         dk ** -0.5 if scale is None else scale,
         _pack_layout(*_strides(q, "q")[:2], 0, *_strides(k, "k")[:2], 0, *_strides(v, "v")[:2], 0,
                      *g.stride(), 0, *beta.stride(), 0, *_strides(out, "out")[:2], 0),
@@ -637,28 +641,27 @@ def block_norm_forward(y, w: Optional[torch.Tensor] = None,
         out_dtype = (residual if residual is not None else out if out is not None else y).dtype
     if group is None:
         group = D if w is None else w.numel()
-    if w is not None:
-        _want(w, (group,), f32, dev, "w")
-    if scale is not None:
-        _want(scale, (D,), f32, dev, "scale")
-    if w_next is not None:
-        _want(w_next, (D,), f32, dev, "w_next")
-        if h is None:
-            h = torch.empty(y.shape, device=dev, dtype=dt)
-    elif h is not None:
-        raise ValueError("h needs w_next")
+    st_y, st_out, st_h = _rows(y, rows, D, dt, dev, "y"), D, D
+    if h is not None:
+        if w_next is None:
+            raise ValueError("h needs w_next")
+        st_h = _rows(h, rows, D, dt, dev, "h")
+    elif w_next is not None:
+        h = torch.empty_like(y, memory_format=torch.contiguous_format)
     if out is None:
-        out = torch.empty(y.shape, device=dev, dtype=out_dtype)
+        out = torch.empty_like(y, dtype=out_dtype, memory_format=torch.contiguous_format)
+    else:
+        st_out = _rows(out, rows, D, out_dtype, dev, "out")
     rc = (_lib or library()).block_norm_forward(
-        y.data_ptr(), _ptr(w), None if gate is None else gate.data_ptr(),
-        None if residual is None else residual.data_ptr(), _ptr(scale), _ptr(w_next), rows, D,
+        y.data_ptr(), _dense(w, (group,), f32, dev, "w"), None if gate is None else gate.data_ptr(),
+        None if residual is None else residual.data_ptr(),
+        _dense(scale, (D,), f32, dev, "scale"), _dense(w_next, (D,), f32, dev, "w_next"), rows, D,
         group, io, _io_dtype(out), gate_act, eps,
         _pack_norm_strides(
-            _rows(y, rows, D, dt, dev, "y"),
+            st_y,
             0 if gate is None else _rows(gate, rows, D, dt, dev, "gate"),
             0 if residual is None else _rows(residual, rows, D, out_dtype, dev, "residual"),
-            _rows(out, rows, D, out_dtype, dev, "out"),
-            0 if h is None else _rows(h, rows, D, dt, dev, "h")),
+            st_out, st_h),
         out.data_ptr(), None if h is None else h.data_ptr(), _raw_stream(dev.index))
     if rc:
         _check(rc, "block_norm_forward")
