@@ -525,7 +525,7 @@ def delta_rule_chunked_forward(q, k, v, g, beta, S0: Optional[torch.Tensor] = No
         _want(out, (B, Hv, N, dv), dt, dev, "out")
     state = (n_seq, Hv, dv, dk)
     if S_final is None:
-        S_final = g.new_empty(state)
+        S_final = torch.empty(state, device=dev, dtype=f32)
     if workspace is None:
         need = lib.delta_rule_workspace_size(B, Hk, Hv, N, dk, dv, n_seq, io)
         workspace = torch.empty(need or 256, device=dev, dtype=torch.uint8)
