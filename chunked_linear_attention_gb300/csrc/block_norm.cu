@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kMaxThreads<VEC, VPT, PARTS, KEEP>, kMinCtas<P
   constexpr int G = KEEP ? VPT : VEC == 1 ? 4 : 1;
   static_assert(VPT % G == 0, "whole groups");
   float w[KEEP ? VPT : 1][VEC], wn[KEEP ? VPT : 1][VEC];   // w: times the residual scale
-  Piece held[KEEP ? VPT : 1];
+  Piece held[KEEP ? VPT : 1] = {};
   auto at = [&](int i) { return KEEP ? held[KEEP ? i : 0] : place(i); };
   auto col = [&](int i) { return KEEP ? held[KEEP ? i : 0].col : (i * p.nt + me) * VEC; };
   if (KEEP) {

@@ -29,8 +29,8 @@
 // takes 2.25 us, of which the tensor pipe works 47% (2690 cycles of products, in
 // pairs); one more order of products to fill the gaps (two MMA warps, other
 // hand-overs) was slower.  B 4, H 4, 8192 tokens, d 128: 149 us (prep 32, L and P
-// 55, join 24, outputs 47, their ends overlapping), token by token 1.7 ms; one
-// sequence of 131072 tokens, 4 heads: 431 us (97, 156, 46, 139).
+// 54, join 24, outputs 46, their ends overlapping), token by token 1.7 ms; one
+// sequence of 131072 tokens, 4 heads: 428 us (97, 156, 46, 136).
 //
 // Roles (512 threads, one CTA per SM, persistent over (segment, head, d_v tile)):
 //   warp 0      TMA: q, k, v in three stages, the chunk's records in two.
@@ -97,7 +97,7 @@ struct ScanParams {
   unsigned long long wait_ns;
   delta_rule_stride so;
   int Hk, Hv, N, dk, dv, tiles;
-  int seqs, seg_chunks, seg_n;   // chunks per segment; segments per sequence (not packed)
+  int seqs, seg_chunks, seg_n;   // not packed: chunks per segment; segments per sequence
   float scale;
   int wide_out;            // rows of out can be stored 16 bytes at a time
 };
@@ -119,7 +119,7 @@ __device__ __forceinline__ SegPlan get_segment(const ScanParams& p, int k, int& 
   const int whole = p.seqs * (p.seg_n - 1);
   SegPlan sg;
   sg.n = p.seg_n;
-  sg.pad = 0;
+  sg.chunks = p.seg_chunks;
   if (k < whole) {
     sg.seq = k / (p.seg_n - 1);
     sg.j = k - sg.seq * (p.seg_n - 1);
@@ -137,13 +137,19 @@ __device__ __forceinline__ int n_items(const ScanParams& p, bool carry) {
   return n * p.Hv * p.tiles;
 }
 
+// A CTA's items are its places in rounds that go to and fro over the CTAs, so that with
+// long items first no CTA gets the longest of every round (24 sequences of 20011
+// tokens, 8 heads: 6 us).  The distance to the second item; this and the next one are
+// two rounds together.
+__device__ __forceinline__ int first_hop() { return 2 * (gridDim.x - 1 - blockIdx.x) + 1; }
+
 // The tokens of a segment, in an item.
 __device__ __forceinline__ void set_range(const ScanParams& p, const SegPlan& sg, Item& it) {
   const SeqPlan sp = seq_plan(p.plan, sg.seq, p.N);
-  const int before = sg.j * p.seg_chunks;
+  const int before = sg.j * sg.chunks;
   it.batch = p.plan ? 0 : sg.seq;
   it.t0 = sp.t0 + before * kC;
-  it.len = sg.j == sg.n - 1 ? sp.len - before * kC : p.seg_chunks * kC;
+  it.len = sg.j == sg.n - 1 ? sp.len - before * kC : sg.chunks * kC;
   it.chunk0 = sp.chunk0 + before;
 }
 
@@ -424,7 +430,8 @@ __global__ void __launch_bounds__(512, 1)
     regs_dec<64>();
     if (warp == 0) {
       int n = 0;
-      for (int i = blockIdx.x; i < items && (ok = together(ok)); i += gridDim.x) {
+      for (int i = blockIdx.x, hop = first_hop(); i < items && (ok = together(ok));
+           i += hop, hop = 2 * gridDim.x - hop) {
         const Item it = get_item(p, i);
         const int hk = it.h / (p.Hv / p.Hk), nc = n_chunks(it.len);
         for (int c = 0; c < nc && (ok = together(ok)); ++c, ++n) {
@@ -479,7 +486,8 @@ __global__ void __launch_bounds__(512, 1)
       const uint32_t id64m = idesc_bf16_f32(64, 1, 0);       // A = V^T, MN-major
       const uint32_t idk = idesc_bf16_f32(DK, 0, 1);         // B = K^T, MN-major
       int n = 0;
-      for (int i = blockIdx.x; i < items && (ok = together(ok)); i += gridDim.x) {
+      for (int i = blockIdx.x, hop = first_hop(); i < items && (ok = together(ok));
+           i += hop, hop = 2 * gridDim.x - hop) {
         const Item it = get_item(p, i);
         const int nc = n_chunks(it.len);
         for (int c = 0; c < nc && (ok = together(ok)); ++c, ++n) {
@@ -600,7 +608,7 @@ __global__ void __launch_bounds__(512, 1)
       if (!together(ok)) drain_mmas(&B->done, el, p.status, p.wait_ns);
     } else if (warp == 2) {
       int n = 0;
-      for (int i = blockIdx.x; i < items; i += gridDim.x) {
+      for (int i = blockIdx.x, hop = first_hop(); i < items; i += hop, hop = 2 * gridDim.x - hop) {
         const Item it = get_item(p, i);
         const int nc = n_chunks(it.len);
         for (int c = 0; c < nc; ++c, ++n) {
@@ -625,7 +633,7 @@ __global__ void __launch_bounds__(512, 1)
     const int q4 = warp & 3, half = (warp - 4) >> 2;
     const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
     int n = 0;
-    for (int i = blockIdx.x; i < items; i += gridDim.x) {
+    for (int i = blockIdx.x, hop = first_hop(); i < items; i += hop, hop = 2 * gridDim.x - hop) {
       const Item it = get_item(p, i);
       const int nc = n_chunks(it.len);
       const int row = 128 * it.tile + 32 * q4 + lane;
@@ -715,7 +723,7 @@ __global__ void __launch_bounds__(512, 1)
     uint8_t* ob = obuf + q4 * 2048;
     const uint32_t obs = smem_u32(ob);
     int n = 0;
-    for (int i = blockIdx.x; i < items; i += gridDim.x) {
+    for (int i = blockIdx.x, hop = first_hop(); i < items; i += hop, hop = 2 * gridDim.x - hop) {
       const Item it = get_item(p, i);
       const int nc = n_chunks(it.len);
       const int col = 128 * it.tile + 32 * q4;
@@ -886,7 +894,8 @@ __global__ void __launch_bounds__(640, 1)
     regs_dec<64>();
     if (warp == 0) {
       int n = 0;
-      for (int i = blockIdx.x; i < items && (ok = together(ok)); i += gridDim.x) {
+      for (int i = blockIdx.x, hop = first_hop(); i < items && (ok = together(ok));
+           i += hop, hop = 2 * gridDim.x - hop) {
         const CarryItem ci = get_carry(p, i);
         const int hk = ci.it.h / (p.Hv / p.Hk), nc = n_chunks(ci.it.len);
         for (int c = 0; c < nc; ++c, ++n) {
@@ -920,7 +929,8 @@ __global__ void __launch_bounds__(640, 1)
       const uint32_t idk = idesc_bf16_f32(DK, 0, 1);
       int n = 0;
       uint32_t nu1 = 0;   // chunks of unit 1
-      for (int i = blockIdx.x; i < items && (ok = together(ok)); i += gridDim.x) {
+      for (int i = blockIdx.x, hop = first_hop(); i < items && (ok = together(ok));
+           i += hop, hop = 2 * gridDim.x - hop) {
         const CarryItem ci = get_carry(p, i);
         const int nc = n_chunks(ci.it.len), units = ci.it.tile == 0 ? 2 : 1;
         for (int c = 0; c < nc && (ok = together(ok)); ++c, ++n) {
@@ -1007,7 +1017,7 @@ __global__ void __launch_bounds__(640, 1)
       if (!together(ok)) drain_mmas(&B->done, el, p.status, p.wait_ns);
     } else if (warp == 2) {
       int n = 0;
-      for (int i = blockIdx.x; i < items; i += gridDim.x) {
+      for (int i = blockIdx.x, hop = first_hop(); i < items; i += hop, hop = 2 * gridDim.x - hop) {
         const CarryItem ci = get_carry(p, i);
         const int nc = n_chunks(ci.it.len);
         // (segments before a sequence's last one hold whole chunks: nothing to zero)
@@ -1023,7 +1033,7 @@ __global__ void __launch_bounds__(640, 1)
     const uint32_t d = tmem + u * kUnitCols + ((uint32_t)(q4 * 32) << 16);
     int n = 0;
     uint32_t m = 0;   // chunks of this unit
-    for (int i = blockIdx.x; i < items; i += gridDim.x) {
+    for (int i = blockIdx.x, hop = first_hop(); i < items; i += hop, hop = 2 * gridDim.x - hop) {
       const CarryItem ci = get_carry(p, i);
       const int nc = n_chunks(ci.it.len);
       if (u == 1 && ci.it.tile != 0) {   // no unit here: pass the stages on
@@ -1167,25 +1177,105 @@ __device__ __forceinline__ I block_before(I x, I* part, I& total) {
   return before + s - x;
 }
 
+// Chunks per segment, for lengths that only the device knows: the cheapest of 64
+// choices from `least` (what the workspace has places for) to the longest sequence, by
+// the measured times of make_plan.  nc: this thread's sequence (of at most
+// kPlanThreads); units: heads by tiles of d_v.  (8000 tokens in 24 sequences, 16 heads:
+// 174 to 183 us with the host's cut, 115 to 157 so; 20011 tokens, 24 sequences, 8 heads:
+// 173 to 189 and 144 to 181; the plan takes 8.7 us.)
+__device__ __forceinline__ int choose_segments(int nc, int n_seq, int least, int units) {
+  constexpr int kChoices = 64;
+  constexpr float kSms = 152.f;
+  __shared__ int len[kPlanThreads];
+  __shared__ float cost[kChoices];
+  __shared__ int longest;
+  const int lane = threadIdx.x & 31;
+  auto choice = [&](int c) {
+    const int most = max(longest, least);
+    if (c == kChoices - 1) return most;
+    const float x = c < 16 ? (float)(least + c) : (float)(least + 16) * exp2f((c - 16) * 0.125f);
+    return x < (float)most ? (int)x : most;
+  };
+  len[threadIdx.x] = nc;
+  if (threadIdx.x == 0) longest = 0;
+  __syncthreads();
+  atomicMax(&longest, nc);
+  __syncthreads();
+  // eight lanes a choice
+#pragma unroll 1
+  for (int c = threadIdx.x >> 3; c < kChoices; c += kPlanThreads / 8) {
+    const int lc = choice(c);
+    float whole = 0.f, left = 0.f, hops = 0.f, most = 0.f;
+    for (int s = lane & 7; s < n_seq; s += 8) {
+      const int before = max(0, (len[s] - 1) / lc);   // segments before the last one
+      const float l = (float)(len[s] - before * lc);
+      whole += (float)before;
+      left += l + 0.6f;
+      hops = fmaxf(hops, (float)before);
+      most = fmaxf(most, l);
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {
+      whole += __shfl_xor_sync(0xffffffffu, whole, o);
+      left += __shfl_xor_sync(0xffffffffu, left, o);
+      hops = fmaxf(hops, __shfl_xor_sync(0xffffffffu, hops, o));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    }
+    if ((lane & 7) == 0) {
+      const float items = whole * units, rounds = ceilf(items / kSms), step = (float)(lc + 1);
+      // last segments that find no free SM in the round that the whole ones begin
+      const float room = rounds * kSms - items, last = (float)n_seq * units;
+      const float behind = items > 0.f && last > room ? fminf(lc, most) * (1.f - room / last) : 0.f;
+      const float mean = (items * step + left * units) / kSms;
+      const float steps = fmaxf(fmaxf(rounds * step + behind, 1.03f * mean + 0.5f), most + 0.6f);
+      cost[c] = 10.f + 2.25f * steps +
+                (items > 0.f ? 12.f + 2.65f * rounds * step + 5.f + 2.f * hops : 5.f);
+    }
+  }
+  __syncthreads();
+  int best = cost[lane + 32] < cost[lane] ? lane + 32 : lane;   // by every warp for itself
+  float low = cost[best];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float x = __shfl_xor_sync(0xffffffffu, low, o);
+    const int c = __shfl_xor_sync(0xffffffffu, best, o);
+    if (x < low || (x == low && c < best)) {
+      low = x;
+      best = c;
+    }
+  }
+  return choice(best);
+}
+
 __global__ void __launch_bounds__(kPlanThreads)
-    delta_plan_kernel(const int* starts, int n_seq, int N, int chunks, int seg_chunks,
-                      int seg_places, SeqPlan* plan, SegPlan* segs, int* order, int* joins,
-                      int* counts, int* status) {
+    delta_plan_kernel(const int* starts, int n_seq, int N, int chunks, int least, bool split,
+                      int units, int seg_places, SeqPlan* plan, SegPlan* segs, int* order,
+                      int* joins, int* counts, int* status) {
   __shared__ int part[kPlanThreads / 32];
   __shared__ long long wide_part[kPlanThreads / 32];
   pdl_launch_dependents();
+  auto bounds = [&](int s, int& t0, int& len) {
+    const int a = starts[s], b = starts[s + 1];
+    const bool good = a >= 0 && a <= b && b <= N;
+    t0 = good ? a : 0;
+    len = good ? b - a : 0;
+    return good;
+  };
+  const bool few = n_seq <= kPlanThreads;   // a thread per sequence
+  int t0 = 0, len = 0, seg_chunks = least;
+  bool good = true;
+  if ((int)threadIdx.x < n_seq) good = bounds(threadIdx.x, t0, len);
+  if (split && few) seg_chunks = choose_segments(n_chunks(len), n_seq, least, units);
+  int last = -1, left = 0;   // this thread's sequence's last segment and its chunks
   // (sequences that overlap may hold more chunks together than an int can count)
   long long chunk0 = 0;
   int seg0 = 0, join0 = 0;
   for (int s0 = 0; s0 < n_seq; s0 += kPlanThreads) {
     const int s = s0 + (int)threadIdx.x;
-    int t0 = 0, len = 0, nc = 0, ns = 0;
+    int nc = 0, ns = 0;
     if (s < n_seq) {
-      const int a = starts[s], b = starts[s + 1];
-      const bool good = a >= 0 && a <= b && b <= N;
+      if (s0 > 0) good = bounds(s, t0, len);
       if (!good) report_status(status, -8);
-      t0 = good ? a : 0;
-      len = good ? b - a : 0;
       nc = n_chunks(len);
       ns = max(1, (nc + seg_chunks - 1) / seg_chunks);
     }
@@ -1205,40 +1295,49 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (ns > 1) joins[jb] = sb;   // the place of its first segment
     join0 += tj;
     if (s < n_seq) {
+      last = sb + ns - 1;
+      left = n_chunks(len) - (ns - 1) * seg_chunks;
       plan[s] = SeqPlan{t0, len, fits ? (int)cb : 0, 0};
       for (int j = 0; j < ns; ++j) {
-        segs[sb + j] = SegPlan{s, j, ns, 0};
+        segs[sb + j] = SegPlan{s, j, ns, seg_chunks};
         if (j + 1 < ns) order[sb - s + j] = sb + j;   // s last ones are before it
       }
     }
     chunk0 += tc;
     seg0 += ts;
   }
-  // The last segments, behind the whole ones, long ones first: each CTA takes every
-  // 152nd item, and the short ones fill up the rounds.  (Order among equals does not
-  // matter to any result.)
+  // The last segments, behind the whole ones, long ones first: the short ones fill up
+  // the rounds.  (Order among equals does not matter to any result.)
   __shared__ int count[kPlanThreads], base[kPlanThreads];
   count[threadIdx.x] = 0;
   __syncthreads();   // segs and plan are written
   const int whole = seg0 - n_seq;
-  auto bin = [&](const SegPlan& sg) {   // by chunks, the most in bin 0
-    const int left = n_chunks(plan[sg.seq].len) - sg.j * seg_chunks;
-    return kPlanThreads - 1 - min(left, kPlanThreads - 1);
+  auto bin = [](int chunks) { return kPlanThreads - 1 - min(chunks, kPlanThreads - 1); };
+  auto chunks_of = [&](const SegPlan& sg) {
+    return n_chunks(plan[sg.seq].len) - sg.j * seg_chunks;
   };
-  for (int i = (int)threadIdx.x; i < seg0; i += kPlanThreads) {
-    const SegPlan sg = segs[i];
-    if (sg.j == sg.n - 1) atomicAdd(&count[bin(sg)], 1);
+  if (few) {
+    if (last >= 0) atomicAdd(&count[bin(left)], 1);
+  } else {
+    for (int i = (int)threadIdx.x; i < seg0; i += kPlanThreads) {
+      const SegPlan sg = segs[i];
+      if (sg.j == sg.n - 1) atomicAdd(&count[bin(chunks_of(sg))], 1);
+    }
   }
   __syncthreads();
   int all;
   base[threadIdx.x] = block_before(count[threadIdx.x], part, all);
   __syncthreads();
-  for (int i = (int)threadIdx.x; i < seg0; i += kPlanThreads) {
-    const SegPlan sg = segs[i];
-    if (sg.j == sg.n - 1) order[whole + atomicAdd(&base[bin(sg)], 1)] = i;
+  if (few) {
+    if (last >= 0) order[whole + atomicAdd(&base[bin(left)], 1)] = last;
+  } else {
+    for (int i = (int)threadIdx.x; i < seg0; i += kPlanThreads) {
+      const SegPlan sg = segs[i];
+      if (sg.j == sg.n - 1) order[whole + atomicAdd(&base[bin(chunks_of(sg))], 1)] = i;
+    }
   }
   for (int i = seg0 + (int)threadIdx.x; i < seg_places; i += kPlanThreads)
-    segs[i] = SegPlan{-1, 0, 1, 0};
+    segs[i] = SegPlan{-1, 0, 1, seg_chunks};
   if (threadIdx.x == 0) {
     counts[0] = whole;
     counts[1] = seg0;
@@ -1571,7 +1670,8 @@ Plan make_plan(int B, int Hv, int N, int dk, int dv, int n_seq, bool packed) {
       if (n > 1) t += 12.0 + 2.65 * rounds((double)units * (n - 1)) * (lc + 1);
     } else {
       // lengths unknown: of n_seq sequences half a segment is left over each, and the
-      // longest is about four times the mean
+      // longest is about four times the mean.  The plan kernel sees them and may cut
+      // longer segments (choose_segments); the workspace holds the ones of this cut.
       const double longest = n_seq > 4 ? 4.0 * nc / n_seq : nc;
       double whole = (double)nc / lc - 0.5 * n_seq;
       hops = longest / lc;
@@ -1700,7 +1800,8 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
   if (packed) {
     ProfScope ps(PT_DELTA_PLAN, a.stream, 0.0, 20.0 * a.n_seq);
     delta_plan_kernel<<<1, kPlanThreads, 0, a.stream>>>(a.seq_starts, a.n_seq, a.N, pl.chunks,
-                                                        pl.seg_chunks, pl.seg_places, plan, segs,
+                                                        pl.seg_chunks, pl.split, a.Hv * p.tiles,
+                                                        pl.seg_places, plan, segs,
                                                         order, joins, counts, a.status);
     if (cudaGetLastError() != cudaSuccess) return TTT_ERR_CUDA;
   }

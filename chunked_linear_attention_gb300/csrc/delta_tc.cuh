@@ -34,7 +34,8 @@ struct SeqPlan {
 // Segment j of n of a sequence: the chunks that one CTA walks (seq < 0: no
 // segment at this place).
 struct SegPlan {
-  int seq, j, n, pad;
+  int seq, j, n;
+  int chunks;   // of each segment but a sequence's last
 };
 
 __host__ __device__ __forceinline__ int n_chunks(int len) {

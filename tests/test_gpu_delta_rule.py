@@ -319,6 +319,21 @@ def test_many_packed_sequences(d):
     check(cla, run(cla, t, S0, starts), oracle(t, S0, starts), torch.bfloat16)
 
 
+@pytest.mark.parametrize("lens", [[2600, 60, 1, 0, 700], [640] * 6, [90] * 40, [64] * 250 + [5000]],
+                         ids=["one_long", "equal", "short", "many"])
+def test_packed_lengths_that_are_cut_differently(lens):
+    """Packed sequences that the plan cuts into long or short segments, or not
+    at all, with two value heads per key head."""
+    cla = lib()
+    starts = [0] + torch.tensor(lens).cumsum(0).tolist()
+    t = inputs(50, 1, 2, 4, starts[-1], 64, 128, torch.bfloat16, 0.02)
+    S0 = torch.randn(len(lens), 4, 128, 64, generator=torch.Generator().manual_seed(51)) * 0.3
+    a = run(cla, t, S0, starts)
+    check(cla, a, oracle(t, S0, starts), torch.bfloat16)
+    b = run(cla, t, S0, starts)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_zero_length_axis_edges_and_one_token_sequences():
     """A packed batch of single tokens, and one in which every sequence is
     empty: outputs untouched, states unchanged."""
