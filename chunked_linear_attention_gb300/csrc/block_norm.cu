@@ -12,14 +12,13 @@
 // that divides the group's pieces, at most 32), and the group's few remaining
 // partial sums through shared memory, always in the same order.
 //
-// Measured: 65536 rows of 1536 with four gated groups, bf16, 104 us (5.8 TB/s, 86%
+// Measured: 65536 rows of 1536 with four gated groups, bf16, 103 us (5.8 TB/s, 87%
 // of a measured copy; one row per CTA, with the weights read anew for each, took
 // 197: its instructions, and not HBM, were the bound); 20011 rows of 1536 with gate,
-// fp32 residual and both norms 69 us (6.2 TB/s); a single row 4 us.  Longer rows
+// fp32 residual and both norms 67 us (6.4 TB/s); a single row 4 us.  Longer rows
 // reach 3.6 to 4.8 TB/s (fewer CTAs per SM to run past each other's barriers), ones
 // of unaligned length 1.2 to 1.6 (an element per access, and issue is the bound).
-#include "common.cuh"
-#include "delta_rule.h"
+#include "delta_tc.cuh"
 #include "prof.h"
 
 namespace ttt {
@@ -164,6 +163,8 @@ __global__ void __launch_bounds__(kMaxThreads<VEC, VPT, PARTS, KEEP>, kMinCtas<P
   const bool NEXT = PARTS < 0 ? p.h != nullptr : (PARTS & 1) != 0;
   // for each row of the CTA: [2][pieces / P] group partials, [2][nt / 32] row partials
   extern __shared__ float smem[];
+  pdl_launch_dependents();
+  pdl_wait();
   const int ty = threadIdx.x / p.nt, tid = threadIdx.x - ty * p.nt, ny = blockDim.x / p.nt;
   const int warp = tid >> 5, lane = tid & 31, nw = p.nt >> 5, np = p.np;
   float* part = smem + ty * 2 * (np + nw);
@@ -411,8 +412,10 @@ int launch_parts(const BlockNormArgs& a, NormParams p) {
                n * (sizeof(T) * (1 + (a.gate ? 1 : 0) + (a.h ? 1 : 0)) +
                     sizeof(TS) * (1 + (a.residual ? 1 : 0))));
   const long long ctas = (a.rows + ny - 1) / ny, most = 152ll * per_sm;
-  kern<<<(unsigned)(ctas < most ? ctas : most), threads, smem, a.stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+  return launch_behind(kern, (unsigned)(ctas < most ? ctas : most), threads, smem, a.stream, p) ==
+                 cudaSuccess
+             ? TTT_OK
+             : TTT_ERR_CUDA;
 }
 
 template <typename T, typename TS>

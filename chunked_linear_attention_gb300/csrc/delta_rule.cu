@@ -8,8 +8,7 @@
 // tokens.  With S the state before the token, both products of a token are
 // taken from it at once, S k and S q (o = scale (a S q + u (k . q))), so a
 // token costs one butterfly over L lanes and not two in a row.
-#include "common.cuh"
-#include "delta_rule.h"
+#include "delta_tc.cuh"
 #include "prof.h"
 
 namespace ttt {
@@ -49,7 +48,7 @@ __device__ __forceinline__ void seq_range(const int* starts, int s, int N, int* 
 // of the shared memory.  Bound by the chain of a token (two dot products, a
 // butterfly, the update), hidden in part by the other CTA of the SM: in fp32 B 4,
 // H 4, 8192 tokens take 1.66 ms at d 128 (0.20 us a token, 16 CTAs' rows of 16
-// fill 128 SMs), 256 tokens of one head 34 us at d 32 and 58 at d 128.  With d_k of
+// fill 128 SMs), 256 tokens of one head 31 us at d 32 and 58 at d 128.  With d_k of
 // 256, two CTAs per SM (128 registers) take 1.0 ms for 2048 tokens and one 1.34; of
 // 512, four rows a thread 1.2 ms for 512 tokens (0.6 us a token) and two 1.5.
 constexpr int kRecWarps = 4;
@@ -77,6 +76,8 @@ __global__ void __launch_bounds__(256, R < 4 ? 2 : 1)
   constexpr int ROWS = kRecWarps * (32 / L) * R;   // rows of this CTA
   constexpr int TOK = 2 * W + ROWS + 4;            // floats per staged token
   extern __shared__ __align__(16) float stage[];   // [2][TT][TOK]
+  pdl_launch_dependents();
+  pdl_wait();
   const int tile = blockIdx.x % p.row_tiles;
   const int sh = blockIdx.x / p.row_tiles;
   const int h = sh % p.Hv, s = sh / p.Hv;
@@ -250,8 +251,8 @@ int launch_recurrent(const DeltaArgs& a, RecParams p) {
   const double tok = (double)a.B * a.N;
   ProfScope ps(PT_DELTA_RECURRENT, a.stream, 7.0 * tok * a.Hv * a.dk * a.dv,
                tok * (a.bf16 ? 2 : 4) * 2.0 * (a.Hk * a.dk + a.Hv * a.dv));
-  kern<<<(unsigned)grid, 256, smem, a.stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+  return launch_behind(kern, (unsigned)grid, 256, smem, a.stream, p) == cudaSuccess ? TTT_OK
+                                                                                    : TTT_ERR_CUDA;
 }
 
 template <typename T>
@@ -284,12 +285,14 @@ constexpr int kStepThreads = 128;
 // One CTA: 4 (32 / L) R rows of one (row of the batch, head).  The state is
 // read and written once, each thread's R E elements all in flight together; the
 // bound is HBM (the states' bytes twice).  Heads of 128 x 128: 256 rows of 32
-// heads 179 us (6.0 TB/s, 90% of a measured copy), 56 rows of 16 heads 24.6 us
-// (4.8 TB/s: beginning and end are a part of it), one row of 4 heads 4 us.
+// heads 180 us (6.0 TB/s, 89% of a measured copy), 56 rows of 16 heads 22.5 us
+// (5.3 TB/s: beginning and end are a part of it), one row of 4 heads 4 us.
 template <typename T, int L, int E, int R, bool VEC>
 __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(
     const __grid_constant__ StepParams p) {
   constexpr int ROWS = (kStepThreads / L) * R;
+  pdl_launch_dependents();
+  pdl_wait();
   const int tile = blockIdx.x % p.row_tiles;
   const int bh = blockIdx.x / p.row_tiles;
   const int h = bh % p.Hv, b = bh / p.Hv;
@@ -392,9 +395,10 @@ int launch_step(const DeltaStepArgs& a, StepParams p) {
   p.row_tiles = (a.dv + ROWS - 1) / ROWS;
   const double heads = (double)a.B * a.Hv;
   ProfScope ps(PT_DELTA_STEP, a.stream, 7.0 * heads * a.dk * a.dv, 8.0 * heads * a.dk * a.dv);
-  delta_step_kernel<T, L, E, R, VEC>
-      <<<(unsigned)(a.B * a.Hv * p.row_tiles), kStepThreads, 0, a.stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+  return launch_behind(delta_step_kernel<T, L, E, R, VEC>, (unsigned)(a.B * a.Hv * p.row_tiles),
+                       kStepThreads, 0, a.stream, p) == cudaSuccess
+             ? TTT_OK
+             : TTT_ERR_CUDA;
 }
 
 template <typename T, bool VEC>
