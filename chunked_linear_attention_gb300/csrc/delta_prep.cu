@@ -16,7 +16,7 @@
 // (sums of a few g lose few bits), and blocks are joined by factors that are at
 // most 1 where g <= 0.
 //
-// Bound by instruction issue and shared memory (issue 48%, l1tex 68%, DRAM 37%): the
+// Bound by instruction issue and shared memory (issue 47%, l1tex 61%, DRAM 36%): the
 // decays, the substitution and the pairs cost about 7000 warp instructions per
 // record.  2048 records (B 4, H 4, 8192 tokens) take 32 us, 8192 (131072 tokens of 4
 // heads) 97 us, against 80 for the bytes.  Six CTAs per SM, so that one's
