@@ -1487,128 +1487,174 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
   }
 }
 
-// The same for few heads, in fp32 on the CUDA cores: a CTA takes R rows, so that a
-// head's step is spread over 128 / R SMs (one SM moves 192 KB in a step above; here a
-// step takes 1.0 us with R = 4, its 64 KB of P).  Each of the eight
-// warps takes sixteen rows of P and 4 columns per lane; the eight partial sums are
-// added in a fixed order.
+// The same for few heads: a CTA takes 16 MT rows, so that a head's step is spread over
+// 8 / MT SMs (one SM moves 192 KB in a step above).  Warp w makes columns 16 w .. of the
+// next state from S's pairs in shared memory and P's, on mma.sync (tcgen05 has no
+// product of 16 rows), and keeps them as fp32; P in three places, two ahead.  (HOPS)
 constexpr int kRowsThreads = 256;
+constexpr int kRowsStages = 3;
+constexpr int kRowStride = 136;   // of the pairs' rows: eight of them in eight bank groups
 
-template <int R>
+template <int MT>
 struct RowsShared {
-  uint8_t P[2][kPBytes];
-  float part[8][R][128];
-  float S[R][128];
-  uint64_t full[2];
+  uint8_t P[kRowsStages][kPBytes];
+  __nv_bfloat16 A[2][2][16 * MT * kRowStride];   // [step & 1][hi, lo]
+  uint64_t full[kRowsStages];
 };
+static_assert(sizeof(RowsShared<2>) <= 227 * 1024, "shared memory");
 
-template <int R>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+      " {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int MT>
 __global__ void __launch_bounds__(kRowsThreads, 1)
     delta_join_rows_kernel(const __grid_constant__ JoinParams p) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  RowsShared<R>& sh = *reinterpret_cast<RowsShared<R>*>(smem_raw);
-  constexpr int kParts = 128 / R;
-  const int row0 = R * (blockIdx.x % kParts), x = blockIdx.x / kParts;
+  RowsShared<MT>& sh = *reinterpret_cast<RowsShared<MT>*>(smem_raw);
+  constexpr int kParts = 8 / MT;
+  const int row0 = 16 * MT * (blockIdx.x % kParts), x = blockIdx.x / kParts;
   const int tile = x % p.tiles, h = x / p.tiles % p.Hv, seq = x / p.tiles / p.Hv;
   const int n = p.seg_n, seg0 = seq * n;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
   pdl_wait();
   bool ok = true;
-  auto load = [&](int j) {
-    mbar_arrive_expect_tx(&sh.full[j & 1], kPBytes);
-    bulk_load_g2s(sh.P[j & 1], p.P + ((long long)(seg0 + j) * p.Hv + h) * kPBytes, kPBytes,
-                  &sh.full[j & 1]);
+  int loaded = 0;   // by thread 0
+  auto load = [&]() {
+    uint64_t* bar = &sh.full[loaded % kRowsStages];
+    mbar_arrive_expect_tx(bar, kPBytes);
+    bulk_load_g2s(sh.P[loaded % kRowsStages],
+                  p.P + ((long long)(seg0 + loaded) * p.Hv + h) * kPBytes, kPBytes, bar);
+    ++loaded;
   };
   if (tid == 0) {
-    mbar_init(&sh.full[0], 1);
-    mbar_init(&sh.full[1], 1);
+    for (int s = 0; s < kRowsStages; ++s) mbar_init(&sh.full[s], 1);
     fence_mbar_init();
-    for (int j = 0; j < 2 && j + 1 < n; ++j) load(j);
+    while (loaded < kRowsStages && loaded + 1 < n) load();
   }
-  // this thread's outputs: column col, rows r0 .. r0 + R / 2
-  const int col = tid & 127, r0 = (tid >> 7) * (R / 2);
-  int at[R / 2];
+  auto place = [&](int j) {
+    return (((long long)(seg0 + j) * p.Hv + h) * p.tiles + tile) * kStateFloats;
+  };
+  // this thread's numbers: rows r, r + 8 of each 16, two columns of each 8
+  const int r = row0 + (lane >> 2), c = 16 * warp + 2 * (lane & 3);
+  auto at = [&](int row, int col) {   // in a tile between the kernels
+    return (int)state_at(row >> 5, col >> 6, (col & 63) >> 2, row & 31) * 4 + (col & 3);
+  };
+  F2 S[MT][2][2];   // [16 rows][8 columns][8 rows]
 #pragma unroll
-  for (int r = 0; r < R / 2; ++r) {
-    const int row = row0 + r0 + r, grow = 128 * tile + row;
-    at[r] = (int)state_at(row >> 5, col >> 6, (col & 63) >> 2, row & 31) * 4 + (col & 3);
-    const float s = p.S0 && grow < p.dv && col < p.dk
-                        ? p.S0[(((long long)seq * p.Hv + h) * p.dv + grow) * p.dk + col]
-                        : 0.f;
-    sh.S[r0 + r][col] = s;
-    if (p.S0)
-      p.Sseg[(((long long)seg0 * p.Hv + h) * p.tiles + tile) * kStateFloats + at[r]] = s;
-  }
-  __syncthreads();
-  const int half = lane >> 4;   // of P's column blocks; 4 columns from 4 (lane & 15) in it
-  int waited = 0;
-  for (int j = 0; j + 1 < n; ++j) {
-    const long long sgh = (long long)(seg0 + j) * p.Hv + h;
-    const float* L = p.L + (sgh * p.tiles + tile) * kStateFloats;
-    float l[R / 2];
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int r = 0; r < R / 2; ++r) l[r] = L[at[r]];
-    if (ok) waited = j;
-    wait_w(ok, &sh.full[j & 1], (j >> 1) & 1, p.status, p.wait_ns);
-    F2 acc[R][2];
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int r = 0; r < R; ++r) acc[r][0] = acc[r][1] = 0;
-    const uint8_t* P = sh.P[j & 1] + half * 16384 + (lane & 1) * 8;
-#pragma unroll 1
-    for (int m = 16 * warp; m < 16 * warp + 16; m += 4) {
-      F2 w[4][2];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int o = (m + e) * 128 + ((((lane & 15) >> 1) ^ ((m + e) & 7)) << 4);
-        const uint2 hi = *reinterpret_cast<const uint2*>(P + o);
-        const uint2 lo = *reinterpret_cast<const uint2*>(P + kPBytes / 2 + o);
-        w[e][0] = add2(pack2(__uint_as_float(hi.x << 16), __uint_as_float(hi.x & 0xffff0000u)),
-                       pack2(__uint_as_float(lo.x << 16), __uint_as_float(lo.x & 0xffff0000u)));
-        w[e][1] = add2(pack2(__uint_as_float(hi.y << 16), __uint_as_float(hi.y & 0xffff0000u)),
-                       pack2(__uint_as_float(lo.y << 16), __uint_as_float(lo.y & 0xffff0000u)));
+      for (int e = 0; e < 2; ++e) {
+        const int row = r + 16 * m + 8 * e, col = c + 8 * t, grow = 128 * tile + row;
+        float2 s = make_float2(0.f, 0.f);
+        if (p.S0 && grow < p.dv && col < p.dk)   // (d_k is even)
+          s = *reinterpret_cast<const float2*>(
+              p.S0 + (((long long)seq * p.Hv + h) * p.dv + grow) * p.dk + col);
+        S[m][t][e] = pack2(s.x, s.y);
+        if (p.S0) *reinterpret_cast<F2*>(p.Sseg + place(0) + at(row, col)) = S[m][t][e];
       }
+  int waited = 0;
+  // operand addresses of this lane
+  const uint32_t a_at = ((lane & 7) + 8 * ((lane >> 3) & 1)) * kRowStride * 2 + 16 * (lane >> 4);
+  const int b_row = (lane & 7) + 8 * ((lane >> 3) & 1), b_chunk = 2 * (warp & 3) + (lane >> 4);
+  const uint32_t b_at = (warp >> 2) * 16384 + b_row * 128 + ((b_chunk ^ (b_row & 7)) << 4);
+#pragma unroll 1
+  for (int j = 0; j + 1 < n; ++j) {
+    F2 L[MT][2][2];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float4 s4 = *reinterpret_cast<const float4*>(&sh.S[r][m]);
-        const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const F2 s2 = pack2(s[e], s[e]);
-          acc[r][0] = fma2(s2, w[e][0], acc[r][0]);
-          acc[r][1] = fma2(s2, w[e][1], acc[r][1]);
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = r + 16 * m + 8 * e, col = c + 8 * t;
+          L[m][t][e] = *reinterpret_cast<const F2*>(p.L + place(j) + at(row, col));
+          uint32_t hi, lo;
+          split2(S[m][t][e], hi, lo);
+          const int o = (row - row0) * kRowStride + col;
+          *reinterpret_cast<uint32_t*>(&sh.A[j & 1][0][o]) = hi;
+          *reinterpret_cast<uint32_t*>(&sh.A[j & 1][1][o]) = lo;
+        }
+    __syncthreads();
+    if (tid == 0 && j > 0 && loaded + 1 < n && ok) {   // everyone is done with P_{j-1}
+      fence_proxy_async_smem();
+      load();
+    }
+    if (ok) waited = j;
+    wait_w(ok, &sh.full[j % kRowsStages], (j / kRowsStages) & 1, p.status, p.wait_ns);
+    const uint32_t P = smem_u32(sh.P[j % kRowsStages]) + b_at;
+    const uint32_t Ah = smem_u32(sh.A[j & 1][0]) + a_at, Al = smem_u32(sh.A[j & 1][1]) + a_at;
+    float acc[MT][2][3][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[m][t][q][e] = 0.f;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t bh[4], bl[4];
+      ldmatrix4_t(bh, P + k * 16 * 128);
+      ldmatrix4_t(bl, P + kPBytes / 2 + k * 16 * 128);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        uint32_t ah[4], al[4];
+        ldmatrix4(ah, Ah + (16 * m * kRowStride + 16 * k) * 2);
+        ldmatrix4(al, Al + (16 * m * kRowStride + 16 * k) * 2);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          mma_bf16(acc[m][t][0], al, bh[2 * t], bh[2 * t + 1]);
+          mma_bf16(acc[m][t][1], ah, bl[2 * t], bl[2 * t + 1]);
+          mma_bf16(acc[m][t][2], ah, bh[2 * t], bh[2 * t + 1]);
         }
       }
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      *reinterpret_cast<ulonglong2*>(&sh.part[warp][r][4 * lane]) =
-          make_ulonglong2(acc[r][0], acc[r][1]);
-    __syncthreads();
-    if (tid == 0 && j + 3 < n && ok) {   // everyone is done with P_j
-      fence_proxy_async_smem();
-      load(j + 2);
-    }
-    float* to = p.Sseg + ((sgh + p.Hv) * p.tiles + tile) * kStateFloats;
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int r = 0; r < R / 2; ++r) {
-      float s = l[r];
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int w = 0; w < 8; ++w) s += sh.part[w][r0 + r][col];
-      sh.S[r0 + r][col] = s;
-      if (ok) to[at[r]] = s;
-    }
-    __syncthreads();
+        for (int e = 0; e < 2; ++e) {
+          const float(&q)[3][4] = acc[m][t];
+          const F2 low = add2(pack2(q[0][2 * e], q[0][2 * e + 1]), pack2(q[1][2 * e], q[1][2 * e + 1]));
+          S[m][t][e] = add2(L[m][t][e], add2(low, pack2(q[2][2 * e], q[2][2 * e + 1])));
+          if (ok)
+            *reinterpret_cast<F2*>(p.Sseg + place(j + 1) + at(r + 16 * m + 8 * e, c + 8 * t)) =
+                S[m][t][e];
+        }
   }
   if (tid == 0 && !ok)   // copies still on their way into this CTA's shared memory
-    for (int j = waited; j < waited + 2 && j + 1 < n; ++j)
-      mbar_wait(&sh.full[j & 1], (j >> 1) & 1, p.status, p.wait_ns);
+    for (int j = waited; j < loaded; ++j)
+      mbar_wait(&sh.full[j % kRowsStages], (j / kRowsStages) & 1, p.status, p.wait_ns);
 }
 
-template <int R>
+template <int MT>
 cudaError_t launch_rows(const JoinParams& j, cudaStream_t stream) {
-  return launch_behind(delta_join_rows_kernel<R>, j.seqs * j.Hv * j.tiles * (128 / R), kRowsThreads,
-                       sizeof(RowsShared<R>), stream, j);
+  return launch_behind(delta_join_rows_kernel<MT>, j.seqs * j.Hv * j.tiles * (8 / MT), kRowsThreads,
+                       sizeof(RowsShared<MT>), stream, j);
 }
 
 int g_ready[64] = {0};   // 0 unknown, 1 usable, 2 not usable
@@ -1629,8 +1675,8 @@ int prepare() {
     if (room(delta_scan_kernel<64>, kSmem) && room(delta_scan_kernel<128>, kSmem) &&
         room(delta_carry_kernel<64>, kCarrySmem) && room(delta_carry_kernel<128>, kCarrySmem) &&
         room(delta_join_kernel, kJoinSmem) &&
-        room(delta_join_rows_kernel<4>, sizeof(RowsShared<4>)) &&
-        room(delta_join_rows_kernel<8>, sizeof(RowsShared<8>)) &&
+        room(delta_join_rows_kernel<1>, sizeof(RowsShared<1>)) &&
+        room(delta_join_rows_kernel<2>, sizeof(RowsShared<2>)) &&
         prepare_delta_prep() == cudaSuccess &&
         cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
       g_ready[dev] = 1;
@@ -1658,7 +1704,7 @@ Plan make_plan(int B, int Hv, int N, int dk, int dv, int n_seq, bool packed) {
   // of L and P 2.65, on one SM; beginnings 10 and 12; a join step 1.0 with four rows
   // per CTA, 1.8 with eight, 2.0 by tiles, and 5 to begin.
   const long long units = (long long)(packed ? 1 : B) * Hv * tiles;
-  const double join = packed || units * 16 > kSms ? 2.0 : units * 32 > kSms ? 1.8 : 1.0;
+  const double join = packed || units * 4 > kSms ? 2.0 : units * 8 > kSms ? 1.2 : 0.8;
   auto rounds = [](double items) { return (double)(long long)((items + kSms - 1) / kSms); };
   double best = 0.0;
   p.seg_chunks = nc;
@@ -1835,8 +1881,8 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
     // by rows where that still fits the card at once
     const long long tiles = (long long)a.n_seq * a.Hv * p.tiles;
     const cudaError_t e =
-        !packed && tiles * 32 <= sms   ? launch_rows<4>(j, a.stream)
-        : !packed && tiles * 16 <= sms ? launch_rows<8>(j, a.stream)
+        !packed && tiles * 8 <= sms   ? launch_rows<1>(j, a.stream)
+        : !packed && tiles * 4 <= sms ? launch_rows<2>(j, a.stream)
                                        : launch_behind(delta_join_kernel, (unsigned)tiles, kJoinThreads,
                                                        kJoinSmem, a.stream, j);
     if (e != cudaSuccess) return TTT_ERR_CUDA;

@@ -7,7 +7,7 @@
 //     T    = (1 + A)^-1 diag(beta),  A_ij = beta_i D_ij k_i . k_j  (i > j)
 // each as a pair of bf16 tiles in the layout of the second kernel's MMAs.
 //
-// The inverse: the four 16 x 16 diagonal blocks by substitution, a warp each, a
+// The inverse: the four 16 x 16 diagonal blocks by substitution, two of them a warp, a
 // column per lane; then joined, T_21 = -T_22 A_21 T_11, first to 32 and then to
 // 64, by products of 16 x 16 blocks on mma.sync tf32 with both operands in two
 // parts (fp32 accuracy; the smallest tcgen05 product has 64 rows).

@@ -262,6 +262,8 @@ SPLITS = [
     (1, 3, 6, 1290, 96, 72),
     (1, 2, 4, 1500, 64, 64),
     (1, 1, 8, 1300, 40, 136),
+    (1, 6, 24, 2500, 128, 64),
+    (1, 20, 20, 3000, 64, 256),
 ]
 
 
