@@ -28,9 +28,9 @@
 // the state's next pairs), with a conversion by the warps between any two.  A step
 // takes 2.25 us, of which the tensor pipe works 47% (2690 cycles of products, in
 // pairs); one more order of products to fill the gaps (two MMA warps, other
-// hand-overs) was slower.  B 4, H 4, 8192 tokens, d 128: 149 us (prep 32, L and P
-// 54, join 24, outputs 46, their ends overlapping), token by token 1.7 ms; one
-// sequence of 131072 tokens, 4 heads: 428 us (97, 156, 46, 136).
+// hand-overs) was slower.  B 4, H 4, 8192 tokens, d 128: 139 us (prep 32, L and P
+// 54, join 14, outputs 46, their ends overlapping), token by token 1.7 ms; one
+// sequence of 131072 tokens, 4 heads: 421 us (97, 156, 41, 136).
 //
 // Roles (512 threads, one CTA per SM, persistent over (segment, head, d_v tile)):
 //   warp 0      TMA: q, k, v in three stages, the chunk's records in two.
@@ -1229,7 +1229,7 @@ __device__ __forceinline__ int choose_segments(int nc, int n_seq, int least, int
       const float mean = (items * step + left * units) / kSms;
       const float steps = fmaxf(fmaxf(rounds * step + behind, 1.03f * mean + 0.5f), most + 0.6f);
       cost[c] = 10.f + 2.25f * steps +
-                (items > 0.f ? 12.f + 2.65f * rounds * step + 5.f + 2.f * hops : 5.f);
+                (items > 0.f ? 12.f + 2.65f * rounds * step + 5.f + 2.3f * hops : 5.f);
     }
   }
   __syncthreads();
@@ -1490,7 +1490,9 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
 // The same for few heads: a CTA takes 16 MT rows, so that a head's step is spread over
 // 8 / MT SMs (one SM moves 192 KB in a step above).  Warp w makes columns 16 w .. of the
 // next state from S's pairs in shared memory and P's, on mma.sync (tcgen05 has no
-// product of 16 rows), and keeps them as fp32; P in three places, two ahead.  (HOPS)
+// product of 16 rows), and keeps them as fp32; P in three places, two ahead.  A step
+// takes 0.95 to 1.05 us (MT = 2: 1.8), bound by the reads of shared memory (the load-store
+// pipe 65% busy, the tensor pipe 35%); on the CUDA cores four rows took 1.0, eight 1.8.
 constexpr int kRowsThreads = 256;
 constexpr int kRowsStages = 3;
 constexpr int kRowStride = 136;   // of the pairs' rows: eight of them in eight bank groups
@@ -1701,10 +1703,10 @@ Plan make_plan(int B, int Hv, int N, int dk, int dv, int n_seq, bool packed) {
   const int nc = n_chunks(N);
   p.chunks = packed ? N / kC + n_seq : B * nc;
   // Chunks per segment, from measured times in us: a step with outputs 2.25 and one
-  // of L and P 2.65, on one SM; beginnings 10 and 12; a join step 1.0 with four rows
-  // per CTA, 1.8 with eight, 2.0 by tiles, and 5 to begin.
+  // of L and P 2.65, on one SM; beginnings 10 and 12; a join step 1.0 with 16 rows per
+  // CTA, 1.8 with 32, 2.3 by tiles, and 5 to begin.
   const long long units = (long long)(packed ? 1 : B) * Hv * tiles;
-  const double join = packed || units * 4 > kSms ? 2.0 : units * 8 > kSms ? 1.2 : 0.8;
+  const double join = packed || units * 4 > kSms ? 2.3 : units * 8 > kSms ? 1.8 : 1.0;
   auto rounds = [](double items) { return (double)(long long)((items + kSms - 1) / kSms); };
   double best = 0.0;
   p.seg_chunks = nc;
