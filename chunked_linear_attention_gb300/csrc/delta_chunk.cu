@@ -1227,9 +1227,11 @@ __device__ __forceinline__ int choose_segments(int nc, int n_seq, int least, int
       const float room = rounds * kSms - items, last = (float)n_seq * units;
       const float behind = items > 0.f && last > room ? fminf(lc, most) * (1.f - room / last) : 0.f;
       const float mean = (items * step + left * units) / kSms;
+      // a join's step is 8 CTAs' work, and they take one item after the other
+      const float join = fmaxf(hops, 8.f * items / kSms + 0.5f * hops);
       const float steps = fmaxf(fmaxf(rounds * step + behind, 1.03f * mean + 0.5f), most + 0.6f);
       cost[c] = 10.f + 2.25f * steps +
-                (items > 0.f ? 12.f + 2.65f * rounds * step + 5.f + 2.3f * hops : 5.f);
+                (items > 0.f ? 12.f + 2.65f * rounds * step + 5.f + join : 5.f);
     }
   }
   __syncthreads();
@@ -1532,131 +1534,147 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   extern __shared__ __align__(128) uint8_t smem_raw[];
   RowsShared<MT>& sh = *reinterpret_cast<RowsShared<MT>*>(smem_raw);
   constexpr int kParts = 8 / MT;
-  const int row0 = 16 * MT * (blockIdx.x % kParts), x = blockIdx.x / kParts;
-  const int tile = x % p.tiles, h = x / p.tiles % p.Hv, seq = x / p.tiles / p.Hv;
-  const int n = p.seg_n, seg0 = seq * n;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
-  pdl_wait();
-  bool ok = true;
-  int loaded = 0;   // by thread 0
-  auto load = [&]() {
-    uint64_t* bar = &sh.full[loaded % kRowsStages];
-    mbar_arrive_expect_tx(bar, kPBytes);
-    bulk_load_g2s(sh.P[loaded % kRowsStages],
-                  p.P + ((long long)(seg0 + loaded) * p.Hv + h) * kPBytes, kPBytes, bar);
-    ++loaded;
-  };
   if (tid == 0) {
     for (int s = 0; s < kRowsStages; ++s) mbar_init(&sh.full[s], 1);
     fence_mbar_init();
-    while (loaded < kRowsStages && loaded + 1 < n) load();
   }
-  auto place = [&](int j) {
-    return (((long long)(seg0 + j) * p.Hv + h) * p.tiles + tile) * kStateFloats;
-  };
-  // this thread's numbers: rows r, r + 8 of each 16, two columns of each 8
-  const int r = row0 + (lane >> 2), c = 16 * warp + 2 * (lane & 3);
-  auto at = [&](int row, int col) {   // in a tile between the kernels
-    return (int)state_at(row >> 5, col >> 6, (col & 63) >> 2, row & 31) * 4 + (col & 3);
-  };
-  F2 S[MT][2][2];   // [16 rows][8 columns][8 rows]
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = r + 16 * m + 8 * e, col = c + 8 * t, grow = 128 * tile + row;
-        float2 s = make_float2(0.f, 0.f);
-        if (p.S0 && grow < p.dv && col < p.dk)   // (d_k is even)
-          s = *reinterpret_cast<const float2*>(
-              p.S0 + (((long long)seq * p.Hv + h) * p.dv + grow) * p.dk + col);
-        S[m][t][e] = pack2(s.x, s.y);
-        if (p.S0) *reinterpret_cast<F2*>(p.Sseg + place(0) + at(row, col)) = S[m][t][e];
-      }
-  int waited = 0;
+  pdl_wait();
+  bool ok = true;
   // operand addresses of this lane
   const uint32_t a_at = ((lane & 7) + 8 * ((lane >> 3) & 1)) * kRowStride * 2 + 16 * (lane >> 4);
   const int b_row = (lane & 7) + 8 * ((lane >> 3) & 1), b_chunk = 2 * (warp & 3) + (lane >> 4);
   const uint32_t b_at = (warp >> 2) * 16384 + b_row * 128 + ((b_chunk ^ (b_row & 7)) << 4);
+  auto at = [&](int row, int col) {   // in a tile between the kernels
+    return (int)state_at(row >> 5, col >> 6, (col & 63) >> 2, row & 31) * 4 + (col & 3);
+  };
+  const int items = (p.counts ? p.counts[2] : p.seqs) * p.Hv * p.tiles * kParts;
+  int done = 0;     // steps of the items before
+  int loaded = 0;   // of P, in all, by thread 0
 #pragma unroll 1
-  for (int j = 0; j + 1 < n; ++j) {
-    F2 L[MT][2][2];
+  for (int i = blockIdx.x; i < items; i += gridDim.x) {
+    const int row0 = 16 * MT * (i % kParts), x = i / kParts;
+    const int tile = x % p.tiles, h = x / p.tiles % p.Hv, k0 = x / p.tiles / p.Hv;
+    const int seg0 = p.segs ? p.joins[k0] : k0 * p.seg_n;
+    const int seq = p.segs ? p.segs[seg0].seq : k0, n = p.segs ? p.segs[seg0].n : p.seg_n;
+    auto load = [&]() {
+      uint64_t* bar = &sh.full[loaded % kRowsStages];
+      mbar_arrive_expect_tx(bar, kPBytes);
+      bulk_load_g2s(sh.P[loaded % kRowsStages],
+                    p.P + ((long long)(seg0 + loaded - done) * p.Hv + h) * kPBytes, kPBytes, bar);
+      ++loaded;
+    };
+    __syncthreads();   // everyone is done with the item before, and sees the barriers
+    if (tid == 0 && ok) {
+      if (done > 0) fence_proxy_async_smem();
+      while (loaded < done + kRowsStages && loaded + 1 < done + n) load();
+    }
+    auto place = [&](int j) {
+      return (((long long)(seg0 + j) * p.Hv + h) * p.tiles + tile) * kStateFloats;
+    };
+    // this thread's numbers: rows r, r + 8 of each 16, two columns of each 8
+    const int r = row0 + (lane >> 2), c = 16 * warp + 2 * (lane & 3);
+    F2 S[MT][2][2];   // [16 rows][8 columns][8 rows]
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int row = r + 16 * m + 8 * e, col = c + 8 * t;
-          L[m][t][e] = *reinterpret_cast<const F2*>(p.L + place(j) + at(row, col));
-          uint32_t hi, lo;
-          split2(S[m][t][e], hi, lo);
-          const int o = (row - row0) * kRowStride + col;
-          *reinterpret_cast<uint32_t*>(&sh.A[j & 1][0][o]) = hi;
-          *reinterpret_cast<uint32_t*>(&sh.A[j & 1][1][o]) = lo;
+          const int row = r + 16 * m + 8 * e, col = c + 8 * t, grow = 128 * tile + row;
+          float2 s = make_float2(0.f, 0.f);
+          if (p.S0 && grow < p.dv && col < p.dk)   // (d_k is even)
+            s = *reinterpret_cast<const float2*>(
+                p.S0 + (((long long)seq * p.Hv + h) * p.dv + grow) * p.dk + col);
+          S[m][t][e] = pack2(s.x, s.y);
+          if (p.S0) *reinterpret_cast<F2*>(p.Sseg + place(0) + at(row, col)) = S[m][t][e];
         }
-    __syncthreads();
-    if (tid == 0 && j > 0 && loaded + 1 < n && ok) {   // everyone is done with P_{j-1}
-      fence_proxy_async_smem();
-      load();
-    }
-    if (ok) waited = j;
-    wait_w(ok, &sh.full[j % kRowsStages], (j / kRowsStages) & 1, p.status, p.wait_ns);
-    const uint32_t P = smem_u32(sh.P[j % kRowsStages]) + b_at;
-    const uint32_t Ah = smem_u32(sh.A[j & 1][0]) + a_at, Al = smem_u32(sh.A[j & 1][1]) + a_at;
-    float acc[MT][2][3][4];
+#pragma unroll 1
+    for (int j = 0; j + 1 < n; ++j, ++done) {
+      F2 L[MT][2][2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
+          for (int e = 0; e < 2; ++e) {
+            const int row = r + 16 * m + 8 * e, col = c + 8 * t;
+            L[m][t][e] = *reinterpret_cast<const F2*>(p.L + place(j) + at(row, col));
+            uint32_t hi, lo;
+            split2(S[m][t][e], hi, lo);
+            const int o = (row - row0) * kRowStride + col;
+            *reinterpret_cast<uint32_t*>(&sh.A[done & 1][0][o]) = hi;
+            *reinterpret_cast<uint32_t*>(&sh.A[done & 1][1][o]) = lo;
+          }
+      __syncthreads();
+      // everyone is done with the step before: its P's place takes the next one
+      if (tid == 0 && ok && j > 0 && loaded - done + j + 1 < n) {
+        fence_proxy_async_smem();
+        const int to = loaded % kRowsStages;
+        mbar_arrive_expect_tx(&sh.full[to], kPBytes);
+        bulk_load_g2s(sh.P[to], p.P + ((long long)(seg0 + loaded - done + j) * p.Hv + h) * kPBytes,
+                      kPBytes, &sh.full[to]);
+        ++loaded;
+      }
+      wait_w(ok, &sh.full[done % kRowsStages], (done / kRowsStages) & 1, p.status, p.wait_ns);
+      const uint32_t P = smem_u32(sh.P[done % kRowsStages]) + b_at;
+      const uint32_t Ah = smem_u32(sh.A[done & 1][0]) + a_at, Al = smem_u32(sh.A[done & 1][1]) + a_at;
+      float acc[MT][2][3][4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[m][t][q][e] = 0.f;
-    __syncwarp();
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      uint32_t bh[4], bl[4];
-      ldmatrix4_t(bh, P + k * 16 * 128);
-      ldmatrix4_t(bl, P + kPBytes / 2 + k * 16 * 128);
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        uint32_t ah[4], al[4];
-        ldmatrix4(ah, Ah + (16 * m * kRowStride + 16 * k) * 2);
-        ldmatrix4(al, Al + (16 * m * kRowStride + 16 * k) * 2);
+          for (int q = 0; q < 3; ++q)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          mma_bf16(acc[m][t][0], al, bh[2 * t], bh[2 * t + 1]);
-          mma_bf16(acc[m][t][1], ah, bl[2 * t], bl[2 * t + 1]);
-          mma_bf16(acc[m][t][2], ah, bh[2 * t], bh[2 * t + 1]);
+            for (int e = 0; e < 4; ++e) acc[m][t][q][e] = 0.f;
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        uint32_t bh[4], bl[4];
+        ldmatrix4_t(bh, P + k * 16 * 128);
+        ldmatrix4_t(bl, P + kPBytes / 2 + k * 16 * 128);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          uint32_t ah[4], al[4];
+          ldmatrix4(ah, Ah + (16 * m * kRowStride + 16 * k) * 2);
+          ldmatrix4(al, Al + (16 * m * kRowStride + 16 * k) * 2);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            mma_bf16(acc[m][t][0], al, bh[2 * t], bh[2 * t + 1]);
+            mma_bf16(acc[m][t][1], ah, bl[2 * t], bl[2 * t + 1]);
+            mma_bf16(acc[m][t][2], ah, bh[2 * t], bh[2 * t + 1]);
+          }
         }
       }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float(&q)[3][4] = acc[m][t];
+            const F2 low =
+                add2(pack2(q[0][2 * e], q[0][2 * e + 1]), pack2(q[1][2 * e], q[1][2 * e + 1]));
+            S[m][t][e] = add2(L[m][t][e], add2(low, pack2(q[2][2 * e], q[2][2 * e + 1])));
+            if (ok)
+              *reinterpret_cast<F2*>(p.Sseg + place(j + 1) + at(r + 16 * m + 8 * e, c + 8 * t)) =
+                  S[m][t][e];
+          }
     }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float(&q)[3][4] = acc[m][t];
-          const F2 low = add2(pack2(q[0][2 * e], q[0][2 * e + 1]), pack2(q[1][2 * e], q[1][2 * e + 1]));
-          S[m][t][e] = add2(L[m][t][e], add2(low, pack2(q[2][2 * e], q[2][2 * e + 1])));
-          if (ok)
-            *reinterpret_cast<F2*>(p.Sseg + place(j + 1) + at(r + 16 * m + 8 * e, c + 8 * t)) =
-                S[m][t][e];
-        }
   }
-  if (tid == 0 && !ok)   // copies still on their way into this CTA's shared memory
-    for (int j = waited; j < loaded; ++j)
+  // copies still on their way into this CTA's shared memory
+  if (tid == 0 && !ok)
+    for (int j = loaded > kRowsStages ? loaded - kRowsStages : 0; j < loaded; ++j)
       mbar_wait(&sh.full[j % kRowsStages], (j / kRowsStages) & 1, p.status, p.wait_ns);
 }
 
 template <int MT>
-cudaError_t launch_rows(const JoinParams& j, cudaStream_t stream) {
-  return launch_behind(delta_join_rows_kernel<MT>, j.seqs * j.Hv * j.tiles * (8 / MT), kRowsThreads,
-                       sizeof(RowsShared<MT>), stream, j);
+cudaError_t launch_rows(const JoinParams& j, int sms, cudaStream_t stream) {
+  const long long items = (long long)j.seqs * j.Hv * j.tiles * (8 / MT);
+  return launch_behind(delta_join_rows_kernel<MT>, (unsigned)(items < sms ? items : sms),
+                       kRowsThreads, sizeof(RowsShared<MT>), stream, j);
 }
 
 int g_ready[64] = {0};   // 0 unknown, 1 usable, 2 not usable
@@ -1706,7 +1724,7 @@ Plan make_plan(int B, int Hv, int N, int dk, int dv, int n_seq, bool packed) {
   // of L and P 2.65, on one SM; beginnings 10 and 12; a join step 1.0 with 16 rows per
   // CTA, 1.8 with 32, 2.3 by tiles, and 5 to begin.
   const long long units = (long long)(packed ? 1 : B) * Hv * tiles;
-  const double join = packed || units * 4 > kSms ? 2.3 : units * 8 > kSms ? 1.8 : 1.0;
+  const double join = packed || units * 8 <= kSms ? 1.0 : units * 4 <= kSms ? 1.8 : 2.3;
   auto rounds = [](double items) { return (double)(long long)((items + kSms - 1) / kSms); };
   double best = 0.0;
   p.seg_chunks = nc;
@@ -1880,11 +1898,13 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
     const double states = (double)pl.seg_places * a.Hv * a.dk;
     ProfScope ps(PT_DELTA_JOIN, a.stream, 2.0 * states * a.dk * a.dv,
                  4.0 * states * (a.dk + 2 * a.dv));
-    // by rows where that still fits the card at once
+    // by rows where that still fits the card at once, and for packed sequences, of which
+    // a few long ones have most of the steps (5 sequences of 20011 tokens, 8 heads: 173 to
+    // 177 us, by tiles 185 to 199; 64 sequences of 30000, 4 heads: 111 to 150 and 113 to 147)
     const long long tiles = (long long)a.n_seq * a.Hv * p.tiles;
     const cudaError_t e =
-        !packed && tiles * 8 <= sms   ? launch_rows<1>(j, a.stream)
-        : !packed && tiles * 4 <= sms ? launch_rows<2>(j, a.stream)
+        packed || tiles * 8 <= sms ? launch_rows<1>(j, sms, a.stream)
+        : tiles * 4 <= sms         ? launch_rows<2>(j, sms, a.stream)
                                        : launch_behind(delta_join_kernel, (unsigned)tiles, kJoinThreads,
                                                        kJoinSmem, a.stream, j);
     if (e != cudaSuccess) return TTT_ERR_CUDA;
