@@ -18,6 +18,8 @@
 // fp32 residual and both norms 67 us (6.4 TB/s); a single row 4 us.  Longer rows
 // reach 3.6 to 4.8 TB/s (fewer CTAs per SM to run past each other's barriers), ones
 // of unaligned length 1.2 to 1.6 (an element per access, and issue is the bound).
+#include <atomic>
+
 #include "delta_tc.cuh"
 #include "prof.h"
 
@@ -387,11 +389,14 @@ __global__ void __launch_bounds__(kMaxThreads<VEC, VPT, PARTS, KEEP>, kMinCtas<P
 template <typename T, typename TS, int VEC, int VPT, int PARTS, bool KEEP>
 int launch_parts(const BlockNormArgs& a, NormParams p) {
   auto kern = block_norm_kernel<T, TS, VEC, VPT, PARTS, KEEP>;
-  static const int regs = [&] {
+  static std::atomic<int> known{0};   // the kernel's registers, once a call has found them
+  int regs = known.load(std::memory_order_relaxed);
+  if (regs == 0) {
     cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
-  }();
-  if (regs == 0) return TTT_ERR_CUDA;
+    if (cudaFuncGetAttributes(&at, kern) != cudaSuccess) return TTT_ERR_CUDA;
+    regs = at.numRegs;
+    known.store(regs, std::memory_order_relaxed);
+  }
   p.pieces = a.D / VEC;
   p.gpieces = a.group / VEC;
   p.P = 1;
