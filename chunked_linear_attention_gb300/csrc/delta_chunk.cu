@@ -1230,8 +1230,8 @@ __device__ __forceinline__ int choose_segments(int nc, int n_seq, int least, int
       // a join's step is 8 CTAs' work, and they take one item after the other
       const float join = fmaxf(hops, 8.f * items / kSms + 0.5f * hops);
       const float steps = fmaxf(fmaxf(rounds * step + behind, 1.03f * mean + 0.5f), most + 0.6f);
-      cost[c] = 10.f + 2.25f * steps +
-                (items > 0.f ? 12.f + 2.65f * rounds * step + 5.f + join : 5.f);
+      cost[c] = 1.f + 2.25f * steps +
+                (items > 0.f ? 5.f + 2.65f * rounds * step + 5.f + join : 4.f);
     }
   }
   __syncthreads();
@@ -1721,8 +1721,11 @@ Plan make_plan(int B, int Hv, int N, int dk, int dv, int n_seq, bool packed) {
   const int nc = n_chunks(N);
   p.chunks = packed ? N / kC + n_seq : B * nc;
   // Chunks per segment, from measured times in us: a step with outputs 2.25 and one
-  // of L and P 2.65, on one SM; beginnings 10 and 12; a join step 1.0 with 16 rows per
-  // CTA, 1.8 with 32, 2.3 by tiles, and 5 to begin.
+  // of L and P 2.65, on one SM; a join step 1.0 with 16 rows per CTA, 1.8 with 32, 2.3 by
+  // tiles; beginnings 1 (most of it beside the kernel before), 5, 5 and, by tiles, 10.
+  // 1024 tokens take 41.0 us in segments and 47.4 whole with 4 heads, 55.2 and 53.5 with
+  // 32; 4096 tokens 82 (nine segments) and 100 (five) with 16 heads, 181 and 191 (whole)
+  // with 48.
   const long long units = (long long)(packed ? 1 : B) * Hv * tiles;
   const double join = packed || units * 8 <= kSms ? 1.0 : units * 4 <= kSms ? 1.8 : 2.3;
   auto rounds = [](double items) { return (double)(long long)((items + kSms - 1) / kSms); };
@@ -1732,8 +1735,8 @@ Plan make_plan(int B, int Hv, int N, int dk, int dv, int n_seq, bool packed) {
     const int lc = (nc + n - 1) / n;
     double t, hops = n - 1;
     if (!packed) {   // sequences of one length: whole rounds of the SMs
-      t = 10.0 + 2.25 * rounds((double)units * n) * (lc + 1);
-      if (n > 1) t += 12.0 + 2.65 * rounds((double)units * (n - 1)) * (lc + 1);
+      t = 1.0 + 2.25 * rounds((double)units * n) * (lc + 1);
+      if (n > 1) t += 5.0 + 2.65 * rounds((double)units * (n - 1)) * (lc + 1);
     } else {
       // lengths unknown: of n_seq sequences half a segment is left over each, and the
       // longest is about four times the mean.  The plan kernel sees them and may cut
@@ -1744,10 +1747,10 @@ Plan make_plan(int B, int Hv, int N, int dk, int dv, int n_seq, bool packed) {
       if (whole < hops) whole = hops;
       if (hops < 1.0) whole = 0.0;
       const double left = longest < lc ? longest : 0.75 * lc + 1.5;
-      t = 10.0 + 2.25 * (rounds(units * whole) * (lc + 1) + rounds((double)units * n_seq) * left);
-      if (whole > 0.0) t += 12.0 + 2.65 * rounds(units * whole) * (lc + 1);
+      t = 1.0 + 2.25 * (rounds(units * whole) * (lc + 1) + rounds((double)units * n_seq) * left);
+      if (whole > 0.0) t += 5.0 + 2.65 * rounds(units * whole) * (lc + 1);
     }
-    if (hops >= 1.0) t += 5.0 + join * hops;
+    if (hops >= 1.0) t += (join > 2.0 ? 10.0 : 5.0) + join * hops;
     if (n == 1 || t < best) {
       best = t;
       p.seg_chunks = lc;
