@@ -63,6 +63,8 @@ size_t delta_rule_workspace_size(int B, int Hk, int Hv, int N, int d_k, int d_v,
  *               the device status word (ttt_device_status); other sequences
  *               that overlap around such entries have undefined results
  *               (nothing outside the tensors is touched).
+ *               They are read on the device: a captured call may be replayed
+ *               with other bounds.
  *   scale       factor of the outputs (d_k^-1/2 is usual).
  *   layout      HOST pointer or NULL.
  *   out         [B, Hv, N, d_v] in io_dtype.  May not overlap an input, nor

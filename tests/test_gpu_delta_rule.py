@@ -336,6 +336,29 @@ def test_packed_lengths_that_are_cut_differently(lens):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_captured_packed_call_with_other_lengths():
+    """A captured packed call is planned on the device: replayed with other
+    bounds it equals a call made with them."""
+    cla = lib()
+    N = 3000
+    t = inputs(54, 1, 1, 2, N, 128, 128, torch.bfloat16, 0.02)
+    S0 = torch.randn(4, 2, 128, 128, generator=torch.Generator().manual_seed(55)) * 0.3
+    packs = ([0, 700, 1400, 2200, 3000], [0, 10, 10, 2950, 2951], [5, 2900, 2930, 2964, 3000])
+    want = [run(cla, t, S0, p) for p in packs]
+    dev, S0d = [x.to(DEV) for x in t], S0.to(DEV)
+    starts = torch.tensor(packs[0], dtype=torch.int32, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, S = cla.delta_rule_chunked_forward(*dev, S0=S0d, seq_starts=starts)
+    for p, (ro, rS) in zip(packs[::-1], want[::-1]):
+        starts.copy_(torch.tensor(p, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(S, rS)
+        assert torch.equal(o[:, :, p[0]:p[-1]], ro[:, :, p[0]:p[-1]])
+    check(cla, want[1], oracle(t, S0, packs[1]), torch.bfloat16)
+
+
 def test_zero_length_axis_edges_and_one_token_sequences():
     """A packed batch of single tokens, and one in which every sequence is
     empty: outputs untouched, states unchanged."""
