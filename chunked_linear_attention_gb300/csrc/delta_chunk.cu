@@ -1549,6 +1549,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   auto at = [&](int row, int col) {   // in a tile between the kernels
     return (int)state_at(row >> 5, col >> 6, (col & 63) >> 2, row & 31) * 4 + (col & 3);
   };
+  const bool small = p.dk <= 64;
   const int items = (p.counts ? p.counts[2] : p.seqs) * p.Hv * p.tiles * kParts;
   int done = 0;     // steps of the items before
   int loaded = 0;   // of P, in all, by thread 0
@@ -1558,17 +1559,23 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     const int tile = x % p.tiles, h = x / p.tiles % p.Hv, k0 = x / p.tiles / p.Hv;
     const int seg0 = p.segs ? p.joins[k0] : k0 * p.seg_n;
     const int seq = p.segs ? p.segs[seg0].seq : k0, n = p.segs ? p.segs[seg0].n : p.seg_n;
-    auto load = [&]() {
+    auto load = [&](int j) {   // d_k up to 64: the first quarter of hi and of lo
       uint64_t* bar = &sh.full[loaded % kRowsStages];
-      mbar_arrive_expect_tx(bar, kPBytes);
-      bulk_load_g2s(sh.P[loaded % kRowsStages],
-                    p.P + ((long long)(seg0 + loaded - done) * p.Hv + h) * kPBytes, kPBytes, bar);
+      uint8_t* to = sh.P[loaded % kRowsStages];
+      const uint8_t* from = p.P + ((long long)(seg0 + j) * p.Hv + h) * kPBytes;
+      mbar_arrive_expect_tx(bar, small ? 2 * kBlk : kPBytes);
+      if (small) {
+        bulk_load_g2s(to, from, kBlk, bar);
+        bulk_load_g2s(to + kPBytes / 2, from + kPBytes / 2, kBlk, bar);
+      } else {
+        bulk_load_g2s(to, from, kPBytes, bar);
+      }
       ++loaded;
     };
     __syncthreads();   // everyone is done with the item before, and sees the barriers
     if (tid == 0 && ok) {
       if (done > 0) fence_proxy_async_smem();
-      while (loaded < done + kRowsStages && loaded + 1 < done + n) load();
+      while (loaded < done + kRowsStages && loaded + 1 < done + n) load(loaded - done);
     }
     auto place = [&](int j) {
       return (((long long)(seg0 + j) * p.Hv + h) * p.tiles + tile) * kStateFloats;
@@ -1611,11 +1618,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       // everyone is done with the step before: its P's place takes the next one
       if (tid == 0 && ok && j > 0 && loaded - done + j + 1 < n) {
         fence_proxy_async_smem();
-        const int to = loaded % kRowsStages;
-        mbar_arrive_expect_tx(&sh.full[to], kPBytes);
-        bulk_load_g2s(sh.P[to], p.P + ((long long)(seg0 + loaded - done + j) * p.Hv + h) * kPBytes,
-                      kPBytes, &sh.full[to]);
-        ++loaded;
+        load(loaded - done + j);
       }
       wait_w(ok, &sh.full[done % kRowsStages], (done / kRowsStages) & 1, p.status, p.wait_ns);
       const uint32_t P = smem_u32(sh.P[done % kRowsStages]) + b_at;
@@ -1632,6 +1635,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       __syncwarp();
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
+        if (small && (k == 4 || warp >= 4)) break;   // zeros
         uint32_t bh[4], bl[4];
         ldmatrix4_t(bh, P + k * 16 * 128);
         ldmatrix4_t(bl, P + kPBytes / 2 + k * 16 * 128);
