@@ -151,3 +151,46 @@ def test_rule_then_norm():
         B, N, -1), scale=t2["scale"].to(DEV), w_next=t2["w_next"].to(DEV))
     t2["y"] = m.reshape(B * N, -1).cpu()
     check((got[0].reshape(B * N, -1), got[1].reshape(B * N, -1)), want(t2, H * d), BF, F32)
+
+
+def test_a_captured_layer_between_copies():
+    """Rule, token and norm captured behind copies and fills, with copies
+    behind them, replayed on new inputs."""
+    cla = lib()
+    from tests.test_gpu_delta_rule import inputs
+    B, H, N, d = 2, 2, 150, 128
+    sets = [[x.to(DEV) for x in inputs(s, B, H, H, N + 1, d, d, BF)] for s in (60, 61)]
+    hold = [torch.empty_like(x) for x in sets[0]]
+    keep = torch.empty(B, H * d, dtype=BF, device=DEV)
+    state = torch.empty(B, H, d, d, device=DEV)
+    saved = torch.empty_like(state)
+
+    def layer(src):
+        for x, y in zip(hold, src):
+            x.copy_(y)
+        state.zero_()
+        o, _ = cla.delta_rule_chunked_forward(*[x[:, :, :N] for x in hold], S0=state, S_final=state)
+        o1 = cla.delta_rule_step(*[x[:, :, N] for x in hold], state)
+        n, _ = cla.block_norm_forward(o1.view(B, H * d), group=d)
+        keep.copy_(n)
+        saved.copy_(state)
+
+    want = []
+    for s in sets:
+        layer(s)
+        want.append((keep.clone(), saved.clone()))
+    stage = [x.clone() for x in sets[0]]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer(stage)
+    for i in (1, 0, 1):
+        for x, y in zip(stage, sets[i]):
+            x.copy_(y)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(keep, want[i][0]) and torch.equal(saved, want[i][1])
+    ro, rS = DO.delta_rule(*[f64(x) for x in sets[1]])
+    assert rel_l2(f64(saved), rS) <= 3.9e-5 + 1e-5
+    ref, _ = DO.block_norm(ro[:, :, N].reshape(B, H * d), group=d)
+    assert rel_l2(f64(keep), ref) <= 2 * (2.0 ** -8 + 4e-5)
