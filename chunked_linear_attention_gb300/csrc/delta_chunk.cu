@@ -29,7 +29,7 @@
 // takes 2.25 us, of which the tensor pipe works 47% (2690 cycles of products, in
 // pairs); one more order of products to fill the gaps (two MMA warps, other
 // hand-overs) was slower.  B 4, H 4, 8192 tokens, d 128: 139 us (prep 32, L and P
-// 54, join 14, outputs 46, their ends overlapping), token by token 1.7 ms; one
+// 54, join 14, outputs 46, their ends overlapping), token by token 1.6 ms; one
 // sequence of 131072 tokens, 4 heads: 421 us (97, 156, 41, 136).
 //
 // Roles (512 threads, one CTA per SM, persistent over (segment, head, d_v tile)):

@@ -8,6 +8,8 @@
 // tokens.  With S the state before the token, both products of a token are
 // taken from it at once, S k and S q (o = scale (a S q + u (k . q))), so a
 // token costs one butterfly over L lanes and not two in a row.
+#include <type_traits>
+
 #include "delta_tc.cuh"
 #include "prof.h"
 
@@ -42,15 +44,38 @@ __device__ __forceinline__ void seq_range(const int* starts, int s, int N, int* 
   len = ok ? b - a : 0;
 }
 
+// Numbers one at a time, or two in one register for the packed instructions.
+__device__ __forceinline__ float fma_(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ F2 fma_(F2 a, F2 b, F2 c) { return fma2(a, b, c); }
+__device__ __forceinline__ float mul_(float a, float b) { return a * b; }
+__device__ __forceinline__ F2 mul_(F2 a, F2 b) { return mul2(a, b); }
+__device__ __forceinline__ void all_(float& v, float x) { v = x; }
+__device__ __forceinline__ void all_(F2& v, float x) { v = pack2(x, x); }
+__device__ __forceinline__ float sum_(const float (&a)[4]) { return (a[0] + a[1]) + (a[2] + a[3]); }
+__device__ __forceinline__ float sum_(const F2 (&a)[2]) {
+  float x, y;
+  unpack2(add2(a[0], a[1]), x, y);
+  return x + y;
+}
+__device__ __forceinline__ void four(float* v, const float* p) {
+  *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p);
+}
+__device__ __forceinline__ void four(F2* v, const float* p) {
+  const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(p);
+  v[0] = x.x;
+  v[1] = x.y;
+}
+
 // ------------------------------------------------------------ whole sequences
 // One CTA: 16 rows of one (sequence, head): four warps compute, four more bring
 // the next TT tokens' k, q, v (as fp32), decay, beta and k . q into the other half
 // of the shared memory.  Bound by the chain of a token (two dot products, a
 // butterfly, the update), hidden in part by the other CTA of the SM: in fp32 B 4,
-// H 4, 8192 tokens take 1.66 ms at d 128 (0.20 us a token, 16 CTAs' rows of 16
+// H 4, 8192 tokens take 1.61 ms at d 128 (0.20 us a token, 16 CTAs' rows of 16
 // fill 128 SMs), 256 tokens of one head 31 us at d 32 and 58 at d 128.  With d_k of
-// 256, two CTAs per SM (128 registers) take 1.0 ms for 2048 tokens and one 1.34; of
-// 512, four rows a thread 1.2 ms for 512 tokens (0.6 us a token) and two 1.5.
+// 256, two CTAs per SM (128 registers) take 0.86 ms for 2048 tokens (before the packed
+// instructions 1.00, and one CTA 1.34); of 512, four rows a thread 1.04 ms for 512 tokens
+// and two 1.5 (held to registers for one block by the launch bounds, 1.60).
 constexpr int kRecWarps = 4;
 
 struct RecParams {
@@ -70,7 +95,7 @@ struct RecParams {
 };
 
 template <typename T, int L, int E, int R, int TT>
-__global__ void __launch_bounds__(256, R < 4 ? 2 : 1)
+__global__ void __launch_bounds__(256, R < 4 ? 2 : 0)
     delta_recurrent_kernel(const __grid_constant__ RecParams p) {
   constexpr int W = L * E;                         // padded d_k
   constexpr int ROWS = kRecWarps * (32 / L) * R;   // rows of this CTA
@@ -145,7 +170,11 @@ __global__ void __launch_bounds__(256, R < 4 ? 2 : 1)
   };
 
   const int l = lane % L;
-  float S[R][E];
+  // Packed from 8 elements a lane on (64 heads, 4096 tokens: d 128 2.49 -> 2.26 ms, d 64 825
+  // -> 792 us; with 4, 64 heads of d 32 and 2048 tokens, 236 -> 244 us).
+  using V = std::conditional_t<(E >= 8), F2, float>;
+  constexpr int PW = sizeof(V) / 4, NA = 4 / PW;
+  V S[R][E / PW];
   int row[R];
   bool mine[R];   // this lane stores the row's outputs
   T* op = out + row0 + warp * R * (32 / L) + lane / L;
@@ -156,11 +185,22 @@ __global__ void __launch_bounds__(256, R < 4 ? 2 : 1)
       row[r] = (warp * R + r) * (32 / L) + lane / L;
       mine[r] = l == 0 && row0 + row[r] < p.dv;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int c = elem<L>(l, e);
-        S[r][e] = p.S0 && row0 + row[r] < p.dv && c < p.dk
-                      ? p.S0[sbase + (long long)(row0 + row[r]) * p.dk + c]
-                      : 0.f;
+      for (int e = 0; e < E; e += 4) {
+        float s[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = elem<L>(l, e + i);
+          s[i] = p.S0 && row0 + row[r] < p.dv && c < p.dk
+                     ? p.S0[sbase + (long long)(row0 + row[r]) * p.dk + c]
+                     : 0.f;
+        }
+        if constexpr (PW == 2) {
+          S[r][e / 2] = pack2(s[0], s[1]);
+          S[r][e / 2 + 1] = pack2(s[2], s[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) S[r][e + i] = s[i];
+        }
       }
     }
   } else if (ntile > 0) {
@@ -174,15 +214,15 @@ __global__ void __launch_bounds__(256, R < 4 ? 2 : 1)
     } else {
       const int n = min(TT, len - it * TT);
       // a token's operands are read while the one before it is worked on
-      float kk[E], qq[E], vv[R];
+      V kk[E / PW], qq[E / PW];
+      float vv[R];
       float4 f;
       const float* d = stage + buf * TT * TOK;
       auto fetch = [&]() {
 #pragma unroll
         for (int e = 0; e < E; e += 4) {
-          *reinterpret_cast<float4*>(&kk[e]) = *reinterpret_cast<const float4*>(d + elem<L>(l, e));
-          *reinterpret_cast<float4*>(&qq[e]) =
-              *reinterpret_cast<const float4*>(d + W + elem<L>(l, e));
+          four(&kk[e / PW], d + elem<L>(l, e));
+          four(&qq[e / PW], d + W + elem<L>(l, e));
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) vv[r] = d[2 * W + row[r]];
@@ -192,22 +232,23 @@ __global__ void __launch_bounds__(256, R < 4 ? 2 : 1)
       fetch();
 #pragma unroll 2
       for (int j = 0; j < n; ++j) {
-        float k0[E], v0[R], sk[R], sq[R];
+        V k0[E / PW];
+        float v0[R], sk[R], sq[R];
         const float4 f0 = f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           v0[r] = vv[r];
-          float a[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f};   // short chains
+          V a[NA] = {}, c[NA] = {};   // short chains
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            a[e & 3] = fmaf(S[r][e], kk[e], a[e & 3]);
-            c[e & 3] = fmaf(S[r][e], qq[e], c[e & 3]);
+          for (int e = 0; e < E / PW; ++e) {
+            a[e % NA] = fma_(S[r][e], kk[e], a[e % NA]);
+            c[e % NA] = fma_(S[r][e], qq[e], c[e % NA]);
           }
-          sk[r] = (a[0] + a[1]) + (a[2] + a[3]);
-          sq[r] = (c[0] + c[1]) + (c[2] + c[3]);
+          sk[r] = sum_(a);
+          sq[r] = sum_(c);
         }
 #pragma unroll
-        for (int e = 0; e < E; ++e) k0[e] = kk[e];
+        for (int e = 0; e < E / PW; ++e) k0[e] = kk[e];
         if (j + 1 < n) fetch();
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -217,8 +258,11 @@ __global__ void __launch_bounds__(256, R < 4 ? 2 : 1)
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const float u = f0.y * (v0[r] - f0.x * sk[r]);
+          V uu, decay;
+          all_(uu, u);
+          all_(decay, f0.x);
 #pragma unroll
-          for (int e = 0; e < E; ++e) S[r][e] = fmaf(u, k0[e], f0.x * S[r][e]);
+          for (int e = 0; e < E / PW; ++e) S[r][e] = fma_(uu, k0[e], mul_(decay, S[r][e]));
           if (mine[r]) op[32 / L * r] = from_f<T>(p.scale * fmaf(u, f0.z, f0.x * sq[r]));
         }
         op += p.lay.out.token;
@@ -230,10 +274,16 @@ __global__ void __launch_bounds__(256, R < 4 ? 2 : 1)
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int c = elem<L>(l, e);
-        if (row0 + row[r] < p.dv && c < p.dk)
-          p.S_final[sbase + (long long)(row0 + row[r]) * p.dk + c] = S[r][e];
+      for (int e = 0; e < E; e += PW) {
+        float s[PW];
+        if constexpr (PW == 2) unpack2(S[r][e / 2], s[0], s[1]);
+        else s[0] = S[r][e];
+#pragma unroll
+        for (int i = 0; i < PW; ++i) {
+          const int c = elem<L>(l, e + i);
+          if (row0 + row[r] < p.dv && c < p.dk)
+            p.S_final[sbase + (long long)(row0 + row[r]) * p.dk + c] = s[i];
+        }
       }
   }
 }
