@@ -71,8 +71,8 @@ __device__ __forceinline__ void four(F2* v, const float* p) {
 // the next TT tokens' k, q, v (as fp32), decay, beta and k . q into the other half
 // of the shared memory.  Bound by the chain of a token (two dot products, a
 // butterfly, the update), hidden in part by the other CTA of the SM: in fp32 B 4,
-// H 4, 8192 tokens take 1.61 ms at d 128 (0.20 us a token, 16 CTAs' rows of 16
-// fill 128 SMs), 256 tokens of one head 31 us at d 32 and 58 at d 128.  With d_k of
+// H 4, 8192 tokens take 1.61 ms at d 128 (0.20 us a token; 128 CTAs, so most
+// SMs hold one), 256 tokens of one head 31 us at d 32 and 58 at d 128.  With d_k of
 // 256, two CTAs per SM (128 registers) take 0.86 ms for 2048 tokens (before the packed
 // instructions 1.00, and one CTA 1.34); of 512, four rows a thread 1.04 ms for 512 tokens
 // and two 1.5 (held to registers for one block by the launch bounds, 1.60).
