@@ -454,8 +454,8 @@ int launch_step(const DeltaStepArgs& a, StepParams p) {
 template <typename T, bool VEC>
 int step_t(const DeltaStepArgs& a, const StepParams& p) {
   if (a.dk <= 32) return launch_step<T, 8, 4, 2, VEC>(a, p);
-  if (a.dk <= 64) return launch_step<T, 8, 8, 2, VEC>(a, p);
-  if (a.dk <= 128) return launch_step<T, 8, 16, 1, VEC>(a, p);
+  if (a.dk <= 64) return launch_step<T, 8, 8, 4, VEC>(a, p);
+  if (a.dk <= 128) return launch_step<T, 8, 16, 2, VEC>(a, p);
   if (a.dk <= 256) return launch_step<T, 16, 16, 1, VEC>(a, p);
   return launch_step<T, 32, 16, 1, VEC>(a, p);
 }
