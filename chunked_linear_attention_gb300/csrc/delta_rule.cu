@@ -335,8 +335,11 @@ constexpr int kStepThreads = 128;
 // One CTA: 4 (32 / L) R rows of one (row of the batch, head).  The state is
 // read and written once, each thread's R E elements all in flight together; the
 // bound is HBM (the states' bytes twice).  Heads of 128 x 128: 256 rows of 32
-// heads 180 us (6.0 TB/s, 89% of a measured copy), 56 rows of 16 heads 22.5 us
-// (5.3 TB/s: beginning and end are a part of it), one row of 4 heads 4 us.
+// heads 163 us (6.6 TB/s, 99% of a measured copy), 56 rows of 16 heads 20.4 us
+// (5.8 TB/s: beginning and end are a part of it), one row of 4 heads 4 us.
+// R: 128 bytes in flight a thread and more (at d_k 128 R = 1 took 177 us, 4 167; at 64
+// one row 115 us for 512 rows of 32 heads, two 89, four 84; at 32 one 53, two 35, four
+// 41; at 256 and 512 one row 177 and 178 us, two 164).
 template <typename T, int L, int E, int R, bool VEC>
 __global__ void __launch_bounds__(kStepThreads) delta_step_kernel(
     const __grid_constant__ StepParams p) {
@@ -456,8 +459,8 @@ int step_t(const DeltaStepArgs& a, const StepParams& p) {
   if (a.dk <= 32) return launch_step<T, 8, 4, 2, VEC>(a, p);
   if (a.dk <= 64) return launch_step<T, 8, 8, 4, VEC>(a, p);
   if (a.dk <= 128) return launch_step<T, 8, 16, 2, VEC>(a, p);
-  if (a.dk <= 256) return launch_step<T, 16, 16, 1, VEC>(a, p);
-  return launch_step<T, 32, 16, 1, VEC>(a, p);
+  if (a.dk <= 256) return launch_step<T, 16, 16, 2, VEC>(a, p);
+  return launch_step<T, 32, 16, 2, VEC>(a, p);
 }
 
 }  // namespace
