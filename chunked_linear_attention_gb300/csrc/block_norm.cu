@@ -12,12 +12,12 @@
 // that divides the group's pieces, at most 32), and the group's few remaining
 // partial sums through shared memory, always in the same order.
 //
-// Measured: 65536 rows of 1536 with four gated groups, bf16, 103 us (5.8 TB/s, 87%
+// Measured: 65536 rows of 1536 with four gated groups, bf16, 101 us (6.0 TB/s, 89%
 // of a measured copy; one row per CTA, with the weights read anew for each, took
 // 197: its instructions, and not HBM, were the bound); 20011 rows of 1536 with gate,
 // fp32 residual and both norms 67 us (6.4 TB/s); a single row 4 us.  Longer rows
-// reach 3.6 to 4.8 TB/s (fewer CTAs per SM to run past each other's barriers), ones
-// of unaligned length 1.2 to 1.6 (an element per access, and issue is the bound).
+// reach 3.7 to 4.9 TB/s (fewer CTAs per SM to run past each other's barriers), ones
+// of unaligned length 1.2 to 1.7 (an element per access, and issue is the bound).
 #include <atomic>
 
 #include "delta_tc.cuh"
@@ -148,11 +148,67 @@ __device__ __forceinline__ void load_w(const float* p, bool there, float (&x)[VE
 // sigmoid(x) from the hardware exponential and reciprocal (2^-22 each; the
 // exponent's own rounding adds |x| 2^-24): the exact division would cost more
 // than the loads.  Saturates to 0 and 1.
-__device__ __forceinline__ float sigmoid_fast(float x) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+__device__ __forceinline__ float sigmoid_fast(float x) {
+  return rcp_fast(1.f + ex2(x * -1.4426950408889634f));
+}
+
+// A piece's arithmetic; PACK: eight numbers, two at a time by the packed instructions
+// (65536 rows of 1536, gated groups: 102.6 -> 100.8 us; kernels short of registers lose by
+// it, 6710 rows of 5000 167 -> 190).
+template <bool PACK, int VEC>
+__device__ __forceinline__ float sum_squares(const float (&m)[VEC], float s) {
+  if constexpr (PACK) {
+    F2 a = pack2(s, 0.f);
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const F2 x = pack2(m[j], m[j + 1]);
+      a = fma2(x, x, a);
+    }
+    float x, y;
+    unpack2(a, x, y);
+    return x + y;
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) s = fmaf(m[j], m[j], s);
+    return s;
+  }
+}
+// m *= c w
+template <bool PACK, int VEC>
+__device__ __forceinline__ void scale_by(float (&m)[VEC], float c, const float (&w)[VEC]) {
+  if constexpr (PACK) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2)
+      unpack2(mul2(pack2(m[j], m[j + 1]), mul2(pack2(c, c), pack2(w[j], w[j + 1]))), m[j], m[j + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) m[j] *= c * w[j];
+  }
+}
+// m *= sigmoid(z), or z sigmoid(z)
+template <bool PACK, int VEC>
+__device__ __forceinline__ void gate_by(float (&m)[VEC], const float (&z)[VEC], bool silu) {
+  if constexpr (PACK) {
+    constexpr float kC = -1.4426950408889634f;
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const F2 zz = pack2(z[j], z[j + 1]);
+      float a, b;
+      unpack2(mul2(zz, pack2(kC, kC)), a, b);
+      unpack2(add2(pack2(ex2(a), ex2(b)), pack2(1.f, 1.f)), a, b);
+      F2 g = pack2(rcp_fast(a), rcp_fast(b));
+      if (silu) g = mul2(g, zz);
+      unpack2(mul2(pack2(m[j], m[j + 1]), g), m[j], m[j + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) m[j] *= silu ? z[j] * sigmoid_fast(z[j]) : sigmoid_fast(z[j]);
+  }
 }
 
 // PARTS: which of gate (4), residual (2) and next norm (1) are there; -1: the
@@ -171,6 +227,7 @@ __global__ void __launch_bounds__(kMaxThreads<VEC, VPT, PARTS, KEEP>, kMinCtas<P
   const int warp = tid >> 5, lane = tid & 31, nw = p.nt >> 5, np = p.np;
   float* part = smem + ty * 2 * (np + nw);
   float* rpart = part + 2 * np;
+  constexpr bool PACK = VEC == 8 && PARTS >= 0;
   // one group: each warp makes a partial sum, whatever the group's length
   const bool one = PARTS < 0 && p.gpieces == p.pieces;
   const int per = one ? nw : p.gpieces / p.P;   // partials of a group
@@ -281,9 +338,7 @@ __global__ void __launch_bounds__(kMaxThreads<VEC, VPT, PARTS, KEEP>, kMinCtas<P
     float all = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      float ss = 0.f;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) ss = fmaf(m[i][j], m[i][j], ss);
+      float ss = sum_squares<PACK>(m[i], 0.f);
       if (one) {
         all += col(i) < p.D ? ss : 0.f;
         continue;
@@ -337,25 +392,16 @@ __global__ void __launch_bounds__(kMaxThreads<VEC, VPT, PARTS, KEEP>, kMinCtas<P
       } else {
         weights(c, f);
       }
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) m[i][j] *= inv * f[j];
+      scale_by<PACK>(m[i], inv, f);
       if (GATE) {
-        if (p.act == BLOCK_GATE_SILU) {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) m[i][j] *= z[i % G][j] * sigmoid_fast(z[i % G][j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) m[i][j] *= sigmoid_fast(z[i % G][j]);
-        }
+        if (p.act == BLOCK_GATE_SILU) gate_by<PACK>(m[i], z[i % G], true);
+        else gate_by<PACK>(m[i], z[i % G], false);
       }
       if (RES) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) m[i][j] += x[i % G][j];
       }
-      if (NEXT) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) rr = fmaf(m[i][j], m[i][j], rr);
-      }
+      if (NEXT) rr = sum_squares<PACK>(m[i], rr);
       store_vec<TS, VEC>(po + c.col, m[i]);
     }
     if (KEEP) po += so;
@@ -377,8 +423,7 @@ __global__ void __launch_bounds__(kMaxThreads<VEC, VPT, PARTS, KEEP>, kMinCtas<P
         } else {
           load_w<VEC>(p.w_next + col(i), true, f);
         }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) m[i][j] *= inv * f[j];
+        scale_by<PACK>(m[i], inv, f);
         store_vec<T, VEC>(ph + col(i), m[i]);
       }
       if (KEEP) ph += shh;
