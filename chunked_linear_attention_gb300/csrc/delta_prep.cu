@@ -12,9 +12,11 @@
 // 64, by products of 16 x 16 blocks on mma.sync tf32 with both operands in two
 // parts (fp32 accuracy; the smallest tcgen05 product has 64 rows).
 //
-// D is never formed from differences of long sums: G runs inside blocks of 16
-// (sums of a few g lose few bits), and blocks are joined by factors that are at
-// most 1 where g <= 0.
+// D is never formed from differences of rounded sums (behind a few tokens that clear the
+// state a sum inside a block of 16 reaches 1e3, and its last bit 1e-4): inside a block
+// the running sum is a pair of fp32 numbers, whose differences keep the small g between
+// two tokens; from a token to its block's end the small g are summed for themselves,
+// from the end on; and blocks are joined by factors that are at most 1 where g <= 0.
 //
 // Bound by instruction issue and shared memory (issue 47%, l1tex 61%, DRAM 36%): the
 // decays, the substitution and the pairs cost about 7000 warp instructions per
@@ -101,8 +103,9 @@ constexpr uint32_t kPCols = 64;
 
 struct PrepShared {
   float beta[kC];
-  float gl[kC];    // running sum of g log2(e) inside each block of 16
-  float el[kC];    // exp2(blk - gl): decay from token j to the end of its block
+  float2 gl[kC];   // running sum of g log2(e) inside each block of 16, and what its
+                   // roundings left out
+  float el[kC];    // decay from token j to the end of its block
   float blk[4];    // each block's sum of g log2(e)
   RecScal scal;
   uint64_t full, done;
@@ -216,18 +219,29 @@ __global__ void __launch_bounds__(kPThreads, 6)
     const int h = hk * group + hg;
     if (warp == 3) {
       constexpr float kLog2e = 1.4426950408889634f;
-      float gl[2], tot[2];
+      float gl[2], rest[2], tot[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         // exp(-104) is zero in fp32: -inf becomes a number that can be subtracted
-        float x = gv[e] < -104.f ? -104.f : gv[e];
-        x *= kLog2e;
+        const float x0 = (gv[e] < -104.f ? -104.f : gv[e]) * kLog2e;
+        float x = x0, r = 0.f;   // the sum up to this token
+        float z = __shfl_down_sync(0xffffffffu, x0, 1, 16);   // and of the tokens behind it
+        if ((lane & 15) == 15) z = 0.f;
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) {
           const float y = __shfl_up_sync(0xffffffffu, x, o, 16);
-          if ((lane & 15) >= o) x += y;
+          const float s = __shfl_up_sync(0xffffffffu, r, o, 16);
+          const float w = __shfl_down_sync(0xffffffffu, z, o, 16);
+          if ((lane & 15) >= o) {   // two numbers as their sum and its rounding error
+            const float sum = __fadd_rn(x, y), part = __fsub_rn(sum, x);
+            r += s + __fadd_rn(__fsub_rn(x, __fsub_rn(sum, part)), __fsub_rn(y, part));
+            x = sum;
+          }
+          if ((lane & 15) + o < 16) z += w;
         }
         gl[e] = x;
+        rest[e] = z;
+        sh.gl[32 * e + lane] = make_float2(x, r);
         tot[e] = __shfl_sync(0xffffffffu, x, 15, 16);   // this lane's block
       }
       float blk[4];
@@ -243,12 +257,10 @@ __global__ void __launch_bounds__(kPThreads, 6)
                                     : (up ? blk[0] + blk[1] + blk[2] : blk[0] + blk[1]);
         const float after = e == 0 ? (up ? blk[2] + blk[3] : blk[1] + blk[2] + blk[3])
                                    : (up ? 0.f : blk[3]);
-        const float rest = tot[e] - gl[e];
         sh.scal.neg[j] = -ex2(gl[e] + before);
-        sh.scal.er[j] = ex2(rest + after);
+        sh.scal.er[j] = ex2(rest[e] + after);
         sh.beta[j] = bv[e];
-        sh.gl[j] = gl[e];
-        sh.el[j] = ex2(rest);
+        sh.el[j] = ex2(rest[e]);
       }
       if (lane == 0) {
 #pragma unroll
@@ -262,7 +274,7 @@ __global__ void __launch_bounds__(kPThreads, 6)
       tc_fence_after();
     }
     __syncthreads();
-    const float gli = sh.gl[row];
+    const float gli = sh.gl[row].x;
     const float mul = warp < 2 ? p.scale : sh.beta[row];
     float decay = gli;   // log2 of the decay from the end of block J to the row
     const uint32_t prow = smem_u32(tile) + 2 * kBlk + row * 128;
@@ -297,14 +309,15 @@ __global__ void __launch_bounds__(kPThreads, 6)
         d[2 * e + 1] = mul2(f2, w.y);
       }
       if (J >= 2 * half) {   // lanes with their diagonal here, or (J > I) nothing
-        const float4* gl4 = reinterpret_cast<const float4*>(&sh.gl[16 * J]);
+        const float4* gl2 = reinterpret_cast<const float4*>(&sh.gl[16 * J]);
         const int last = row - 16 * J;   // last column of the row's part
         if (J >= I) {
+          const float gri = sh.gl[row].y;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 w = gl4[e];
-            d[2 * e] = pack2(mul * ex2(gli - w.x), mul * ex2(gli - w.y));
-            d[2 * e + 1] = pack2(mul * ex2(gli - w.z), mul * ex2(gli - w.w));
+          for (int e = 0; e < 8; ++e) {
+            const float4 w = gl2[e];
+            d[e] = pack2(mul * ex2((gli - w.x) + (gri - w.y)),
+                         mul * ex2((gli - w.z) + (gri - w.w)));
           }
         }
         tmem_wait_bind(x);
