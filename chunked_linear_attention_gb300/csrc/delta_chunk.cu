@@ -384,7 +384,6 @@ __global__ void __launch_bounds__(512, 1)
   uint8_t* obuf = reinterpret_cast<uint8_t*>(scal + 4);   // outputs on their way
   Bars* B = reinterpret_cast<Bars*>(obuf + kOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_launch_dependents();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -417,6 +416,7 @@ __global__ void __launch_bounds__(512, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B->tmem;
+  pdl_launch_dependents();   // (with TMEM in hand: see launch_behind)
   pdl_wait();
   const int items = n_items(p, false);
   bool ok = true;   // after a wait that ran out: no more waiting, run to the end
@@ -857,7 +857,6 @@ __global__ void __launch_bounds__(640, 1)
   RecScal* scal = reinterpret_cast<RecScal*>(smem + kCarryStages * kCarryBytes);
   CarryBars* B = reinterpret_cast<CarryBars*>(scal + kCarryStages);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_launch_dependents();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kCarryStages; ++s) {
@@ -881,6 +880,7 @@ __global__ void __launch_bounds__(640, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B->tmem;
+  pdl_launch_dependents();   // (with TMEM in hand: see launch_behind)
   pdl_wait();
   const int items = n_items(p, true);
   bool ok = true;
@@ -1383,7 +1383,6 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
   JoinBars* B = reinterpret_cast<JoinBars*>(smem + 2 * kPBytes);
   const int tile = blockIdx.x % p.tiles, x = blockIdx.x / p.tiles;
   const int h = x % p.Hv, k = x / p.Hv;
-  pdl_launch_dependents();
   pdl_wait();
   if (k >= (p.counts ? p.counts[2] : p.seqs)) return;
   const int seg0 = p.segs ? p.joins[k] : k * p.seg_n;
@@ -1401,6 +1400,7 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B->tmem;   // 128 columns of S's pairs, 128 of the product
+  pdl_launch_dependents();
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) { wait_w(ok, bar, parity, p.status, p.wait_ns); };
   if (warp == 8) {

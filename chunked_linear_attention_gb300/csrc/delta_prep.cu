@@ -131,7 +131,6 @@ __global__ void __launch_bounds__(kPThreads, 6)
   PrepShared& sh = *reinterpret_cast<PrepShared*>(tile + 4 * kBlk);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hk = blockIdx.x % p.Hk, place = blockIdx.x / p.Hk;
-  pdl_launch_dependents();
   if (p.plan) pdl_wait();   // the plan is the kernel before
   // the chunk at this place
   int seq, c;
@@ -186,6 +185,7 @@ __global__ void __launch_bounds__(kPThreads, 6)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  pdl_launch_dependents();   // (with TMEM in hand: see launch_behind)
   if (warp == 0 || valid < kC) wait_w(ok, &sh.full, 0, p.status, p.wait_ns);
   if (valid < kC) {   // rows behind the sequence's end: other tokens, or none
     const int pieces = (kC - valid) * 8;
