@@ -450,10 +450,13 @@ int launch_parts(const BlockNormArgs& a, NormParams p) {
   // rows per CTA: up to 256 threads; CTAs: what the SMs hold of them at once, so
   // that all run to the end together
   const int ny = p.nt >= 256 ? 1 : 256 / p.nt, threads = p.nt * ny;
-  p.np = p.pieces / p.P > p.nt / 32 ? p.pieces / p.P : p.nt / 32;
+  p.np = PARTS < 0 && p.gpieces == p.pieces ? p.nt / 32 : p.pieces / p.P;
   const int smem = ny * 2 * (p.np + p.nt / 32) * 4;
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  // always the limit of the longest rows (of unaligned groups, a partial sum an element):
+  // one call's own size could be below what another host thread is about to launch with
+  constexpr int kMostSmem = 2 * (16384 + 32) * 4;
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kMostSmem) != cudaSuccess)
     return TTT_ERR_CUDA;
   int per_sm = 65536 / ((regs + 7) / 8 * 8 * threads);
   per_sm = per_sm < 1 ? 1 : per_sm > 2048 / threads ? 2048 / threads : per_sm;
