@@ -428,11 +428,12 @@ def linattn_chunked_forward_noalloc(q, k, v, eta, chunk: int, mask_mode: int,
 
 # The delta-rule and norm calls are made once per layer and decoded token, so
 # their bindings keep the host's share short: strides travel as packed bytes,
-# and the stream is looked up by device index.
+# and the stream is looked up by device index (None in a torch without CUDA, which
+# has no tensors that get so far).
 _pack_layout = struct.Struct("18q").pack
 _pack_norm_strides = struct.Struct("5q").pack
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 _BF16, _F32 = torch.bfloat16, torch.float32
 
 
