@@ -36,7 +36,7 @@ EXPORTED = (
     "ttt_profile_stop", "linattn_chunked_forward_noalloc", "ttt_layer_host_workspace_size",
     "ttt_layer_forward_host", "ttt_selftest_withhold_release", "linattn_rule_workspace_size",
     "linattn_chunked_forward_rule", "delta_rule_workspace_size", "delta_rule_chunked_forward",
-    "delta_rule_step", "block_norm_forward",
+    "delta_rule_step", "block_norm_forward", "ttt_selftest_withhold_delta",
 )
 
 
@@ -138,6 +138,8 @@ def _declare(lib):
     lib.block_norm_forward.restype = i
     lib.block_norm_forward.argtypes = [vp] * 6 + [ll] + [i] * 5 + [
         f32, ctypes.c_char_p, vp, vp, vp]
+    lib.ttt_selftest_withhold_delta.restype = None
+    lib.ttt_selftest_withhold_delta.argtypes = [i]
     lib.ttt_selftest_withhold_release.restype = None
     lib.ttt_selftest_withhold_release.argtypes = [i]
     lib.ttt_launch_count.restype = ctypes.c_ulonglong
@@ -702,6 +704,12 @@ def selftest_withhold_release(bh: int):
     state items never report completion, so the items waiting for them run
     into their bounded waits (-1 turns it off).  See include/ttt_selftest.h."""
     library().ttt_selftest_withhold_release(int(bh))
+
+
+def selftest_withhold_delta(kernel: int):
+    """Test hook: from the next delta-rule call on, a wait of one of the chunk
+    form's kernels runs out (0 turns it off).  See include/ttt_selftest.h."""
+    library().ttt_selftest_withhold_delta(int(kernel))
 
 
 def selftest_gemm(A, B, a_mn_major: bool, b_mn_major: bool, tile_n: int = 128, stream=None):

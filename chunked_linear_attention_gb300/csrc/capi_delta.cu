@@ -7,6 +7,7 @@
 
 #include "capi_util.h"
 #include "delta_rule.h"
+#include "ttt_selftest.h"
 
 namespace {
 
@@ -143,6 +144,8 @@ int delta_rule_step(const void* q, const void* k, const void* v, const float* g,
   a.stream = reinterpret_cast<cudaStream_t>(stream);
   return ttt::delta_rule_step_launch(a);
 }
+
+void ttt_selftest_withhold_delta(int kernel) { ttt::delta_rule_withhold(kernel); }
 
 int block_norm_forward(const void* y, const float* w, const void* gate, const void* residual,
                        const float* scale, const float* w_next, long long rows, int D, int group,

@@ -40,6 +40,7 @@
 //   warps 4-11  the chain S -> K S^T -> X -> S: warp w has rows 32 (w % 4) .. and half
 //               of the columns, and hands them to the MMAs 16 at a time.
 //   warps 12-15 the outputs.
+#include <atomic>
 #include <mutex>
 
 #include "builder.h"
@@ -100,6 +101,7 @@ struct ScanParams {
   int seqs, seg_chunks, seg_n;   // not packed: chunks per segment; segments per sequence
   float scale;
   int wide_out;            // rows of out can be stored 16 bytes at a time
+  int withhold;            // test hook: the first CTA's second chunk is never ready
 };
 
 struct Item {
@@ -425,6 +427,14 @@ __global__ void __launch_bounds__(512, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
+  // (see wait_w)
+  auto arrive_if = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0 && ok) mbar_arrive(bar);
+  };
+  auto commit = [&](uint64_t* bar) {
+    if (ok) umma_commit(bar);
+  };
 
   if (warp < 4) {
     regs_dec<64>();
@@ -471,7 +481,8 @@ __global__ void __launch_bounds__(512, 1)
           __syncwarp();
         }
       }
-      if (!together(ok)) {   // copies still on their way into this CTA's shared memory
+      {   // copies still on their way into this CTA's shared memory
+        ok = together(ok);
         for (int m = n > kStages ? n - kStages : 0; m < n; ++m)
           mbar_wait_w(&B->full[m % kStages], (m / kStages) & 1, p.status, p.wait_ns);
         for (int m = n > 2 ? n - 2 : 0; m < n; ++m) {
@@ -511,7 +522,7 @@ __global__ void __launch_bounds__(512, 1)
                 umma_ts(tmem + kKS, a + 8, kb, id64, b + h != 0);
                 umma_ts(tmem + kKS, a, kb, id64, 1);
               }
-              if (b == NB - 1) umma_commit(&B->ks_full);
+              if (b == NB - 1) commit(&B->ks_full);
             }
             __syncwarp();
           }
@@ -542,8 +553,8 @@ __global__ void __launch_bounds__(512, 1)
                 umma_ts(tmem + kX, y, th + k * 2, id64, 1);
               }
               if (b == 1) {
-                umma_commit(&B->x_full);
-                umma_commit(&B->t_free[ph]);
+                commit(&B->x_full);
+                commit(&B->t_free[ph]);
               }
             }
             __syncwarp();
@@ -573,8 +584,8 @@ __global__ void __launch_bounds__(512, 1)
                 umma_ts(tmem + kDS, x, km + k * 128, idk, 1);
               }
               if (b == 1) {
-                umma_commit(&B->ds_full);
-                umma_commit(&B->empty[n % kStages]);
+                commit(&B->ds_full);
+                commit(&B->empty[n % kStages]);
               }
             }
             __syncwarp();
@@ -593,8 +604,8 @@ __global__ void __launch_bounds__(512, 1)
               umma_ts(tmem + kO, x, pL + k * 2, id64, 1);
               umma_ts(tmem + kO, x, pH + k * 2, id64, 1);
             }
-            umma_commit(&B->o_full);
-            umma_commit(&B->p_free[ph]);
+            commit(&B->o_full);
+            commit(&B->p_free[ph]);
           }
           __syncwarp();
         }
@@ -623,7 +634,7 @@ __global__ void __launch_bounds__(512, 1)
                 sts128(st + b * kBlk + x * 16, make_uint4(0, 0, 0, 0));
             fence_proxy_async_smem();
           }
-          arrive(&B->ready[s]);
+          if (!(p.withhold && blockIdx.x == 0 && n == 1)) arrive_if(&B->ready[s]);
         }
       }
     }
@@ -889,6 +900,14 @@ __global__ void __launch_bounds__(640, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
+  // (see wait_w)
+  auto arrive_if = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0 && ok) mbar_arrive(bar);
+  };
+  auto commit = [&](uint64_t* bar) {
+    if (ok) umma_commit(bar);
+  };
 
   if (warp < 4) {
     regs_dec<64>();
@@ -918,9 +937,9 @@ __global__ void __launch_bounds__(640, 1)
           __syncwarp();
         }
       }
-      if (!together(ok))   // copies still on their way into this CTA's shared memory
-        for (int m = n > kCarryStages ? n - kCarryStages : 0; m < n; ++m)
-          mbar_wait_w(&B->full[m % kCarryStages], (m / kCarryStages) & 1, p.status, p.wait_ns);
+      ok = together(ok);   // copies still on their way into this CTA's shared memory
+      for (int m = n > kCarryStages ? n - kCarryStages : 0; m < n; ++m)
+        mbar_wait_w(&B->full[m % kCarryStages], (m / kCarryStages) & 1, p.status, p.wait_ns);
     } else if (warp == 1) {
       const bool el = elect_lane();
       const uint32_t base = smem_u32(smem);
@@ -967,7 +986,7 @@ __global__ void __launch_bounds__(640, 1)
                 umma_ts(d + kUA, d + 16 * k + 8, b, id64, k != 0);
                 umma_ts(d + kUA, d + 16 * k, b, id64, 1);
               }
-              umma_commit(&B->ks_full[u]);
+              commit(&B->ks_full[u]);
             }
             __syncwarp();
           }
@@ -985,7 +1004,7 @@ __global__ void __launch_bounds__(640, 1)
                 umma_ts(d + kUX, y, tl + k * 2, id64, 1);
                 umma_ts(d + kUX, y, th + k * 2, id64, 1);
               }
-              umma_commit(&B->x_full[u]);
+              commit(&B->x_full[u]);
             }
             __syncwarp();
           }
@@ -1003,8 +1022,8 @@ __global__ void __launch_bounds__(640, 1)
                 umma_ts(d, x + 8, km + k * 128, idk, k != 0);
                 umma_ts(d, x, km + k * 128, idk, 1);
               }
-              umma_commit(&B->ds_full[u]);
-              if (u == units - 1) umma_commit(&B->empty[s]);
+              commit(&B->ds_full[u]);
+              if (u == units - 1) commit(&B->empty[s]);
             }
             __syncwarp();
           }
@@ -1023,7 +1042,7 @@ __global__ void __launch_bounds__(640, 1)
         // (segments before a sequence's last one hold whole chunks: nothing to zero)
         for (int c = 0; c < nc; ++c, ++n) {
           wait(&B->full[n % kCarryStages], (n / kCarryStages) & 1);
-          arrive(&B->ready[n % kCarryStages]);
+          if (!(p.withhold && blockIdx.x == 0 && n == 1)) arrive_if(&B->ready[n % kCarryStages]);
         }
       }
     }
@@ -1039,7 +1058,7 @@ __global__ void __launch_bounds__(640, 1)
       if (u == 1 && ci.it.tile != 0) {   // no unit here: pass the stages on
         for (int c = 0; c < nc; ++c, ++n) {
           wait(&B->ready[n % kCarryStages], (n / kCarryStages) & 1);
-          arrive(&B->empty[n % kCarryStages]);
+          arrive_if(&B->empty[n % kCarryStages]);
         }
         continue;
       }
@@ -1100,7 +1119,7 @@ __global__ void __launch_bounds__(640, 1)
         tc_fence_before();
         arrive(&B->xs_ready[u]);
         const F2 eall = pack2(sc.eall, sc.eall);
-        arrive(&B->empty[s]);
+        arrive_if(&B->empty[s]);
 
         wait(&B->ds_full[u], ph);
         tc_fence_after();
@@ -1373,6 +1392,7 @@ struct JoinParams {
   int* status;
   unsigned long long wait_ns;
   int Hv, dk, dv, tiles;
+  int withhold;            // test hook: the first CTA's second step is never ready
 };
 
 __global__ void __launch_bounds__(kJoinThreads, 1)
@@ -1464,7 +1484,8 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&B->s_ready);
+      const bool withheld = p.withhold && blockIdx.x == 0 && warp == 0 && j == 1;
+      if (lane == 0 && ok && !withheld) mbar_arrive(&B->s_ready);
       // beside the product: its 128 KB through the load-store units take as long
       load_state<16>(p.L + place(j), q4, half, lane, L);
       if (ok && (j > 0 || p.S0)) store_state<16>(p.Sseg + place(j), q4, half, lane, S);
@@ -1563,6 +1584,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       uint64_t* bar = &sh.full[loaded % kRowsStages];
       uint8_t* to = sh.P[loaded % kRowsStages];
       const uint8_t* from = p.P + ((long long)(seg0 + j) * p.Hv + h) * kPBytes;
+      if (p.withhold && blockIdx.x == 0 && loaded == 1) {
+        ++loaded;
+        return;
+      }
       mbar_arrive_expect_tx(bar, small ? 2 * kBlk : kPBytes);
       if (small) {
         bulk_load_g2s(to, from, kBlk, bar);
@@ -1681,6 +1706,8 @@ cudaError_t launch_rows(const JoinParams& j, int sms, cudaStream_t stream) {
                        kRowsThreads, sizeof(RowsShared<MT>), stream, j);
 }
 
+std::atomic<int> g_withhold{0};   // test hook: 1 prep, 2 L and P, 3 join, 4 outputs
+
 int g_ready[64] = {0};   // 0 unknown, 1 usable, 2 not usable
 int g_sms[64] = {0};
 std::mutex g_mu;
@@ -1798,6 +1825,8 @@ bool delta_map(CUtensorMap* m, const void* ptr, const delta_rule_stride& s, int 
   return encode_bf16_4d(m, ptr, dims, st, box);
 }
 
+void delta_rule_withhold(int kernel) { g_withhold.store(kernel); }
+
 size_t delta_rule_chunk_workspace(int B, int Hv, int N, int dk, int dv, int n_seq) {
   if (dk > 128 || dk % 8 != 0 || dv % 8 != 0) return 0;
   size_t need = 0;
@@ -1840,6 +1869,8 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
   r.scal = reinterpret_cast<RecScal*>(ws + pl.scal);
   r.status = a.status;
   r.wait_ns = a.wait_ns;
+  const int withhold = g_withhold.load(std::memory_order_relaxed);
+  r.withhold = withhold == 1;
 
   p.plan = plan;
   p.segs = segs;
@@ -1881,6 +1912,7 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
   if (launch_delta_prep(r, pl.chunks, a.stream) != cudaSuccess) return TTT_ERR_CUDA;
   if (pl.split) {
     {
+      p.withhold = withhold == 2;
       const int items = (packed ? pl.seg_places : a.B * (pl.seg_n - 1)) * a.Hv * p.tiles;
       ProfScope ps(PT_DELTA_CARRY, a.stream, 5.0 * tok * a.Hv * a.dk * (a.dv + a.dk),
                    tok * 2.0 * (a.Hk * a.dk + a.Hv * a.dv));
@@ -1902,6 +1934,7 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
     j.wait_ns = a.wait_ns;
     j.Hv = a.Hv; j.dk = a.dk; j.dv = a.dv;
     j.tiles = p.tiles;
+    j.withhold = withhold == 3;
     const double states = (double)pl.seg_places * a.Hv * a.dk;
     ProfScope ps(PT_DELTA_JOIN, a.stream, 2.0 * states * a.dk * a.dv,
                  4.0 * states * (a.dk + 2 * a.dv));
@@ -1917,6 +1950,7 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
     if (e != cudaSuccess) return TTT_ERR_CUDA;
   }
   const int items = pl.seg_places * a.Hv * p.tiles;
+  p.withhold = withhold == 4;
   ProfScope ps(PT_DELTA_CHUNK, a.stream, 7.0 * tok * a.Hv * a.dk * a.dv,
                tok * 4.0 * (a.Hk * a.dk + a.Hv * a.dv));
   return launch_behind(a.dk > 64 ? delta_scan_kernel<128> : delta_scan_kernel<64>, items < sms ? items : sms, 512, kSmem, a.stream, p) ==

@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(kPThreads, 6)
     mbar_init(&sh.full, 1);
     mbar_init(&sh.done, 1);
     fence_mbar_init();
-    const int blocks = p.dk > 64 ? 2 : 1;
-    mbar_arrive_expect_tx(&sh.full, 2 * blocks * kBlk);
+    const int blocks = p.withhold && blockIdx.x == 0 ? 0 : p.dk > 64 ? 2 : 1;
+    if (blocks) mbar_arrive_expect_tx(&sh.full, 2 * blocks * kBlk);
     for (int b = 0; b < blocks; ++b) {
       tma_load_4d(tile + 2 * b * kBlk, &p.q, 64 * b, t0, hk, batch, &sh.full);
       tma_load_4d(tile + (2 * b + 1) * kBlk, &p.k, 64 * b, t0, hk, batch, &sh.full);
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kPThreads, 6)
     if (elect_lane()) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        if (k == 4 && p.dk <= 64) break;
+        if (!ok || (k == 4 && p.dk <= 64)) break;
         const uint32_t o = (k >> 2) * (2 * kBlk / 16) + (k & 3) * 2;
         umma_bf16(tmem, a + o, b + o, id, k != 0);
       }

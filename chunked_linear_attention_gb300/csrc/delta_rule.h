@@ -51,6 +51,8 @@ int delta_rule_recurrent(const DeltaArgs& a);
 // Chunks of 64 tokens on the tensor cores (bf16, d_k <= 128, aligned strides).
 // Returns 1 where it does not apply, else a ttt_status.
 int delta_rule_chunk_launch(const DeltaArgs& a);
+// Test hook: see ttt_selftest_withhold_delta.
+void delta_rule_withhold(int kernel);
 // Workspace bytes of such a call (0 where it never applies).
 size_t delta_rule_chunk_workspace(int B, int Hv, int N, int dk, int dv, int n_seq);
 

@@ -14,7 +14,9 @@
  *
  * Conventions are those of ttt.h (device pointers unless an argument says
  * "host", asynchronous on `stream`, host-side argument checks before anything
- * is enqueued, no allocation on the call path).  The states are fp32
+ * is enqueued, no allocation on the call path).  After a bounded wait that ran out
+ * (TTT_ERR_TIMEOUT in the device status word) the results of the call are
+ * undefined; nothing but its outputs is touched.  The states are fp32
  * throughout.  Tensors need not be dense: see delta_rule_layout.
  *
  * Heads: q and k have Hk heads, v, g, beta, out and the state Hv heads; Hv is

@@ -39,6 +39,20 @@ int ttt_selftest_gemm(const void* A, const void* B, float* D, int Z, int M, int 
  * off.  Process-wide; not for production use. */
 void ttt_selftest_withhold_release(int bh);
 
+/* Test hook for the bounded waits of the chunk form of
+ * delta_rule_chunked_forward.  From the next call on, the first CTA of one of
+ * its kernels never sees one of its waits satisfied:
+ *   1  records of the chunks: its tiles are not loaded;
+ *   2  L and P of the segments: its second chunk is not handed on;
+ *   3  join of the segments: its second step's operand is not handed on;
+ *   4  outputs: its second chunk is not handed on.
+ * The roles of that CTA run into their wait limits, record TTT_ERR_TIMEOUT in
+ * the device status word, wait for the copies and products that they have
+ * issued, and end.  The states and outputs of the first
+ * key head's value heads are undefined then; other heads are computed as
+ * usual.  0 turns the hook off.  Process-wide; not for production use. */
+void ttt_selftest_withhold_delta(int kernel);
+
 #ifdef __cplusplus
 }
 #endif
