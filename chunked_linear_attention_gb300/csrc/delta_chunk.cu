@@ -1270,8 +1270,8 @@ __device__ __forceinline__ int choose_segments(int nc, int n_seq, int least, int
 
 __global__ void __launch_bounds__(kPlanThreads)
     delta_plan_kernel(const int* starts, int n_seq, int N, int chunks, int least, bool split,
-                      int units, int seg_places, SeqPlan* plan, SegPlan* segs, int* order,
-                      int* joins, int* counts, int* status) {
+                      int units, SeqPlan* plan, SegPlan* segs, int* order, int* joins, int* counts,
+                      int* status) {
   __shared__ int part[kPlanThreads / 32];
   __shared__ long long wide_part[kPlanThreads / 32];
   pdl_launch_dependents();
@@ -1357,8 +1357,6 @@ __global__ void __launch_bounds__(kPlanThreads)
       if (sg.j == sg.n - 1) order[whole + atomicAdd(&base[bin(chunks_of(sg))], 1)] = i;
     }
   }
-  for (int i = seg0 + (int)threadIdx.x; i < seg_places; i += kPlanThreads)
-    segs[i] = SegPlan{-1, 0, 1, seg_chunks};
   if (threadIdx.x == 0) {
     counts[0] = whole;
     counts[1] = seg0;
@@ -1369,7 +1367,8 @@ __global__ void __launch_bounds__(kPlanThreads)
 // ---------------------------------------------------------------- start states of the segments
 // S_{j+1} = S_j P_j + L_j: a CTA takes 128 rows of the state of one (sequence, head)
 // through all segments, S as pairs in TMEM, P_j as pairs from the carry pass (64 KB
-// by bulk copy, the next one on its way), three products, L_j added in fp32.
+// by bulk copy, the next one on its way), three products, L_j added in fp32.  For
+// sequences of one length (packed ones go by rows, below).
 // Warps 0-7: rows 32 (w % 4) .., half of the columns; warp 8: copies and MMAs.
 // (A step in fp32 on the CUDA cores took 16 SMs 2.5 us.)
 constexpr int kJoinThreads = 288;
@@ -1402,11 +1401,8 @@ __global__ void __launch_bounds__(kJoinThreads, 1)
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   JoinBars* B = reinterpret_cast<JoinBars*>(smem + 2 * kPBytes);
   const int tile = blockIdx.x % p.tiles, x = blockIdx.x / p.tiles;
-  const int h = x % p.Hv, k = x / p.Hv;
+  const int h = x % p.Hv, seq = x / p.Hv, n = p.seg_n, seg0 = seq * n;
   pdl_wait();
-  if (k >= (p.counts ? p.counts[2] : p.seqs)) return;
-  const int seg0 = p.segs ? p.joins[k] : k * p.seg_n;
-  const int seq = p.segs ? p.segs[seg0].seq : k, n = p.segs ? p.segs[seg0].n : p.seg_n;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(&B->full[0], 1);
@@ -1905,8 +1901,7 @@ int delta_rule_chunk_launch(const DeltaArgs& a) {
     ProfScope ps(PT_DELTA_PLAN, a.stream, 0.0, 20.0 * a.n_seq);
     delta_plan_kernel<<<1, kPlanThreads, 0, a.stream>>>(a.seq_starts, a.n_seq, a.N, pl.chunks,
                                                         pl.seg_chunks, pl.split, a.Hv * p.tiles,
-                                                        pl.seg_places, plan, segs,
-                                                        order, joins, counts, a.status);
+                                                        plan, segs, order, joins, counts, a.status);
     if (cudaGetLastError() != cudaSuccess) return TTT_ERR_CUDA;
   }
   if (launch_delta_prep(r, pl.chunks, a.stream) != cudaSuccess) return TTT_ERR_CUDA;

@@ -31,8 +31,7 @@ struct SeqPlan {
   int t0, len, chunk0, pad;
 };
 
-// Segment j of n of a sequence: the chunks that one CTA walks (seq < 0: no
-// segment at this place).
+// Segment j of n of a sequence: the chunks that one CTA walks.
 struct SegPlan {
   int seq, j, n;
   int chunks;   // of each segment but a sequence's last
