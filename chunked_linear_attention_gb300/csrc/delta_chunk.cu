@@ -1304,7 +1304,8 @@ __global__ void __launch_bounds__(kPlanThreads)
     int ts;
     const long long cb = chunk0 + block_before<long long>(nc, wide_part, tc);
     // bounds that ascend fit always; sequences that overlap (bad bounds between
-    // them) may hold more chunks than there are places: those stay empty
+    // them) may hold more chunks than there are places: those stay empty, and begin
+    // behind the last place (the chunks' kernel searches ascending first chunks)
     const bool fits = cb + nc <= chunks;
     if (!fits && s < n_seq) {
       len = 0;
@@ -1318,7 +1319,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (s < n_seq) {
       last = sb + ns - 1;
       left = n_chunks(len) - (ns - 1) * seg_chunks;
-      plan[s] = SeqPlan{t0, len, fits ? (int)cb : 0, 0};
+      plan[s] = SeqPlan{t0, len, fits ? (int)cb : chunks, 0};
       for (int j = 0; j < ns; ++j) {
         segs[sb + j] = SegPlan{s, j, ns, seg_chunks};
         if (j + 1 < ns) order[sb - s + j] = sb + j;   // s last ones are before it

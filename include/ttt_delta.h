@@ -62,8 +62,10 @@ size_t delta_rule_workspace_size(int B, int Hk, int Hv, int N, int d_k, int d_v,
  *               may be 0.  Tokens of no sequence are not read and their rows
  *               of out are not written.  Entries that are not ascending or not
  *               within 0..N make their sequence empty and set TTT_ERR_ARG in
- *               the device status word (ttt_device_status); other sequences
- *               that overlap around such entries have undefined results
+ *               the device status word (ttt_device_status).  Other sequences may
+ *               overlap around such entries: the rows of out that several
+ *               share are undefined, and from the sequence on with which their
+ *               lengths add up to more than N all may be taken for empty
  *               (nothing outside the tensors is touched).
  *               They are read on the device: a captured call may be replayed
  *               with other bounds.
