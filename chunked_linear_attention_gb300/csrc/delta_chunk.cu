@@ -28,9 +28,9 @@
 // the state's next pairs), with a conversion by the warps between any two.  A step
 // takes 2.25 us, of which the tensor pipe works 47% (2690 cycles of products, in
 // pairs); one more order of products to fill the gaps (two MMA warps, other
-// hand-overs) was slower.  B 4, H 4, 8192 tokens, d 128: 139 us (prep 32, L and P
-// 54, join 14, outputs 46, their ends overlapping), token by token 1.6 ms; one
-// sequence of 131072 tokens, 4 heads: 421 us (97, 156, 41, 136).
+// hand-overs) was slower.  B 4, H 4, 8192 tokens, d 128: 138 us (prep 33, L and P
+// 54, join 14, outputs 47, their ends overlapping), token by token 1.6 ms; one
+// sequence of 131072 tokens, 4 heads: 425 us (101, 157, 42, 136).
 //
 // Roles (512 threads, one CTA per SM, persistent over (segment, head, d_v tile)):
 //   warp 0      TMA: q, k, v in three stages, the chunk's records in two.

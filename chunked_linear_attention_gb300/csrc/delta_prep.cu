@@ -18,10 +18,11 @@
 // two tokens; from a token to its block's end the small g are summed for themselves,
 // from the end on; and blocks are joined by factors that are at most 1 where g <= 0.
 //
-// Bound by instruction issue and shared memory (issue 47%, l1tex 61%, DRAM 36%): the
-// decays, the substitution and the pairs cost about 7000 warp instructions per
-// record.  2048 records (B 4, H 4, 8192 tokens) take 32 us, 8192 (131072 tokens of 4
-// heads) 97 us, against 80 for the bytes.  Six CTAs per SM, so that one's
+// Bound by instruction issue and shared memory (issue 48%, l1tex 61%, DRAM 34%): the
+// decays, the substitution and the pairs cost about 7400 warp instructions per
+// record.  2048 records (B 4, H 4, 8192 tokens) take 33 us, 8192 (131072 tokens of 4
+// heads) 101 us, against 80 for the bytes (32 and 98 with the running sum in one number;
+// its differences by packed instructions, at more registers, took 34).  Six CTAs per SM, so that one's
 // substitution runs beside another's products; T's tiles lie over the scratch, and
 // the record over q and k, to make room for them.
 #include "delta_tc.cuh"

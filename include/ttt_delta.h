@@ -45,7 +45,10 @@ typedef struct {
 } delta_rule_layout;
 
 /* Bytes of device workspace delta_rule_chunked_forward needs (0 if the
- * arguments are invalid; otherwise at least 256). */
+ * arguments are invalid; otherwise at least 256).  For the chunk form (below)
+ * these are 33296 bytes per 64 tokens and value head (32 KB of matrices: 2.2 GB
+ * for 131072 tokens of 32 heads) and, where sequences are cut into segments, per
+ * segment and value head 64 KB and another 128 KB per 128 of d_v. */
 size_t delta_rule_workspace_size(int B, int Hk, int Hv, int N, int d_k, int d_v, int n_seq,
                                  int io_dtype);
 
@@ -86,7 +89,8 @@ size_t delta_rule_workspace_size(int B, int Hk, int Hv, int N, int d_k, int d_v,
  * a NaN or infinity in a token's k, v, g or beta may also reach the outputs of
  * the up to 63 tokens before it in its chunk.  All other calls, and ones of a few tokens,
  * run token by token in fp32.
- * Decays below exp(-104) count as exp(-104) (zero in fp32).
+ * Decays below exp(-104) count as exp(-104); in the chunk form a decay below
+ * 2^-126, of one token or of several together, is zero.
  * Supported: d_k <= 512, d_v <= 1024, n_seq * Hv at most 2^20, and
  * B * Hv * N below 2^31.
  * S0 and S_final must be 16-byte aligned. */

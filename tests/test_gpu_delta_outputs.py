@@ -1,5 +1,5 @@
 """bf16 outputs of the chunk form held to output_bound (see
-test_delta_output_bound.py), which a dropped low part of any pair passes, and
+test_delta_output_bound.py), which a dropped low part of any pair exceeds, and
 outputs whose rows cannot be stored 16 bytes at a time."""
 import numpy as np
 import pytest
