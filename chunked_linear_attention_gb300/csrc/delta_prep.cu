@@ -22,9 +22,9 @@
 // decays, the substitution and the pairs cost about 7400 warp instructions per
 // record.  2048 records (B 4, H 4, 8192 tokens) take 33 us, 8192 (131072 tokens of 4
 // heads) 101 us, against 80 for the bytes (32 and 98 with the running sum in one number;
-// its differences by packed instructions, at more registers, took 34).  Six CTAs per SM, so that one's
-// substitution runs beside another's products; T's tiles lie over the scratch, and
-// the record over q and k, to make room for them.
+// its differences by packed instructions, at more registers, took 34).  Six
+// CTAs per SM, so that one's substitution runs beside another's products; T's tiles lie
+// over the scratch, and the record over q and k, to make room for them.
 #include "delta_tc.cuh"
 #include "prof.h"
 

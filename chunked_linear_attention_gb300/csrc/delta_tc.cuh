@@ -150,8 +150,9 @@ __device__ __forceinline__ float ex2(float x) {
 // calls pdl_wait() before it touches memory.  A kernel that uses TMEM lets the next
 // one begin (pdl_launch_dependents) only once it holds its own: a CTA of the next kernel
 // keeps what it allocates until this kernel has ended, so that a CTA of this one that
-// came to the same SM with its allocation still ahead would wait for ever.  Short launches in a row gain their launch's
-// latency too: 56 tokens of 16 heads 24.6 -> 22.5 us, 20011 rows of 1536 69.6 -> 67.5.
+// came to the same SM with its allocation still ahead would wait for ever.  Short launches
+// in a row gain their launch's latency too: 56 tokens of 16 heads 24.6 -> 22.5 us, 20011
+// rows of 1536 69.6 -> 67.5.
 template <typename P>
 cudaError_t launch_behind(void (*kern)(P), unsigned grid, unsigned block, size_t smem,
                           cudaStream_t stream, const P& params) {
