@@ -37,6 +37,8 @@ EXPORTED = (
     "ttt_layer_forward_host", "ttt_selftest_withhold_release", "linattn_rule_workspace_size",
     "linattn_chunked_forward_rule", "delta_rule_workspace_size", "delta_rule_chunked_forward",
     "delta_rule_step", "block_norm_forward", "ttt_selftest_withhold_delta",
+    "window_attention_forward", "window_attention_step", "selective_scan_workspace_size",
+    "selective_scan_forward", "selective_scan_step", "short_conv_forward", "short_conv_step",
 )
 
 
@@ -138,6 +140,21 @@ def _declare(lib):
     lib.block_norm_forward.restype = i
     lib.block_norm_forward.argtypes = [vp] * 6 + [ll] + [i] * 5 + [
         f32, ctypes.c_char_p, vp, vp, vp]
+    cp = ctypes.c_char_p
+    lib.window_attention_forward.restype = i
+    lib.window_attention_forward.argtypes = [vp] * 6 + [i, vp, vp] + [i] * 9 + [f32, cp, vp, vp]
+    lib.window_attention_step.restype = i
+    lib.window_attention_step.argtypes = [vp] * 7 + [i] * 8 + [f32, cp, vp, vp]
+    lib.selective_scan_workspace_size.restype = sz
+    lib.selective_scan_workspace_size.argtypes = [i] * 7
+    lib.selective_scan_forward.restype = i
+    lib.selective_scan_forward.argtypes = [vp] * 10 + [i] * 8 + [cp, vp, vp, vp, sz, vp]
+    lib.selective_scan_step.restype = i
+    lib.selective_scan_step.argtypes = [vp] * 10 + [i] * 7 + [cp, vp, vp]
+    lib.short_conv_forward.restype = i
+    lib.short_conv_forward.argtypes = [vp] * 5 + [i] * 7 + [cp, vp, vp, vp]
+    lib.short_conv_step.restype = i
+    lib.short_conv_step.argtypes = [vp] * 5 + [i] * 6 + [cp, vp, vp]
     lib.ttt_selftest_withhold_delta.restype = None
     lib.ttt_selftest_withhold_delta.argtypes = [i]
     lib.ttt_selftest_withhold_release.restype = None
@@ -671,6 +688,332 @@ def block_norm_forward(y, w: Optional[torch.Tensor] = None,
     return out, h
 
 
+# ---------------------------------------------------------------- fixed-state mixers
+_pack_window = struct.Struct("12q").pack
+_pack_scan = struct.Struct("12q").pack
+_pack_conv = struct.Struct("4q").pack
+
+
+def _starts(seq_starts, B, dev):
+    """(address, number of sequences) of packed sequences' bounds."""
+    if seq_starts is None:
+        return None, B
+    if B != 1:
+        raise ValueError("seq_starts needs B = 1")
+    n_seq = seq_starts.numel() - 1
+    if n_seq < 1 or not seq_starts.is_contiguous():
+        raise ValueError("seq_starts must be a contiguous vector of n_seq + 1 entries")
+    _want(seq_starts, (n_seq + 1,), torch.int32, dev, "seq_starts")
+    return seq_starts.data_ptr(), n_seq
+
+
+def _gpu(t):
+    if t.device.type != "cuda":
+        raise ValueError("tensors passed to the CUDA path must be on a CUDA device")
+    return t.device
+
+
+def _places(cache_k, cache_v, Hk, places, d, dt, dev):
+    """Number of slots of a pair of window-attention caches."""
+    if cache_k.dim() != 4:
+        raise ValueError("cache_k must have four dimensions")
+    shape = (cache_k.shape[0], Hk, places, d)
+    _dense(cache_k, shape, dt, dev, "cache_k")
+    _dense(cache_v, shape, dt, dev, "cache_v")
+    return shape[0]
+
+
+def window_attention_forward(q, k, v, window: int, sinks: int = 0,
+                             scale: Optional[float] = None,
+                             cache_k: Optional[torch.Tensor] = None,
+                             cache_v: Optional[torch.Tensor] = None,
+                             slots: Optional[torch.Tensor] = None,
+                             past: Optional[torch.Tensor] = None,
+                             seq_starts: Optional[torch.Tensor] = None,
+                             out: Optional[torch.Tensor] = None, stream=None):
+    """Causal attention with a sliding window over whole sequences, whose first
+    ``sinks`` tokens stay visible (see ``window_attention_forward`` in
+    include/ttt_mixers.h).
+
+    q [B, Hq, N, d], k, v [B, Hk, N, d], bf16 or fp32, any strides with the
+    last dimension contiguous.  cache_k, cache_v [n_slots, Hk, sinks + window, d]
+    of the same type, contiguous, updated in place: the keys and values that
+    ``window_attention_step`` and later turns read.  slots int32 [n_seq or B]
+    (negative: no cache) or None; past int32 [n_seq or B], the tokens already in
+    the caches, or None.  seq_starts: int32 [n_seq + 1] for sequences packed along
+    the token axis (B = 1).  scale: d ** -0.5 when None.  Without ``out``, the
+    outputs are stored in q's order of dimensions.  Returns out [B, Hq, N, d].
+    """
+    dev = _gpu(q)
+    if stream is not None or dev.index != _current_device():
+        with _elsewhere(dev, stream):
+            return window_attention_forward(q, k, v, window, sinks, scale, cache_k, cache_v, slots,
+                                            past, seq_starts, out)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must have four dimensions")
+    B, Hq, N, d = q.shape
+    Hk, dt, io = k.shape[1], q.dtype, _io_dtype(q)
+    _want(k, (B, Hk, N, d), dt, dev, "k")
+    _want(v, (B, Hk, N, d), dt, dev, "v")
+    starts, n_seq = _starts(seq_starts, B, dev)
+    n_slots = 0
+    if cache_k is not None and cache_v is not None:
+        n_slots = _places(cache_k, cache_v, Hk, sinks + window, d, dt, dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _want(out, (B, Hq, N, d), dt, dev, "out")
+    rc = (_lib or library()).window_attention_forward(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        None if cache_k is None else cache_k.data_ptr(),
+        None if cache_v is None else cache_v.data_ptr(),
+        _dense(slots, (n_seq,), torch.int32, dev, "slots"), n_slots,
+        _dense(past, (n_seq,), torch.int32, dev, "past"), starts, n_seq, B, Hq, Hk, N, d, window,
+        sinks, io, d ** -0.5 if scale is None else scale,
+        _pack_window(*_strides(q, "q")[:3], *_strides(k, "k")[:3], *_strides(v, "v")[:3],
+                     *_strides(out, "out")[:3]),
+        out.data_ptr(), _raw_stream(dev.index))
+    if rc:
+        _check(rc, "window_attention_forward")
+    return out
+
+
+def window_attention_step(q, k, v, cache_k, cache_v, positions, window: int, sinks: int = 0,
+                          slots: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                          out: Optional[torch.Tensor] = None, stream=None):
+    """One token of each of B sequences: its key and value are put into the
+    cache, and it attends to what the cache then holds (see
+    ``window_attention_step`` in include/ttt_mixers.h).
+
+    q [B, Hq, d], k, v [B, Hk, d], bf16 or fp32, last dimension contiguous;
+    cache_k, cache_v [n_slots, Hk, sinks + window, d] of the same type; positions
+    int32 [B], the number of tokens before; slots int32 [B] (negative: an idle
+    row) or None.  Returns out [B, Hq, d].
+    """
+    dev = _gpu(q)
+    if stream is not None or dev.index != _current_device():
+        with _elsewhere(dev, stream):
+            return window_attention_step(q, k, v, cache_k, cache_v, positions, window, sinks, slots,
+                                         scale, out)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must have three dimensions")
+    B, Hq, d = q.shape
+    Hk, dt, io = k.shape[1], q.dtype, _io_dtype(q)
+    _want(k, (B, Hk, d), dt, dev, "k")
+    _want(v, (B, Hk, d), dt, dev, "v")
+    n_slots = _places(cache_k, cache_v, Hk, sinks + window, d, dt, dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _want(out, (B, Hq, d), dt, dev, "out")
+    rc = (_lib or library()).window_attention_step(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), cache_k.data_ptr(), cache_v.data_ptr(),
+        _dense(positions, (B,), torch.int32, dev, "positions"),
+        _dense(slots, (B,), torch.int32, dev, "slots"), n_slots, B, Hq, Hk, d, window, sinks, io,
+        d ** -0.5 if scale is None else scale,
+        _pack_window(*_strides(q, "q")[:2], 0, *_strides(k, "k")[:2], 0, *_strides(v, "v")[:2], 0,
+                     *_strides(out, "out")[:2], 0),
+        out.data_ptr(), _raw_stream(dev.index))
+    if rc:
+        _check(rc, "window_attention_step")
+    return out
+
+
+def _groups(t, rows, G, S, dtype, dev, what):
+    """Strides of a [rows.., G, S] tensor whose tokens are contiguous."""
+    _want(t, (*rows, G, S), dtype, dev, what)
+    st = t.stride()
+    if (S > 1 and st[-1] != 1) or (G > 1 and st[-2] != S):
+        raise ValueError(f"{what} must be contiguous in its last two dimensions")
+    return st[:-2]
+
+
+def selective_scan_workspace_size(B, N, D, S, G, n_seq, io_dtype) -> int:
+    return library().selective_scan_workspace_size(B, N, D, S, G, n_seq, io_dtype)
+
+
+def selective_scan_forward(x, dt, A, B, C, D: Optional[torch.Tensor] = None,
+                           dt_bias: Optional[torch.Tensor] = None,
+                           z: Optional[torch.Tensor] = None, dt_softplus: bool = True,
+                           state: Optional[torch.Tensor] = None,
+                           seq_starts: Optional[torch.Tensor] = None,
+                           out: Optional[torch.Tensor] = None,
+                           state_out: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None):
+    """The selective state space scan over whole sequences (see
+    ``selective_scan_forward`` in include/ttt_mixers.h).
+
+    x, dt, z [batch, N, channels], bf16 or fp32, any strides with the last dimension
+    contiguous; A [channels, S] fp32; B, C [batch, N, G, S] in x's type, a token's
+    numbers contiguous; D, dt_bias [channels] fp32 or None; state fp32
+    [n_seq or batch, channels, S] or None (zeros).  seq_starts: int32 [n_seq + 1]
+    for sequences packed along the token axis (batch of 1).  Returns (out
+    [batch, N, channels], state_out [n_seq or batch, channels, S]).
+    """
+    dev = _gpu(x)
+    if stream is not None or dev.index != _current_device():
+        with _elsewhere(dev, stream):
+            return selective_scan_forward(x, dt, A, B, C, D, dt_bias, z, dt_softplus, state,
+                                          seq_starts, out, state_out, workspace)
+    if x.dim() != 3 or B.dim() != 4:
+        raise ValueError("x must have three dimensions, B four")
+    nb, N, ch = x.shape
+    G, S = B.shape[2:]
+    io, f32, rows = _io_dtype(x), _F32, (nb, N)
+    _want(dt, x.shape, x.dtype, dev, "dt")
+    if z is not None:
+        _want(z, x.shape, x.dtype, dev, "z")
+    sb, sc = (_groups(t, rows, G, S, x.dtype, dev, w) for t, w in ((B, "B"), (C, "C")))
+    starts, n_seq = _starts(seq_starts, nb, dev)
+    lib = _lib or library()
+    if out is None:
+        out = torch.empty(x.shape, device=dev, dtype=x.dtype)
+    else:
+        _want(out, x.shape, x.dtype, dev, "out")
+    if state_out is None:
+        state_out = torch.empty((n_seq, ch, S), device=dev, dtype=f32)
+    if workspace is None:
+        need = lib.selective_scan_workspace_size(nb, N, ch, S, G, n_seq, io)
+        workspace = torch.empty(need or 256, device=dev, dtype=torch.uint8)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    rc = lib.selective_scan_forward(
+        x.data_ptr(), dt.data_ptr(), _dense(A, (ch, S), f32, dev, "A"), B.data_ptr(), C.data_ptr(),
+        _dense(D, (ch,), f32, dev, "D"), _dense(dt_bias, (ch,), f32, dev, "dt_bias"),
+        None if z is None else z.data_ptr(), _dense(state, (n_seq, ch, S), f32, dev, "state"),
+        starts, n_seq, nb, N, ch, S, G, io, int(bool(dt_softplus)),
+        _pack_scan(*_strides(x, "x")[:2], *_strides(dt, "dt")[:2],
+                   *((0, 0) if z is None else _strides(z, "z")[:2]), *sb, *sc,
+                   *_strides(out, "out")[:2]),
+        out.data_ptr(), _dense(state_out, (n_seq, ch, S), f32, dev, "state_out"),
+        workspace.data_ptr(), workspace.nbytes, _raw_stream(dev.index))
+    if rc:
+        _check(rc, "selective_scan_forward")
+    return out, state_out
+
+
+def selective_scan_step(x, dt, A, B, C, state, D: Optional[torch.Tensor] = None,
+                        dt_bias: Optional[torch.Tensor] = None,
+                        z: Optional[torch.Tensor] = None, dt_softplus: bool = True,
+                        slots: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None, stream=None):
+    """The selective state space scan for one token of each row, on a pool of
+    states that is updated in place (see ``selective_scan_step`` in
+    include/ttt_mixers.h).
+
+    x, dt, z [rows, channels], B, C [rows, G, S]; state [n_slots, channels, S]
+    fp32; slots int32 [rows] (negative: an idle row) or None.  The others as for
+    ``selective_scan_forward``.  Returns out [rows, channels].
+    """
+    dev = _gpu(x)
+    if stream is not None or dev.index != _current_device():
+        with _elsewhere(dev, stream):
+            return selective_scan_step(x, dt, A, B, C, state, D, dt_bias, z, dt_softplus, slots, out)
+    if x.dim() != 2 or B.dim() != 3 or state.dim() != 3:
+        raise ValueError("x must have two dimensions, B and state three")
+    nb, ch = x.shape
+    G, S = B.shape[1:]
+    io, f32 = _io_dtype(x), _F32
+    _want(dt, x.shape, x.dtype, dev, "dt")
+    if z is not None:
+        _want(z, x.shape, x.dtype, dev, "z")
+    (sb,), (sc,) = (_groups(t, (nb,), G, S, x.dtype, dev, w) for t, w in ((B, "B"), (C, "C")))
+    n_slots = state.shape[0]
+    if out is None:
+        out = torch.empty(x.shape, device=dev, dtype=x.dtype)
+    else:
+        _want(out, x.shape, x.dtype, dev, "out")
+    rc = (_lib or library()).selective_scan_step(
+        x.data_ptr(), dt.data_ptr(), _dense(A, (ch, S), f32, dev, "A"), B.data_ptr(), C.data_ptr(),
+        _dense(D, (ch,), f32, dev, "D"), _dense(dt_bias, (ch,), f32, dev, "dt_bias"),
+        None if z is None else z.data_ptr(), _dense(state, (n_slots, ch, S), f32, dev, "state"),
+        _dense(slots, (nb,), torch.int32, dev, "slots"), n_slots, nb, ch, S, G, io,
+        int(bool(dt_softplus)),
+        _pack_scan(_strides(x, "x")[0], 0, _strides(dt, "dt")[0], 0,
+                   0 if z is None else _strides(z, "z")[0], 0, sb, 0, sc, 0,
+                   _strides(out, "out")[0], 0),
+        out.data_ptr(), _raw_stream(dev.index))
+    if rc:
+        _check(rc, "selective_scan_step")
+    return out
+
+
+def short_conv_forward(x, w, bias: Optional[torch.Tensor] = None, silu: bool = False,
+                       state: Optional[torch.Tensor] = None,
+                       seq_starts: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None,
+                       state_out: Optional[torch.Tensor] = None, stream=None):
+    """The short causal convolution of each channel over whole sequences (see
+    ``short_conv_forward`` in include/ttt_mixers.h).
+
+    x [B, N, D], bf16 or fp32, any strides with the last dimension contiguous;
+    w [D, W] fp32 (w[:, W - 1] meets the token itself); bias [D] fp32 or None;
+    state [n_seq or B, W - 1, D] in x's type, the inputs before each sequence,
+    oldest first, or None (zeros).  seq_starts: int32 [n_seq + 1] for sequences
+    packed along the token axis (B = 1).  Returns (out [B, N, D], state_out).
+    """
+    dev = _gpu(x)
+    if stream is not None or dev.index != _current_device():
+        with _elsewhere(dev, stream):
+            return short_conv_forward(x, w, bias, silu, state, seq_starts, out, state_out)
+    if x.dim() != 3 or w.dim() != 2:
+        raise ValueError("x must have three dimensions, w two")
+    B, N, D = x.shape
+    W, dt = w.shape[1], x.dtype
+    io = _io_dtype(x)
+    starts, n_seq = _starts(seq_starts, B, dev)
+    rows = (n_seq, W - 1, D)
+    if out is None:
+        out = torch.empty(x.shape, device=dev, dtype=dt)
+    else:
+        _want(out, x.shape, dt, dev, "out")
+    if state_out is None:
+        state_out = torch.empty(rows, device=dev, dtype=dt)
+    rc = (_lib or library()).short_conv_forward(
+        x.data_ptr(), _dense(w, (D, W), _F32, dev, "w"), _dense(bias, (D,), _F32, dev, "bias"),
+        _dense(state, rows, dt, dev, "state"), starts, n_seq, B, N, D, W, io, int(bool(silu)),
+        _pack_conv(*_strides(x, "x")[:2], *_strides(out, "out")[:2]), out.data_ptr(),
+        _dense(state_out, rows, dt, dev, "state_out"), _raw_stream(dev.index))
+    if rc:
+        _check(rc, "short_conv_forward")
+    return out, state_out
+
+
+def short_conv_step(x, w, state, bias: Optional[torch.Tensor] = None, silu: bool = False,
+                    slots: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    stream=None):
+    """The short causal convolution for one token of each row, on a pool of
+    states that is updated in place (see ``short_conv_step`` in
+    include/ttt_mixers.h).
+
+    x [B, D]; w [D, W] fp32; state [n_slots, W - 1, D] in x's type; slots int32
+    [B] (negative: an idle row) or None.  Returns out [B, D].
+    """
+    dev = _gpu(x)
+    if stream is not None or dev.index != _current_device():
+        with _elsewhere(dev, stream):
+            return short_conv_step(x, w, state, bias, silu, slots, out)
+    if x.dim() != 2 or w.dim() != 2 or state.dim() != 3:
+        raise ValueError("x and w must have two dimensions, state three")
+    B, D = x.shape
+    W, dt = w.shape[1], x.dtype
+    io = _io_dtype(x)
+    n_slots = state.shape[0]
+    if out is None:
+        out = torch.empty(x.shape, device=dev, dtype=dt)
+    else:
+        _want(out, x.shape, dt, dev, "out")
+    rc = (_lib or library()).short_conv_step(
+        x.data_ptr(), _dense(w, (D, W), _F32, dev, "w"), _dense(bias, (D,), _F32, dev, "bias"),
+        _dense(state, (n_slots, W - 1, D), dt, dev, "state"),
+        _dense(slots, (B,), torch.int32, dev, "slots"), n_slots, B, D, W, io, int(bool(silu)),
+        _pack_conv(_strides(x, "x")[0], 0, _strides(out, "out")[0], 0), out.data_ptr(),
+        _raw_stream(dev.index))
+    if rc:
+        _check(rc, "short_conv_step")
+    return out
+
+
 def device_status(stream=None) -> int:
     """Synchronises the stream; returns and clears the device status word."""
     return library().ttt_device_status(_stream(stream))
@@ -687,8 +1030,8 @@ def profile_start():
 
 def profile_stop():
     """Per launch kind: dict(name, kernel, launches, ms, flops, bytes, sm_ms)."""
-    arr = (ProfileEntry * 32)()
-    n = library().ttt_profile_stop(arr, 32)
+    arr = (ProfileEntry * 64)()
+    n = library().ttt_profile_stop(arr, 64)
     if n < 0:
         raise TTTError(n, "ttt_profile_stop")
     return [dict(name=e.name.decode(), kernel=e.kernel.decode(), launches=e.launches, ms=e.ms,

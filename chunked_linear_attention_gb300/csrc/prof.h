@@ -33,6 +33,15 @@ enum ProfTag : int {
   PT_DELTA_RECURRENT,
   PT_DELTA_STEP,
   PT_BLOCK_NORM,
+  PT_WIN_SIMT,
+  PT_WIN_STORE,
+  PT_WIN_STEP,
+  PT_SCAN_CARRY,
+  PT_SCAN_JOIN,
+  PT_SCAN,
+  PT_SCAN_STEP,
+  PT_CONV,
+  PT_CONV_STEP,
   PT_COUNT
 };
 

@@ -1,0 +1,486 @@
+// The selective state space scan: whole sequences, and single tokens on a pool of
+// states.  Per channel, with a state h of S numbers and r = softplus(dt + bias),
+//     h <- exp(r A) h + r x B_t,   y_t = (C_t . h + Dx x) z sigmoid(z).
+//
+// The channels are independent; so are the numbers of a state until y sums over them.
+// A thread holds CPT neighbouring channels x SPT numbers of the state, and L lanes one
+// channel's state; B and C of some tokens are in shared memory as fp32, for all channels
+// of a group.  With A' = A log2(e) each element of the state costs one base-2 exponential
+// and four fp32 operations, issued in pairs: the exponentials (32 a clock and SM) and
+// the fp32 pipe (128) are full at the same time.
+//
+// Few long sequences would leave most of the card idle (a token follows the one
+// before), so the token axis is cut into segments.  A segment maps the state that it
+// begins with to exp(R A) h + l, with R the sum of its r and l its end state from
+// zero; the carry pass finds l and R for all segments at once, the join pass the states at
+// the segments' starts one after the other, and the output pass runs all segments at
+// once.  The carry makes every exponential twice; it is taken where the channels alone
+// do not fill the card.
+//
+// Packed sequences lie on the token axis as they are: a segment in which a sequence
+// begins ends with a state that knows nothing of what came before the segment.
+#include <climits>
+
+#include "mixers.cuh"
+#include "mixers.h"
+#include "prof.h"
+
+namespace ttt {
+
+namespace {
+
+constexpr int kScanThreads = 128;
+constexpr int kScanSms = 152;
+constexpr float kLog2e = 1.44269504088896341f;
+
+struct ScanParams {
+  const void* x;
+  const void* dt;
+  const float* A;
+  const void* Bm;
+  const void* Cm;
+  const float* Dx;
+  const float* dt_bias;
+  const void* z;
+  const float* state_in;
+  const int* starts;
+  void* out;
+  float* state_out;
+  float* seg_state;    // [B][segs][D][S]: end states from zero, then start states
+  float* seg_sum;      // [B][segs][D]: sums of r, for exp(R A)
+  int* seg_new;        // [B][segs]: a sequence begins, or a token is in none, in the segment
+  int* status;
+  int n_seq, N, D, S, G, segs, seg_tokens, blocks;   // channel blocks per group
+  int softplus;
+  selective_scan_layout lay;
+};
+
+template <int L>
+__device__ __forceinline__ float sum_over(float x) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+template <typename T, int CPT, int SPT, int L, bool CARRY, bool VEC>
+__global__ void __launch_bounds__(kScanThreads) selective_scan_kernel(
+    const __grid_constant__ ScanParams p) {
+  constexpr int TT = 16;                           // tokens of B and C in shared memory
+  constexpr int SP = SPT * L;                      // padded S
+  constexpr int CH = kScanThreads / L * CPT;       // channels of this CTA
+  __shared__ __align__(16) float bc[TT][CARRY ? 1 : 2][SP];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int seg = blockIdx.x, b = blockIdx.z;
+  const int g = blockIdx.y / p.blocks, blk = blockIdx.y % p.blocks;
+  const int Dg = p.D / p.G, tid = threadIdx.x, l = tid % L;
+  const int cg = blk * CH + tid / L * CPT;         // first channel, in the group
+  const int n = VEC ? (cg < Dg ? CPT : 0) : max(0, min(CPT, Dg - cg));
+  const int c = n > 0 ? g * Dg + cg : g * Dg;      // idle threads read along and store nothing
+  if (seg == 0 && blockIdx.y == 0 && b == 0 && p.starts && !CARRY)
+    check_starts(p.starts, p.n_seq, p.N, p.status);
+  const T* x = static_cast<const T*>(p.x) + b * p.lay.x.batch + c;
+  const T* dt = static_cast<const T*>(p.dt) + b * p.lay.dt.batch + c;
+  const T* z = CARRY || !p.z ? nullptr : static_cast<const T*>(p.z) + b * p.lay.z.batch + c;
+  T* out = static_cast<T*>(p.out) + b * p.lay.out.batch + c;
+  const T* Bm = static_cast<const T*>(p.Bm) + b * p.lay.B.batch + (long long)g * p.S;
+  const T* Cm = static_cast<const T*>(p.Cm) + b * p.lay.C.batch + (long long)g * p.S;
+
+  F2 A[CPT][SPT / 2], h[CPT][SPT / 2];
+  float bias[CPT], dx[CPT], sum[CPT];
+#pragma unroll
+  for (int e = 0; e < CPT; ++e) {
+    bias[e] = p.dt_bias && e < n ? p.dt_bias[c + e] : 0.f;
+    dx[e] = p.Dx && e < n ? p.Dx[c + e] : 0.f;
+    sum[e] = 0.f;
+#pragma unroll
+    for (int s = 0; s < SPT; s += 2) {
+      float a[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        a[i] = e < n && l * SPT + s + i < p.S
+                   ? p.A[(long long)(c + e) * p.S + l * SPT + s + i] * kLog2e : 0.f;
+      A[e][s / 2] = pack2(a[0], a[1]);
+      h[e][s / 2] = 0ull;
+    }
+  }
+  auto load_state = [&](const float* src) {   // [D][S] of one sequence or segment, or NULL
+#pragma unroll
+    for (int e = 0; e < CPT; ++e)
+#pragma unroll
+      for (int s = 0; s < SPT; s += 2) {
+        float v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          v[i] = src && e < n && l * SPT + s + i < p.S
+                     ? src[(long long)(c + e) * p.S + l * SPT + s + i] : 0.f;
+        h[e][s / 2] = pack2(v[0], v[1]);
+      }
+  };
+  auto store_state = [&](float* dst) {
+#pragma unroll
+    for (int e = 0; e < CPT; ++e)
+#pragma unroll
+      for (int s = 0; s < SPT; s += 2) {
+        float v[2];
+        unpack2(h[e][s / 2], v[0], v[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (e < n && l * SPT + s + i < p.S)
+            dst[(long long)(c + e) * p.S + l * SPT + s + i] = v[i];
+      }
+  };
+  const long long one = (long long)p.D * p.S;
+
+  // the states of empty sequences, spread over the segments
+  if (!CARRY && p.state_out && p.starts)
+    for (int s = seg; s < p.n_seq; s += p.segs)
+      if (p.starts[s] == p.starts[s + 1]) {
+        load_state(p.state_in ? p.state_in + s * one : nullptr);
+        store_state(p.state_out + s * one);
+      }
+
+  const long long first = (long long)seg * p.seg_tokens;
+  const int end = (int)min(first + p.seg_tokens, (long long)p.N);
+  int t = (int)first;
+  bool fresh = false;   // the state knows nothing of what came before the segment
+  if (!CARRY && seg > 0) load_state(p.seg_state + ((long long)b * p.segs + seg) * one);
+  else load_state(nullptr);
+
+  while (t < end) {
+    const TokenSeq sq = token_seq(p.starts, p.n_seq, b, p.N, t);
+    if (sq.seq < 0) {
+      fresh = true;
+      // before the first and behind the last sequence in one go
+      if (t < p.starts[0]) t = min(end, p.starts[0]);
+      else if (t >= p.starts[p.n_seq]) t = end;
+      else ++t;
+      continue;
+    }
+    if (t == sq.t0) {
+      load_state(p.state_in ? p.state_in + sq.seq * one : nullptr);
+      fresh = true;
+    }
+    const int stop = min(end, sq.t1);
+    for (; t < stop; t += TT) {
+      const int m = min(TT, stop - t);
+      __syncthreads();
+      for (int e = tid; e < m * SP; e += kScanThreads) {
+        const int j = e / SP, s = e % SP;
+        bc[j][0][s] = s < p.S ? to_f<T>(Bm[(t + j) * p.lay.B.token + s]) : 0.f;
+        if (!CARRY) bc[j][CARRY ? 0 : 1][s] = s < p.S ? to_f<T>(Cm[(t + j) * p.lay.C.token + s]) : 0.f;
+      }
+      __syncthreads();
+      for (int j = 0; j < m; ++j) {
+        float xv[CPT], r[CPT], y[CPT], zv[CPT];
+        load_row<T, CPT, VEC>(x + (t + j) * p.lay.x.token, n, xv);
+        load_row<T, CPT, VEC>(dt + (t + j) * p.lay.dt.token, n, r);
+        if (z) load_row<T, CPT, VEC>(z + (t + j) * p.lay.z.token, n, zv);
+        F2 acc[CPT];
+#pragma unroll
+        for (int e = 0; e < CPT; ++e) {
+          r[e] += bias[e];
+          if (p.softplus) r[e] = softplus_f(r[e]);
+          if (CARRY) sum[e] += r[e];
+          const F2 rr = pack2(r[e], r[e]);
+          const float u = r[e] * xv[e];
+          const F2 uu = pack2(u, u);
+          acc[e] = 0ull;
+#pragma unroll
+          for (int s = 0; s < SPT / 2; ++s) {
+            float a0, a1;
+            unpack2(mul2(rr, A[e][s]), a0, a1);
+            const F2 a = pack2(ex2(a0), ex2(a1));
+            const F2 Bv = *reinterpret_cast<const F2*>(&bc[j][0][l * SPT + 2 * s]);
+            h[e][s] = fma2(a, h[e][s], mul2(uu, Bv));
+            if (!CARRY)
+              acc[e] = fma2(*reinterpret_cast<const F2*>(&bc[j][CARRY ? 0 : 1][l * SPT + 2 * s]), h[e][s], acc[e]);
+          }
+        }
+        if (!CARRY) {
+#pragma unroll
+          for (int e = 0; e < CPT; ++e) {
+            float a0, a1;
+            unpack2(acc[e], a0, a1);
+            y[e] = sum_over<L>(a0 + a1) + dx[e] * xv[e];
+            if (z) y[e] *= silu_f(zv[e]);
+          }
+          if (l == 0 && n > 0)
+            store_row<T, CPT, VEC>(out + (t + j) * p.lay.out.token, n, y);
+        }
+      }
+    }
+    t = stop;
+    if (!CARRY && p.state_out && stop == sq.t1) store_state(p.state_out + sq.seq * one);
+  }
+  if (CARRY) {
+    const long long at = (long long)b * p.segs + seg;
+    store_state(p.seg_state + at * one);
+    if (l == 0) {
+#pragma unroll
+      for (int e = 0; e < CPT; ++e)
+        if (e < n) p.seg_sum[at * p.D + c + e] = sum[e];
+    }
+    if (blockIdx.y == 0 && tid == 0) p.seg_new[at] = fresh;
+  }
+}
+
+// The start states of the segments 1, 2, ..: one thread per number of the state.
+__global__ void __launch_bounds__(256) scan_join_kernel(const __grid_constant__ ScanParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long one = (long long)p.D * p.S;
+  const long long i = blockIdx.x * 256ll + threadIdx.x;
+  if (i >= one) return;
+  const int b = blockIdx.y;
+  const float A = p.A[i] * kLog2e;
+  float* st = p.seg_state + (long long)b * p.segs * one + i;
+  const float* sum = p.seg_sum + (long long)b * p.segs * p.D + i / p.S;
+  const int* fresh = p.seg_new + (long long)b * p.segs;
+  float h = 0.f;
+  constexpr int U = 8;   // segments whose numbers are on their way together
+  for (int j = 0; j < p.segs - 1; j += U) {
+    float l[U], f[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const bool in = j + k < p.segs - 1;
+      l[k] = in ? st[(j + k) * one] : 0.f;
+      f[k] = in && !fresh[j + k] ? ex2(A * sum[(long long)(j + k) * p.D]) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (j + k >= p.segs - 1) break;
+      if (j + k > 0) st[(j + k) * one] = h;
+      h = f[k] == 0.f ? l[k] : fmaf(f[k], h, l[k]);
+    }
+  }
+  st[(p.segs - 1) * one] = h;
+}
+
+struct ScanShape {
+  int cpt, spt, lanes;   // a thread's channels and numbers, lanes per channel
+  int segs, seg_tokens, blocks;
+};
+
+ScanShape scan_shape(int B, int N, int D, int S, int G) {
+  ScanShape s;
+  // Many channels and tokens: four channels a thread, so that each number of B and C from
+  // shared memory serves four.  Otherwise one channel over S / 4 lanes, so that a token takes
+  // little time.
+  const long long work = (long long)B * N * D;
+  if (work >= 1 << 21 && D / G >= 128) {
+    s.cpt = 4;
+    s.spt = S <= 8 ? 8 : 16;
+  } else {
+    s.cpt = 1;
+    s.spt = 4;
+  }
+  s.lanes = 1;
+  while (s.spt * s.lanes < S) s.lanes *= 2;
+  const int ch = kScanThreads / s.lanes * s.cpt;
+  s.blocks = (D / G + ch - 1) / ch;
+  // two rounds of CTAs on every SM, no segment shorter than 64 tokens
+  const long long ctas = (long long)B * G * s.blocks;
+  long long segs = ctas >= kScanSms ? 1 : (4ll * kScanSms + ctas - 1) / ctas;
+  const long long most = (N + 63) / 64;
+  if (segs > most) segs = most;
+  if (segs < 3) segs = 1;   // two segments carry as long as one runs
+  s.seg_tokens = (int)(((N + segs - 1) / segs + 15) / 16 * 16);
+  s.segs = (N + s.seg_tokens - 1) / s.seg_tokens;
+  return s;
+}
+
+template <typename T, int CPT, int SPT, int L>
+int launch_scan(const ScanArgs& a, ScanParams p, const ScanShape& s) {
+  constexpr int E = CPT;
+  const unsigned bytes = E * sizeof(T);
+  auto ok = [&](const void* ptr, const mixer_stride& st) {
+    return (reinterpret_cast<uintptr_t>(ptr) & (bytes - 1)) == 0 && st.batch % E == 0 &&
+           st.token % E == 0;
+  };
+  const bool vec = CPT > 1 && (a.D / a.G) % E == 0 && ok(a.x, a.lay.x) && ok(a.dt, a.lay.dt) &&
+                   (!a.z || ok(a.z, a.lay.z)) && ok(a.out, a.lay.out);
+  const double n = (double)a.B * a.N * a.D;
+  if (s.segs > 1) {
+    {
+      ProfScope ps(PT_SCAN_CARRY, a.stream, 4.0 * n * a.S, 2.0 * n * sizeof(T));
+      const dim3 grid(s.segs - 1, a.G * s.blocks, a.B);
+      const cudaError_t e =
+          vec ? launch_grid(selective_scan_kernel<T, CPT, SPT, L, true, CPT != 1>, grid, kScanThreads, 0, a.stream, p)
+              : launch_grid(selective_scan_kernel<T, CPT, SPT, L, true, false>, grid, kScanThreads, 0, a.stream, p);
+      if (e != cudaSuccess) return TTT_ERR_CUDA;
+    }
+    const long long one = (long long)a.D * a.S;
+    ProfScope ps(PT_SCAN_JOIN, a.stream, 2.0 * a.B * s.segs * one, 8.0 * a.B * s.segs * one);
+    if (launch_grid(scan_join_kernel, dim3((unsigned)((one + 255) / 256), a.B), 256, 0, a.stream, p) != cudaSuccess)
+      return TTT_ERR_CUDA;
+  }
+  ProfScope ps(PT_SCAN, a.stream, 6.0 * n * a.S, (a.z ? 4.0 : 3.0) * n * sizeof(T));
+  const dim3 grid(s.segs, a.G * s.blocks, a.B);
+  const cudaError_t e =
+      vec ? launch_grid(selective_scan_kernel<T, CPT, SPT, L, false, CPT != 1>, grid, kScanThreads, 0, a.stream, p)
+          : launch_grid(selective_scan_kernel<T, CPT, SPT, L, false, false>, grid, kScanThreads, 0, a.stream, p);
+  return e == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+}
+
+template <typename T, int CPT, int SPT>
+int scan_lanes(const ScanArgs& a, const ScanParams& p, const ScanShape& s) {
+  if (s.lanes == 1) return launch_scan<T, CPT, SPT, 1>(a, p, s);
+  if constexpr (SPT != 8) {   // 8 numbers a thread serve S <= 8 alone
+    if (s.lanes == 2) return launch_scan<T, CPT, SPT, 2>(a, p, s);
+    if (s.lanes == 4) return launch_scan<T, CPT, SPT, 4>(a, p, s);
+    if (s.lanes == 8) return launch_scan<T, CPT, SPT, 8>(a, p, s);
+    if constexpr (SPT == 4) {
+      if (s.lanes == 16) return launch_scan<T, CPT, SPT, 16>(a, p, s);
+      if (s.lanes == 32) return launch_scan<T, CPT, SPT, 32>(a, p, s);
+    }
+  }
+  return TTT_ERR_UNSUPPORTED;
+}
+
+template <typename T>
+int scan_t(const ScanArgs& a, const ScanParams& p, const ScanShape& s) {
+  if (s.cpt == 1) return scan_lanes<T, 1, 4>(a, p, s);
+  if (s.spt == 8) return scan_lanes<T, 4, 8>(a, p, s);
+  return scan_lanes<T, 4, 16>(a, p, s);
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// ------------------------------------------------------------ single tokens
+struct ScanStepParams {
+  const void* x;
+  const void* dt;
+  const float* A;
+  const void* Bm;
+  const void* Cm;
+  const float* Dx;
+  const float* dt_bias;
+  const void* z;
+  float* state;
+  const int* slots;
+  void* out;
+  int* status;
+  int n_slots, D, S, G, softplus;
+  selective_scan_layout lay;
+};
+
+// Four numbers of a state a thread, L lanes a channel; bound by HBM, the states' bytes
+// twice.
+template <typename T, int L, bool VEC>
+__global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ ScanStepParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int b = blockIdx.y, l = threadIdx.x % L;
+  const int c = blockIdx.x * (128 / L) + threadIdx.x / L;
+  const int slot = row_slot(p.slots, p.n_slots, b, p.status);
+  const bool in = c < p.D;
+  T* out = static_cast<T*>(p.out) + b * p.lay.out.batch + c;
+  if (slot < 0) {
+    if (in && l == 0) *out = from_f<T>(0.f);
+    return;
+  }
+  const int g = in ? c / (p.D / p.G) : 0, s0 = l * 4;
+  const T* Bm = static_cast<const T*>(p.Bm) + b * p.lay.B.batch + (long long)g * p.S;
+  const T* Cm = static_cast<const T*>(p.Cm) + b * p.lay.C.batch + (long long)g * p.S;
+  float* st = p.state + ((long long)slot * p.D + c) * p.S + s0;
+  const float* A = p.A + (long long)c * p.S + s0;
+  float h[4], a[4], acc = 0.f;
+  const int n = in ? min(4, p.S - s0) : 0;
+  load_row<float, 4, VEC>(st, n, h);
+  load_row<float, 4, VEC>(A, n, a);
+  float xv = 0.f, r = 0.f, zv = 0.f;
+  if (in) {
+    xv = to_f<T>(static_cast<const T*>(p.x)[b * p.lay.x.batch + c]);
+    r = to_f<T>(static_cast<const T*>(p.dt)[b * p.lay.dt.batch + c]);
+    if (p.dt_bias) r += p.dt_bias[c];
+    if (p.z) zv = to_f<T>(static_cast<const T*>(p.z)[b * p.lay.z.batch + c]);
+  }
+  if (p.softplus) r = softplus_f(r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float Bv = i < n ? to_f<T>(Bm[s0 + i]) : 0.f, Cv = i < n ? to_f<T>(Cm[s0 + i]) : 0.f;
+    h[i] = fmaf(ex2(r * (a[i] * kLog2e)), h[i], r * xv * Bv);
+    acc = fmaf(Cv, h[i], acc);
+  }
+  if (n > 0) store_row<float, 4, VEC>(st, n, h);
+  acc = sum_over<L>(acc);
+  if (in && l == 0) {
+    if (p.Dx) acc = fmaf(p.Dx[c], xv, acc);
+    if (p.z) acc *= silu_f(zv);
+    *out = from_f<T>(acc);
+  }
+}
+
+template <typename T, int L>
+int launch_scan_step(const ScanStepArgs& a, const ScanStepParams& p) {
+  const int per = 128 / L;
+  const dim3 grid((a.D + per - 1) / per, a.B);
+  const double n = (double)a.B * a.D * a.S;
+  ProfScope ps(PT_SCAN_STEP, a.stream, 6.0 * n, 8.0 * n);
+  // the lanes' four numbers lie in one 16-byte piece where S is 4 L
+  const bool vec = a.S == 4 * L && (reinterpret_cast<uintptr_t>(a.state) & 15) == 0 &&
+                   (reinterpret_cast<uintptr_t>(a.A) & 15) == 0 && a.D % per == 0;
+  const cudaError_t e = vec ? launch_grid(scan_step_kernel<T, L, true>, grid, 128, 0, a.stream, p)
+                            : launch_grid(scan_step_kernel<T, L, false>, grid, 128, 0, a.stream, p);
+  return e == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+}
+
+template <typename T>
+int scan_step_t(const ScanStepArgs& a, const ScanStepParams& p) {
+  if (a.S <= 4) return launch_scan_step<T, 1>(a, p);
+  if (a.S <= 8) return launch_scan_step<T, 2>(a, p);
+  if (a.S <= 16) return launch_scan_step<T, 4>(a, p);
+  if (a.S <= 32) return launch_scan_step<T, 8>(a, p);
+  if (a.S <= 64) return launch_scan_step<T, 16>(a, p);
+  return launch_scan_step<T, 32>(a, p);
+}
+
+}  // namespace
+
+size_t selective_scan_workspace(int B, int N, int D, int S, int G, int n_seq, int bf16) {
+  (void)n_seq;
+  (void)bf16;
+  const ScanShape s = scan_shape(B, N, D, S, G);
+  if (s.segs == 1) return 0;
+  const size_t k = (size_t)B * s.segs;
+  return align256(k * D * S * 4) + align256(k * D * 4) + align256(k * 4);
+}
+
+int selective_scan_launch(const ScanArgs& a) {
+  const ScanShape s = scan_shape(a.B, a.N, a.D, a.S, a.G);
+  ScanParams p{};
+  p.x = a.x; p.dt = a.dt; p.A = a.A; p.Bm = a.Bm; p.Cm = a.Cm; p.Dx = a.Dx;
+  p.dt_bias = a.dt_bias; p.z = a.z; p.state_in = a.state_in;
+  p.starts = a.seq_starts;
+  p.out = a.out;
+  p.state_out = a.state_out;
+  p.status = a.status;
+  p.n_seq = a.n_seq; p.N = a.N; p.D = a.D; p.S = a.S; p.G = a.G;
+  p.segs = s.segs; p.seg_tokens = s.seg_tokens; p.blocks = s.blocks;
+  p.softplus = a.softplus;
+  p.lay = a.lay;
+  char* ws = static_cast<char*>(a.workspace);
+  const size_t k = (size_t)a.B * s.segs;
+  p.seg_state = reinterpret_cast<float*>(ws);
+  ws += align256(k * a.D * a.S * 4);
+  p.seg_sum = reinterpret_cast<float*>(ws);
+  ws += align256(k * a.D * 4);
+  p.seg_new = reinterpret_cast<int*>(ws);
+  return a.bf16 ? scan_t<__nv_bfloat16>(a, p, s) : scan_t<float>(a, p, s);
+}
+
+int selective_scan_step_launch(const ScanStepArgs& a) {
+  ScanStepParams p{};
+  p.x = a.x; p.dt = a.dt; p.A = a.A; p.Bm = a.Bm; p.Cm = a.Cm; p.Dx = a.Dx;
+  p.dt_bias = a.dt_bias; p.z = a.z; p.state = a.state;
+  p.slots = a.slots;
+  p.out = a.out;
+  p.status = a.status;
+  p.n_slots = a.n_slots; p.D = a.D; p.S = a.S; p.G = a.G;
+  p.softplus = a.softplus;
+  p.lay = a.lay;
+  return a.bf16 ? scan_step_t<__nv_bfloat16>(a, p) : scan_step_t<float>(a, p);
+}
+
+}  // namespace ttt
