@@ -143,7 +143,8 @@ int window_attention_forward(const void* q, const void* k, const void* v, void* 
   a.status = st;
   a.wait_ns = ttt::capi_wait_limit_ns();
   a.stream = reinterpret_cast<cudaStream_t>(stream);
-  rc = ttt::window_attention_simt(a);
+  rc = ttt::window_attention_tc(a);
+  if (rc == 1) rc = ttt::window_attention_simt(a);
   if (rc == TTT_OK && cache_k) rc = ttt::window_attention_store(a);
   return rc;
 }

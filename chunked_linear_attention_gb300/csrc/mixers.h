@@ -29,6 +29,9 @@ struct WindowArgs {
 
 // Every type, size and stride, in fp32.  Returns a ttt_status.
 int window_attention_simt(const WindowArgs& a);
+// On the tensor cores (bf16, d <= 128, aligned strides, scale > 0).  Returns 1 where it
+// does not apply, else a ttt_status.
+int window_attention_tc(const WindowArgs& a);
 // The new keys and values into the caches, behind the attention.
 int window_attention_store(const WindowArgs& a);
 

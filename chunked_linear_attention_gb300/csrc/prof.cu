@@ -26,7 +26,7 @@ const char* kTagName[PT_COUNT] = {
     "norm", "lin.scale", "gemm.lin_partial", "lin.prefix", "gemm.lin_out", "gemm.selftest", "muon.cluster",
     "muon.half", "lin.fused", "gemm.apply_proj", "gemm.apply_out", "gemm.featurize",
     "delta.plan", "delta.prep", "delta.carry", "delta.join", "delta.chunk", "delta.recurrent", "delta.step", "block.norm",
-    "window.simt", "window.store", "window.step", "scan.carry", "scan.join", "scan.out",
+    "window.tc", "window.simt", "window.store", "window.step", "scan.carry", "scan.join", "scan.out",
     "scan.step", "conv", "conv.step"};
 const char* kTagKernel[PT_COUNT] = {
     "init_layer_kernel", "umma_gemm_kernel", "umma_gemm_kernel", "umma_gemm_kernel",
@@ -35,7 +35,7 @@ const char* kTagKernel[PT_COUNT] = {
     "ns_cluster_kernel", "ns_half_kernel", "linattn_fused_kernel",
     "umma_gemm_kernel", "umma_gemm_kernel", "umma_gemm_kernel", "delta_plan_kernel",
     "delta_prep_kernel", "delta_carry_kernel", "delta_join_kernel", "delta_scan_kernel",
-    "delta_recurrent_kernel", "delta_step_kernel", "block_norm_kernel", "window_attention_kernel",
+    "delta_recurrent_kernel", "delta_step_kernel", "block_norm_kernel", "window_tc_kernel", "window_attention_kernel",
     "window_store_kernel", "window_step_kernel", "selective_scan_kernel", "scan_join_kernel",
     "selective_scan_kernel", "scan_step_kernel", "short_conv_kernel", "conv_step_kernel"};
 

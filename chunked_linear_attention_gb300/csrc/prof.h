@@ -33,6 +33,7 @@ enum ProfTag : int {
   PT_DELTA_RECURRENT,
   PT_DELTA_STEP,
   PT_BLOCK_NORM,
+  PT_WIN_TC,
   PT_WIN_SIMT,
   PT_WIN_STORE,
   PT_WIN_STEP,

@@ -85,6 +85,7 @@ __device__ __forceinline__ bool sees_new(const WinRow& r, int j, int end) {
 // on, of which those behind the sinks are a ring whose newest lap ends before `head`.
 struct WinCache {
   int seq, slot, count, past, head;
+  int i0, i1;   // the sequence's queries in the tile
 };
 
 __device__ __forceinline__ bool sees_cache(const WinRow& r, const WinCache& c, int place, int sinks,
@@ -185,6 +186,8 @@ __device__ __forceinline__ bool win_next(const WinParams& p, WinList& w, WinTile
     seq_past(p, w.seq, w.c.slot, w.c.past);
     if (w.c.past <= 0) continue;
     w.c.seq = w.seq;
+    w.c.i0 = a;
+    w.c.i1 = e;
     const int ring = w.c.past - p.sinks;   // tokens that went into the ring
     w.c.head = ring > 0 ? ring % p.window : 0;
     w.c.count = min(w.c.past, p.sinks);
@@ -198,5 +201,7 @@ __device__ __forceinline__ bool win_next(const WinParams& p, WinList& w, WinTile
   w.place += w.KT;
   return true;
 }
+
+WinParams win_params(const WindowArgs& a);
 
 }  // namespace ttt

@@ -1,0 +1,648 @@
+// Window attention on the tensor cores: bf16, d <= 128.
+//
+// A block has 256 queries of one head, as two tiles of 128 rows that share the key tiles
+// of 128 (win_attn.cuh has the list).  Per key tile and query tile
+//     S = Q K^T      (128 x 128, fp32 in TMEM)
+//     P = exp2(c S - c m),  l += sum P     (c = scale log2 e; one thread per row)
+//     O += P V       (P as bf16 in the TMEM columns that S had)
+// with m the row's largest score so far.  O is only rescaled, in TMEM, when a row's
+// largest score has grown by more than 8 / c since the last time: until then its weights
+// are at most 2^8 too large, and so are their sums.  P is rounded to bf16 (2^-8 of each
+// weight) as the operand of the second product; l sums what was not rounded.
+//
+// What bounds it: per pair of tiles the products take 1024 clocks of the tensor core
+// (d 128) and the exponentials 1024 of the special-function units (32 a clock), so
+// the two tiles work in turn: while one's products run, the other's weights are made.
+//
+// A value that a query does not see still meets its weight 0 in P V, where NaN or
+// infinity would spoil the row.  So outputs that are not finite are computed again, from
+// the keys that the row sees alone (which leaves what is really NaN or infinite).
+//
+// Roles (384 threads, one block per SM, persistent over (tile pair, head)):
+//   warp 0      TMA: Q, and K and V through a ring of tiles.
+//   warp 1      all products.
+//   warps 4-7   rows of the first tile, warps 8-11 of the second: softmax, rescaling,
+//               outputs.
+#include <mutex>
+
+#include "builder.h"
+#include "prof.h"
+#include "win_attn.cuh"
+
+namespace ttt {
+
+namespace {
+
+constexpr int kM = 128;                  // rows of a tile, keys of a key tile
+constexpr int kThreads = 384;
+constexpr int kRegsFew = 104, kRegsMany = 200;
+static_assert(128 * kRegsFew + 256 * kRegsMany <= kThreads * 168, "registers at launch");
+
+template <int DP>
+struct Plan {
+  static constexpr int kTile = kM * DP * 2;                  // bytes of a tile of Q, K or V
+  static constexpr int kStages = DP == 128 ? 5 : 10;
+  static constexpr int kSmem = 2 * kTile + kStages * kTile + 1024 + 512;
+};
+static_assert(Plan<128>::kSmem <= 227 * 1024 && Plan<64>::kSmem <= 227 * 1024, "shared memory");
+
+struct Bars {
+  uint64_t q_full, q_free;
+  uint64_t full[10], empty[10];
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t done;
+  uint32_t tmem;
+};
+static_assert(sizeof(Bars) <= 512, "control region");
+
+struct TcParams {
+  CUtensorMap q, k, v, ck, cv;
+  WinParams w;
+  int tiles;            // pairs of query tiles of the token axis
+  long long items;      // (batch, tile pair, head)
+  int wide_out;         // rows of out can be stored 16 bytes at a time
+};
+
+// The queries a .. e - 1 of one tile: which key tiles they need.
+struct SubTile {
+  int a, e, lo, s0, s1;
+};
+
+__device__ __forceinline__ SubTile sub_tile(const WinParams& p, int b, int a, int e) {
+  SubTile s;
+  s.a = a;
+  s.e = min(e, p.N);
+  const WinRow r = win_row(p, b, a);
+  s.lo = r.i >= 0 ? r.lo : max(0, a - p.window + 1);
+  s.s0 = r.i >= 0 ? r.t0 : 0;
+  s.s1 = r.i >= 0 ? r.sink1 : 0;
+  return s;
+}
+
+__device__ __forceinline__ bool needs(const SubTile& s, const WinTile& t) {
+  if (s.a >= s.e) return false;
+  if (t.seq >= 0) return max(s.a, t.c.i0) < min(s.e, t.c.i1);
+  return t.base < s.e &&
+         (t.base + kM > s.lo || (t.base < s.s1 && t.base + kM > s.s0));
+}
+
+struct Item {
+  int b, h, i0;
+};
+__device__ __forceinline__ Item get_item(const TcParams& p, long long n) {
+  Item it;
+  it.h = (int)(n % p.w.Hq);
+  const long long r = n / p.w.Hq;
+  it.i0 = (int)(r % p.tiles) * 2 * kM;
+  it.b = (int)(r / p.tiles);
+  return it;
+}
+
+__device__ __forceinline__ void umma_ts_w(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&w)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]),
+      "r"(w[8]), "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// The block's registers, from the warps that load and issue to those that hold rows.
+__device__ __forceinline__ void regs_few() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+}
+__device__ __forceinline__ void regs_many() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+// Bits of the columns x0 .. x1 - 1 among the 32 from `at` on.
+__device__ __forceinline__ uint32_t span_bits(int x0, int x1, int at) {
+  const int lo = max(x0 - at, 0), hi = min(x1 - at, 32);
+  if (lo >= hi) return 0u;
+  return (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
+}
+
+// One row again, from what it sees alone, by a whole warp: lanes share the keys, then the
+// output's columns.
+__device__ __noinline__ void row_alone(const TcParams& tp, int b, int h, int i0, int i) {
+  const WinParams& p = tp.w;
+  const int lane = threadIdx.x & 31, hk = h / (p.Hq / p.Hk);
+  using T = __nv_bfloat16;
+  const T* q = static_cast<const T*>(p.q) + b * p.lay.q.batch + h * p.lay.q.head + i * p.lay.q.token;
+  const T* k = static_cast<const T*>(p.k) + b * p.lay.k.batch + hk * p.lay.k.head;
+  const T* v = static_cast<const T*>(p.v) + b * p.lay.v.batch + hk * p.lay.v.head;
+  T* out = static_cast<T*>(p.out) + b * p.lay.out.batch + h * p.lay.out.head + i * p.lay.out.token;
+  bool fine = true;
+  for (int c = lane; c < p.d; c += 32) fine = fine && isfinite(to_f<T>(q[c]));
+  if (!__all_sync(0xffffffffu, fine)) {   // every score is NaN or infinite
+    for (int c = lane; c < p.d; c += 32) out[c] = from_f<T>(NAN);
+    return;
+  }
+  const WinRow row = win_row(p, b, i);
+  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  WinList w = win_list(p, b, i0, i0 + 2 * kM, kM);
+  WinTile t;
+  while (win_next(p, w, t)) {
+    const T *ks = k, *vs = v;
+    long long sk = p.lay.k.token, sv = p.lay.v.token;
+    if (t.seq >= 0) {
+      const long long at = ((long long)t.c.slot * p.Hk + hk) * (p.sinks + p.window) * p.d;
+      ks = static_cast<const T*>(p.cache_k) + at;
+      vs = static_cast<const T*>(p.cache_v) + at;
+      sk = sv = p.d;
+    }
+    for (int j0 = t.base; j0 < min(t.base + kM, t.end); j0 += 32) {
+      const int j = j0 + lane;
+      const bool in = j >= 0 && j < t.base + kM && j < t.end &&
+                      (t.seq < 0 ? sees_new(row, j, t.end)
+                                 : sees_cache(row, t.c, j, p.sinks, p.window));
+      float s = -INFINITY;
+      if (in) {
+        s = 0.f;
+        for (int c = 0; c < p.d; ++c) s = fmaf(to_f<T>(q[c]), to_f<T>(ks[j * sk + c]), s);
+        s *= p.scale;
+      }
+      float top = s;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn;
+      const float f = ex2(m - base);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] *= f;
+      const float x = in ? ex2(s - base) : 0.f;
+      unsigned seen = __ballot_sync(0xffffffffu, in);
+      while (seen) {
+        const int n = __ffs(seen) - 1;
+        seen &= seen - 1;
+        const float xn = __shfl_sync(0xffffffffu, x, n);
+        l += xn;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (lane + 32 * e < p.d) acc[e] = fmaf(xn, to_f<T>(vs[(j0 + n) * sv + lane + 32 * e]), acc[e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (lane + 32 * e < p.d) out[lane + 32 * e] = from_f<T>(acc[e] / l);
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_constant__ TcParams tp) {
+  using PL = Plan<DP>;
+  constexpr int NS = PL::kStages, TB = PL::kTile, NB = DP / 64;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* Q = smem;
+  uint8_t* ring = smem + 2 * TB;
+  Bars* B = reinterpret_cast<Bars*>(ring + NS * TB);
+  const WinParams& p = tp.w;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const unsigned long long lim = p.wait_ns;
+
+  if (tid == 0) {
+    mbar_init(&B->q_full, 1);
+    mbar_init(&B->q_free, 1);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&B->full[s], 1);
+      mbar_init(&B->empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&B->s_full[t], 1);
+      mbar_init(&B->p_full[t], kM);
+      mbar_init(&B->o_full[t], 1);
+      mbar_init(&B->o_free[t], kM);
+    }
+    mbar_init(&B->done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&B->tmem, 512);
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B->tmem;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- loads
+    regs_few();
+    if (blockIdx.x == 0 && p.starts) {   // reports bounds that are none
+      bool bad = false;
+      for (int i = lane; i < p.n_seq; i += 32) {
+        const int a = p.starts[i], e = p.starts[i + 1];
+        bad |= a < 0 || e < a || e > p.N;
+      }
+      if (bad) report_status(p.status, kStatusBadArg);
+    }
+    if (lane == 0) {
+      int fills = 0, q_loads = 0;
+      bool ok = true;
+      auto load = [&](const CUtensorMap* map, int y, int z, int w) {
+        const int s = fills % NS;
+        ok = ok && mbar_wait(&B->empty[s], ((fills / NS) & 1) ^ 1, p.status, lim);
+        if (!ok) return;
+        mbar_arrive_expect_tx(&B->full[s], TB);
+#pragma unroll
+        for (int x = 0; x < NB; ++x)
+          tma_load_4d(ring + s * TB + x * (kM * 128), map, x * 64, y, z, w, &B->full[s]);
+        ++fills;
+      };
+      for (long long n = blockIdx.x; n < tp.items && ok; n += gridDim.x) {
+        const Item it = get_item(tp, n);
+        const int hk = it.h / (p.Hq / p.Hk);
+        ok = mbar_wait(&B->q_free, (q_loads & 1) ^ 1, p.status, lim);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&B->q_full, 2 * TB);
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int x = 0; x < NB; ++x)
+            tma_load_4d(Q + t * TB + x * (kM * 128), &tp.q, x * 64, it.i0 + t * kM, it.h, it.b, &B->q_full);
+        ++q_loads;
+        const SubTile s0 = sub_tile(p, it.b, it.i0, it.i0 + kM);
+        const SubTile s1 = sub_tile(p, it.b, it.i0 + kM, it.i0 + 2 * kM);
+        WinList w = win_list(p, it.b, it.i0, it.i0 + 2 * kM, kM);
+        WinTile t;
+        while (ok && win_next(p, w, t)) {
+          if (!needs(s0, t) && !needs(s1, t)) continue;
+          const bool c = t.seq >= 0;
+          load(c ? &tp.ck : &tp.k, t.base, hk, c ? t.c.slot : it.b);
+          load(c ? &tp.cv : &tp.v, t.base, hk, c ? t.c.slot : it.b);
+        }
+      }
+      if (!ok) {   // what is on its way lands before the block ends
+        if (q_loads) mbar_wait(&B->q_full, (q_loads - 1) & 1, p.status, lim);
+        for (int k = 1; k <= NS && k <= fills; ++k)
+          mbar_wait(&B->full[(fills - k) % NS], ((fills - k) / NS) & 1, p.status, lim);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- products
+    regs_few();
+    const uint32_t id_s = idesc_bf16_f32(kM, 0, 0), id_o = idesc_bf16_f32(DP, 0, 1);
+    const uint64_t qd = smem_desc_sw128(smem_u32(Q), 16, 1024);
+    const uint64_t kd = smem_desc_sw128(smem_u32(ring), 16, 1024);
+    const uint64_t vd = smem_desc_sw128(smem_u32(ring), kM * 128, 1024);
+    int uses = 0, items = 0;            // ring tiles taken; query tiles taken
+    int np[2] = {0, 0}, no[2] = {0, 0}; // weights awaited, outputs begun
+    bool ok = true;
+    auto scores = [&](int t, int s) {   // S_t = Q_t K^T with K in ring stage s
+#pragma unroll
+      for (int k = 0; k < DP / 16; ++k) {
+        const uint32_t o = (k >> 2) * (kM * 8) + (k & 3) * 2;
+        umma_bf16_w(tmem + t * kM, qd + t * (TB >> 4) + o, kd + s * (TB >> 4) + o, id_s, k != 0);
+      }
+      umma_commit_w(&B->s_full[t]);
+    };
+    auto outputs = [&](int t, int s, bool first) {   // O_t += P_t V with V in stage s
+#pragma unroll
+      for (int k = 0; k < kM / 16; ++k)
+        umma_ts_w(tmem + 256 + t * kM, tmem + t * kM + k * 8, vd + s * (TB >> 4) + k * 128, id_o,
+                  !first || k != 0);
+    };
+    for (long long n = blockIdx.x; n < tp.items && ok; n += gridDim.x) {
+      const Item it = get_item(tp, n);
+      const SubTile st[2] = {sub_tile(p, it.b, it.i0, it.i0 + kM),
+                             sub_tile(p, it.b, it.i0 + kM, it.i0 + 2 * kM)};
+      ok = mbar_wait_w(&B->q_full, items & 1, p.status, lim);
+      ++items;
+      WinList w = win_list(p, it.b, it.i0, it.i0 + 2 * kM, kM);
+      WinTile t;
+      bool begun[2] = {false, false};
+      bool cur[2] = {false, false};     // the tile whose weights are awaited
+      int v_at = 0;                     // its V's place in the ring
+      bool more = true;
+      while (ok && (more || cur[0] || cur[1])) {
+        // the next tile that either needs
+        bool nxt[2] = {false, false};
+        more = false;
+        while (win_next(p, w, t)) {
+          nxt[0] = needs(st[0], t);
+          nxt[1] = needs(st[1], t);
+          if (nxt[0] || nxt[1]) {
+            more = true;
+            break;
+          }
+        }
+        if (!more) umma_commit_w(&B->q_free);   // all scores of this item are under way
+        const int k_at = uses;
+        bool k_here = false;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (cur[u]) {
+            ok = ok && mbar_wait_w(&B->p_full[u], np[u] & 1, p.status, lim);
+            ++np[u];
+            if (!begun[u]) {
+              ok = ok && mbar_wait_w(&B->o_free[u], (no[u] & 1) ^ 1, p.status, lim);
+              ++no[u];
+            }
+            if (!ok) break;
+            if (u == 0 || !cur[0])
+              ok = mbar_wait_w(&B->full[v_at % NS], (v_at / NS) & 1, p.status, lim);
+            if (!ok) break;
+            tc_fence_after();
+            outputs(u, v_at % NS, !begun[u]);
+            begun[u] = true;
+          }
+          if (u == 1 && (cur[0] || cur[1])) umma_commit_w(&B->empty[v_at % NS]);
+          if (nxt[u]) {
+            if (!k_here) {
+              ok = mbar_wait_w(&B->full[k_at % NS], (k_at / NS) & 1, p.status, lim);
+              if (!ok) break;
+              tc_fence_after();
+              k_here = true;
+            }
+            scores(u, k_at % NS);
+          }
+        }
+        if (!ok) break;
+        if (more) {
+          umma_commit_w(&B->empty[k_at % NS]);
+          v_at = k_at + 1;
+          uses = k_at + 2;
+        }
+        cur[0] = more && nxt[0];
+        cur[1] = more && nxt[1];
+      }
+      if (!ok) break;
+      for (int u = 0; u < 2; ++u)
+        if (begun[u]) umma_commit_w(&B->o_full[u]);
+    }
+    if (!ok) {   // the products under way end before their TMEM is given back
+      umma_commit_w(&B->done);
+      mbar_wait_w(&B->done, 0, p.status, lim);
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- rows
+    regs_many();
+    const int t = (warp - 4) >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t S = tmem + t * kM + lanes, O = tmem + 256 + t * kM + lanes;
+    const float c = p.scale, grow = 8.f / c;
+    const F2 c2 = pack2(c, c);
+    int ns = 0, no = 0;
+    bool ok = true;
+    for (long long n = blockIdx.x; n < tp.items && ok; n += gridDim.x) {
+      const Item it = get_item(tp, n);
+      const SubTile st = sub_tile(p, it.b, it.i0 + t * kM, it.i0 + (t + 1) * kM);
+      if (st.a >= st.e) continue;
+      WinRow row = win_row(p, it.b, st.a + r);
+      const bool live = row.i >= 0;
+      if (!live) {   // stored nowhere: sees what there is
+        row.i = 0x7fffffff;
+        row.lo = row.t0 = 0;
+        row.wlo = -0x40000000;
+      }
+      const int i_min = __reduce_min_sync(0xffffffffu, row.i);
+      const int lo_max = __reduce_max_sync(0xffffffffu, row.lo);
+      float m = -INFINITY, l = 0.f;
+      bool begun = false;
+      WinList w = win_list(p, it.b, it.i0, it.i0 + 2 * kM, kM);
+      WinTile kt;
+      while (win_next(p, w, kt)) {
+        if (!needs(st, kt)) continue;
+        ok = mbar_wait_w(&B->s_full[t], ns & 1, p.status, lim);
+        if (!ok) break;
+        ++ns;
+        tc_fence_after();
+        float s[4][32];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tmem_ld32(S + 32 * x, s[x]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tmem_wait32(s[x]);
+        const bool whole = kt.seq < 0 && kt.base >= lo_max && kt.base + kM - 1 <= i_min &&
+                           kt.base + kM <= kt.end;
+        if (!whole) {
+          // up to three spans of columns that the row sees
+          int a0, a1, b0, b1, c0 = 0, c1 = 0;
+          if (kt.seq < 0) {
+            const int top = min(row.i == 0x7fffffff ? row.i : row.i + 1, kt.end);
+            a0 = max(row.lo, 0) - kt.base;
+            a1 = top - kt.base;
+            b0 = row.t0 - kt.base;
+            b1 = min(row.sink1, top) - kt.base;
+            if (row.t0 == 0x7fffffff) b1 = b0;
+          } else {
+            // places of the ring up to the head are of the newest lap, the others of the one
+            // before
+            const int x = row.wlo - kt.c.past + kt.c.head, sk = p.sinks;
+            a0 = -kt.base;
+            a1 = min(sk, kt.c.count) - kt.base;
+            b0 = sk + max(x, 0) - kt.base;
+            b1 = min(sk + kt.c.head, kt.c.count) - kt.base;
+            c0 = sk + max(x + p.window, kt.c.head) - kt.base;
+            c1 = kt.c.count - kt.base;
+            if (live && row.seq != kt.c.seq) a1 = b1 = c1 = -1;
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t bits = span_bits(a0, a1, 32 * x) | span_bits(b0, b1, 32 * x) |
+                                  span_bits(c0, c1, 32 * x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[x][e] = (bits >> e) & 1 ? s[x][e] : -INFINITY;
+          }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(s[x][e], s[x][e + 1]));
+        if (!begun) {
+          m = top;
+        } else if (__any_sync(0xffffffffu, top > m + grow)) {
+          const float f = top > m + grow ? ex2((m - top) * c) : 1.f;
+          if (top > m + grow) m = top;
+          l *= f;
+#pragma unroll
+          for (int x = 0; x < DP / 16; ++x) {
+            float o[16];
+            tmem_ld16_nowait(O + 16 * x, o);
+            tmem_wait_bind(o);
+            uint32_t ow[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e] * f);
+            tmem_st16(O + 16 * x, ow);
+          }
+        }
+        begun = true;
+        const float mc = m == -INFINITY ? 0.f : m * c;
+        const F2 mc2 = pack2(-mc, -mc);
+        F2 sum0 = 0ull, sum1 = 0ull;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t pw[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float v0, v1, v2, v3;
+            unpack2(fma2(pack2(s[x][e], s[x][e + 1]), c2, mc2), v0, v1);
+            unpack2(fma2(pack2(s[x][e + 2], s[x][e + 3]), c2, mc2), v2, v3);
+            v0 = ex2(v0);
+            v1 = ex2(v1);
+            v2 = ex2(v2);
+            v3 = ex2(v3);
+            sum0 = add2(sum0, pack2(v0, v1));
+            sum1 = add2(sum1, pack2(v2, v3));
+            pw[e / 2] = bf16_pair(v0, v1);
+            pw[e / 2 + 1] = bf16_pair(v2, v3);
+          }
+          tmem_st16(S + 16 * x, pw);
+        }
+        float x0, x1;
+        unpack2(add2(sum0, sum1), x0, x1);
+        l += x0 + x1;
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&B->p_full[t]);
+      }
+      if (!ok) break;
+      if (!begun) continue;
+      ok = mbar_wait_w(&B->o_full[t], no & 1, p.status, lim);
+      if (!ok) break;
+      ++no;
+      tc_fence_after();
+      const float f = 1.f / l;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + it.b * p.lay.out.batch +
+                           it.h * p.lay.out.head + (long long)(st.a + r) * p.lay.out.token;
+      bool fine = true;
+#pragma unroll
+      for (int x = 0; x < DP / 32; ++x) {
+        float o[32];
+        tmem_ld32(O + 32 * x, o);
+        tmem_wait32(o);
+        uint32_t ow[16];
+        float big = 0.f;
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          o[e] *= f;
+          o[e + 1] *= f;
+          big = fmaf(o[e], 0.f, fmaf(o[e + 1], 0.f, big));   // NaN if any is not finite
+          ow[e / 2] = bf16_pair(o[e], o[e + 1]);
+        }
+        fine = fine && big == 0.f;
+        if (live) {
+          if (tp.wide_out) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (32 * x + 8 * e < p.d)
+                *reinterpret_cast<uint4*>(out + 32 * x + 8 * e) =
+                    make_uint4(ow[4 * e], ow[4 * e + 1], ow[4 * e + 2], ow[4 * e + 3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * x + e < p.d) out[32 * x + e] = from_f<__nv_bfloat16>(o[e]);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&B->o_free[t]);
+      unsigned again = __ballot_sync(0xffffffffu, live && !fine);
+      while (again) {
+        const int x = __ffs(again) - 1;
+        again &= again - 1;
+        row_alone(tp, it.b, it.h, it.i0, st.a + (r & ~31) + x);
+      }
+    }
+  } else {
+    regs_few();   // all of a warpgroup
+  }
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+int g_ready[64] = {0};   // 0 unknown, 1 usable, 2 not usable
+int g_sms[64] = {0};
+std::mutex g_mu;
+
+// One-time setup of the current device; the number of SMs, 0 if not usable.
+int prepare() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_ready[dev] == 0) {
+    g_ready[dev] = 2;
+    g_sms[dev] = device_sm_count();
+    if (cudaFuncSetAttribute(window_tc_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Plan<64>::kSmem) == cudaSuccess &&
+        cudaFuncSetAttribute(window_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Plan<128>::kSmem) == cudaSuccess && g_sms[dev] > 0)
+      g_ready[dev] = 1;
+  }
+  return g_ready[dev] == 1 ? g_sms[dev] : 0;
+}
+
+// [B, H, N, d] with the given strides as a map of 64 x 128 boxes; false where TMA cannot
+// take it.
+bool win_map(CUtensorMap* m, const void* ptr, const delta_rule_stride& s, long long B, long long H,
+             long long N, int d) {
+  const unsigned long long dims[4] = {(unsigned long long)d, (unsigned long long)N,
+                                      (unsigned long long)H, (unsigned long long)B};
+  // the stride of a dimension of one element is never used: give a valid one
+  auto bytes = [](long long x, long long n) { return n > 1 ? (unsigned long long)x * 2 : 16ull; };
+  const unsigned long long st[3] = {bytes(s.token, N), bytes(s.head, H), bytes(s.batch, B)};
+  for (unsigned long long x : st)
+    if (x == 0 || x % 16 != 0 || x >= (1ull << 40)) return false;
+  if ((reinterpret_cast<uintptr_t>(ptr) & 15) != 0 || d % 8 != 0) return false;
+  const unsigned box[4] = {64, kM, 1, 1};
+  return encode_bf16_4d(m, ptr, dims, st, box);
+}
+
+}  // namespace
+
+int window_attention_tc(const WindowArgs& a) {
+  if (!a.bf16 || a.d > 128 || a.d % 8 != 0 || !(a.scale > 0.f)) return 1;
+  TcParams p;
+  if (!win_map(&p.q, a.q, a.lay.q, a.B, a.Hq, a.N, a.d) ||
+      !win_map(&p.k, a.k, a.lay.k, a.B, a.Hk, a.N, a.d) ||
+      !win_map(&p.v, a.v, a.lay.v, a.B, a.Hk, a.N, a.d))
+    return 1;
+  if (a.past) {
+    const long long places = (long long)a.window + a.sinks;
+    const delta_rule_stride s = {(long long)a.Hk * places * a.d, places * a.d, a.d};
+    if (!win_map(&p.ck, a.cache_k, s, a.n_slots, a.Hk, places, a.d) ||
+        !win_map(&p.cv, a.cache_v, s, a.n_slots, a.Hk, places, a.d))
+      return 1;
+  } else {
+    p.ck = p.k;
+    p.cv = p.v;
+  }
+  const int sms = prepare();
+  if (!sms) return TTT_ERR_CUDA;
+  p.w = win_params(a);
+  p.tiles = (a.N + 2 * kM - 1) / (2 * kM);
+  p.items = (long long)a.B * p.tiles * a.Hq;
+  p.wide_out = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.lay.out.batch % 8 == 0 &&
+               a.lay.out.head % 8 == 0 && a.lay.out.token % 8 == 0;
+  const unsigned grid = (unsigned)(p.items < sms ? p.items : sms);
+  const double tok = (double)a.B * a.N;
+  const double seen = a.N < (double)a.window + a.sinks ? a.N * 0.5 : (double)a.window + a.sinks;
+  ProfScope ps(PT_WIN_TC, a.stream, 4.0 * tok * a.Hq * a.d * seen, tok * 4.0 * a.d * (a.Hq + a.Hk));
+  const cudaError_t e =
+      a.d <= 64 ? launch_behind(window_tc_kernel<64>, grid, kThreads, Plan<64>::kSmem, a.stream, p)
+                : launch_behind(window_tc_kernel<128>, grid, kThreads, Plan<128>::kSmem, a.stream, p);
+  return e == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+}
+
+}  // namespace ttt
