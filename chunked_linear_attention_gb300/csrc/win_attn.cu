@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(256) window_attention_kernel(const __grid_cons
 #pragma unroll
     for (int c = 0; c < DP / 16; ++c) o[r][c] = 0.f;
   }
-  WinList w = win_list(p, b, i0, i0 + kQT, kKT);
+  WinList<kKT> w = win_list<kKT>(p, b, i0, i0 + kQT);
   WinTile t;
   while (win_next(p, w, t)) {
     // keys transposed, values as they are; rows that no query of this tile can see are

@@ -105,24 +105,25 @@ struct WinTile {
   WinCache c;  // for a cache
 };
 
+template <int KT>
 struct WinList {
   int sink0, sink1;   // the call's sinks in front of the window tiles
   int at, end;        // the window tiles
   int seq, seq1, place;
-  int i0, i1, b, KT;
+  int i0, i1, b;
   WinCache c;
 };
 
-__device__ __forceinline__ WinList win_list(const WinParams& p, int b, int i0, int i1, int KT) {
-  WinList w;
+template <int KT>
+__device__ __forceinline__ WinList<KT> win_list(const WinParams& p, int b, int i0, int i1) {
+  WinList<KT> w;
   i1 = min(i1, p.N);
   w.i0 = i0;
   w.i1 = i1;
   w.b = b;
-  w.KT = KT;
   const WinRow r = win_row(p, b, i0);
   const int lo = r.i >= 0 ? r.lo : max(0, i0 - p.window + 1);
-  w.at = i0 - (i0 - lo + KT - 1) / KT * KT;
+  w.at = i0 - (int)((unsigned)(i0 - lo + KT - 1) / KT * KT);
   w.end = i1;
   w.sink0 = r.i >= 0 ? r.t0 : 0;
   w.sink1 = r.i >= 0 ? min(r.sink1, w.at) : 0;
@@ -155,18 +156,19 @@ __device__ __forceinline__ WinList win_list(const WinParams& p, int b, int i0, i
   return w;
 }
 
-__device__ __forceinline__ bool win_next(const WinParams& p, WinList& w, WinTile& t) {
+template <int KT>
+__device__ __forceinline__ bool win_next(const WinParams& p, WinList<KT>& w, WinTile& t) {
   t.seq = -1;
   if (w.sink0 < w.sink1) {
     t.base = w.sink0;
     t.end = w.sink1;
-    w.sink0 += w.KT;
+    w.sink0 += KT;
     return true;
   }
   if (w.at < w.end) {
     t.base = w.at;
     t.end = w.end;
-    w.at += w.KT;
+    w.at += KT;
     return true;
   }
   while (w.place >= w.c.count) {
@@ -198,7 +200,7 @@ __device__ __forceinline__ bool win_next(const WinParams& p, WinList& w, WinTile
   t.base = w.place;
   t.end = w.c.count;
   t.c = w.c;
-  w.place += w.KT;
+  w.place += KT;
   return true;
 }
 

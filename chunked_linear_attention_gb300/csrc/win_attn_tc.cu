@@ -5,10 +5,10 @@
 //     S = Q K^T      (128 x 128, fp32 in TMEM)
 //     P = exp2(c S - c m),  l += sum P     (c = scale log2 e; one thread per row)
 //     O += P V       (P as bf16 in the TMEM columns that S had)
-// with m the row's largest score so far.  O is only rescaled, in TMEM, when a row's
-// largest score has grown by more than 8 / c since the last time: until then its weights
-// are at most 2^8 too large, and so are their sums.  P is rounded to bf16 (2^-8 of each
-// weight) as the operand of the second product; l sums what was not rounded.
+// with m the row's largest score so far.  O and l are only rescaled, in TMEM, when that has
+// grown by more than 8 / c since the last time: until then the weights are at most 2^8 too
+// large, and so are their sums.  P is rounded to bf16 (2^-8 of each weight) as the operand
+// of the second product; l sums what was not rounded.
 //
 // What bounds it: per pair of tiles the products take 1024 clocks of the tensor core
 // (d 128) and the exponentials 1024 of the special-function units (32 a clock), so
@@ -21,6 +21,7 @@
 // Roles (384 threads, one block per SM, persistent over (tile pair, head)):
 //   warp 0      TMA: Q, and K and V through a ring of tiles.
 //   warp 1      all products.
+//   warp 2      the list of key tiles, for all others.
 //   warps 4-7   rows of the first tile, warps 8-11 of the second: softmax, rescaling,
 //               outputs.
 #include <mutex>
@@ -35,40 +36,62 @@ namespace {
 
 constexpr int kM = 128;                  // rows of a tile, keys of a key tile
 constexpr int kThreads = 384;
-constexpr int kRegsFew = 104, kRegsMany = 200;
-static_assert(128 * kRegsFew + 256 * kRegsMany <= kThreads * 168, "registers at launch");
 
 template <int DP>
 struct Plan {
   static constexpr int kTile = kM * DP * 2;                  // bytes of a tile of Q, K or V
-  static constexpr int kStages = DP == 128 ? 5 : 10;
-  static constexpr int kSmem = 2 * kTile + kStages * kTile + 1024 + 512;
+  static constexpr int kStages = DP == 128 ? 4 : 8;
+  static constexpr int kStaging = 8 * 32 * 128;              // 32 rows of 64 outputs a warp
+  static constexpr int kSmem = 2 * kTile + kStages * kTile + kStaging + 1024 + 1024;
 };
 static_assert(Plan<128>::kSmem <= 227 * 1024 && Plan<64>::kSmem <= 227 * 1024, "shared memory");
 
+// What the list warp tells the others, one entry per key tile that either query tile
+// needs, one behind each item and one at the end.
+enum : int {
+  kNeed = 1,      // << t: query tile t needs the key tile
+  kWhole = 4,     // << t: all its queries see all of it
+  kCache = 16,    // the key tile lies in a cache
+  kTileEntry = 32,
+  kStop = 64
+};
+struct Entry {
+  int flags;
+  int b, h, i0;        // the item
+  int base, end;       // the key tile: see WinTile
+  int seq, slot, count, past, head;
+  int pad;
+};
+static_assert(sizeof(Entry) == 48, "read 16 bytes at a time");
+constexpr int kEntries = 8;
+constexpr int kReaders = 10;   // the loads' thread, the products' warp, eight row warps
+
 struct Bars {
+  uint64_t e_full[kEntries], e_free[kEntries];
   uint64_t q_full, q_free;
-  uint64_t full[10], empty[10];
+  uint64_t full[8], empty[8];
   uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t done;
   uint32_t tmem;
+  alignas(16) Entry entry[kEntries];
 };
-static_assert(sizeof(Bars) <= 512, "control region");
+static_assert(sizeof(Bars) <= 1024, "control region");
 
 struct TcParams {
   CUtensorMap q, k, v, ck, cv;
   WinParams w;
   int tiles;            // pairs of query tiles of the token axis
-  long long items;      // (batch, tile pair, head)
+  unsigned items;       // (batch, tile pair, head)
   int wide_out;         // rows of out can be stored 16 bytes at a time
 };
 
-// The queries a .. e - 1 of one tile: which key tiles they need.
+// The queries a .. e - 1 of one tile: which key tiles they need, and see in whole.
 struct SubTile {
   int a, e, lo, s0, s1;
+  int lo_last;   // first key of the last query's window
 };
 
-__device__ __forceinline__ SubTile sub_tile(const WinParams& p, int b, int a, int e) {
+__device__ __noinline__ SubTile sub_tile(const WinParams& p, int b, int a, int e) {
   SubTile s;
   s.a = a;
   s.e = min(e, p.N);
@@ -76,6 +99,7 @@ __device__ __forceinline__ SubTile sub_tile(const WinParams& p, int b, int a, in
   s.lo = r.i >= 0 ? r.lo : max(0, a - p.window + 1);
   s.s0 = r.i >= 0 ? r.t0 : 0;
   s.s1 = r.i >= 0 ? r.sink1 : 0;
+  s.lo_last = s.a < s.e ? win_row(p, b, s.e - 1).lo : 0;
   return s;
 }
 
@@ -86,15 +110,21 @@ __device__ __forceinline__ bool needs(const SubTile& s, const WinTile& t) {
          (t.base + kM > s.lo || (t.base < s.s1 && t.base + kM > s.s0));
 }
 
+// The windows of a tile's queries begin one behind another, so that the last one's and the
+// first query bound them all.
+__device__ __forceinline__ bool sees_whole(const SubTile& s, const WinTile& t) {
+  return t.seq < 0 && t.base >= s.lo_last && t.base + kM - 1 <= s.a && t.base + kM <= t.end;
+}
+
 struct Item {
   int b, h, i0;
 };
-__device__ __forceinline__ Item get_item(const TcParams& p, long long n) {
+__device__ __forceinline__ Item get_item(const TcParams& p, unsigned n) {
   Item it;
-  it.h = (int)(n % p.w.Hq);
-  const long long r = n / p.w.Hq;
-  it.i0 = (int)(r % p.tiles) * 2 * kM;
-  it.b = (int)(r / p.tiles);
+  const unsigned r = n / (unsigned)p.w.Hq;
+  it.h = (int)(n - r * (unsigned)p.w.Hq);
+  it.b = (int)(r / (unsigned)p.tiles);
+  it.i0 = (int)(r - (unsigned)it.b * (unsigned)p.tiles) * 2 * kM;
   return it;
 }
 
@@ -120,12 +150,25 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// The block's registers, from the warps that load and issue to those that hold rows.
-__device__ __forceinline__ void regs_few() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+// Bounded waits whose slow part is a call: the code that every tile runs has to stay in the
+// instruction cache (with everything in line, a third of the time went into fetching it).
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* status,
+                                       unsigned long long lim) {
+  return mbar_wait(bar, parity, status, lim);
 }
-__device__ __forceinline__ void regs_many() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, int* status,
+                                         unsigned long long lim) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, status, lim);
+}
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, int* status,
+                                         unsigned long long lim) {
+  return __all_sync(0xffffffffu, wait_one(bar, parity, status, lim));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
@@ -158,7 +201,7 @@ __device__ __noinline__ void row_alone(const TcParams& tp, int b, int h, int i0,
   }
   const WinRow row = win_row(p, b, i);
   float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  WinList w = win_list(p, b, i0, i0 + 2 * kM, kM);
+  WinList<kM> w = win_list<kM>(p, b, i0, i0 + 2 * kM);
   WinTile t;
   while (win_next(p, w, t)) {
     const T *ks = k, *vs = v;
@@ -207,6 +250,28 @@ __device__ __noinline__ void row_alone(const TcParams& tp, int b, int h, int i0,
     if (lane + 32 * e < p.d) out[lane + 32 * e] = from_f<T>(acc[e] / l);
 }
 
+// The next entry, by a whole warp (by one thread: `alone`).
+struct Reader {
+  int n;
+  template <bool ALONE>
+  __device__ __forceinline__ bool next(Bars* B, Entry& e, int* status, unsigned long long lim) {
+    const int s = n % kEntries;
+    const uint32_t ph = (n / kEntries) & 1;
+    const bool ok = ALONE ? wait_one(&B->e_full[s], ph, status, lim)
+                          : wait_all(&B->e_full[s], ph, status, lim);
+    if (!ok) return false;
+    const int4* src = reinterpret_cast<const int4*>(&B->entry[s]);
+    int4* dst = reinterpret_cast<int4*>(&e);
+    dst[0] = src[0];
+    dst[1] = src[1];
+    dst[2] = src[2];
+    if (!ALONE) __syncwarp();
+    if (ALONE || (threadIdx.x & 31) == 0) mbar_arrive(&B->e_free[s]);
+    ++n;
+    return true;
+  }
+};
+
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_constant__ TcParams tp) {
   using PL = Plan<DP>;
@@ -215,7 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint8_t* Q = smem;
   uint8_t* ring = smem + 2 * TB;
-  Bars* B = reinterpret_cast<Bars*>(ring + NS * TB);
+  uint8_t* staging = ring + NS * TB;
+  Bars* B = reinterpret_cast<Bars*>(staging + PL::kStaging);
   const WinParams& p = tp.w;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const unsigned long long lim = p.wait_ns;
@@ -223,15 +289,19 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
   if (tid == 0) {
     mbar_init(&B->q_full, 1);
     mbar_init(&B->q_free, 1);
+    for (int s = 0; s < kEntries; ++s) {
+      mbar_init(&B->e_full[s], 1);
+      mbar_init(&B->e_free[s], kReaders);
+    }
     for (int s = 0; s < NS; ++s) {
       mbar_init(&B->full[s], 1);
       mbar_init(&B->empty[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&B->s_full[t], 1);
-      mbar_init(&B->p_full[t], kM);
+      mbar_init(&B->p_full[t], 4);   // a lane of each warp
       mbar_init(&B->o_full[t], 1);
-      mbar_init(&B->o_free[t], kM);
+      mbar_init(&B->o_free[t], 4);
     }
     mbar_init(&B->done, 1);
     fence_mbar_init();
@@ -248,21 +318,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
 
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
-    regs_few();
-    if (blockIdx.x == 0 && p.starts) {   // reports bounds that are none
-      bool bad = false;
-      for (int i = lane; i < p.n_seq; i += 32) {
-        const int a = p.starts[i], e = p.starts[i + 1];
-        bad |= a < 0 || e < a || e > p.N;
-      }
-      if (bad) report_status(p.status, kStatusBadArg);
-    }
     if (lane == 0) {
       int fills = 0, q_loads = 0;
-      bool ok = true;
+      bool ok = true, first = true;   // first key tile of an item
       auto load = [&](const CUtensorMap* map, int y, int z, int w) {
         const int s = fills % NS;
-        ok = ok && mbar_wait(&B->empty[s], ((fills / NS) & 1) ^ 1, p.status, lim);
+        ok = ok && wait_one(&B->empty[s], ((fills / NS) & 1) ^ 1, p.status, lim);
         if (!ok) return;
         mbar_arrive_expect_tx(&B->full[s], TB);
 #pragma unroll
@@ -270,44 +331,46 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
           tma_load_4d(ring + s * TB + x * (kM * 128), map, x * 64, y, z, w, &B->full[s]);
         ++fills;
       };
-      for (long long n = blockIdx.x; n < tp.items && ok; n += gridDim.x) {
-        const Item it = get_item(tp, n);
-        const int hk = it.h / (p.Hq / p.Hk);
-        ok = mbar_wait(&B->q_free, (q_loads & 1) ^ 1, p.status, lim);
-        if (!ok) break;
-        mbar_arrive_expect_tx(&B->q_full, 2 * TB);
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int x = 0; x < NB; ++x)
-            tma_load_4d(Q + t * TB + x * (kM * 128), &tp.q, x * 64, it.i0 + t * kM, it.h, it.b, &B->q_full);
-        ++q_loads;
-        const SubTile s0 = sub_tile(p, it.b, it.i0, it.i0 + kM);
-        const SubTile s1 = sub_tile(p, it.b, it.i0 + kM, it.i0 + 2 * kM);
-        WinList w = win_list(p, it.b, it.i0, it.i0 + 2 * kM, kM);
-        WinTile t;
-        while (ok && win_next(p, w, t)) {
-          if (!needs(s0, t) && !needs(s1, t)) continue;
-          const bool c = t.seq >= 0;
-          load(c ? &tp.ck : &tp.k, t.base, hk, c ? t.c.slot : it.b);
-          load(c ? &tp.cv : &tp.v, t.base, hk, c ? t.c.slot : it.b);
+      Reader rd{0};
+      Entry e;
+      while (ok) {
+        ok = rd.next<true>(B, e, p.status, lim);
+        if (!ok || (e.flags & kStop)) break;
+        if (!(e.flags & kTileEntry)) {
+          first = true;
+          continue;
         }
+        const int hk = e.h / (p.Hq / p.Hk);
+        const bool c = e.flags & kCache;
+        load(c ? &tp.ck : &tp.k, e.base, hk, c ? e.slot : e.b);
+        if (first) {   // the first keys do not wait for the last item's queries
+          ok = ok && wait_one(&B->q_free, (q_loads & 1) ^ 1, p.status, lim);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&B->q_full, 2 * TB);
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int x = 0; x < NB; ++x)
+              tma_load_4d(Q + t * TB + x * (kM * 128), &tp.q, x * 64, e.i0 + t * kM, e.h, e.b, &B->q_full);
+          ++q_loads;
+          first = false;
+        }
+        load(c ? &tp.cv : &tp.v, e.base, hk, c ? e.slot : e.b);
       }
       if (!ok) {   // what is on its way lands before the block ends
-        if (q_loads) mbar_wait(&B->q_full, (q_loads - 1) & 1, p.status, lim);
+        if (q_loads) wait_one(&B->q_full, (q_loads - 1) & 1, p.status, lim);
         for (int k = 1; k <= NS && k <= fills; ++k)
-          mbar_wait(&B->full[(fills - k) % NS], ((fills - k) / NS) & 1, p.status, lim);
+          wait_one(&B->full[(fills - k) % NS], ((fills - k) / NS) & 1, p.status, lim);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- products
-    regs_few();
     const uint32_t id_s = idesc_bf16_f32(kM, 0, 0), id_o = idesc_bf16_f32(DP, 0, 1);
     const uint64_t qd = smem_desc_sw128(smem_u32(Q), 16, 1024);
     const uint64_t kd = smem_desc_sw128(smem_u32(ring), 16, 1024);
     const uint64_t vd = smem_desc_sw128(smem_u32(ring), kM * 128, 1024);
-    int uses = 0, items = 0;            // ring tiles taken; query tiles taken
-    int np[2] = {0, 0}, no[2] = {0, 0}; // weights awaited, outputs begun
+    int uses = 0, items = 0;            // ring tiles taken; items with key tiles
+    int np = 0, no = 0;                 // parities of the weights awaited, the outputs begun
     bool ok = true;
     auto scores = [&](int t, int s) {   // S_t = Q_t K^T with K in ring stage s
 #pragma unroll
@@ -323,250 +386,338 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
         umma_ts_w(tmem + 256 + t * kM, tmem + t * kM + k * 8, vd + s * (TB >> 4) + k * 128, id_o,
                   !first || k != 0);
     };
-    for (long long n = blockIdx.x; n < tp.items && ok; n += gridDim.x) {
-      const Item it = get_item(tp, n);
-      const SubTile st[2] = {sub_tile(p, it.b, it.i0, it.i0 + kM),
-                             sub_tile(p, it.b, it.i0 + kM, it.i0 + 2 * kM)};
-      ok = mbar_wait_w(&B->q_full, items & 1, p.status, lim);
-      ++items;
-      WinList w = win_list(p, it.b, it.i0, it.i0 + 2 * kM, kM);
-      WinTile t;
-      bool begun[2] = {false, false};
-      bool cur[2] = {false, false};     // the tile whose weights are awaited
-      int v_at = 0;                     // its V's place in the ring
-      bool more = true;
-      while (ok && (more || cur[0] || cur[1])) {
-        // the next tile that either needs
-        bool nxt[2] = {false, false};
-        more = false;
-        while (win_next(p, w, t)) {
-          nxt[0] = needs(st[0], t);
-          nxt[1] = needs(st[1], t);
-          if (nxt[0] || nxt[1]) {
-            more = true;
-            break;
+    Reader rd{0};
+    Entry e;
+    int cur = 0;                        // who awaits V, at v_at in the ring
+    int v_at = 0;
+    int begun = 0, told = 0;            // bits of the query tiles, in this item
+    while (ok) {
+      ok = rd.next<false>(B, e, p.status, lim);
+      if (!ok || (e.flags & kStop)) break;
+      const bool tile = e.flags & kTileEntry;
+      const int nxt = tile ? e.flags & 3 : 0;
+      if (tile && !cur) {   // an item begins (the entries of one follow one another)
+        ok = wait_all(&B->q_full, items & 1, p.status, lim);
+        ++items;
+      }
+      if (!tile && cur) umma_commit_w(&B->q_free);   // all scores of this item are under way
+      const int k_at = uses, ks = k_at % NS, vs = v_at % NS;
+      bool k_here = false, v_here = false;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (cur & (1 << u)) {
+          const bool first = !(begun & (1 << u));
+          ok = ok && wait_all(&B->p_full[u], (np >> u) & 1, p.status, lim);
+          if (first) {
+            ok = ok && wait_all(&B->o_free[u], ((no >> u) & 1) ^ 1, p.status, lim);
+            no ^= 1 << u;
+          }
+          if (!v_here) ok = ok && wait_all(&B->full[vs], (v_at / NS) & 1, p.status, lim);
+          if (!ok) break;
+          v_here = true;
+          tc_fence_after();
+          outputs(u, vs, first);
+          np ^= 1 << u;
+          begun |= 1 << u;
+          // the first tile's window begins the list's window tiles: without caches behind
+          // them, it has had its last where it needs no next one
+          if (u == 0 && !(nxt & 1) && !p.past) {
+            umma_commit_w(&B->o_full[0]);
+            told = 1;
           }
         }
-        if (!more) umma_commit_w(&B->q_free);   // all scores of this item are under way
-        const int k_at = uses;
-        bool k_here = false;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (cur[u]) {
-            ok = ok && mbar_wait_w(&B->p_full[u], np[u] & 1, p.status, lim);
-            ++np[u];
-            if (!begun[u]) {
-              ok = ok && mbar_wait_w(&B->o_free[u], (no[u] & 1) ^ 1, p.status, lim);
-              ++no[u];
-            }
-            if (!ok) break;
-            if (u == 0 || !cur[0])
-              ok = mbar_wait_w(&B->full[v_at % NS], (v_at / NS) & 1, p.status, lim);
+        if (u == 1 && cur) umma_commit_w(&B->empty[vs]);
+        if (nxt & (1 << u)) {
+          if (!k_here) {
+            ok = ok && wait_all(&B->full[ks], (k_at / NS) & 1, p.status, lim);
             if (!ok) break;
             tc_fence_after();
-            outputs(u, v_at % NS, !begun[u]);
-            begun[u] = true;
           }
-          if (u == 1 && (cur[0] || cur[1])) umma_commit_w(&B->empty[v_at % NS]);
-          if (nxt[u]) {
-            if (!k_here) {
-              ok = mbar_wait_w(&B->full[k_at % NS], (k_at / NS) & 1, p.status, lim);
-              if (!ok) break;
-              tc_fence_after();
-              k_here = true;
-            }
-            scores(u, k_at % NS);
-          }
+          k_here = true;
+          scores(u, ks);
         }
-        if (!ok) break;
-        if (more) {
-          umma_commit_w(&B->empty[k_at % NS]);
-          v_at = k_at + 1;
-          uses = k_at + 2;
-        }
-        cur[0] = more && nxt[0];
-        cur[1] = more && nxt[1];
       }
       if (!ok) break;
-      for (int u = 0; u < 2; ++u)
-        if (begun[u]) umma_commit_w(&B->o_full[u]);
+      if (tile) {
+        umma_commit_w(&B->empty[ks]);
+        v_at = k_at + 1;
+        uses = k_at + 2;
+      } else {
+        for (int u = 0; u < 2; ++u)
+          if ((begun & ~told) & (1 << u)) umma_commit_w(&B->o_full[u]);
+        begun = told = 0;
+      }
+      cur = nxt;
     }
     if (!ok) {   // the products under way end before their TMEM is given back
       umma_commit_w(&B->done);
-      mbar_wait_w(&B->done, 0, p.status, lim);
+      wait_all(&B->done, 0, p.status, lim);
     }
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- the list
+    if (blockIdx.x == 0 && p.starts) {   // reports bounds that are none
+      bool bad = false;
+      for (int i = lane; i < p.n_seq; i += 32) {
+        const int a = p.starts[i], e = p.starts[i + 1];
+        bad |= a < 0 || e < a || e > p.N;
+      }
+      if (bad) report_status(p.status, kStatusBadArg);
+    }
+    if (lane == 0) {
+      int n = 0;
+      bool ok = true;
+      auto put = [&](const Entry& e) {
+        const int s = n % kEntries;
+        ok = ok && wait_one(&B->e_free[s], ((n / kEntries) & 1) ^ 1, p.status, lim);
+        if (!ok) return;
+        const int4* src = reinterpret_cast<const int4*>(&e);
+        int4* dst = reinterpret_cast<int4*>(&B->entry[s]);
+        dst[0] = src[0];
+        dst[1] = src[1];
+        dst[2] = src[2];
+        mbar_arrive(&B->e_full[s]);
+        ++n;
+      };
+      Entry e = {};
+      for (unsigned item = blockIdx.x; item < tp.items && ok; item += gridDim.x) {
+        const Item it = get_item(tp, item);
+        e.b = it.b;
+        e.h = it.h;
+        e.i0 = it.i0;
+        const SubTile s0 = sub_tile(p, it.b, it.i0, it.i0 + kM);
+        const SubTile s1 = sub_tile(p, it.b, it.i0 + kM, it.i0 + 2 * kM);
+        WinList<kM> w = win_list<kM>(p, it.b, it.i0, it.i0 + 2 * kM);
+        WinTile t;
+        while (ok && win_next(p, w, t)) {
+          const bool n0 = needs(s0, t), n1 = needs(s1, t);
+          if (!n0 && !n1) continue;
+          e.flags = kTileEntry | (n0 ? kNeed : 0) | (n1 ? kNeed << 1 : 0) |
+                    (sees_whole(s0, t) ? kWhole : 0) | (sees_whole(s1, t) ? kWhole << 1 : 0);
+          e.base = t.base;
+          e.end = t.end;
+          if (t.seq >= 0) {
+            e.flags |= kCache;
+            e.seq = t.seq;
+            e.slot = t.c.slot;
+            e.count = t.c.count;
+            e.past = t.c.past;
+            e.head = t.c.head;
+          }
+          put(e);
+        }
+        e.flags = 0;
+        put(e);
+      }
+      e.flags = kStop;
+      put(e);
+    }
+    __syncwarp();
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- rows
-    regs_many();
     const int t = (warp - 4) >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t S = tmem + t * kM + lanes, O = tmem + 256 + t * kM + lanes;
     const float c = p.scale, grow = 8.f / c;
-    const F2 c2 = pack2(c, c);
+    uint8_t* stage = staging + (warp - 4) * (32 * 128);
     int ns = 0, no = 0;
-    bool ok = true;
-    for (long long n = blockIdx.x; n < tp.items && ok; n += gridDim.x) {
-      const Item it = get_item(tp, n);
-      const SubTile st = sub_tile(p, it.b, it.i0 + t * kM, it.i0 + (t + 1) * kM);
-      if (st.a >= st.e) continue;
-      WinRow row = win_row(p, it.b, st.a + r);
-      const bool live = row.i >= 0;
-      if (!live) {   // stored nowhere: sees what there is
-        row.i = 0x7fffffff;
-        row.lo = row.t0 = 0;
-        row.wlo = -0x40000000;
+    bool ok = true, begun = false;   // begun: in this item
+    float m = -INFINITY, l = 0.f;   // the row's reference and sum
+    int ib = 0, ih = 0, i0 = 0;
+    WinRow row;
+    row.i = -1;
+    bool live = false;
+    auto rescale = [&](float to) {
+      const float f = to > m ? ex2((m - to) * c) : 1.f;
+      m = to;
+      l *= f;
+      if (!begun) return;
+#pragma unroll 1   // rare: what is run for every tile has to stay in the instruction cache
+      for (int x = 0; x < DP / 16; ++x) {
+        float o[16];
+        tmem_ld16_nowait(O + 16 * x, o);
+        tmem_wait_bind(o);
+        uint32_t ow[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e] * f);
+        tmem_st16(O + 16 * x, ow);
       }
-      const int i_min = __reduce_min_sync(0xffffffffu, row.i);
-      const int lo_max = __reduce_max_sync(0xffffffffu, row.lo);
-      float m = -INFINITY, l = 0.f;
-      bool begun = false;
-      WinList w = win_list(p, it.b, it.i0, it.i0 + 2 * kM, kM);
-      WinTile kt;
-      while (win_next(p, w, kt)) {
-        if (!needs(st, kt)) continue;
-        ok = mbar_wait_w(&B->s_full[t], ns & 1, p.status, lim);
+    };
+    Reader rd{0};
+    Entry e;
+    while (ok) {
+      ok = rd.next<false>(B, e, p.status, lim);
+      if (!ok || (e.flags & kStop)) break;
+      if (e.flags & (kNeed << t)) {
+        if (!begun) {
+          ib = e.b;
+          ih = e.h;
+          i0 = e.i0;
+          m = -INFINITY;
+          l = 0.f;
+          row = win_row(p, ib, i0 + t * kM + r);
+          live = row.i >= 0;
+          if (!live) {   // stored nowhere: sees what there is
+            row.i = 0x7ffffffe;
+            row.lo = row.t0 = row.sink1 = 0;
+          }
+        }
+        ok = wait_all(&B->s_full[t], ns & 1, p.status, lim);
         if (!ok) break;
         ++ns;
         tc_fence_after();
-        float s[4][32];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) tmem_ld32(S + 32 * x, s[x]);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) tmem_wait32(s[x]);
-        const bool whole = kt.seq < 0 && kt.base >= lo_max && kt.base + kM - 1 <= i_min &&
-                           kt.base + kM <= kt.end;
+        const bool whole = e.flags & (kWhole << t);
+        // up to three spans of columns that the row sees
+        int a0 = 0, a1 = kM, b0 = 0, b1 = 0, c0 = 0, c1 = 0;
         if (!whole) {
-          // up to three spans of columns that the row sees
-          int a0, a1, b0, b1, c0 = 0, c1 = 0;
-          if (kt.seq < 0) {
-            const int top = min(row.i == 0x7fffffff ? row.i : row.i + 1, kt.end);
-            a0 = max(row.lo, 0) - kt.base;
-            a1 = top - kt.base;
-            b0 = row.t0 - kt.base;
-            b1 = min(row.sink1, top) - kt.base;
-            if (row.t0 == 0x7fffffff) b1 = b0;
+          if (!(e.flags & kCache)) {
+            const int top = min(row.i + 1, e.end);
+            a0 = row.lo - e.base;
+            a1 = top - e.base;
+            b0 = row.t0 - e.base;
+            b1 = min(row.sink1, top) - e.base;
           } else {
             // places of the ring up to the head are of the newest lap, the others of the one
             // before
-            const int x = row.wlo - kt.c.past + kt.c.head, sk = p.sinks;
-            a0 = -kt.base;
-            a1 = min(sk, kt.c.count) - kt.base;
-            b0 = sk + max(x, 0) - kt.base;
-            b1 = min(sk + kt.c.head, kt.c.count) - kt.base;
-            c0 = sk + max(x + p.window, kt.c.head) - kt.base;
-            c1 = kt.c.count - kt.base;
-            if (live && row.seq != kt.c.seq) a1 = b1 = c1 = -1;
+            const int x = row.wlo - e.past + e.head, sk = p.sinks;
+            a0 = -e.base;
+            a1 = min(sk, e.count) - e.base;
+            b0 = sk + max(x, 0) - e.base;
+            b1 = min(sk + e.head, e.count) - e.base;
+            c0 = sk + max(x + p.window, e.head) - e.base;
+            c1 = e.count - e.base;
+            if (row.seq != e.seq) a1 = b1 = c1 = -1;
           }
+        }
+        auto mask = [&](float (&s)[32], int x) {
+          const uint32_t bits = span_bits(a0, a1, 32 * x) | span_bits(b0, b1, 32 * x) |
+                                span_bits(c0, c1, 32 * x);
 #pragma unroll
+          for (int y = 0; y < 32; ++y) s[y] = (bits >> y) & 1 ? s[y] : -INFINITY;
+        };
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto largest = [&](const float (&s)[32]) {
+#pragma unroll
+          for (int y = 0; y < 32; y += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tops[i] = max3(tops[i], s[y + 2 * i], s[y + 2 * i + 1]);
+        };
+        if (whole) {
+          float s[4][32];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) tmem_ld32(S + 32 * x, s[x]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) tmem_wait32(s[x]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) largest(s[x]);
+        } else {
+#pragma unroll 1
           for (int x = 0; x < 4; ++x) {
-            const uint32_t bits = span_bits(a0, a1, 32 * x) | span_bits(b0, b1, 32 * x) |
-                                  span_bits(c0, c1, 32 * x);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s[x][e] = (bits >> e) & 1 ? s[x][e] : -INFINITY;
+            float s[32];
+            tmem_ld32(S + 32 * x, s);
+            tmem_wait32(s);
+            mask(s, x);
+            largest(s);
           }
         }
-        float top = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(s[x][e], s[x][e + 1]));
-        if (!begun) {
-          m = top;
-        } else if (__any_sync(0xffffffffu, top > m + grow)) {
-          const float f = top > m + grow ? ex2((m - top) * c) : 1.f;
-          if (top > m + grow) m = top;
-          l *= f;
-#pragma unroll
-          for (int x = 0; x < DP / 16; ++x) {
-            float o[16];
-            tmem_ld16_nowait(O + 16 * x, o);
-            tmem_wait_bind(o);
-            uint32_t ow[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e] * f);
-            tmem_st16(O + 16 * x, ow);
-          }
-        }
+        const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
+        if (__any_sync(0xffffffffu, top > m + grow)) rescale(top > m + grow ? top : m);
         begun = true;
+        float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
         const float mc = m == -INFINITY ? 0.f : m * c;
-        const F2 mc2 = pack2(-mc, -mc);
-        F2 sum0 = 0ull, sum1 = 0ull;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {   // the scores once more: 128 of them are not kept
+          float s[32];
           uint32_t pw[16];
+          tmem_ld32(S + 32 * x, s);
+          tmem_wait32(s);
+          if (!whole) mask(s, x);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            float v0, v1, v2, v3;
-            unpack2(fma2(pack2(s[x][e], s[x][e + 1]), c2, mc2), v0, v1);
-            unpack2(fma2(pack2(s[x][e + 2], s[x][e + 3]), c2, mc2), v2, v3);
-            v0 = ex2(v0);
-            v1 = ex2(v1);
-            v2 = ex2(v2);
-            v3 = ex2(v3);
-            sum0 = add2(sum0, pack2(v0, v1));
-            sum1 = add2(sum1, pack2(v2, v3));
-            pw[e / 2] = bf16_pair(v0, v1);
-            pw[e / 2 + 1] = bf16_pair(v2, v3);
+          for (int y = 0; y < 32; y += 4) {
+            const float v0 = ex2(fmaf(s[y], c, -mc)), v1 = ex2(fmaf(s[y + 1], c, -mc));
+            const float v2 = ex2(fmaf(s[y + 2], c, -mc)), v3 = ex2(fmaf(s[y + 3], c, -mc));
+            sum0 += v0;
+            sum1 += v1;
+            sum2 += v2;
+            sum3 += v3;
+            pw[y / 2] = bf16_pair(v0, v1);
+            pw[y / 2 + 1] = bf16_pair(v2, v3);
           }
           tmem_st16(S + 16 * x, pw);
         }
-        float x0, x1;
-        unpack2(add2(sum0, sum1), x0, x1);
-        l += x0 + x1;
+        l += (sum0 + sum1) + (sum2 + sum3);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&B->p_full[t]);
-      }
-      if (!ok) break;
-      if (!begun) continue;
-      ok = mbar_wait_w(&B->o_full[t], no & 1, p.status, lim);
-      if (!ok) break;
-      ++no;
-      tc_fence_after();
-      const float f = 1.f / l;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + it.b * p.lay.out.batch +
-                           it.h * p.lay.out.head + (long long)(st.a + r) * p.lay.out.token;
-      bool fine = true;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B->p_full[t]);
+      } else if (!(e.flags & kTileEntry) && begun) {
+        begun = false;
+        ok = wait_all(&B->o_full[t], no & 1, p.status, lim);
+        if (!ok) break;
+        ++no;
+        tc_fence_after();
+        const float f = 1.f / l;
+        const int first = i0 + t * kM + (r & ~31);   // the warp's rows
+        const unsigned rows = __ballot_sync(0xffffffffu, live);
+        __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + ib * p.lay.out.batch +
+                            ih * p.lay.out.head + (first + (lane >> 3)) * p.lay.out.token +
+                            (lane & 7) * 8;
+        bool fine = true;
+#pragma unroll 1
+        for (int y = 0; y < NB; ++y) {   // 64 columns, through shared memory: whole lines are stored
+          __syncwarp();
+#pragma unroll 1
+          for (int x = 0; x < 2; ++x) {
+            float o[32];
+            tmem_ld32(O + 64 * y + 32 * x, o);
+            tmem_wait32(o);
+            uint32_t ow[16];
+            float big = 0.f;
 #pragma unroll
-      for (int x = 0; x < DP / 32; ++x) {
-        float o[32];
-        tmem_ld32(O + 32 * x, o);
-        tmem_wait32(o);
-        uint32_t ow[16];
-        float big = 0.f;
+            for (int i = 0; i < 32; i += 2) {
+              o[i] *= f;
+              o[i + 1] *= f;
+              big = fmaf(o[i], 0.f, fmaf(o[i + 1], 0.f, big));   // NaN if any is not finite
+              ow[i / 2] = bf16_pair(o[i], o[i + 1]);
+            }
+            fine = fine && big == 0.f;
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          o[e] *= f;
-          o[e + 1] *= f;
-          big = fmaf(o[e], 0.f, fmaf(o[e + 1], 0.f, big));   // NaN if any is not finite
-          ow[e / 2] = bf16_pair(o[e], o[e + 1]);
-        }
-        fine = fine && big == 0.f;
-        if (live) {
-          if (tp.wide_out) {
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * x + i) ^ (lane & 7)) << 4)) =
+                  make_uint4(ow[4 * i], ow[4 * i + 1], ow[4 * i + 2], ow[4 * i + 3]);
+          }
+          __syncwarp();
+          if (y == NB - 1) {   // the outputs are read: the next item's products may begin
+            tc_fence_before();
+            if (lane == 0) mbar_arrive(&B->o_free[t]);
+          }
+          if (64 * y + (lane & 7) * 8 < p.d) {
+            __nv_bfloat16* at = to + 64 * y;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (32 * x + 8 * e < p.d)
-                *reinterpret_cast<uint4*>(out + 32 * x + 8 * e) =
-                    make_uint4(ow[4 * e], ow[4 * e + 1], ow[4 * e + 2], ow[4 * e + 3]);
-          } else {
+            for (int i = 0; i < 8; ++i) {
+              const int n = 4 * i + (lane >> 3);
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + n * 128 + (((lane & 7) ^ (n & 7)) << 4));
+              if ((rows >> n) & 1) {
+                if (tp.wide_out) {
+                  *reinterpret_cast<uint4*>(at) = v;
+                } else {
+                  const __nv_bfloat16* w8 = reinterpret_cast<const __nv_bfloat16*>(&v);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * x + e < p.d) out[32 * x + e] = from_f<__nv_bfloat16>(o[e]);
+                  for (int j = 0; j < 8; ++j) at[j] = w8[j];
+                }
+              }
+              at += 4 * p.lay.out.token;
+            }
           }
         }
-      }
-      tc_fence_before();
-      mbar_arrive(&B->o_free[t]);
-      unsigned again = __ballot_sync(0xffffffffu, live && !fine);
-      while (again) {
-        const int x = __ffs(again) - 1;
-        again &= again - 1;
-        row_alone(tp, it.b, it.h, it.i0, st.a + (r & ~31) + x);
+        __syncwarp();
+        unsigned again = __ballot_sync(0xffffffffu, live && !fine);
+        while (again) {
+          const int x = __ffs(again) - 1;
+          again &= again - 1;
+          row_alone(tp, ib, ih, i0, first + x);
+        }
       }
     }
-  } else {
-    regs_few();   // all of a warpgroup
   }
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
@@ -632,10 +783,12 @@ int window_attention_tc(const WindowArgs& a) {
   if (!sms) return TTT_ERR_CUDA;
   p.w = win_params(a);
   p.tiles = (a.N + 2 * kM - 1) / (2 * kM);
-  p.items = (long long)a.B * p.tiles * a.Hq;
+  const long long items = (long long)a.B * p.tiles * a.Hq;
+  if (items > 0x7fffffff) return 1;
+  p.items = (unsigned)items;
   p.wide_out = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.lay.out.batch % 8 == 0 &&
                a.lay.out.head % 8 == 0 && a.lay.out.token % 8 == 0;
-  const unsigned grid = (unsigned)(p.items < sms ? p.items : sms);
+  const unsigned grid = (unsigned)(items < sms ? items : sms);
   const double tok = (double)a.B * a.N;
   const double seen = a.N < (double)a.window + a.sinks ? a.N * 0.5 : (double)a.window + a.sinks;
   ProfScope ps(PT_WIN_TC, a.stream, 4.0 * tok * a.Hq * a.d * seen, tok * 4.0 * a.d * (a.Hq + a.Hk));
