@@ -402,42 +402,38 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
       }
       if (!tile && cur) umma_commit_w(&B->q_free);   // all scores of this item are under way
       const int k_at = uses, ks = k_at % NS, vs = v_at % NS;
-      bool k_here = false, v_here = false;
+      // what is there long before the weights
+      if (cur) ok = wait_all(&B->full[vs], (v_at / NS) & 1, p.status, lim);
+      if (tile) ok = ok && wait_all(&B->full[ks], (k_at / NS) & 1, p.status, lim);
+      const int fresh = cur & ~begun;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (fresh & (1 << u)) {
+          ok = ok && wait_all(&B->o_free[u], ((no >> u) & 1) ^ 1, p.status, lim);
+          no ^= 1 << u;
+        }
+      if (!ok) break;
+      tc_fence_after();
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         if (cur & (1 << u)) {
-          const bool first = !(begun & (1 << u));
-          ok = ok && wait_all(&B->p_full[u], (np >> u) & 1, p.status, lim);
-          if (first) {
-            ok = ok && wait_all(&B->o_free[u], ((no >> u) & 1) ^ 1, p.status, lim);
-            no ^= 1 << u;
-          }
-          if (!v_here) ok = ok && wait_all(&B->full[vs], (v_at / NS) & 1, p.status, lim);
+          ok = wait_all(&B->p_full[u], (np >> u) & 1, p.status, lim);
           if (!ok) break;
-          v_here = true;
           tc_fence_after();
-          outputs(u, vs, first);
+          outputs(u, vs, fresh & (1 << u));
           np ^= 1 << u;
-          begun |= 1 << u;
-          // the first tile's window begins the list's window tiles: without caches behind
-          // them, it has had its last where it needs no next one
-          if (u == 0 && !(nxt & 1) && !p.past) {
-            umma_commit_w(&B->o_full[0]);
-            told = 1;
-          }
         }
-        if (u == 1 && cur) umma_commit_w(&B->empty[vs]);
-        if (nxt & (1 << u)) {
-          if (!k_here) {
-            ok = ok && wait_all(&B->full[ks], (k_at / NS) & 1, p.status, lim);
-            if (!ok) break;
-            tc_fence_after();
-          }
-          k_here = true;
-          scores(u, ks);
+        if (nxt & (1 << u)) scores(u, ks);
+        // the first tile's window begins the list's window tiles: without caches behind them,
+        // it has had its last where it needs no next one
+        if (u == 0 && (cur & 1) && !(nxt & 1) && !p.past) {
+          umma_commit_w(&B->o_full[0]);
+          told = 1;
         }
       }
       if (!ok) break;
+      begun |= cur;
+      if (cur) umma_commit_w(&B->empty[vs]);
       if (tile) {
         umma_commit_w(&B->empty[ks]);
         v_at = k_at + 1;
@@ -588,11 +584,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
             if (row.seq != e.seq) a1 = b1 = c1 = -1;
           }
         }
-        auto mask = [&](float (&s)[32], int x) {
-          const uint32_t bits = span_bits(a0, a1, 32 * x) | span_bits(b0, b1, 32 * x) |
-                                span_bits(c0, c1, 32 * x);
+        auto seen = [&](int x) {   // bits of the 32 columns of part x
+          return span_bits(a0, a1, 32 * x) | span_bits(b0, b1, 32 * x) | span_bits(c0, c1, 32 * x);
+        };
+        auto mask = [&](float (&s)[32], uint32_t bits) {
+          if (__all_sync(0xffffffffu, bits == 0xffffffffu)) return;
 #pragma unroll
-          for (int y = 0; y < 32; ++y) s[y] = (bits >> y) & 1 ? s[y] : -INFINITY;
+          for (int y = 0; y < 32; ++y) s[y] = bits & (1u << y) ? s[y] : -INFINITY;
         };
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         auto largest = [&](const float (&s)[32]) {
@@ -612,10 +610,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
         } else {
 #pragma unroll 1
           for (int x = 0; x < 4; ++x) {
+            const uint32_t bits = seen(x);
+            if (!__any_sync(0xffffffffu, bits)) continue;
             float s[32];
             tmem_ld32(S + 32 * x, s);
             tmem_wait32(s);
-            mask(s, x);
+            mask(s, bits);
             largest(s);
           }
         }
@@ -630,7 +630,16 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
           uint32_t pw[16];
           tmem_ld32(S + 32 * x, s);
           tmem_wait32(s);
-          if (!whole) mask(s, x);
+          if (!whole) {
+            const uint32_t bits = seen(x);
+            if (!__any_sync(0xffffffffu, bits)) {
+#pragma unroll
+              for (int y = 0; y < 16; ++y) pw[y] = 0u;
+              tmem_st16(S + 16 * x, pw);
+              continue;
+            }
+            mask(s, bits);
+          }
 #pragma unroll
           for (int y = 0; y < 32; y += 4) {
             const float v0 = ex2(fmaf(s[y], c, -mc)), v1 = ex2(fmaf(s[y + 1], c, -mc));
@@ -661,19 +670,20 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
         __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + ib * p.lay.out.batch +
                             ih * p.lay.out.head + (first + (lane >> 3)) * p.lay.out.token +
                             (lane & 7) * 8;
+        const long long step = 4 * p.lay.out.token;
         bool fine = true;
 #pragma unroll 1
         for (int y = 0; y < NB; ++y) {   // 64 columns, through shared memory: whole lines are stored
           __syncwarp();
 #pragma unroll 1
-          for (int x = 0; x < 2; ++x) {
-            float o[32];
-            tmem_ld32(O + 64 * y + 32 * x, o);
-            tmem_wait32(o);
-            uint32_t ow[16];
+          for (int x = 0; x < 4; ++x) {
+            float o[16];
+            tmem_ld16_nowait(O + 64 * y + 16 * x, o);
+            tmem_wait_bind(o);
+            uint32_t ow[8];
             float big = 0.f;
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
+            for (int i = 0; i < 16; i += 2) {
               o[i] *= f;
               o[i + 1] *= f;
               big = fmaf(o[i], 0.f, fmaf(o[i + 1], 0.f, big));   // NaN if any is not finite
@@ -681,8 +691,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
             }
             fine = fine && big == 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * x + i) ^ (lane & 7)) << 4)) =
+            for (int i = 0; i < 2; ++i)
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((2 * x + i) ^ (lane & 7)) << 4)) =
                   make_uint4(ow[4 * i], ow[4 * i + 1], ow[4 * i + 2], ow[4 * i + 3]);
           }
           __syncwarp();
@@ -692,9 +702,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
           }
           if (64 * y + (lane & 7) * 8 < p.d) {
             __nv_bfloat16* at = to + 64 * y;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int n = 4 * i + (lane >> 3);
+#pragma unroll 2
+            for (int n = lane >> 3; n < 32; n += 4) {
               const uint4 v = *reinterpret_cast<const uint4*>(stage + n * 128 + (((lane & 7) ^ (n & 7)) << 4));
               if ((rows >> n) & 1) {
                 if (tp.wide_out) {
@@ -705,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
                   for (int j = 0; j < 8; ++j) at[j] = w8[j];
                 }
               }
-              at += 4 * p.lay.out.token;
+              at += step;
             }
           }
         }
