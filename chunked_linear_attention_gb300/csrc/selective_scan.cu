@@ -62,27 +62,77 @@ __device__ __forceinline__ float sum_over(float x) {
   return x;
 }
 
+// Sums of CPT channels over L lanes, spread over the lanes where there are four channels:
+// each step sends the half that the other lane goes on with.  Lane l ends with
+// `kept` channels from own_first on (all lanes above the fourth hold copies).
+template <int CPT, int L>
+struct LaneSums {
+  static constexpr int kept = CPT == 1 || L >= 4 ? 1 : CPT / L;
+  __device__ static __forceinline__ int own_first(int l) {
+    if (CPT == 1 || L == 1) return 0;
+    return L == 2 ? 2 * l : 2 * (l & 1) + ((l >> 1) & 1);
+  }
+  __device__ static __forceinline__ bool writes(int l) { return CPT == 1 ? l == 0 : l < 4; }
+  __device__ static __forceinline__ void sum(const float (&v)[CPT], int l, float (&y)[kept]) {
+    if constexpr (CPT == 1) {
+      y[0] = sum_over<L>(v[0]);
+    } else if constexpr (L == 1) {
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) y[i] = v[i];
+    } else {
+      const bool hi = l & 1;
+      const float a = (hi ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 1);
+      const float c = (hi ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 1);
+      if constexpr (L == 2) {
+        y[0] = a;
+        y[1] = c;
+      } else {
+        const bool up = l & 2;
+        float s = (up ? c : a) + __shfl_xor_sync(0xffffffffu, up ? a : c, 2);
+#pragma unroll
+        for (int o = 4; o < L; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        y[0] = s;
+      }
+    }
+  }
+};
+
+// Tokens of a tile, and bytes of shared memory: r and r x of its channels, B and C.
+constexpr int kTile = 16;
+template <int CPT, int SPT, int L, bool CARRY>
+constexpr int scan_smem() {
+  return kTile * (kScanThreads / L * CPT * 8 + (CARRY ? 1 : 2) * SPT * L * 4);
+}
+
 template <typename T, int CPT, int SPT, int L, bool CARRY, bool VEC>
-__global__ void __launch_bounds__(kScanThreads) selective_scan_kernel(
+__global__ void __launch_bounds__(kScanThreads, CPT == 1 ? 8 : 4) selective_scan_kernel(
     const __grid_constant__ ScanParams p) {
-  constexpr int TT = 16;                           // tokens of B and C in shared memory
   constexpr int SP = SPT * L;                      // padded S
   constexpr int CH = kScanThreads / L * CPT;       // channels of this CTA
-  __shared__ __align__(16) float bc[TT][CARRY ? 1 : 2][SP];
+  constexpr int NV = CH / CPT, STEP = kScanThreads / NV;   // groups of CPT channels; rows at once
+  using Sums = LaneSums<CPT, L>;
+  extern __shared__ __align__(16) float sm[];
+  float2* ru = reinterpret_cast<float2*>(sm);      // [kTile][CH]: r and r x, then y in r's place
+  float* bc = sm + kTile * CH * 2;                 // [kTile][B, C][SP]
+  constexpr int BC = (CARRY ? 1 : 2) * SP;
   pdl_launch_dependents();
   pdl_wait();
   const int seg = blockIdx.x, b = blockIdx.z;
   const int g = blockIdx.y / p.blocks, blk = blockIdx.y % p.blocks;
   const int Dg = p.D / p.G, tid = threadIdx.x, l = tid % L;
-  const int cg = blk * CH + tid / L * CPT;         // first channel, in the group
-  const int n = VEC ? (cg < Dg ? CPT : 0) : max(0, min(CPT, Dg - cg));
-  const int c = n > 0 ? g * Dg + cg : g * Dg;      // idle threads read along and store nothing
   if (seg == 0 && blockIdx.y == 0 && b == 0 && p.starts && !CARRY)
     check_starts(p.starts, p.n_seq, p.N, p.status);
-  const T* x = static_cast<const T*>(p.x) + b * p.lay.x.batch + c;
-  const T* dt = static_cast<const T*>(p.dt) + b * p.lay.dt.batch + c;
-  const T* z = CARRY || !p.z ? nullptr : static_cast<const T*>(p.z) + b * p.lay.z.batch + c;
-  T* out = static_cast<T*>(p.out) + b * p.lay.out.batch + c;
+  // channels whose states this thread holds
+  const int cl = tid / L * CPT, cg = blk * CH + cl;
+  const int n = max(0, min(CPT, Dg - cg));
+  const int c = g * Dg + (n > 0 ? cg : 0);         // idle threads read along and store nothing
+  // channels that this thread loads and stores, of every STEP-th row
+  const int vl = tid % NV * CPT, vg = blk * CH + vl, row0 = tid / NV;
+  const int vn = max(0, min(CPT, Dg - vg)), vc = g * Dg + vg;
+  const T* x = static_cast<const T*>(p.x) + b * p.lay.x.batch + vc;
+  const T* dt = static_cast<const T*>(p.dt) + b * p.lay.dt.batch + vc;
+  const T* z = CARRY || !p.z ? nullptr : static_cast<const T*>(p.z) + b * p.lay.z.batch + vc;
+  T* out = static_cast<T*>(p.out) + b * p.lay.out.batch + vc;
   const T* Bm = static_cast<const T*>(p.Bm) + b * p.lay.B.batch + (long long)g * p.S;
   const T* Cm = static_cast<const T*>(p.Cm) + b * p.lay.C.batch + (long long)g * p.S;
 
@@ -90,8 +140,8 @@ __global__ void __launch_bounds__(kScanThreads) selective_scan_kernel(
   float bias[CPT], dx[CPT], sum[CPT];
 #pragma unroll
   for (int e = 0; e < CPT; ++e) {
-    bias[e] = p.dt_bias && e < n ? p.dt_bias[c + e] : 0.f;
-    dx[e] = p.Dx && e < n ? p.Dx[c + e] : 0.f;
+    bias[e] = p.dt_bias && e < vn ? p.dt_bias[vc + e] : 0.f;
+    dx[e] = !CARRY && p.Dx && e < vn ? p.Dx[vc + e] : 0.f;
     sum[e] = 0.f;
 #pragma unroll
     for (int s = 0; s < SPT; s += 2) {
@@ -101,7 +151,6 @@ __global__ void __launch_bounds__(kScanThreads) selective_scan_kernel(
         a[i] = e < n && l * SPT + s + i < p.S
                    ? p.A[(long long)(c + e) * p.S + l * SPT + s + i] * kLog2e : 0.f;
       A[e][s / 2] = pack2(a[0], a[1]);
-      h[e][s / 2] = 0ull;
     }
   }
   auto load_state = [&](const float* src) {   // [D][S] of one sequence or segment, or NULL
@@ -162,51 +211,96 @@ __global__ void __launch_bounds__(kScanThreads) selective_scan_kernel(
       fresh = true;
     }
     const int stop = min(end, sq.t1);
-    for (; t < stop; t += TT) {
-      const int m = min(TT, stop - t);
-      __syncthreads();
+    for (; t < stop; t += kTile) {
+      const int m = min(kTile, stop - t);
+      __syncthreads();   // the tile before is done with the shared memory
       for (int e = tid; e < m * SP; e += kScanThreads) {
         const int j = e / SP, s = e % SP;
-        bc[j][0][s] = s < p.S ? to_f<T>(Bm[(t + j) * p.lay.B.token + s]) : 0.f;
-        if (!CARRY) bc[j][CARRY ? 0 : 1][s] = s < p.S ? to_f<T>(Cm[(t + j) * p.lay.C.token + s]) : 0.f;
+        bc[j * BC + s] = s < p.S ? to_f<T>(Bm[(t + j) * p.lay.B.token + s]) : 0.f;
+        if (!CARRY) bc[j * BC + SP + s] = s < p.S ? to_f<T>(Cm[(t + j) * p.lay.C.token + s]) : 0.f;
       }
-      __syncthreads();
-      for (int j = 0; j < m; ++j) {
-        float xv[CPT], r[CPT], y[CPT], zv[CPT];
-        load_row<T, CPT, VEC>(x + (t + j) * p.lay.x.token, n, xv);
-        load_row<T, CPT, VEC>(dt + (t + j) * p.lay.dt.token, n, r);
-        if (z) load_row<T, CPT, VEC>(z + (t + j) * p.lay.z.token, n, zv);
-        F2 acc[CPT];
+      if (vn > 0) {
+#pragma unroll 4
+        for (int j = row0; j < m; j += STEP) {
+          float xv[CPT], r[CPT];
+          load_row<T, CPT, VEC>(x + (t + j) * p.lay.x.token, vn, xv);
+          load_row<T, CPT, VEC>(dt + (t + j) * p.lay.dt.token, vn, r);
 #pragma unroll
-        for (int e = 0; e < CPT; ++e) {
-          r[e] += bias[e];
-          if (p.softplus) r[e] = softplus_f(r[e]);
-          if (CARRY) sum[e] += r[e];
-          const F2 rr = pack2(r[e], r[e]);
-          const float u = r[e] * xv[e];
-          const F2 uu = pack2(u, u);
-          acc[e] = 0ull;
-#pragma unroll
-          for (int s = 0; s < SPT / 2; ++s) {
-            float a0, a1;
-            unpack2(mul2(rr, A[e][s]), a0, a1);
-            const F2 a = pack2(ex2(a0), ex2(a1));
-            const F2 Bv = *reinterpret_cast<const F2*>(&bc[j][0][l * SPT + 2 * s]);
-            h[e][s] = fma2(a, h[e][s], mul2(uu, Bv));
-            if (!CARRY)
-              acc[e] = fma2(*reinterpret_cast<const F2*>(&bc[j][CARRY ? 0 : 1][l * SPT + 2 * s]), h[e][s], acc[e]);
+          for (int e = 0; e < CPT; ++e) {
+            r[e] += bias[e];
+            if (p.softplus) r[e] = softplus_f(r[e]);
+            ru[j * CH + vl + e] = make_float2(r[e], r[e] * xv[e]);
           }
         }
-        if (!CARRY) {
+      }
+      __syncthreads();
+#pragma unroll 1
+      for (int j = 0; j < m; ++j) {
+        float2* my = ru + j * CH + cl;
+        const float* bj = bc + j * BC + l * SPT;
+        float2 q[CPT];
+#pragma unroll
+        for (int e = 0; e < CPT; e += 2) {
+          if constexpr (CPT > 1) {
+            const float4 v = *reinterpret_cast<const float4*>(my + e);
+            q[e] = make_float2(v.x, v.y);
+            q[e + 1] = make_float2(v.z, v.w);
+          } else {
+            q[e] = my[e];
+          }
+        }
+        F2 acc[CPT];
+#pragma unroll
+        for (int e = 0; e < CPT; ++e) acc[e] = 0ull;
+#pragma unroll
+        for (int s = 0; s < SPT / 2; s += 2) {
+          const ulonglong2 Bv = *reinterpret_cast<const ulonglong2*>(bj + 2 * s);
+          ulonglong2 Cv = make_ulonglong2(0ull, 0ull);
+          if (!CARRY) Cv = *reinterpret_cast<const ulonglong2*>(bj + SP + 2 * s);
+#pragma unroll
+          for (int e = 0; e < CPT; ++e) {
+            const F2 rr = pack2(q[e].x, q[e].x), uu = pack2(q[e].y, q[e].y);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float a0, a1;
+              unpack2(mul2(rr, A[e][s + i]), a0, a1);
+              h[e][s + i] = fma2(pack2(ex2(a0), ex2(a1)), h[e][s + i], mul2(uu, i ? Bv.y : Bv.x));
+              if (!CARRY) acc[e] = fma2(i ? Cv.y : Cv.x, h[e][s + i], acc[e]);
+            }
+          }
+        }
+        if (CARRY) {
+#pragma unroll
+          for (int e = 0; e < CPT; ++e) sum[e] += q[e].x;
+        } else {
+          float v[CPT], y[Sums::kept];
 #pragma unroll
           for (int e = 0; e < CPT; ++e) {
             float a0, a1;
             unpack2(acc[e], a0, a1);
-            y[e] = sum_over<L>(a0 + a1) + dx[e] * xv[e];
+            v[e] = a0 + a1;
+          }
+          Sums::sum(v, l, y);
+          if (Sums::writes(l)) {
+#pragma unroll
+            for (int e = 0; e < Sums::kept; ++e) my[Sums::own_first(l) + e].x = y[e];
+          }
+        }
+      }
+      if (CARRY) continue;
+      __syncthreads();
+      if (vn > 0) {
+#pragma unroll 4
+        for (int j = row0; j < m; j += STEP) {
+          float xv[CPT], zv[CPT], y[CPT];
+          load_row<T, CPT, VEC>(x + (t + j) * p.lay.x.token, vn, xv);
+          if (z) load_row<T, CPT, VEC>(z + (t + j) * p.lay.z.token, vn, zv);
+#pragma unroll
+          for (int e = 0; e < CPT; ++e) {
+            y[e] = fmaf(dx[e], xv[e], ru[j * CH + vl + e].x);
             if (z) y[e] *= silu_f(zv[e]);
           }
-          if (l == 0 && n > 0)
-            store_row<T, CPT, VEC>(out + (t + j) * p.lay.out.token, n, y);
+          store_row<T, CPT, VEC>(out + (t + j) * p.lay.out.token, vn, y);
         }
       }
     }
@@ -268,26 +362,31 @@ ScanShape scan_shape(int B, int N, int D, int S, int G) {
   // shared memory serves four.  Otherwise one channel over S / 4 lanes, so that a token takes
   // little time.
   const long long work = (long long)B * N * D;
-  if (work >= 1 << 21 && D / G >= 128) {
-    s.cpt = 4;
-    s.spt = S <= 8 ? 8 : 16;
-  } else {
-    s.cpt = 1;
-    s.spt = 4;
-  }
+  const bool wide = work >= 1 << 21 && D / G >= 128;
+  s.cpt = wide ? 4 : 1;
+  s.spt = wide ? 8 : 4;
   s.lanes = 1;
   while (s.spt * s.lanes < S) s.lanes *= 2;
   const int ch = kScanThreads / s.lanes * s.cpt;
   s.blocks = (D / G + ch - 1) / ch;
-  // two rounds of CTAs on every SM, no segment shorter than 64 tokens
-  const long long ctas = (long long)B * G * s.blocks;
-  long long segs = ctas >= kScanSms ? 1 : (4ll * kScanSms + ctas - 1) / ctas;
+  // one round of CTAs, four on every SM; no segment shorter than 64 tokens
+  const long long ctas = (long long)B * G * s.blocks, room = 4 * kScanSms;
+  long long segs = room / ctas;
   const long long most = (N + 63) / 64;
   if (segs > most) segs = most;
   if (segs < 3) segs = 1;   // two segments carry as long as one runs
-  s.seg_tokens = (int)(((N + segs - 1) / segs + 15) / 16 * 16);
+  s.seg_tokens = (int)(((N + segs - 1) / segs + kTile - 1) / kTile * kTile);
   s.segs = (N + s.seg_tokens - 1) / s.seg_tokens;
   return s;
+}
+
+template <typename P>
+cudaError_t scan_launch(void (*kern)(P), dim3 grid, int smem, cudaStream_t stream, const P& p) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_grid(kern, grid, kScanThreads, smem, stream, p);
 }
 
 template <typename T, int CPT, int SPT, int L>
@@ -306,8 +405,8 @@ int launch_scan(const ScanArgs& a, ScanParams p, const ScanShape& s) {
       ProfScope ps(PT_SCAN_CARRY, a.stream, 4.0 * n * a.S, 2.0 * n * sizeof(T));
       const dim3 grid(s.segs - 1, a.G * s.blocks, a.B);
       const cudaError_t e =
-          vec ? launch_grid(selective_scan_kernel<T, CPT, SPT, L, true, CPT != 1>, grid, kScanThreads, 0, a.stream, p)
-              : launch_grid(selective_scan_kernel<T, CPT, SPT, L, true, false>, grid, kScanThreads, 0, a.stream, p);
+          vec ? scan_launch(selective_scan_kernel<T, CPT, SPT, L, true, CPT != 1>, grid, scan_smem<CPT, SPT, L, true>(), a.stream, p)
+              : scan_launch(selective_scan_kernel<T, CPT, SPT, L, true, false>, grid, scan_smem<CPT, SPT, L, true>(), a.stream, p);
       if (e != cudaSuccess) return TTT_ERR_CUDA;
     }
     const long long one = (long long)a.D * a.S;
@@ -318,31 +417,25 @@ int launch_scan(const ScanArgs& a, ScanParams p, const ScanShape& s) {
   ProfScope ps(PT_SCAN, a.stream, 6.0 * n * a.S, (a.z ? 4.0 : 3.0) * n * sizeof(T));
   const dim3 grid(s.segs, a.G * s.blocks, a.B);
   const cudaError_t e =
-      vec ? launch_grid(selective_scan_kernel<T, CPT, SPT, L, false, CPT != 1>, grid, kScanThreads, 0, a.stream, p)
-          : launch_grid(selective_scan_kernel<T, CPT, SPT, L, false, false>, grid, kScanThreads, 0, a.stream, p);
+      vec ? scan_launch(selective_scan_kernel<T, CPT, SPT, L, false, CPT != 1>, grid, scan_smem<CPT, SPT, L, false>(), a.stream, p)
+          : scan_launch(selective_scan_kernel<T, CPT, SPT, L, false, false>, grid, scan_smem<CPT, SPT, L, false>(), a.stream, p);
   return e == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 
 template <typename T, int CPT, int SPT>
 int scan_lanes(const ScanArgs& a, const ScanParams& p, const ScanShape& s) {
   if (s.lanes == 1) return launch_scan<T, CPT, SPT, 1>(a, p, s);
-  if constexpr (SPT != 8) {   // 8 numbers a thread serve S <= 8 alone
-    if (s.lanes == 2) return launch_scan<T, CPT, SPT, 2>(a, p, s);
-    if (s.lanes == 4) return launch_scan<T, CPT, SPT, 4>(a, p, s);
-    if (s.lanes == 8) return launch_scan<T, CPT, SPT, 8>(a, p, s);
-    if constexpr (SPT == 4) {
-      if (s.lanes == 16) return launch_scan<T, CPT, SPT, 16>(a, p, s);
-      if (s.lanes == 32) return launch_scan<T, CPT, SPT, 32>(a, p, s);
-    }
-  }
+  if (s.lanes == 2) return launch_scan<T, CPT, SPT, 2>(a, p, s);
+  if (s.lanes == 4) return launch_scan<T, CPT, SPT, 4>(a, p, s);
+  if (s.lanes == 8) return launch_scan<T, CPT, SPT, 8>(a, p, s);
+  if (s.lanes == 16) return launch_scan<T, CPT, SPT, 16>(a, p, s);
+  if constexpr (SPT == 4) return launch_scan<T, CPT, SPT, 32>(a, p, s);
   return TTT_ERR_UNSUPPORTED;
 }
 
 template <typename T>
 int scan_t(const ScanArgs& a, const ScanParams& p, const ScanShape& s) {
-  if (s.cpt == 1) return scan_lanes<T, 1, 4>(a, p, s);
-  if (s.spt == 8) return scan_lanes<T, 4, 8>(a, p, s);
-  return scan_lanes<T, 4, 16>(a, p, s);
+  return s.cpt == 1 ? scan_lanes<T, 1, 4>(a, p, s) : scan_lanes<T, 4, 8>(a, p, s);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
