@@ -60,26 +60,70 @@ __device__ __forceinline__ int row_slot(const int* slots, int n_slots, int b, in
   return bad ? -1 : slot;
 }
 
-// log(1 + e^x), from log1p(u) = 2 atanh(u / (2 + u)) with u = e^-|x| in (0, 1]: the series
-// in s = u / (2 + u) <= 1/3 ends at s^15, whose first missing term is 1/9^8 / 17 = 1.4e-9
-// of the sum, below half a step of fp32.
-__device__ __forceinline__ float softplus_f(float x) {
-  const float u = expf(-fabsf(x));
-  const float s = __fdividef(u, 2.f + u), t = s * s;
-  float p = 1.f / 15.f;
-  p = fmaf(p, t, 1.f / 13.f);
-  p = fmaf(p, t, 1.f / 11.f);
-  p = fmaf(p, t, 1.f / 9.f);
-  p = fmaf(p, t, 1.f / 7.f);
-  p = fmaf(p, t, 1.f / 5.f);
-  p = fmaf(p, t, 1.f / 3.f);
-  p = fmaf(p, t, 1.f);
-  return fmaxf(x, 0.f) + 2.f * s * p;
+// e^x through the base-2 exponential: off by 2^-22 and |x| 2^-24 (the product's rounding).
+__device__ __forceinline__ float exp_f(float x) { return ex2(x * 1.44269504088896341f); }
+
+// 1 / x for x in [1, 2^126); 0 above.
+__device__ __forceinline__ float rcp_f(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// x sigmoid(x).  Where e^-x passes 2^126 (x < -87) the fast quotient is 0; x = -inf gives
-// NaN, as the product -inf * 0 does.
-__device__ __forceinline__ float silu_f(float x) { return __fdividef(x, 1.f + expf(-x)); }
+// log(1 + e^x), from log1p(u) = 2 atanh(u / (2 + u)) with u = e^-|x| in (0, 1]: the series
+// in s = u / (2 + u) <= 1/3 ends at s^11, whose first missing term is at most 1/9^6 / 13 =
+// 1.4e-7 of the sum.  Two at a time, for the packed instructions.
+__device__ __forceinline__ void softplus2(float& x0, float& x1) {
+  const float u0 = exp_f(-fabsf(x0)), u1 = exp_f(-fabsf(x1));
+  const F2 s = pack2(u0 * rcp_f(2.f + u0), u1 * rcp_f(2.f + u1)), t = mul2(s, s);
+  auto all = [](float v) { return pack2(v, v); };
+  F2 p = all(1.f / 11.f);
+  p = fma2(p, t, all(1.f / 9.f));
+  p = fma2(p, t, all(1.f / 7.f));
+  p = fma2(p, t, all(1.f / 5.f));
+  p = fma2(p, t, all(1.f / 3.f));
+  p = fma2(p, t, all(1.f));
+  p = mul2(p, add2(s, s));
+  float y0, y1;
+  unpack2(p, y0, y1);
+  x0 = fmaxf(x0, 0.f) + y0;
+  x1 = fmaxf(x1, 0.f) + y1;
+}
+
+// x sigmoid(x).  Where e^-x passes 2^126 (x < -87) it is 0; x = -inf gives NaN, as the
+// product -inf * 0 does.
+__device__ __forceinline__ float silu_f(float x) { return x * rcp_f(1.f + exp_f(-x)); }
+
+// E neighbouring elements as they are; VEC: by one access (aligned to it).
+template <typename T, int E>
+struct alignas(sizeof(T) * E) Pack {
+  T v[E];
+};
+template <typename T, int E, bool VEC>
+__device__ __forceinline__ void load_pack(const T* p, int n, Pack<T, E>& v) {
+  if constexpr (VEC) {
+    v = *reinterpret_cast<const Pack<T, E>*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v.v[i] = i < n ? p[i] : from_f<T>(0.f);
+  }
+}
+
+// A pack as fp32 (two bf16 numbers of a word: the upper one is its own fp32 number).
+template <typename T, int E>
+__device__ __forceinline__ void pack_f(const Pack<T, E>& q, float (&v)[E]) {
+  if constexpr (sizeof(T) == 2 && E % 2 == 0) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&q);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = to_f<T>(q.v[i]);
+  }
+}
 
 // E neighbouring elements as fp32, and back; VEC: by one access (aligned to it).
 template <typename T, int E, bool VEC>

@@ -97,51 +97,275 @@ struct LaneSums {
   }
 };
 
-// Tokens of a tile, and bytes of shared memory: r and r x of its channels, B and C.
-constexpr int kTile = 16;
+// Tokens of a tile, and bytes of shared memory: two tiles of r and r x, B and C.
+template <int CPT, int L>
+constexpr int scan_tile() {
+  return kScanThreads / L * CPT > 256 ? 8 : 16;
+}
 template <int CPT, int SPT, int L, bool CARRY>
 constexpr int scan_smem() {
-  return kTile * (kScanThreads / L * CPT * 8 + (CARRY ? 1 : 2) * SPT * L * 4);
+  return 2 * scan_tile<CPT, L>() * (kScanThreads / L * CPT * 8 + (CARRY ? 1 : 2) * SPT * L * 4);
 }
 
+// The tiles of a segment: tokens t .. t + m - 1 of one sequence.
+struct ScanTile {
+  int t, m, seq;    // m 0: no more
+  bool first, last; // of the sequence
+};
+
+struct ScanTiles {
+  int t, end;
+  TokenSeq sq;
+  bool fresh;       // the state knows nothing of what came before the segment
+};
+
+template <int TILE>
+__device__ __forceinline__ ScanTile next_tile(const ScanParams& p, ScanTiles& w, int b) {
+  ScanTile r;
+  r.t = w.t;
+  r.m = 0;
+  r.seq = -1;
+  r.first = r.last = false;
+  while (w.t < w.end) {
+    if (w.t >= w.sq.t1) {
+      w.sq = token_seq(p.starts, p.n_seq, b, p.N, w.t);
+      if (w.sq.seq < 0) {
+        w.sq.t1 = 0;
+        w.fresh = true;
+        // before the first and behind the last sequence in one go
+        if (w.t < p.starts[0]) w.t = min(w.end, p.starts[0]);
+        else if (w.t >= p.starts[p.n_seq]) w.t = w.end;
+        else ++w.t;
+        continue;
+      }
+    }
+    r.t = w.t;
+    r.seq = w.sq.seq;
+    r.m = min(TILE, min(w.end, w.sq.t1) - w.t);
+    r.first = w.t == w.sq.t0;
+    w.fresh |= r.first;
+    w.t += r.m;
+    r.last = w.t == w.sq.t1;
+    break;
+  }
+  return r;
+}
+
+// One CTA: CH channels of one segment.  Four warps run the recurrence on a tile in shared
+// memory; four more bring the next tile's r, r x, B and C meanwhile, and turn the last tile's
+// sums into outputs.
 template <typename T, int CPT, int SPT, int L, bool CARRY, bool VEC>
-__global__ void __launch_bounds__(kScanThreads, CPT == 1 ? 8 : 4) selective_scan_kernel(
+__global__ void __launch_bounds__(2 * kScanThreads, CPT == 1 ? 3 : 2) selective_scan_kernel(
     const __grid_constant__ ScanParams p) {
   constexpr int SP = SPT * L;                      // padded S
   constexpr int CH = kScanThreads / L * CPT;       // channels of this CTA
+  constexpr int kTile = scan_tile<CPT, L>();
   constexpr int NV = CH / CPT, STEP = kScanThreads / NV;   // groups of CPT channels; rows at once
+  constexpr int ROWS = kTile / STEP > 0 ? kTile / STEP : 1;
+  // of them at a time: registers
+  constexpr int kMost = VEC && sizeof(T) == 2 ? (CARRY ? 4 : 2) : CPT == 1 ? 4 : 1;
+  constexpr int RB = ROWS < kMost ? ROWS : kMost;
   using Sums = LaneSums<CPT, L>;
-  extern __shared__ __align__(16) float sm[];
-  float2* ru = reinterpret_cast<float2*>(sm);      // [kTile][CH]: r and r x, then y in r's place
-  float* bc = sm + kTile * CH * 2;                 // [kTile][B, C][SP]
   constexpr int BC = (CARRY ? 1 : 2) * SP;
+  extern __shared__ __align__(16) float sm[];
+  float2* ru = reinterpret_cast<float2*>(sm);      // [2][kTile][CH]: r and r x, then y in r's place
+  float* bc = sm + 2 * kTile * CH * 2;             // [2][kTile][B, C][SP]
   pdl_launch_dependents();
   pdl_wait();
   const int seg = blockIdx.x, b = blockIdx.z;
   const int g = blockIdx.y / p.blocks, blk = blockIdx.y % p.blocks;
-  const int Dg = p.D / p.G, tid = threadIdx.x, l = tid % L;
+  const int Dg = p.D / p.G, tid = threadIdx.x % kScanThreads, l = tid % L;
+  const bool loads = threadIdx.x >= kScanThreads;
   if (seg == 0 && blockIdx.y == 0 && b == 0 && p.starts && !CARRY)
     check_starts(p.starts, p.n_seq, p.N, p.status);
-  // channels whose states this thread holds
+  const long long one = (long long)p.D * p.S;
+  ScanTiles w;
+  w.t = (int)((long long)seg * p.seg_tokens);
+  w.end = (int)min((long long)seg * p.seg_tokens + p.seg_tokens, (long long)p.N);
+  w.sq.t1 = 0;
+  w.fresh = false;
+
+  // registers of a block: 256 x 128 at launch, more for the warps with the states
+  constexpr int kFew = 96, kMany = 152;
+  static_assert(kFew + kMany <= 2 * 128, "registers at launch");
+  if (loads) {
+    if constexpr (CPT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFew));
+    const int vl = tid % NV * CPT, vg = blk * CH + vl, row0 = tid / NV;
+    const int vn = max(0, min(CPT, Dg - vg)), vc = g * Dg + vg;
+    const T* x = static_cast<const T*>(p.x) + b * p.lay.x.batch + vc;
+    const T* dt = static_cast<const T*>(p.dt) + b * p.lay.dt.batch + vc;
+    const T* z = CARRY || !p.z ? nullptr : static_cast<const T*>(p.z) + b * p.lay.z.batch + vc;
+    T* out = static_cast<T*>(p.out) + b * p.lay.out.batch + vc;
+    const T* Bm = static_cast<const T*>(p.Bm) + b * p.lay.B.batch + (long long)g * p.S;
+    const T* Cm = static_cast<const T*>(p.Cm) + b * p.lay.C.batch + (long long)g * p.S;
+    float bias[CPT], dx[CPT];
+#pragma unroll
+    for (int e = 0; e < CPT; ++e) {
+      bias[e] = p.dt_bias && e < vn ? p.dt_bias[vc + e] : 0.f;
+      dx[e] = !CARRY && p.Dx && e < vn ? p.Dx[vc + e] : 0.f;
+    }
+    // A turn finishes the tile `done` and puts the tile `next` in its place: a thread has the
+    // same rows and channels of both.  What it needs is on its way one part of a turn ahead.
+    using V = Pack<T, CPT>;
+    struct Part {
+      V xd[RB], zd[RB], xn[RB], rn[RB];
+    };
+    // (the rows of a part lie STEP tokens apart)
+    const long long dx_ = STEP * p.lay.x.token, ddt = STEP * p.lay.dt.token,
+                    dz = STEP * p.lay.z.token, dout = STEP * p.lay.out.token;
+    auto fetch = [&](const ScanTile& done, const ScanTile& next, int i0, Part& q) {
+      const int r0 = row0 + i0 * STEP;
+      const int nd = CARRY || vn <= 0 ? 0 : done.m, nn = vn <= 0 ? 0 : next.m;
+      const T* a = x + (done.t + r0) * p.lay.x.token;
+      const T* c = z + (done.t + r0) * p.lay.z.token;
+      const T* d = x + (next.t + r0) * p.lay.x.token;
+      const T* e = dt + (next.t + r0) * p.lay.dt.token;
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        if (!CARRY && r0 + i * STEP < nd) {
+          load_pack<T, CPT, VEC>(a, vn, q.xd[i]);
+          if (z) load_pack<T, CPT, VEC>(c, vn, q.zd[i]);
+        }
+        if (r0 + i * STEP < nn) {
+          load_pack<T, CPT, VEC>(d, vn, q.xn[i]);
+          load_pack<T, CPT, VEC>(e, vn, q.rn[i]);
+        }
+        a += dx_;
+        c += dz;
+        d += dx_;
+        e += ddt;
+      }
+    };
+    auto use = [&](const ScanTile& done, const ScanTile& next, float2* my, int i0, const Part& q) {
+      const int r0 = row0 + i0 * STEP;
+      const int nd = CARRY || vn <= 0 ? 0 : done.m, nn = vn <= 0 ? 0 : next.m;
+      T* o = out + (done.t + r0) * p.lay.out.token;
+      float2* at = my + r0 * CH;
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        if (!CARRY && r0 + i * STEP < nd) {
+          float y[CPT];
+#pragma unroll
+          for (int e = 0; e < CPT; e += 2) {
+            if constexpr (CPT > 1) {
+              const float4 v = *reinterpret_cast<const float4*>(at + e);
+              y[e] = v.x;
+              y[e + 1] = v.z;
+            } else {
+              y[e] = at[e].x;
+            }
+          }
+          float xv[CPT], zv[CPT];
+          pack_f(q.xd[i], xv);
+          if (z) pack_f(q.zd[i], zv);
+#pragma unroll
+          for (int e = 0; e < CPT; ++e) {
+            y[e] = fmaf(dx[e], xv[e], y[e]);
+            if (z) y[e] *= silu_f(zv[e]);
+          }
+          store_row<T, CPT, VEC>(o, vn, y);
+        }
+        if (r0 + i * STEP < nn) {
+          float r[CPT + 1], xv[CPT], rv[CPT];
+          pack_f(q.xn[i], xv);
+          pack_f(q.rn[i], rv);
+#pragma unroll
+          for (int e = 0; e < CPT; ++e) r[e] = rv[e] + bias[e];
+          r[CPT] = 0.f;
+          if (p.softplus) {
+#pragma unroll
+            for (int e = 0; e < CPT; e += 2) softplus2(r[e], r[e + 1]);
+          }
+          if constexpr (CPT > 1) {
+#pragma unroll
+            for (int e = 0; e < CPT; e += 2)
+              *reinterpret_cast<float4*>(at + e) =
+                  make_float4(r[e], r[e] * xv[e], r[e + 1], r[e + 1] * xv[e + 1]);
+          } else {
+            at[0] = make_float2(r[0], r[0] * xv[0]);
+          }
+        }
+        o += dout;
+        at += STEP * CH;
+      }
+    };
+    // B and C of a tile, a turn ahead too where they are few
+    constexpr int NBC = (kTile * SP + kScanThreads - 1) / kScanThreads;
+    constexpr bool AHEAD = NBC <= 4;
+    T bq[AHEAD ? NBC : 1], cq[AHEAD ? NBC : 1];
+    auto fetch_bc = [&](const ScanTile& next) {
+      if constexpr (AHEAD) {
+#pragma unroll
+        for (int i = 0; i < NBC; ++i) {
+          const int e = tid + i * kScanThreads, j = e / SP, s = e % SP;
+          bq[i] = cq[i] = from_f<T>(0.f);
+          if (j < next.m && s < p.S) {
+            bq[i] = Bm[(next.t + j) * p.lay.B.token + s];
+            if (!CARRY) cq[i] = Cm[(next.t + j) * p.lay.C.token + s];
+          }
+        }
+      }
+    };
+    // the turn's parts, with the first one of the turn after it (done2, next2) fetched last
+    auto turn = [&](const ScanTile& done, const ScanTile& next, const ScanTile& done2,
+                    const ScanTile& next2, int buf, Part& q) {
+      float2* my = ru + buf * kTile * CH + vl;
+      float* mb = bc + buf * kTile * BC;
+      if constexpr (AHEAD) {
+#pragma unroll
+        for (int i = 0; i < NBC; ++i) {
+          const int e = tid + i * kScanThreads, j = e / SP, s = e % SP;
+          if (j < kTile) {
+            mb[j * BC + s] = to_f<T>(bq[i]);
+            if (!CARRY) mb[j * BC + SP + s] = to_f<T>(cq[i]);
+          }
+        }
+        fetch_bc(next2);
+      } else {
+        for (int e = tid; e < next.m * SP; e += kScanThreads) {
+          const int j = e / SP, s = e % SP;
+          mb[j * BC + s] = s < p.S ? to_f<T>(Bm[(next.t + j) * p.lay.B.token + s]) : 0.f;
+          if (!CARRY)
+            mb[j * BC + SP + s] = s < p.S ? to_f<T>(Cm[(next.t + j) * p.lay.C.token + s]) : 0.f;
+        }
+      }
+#pragma unroll 1
+      for (int i0 = 0; i0 < ROWS; i0 += RB) {
+        Part f;
+        const bool more = i0 + RB < ROWS;
+        fetch(more ? done : done2, more ? next : next2, more ? i0 + RB : 0, f);
+        use(done, next, my, i0, q);
+        q = f;
+      }
+    };
+    ScanTile none;
+    none.t = none.m = 0;
+    ScanTile prev = none, cur = next_tile<kTile>(p, w, b), nxt = next_tile<kTile>(p, w, b);
+    Part q;
+    fetch(none, cur, 0, q);
+    fetch_bc(cur);
+    turn(none, cur, none, nxt, 0, q);
+    __syncthreads();
+    for (int k = 0; cur.m > 0; ++k) {
+      const ScanTile nx2 = next_tile<kTile>(p, w, b);
+      turn(prev, nxt, cur, nx2, (k + 1) & 1, q);
+      __syncthreads();
+      prev = cur;
+      cur = nxt;
+      nxt = nx2;
+      if (cur.m == 0 && !CARRY) turn(prev, none, none, none, k & 1, q);
+    }
+    return;
+  }
+
+  if constexpr (CPT > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMany));
   const int cl = tid / L * CPT, cg = blk * CH + cl;
   const int n = max(0, min(CPT, Dg - cg));
-  const int c = g * Dg + (n > 0 ? cg : 0);         // idle threads read along and store nothing
-  // channels that this thread loads and stores, of every STEP-th row
-  const int vl = tid % NV * CPT, vg = blk * CH + vl, row0 = tid / NV;
-  const int vn = max(0, min(CPT, Dg - vg)), vc = g * Dg + vg;
-  const T* x = static_cast<const T*>(p.x) + b * p.lay.x.batch + vc;
-  const T* dt = static_cast<const T*>(p.dt) + b * p.lay.dt.batch + vc;
-  const T* z = CARRY || !p.z ? nullptr : static_cast<const T*>(p.z) + b * p.lay.z.batch + vc;
-  T* out = static_cast<T*>(p.out) + b * p.lay.out.batch + vc;
-  const T* Bm = static_cast<const T*>(p.Bm) + b * p.lay.B.batch + (long long)g * p.S;
-  const T* Cm = static_cast<const T*>(p.Cm) + b * p.lay.C.batch + (long long)g * p.S;
-
+  const int c = g * Dg + (n > 0 ? cg : 0);   // idle threads run along and store nothing
   F2 A[CPT][SPT / 2], h[CPT][SPT / 2];
-  float bias[CPT], dx[CPT], sum[CPT];
+  float sum[CPT];
 #pragma unroll
   for (int e = 0; e < CPT; ++e) {
-    bias[e] = p.dt_bias && e < vn ? p.dt_bias[vc + e] : 0.f;
-    dx[e] = !CARRY && p.Dx && e < vn ? p.Dx[vc + e] : 0.f;
     sum[e] = 0.f;
 #pragma unroll
     for (int s = 0; s < SPT; s += 2) {
@@ -179,8 +403,6 @@ __global__ void __launch_bounds__(kScanThreads, CPT == 1 ? 8 : 4) selective_scan
             dst[(long long)(c + e) * p.S + l * SPT + s + i] = v[i];
       }
   };
-  const long long one = (long long)p.D * p.S;
-
   // the states of empty sequences, spread over the segments
   if (!CARRY && p.state_out && p.starts)
     for (int s = seg; s < p.n_seq; s += p.segs)
@@ -188,124 +410,69 @@ __global__ void __launch_bounds__(kScanThreads, CPT == 1 ? 8 : 4) selective_scan
         load_state(p.state_in ? p.state_in + s * one : nullptr);
         store_state(p.state_out + s * one);
       }
-
-  const long long first = (long long)seg * p.seg_tokens;
-  const int end = (int)min(first + p.seg_tokens, (long long)p.N);
-  int t = (int)first;
-  bool fresh = false;   // the state knows nothing of what came before the segment
   if (!CARRY && seg > 0) load_state(p.seg_state + ((long long)b * p.segs + seg) * one);
   else load_state(nullptr);
-
-  while (t < end) {
-    const TokenSeq sq = token_seq(p.starts, p.n_seq, b, p.N, t);
-    if (sq.seq < 0) {
-      fresh = true;
-      // before the first and behind the last sequence in one go
-      if (t < p.starts[0]) t = min(end, p.starts[0]);
-      else if (t >= p.starts[p.n_seq]) t = end;
-      else ++t;
-      continue;
-    }
-    if (t == sq.t0) {
-      load_state(p.state_in ? p.state_in + sq.seq * one : nullptr);
-      fresh = true;
-    }
-    const int stop = min(end, sq.t1);
-    for (; t < stop; t += kTile) {
-      const int m = min(kTile, stop - t);
-      __syncthreads();   // the tile before is done with the shared memory
-      for (int e = tid; e < m * SP; e += kScanThreads) {
-        const int j = e / SP, s = e % SP;
-        bc[j * BC + s] = s < p.S ? to_f<T>(Bm[(t + j) * p.lay.B.token + s]) : 0.f;
-        if (!CARRY) bc[j * BC + SP + s] = s < p.S ? to_f<T>(Cm[(t + j) * p.lay.C.token + s]) : 0.f;
-      }
-      if (vn > 0) {
-#pragma unroll 4
-        for (int j = row0; j < m; j += STEP) {
-          float xv[CPT], r[CPT];
-          load_row<T, CPT, VEC>(x + (t + j) * p.lay.x.token, vn, xv);
-          load_row<T, CPT, VEC>(dt + (t + j) * p.lay.dt.token, vn, r);
-#pragma unroll
-          for (int e = 0; e < CPT; ++e) {
-            r[e] += bias[e];
-            if (p.softplus) r[e] = softplus_f(r[e]);
-            ru[j * CH + vl + e] = make_float2(r[e], r[e] * xv[e]);
-          }
-        }
-      }
-      __syncthreads();
+  ScanTile cur = next_tile<kTile>(p, w, b);
+  __syncthreads();
+  for (int k = 0; cur.m > 0; ++k) {
+    const ScanTile nxt = next_tile<kTile>(p, w, b);
+    if (cur.first) load_state(p.state_in ? p.state_in + cur.seq * one : nullptr);
+    float2* my = ru + (k & 1) * kTile * CH + cl;
+    const float* bj = bc + (k & 1) * kTile * BC + l * SPT;
 #pragma unroll 1
-      for (int j = 0; j < m; ++j) {
-        float2* my = ru + j * CH + cl;
-        const float* bj = bc + j * BC + l * SPT;
-        float2 q[CPT];
+    for (int j = 0; j < cur.m; ++j, my += CH, bj += BC) {
+      float2 q[CPT];
 #pragma unroll
-        for (int e = 0; e < CPT; e += 2) {
-          if constexpr (CPT > 1) {
-            const float4 v = *reinterpret_cast<const float4*>(my + e);
-            q[e] = make_float2(v.x, v.y);
-            q[e + 1] = make_float2(v.z, v.w);
-          } else {
-            q[e] = my[e];
-          }
-        }
-        F2 acc[CPT];
-#pragma unroll
-        for (int e = 0; e < CPT; ++e) acc[e] = 0ull;
-#pragma unroll
-        for (int s = 0; s < SPT / 2; s += 2) {
-          const ulonglong2 Bv = *reinterpret_cast<const ulonglong2*>(bj + 2 * s);
-          ulonglong2 Cv = make_ulonglong2(0ull, 0ull);
-          if (!CARRY) Cv = *reinterpret_cast<const ulonglong2*>(bj + SP + 2 * s);
-#pragma unroll
-          for (int e = 0; e < CPT; ++e) {
-            const F2 rr = pack2(q[e].x, q[e].x), uu = pack2(q[e].y, q[e].y);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float a0, a1;
-              unpack2(mul2(rr, A[e][s + i]), a0, a1);
-              h[e][s + i] = fma2(pack2(ex2(a0), ex2(a1)), h[e][s + i], mul2(uu, i ? Bv.y : Bv.x));
-              if (!CARRY) acc[e] = fma2(i ? Cv.y : Cv.x, h[e][s + i], acc[e]);
-            }
-          }
-        }
-        if (CARRY) {
-#pragma unroll
-          for (int e = 0; e < CPT; ++e) sum[e] += q[e].x;
+      for (int e = 0; e < CPT; e += 2) {
+        if constexpr (CPT > 1) {
+          const float4 v = *reinterpret_cast<const float4*>(my + e);
+          q[e] = make_float2(v.x, v.y);
+          q[e + 1] = make_float2(v.z, v.w);
         } else {
-          float v[CPT], y[Sums::kept];
+          q[e] = my[e];
+        }
+      }
+      F2 acc[CPT];
 #pragma unroll
-          for (int e = 0; e < CPT; ++e) {
+      for (int e = 0; e < CPT; ++e) acc[e] = 0ull;
+#pragma unroll
+      for (int s = 0; s < SPT / 2; s += 2) {
+        const ulonglong2 Bv = *reinterpret_cast<const ulonglong2*>(bj + 2 * s);
+        ulonglong2 Cv = make_ulonglong2(0ull, 0ull);
+        if (!CARRY) Cv = *reinterpret_cast<const ulonglong2*>(bj + SP + 2 * s);
+#pragma unroll
+        for (int e = 0; e < CPT; ++e) {
+          const F2 rr = pack2(q[e].x, q[e].x), uu = pack2(q[e].y, q[e].y);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
             float a0, a1;
-            unpack2(acc[e], a0, a1);
-            v[e] = a0 + a1;
-          }
-          Sums::sum(v, l, y);
-          if (Sums::writes(l)) {
-#pragma unroll
-            for (int e = 0; e < Sums::kept; ++e) my[Sums::own_first(l) + e].x = y[e];
+            unpack2(mul2(rr, A[e][s + i]), a0, a1);
+            h[e][s + i] = fma2(pack2(ex2(a0), ex2(a1)), h[e][s + i], mul2(uu, i ? Bv.y : Bv.x));
+            if (!CARRY) acc[e] = fma2(i ? Cv.y : Cv.x, h[e][s + i], acc[e]);
           }
         }
       }
-      if (CARRY) continue;
-      __syncthreads();
-      if (vn > 0) {
-#pragma unroll 4
-        for (int j = row0; j < m; j += STEP) {
-          float xv[CPT], zv[CPT], y[CPT];
-          load_row<T, CPT, VEC>(x + (t + j) * p.lay.x.token, vn, xv);
-          if (z) load_row<T, CPT, VEC>(z + (t + j) * p.lay.z.token, vn, zv);
+      if (CARRY) {
 #pragma unroll
-          for (int e = 0; e < CPT; ++e) {
-            y[e] = fmaf(dx[e], xv[e], ru[j * CH + vl + e].x);
-            if (z) y[e] *= silu_f(zv[e]);
-          }
-          store_row<T, CPT, VEC>(out + (t + j) * p.lay.out.token, vn, y);
+        for (int e = 0; e < CPT; ++e) sum[e] += q[e].x;
+      } else {
+        float v[CPT], y[Sums::kept];
+#pragma unroll
+        for (int e = 0; e < CPT; ++e) {
+          float a0, a1;
+          unpack2(acc[e], a0, a1);
+          v[e] = a0 + a1;
+        }
+        Sums::sum(v, l, y);
+        if (Sums::writes(l)) {
+#pragma unroll
+          for (int e = 0; e < Sums::kept; ++e) my[Sums::own_first(l) + e].x = y[e];
         }
       }
     }
-    t = stop;
-    if (!CARRY && p.state_out && stop == sq.t1) store_state(p.state_out + sq.seq * one);
+    if (!CARRY && p.state_out && cur.last) store_state(p.state_out + cur.seq * one);
+    __syncthreads();
+    cur = nxt;
   }
   if (CARRY) {
     const long long at = (long long)b * p.segs + seg;
@@ -315,7 +482,7 @@ __global__ void __launch_bounds__(kScanThreads, CPT == 1 ? 8 : 4) selective_scan
       for (int e = 0; e < CPT; ++e)
         if (e < n) p.seg_sum[at * p.D + c + e] = sum[e];
     }
-    if (blockIdx.y == 0 && tid == 0) p.seg_new[at] = fresh;
+    if (blockIdx.y == 0 && tid == 0) p.seg_new[at] = w.fresh;
   }
 }
 
@@ -369,13 +536,13 @@ ScanShape scan_shape(int B, int N, int D, int S, int G) {
   while (s.spt * s.lanes < S) s.lanes *= 2;
   const int ch = kScanThreads / s.lanes * s.cpt;
   s.blocks = (D / G + ch - 1) / ch;
-  // one round of CTAs, four on every SM; no segment shorter than 64 tokens
-  const long long ctas = (long long)B * G * s.blocks, room = 4 * kScanSms;
+  // one round of CTAs, two on every SM; no segment shorter than 64 tokens
+  const long long ctas = (long long)B * G * s.blocks, room = 2 * kScanSms;
   long long segs = room / ctas;
   const long long most = (N + 63) / 64;
   if (segs > most) segs = most;
   if (segs < 3) segs = 1;   // two segments carry as long as one runs
-  s.seg_tokens = (int)(((N + segs - 1) / segs + kTile - 1) / kTile * kTile);
+  s.seg_tokens = (int)(((N + segs - 1) / segs + 15) / 16 * 16);   // whole tiles
   s.segs = (N + s.seg_tokens - 1) / s.seg_tokens;
   return s;
 }
@@ -386,7 +553,7 @@ cudaError_t scan_launch(void (*kern)(P), dim3 grid, int smem, cudaStream_t strea
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  return launch_grid(kern, grid, kScanThreads, smem, stream, p);
+  return launch_grid(kern, grid, 2 * kScanThreads, smem, stream, p);
 }
 
 template <typename T, int CPT, int SPT, int L>
@@ -489,7 +656,10 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ 
     if (p.dt_bias) r += p.dt_bias[c];
     if (p.z) zv = to_f<T>(static_cast<const T*>(p.z)[b * p.lay.z.batch + c]);
   }
-  if (p.softplus) r = softplus_f(r);
+  if (p.softplus) {
+    float none = 0.f;
+    softplus2(r, none);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float Bv = i < n ? to_f<T>(Bm[s0 + i]) : 0.f, Cv = i < n ? to_f<T>(Cm[s0 + i]) : 0.f;
