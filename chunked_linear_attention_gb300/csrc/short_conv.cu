@@ -29,43 +29,96 @@ struct ConvParams {
 };
 
 // ------------------------------------------------------------ whole sequences
-// A thread has E neighbouring channels (16 bytes) of TT tokens, the last W - 1 inputs in
-// registers; neighbouring threads have neighbouring channels.  The inputs before its first
-// token are read again, from the L2.
-constexpr int kConvTokens = 16;
+// A thread has E neighbouring channels (16 bytes) of kConvTokens tokens, the last W - 1
+// inputs in registers; neighbouring threads have neighbouring channels.  The inputs before
+// its first token are read again, from the L2.  Four tokens are worked on while the next
+// four are on their way; channels go in pairs through the packed fp32 instructions (an
+// element takes two exponential-unit operations for the SiLU and about eight others, which
+// would take longer one at a time than the memory does).
+constexpr int kConvTokens = 32, kConvGroup = 4;
 
 template <typename T, int W, int E, bool VEC>
 __global__ void __launch_bounds__(128) short_conv_kernel(const __grid_constant__ ConvParams p) {
+  constexpr int P = (E + 1) / 2, U = kConvGroup;   // pairs of channels
   pdl_launch_dependents();
   pdl_wait();
   if (blockIdx.x == 0 && p.starts) check_starts(p.starts, p.n_seq, p.N, p.status);
   const long long u = blockIdx.x * 128ll + threadIdx.x;
   if (u >= p.units) return;
-  const int c = (int)(u % p.vecs) * E;
-  const long long bt = u / p.vecs;
-  const int tile = (int)(bt % p.tiles), b = (int)(bt / p.tiles);
+  const int bt = (int)(u / p.vecs), c = (int)(u - (long long)bt * p.vecs) * E;
+  const int b = bt / p.tiles, tile = bt - b * p.tiles;
   const int n = VEC ? E : min(E, p.D - c);
-  float w[W][E], bias[E];
+  F2 w[W][P], bias[P];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    bias[e] = p.bias && e < n ? p.bias[c + e] : 0.f;
+  for (int e = 0; e < P; ++e) {
+    float v[2];
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j][e] = e < n ? p.w[(long long)(c + e) * W + j] : 0.f;
+    for (int i = 0; i < 2; ++i) v[i] = p.bias && 2 * e + i < n ? p.bias[c + 2 * e + i] : 0.f;
+    bias[e] = pack2(v[0], v[1]);
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        v[i] = 2 * e + i < n ? p.w[(long long)(c + 2 * e + i) * W + j] : 0.f;
+      w[j][e] = pack2(v[0], v[1]);
+    }
   }
   const T* x = static_cast<const T*>(p.x) + b * p.lay.x.batch + c;
   T* out = static_cast<T*>(p.out) + b * p.lay.out.batch + c;
   const T* sin = static_cast<const T*>(p.state_in);
   T* sout = static_cast<T*>(p.state_out);
+  using V = Pack<T, E>;
 
-  // input `row` of a sequence's state (0: the oldest) before its first token
-  auto from_state = [&](int seq, int row, float (&v)[E]) {
+  auto zero = [&](V& v) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = 0.f;
-    if (sin) load_row<T, E, VEC>(sin + ((long long)seq * (W - 1) + row) * p.D + c, n, v);
+    for (int e = 0; e < E; ++e) v.v[e] = from_f<T>(0.f);
   };
-  auto input = [&](const TokenSeq& s, int t, float (&v)[E]) {   // token t, perhaps before t0
-    if (t >= s.t0) load_row<T, E, VEC>(x + t * p.lay.x.token, n, v);
+  // input `row` of a sequence's state (0: the oldest) before its first token
+  auto from_state = [&](int seq, int row, V& v) {
+    zero(v);
+    if (sin) load_pack<T, E, VEC>(sin + ((long long)seq * (W - 1) + row) * p.D + c, n, v);
+  };
+  auto to_state = [&](int seq, int row, const V& v) {
+    T* to = sout + ((long long)seq * (W - 1) + row) * p.D + c;
+    if constexpr (VEC) {
+      *reinterpret_cast<V*>(to) = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (e < n) to[e] = v.v[e];
+    }
+  };
+  auto input = [&](const TokenSeq& s, int t, V& v) {   // token t, perhaps before t0
+    if (t >= s.t0) load_pack<T, E, VEC>(x + t * p.lay.x.token, n, v);
     else from_state(s.seq, W - 1 + (t - s.t0), v);
+  };
+  auto pairs = [&](const V& q, F2 (&v)[P]) {
+    float f[E];
+    pack_f(q, f);
+#pragma unroll
+    for (int e = 0; e < P; ++e) v[e] = pack2(f[2 * e], 2 * e + 1 < E ? f[2 * e + 1] : 0.f);
+  };
+  const F2 l2e = pack2(-1.44269504088896341f, -1.44269504088896341f), ones = pack2(1.f, 1.f);
+  // one output from the W inputs that end with its token
+  auto one = [&](const F2 (*h)[P], T* to) {
+    float y[E];
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      F2 a = bias[e];
+#pragma unroll
+      for (int j = 0; j < W; ++j) a = fma2(w[j][e], h[j][e], a);
+      if (p.silu) {   // a / (1 + e^-a)
+        float e0, e1;
+        unpack2(mul2(a, l2e), e0, e1);
+        unpack2(add2(pack2(ex2(e0), ex2(e1)), ones), e0, e1);
+        a = mul2(a, pack2(rcp_f(e0), rcp_f(e1)));
+      }
+      float a0, a1;
+      unpack2(a, a0, a1);
+      y[2 * e] = a0;
+      if (2 * e + 1 < E) y[2 * e + 1] = a1;
+    }
+    store_row<T, E, VEC>(to, n, y);
   };
 
   // the states of empty sequences, spread over the tiles
@@ -73,9 +126,9 @@ __global__ void __launch_bounds__(128) short_conv_kernel(const __grid_constant__
     for (int s = tile; s < p.n_seq; s += p.tiles)
       if (p.starts[s] == p.starts[s + 1])
         for (int r = 0; r < W - 1; ++r) {
-          float v[E];
+          V v;
           from_state(s, r, v);
-          store_row<T, E, VEC>(sout + ((long long)s * (W - 1) + r) * p.D + c, n, v);
+          to_state(s, r, v);
         }
 
   const int end = min((tile + 1) * kConvTokens, p.N);
@@ -86,31 +139,52 @@ __global__ void __launch_bounds__(128) short_conv_kernel(const __grid_constant__
       ++t;
       continue;
     }
-    float h[W - 1][E];
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) input(s, t - (W - 1) + j, h[j]);
+    F2 h[W - 1 + U][P];   // inputs t - W + 1 .. t + U - 1
+    V q[U];
     const int stop = min(end, s.t1);
-#pragma unroll 4
-    for (; t < stop; ++t) {
-      float v[E], y[E];
-      load_row<T, E, VEC>(x + t * p.lay.x.token, n, v);
+    const T* xt = x + t * p.lay.x.token;
+    T* ot = out + t * p.lay.out.token;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        float a = bias[e];
+    for (int i = 0; i < U; ++i)
+      if (t + i < stop) load_pack<T, E, VEC>(xt + i * p.lay.x.token, n, q[i]);
+    {
+      V v[W - 1];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) a = fmaf(w[j][e], h[j][e], a);
-        a = fmaf(w[W - 1][e], v[e], a);
-        y[e] = p.silu ? silu_f(a) : a;
+      for (int j = 0; j < W - 1; ++j) input(s, t - (W - 1) + j, v[j]);
 #pragma unroll
-        for (int j = 0; j + 1 < W - 1; ++j) h[j][e] = h[j + 1][e];
-        h[W - 2][e] = v[e];
+      for (int j = 0; j < W - 1; ++j) pairs(v[j], h[j]);
+    }
+#pragma unroll 1
+    while (t < stop) {
+      const int m = min(U, stop - t);
+#pragma unroll
+      for (int i = 0; i < U; ++i) pairs(q[i], h[W - 1 + i]);
+      xt += U * p.lay.x.token;
+      if (t + 2 * U <= stop) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) load_pack<T, E, VEC>(xt + i * p.lay.x.token, n, q[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (t + U + i < stop) load_pack<T, E, VEC>(xt + i * p.lay.x.token, n, q[i]);
       }
-      store_row<T, E, VEC>(out + t * p.lay.out.token, n, y);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (i < m) one(h + i, ot + i * p.lay.out.token);
+      ot += U * p.lay.out.token;
+      t += m;
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int e = 0; e < P; ++e) h[j][e] = h[j + U][e];
     }
     if (sout && stop == s.t1) {
 #pragma unroll
-      for (int r = 0; r < W - 1; ++r)
-        store_row<T, E, VEC>(sout + ((long long)s.seq * (W - 1) + r) * p.D + c, n, h[r]);
+      for (int r = 0; r < W - 1; ++r) {
+        V v;
+        input(s, s.t1 - (W - 1) + r, v);
+        to_state(s.seq, r, v);
+      }
     }
   }
 }
@@ -128,7 +202,7 @@ int conv_w(const ConvArgs& a, ConvParams p) {
   p.tiles = (a.N + kConvTokens - 1) / kConvTokens;
   p.units = (long long)a.B * p.tiles * p.vecs;
   const long long grid = (p.units + 127) / 128;
-  if (grid > INT_MAX) return TTT_ERR_UNSUPPORTED;
+  if (grid > INT_MAX || (long long)a.B * p.tiles > INT_MAX) return TTT_ERR_UNSUPPORTED;
   const double n = (double)a.B * a.N * a.D;
   ProfScope ps(PT_CONV, a.stream, 2.0 * n * W, 2.0 * n * sizeof(T));
   const cudaError_t e =
