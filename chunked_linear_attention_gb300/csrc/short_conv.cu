@@ -22,20 +22,21 @@ struct ConvParams {
   void* out;
   void* state_out;
   int* status;
-  int n_seq, N, D, vecs, tiles;
+  int n_seq, N, D, vecs, tiles, tokens;
   long long units;       // batch x tiles x vecs
   int silu;
   short_conv_layout lay;
 };
 
 // ------------------------------------------------------------ whole sequences
-// A thread has E neighbouring channels (16 bytes) of kConvTokens tokens, the last W - 1
-// inputs in registers; neighbouring threads have neighbouring channels.  The inputs before
-// its first token are read again, from the L2.  Four tokens are worked on while the next
-// four are on their way; channels go in pairs through the packed fp32 instructions (an
-// element takes two exponential-unit operations for the SiLU and about eight others, which
-// would take longer one at a time than the memory does).
-constexpr int kConvTokens = 32, kConvGroup = 4;
+// A thread has E neighbouring channels of up to 64 tokens, the last W - 1 inputs in
+// registers; neighbouring threads have neighbouring channels.  The inputs before its first
+// token are read again, from the L2.  Eight tokens are worked on while the next eight are on
+// their way; channels go in pairs through the packed fp32 instructions.  What is in flight
+// decides: with eight bf16 channels a thread (16 bytes an access, 159 registers) 2 x 32768
+// tokens of 1536 channels take 108 us, with four (8 bytes) and four tokens 88, and eight
+// tokens 76; the filters spilled to local memory for more blocks cost far more.
+constexpr int kConvGroup = 8;
 
 template <typename T, int W, int E, bool VEC>
 __global__ void __launch_bounds__(128) short_conv_kernel(const __grid_constant__ ConvParams p) {
@@ -131,8 +132,8 @@ __global__ void __launch_bounds__(128) short_conv_kernel(const __grid_constant__
           to_state(s, r, v);
         }
 
-  const int end = min((tile + 1) * kConvTokens, p.N);
-  int t = tile * kConvTokens;
+  const int end = min((tile + 1) * p.tokens, p.N);
+  int t = tile * p.tokens;
   while (t < end) {
     const TokenSeq s = token_seq(p.starts, p.n_seq, b, p.N, t);
     if (s.seq < 0) {   // tokens of no sequence
@@ -193,13 +194,18 @@ bool wide(const void* x, int bytes) { return (reinterpret_cast<uintptr_t>(x) & (
 
 template <typename T, int W>
 int conv_w(const ConvArgs& a, ConvParams p) {
-  constexpr int E = 16 / sizeof(T);
-  const bool vec = a.D % E == 0 && wide(a.x, 16) && wide(a.out, 16) && wide(a.state_in, 16) &&
-                   wide(a.state_out, 16) && a.lay.x.batch % E == 0 && a.lay.x.token % E == 0 &&
+  constexpr int E = 4, bytes = E * sizeof(T);
+  const bool vec = a.D % E == 0 && wide(a.x, bytes) && wide(a.out, bytes) &&
+                   wide(a.state_in, bytes) && wide(a.state_out, bytes) && a.lay.x.batch % E == 0 && a.lay.x.token % E == 0 &&
                    a.lay.out.batch % E == 0 && a.lay.out.token % E == 0;
   const int per = vec ? E : 1;
   p.vecs = (a.D + per - 1) / per;
-  p.tiles = (a.N + kConvTokens - 1) / kConvTokens;
+  // long tiles read few inputs twice, short ones fill the card: as long as there are 1024
+  // threads for every SM (20011 tokens of 1000 channels: 64 tokens 34.8 us, 32 33.0)
+  p.tokens = 64;
+  while (p.tokens > 8 && (long long)a.B * ((a.N + p.tokens - 1) / p.tokens) * p.vecs < 152 * 1024)
+    p.tokens /= 2;
+  p.tiles = (a.N + p.tokens - 1) / p.tokens;
   p.units = (long long)a.B * p.tiles * p.vecs;
   const long long grid = (p.units + 127) / 128;
   if (grid > INT_MAX || (long long)a.B * p.tiles > INT_MAX) return TTT_ERR_UNSUPPORTED;

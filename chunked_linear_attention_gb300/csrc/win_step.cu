@@ -39,6 +39,111 @@ struct WinStepParams {
   window_attention_layout lay;
 };
 
+// A block's part of the work.
+template <typename T>
+struct StepRowT {
+  int b, h0, heads, split, from, to, own;
+  const T* kn;
+  const T* vn;
+  const T* ck;
+  const T* cv;
+};
+
+// False for an idle row (the same in the whole cluster), whose outputs are set to zero.
+// Otherwise the new key and value are on their way to their place.
+template <typename T>
+__device__ __forceinline__ bool step_row(const WinStepParams& p, int G, StepRowT<T>& r) {
+  r.split = blockIdx.x % p.splits;   // rank in the cluster
+  const int chunk = blockIdx.x / p.splits % p.chunks;
+  const int hk = blockIdx.x / p.splits / p.chunks;
+  r.b = blockIdx.y;
+  const int group = p.Hq / p.Hk, tid = threadIdx.x;
+  r.h0 = hk * group + chunk * G;
+  r.heads = min(G, group - chunk * G);
+  int slot = row_slot(p.slots, p.n_slots, r.b, p.status);
+  const int t = slot >= 0 ? p.positions[r.b] : 0;
+  if (t < 0) {
+    if (tid == 0) report_status(p.status, kStatusBadArg);
+    slot = -1;
+  }
+  if (slot < 0) {
+    T* out = static_cast<T*>(p.out) + r.b * p.lay.out.batch + r.h0 * p.lay.out.head;
+    if (r.split == 0)
+      for (int e = tid; e < r.heads * p.d; e += kWarps * 32)
+        out[e / p.d * p.lay.out.head + e % p.d] = from_f<T>(0.f);
+    return false;
+  }
+  const int places = p.sinks + p.window;
+  const int count = t < places ? t + 1 : places;
+  r.own = t < p.sinks ? t : p.sinks + (t - p.sinks) % p.window;
+  r.kn = static_cast<const T*>(p.k) + r.b * p.lay.k.batch + hk * p.lay.k.head;
+  r.vn = static_cast<const T*>(p.v) + r.b * p.lay.v.batch + hk * p.lay.v.head;
+  const long long at = ((long long)slot * p.Hk + hk) * places * p.d;
+  T* ck = static_cast<T*>(p.cache_k) + at;
+  T* cv = static_cast<T*>(p.cache_v) + at;
+  if (r.split == 0 && chunk == 0)
+    for (int e = tid; e < p.d; e += kWarps * 32) {
+      ck[(long long)r.own * p.d + e] = r.kn[e];
+      cv[(long long)r.own * p.d + e] = r.vn[e];
+    }
+  r.ck = ck;
+  r.cv = cv;
+  r.from = (int)((long long)count * r.split / p.splits);
+  r.to = (int)((long long)count * (r.split + 1) / p.splits);
+  return true;
+}
+
+// The warps' sums, then the cluster's blocks' (a part of the outputs each).
+template <typename T, int DP, int G>
+__device__ __forceinline__ void step_join(const WinStepParams& p, const StepRowT<T>& r,
+                                          float (&acc_s)[kWarps][G][DP], float (&m_s)[kWarps][G],
+                                          float (&l_s)[kWarps][G], float (&acc_b)[G][DP],
+                                          float (&m_b)[G], float (&l_b)[G]) {
+  const int tid = threadIdx.x;
+  T* out = static_cast<T*>(p.out) + r.b * p.lay.out.batch + r.h0 * p.lay.out.head;
+  __syncthreads();
+  for (int e = tid; e < r.heads * DP; e += kWarps * 32) {
+    const int g = e / DP, x = e % DP;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_s[w][g]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float a = 0.f, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = ex2(m_s[w][g] - base);
+      a = fmaf(f, acc_s[w][g][x], a);
+      sum = fmaf(f, l_s[w][g], sum);
+    }
+    if (p.splits == 1) {
+      if (x < p.d) out[g * p.lay.out.head + x] = from_f<T>(a / sum);
+    } else {
+      acc_b[g][x] = a;
+      if (x == 0) {
+        m_b[g] = top;
+        l_b[g] = sum;
+      }
+    }
+  }
+  if (p.splits == 1) return;
+  cg::cluster_group cl = cg::this_cluster();
+  cl.sync();
+  for (int e = r.split * kWarps * 32 + tid; e < r.heads * p.d; e += p.splits * kWarps * 32) {
+    const int g = e / p.d, x = e % p.d;
+    float top = -INFINITY;
+    for (int i = 0; i < p.splits; ++i) top = fmaxf(top, *cl.map_shared_rank(&m_b[g], i));
+    const float base = top == -INFINITY ? 0.f : top;
+    float a = 0.f, sum = 0.f;
+    for (int i = 0; i < p.splits; ++i) {
+      const float f = ex2(*cl.map_shared_rank(&m_b[g], i) - base);
+      a = fmaf(f, *cl.map_shared_rank(&acc_b[g][x], i), a);
+      sum = fmaf(f, *cl.map_shared_rank(&l_b[g], i), sum);
+    }
+    out[g * p.lay.out.head + x] = from_f<T>(a / sum);
+  }
+  cl.sync();   // no block ends while another reads from it
+}
+
 template <typename T, int DP, int G, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32) window_step_kernel(
     const __grid_constant__ WinStepParams p) {
@@ -50,41 +155,12 @@ __global__ void __launch_bounds__(kWarps * 32) window_step_kernel(
   __shared__ float acc_b[G][DP], m_b[G], l_b[G];   // of this block
   pdl_launch_dependents();
   pdl_wait();
-  const int split = blockIdx.x % p.splits;   // rank in the cluster
-  const int chunk = blockIdx.x / p.splits % p.chunks;
-  const int hk = blockIdx.x / p.splits / p.chunks, b = blockIdx.y;
-  const int group = p.Hq / p.Hk, h0 = hk * group + chunk * G;
-  const int heads = min(G, group - chunk * G);
+  StepRowT<T> row;
+  if (!step_row<T>(p, G, row)) return;
+  const int b = row.b, h0 = row.h0, heads = row.heads, own = row.own, from = row.from, to = row.to;
+  const T *kn = row.kn, *vn = row.vn, *ck = row.ck, *cv = row.cv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ld = lane % LPK, lk = lane / LPK;
-  T* out = static_cast<T*>(p.out) + b * p.lay.out.batch + h0 * p.lay.out.head;
-  int slot = row_slot(p.slots, p.n_slots, b, p.status);
-  if (slot >= 0) {
-    if (p.positions[b] < 0) {
-      if (tid == 0) report_status(p.status, kStatusBadArg);
-      slot = -1;
-    }
-  }
-  if (slot < 0) {   // the same for the whole cluster
-    if (split == 0)
-      for (int e = tid; e < heads * p.d; e += kWarps * 32)
-        out[e / p.d * p.lay.out.head + e % p.d] = from_f<T>(0.f);
-    return;
-  }
-  const int t = p.positions[b];
-  const int places = p.sinks + p.window;
-  const int count = t < places ? t + 1 : places;
-  const int own = t < p.sinks ? t : p.sinks + (t - p.sinks) % p.window;
-  const T* kn = static_cast<const T*>(p.k) + b * p.lay.k.batch + hk * p.lay.k.head;
-  const T* vn = static_cast<const T*>(p.v) + b * p.lay.v.batch + hk * p.lay.v.head;
-  const long long at = ((long long)slot * p.Hk + hk) * places * p.d;
-  T* ck = static_cast<T*>(p.cache_k) + at;
-  T* cv = static_cast<T*>(p.cache_v) + at;
-  if (split == 0 && chunk == 0)
-    for (int e = tid; e < p.d; e += kWarps * 32) {
-      ck[(long long)own * p.d + e] = kn[e];
-      cv[(long long)own * p.d + e] = vn[e];
-    }
   // this lane's 8 dimensions
   const int c = ld * 8, n = VEC ? (c < p.d ? 8 : 0) : max(0, min(8, p.d - c));
   float q[G][8], acc[G][8], m[G], l[G];
@@ -99,8 +175,6 @@ __global__ void __launch_bounds__(kWarps * 32) window_step_kernel(
                                          (h0 + g) * p.lay.q.head + c + e]) * p.scale : 0.f;
     }
   }
-  const int from = (int)((long long)count * split / p.splits);
-  const int to = (int)((long long)count * (split + 1) / p.splits);
   // 8 numbers of a row: two 16-byte pieces in fp32
   auto row8 = [&](const T* x, float (&f)[8]) {
     if constexpr (VEC && sizeof(T) == 4) {
@@ -161,7 +235,7 @@ __global__ void __launch_bounds__(kWarps * 32) window_step_kernel(
       }
     }
   }
-  // the key lanes of a warp, its warps, the cluster's blocks
+  // the key lanes of a warp
 #pragma unroll
   for (int g = 0; g < G; ++g) {
 #pragma unroll
@@ -185,58 +259,167 @@ __global__ void __launch_bounds__(kWarps * 32) window_step_kernel(
       }
     }
   }
-  __syncthreads();
-  for (int e = tid; e < G * DP; e += kWarps * 32) {
-    const int g = e / DP, x = e % DP;
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_s[w][g]);
-    const float base = top == -INFINITY ? 0.f : top;
-    float a = 0.f, sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = ex2(m_s[w][g] - base);
-      a = fmaf(f, acc_s[w][g][x], a);
-      sum = fmaf(f, l_s[w][g], sum);
-    }
-    if (p.splits == 1) {
-      if (g < heads && x < p.d) out[g * p.lay.out.head + x] = from_f<T>(a / sum);
-    } else {
-      acc_b[g][x] = a;
-      if (x == 0) {
-        m_b[g] = top;
-        l_b[g] = sum;
-      }
-    }
-  }
-  if (p.splits == 1) return;
-  cg::cluster_group cl = cg::this_cluster();
-  cl.sync();
-  // a part of the outputs each
-  for (int e = split * kWarps * 32 + tid; e < heads * p.d; e += p.splits * kWarps * 32) {
-    const int g = e / p.d, x = e % p.d;
-    float top = -INFINITY;
-    for (int r = 0; r < p.splits; ++r) top = fmaxf(top, *cl.map_shared_rank(&m_b[g], r));
-    const float base = top == -INFINITY ? 0.f : top;
-    float a = 0.f, sum = 0.f;
-    for (int r = 0; r < p.splits; ++r) {
-      const float f = ex2(*cl.map_shared_rank(&m_b[g], r) - base);
-      a = fmaf(f, *cl.map_shared_rank(&acc_b[g][x], r), a);
-      sum = fmaf(f, *cl.map_shared_rank(&l_b[g], r), sum);
-    }
-    out[g * p.lay.out.head + x] = from_f<T>(a / sum);
-  }
-  cl.sync();   // no block ends while another reads from it
+  step_join<T, DP, G>(p, row, acc_s, m_s, l_s, acc_b, m_b, l_b);
 }
 
-template <typename T, int DP, int G>
-int launch_win_step(const WindowStepArgs& a, WinStepParams p) {
-  constexpr int per = 16 / sizeof(T);
-  auto ok = [&](const void* x, const delta_rule_stride& s) {
-    return (reinterpret_cast<uintptr_t>(x) & 15) == 0 && s.batch % per == 0 && s.head % per == 0;
-  };
-  // rows of 8 numbers, 16 bytes at a time: the caches are dense and 16-byte aligned
-  const bool vec = a.d % 8 == 0 && ok(a.k, a.lay.k) && ok(a.v, a.lay.v);
+// ------------------------------------------------------------ bf16 on the tensor cores
+// With several query heads a key head the products above take longer than the keys and
+// values (8 FMA and their reduction for each number read): for bf16 they go through the
+// warp-wide matrix instruction, 16 keys at a time.
+//   S [heads x keys] = Q K^T: rows are the heads (8 at most; the other 8 rows are idle).  A
+//       lane reads 16 bytes of a key and uses them as the two operands' halves of two
+//       products: the dimensions of a product are those that its lanes have read.
+//   O [heads x d] = P V: the weights as a pair hi + lo of bf16 numbers (off by 2^-17), hi in
+//       rows 0 - 7 and lo in rows 8 - 15, so that one product takes both.  A lane reads 16
+//       bytes of four values' rows and pairs those of neighbouring keys.
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kWarps * 32, 2) window_step_mma_kernel(
+    const __grid_constant__ WinStepParams p) {
+  using T = __nv_bfloat16;
+  constexpr int G = 8, H = DP / 64;   // heads; halves of 64 dimensions
+  __shared__ float acc_s[kWarps][G][DP];
+  __shared__ float m_s[kWarps][G], l_s[kWarps][G];
+  __shared__ float acc_b[G][DP], m_b[G], l_b[G];   // of this block
+  pdl_launch_dependents();
+  pdl_wait();
+  StepRowT<T> r;
+  if (!step_row<T>(p, G, r)) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
+  const T* ck = r.ck;
+  const T* cv = r.cv;
+  // this lane's dimensions of head g: 32 i + 8 q4 ..
+  uint4 q[2 * H];
+#pragma unroll
+  for (int i = 0; i < 2 * H; ++i) {
+    q[i] = make_uint4(0u, 0u, 0u, 0u);
+    const int c = 32 * i + 8 * q4;
+    if (g < r.heads && c < p.d) {
+      const T* src = static_cast<const T*>(p.q) + r.b * p.lay.q.batch + (r.h0 + g) * p.lay.q.head + c;
+      uint16_t w[8];   // rows of q at any address
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = reinterpret_cast<const uint16_t*>(src)[e];
+      q[i] = make_uint4(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16,
+                        w[4] | (uint32_t)w[5] << 16, w[6] | (uint32_t)w[7] << 16);
+    }
+  }
+  float acc[H][8][4], m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int y = 0; y < H; ++y)
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[y][n][e] = 0.f;
+
+  for (int j0 = r.from + warp * 16; j0 < r.to; j0 += kWarps * 16) {
+    uint4 k[2][2 * H], v[H][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {   // key j0 + 8 t + g
+      const int j = j0 + 8 * t + g;
+      const T* row = j == r.own ? r.kn : ck + (long long)(j < r.to ? j : r.from) * p.d;
+#pragma unroll
+      for (int i = 0; i < 2 * H; ++i) {
+        const int c = 32 * i + 8 * q4;
+        k[t][i] = c < p.d ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {   // keys j0 + 2 q4, + 1, + 8, + 9; zero behind the last
+      const int j = j0 + 2 * q4 + (t & 1) + 4 * (t & 2);
+      const T* row = j == r.own ? r.vn : cv + (long long)j * p.d;
+#pragma unroll
+      for (int y = 0; y < H; ++y) {
+        const int c = 64 * y + 8 * g;
+        v[y][t] = j < r.to && c < p.d ? *reinterpret_cast<const uint4*>(row + c)
+                                      : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    float s[2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2 * H; ++i) {
+        mma16816(s[t], q[i].x, 0u, q[i].y, 0u, k[t][i].x, k[t][i].y);
+        mma16816(s[t], q[i].z, 0u, q[i].w, 0u, k[t][i].z, k[t][i].w);
+      }
+    }
+    // head g, keys j0 + 2 q4, + 1, + 8, + 9
+    float x[4];
+    float top = m;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = j0 + 2 * q4 + (e & 1) + 4 * (e & 2);
+      x[e] = j < r.to ? s[e >> 1][e & 1] * p.scale : -INFINITY;
+      top = fmaxf(top, x[e]);
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const float base = top == -INFINITY ? 0.f : top;
+    if (__any_sync(0xffffffffu, top > m)) {
+      const float f = ex2(m - base);
+      l *= f;
+#pragma unroll
+      for (int y = 0; y < H; ++y)
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[y][n][e] *= f;
+    }
+    m = top;
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = ex2(x[e] - base);
+      l += x[e];
+    }
+    split2(pack2(x[0], x[1]), hi[0], lo[0]);
+    split2(pack2(x[2], x[3]), hi[1], lo[1]);
+#pragma unroll
+    for (int y = 0; y < H; ++y)
+#pragma unroll
+      for (int n = 0; n < 8; n += 2) {
+        // dimensions 64 y + 8 g + n, + 1 of the four keys
+        auto word = [&](const uint4& w) { return n < 2 ? w.x : n < 4 ? w.y : n < 6 ? w.z : w.w; };
+        const uint32_t a = word(v[y][0]), b = word(v[y][1]), c = word(v[y][2]), d = word(v[y][3]);
+        mma16816(acc[y][n], hi[0], lo[0], hi[1], lo[1], __byte_perm(a, b, 0x5410),
+                 __byte_perm(c, d, 0x5410));
+        mma16816(acc[y][n + 1], hi[0], lo[0], hi[1], lo[1], __byte_perm(a, b, 0x7632),
+                 __byte_perm(c, d, 0x7632));
+      }
+  }
+  l += __shfl_xor_sync(0xffffffffu, l, 1);
+  l += __shfl_xor_sync(0xffffffffu, l, 2);
+  // the sums of hi and of lo; column 2 q4 + e of the products with n has dimension
+  // 64 y + 8 (2 q4 + e) + n
+#pragma unroll
+  for (int y = 0; y < H; ++y)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int n = 0; n < 8; n += 4)
+        *reinterpret_cast<float4*>(&acc_s[warp][g][64 * y + 8 * (2 * q4 + e) + n]) = make_float4(
+            acc[y][n][e] + acc[y][n][e + 2], acc[y][n + 1][e] + acc[y][n + 1][e + 2],
+            acc[y][n + 2][e] + acc[y][n + 2][e + 2], acc[y][n + 3][e] + acc[y][n + 3][e + 2]);
+  if (q4 == 0) {
+    m_s[warp][g] = m;
+    l_s[warp][g] = l;
+  }
+  step_join<T, DP, G>(p, r, acc_s, m_s, l_s, acc_b, m_b, l_b);
+}
+
+// G: query heads that a block takes together.
+template <typename T>
+int win_step_go(const WindowStepArgs& a, WinStepParams p, int G, void (*kern)(WinStepParams)) {
   p.chunks = (a.Hq / a.Hk + G - 1) / G;
   // two blocks a SM, and no block with less than 128 places
   const long long ctas = (long long)a.B * a.Hk * p.chunks, places = (long long)a.window + a.sinks;
@@ -246,10 +429,24 @@ int launch_win_step(const WindowStepArgs& a, WinStepParams p) {
   const double pairs = (double)a.B * places;
   ProfScope ps(PT_WIN_STEP, a.stream, 4.0 * pairs * a.Hq * a.d, 2.0 * pairs * a.Hk * a.d * sizeof(T));
   const dim3 grid((unsigned)(a.Hk * p.chunks * p.splits), a.B);
-  const cudaError_t e =
-      vec ? launch_grid(window_step_kernel<T, DP, G, true>, grid, kWarps * 32, 0, a.stream, p, p.splits)
-          : launch_grid(window_step_kernel<T, DP, G, false>, grid, kWarps * 32, 0, a.stream, p, p.splits);
-  return e == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+  return launch_grid(kern, grid, kWarps * 32, 0, a.stream, p, p.splits) == cudaSuccess ? TTT_OK
+                                                                                       : TTT_ERR_CUDA;
+}
+
+// Rows of 8 numbers, 16 bytes at a time: the caches are dense and 16-byte aligned.
+template <typename T>
+bool rows_of_8(const WindowStepArgs& a) {
+  constexpr int per = 16 / sizeof(T);
+  auto ok = [&](const void* x, const delta_rule_stride& s) {
+    return (reinterpret_cast<uintptr_t>(x) & 15) == 0 && s.batch % per == 0 && s.head % per == 0;
+  };
+  return a.d % 8 == 0 && ok(a.k, a.lay.k) && ok(a.v, a.lay.v);
+}
+
+template <typename T, int DP, int G>
+int launch_win_step(const WindowStepArgs& a, const WinStepParams& p) {
+  return win_step_go<T>(a, p, G, rows_of_8<T>(a) ? window_step_kernel<T, DP, G, true>
+                                                 : window_step_kernel<T, DP, G, false>);
 }
 
 template <typename T, int DP>
@@ -262,6 +459,10 @@ int step_g(const WindowStepArgs& a, const WinStepParams& p) {
 
 template <typename T>
 int step_d(const WindowStepArgs& a, const WinStepParams& p) {
+  if constexpr (sizeof(T) == 2) {
+    if (a.d <= 128 && rows_of_8<T>(a))
+      return win_step_go<T>(a, p, 8, a.d <= 64 ? window_step_mma_kernel<64> : window_step_mma_kernel<128>);
+  }
   if (a.d <= 64) return step_g<T, 64>(a, p);
   if (a.d <= 128) return step_g<T, 128>(a, p);
   return step_g<T, 256>(a, p);
