@@ -621,72 +621,115 @@ struct ScanStepParams {
   const int* slots;
   void* out;
   int* status;
-  int n_slots, D, S, G, softplus;
+  int n_slots, B, D, S, G, softplus;
   selective_scan_layout lay;
 };
 
-// Four numbers of a state a thread, L lanes a channel; bound by HBM, the states' bytes
-// twice.
-template <typename T, int L, bool VEC>
+// Four numbers of a state a thread, L lanes a channel, R rows of the batch; bound by HBM,
+// the states' bytes twice.  With four rows a thread has 64 bytes on their way, and A and the
+// check of the slots serve all four: 250 rows of 4096 x 16 take 34 us, one row a thread 44;
+// up to 32 rows a block, two at a time with the next two on their way, 55 (fewer blocks).
+template <typename T, int L, int R, bool VEC>
 __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ ScanStepParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int b = blockIdx.y, l = threadIdx.x % L;
+  __shared__ unsigned taken;
+  const int b0 = blockIdx.y * R, l = threadIdx.x % L;
   const int c = blockIdx.x * (128 / L) + threadIdx.x / L;
-  const int slot = row_slot(p.slots, p.n_slots, b, p.status);
   const bool in = c < p.D;
-  T* out = static_cast<T*>(p.out) + b * p.lay.out.batch + c;
-  if (slot < 0) {
-    if (in && l == 0) *out = from_f<T>(0.f);
-    return;
+  int slot[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    slot[i] = b0 + i < p.B ? (p.slots ? p.slots[b0 + i] : b0 + i) : -1;
+  if (p.slots) {   // slots outside the pool and ones that an earlier row uses
+    if (threadIdx.x == 0) taken = 0u;
+    __syncthreads();
+    unsigned bad = 0u;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (slot[i] >= p.n_slots) bad |= 1u << i;
+    for (int e = threadIdx.x; e < min(b0 + R - 1, p.B); e += 128) {
+      const int other = p.slots[e];
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (slot[i] >= 0 && other == slot[i] && e < b0 + i) bad |= 1u << i;
+    }
+    if (bad) atomicOr(&taken, bad);
+    __syncthreads();
+    if (taken && threadIdx.x == 0) report_status(p.status, kStatusBadArg);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if ((taken >> i) & 1) slot[i] = -1;
   }
   const int g = in ? c / (p.D / p.G) : 0, s0 = l * 4;
-  const T* Bm = static_cast<const T*>(p.Bm) + b * p.lay.B.batch + (long long)g * p.S;
-  const T* Cm = static_cast<const T*>(p.Cm) + b * p.lay.C.batch + (long long)g * p.S;
-  float* st = p.state + ((long long)slot * p.D + c) * p.S + s0;
-  const float* A = p.A + (long long)c * p.S + s0;
-  float h[4], a[4], acc = 0.f;
-  const int n = in ? min(4, p.S - s0) : 0;
-  load_row<float, 4, VEC>(st, n, h);
-  load_row<float, 4, VEC>(A, n, a);
-  float xv = 0.f, r = 0.f, zv = 0.f;
-  if (in) {
-    xv = to_f<T>(static_cast<const T*>(p.x)[b * p.lay.x.batch + c]);
-    r = to_f<T>(static_cast<const T*>(p.dt)[b * p.lay.dt.batch + c]);
-    if (p.dt_bias) r += p.dt_bias[c];
-    if (p.z) zv = to_f<T>(static_cast<const T*>(p.z)[b * p.lay.z.batch + c]);
-  }
-  if (p.softplus) {
-    float none = 0.f;
-    softplus2(r, none);
-  }
+  const int n = in ? max(0, min(4, p.S - s0)) : 0;
+  float h[R][4], a[4];
+  float xv[R], r[R], zv[R];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float Bv = i < n ? to_f<T>(Bm[s0 + i]) : 0.f, Cv = i < n ? to_f<T>(Cm[s0 + i]) : 0.f;
-    h[i] = fmaf(ex2(r * (a[i] * kLog2e)), h[i], r * xv * Bv);
-    acc = fmaf(Cv, h[i], acc);
+  for (int i = 0; i < R; ++i) {
+    const int b = b0 + i;
+    xv[i] = r[i] = zv[i] = 0.f;
+    if (slot[i] < 0) continue;
+    load_row<float, 4, VEC>(p.state + ((long long)slot[i] * p.D + c) * p.S + s0, n, h[i]);
+    if (in) {
+      xv[i] = to_f<T>(static_cast<const T*>(p.x)[b * p.lay.x.batch + c]);
+      r[i] = to_f<T>(static_cast<const T*>(p.dt)[b * p.lay.dt.batch + c]);
+      if (p.z) zv[i] = to_f<T>(static_cast<const T*>(p.z)[b * p.lay.z.batch + c]);
+    }
   }
-  if (n > 0) store_row<float, 4, VEC>(st, n, h);
-  acc = sum_over<L>(acc);
-  if (in && l == 0) {
-    if (p.Dx) acc = fmaf(p.Dx[c], xv, acc);
-    if (p.z) acc *= silu_f(zv);
-    *out = from_f<T>(acc);
+  load_row<float, 4, VEC>(p.A + (long long)c * p.S + s0, n, a);
+  const float bias = in && p.dt_bias ? p.dt_bias[c] : 0.f, dx = in && p.Dx ? p.Dx[c] : 0.f;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int b = b0 + i;
+    if (b >= p.B) break;
+    T* out = static_cast<T*>(p.out) + b * p.lay.out.batch + c;
+    if (slot[i] < 0) {
+      if (in && l == 0) *out = from_f<T>(0.f);
+      continue;
+    }
+    const T* Bm = static_cast<const T*>(p.Bm) + b * p.lay.B.batch + (long long)g * p.S;
+    const T* Cm = static_cast<const T*>(p.Cm) + b * p.lay.C.batch + (long long)g * p.S;
+    float rr = r[i] + bias, acc = 0.f, Bv[4], Cv[4];
+    load_row<T, 4, VEC>(Bm + s0, n, Bv);
+    load_row<T, 4, VEC>(Cm + s0, n, Cv);
+    if (p.softplus) {
+      float none = 0.f;
+      softplus2(rr, none);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      h[i][e] = fmaf(ex2(rr * (a[e] * kLog2e)), h[i][e], rr * xv[i] * Bv[e]);
+      acc = fmaf(Cv[e], h[i][e], acc);
+    }
+    if (n > 0)
+      store_row<float, 4, VEC>(p.state + ((long long)slot[i] * p.D + c) * p.S + s0, n, h[i]);
+    acc = sum_over<L>(acc);
+    if (in && l == 0) {
+      acc = fmaf(dx, xv[i], acc);
+      if (p.z) acc *= silu_f(zv[i]);
+      *out = from_f<T>(acc);
+    }
   }
 }
 
 template <typename T, int L>
 int launch_scan_step(const ScanStepArgs& a, const ScanStepParams& p) {
   const int per = 128 / L;
-  const dim3 grid((a.D + per - 1) / per, a.B);
   const double n = (double)a.B * a.D * a.S;
   ProfScope ps(PT_SCAN_STEP, a.stream, 6.0 * n, 8.0 * n);
-  // the lanes' four numbers lie in one 16-byte piece where S is 4 L
-  const bool vec = a.S == 4 * L && (reinterpret_cast<uintptr_t>(a.state) & 15) == 0 &&
-                   (reinterpret_cast<uintptr_t>(a.A) & 15) == 0 && a.D % per == 0;
-  const cudaError_t e = vec ? launch_grid(scan_step_kernel<T, L, true>, grid, 128, 0, a.stream, p)
-                            : launch_grid(scan_step_kernel<T, L, false>, grid, 128, 0, a.stream, p);
-  return e == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+  // the lanes' four numbers lie in one 16-byte piece where S is 4 L; those of B and C too
+  auto ok = [](const void* x, unsigned bytes) { return (reinterpret_cast<uintptr_t>(x) & (bytes - 1)) == 0; };
+  const bool vec = a.S == 4 * L && a.D % per == 0 && ok(a.state, 16) && ok(a.A, 16) &&
+                   ok(a.Bm, 4 * sizeof(T)) && ok(a.Cm, 4 * sizeof(T)) && a.lay.B.batch % 4 == 0 &&
+                   a.lay.C.batch % 4 == 0;
+  // four rows a thread where that leaves every SM two blocks
+  const int R = (long long)((a.D + per - 1) / per) * ((a.B + 3) / 4) >= 2 * kScanSms ? 4 : 1;
+  const dim3 grid((a.D + per - 1) / per, (a.B + R - 1) / R);
+  void (*kern)(ScanStepParams) =
+      R == 4 ? (vec ? scan_step_kernel<T, L, 4, true> : scan_step_kernel<T, L, 4, false>)
+             : (vec ? scan_step_kernel<T, L, 1, true> : scan_step_kernel<T, L, 1, false>);
+  return launch_grid(kern, grid, 128, 0, a.stream, p) == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 
 template <typename T>
@@ -740,7 +783,7 @@ int selective_scan_step_launch(const ScanStepArgs& a) {
   p.slots = a.slots;
   p.out = a.out;
   p.status = a.status;
-  p.n_slots = a.n_slots; p.D = a.D; p.S = a.S; p.G = a.G;
+  p.n_slots = a.n_slots; p.B = a.B; p.D = a.D; p.S = a.S; p.G = a.G;
   p.softplus = a.softplus;
   p.lay = a.lay;
   return a.bf16 ? scan_step_t<__nv_bfloat16>(a, p) : scan_step_t<float>(a, p);
