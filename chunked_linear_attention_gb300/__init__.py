@@ -9,6 +9,7 @@ shared library is missing or cannot load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 from typing import Optional, Sequence
@@ -155,6 +156,10 @@ def _declare(lib):
     lib.short_conv_forward.argtypes = [vp] * 5 + [i] * 7 + [cp, vp, vp, vp]
     lib.short_conv_step.restype = i
     lib.short_conv_step.argtypes = [vp] * 5 + [i] * 6 + [cp, vp, vp]
+    for name in ("window_forward", "window_step", "scan_forward", "scan_step", "conv_forward",
+                 "conv_step"):   # the same calls with their arguments as one packed record
+        call = getattr(lib, "ttt_binding_" + name)
+        call.restype, call.argtypes = i, [cp]
     lib.ttt_selftest_withhold_delta.restype = None
     lib.ttt_selftest_withhold_delta.argtypes = [i]
     lib.ttt_selftest_withhold_release.restype = None
@@ -689,38 +694,54 @@ def block_norm_forward(y, w: Optional[torch.Tensor] = None,
 
 
 # ---------------------------------------------------------------- fixed-state mixers
-_pack_window = struct.Struct("12q").pack
-_pack_scan = struct.Struct("12q").pack
-_pack_conv = struct.Struct("4q").pack
+# Made once per layer and decoded token too: arguments travel as one packed record.
+_pack_window = struct.Struct("@10P12q10if").pack
+_pack_scan = struct.Struct("@13PNP12q8i").pack
+_pack_conv = struct.Struct("@8P4q7i").pack
+_I32 = torch.int32
+
+
+def _elsewhere_needed(t, stream):
+    """Whether the call has to be made under another current device or stream."""
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the CUDA path must be on a CUDA device")
+    return stream is not None or t.get_device() != _current_device()
+
+
+def _addr(t, shape, dtype, dev, what):
+    """Address of a contiguous tensor of this shape, or 0 for None."""
+    if t is None:
+        return 0
+    if t.shape != shape or t.dtype is not dtype or t.device != dev:
+        _want(t, shape, dtype, dev, what)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
 
 
 def _starts(seq_starts, B, dev):
     """(address, number of sequences) of packed sequences' bounds."""
     if seq_starts is None:
-        return None, B
+        return 0, B
     if B != 1:
         raise ValueError("seq_starts needs B = 1")
     n_seq = seq_starts.numel() - 1
-    if n_seq < 1 or not seq_starts.is_contiguous():
+    if n_seq < 1:
         raise ValueError("seq_starts must be a contiguous vector of n_seq + 1 entries")
-    _want(seq_starts, (n_seq + 1,), torch.int32, dev, "seq_starts")
-    return seq_starts.data_ptr(), n_seq
+    return _addr(seq_starts, (n_seq + 1,), _I32, dev, "seq_starts"), n_seq
 
 
-def _gpu(t):
-    if t.device.type != "cuda":
-        raise ValueError("tensors passed to the CUDA path must be on a CUDA device")
-    return t.device
-
-
-def _places(cache_k, cache_v, Hk, places, d, dt, dev):
-    """Number of slots of a pair of window-attention caches."""
+def _caches(cache_k, cache_v, Hk, places, d, dt, dev):
+    """(number of slots, addresses) of a pair of window-attention caches."""
+    if cache_k is None or cache_v is None:
+        if cache_k is not cache_v:
+            raise ValueError("cache_k and cache_v are given together")
+        return 0, 0, 0
     if cache_k.dim() != 4:
         raise ValueError("cache_k must have four dimensions")
     shape = (cache_k.shape[0], Hk, places, d)
-    _dense(cache_k, shape, dt, dev, "cache_k")
-    _dense(cache_v, shape, dt, dev, "cache_v")
-    return shape[0]
+    return (shape[0], _addr(cache_k, shape, dt, dev, "cache_k"),
+            _addr(cache_v, shape, dt, dev, "cache_v"))
 
 
 def window_attention_forward(q, k, v, window: int, sinks: int = 0,
@@ -744,35 +765,30 @@ def window_attention_forward(q, k, v, window: int, sinks: int = 0,
     the token axis (B = 1).  scale: d ** -0.5 when None.  Without ``out``, the
     outputs are stored in q's order of dimensions.  Returns out [B, Hq, N, d].
     """
-    dev = _gpu(q)
-    if stream is not None or dev.index != _current_device():
-        with _elsewhere(dev, stream):
+    if _elsewhere_needed(q, stream):
+        with _elsewhere(q.device, stream):
             return window_attention_forward(q, k, v, window, sinks, scale, cache_k, cache_v, slots,
                                             past, seq_starts, out)
+    dev, dt, io = q.device, q.dtype, _io_dtype(q)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q and k must have four dimensions")
     B, Hq, N, d = q.shape
-    Hk, dt, io = k.shape[1], q.dtype, _io_dtype(q)
-    _want(k, (B, Hk, N, d), dt, dev, "k")
-    _want(v, (B, Hk, N, d), dt, dev, "v")
+    Hk = k.shape[1]
+    shape = (B, Hk, N, d)
+    _want(k, shape, dt, dev, "k")
+    _want(v, shape, dt, dev, "v")
     starts, n_seq = _starts(seq_starts, B, dev)
-    n_slots = 0
-    if cache_k is not None and cache_v is not None:
-        n_slots = _places(cache_k, cache_v, Hk, sinks + window, d, dt, dev)
+    n_slots, ck, cv = _caches(cache_k, cache_v, Hk, sinks + window, d, dt, dev)
     if out is None:
         out = torch.empty_like(q)
     else:
         _want(out, (B, Hq, N, d), dt, dev, "out")
-    rc = (_lib or library()).window_attention_forward(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(),
-        None if cache_k is None else cache_k.data_ptr(),
-        None if cache_v is None else cache_v.data_ptr(),
-        _dense(slots, (n_seq,), torch.int32, dev, "slots"), n_slots,
-        _dense(past, (n_seq,), torch.int32, dev, "past"), starts, n_seq, B, Hq, Hk, N, d, window,
-        sinks, io, d ** -0.5 if scale is None else scale,
-        _pack_window(*_strides(q, "q")[:3], *_strides(k, "k")[:3], *_strides(v, "v")[:3],
-                     *_strides(out, "out")[:3]),
-        out.data_ptr(), _raw_stream(dev.index))
+    rc = (_lib or library()).ttt_binding_window_forward(_pack_window(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), ck, cv,
+        _addr(slots, (n_seq,), _I32, dev, "slots"), _addr(past, (n_seq,), _I32, dev, "past"), starts,
+        out.data_ptr(), _raw_stream(dev.index), *_strides(q, "q")[:3], *_strides(k, "k")[:3],
+        *_strides(v, "v")[:3], *_strides(out, "out")[:3], n_slots, n_seq, B, Hq, Hk, N, d, window,
+        sinks, io, d ** -0.5 if scale is None else scale))
     if rc:
         _check(rc, "window_attention_forward")
     return out
@@ -790,46 +806,48 @@ def window_attention_step(q, k, v, cache_k, cache_v, positions, window: int, sin
     int32 [B], the number of tokens before; slots int32 [B] (negative: an idle
     row) or None.  Returns out [B, Hq, d].
     """
-    dev = _gpu(q)
-    if stream is not None or dev.index != _current_device():
-        with _elsewhere(dev, stream):
+    if _elsewhere_needed(q, stream):
+        with _elsewhere(q.device, stream):
             return window_attention_step(q, k, v, cache_k, cache_v, positions, window, sinks, slots,
                                          scale, out)
+    dev, dt, io = q.device, q.dtype, _io_dtype(q)
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k must have three dimensions")
     B, Hq, d = q.shape
-    Hk, dt, io = k.shape[1], q.dtype, _io_dtype(q)
-    _want(k, (B, Hk, d), dt, dev, "k")
-    _want(v, (B, Hk, d), dt, dev, "v")
-    n_slots = _places(cache_k, cache_v, Hk, sinks + window, d, dt, dev)
+    Hk = k.shape[1]
+    shape = (B, Hk, d)
+    _want(k, shape, dt, dev, "k")
+    _want(v, shape, dt, dev, "v")
+    n_slots, ck, cv = _caches(cache_k, cache_v, Hk, sinks + window, d, dt, dev)
     if out is None:
         out = torch.empty_like(q)
     else:
         _want(out, (B, Hq, d), dt, dev, "out")
-    rc = (_lib or library()).window_attention_step(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), cache_k.data_ptr(), cache_v.data_ptr(),
-        _dense(positions, (B,), torch.int32, dev, "positions"),
-        _dense(slots, (B,), torch.int32, dev, "slots"), n_slots, B, Hq, Hk, d, window, sinks, io,
-        d ** -0.5 if scale is None else scale,
-        _pack_window(*_strides(q, "q")[:2], 0, *_strides(k, "k")[:2], 0, *_strides(v, "v")[:2], 0,
-                     *_strides(out, "out")[:2], 0),
-        out.data_ptr(), _raw_stream(dev.index))
+    rc = (_lib or library()).ttt_binding_window_step(_pack_window(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), ck, cv, _addr(slots, (B,), _I32, dev, "slots"),
+        _addr(positions, (B,), _I32, dev, "positions"), 0, out.data_ptr(), _raw_stream(dev.index),
+        *_strides(q, "q")[:2], 0, *_strides(k, "k")[:2], 0, *_strides(v, "v")[:2], 0,
+        *_strides(out, "out")[:2], 0, n_slots, B, B, Hq, Hk, 1, d, window, sinks, io,
+        d ** -0.5 if scale is None else scale))
     if rc:
         _check(rc, "window_attention_step")
     return out
 
 
-def _groups(t, rows, G, S, dtype, dev, what):
+def _groups(t, shape, dtype, dev, what):
     """Strides of a [rows.., G, S] tensor whose tokens are contiguous."""
-    _want(t, (*rows, G, S), dtype, dev, what)
+    _want(t, shape, dtype, dev, what)
     st = t.stride()
-    if (S > 1 and st[-1] != 1) or (G > 1 and st[-2] != S):
+    if (shape[-1] > 1 and st[-1] != 1) or (shape[-2] > 1 and st[-2] != shape[-1]):
         raise ValueError(f"{what} must be contiguous in its last two dimensions")
     return st[:-2]
 
 
 def selective_scan_workspace_size(B, N, D, S, G, n_seq, io_dtype) -> int:
     return library().selective_scan_workspace_size(B, N, D, S, G, n_seq, io_dtype)
+
+
+_scan_need = functools.lru_cache(maxsize=4096)(selective_scan_workspace_size)   # by sizes alone
 
 
 def selective_scan_forward(x, dt, A, B, C, D: Optional[torch.Tensor] = None,
@@ -850,43 +868,43 @@ def selective_scan_forward(x, dt, A, B, C, D: Optional[torch.Tensor] = None,
     for sequences packed along the token axis (batch of 1).  Returns (out
     [batch, N, channels], state_out [n_seq or batch, channels, S]).
     """
-    dev = _gpu(x)
-    if stream is not None or dev.index != _current_device():
-        with _elsewhere(dev, stream):
+    if _elsewhere_needed(x, stream):
+        with _elsewhere(x.device, stream):
             return selective_scan_forward(x, dt, A, B, C, D, dt_bias, z, dt_softplus, state,
                                           seq_starts, out, state_out, workspace)
     if x.dim() != 3 or B.dim() != 4:
         raise ValueError("x must have three dimensions, B four")
-    nb, N, ch = x.shape
-    G, S = B.shape[2:]
-    io, f32, rows = _io_dtype(x), _F32, (nb, N)
-    _want(dt, x.shape, x.dtype, dev, "dt")
+    dev, ty, io, f32, shape = x.device, x.dtype, _io_dtype(x), _F32, x.shape
+    nb, N, ch = shape
+    bc = B.shape
+    G, S = bc[2:]
+    _want(dt, shape, ty, dev, "dt")
     if z is not None:
-        _want(z, x.shape, x.dtype, dev, "z")
-    sb, sc = (_groups(t, rows, G, S, x.dtype, dev, w) for t, w in ((B, "B"), (C, "C")))
+        _want(z, shape, ty, dev, "z")
+    if bc[:2] != (nb, N):
+        raise ValueError(f"B must hold {nb} x {N} tokens, got shape {tuple(bc)}")
+    sb, sc = _groups(B, bc, ty, dev, "B"), _groups(C, bc, ty, dev, "C")
     starts, n_seq = _starts(seq_starts, nb, dev)
-    lib = _lib or library()
+    states = (n_seq, ch, S)
     if out is None:
-        out = torch.empty(x.shape, device=dev, dtype=x.dtype)
+        out = torch.empty_like(x)   # x's order of dimensions
     else:
-        _want(out, x.shape, x.dtype, dev, "out")
+        _want(out, shape, ty, dev, "out")
     if state_out is None:
-        state_out = torch.empty((n_seq, ch, S), device=dev, dtype=f32)
+        state_out = A.new_empty(states)
     if workspace is None:
-        need = lib.selective_scan_workspace_size(nb, N, ch, S, G, n_seq, io)
-        workspace = torch.empty(need or 256, device=dev, dtype=torch.uint8)
+        workspace = torch.empty(max(_scan_need(nb, N, ch, S, G, n_seq, io), 256), device=dev,
+                                dtype=torch.uint8)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {dev}")
-    rc = lib.selective_scan_forward(
-        x.data_ptr(), dt.data_ptr(), _dense(A, (ch, S), f32, dev, "A"), B.data_ptr(), C.data_ptr(),
-        _dense(D, (ch,), f32, dev, "D"), _dense(dt_bias, (ch,), f32, dev, "dt_bias"),
-        None if z is None else z.data_ptr(), _dense(state, (n_seq, ch, S), f32, dev, "state"),
-        starts, n_seq, nb, N, ch, S, G, io, int(bool(dt_softplus)),
-        _pack_scan(*_strides(x, "x")[:2], *_strides(dt, "dt")[:2],
-                   *((0, 0) if z is None else _strides(z, "z")[:2]), *sb, *sc,
-                   *_strides(out, "out")[:2]),
-        out.data_ptr(), _dense(state_out, (n_seq, ch, S), f32, dev, "state_out"),
-        workspace.data_ptr(), workspace.nbytes, _raw_stream(dev.index))
+    rc = (_lib or library()).ttt_binding_scan_forward(_pack_scan(
+        x.data_ptr(), dt.data_ptr(), _addr(A, (ch, S), f32, dev, "A"), B.data_ptr(), C.data_ptr(),
+        _addr(D, (ch,), f32, dev, "D"), _addr(dt_bias, (ch,), f32, dev, "dt_bias"),
+        0 if z is None else z.data_ptr(), _addr(state, states, f32, dev, "state"), starts,
+        out.data_ptr(), _addr(state_out, states, f32, dev, "state_out"), workspace.data_ptr(),
+        workspace.nbytes, _raw_stream(dev.index), *_strides(x, "x")[:2], *_strides(dt, "dt")[:2],
+        *((0, 0) if z is None else _strides(z, "z")[:2]), *sb, *sc, *_strides(out, "out")[:2], n_seq,
+        nb, N, ch, S, G, io, 1 if dt_softplus else 0))
     if rc:
         _check(rc, "selective_scan_forward")
     return out, state_out
@@ -905,34 +923,34 @@ def selective_scan_step(x, dt, A, B, C, state, D: Optional[torch.Tensor] = None,
     fp32; slots int32 [rows] (negative: an idle row) or None.  The others as for
     ``selective_scan_forward``.  Returns out [rows, channels].
     """
-    dev = _gpu(x)
-    if stream is not None or dev.index != _current_device():
-        with _elsewhere(dev, stream):
+    if _elsewhere_needed(x, stream):
+        with _elsewhere(x.device, stream):
             return selective_scan_step(x, dt, A, B, C, state, D, dt_bias, z, dt_softplus, slots, out)
     if x.dim() != 2 or B.dim() != 3 or state.dim() != 3:
         raise ValueError("x must have two dimensions, B and state three")
-    nb, ch = x.shape
-    G, S = B.shape[1:]
-    io, f32 = _io_dtype(x), _F32
-    _want(dt, x.shape, x.dtype, dev, "dt")
+    dev, ty, io, f32, shape = x.device, x.dtype, _io_dtype(x), _F32, x.shape
+    nb, ch = shape
+    bc = B.shape
+    G, S = bc[1:]
+    _want(dt, shape, ty, dev, "dt")
     if z is not None:
-        _want(z, x.shape, x.dtype, dev, "z")
-    (sb,), (sc,) = (_groups(t, (nb,), G, S, x.dtype, dev, w) for t, w in ((B, "B"), (C, "C")))
+        _want(z, shape, ty, dev, "z")
+    if bc[0] != nb:
+        raise ValueError(f"B must hold {nb} rows, got shape {tuple(bc)}")
+    (sb,), (sc,) = _groups(B, bc, ty, dev, "B"), _groups(C, bc, ty, dev, "C")
     n_slots = state.shape[0]
     if out is None:
-        out = torch.empty(x.shape, device=dev, dtype=x.dtype)
+        out = torch.empty_like(x)
     else:
-        _want(out, x.shape, x.dtype, dev, "out")
-    rc = (_lib or library()).selective_scan_step(
-        x.data_ptr(), dt.data_ptr(), _dense(A, (ch, S), f32, dev, "A"), B.data_ptr(), C.data_ptr(),
-        _dense(D, (ch,), f32, dev, "D"), _dense(dt_bias, (ch,), f32, dev, "dt_bias"),
-        None if z is None else z.data_ptr(), _dense(state, (n_slots, ch, S), f32, dev, "state"),
-        _dense(slots, (nb,), torch.int32, dev, "slots"), n_slots, nb, ch, S, G, io,
-        int(bool(dt_softplus)),
-        _pack_scan(_strides(x, "x")[0], 0, _strides(dt, "dt")[0], 0,
-                   0 if z is None else _strides(z, "z")[0], 0, sb, 0, sc, 0,
-                   _strides(out, "out")[0], 0),
-        out.data_ptr(), _raw_stream(dev.index))
+        _want(out, shape, ty, dev, "out")
+    rc = (_lib or library()).ttt_binding_scan_step(_pack_scan(
+        x.data_ptr(), dt.data_ptr(), _addr(A, (ch, S), f32, dev, "A"), B.data_ptr(), C.data_ptr(),
+        _addr(D, (ch,), f32, dev, "D"), _addr(dt_bias, (ch,), f32, dev, "dt_bias"),
+        0 if z is None else z.data_ptr(), 0, _addr(slots, (nb,), _I32, dev, "slots"), out.data_ptr(),
+        _addr(state, (n_slots, ch, S), f32, dev, "state"), 0, 0, _raw_stream(dev.index),
+        _strides(x, "x")[0], 0, _strides(dt, "dt")[0], 0, 0 if z is None else _strides(z, "z")[0], 0,
+        sb, 0, sc, 0, _strides(out, "out")[0], 0, n_slots, nb, 1, ch, S, G, io,
+        1 if dt_softplus else 0))
     if rc:
         _check(rc, "selective_scan_step")
     return out
@@ -952,28 +970,27 @@ def short_conv_forward(x, w, bias: Optional[torch.Tensor] = None, silu: bool = F
     oldest first, or None (zeros).  seq_starts: int32 [n_seq + 1] for sequences
     packed along the token axis (B = 1).  Returns (out [B, N, D], state_out).
     """
-    dev = _gpu(x)
-    if stream is not None or dev.index != _current_device():
-        with _elsewhere(dev, stream):
+    if _elsewhere_needed(x, stream):
+        with _elsewhere(x.device, stream):
             return short_conv_forward(x, w, bias, silu, state, seq_starts, out, state_out)
     if x.dim() != 3 or w.dim() != 2:
         raise ValueError("x must have three dimensions, w two")
-    B, N, D = x.shape
-    W, dt = w.shape[1], x.dtype
-    io = _io_dtype(x)
+    dev, ty, io, shape = x.device, x.dtype, _io_dtype(x), x.shape
+    B, N, D = shape
+    W = w.shape[1]
     starts, n_seq = _starts(seq_starts, B, dev)
-    rows = (n_seq, W - 1, D)
+    rows = (n_seq, max(W - 1, 0), D)
     if out is None:
-        out = torch.empty(x.shape, device=dev, dtype=dt)
+        out = torch.empty_like(x)   # x's order of dimensions
     else:
-        _want(out, x.shape, dt, dev, "out")
+        _want(out, shape, ty, dev, "out")
     if state_out is None:
-        state_out = torch.empty(rows, device=dev, dtype=dt)
-    rc = (_lib or library()).short_conv_forward(
-        x.data_ptr(), _dense(w, (D, W), _F32, dev, "w"), _dense(bias, (D,), _F32, dev, "bias"),
-        _dense(state, rows, dt, dev, "state"), starts, n_seq, B, N, D, W, io, int(bool(silu)),
-        _pack_conv(*_strides(x, "x")[:2], *_strides(out, "out")[:2]), out.data_ptr(),
-        _dense(state_out, rows, dt, dev, "state_out"), _raw_stream(dev.index))
+        state_out = x.new_empty(rows)
+    rc = (_lib or library()).ttt_binding_conv_forward(_pack_conv(
+        x.data_ptr(), _addr(w, (D, W), _F32, dev, "w"), _addr(bias, (D,), _F32, dev, "bias"),
+        _addr(state, rows, ty, dev, "state"), starts, out.data_ptr(),
+        _addr(state_out, rows, ty, dev, "state_out"), _raw_stream(dev.index), *_strides(x, "x")[:2],
+        *_strides(out, "out")[:2], n_seq, B, N, D, W, io, 1 if silu else 0))
     if rc:
         _check(rc, "short_conv_forward")
     return out, state_out
@@ -989,26 +1006,24 @@ def short_conv_step(x, w, state, bias: Optional[torch.Tensor] = None, silu: bool
     x [B, D]; w [D, W] fp32; state [n_slots, W - 1, D] in x's type; slots int32
     [B] (negative: an idle row) or None.  Returns out [B, D].
     """
-    dev = _gpu(x)
-    if stream is not None or dev.index != _current_device():
-        with _elsewhere(dev, stream):
+    if _elsewhere_needed(x, stream):
+        with _elsewhere(x.device, stream):
             return short_conv_step(x, w, state, bias, silu, slots, out)
     if x.dim() != 2 or w.dim() != 2 or state.dim() != 3:
         raise ValueError("x and w must have two dimensions, state three")
-    B, D = x.shape
-    W, dt = w.shape[1], x.dtype
-    io = _io_dtype(x)
-    n_slots = state.shape[0]
+    dev, ty, io, shape = x.device, x.dtype, _io_dtype(x), x.shape
+    B, D = shape
+    W, n_slots = w.shape[1], state.shape[0]
     if out is None:
-        out = torch.empty(x.shape, device=dev, dtype=dt)
+        out = torch.empty_like(x)
     else:
-        _want(out, x.shape, dt, dev, "out")
-    rc = (_lib or library()).short_conv_step(
-        x.data_ptr(), _dense(w, (D, W), _F32, dev, "w"), _dense(bias, (D,), _F32, dev, "bias"),
-        _dense(state, (n_slots, W - 1, D), dt, dev, "state"),
-        _dense(slots, (B,), torch.int32, dev, "slots"), n_slots, B, D, W, io, int(bool(silu)),
-        _pack_conv(_strides(x, "x")[0], 0, _strides(out, "out")[0], 0), out.data_ptr(),
-        _raw_stream(dev.index))
+        _want(out, shape, ty, dev, "out")
+    rc = (_lib or library()).ttt_binding_conv_step(_pack_conv(
+        x.data_ptr(), _addr(w, (D, W), _F32, dev, "w"), _addr(bias, (D,), _F32, dev, "bias"), 0,
+        _addr(slots, (B,), _I32, dev, "slots"), out.data_ptr(),
+        _addr(state, (n_slots, max(W - 1, 0), D), ty, dev, "state"), _raw_stream(dev.index),
+        _strides(x, "x")[0], 0, _strides(out, "out")[0], 0, n_slots, B, 1, D, W, io,
+        1 if silu else 0))
     if rc:
         _check(rc, "short_conv_step")
     return out

@@ -339,4 +339,82 @@ int short_conv_step(const void* x, const float* w, const float* bias, void* stat
   return ttt::short_conv_step_launch(a);
 }
 
+// The Python binding's forms of the calls: their arguments in one record each (a call with
+// 24 arguments through ctypes takes 7 us of the host's time, one with a record 1.5).  The
+// records' fields lie as struct.pack puts them.
+struct WindowRecord {
+  const void *q, *k, *v;
+  void *cache_k, *cache_v;
+  const int *slots, *past, *seq_starts;
+  void* out;
+  ttt_stream_t stream;
+  window_attention_layout lay;
+  int n_slots, n_seq, B, Hq, Hk, N, d, window, sinks, io;
+  float scale;
+};
+
+int ttt_binding_window_forward(const WindowRecord* r) {
+  return window_attention_forward(r->q, r->k, r->v, r->cache_k, r->cache_v, r->slots, r->n_slots,
+                                  r->past, r->seq_starts, r->n_seq, r->B, r->Hq, r->Hk, r->N, r->d,
+                                  r->window, r->sinks, r->io, r->scale, &r->lay, r->out, r->stream);
+}
+
+// past: the positions; n_seq and N are not used.
+int ttt_binding_window_step(const WindowRecord* r) {
+  return window_attention_step(r->q, r->k, r->v, r->cache_k, r->cache_v, r->past, r->slots,
+                               r->n_slots, r->B, r->Hq, r->Hk, r->d, r->window, r->sinks, r->io,
+                               r->scale, &r->lay, r->out, r->stream);
+}
+
+struct ScanRecord {
+  const void *x, *dt;
+  const float* A;
+  const void *B, *C;
+  const float *D, *dt_bias;
+  const void* z;
+  const float* state;
+  const int* index;   // seq_starts or slots
+  void* out;
+  float* state_out;   // or the pool
+  void* workspace;
+  size_t workspace_bytes;
+  ttt_stream_t stream;
+  selective_scan_layout lay;
+  int n, batch, N, channels, S, G, io, softplus;   // n: sequences or slots
+};
+
+int ttt_binding_scan_forward(const ScanRecord* r) {
+  return selective_scan_forward(r->x, r->dt, r->A, r->B, r->C, r->D, r->dt_bias, r->z, r->state,
+                                r->index, r->n, r->batch, r->N, r->channels, r->S, r->G, r->io,
+                                r->softplus, &r->lay, r->out, r->state_out, r->workspace,
+                                r->workspace_bytes, r->stream);
+}
+
+int ttt_binding_scan_step(const ScanRecord* r) {
+  return selective_scan_step(r->x, r->dt, r->A, r->B, r->C, r->D, r->dt_bias, r->z, r->state_out,
+                             r->index, r->n, r->batch, r->channels, r->S, r->G, r->io, r->softplus,
+                             &r->lay, r->out, r->stream);
+}
+
+struct ConvRecord {
+  const void* x;
+  const float *w, *bias;
+  const void* state;
+  const int* index;
+  void *out, *state_out;
+  ttt_stream_t stream;
+  short_conv_layout lay;
+  int n, B, N, D, W, io, silu;
+};
+
+int ttt_binding_conv_forward(const ConvRecord* r) {
+  return short_conv_forward(r->x, r->w, r->bias, r->state, r->index, r->n, r->B, r->N, r->D, r->W,
+                            r->io, r->silu, &r->lay, r->out, r->state_out, r->stream);
+}
+
+int ttt_binding_conv_step(const ConvRecord* r) {
+  return short_conv_step(r->x, r->w, r->bias, r->state_out, r->index, r->n, r->B, r->D, r->W, r->io,
+                         r->silu, &r->lay, r->out, r->stream);
+}
+
 }  // extern "C"

@@ -20,7 +20,7 @@
 //
 // Roles (384 threads, one block per SM, persistent over (tile pair, head)):
 //   warp 0      TMA: Q, and K and V through a ring of tiles.
-//   warp 1      all products.
+//   warps 1, 3  the products of the first and of the second query tile.
 //   warp 2      the list of key tiles, for all others.
 //   warps 4-7   rows of the first tile, warps 8-11 of the second: softmax, rescaling,
 //               outputs.
@@ -34,44 +34,48 @@ namespace ttt {
 
 namespace {
 
-constexpr int kM = 128;                  // rows of a tile, keys of a key tile
+constexpr int kM = 128;                  // rows of a tile
+constexpr int kKeys = 64;                // keys of a key tile
 constexpr int kThreads = 384;
 
 template <int DP>
 struct Plan {
-  static constexpr int kTile = kM * DP * 2;                  // bytes of a tile of Q, K or V
-  static constexpr int kStages = DP == 128 ? 4 : 8;
+  static constexpr int kQ = kM * DP * 2;                     // bytes of a tile of Q
+  static constexpr int kKv = kKeys * DP * 2;                 // of K or V
+  static constexpr int kStages = 64 * 1024 / kKv;            // of a K and a V each
   static constexpr int kStaging = 8 * 32 * 128;              // 32 rows of 64 outputs a warp
-  static constexpr int kSmem = 2 * kTile + kStages * kTile + kStaging + 1024 + 1024;
+  static constexpr int kSmem = 2 * kQ + 2 * kStages * kKv + kStaging + 1024 + 1024;
 };
+constexpr int kMostStages = Plan<64>::kStages;
 static_assert(Plan<128>::kSmem <= 227 * 1024 && Plan<64>::kSmem <= 227 * 1024, "shared memory");
 
-// What the list warp tells the others, one entry per key tile that either query tile
-// needs, one behind each item and one at the end.
+// What the list warp tells the others: one entry per key tile that either query tile needs.
 enum : int {
   kNeed = 1,      // << t: query tile t needs the key tile
   kWhole = 4,     // << t: all its queries see all of it
   kCache = 16,    // the key tile lies in a cache
   kTileEntry = 32,
-  kStop = 64
+  kLast = 64,     // of its item
+  kStop = 128     // of the block (without kTileEntry: there was none)
 };
 struct Entry {
   int flags;
-  int b, h, i0;        // the item
   int base, end;       // the key tile: see WinTile
-  int seq, slot, count, past, head;
+  int i0, b, h;        // the item
+  int seq, slot, count, past, head;   // a cache
   int pad;
 };
 static_assert(sizeof(Entry) == 48, "read 16 bytes at a time");
 constexpr int kEntries = 8;
-constexpr int kReaders = 10;   // the loads' thread, the products' warp, eight row warps
+constexpr int kReaders = 11;   // the loads' thread, the products' two warps, eight row warps
 
 struct Bars {
   uint64_t e_full[kEntries], e_free[kEntries];
   uint64_t q_full, q_free;
-  uint64_t full[8], empty[8];
-  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
-  uint64_t done;
+  uint64_t full[kMostStages], empty[kMostStages];
+  uint64_t s_full[2][2], p_full[2][2];   // by query tile and buffer
+  uint64_t pv_done[2], o_full[2], o_free[2];
+  uint64_t done[2];
   uint32_t tmem;
   alignas(16) Entry entry[kEntries];
 };
@@ -107,13 +111,13 @@ __device__ __forceinline__ bool needs(const SubTile& s, const WinTile& t) {
   if (s.a >= s.e) return false;
   if (t.seq >= 0) return max(s.a, t.c.i0) < min(s.e, t.c.i1);
   return t.base < s.e &&
-         (t.base + kM > s.lo || (t.base < s.s1 && t.base + kM > s.s0));
+         (t.base + kKeys > s.lo || (t.base < s.s1 && t.base + kKeys > s.s0));
 }
 
 // The windows of a tile's queries begin one behind another, so that the last one's and the
 // first query bound them all.
 __device__ __forceinline__ bool sees_whole(const SubTile& s, const WinTile& t) {
-  return t.seq < 0 && t.base >= s.lo_last && t.base + kM - 1 <= s.a && t.base + kM <= t.end;
+  return t.seq < 0 && t.base >= s.lo_last && t.base + kKeys - 1 <= s.a && t.base + kKeys <= t.end;
 }
 
 struct Item {
@@ -201,7 +205,7 @@ __device__ __noinline__ void row_alone(const TcParams& tp, int b, int h, int i0,
   }
   const WinRow row = win_row(p, b, i);
   float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  WinList<kM> w = win_list<kM>(p, b, i0, i0 + 2 * kM);
+  WinList<kKeys> w = win_list<kKeys>(p, b, i0, i0 + 2 * kM);
   WinTile t;
   while (win_next(p, w, t)) {
     const T *ks = k, *vs = v;
@@ -212,9 +216,9 @@ __device__ __noinline__ void row_alone(const TcParams& tp, int b, int h, int i0,
       vs = static_cast<const T*>(p.cache_v) + at;
       sk = sv = p.d;
     }
-    for (int j0 = t.base; j0 < min(t.base + kM, t.end); j0 += 32) {
+    for (int j0 = t.base; j0 < min(t.base + kKeys, t.end); j0 += 32) {
       const int j = j0 + lane;
-      const bool in = j >= 0 && j < t.base + kM && j < t.end &&
+      const bool in = j >= 0 && j < t.base + kKeys && j < t.end &&
                       (t.seq < 0 ? sees_new(row, j, t.end)
                                  : sees_cache(row, t.c, j, p.sinks, p.window));
       float s = -INFINITY;
@@ -250,37 +254,35 @@ __device__ __noinline__ void row_alone(const TcParams& tp, int b, int h, int i0,
     if (lane + 32 * e < p.d) out[lane + 32 * e] = from_f<T>(acc[e] / l);
 }
 
-// The next entry, by a whole warp (by one thread: `alone`).
+// The entries, read by a whole warp (by one thread: ALONE).
+template <bool ALONE>
 struct Reader {
   int n;
-  template <bool ALONE>
-  __device__ __forceinline__ bool next(Bars* B, Entry& e, int* status, unsigned long long lim) {
-    const int s = n % kEntries;
+  __device__ __forceinline__ bool wait(Bars* B, int* status, unsigned long long lim) {
+    uint64_t* bar = &B->e_full[n % kEntries];
     const uint32_t ph = (n / kEntries) & 1;
-    const bool ok = ALONE ? wait_one(&B->e_full[s], ph, status, lim)
-                          : wait_all(&B->e_full[s], ph, status, lim);
-    if (!ok) return false;
-    const int4* src = reinterpret_cast<const int4*>(&B->entry[s]);
-    int4* dst = reinterpret_cast<int4*>(&e);
-    dst[0] = src[0];
-    dst[1] = src[1];
-    dst[2] = src[2];
+    return ALONE ? wait_one(bar, ph, status, lim) : wait_all(bar, ph, status, lim);
+  }
+  // 16 bytes of the entry
+  __device__ __forceinline__ void part(Bars* B, Entry& e, int i) {
+    reinterpret_cast<int4*>(&e)[i] = reinterpret_cast<const int4*>(&B->entry[n % kEntries])[i];
+  }
+  __device__ __forceinline__ void done(Bars* B) {
     if (!ALONE) __syncwarp();
-    if (ALONE || (threadIdx.x & 31) == 0) mbar_arrive(&B->e_free[s]);
+    if (ALONE || (threadIdx.x & 31) == 0) mbar_arrive(&B->e_free[n % kEntries]);
     ++n;
-    return true;
   }
 };
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_constant__ TcParams tp) {
   using PL = Plan<DP>;
-  constexpr int NS = PL::kStages, TB = PL::kTile, NB = DP / 64;
+  constexpr int NS = PL::kStages, QB = PL::kQ, TB = PL::kKv, NB = DP / 64;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint8_t* Q = smem;
-  uint8_t* ring = smem + 2 * TB;
-  uint8_t* staging = ring + NS * TB;
+  uint8_t* ring = smem + 2 * QB;
+  uint8_t* staging = ring + 2 * NS * TB;
   Bars* B = reinterpret_cast<Bars*>(staging + PL::kStaging);
   const WinParams& p = tp.w;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -288,22 +290,26 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
 
   if (tid == 0) {
     mbar_init(&B->q_full, 1);
-    mbar_init(&B->q_free, 1);
+    mbar_init(&B->q_free, 2);   // by the products of both query tiles, as are K and V
     for (int s = 0; s < kEntries; ++s) {
       mbar_init(&B->e_full[s], 1);
       mbar_init(&B->e_free[s], kReaders);
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(&B->full[s], 1);
-      mbar_init(&B->empty[s], 1);
+      mbar_init(&B->empty[s], 2);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&B->s_full[t], 1);
-      mbar_init(&B->p_full[t], 4);   // a lane of each warp
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&B->s_full[t][i], 1);
+        mbar_init(&B->p_full[t][i], 4);   // a lane of each warp
+      }
+      mbar_init(&B->pv_done[t], 1);
       mbar_init(&B->o_full[t], 1);
       mbar_init(&B->o_free[t], 4);
     }
-    mbar_init(&B->done, 1);
+    mbar_init(&B->done[0], 1);
+    mbar_init(&B->done[1], 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -321,40 +327,41 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
     if (lane == 0) {
       int fills = 0, q_loads = 0;
       bool ok = true, first = true;   // first key tile of an item
-      auto load = [&](const CUtensorMap* map, int y, int z, int w) {
-        const int s = fills % NS;
-        ok = ok && wait_one(&B->empty[s], ((fills / NS) & 1) ^ 1, p.status, lim);
-        if (!ok) return;
-        mbar_arrive_expect_tx(&B->full[s], TB);
-#pragma unroll
-        for (int x = 0; x < NB; ++x)
-          tma_load_4d(ring + s * TB + x * (kM * 128), map, x * 64, y, z, w, &B->full[s]);
-        ++fills;
-      };
-      Reader rd{0};
+      Reader<true> rd{0};
       Entry e;
       while (ok) {
-        ok = rd.next<true>(B, e, p.status, lim);
-        if (!ok || (e.flags & kStop)) break;
-        if (!(e.flags & kTileEntry)) {
-          first = true;
-          continue;
-        }
-        const int hk = e.h / (p.Hq / p.Hk);
+        ok = rd.wait(B, p.status, lim);
+        if (!ok) break;
+        for (int i = 0; i < 3; ++i) rd.part(B, e, i);
+        rd.done(B);
+        if (!(e.flags & kTileEntry)) break;
+        const int hk = e.h / (p.Hq / p.Hk), s = fills % NS;
         const bool c = e.flags & kCache;
-        load(c ? &tp.ck : &tp.k, e.base, hk, c ? e.slot : e.b);
+        const CUtensorMap *mk = c ? &tp.ck : &tp.k, *mv = c ? &tp.cv : &tp.v;
+        const int w = c ? e.slot : e.b;
+        ok = wait_one(&B->empty[s], ((fills / NS) & 1) ^ 1, p.status, lim);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&B->full[s], 2 * TB);
+        uint8_t* st = ring + s * 2 * TB;
+#pragma unroll
+        for (int x = 0; x < NB; ++x)
+          tma_load_4d(st + x * (kKeys * 128), mk, x * 64, e.base, hk, w, &B->full[s]);
+#pragma unroll
+        for (int x = 0; x < NB; ++x)
+          tma_load_4d(st + TB + x * (kKeys * 128), mv, x * 64, e.base, hk, w, &B->full[s]);
+        ++fills;
         if (first) {   // the first keys do not wait for the last item's queries
-          ok = ok && wait_one(&B->q_free, (q_loads & 1) ^ 1, p.status, lim);
+          ok = wait_one(&B->q_free, (q_loads & 1) ^ 1, p.status, lim);
           if (!ok) break;
-          mbar_arrive_expect_tx(&B->q_full, 2 * TB);
+          mbar_arrive_expect_tx(&B->q_full, 2 * QB);
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int x = 0; x < NB; ++x)
-              tma_load_4d(Q + t * TB + x * (kM * 128), &tp.q, x * 64, e.i0 + t * kM, e.h, e.b, &B->q_full);
+              tma_load_4d(Q + t * QB + x * (kM * 128), &tp.q, x * 64, e.i0 + t * kM, e.h, e.b, &B->q_full);
           ++q_loads;
-          first = false;
         }
-        load(c ? &tp.cv : &tp.v, e.base, hk, c ? e.slot : e.b);
+        first = e.flags & kLast;
+        if (e.flags & kStop) break;
       }
       if (!ok) {   // what is on its way lands before the block ends
         if (q_loads) wait_one(&B->q_full, (q_loads - 1) & 1, p.status, lim);
@@ -363,91 +370,101 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 3) {
     // ---------------------------------------------------------------- products
-    const uint32_t id_s = idesc_bf16_f32(kM, 0, 0), id_o = idesc_bf16_f32(DP, 0, 1);
-    const uint64_t qd = smem_desc_sw128(smem_u32(Q), 16, 1024);
+    // A warp for each query tile, so that neither waits for the other's weights (one warp for
+    // both took longer over its entries, waits and instructions than the products themselves).
+    // S of the tile's key tile j, then O of j - 2: the scores lie in two buffers, so that the
+    // rows find the next ones when they are done with a tile.
+    const int u = warp >> 1;
+    const uint32_t Su = tmem + u * kM, Ou = tmem + 256 + u * kM;
+    const uint32_t id_s = idesc_bf16_f32(kKeys, 0, 0), id_o = idesc_bf16_f32(DP, 0, 1);
+    const uint64_t qd = smem_desc_sw128(smem_u32(Q + u * QB), 16, 1024);
     const uint64_t kd = smem_desc_sw128(smem_u32(ring), 16, 1024);
-    const uint64_t vd = smem_desc_sw128(smem_u32(ring), kM * 128, 1024);
-    int uses = 0, items = 0;            // ring tiles taken; items with key tiles
-    int np = 0, no = 0;                 // parities of the weights awaited, the outputs begun
+    const uint64_t vd = smem_desc_sw128(smem_u32(ring + TB), kKeys * 128, 1024);
+    int items = 0;                      // with key tiles
+    uint32_t ns = 0, np = 0, no = 0;    // scores made, weights taken; parity of the outputs begun
     bool ok = true;
-    auto scores = [&](int t, int s) {   // S_t = Q_t K^T with K in ring stage s
-#pragma unroll
-      for (int k = 0; k < DP / 16; ++k) {
-        const uint32_t o = (k >> 2) * (kM * 8) + (k & 3) * 2;
-        umma_bf16_w(tmem + t * kM, qd + t * (TB >> 4) + o, kd + s * (TB >> 4) + o, id_s, k != 0);
+    bool inside = false, begun = false; // an item; its outputs
+    int v0 = -1, v1 = -1;               // stages whose V await their weights
+    Reader<false> rd{0};
+    auto outputs = [&]() {   // O += P V for v0
+      if (!begun) {
+        ok = ok && wait_all(&B->o_free[u], no ^ 1, p.status, lim);
+        no ^= 1;
       }
-      umma_commit_w(&B->s_full[t]);
-    };
-    auto outputs = [&](int t, int s, bool first) {   // O_t += P_t V with V in stage s
-#pragma unroll
-      for (int k = 0; k < kM / 16; ++k)
-        umma_ts_w(tmem + 256 + t * kM, tmem + t * kM + k * 8, vd + s * (TB >> 4) + k * 128, id_o,
-                  !first || k != 0);
-    };
-    Reader rd{0};
-    Entry e;
-    int cur = 0;                        // who awaits V, at v_at in the ring
-    int v_at = 0;
-    int begun = 0, told = 0;            // bits of the query tiles, in this item
-    while (ok) {
-      ok = rd.next<false>(B, e, p.status, lim);
-      if (!ok || (e.flags & kStop)) break;
-      const bool tile = e.flags & kTileEntry;
-      const int nxt = tile ? e.flags & 3 : 0;
-      if (tile && !cur) {   // an item begins (the entries of one follow one another)
-        ok = wait_all(&B->q_full, items & 1, p.status, lim);
-        ++items;
-      }
-      if (!tile && cur) umma_commit_w(&B->q_free);   // all scores of this item are under way
-      const int k_at = uses, ks = k_at % NS, vs = v_at % NS;
-      // what is there long before the weights
-      if (cur) ok = wait_all(&B->full[vs], (v_at / NS) & 1, p.status, lim);
-      if (tile) ok = ok && wait_all(&B->full[ks], (k_at / NS) & 1, p.status, lim);
-      const int fresh = cur & ~begun;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        if (fresh & (1 << u)) {
-          ok = ok && wait_all(&B->o_free[u], ((no >> u) & 1) ^ 1, p.status, lim);
-          no ^= 1 << u;
-        }
-      if (!ok) break;
+      const uint32_t buf = np & 1;
+      ok = ok && wait_all(&B->p_full[u][buf], (np >> 1) & 1, p.status, lim);
+      if (!ok) return;
       tc_fence_after();
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (cur & (1 << u)) {
-          ok = wait_all(&B->p_full[u], (np >> u) & 1, p.status, lim);
-          if (!ok) break;
-          tc_fence_after();
-          outputs(u, vs, fresh & (1 << u));
-          np ^= 1 << u;
+      for (int k = 0; k < kKeys / 16; ++k)
+        umma_ts_w(Ou, Su + buf * kKeys + k * 8, vd + v0 * (2 * TB >> 4) + k * 128, id_o, begun || k != 0);
+      umma_commit_w(&B->pv_done[u]);
+      ++np;
+      begun = true;
+    };
+    while (ok) {
+      // a stage that is full has an entry (the loads' thread read it before): what is left to
+      // wait for is the first, for there may be none
+      const int ks = rd.n % NS;
+      if (rd.n == 0) {
+        ok = rd.wait(B, p.status, lim);
+        if (!ok || !(B->entry[0].flags & kTileEntry)) break;
+      }
+      ok = wait_all(&B->full[ks], (rd.n / NS) & 1, p.status, lim);
+      if (!ok) break;
+      const int flags = *reinterpret_cast<volatile int*>(&B->entry[rd.n % kEntries].flags);
+      rd.done(B);
+      if (!inside) {
+        ok = wait_all(&B->q_full, items & 1, p.status, lim);
+        if (!ok) break;
+        ++items;
+        inside = true;
+      }
+      tc_fence_after();
+      const bool mine = flags & (kNeed << u);
+      if (mine) {
+        if (v0 >= 0) outputs();
+        if (!ok) break;
+        const uint32_t buf = ns & 1;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k)   // S = Q K^T
+          umma_bf16_w(Su + buf * kKeys, qd + (k >> 2) * (kM * 8) + (k & 3) * 2,
+                      kd + ks * (2 * TB >> 4) + (k >> 2) * (kKeys * 8) + (k & 3) * 2, id_s, k != 0);
+        umma_commit_w(&B->s_full[u][buf]);
+        ++ns;
+        if (v0 >= 0) umma_commit_w(&B->empty[v0]);
+        v0 = v1;
+        v1 = ks;
+        if (!(flags & kLast)) continue;
+      }
+      // another's key tile or an item's end: what awaits its weights goes first, for its stage
+      // may be in the way of the tiles to come
+#pragma unroll 1
+      for (int i = 0; i < 2 && ok; ++i) {
+        if (v0 >= 0) {
+          outputs();
+          if (ok) umma_commit_w(&B->empty[v0]);
         }
-        if (nxt & (1 << u)) scores(u, ks);
-        // the first tile's window begins the list's window tiles: without caches behind them,
-        // it has had its last where it needs no next one
-        if (u == 0 && (cur & 1) && !(nxt & 1) && !p.past) {
-          umma_commit_w(&B->o_full[0]);
-          told = 1;
-        }
+        v0 = v1;
+        v1 = -1;
       }
       if (!ok) break;
-      begun |= cur;
-      if (cur) umma_commit_w(&B->empty[vs]);
-      if (tile) {
-        umma_commit_w(&B->empty[ks]);
-        v_at = k_at + 1;
-        uses = k_at + 2;
-      } else {
-        for (int u = 0; u < 2; ++u)
-          if ((begun & ~told) & (1 << u)) umma_commit_w(&B->o_full[u]);
-        begun = told = 0;
+      if (!mine) {
+        if (lane == 0) mbar_arrive(&B->empty[ks]);
+        __syncwarp();
       }
-      cur = nxt;
+      if (flags & kLast) {
+        umma_commit_w(&B->q_free);
+        if (begun) umma_commit_w(&B->o_full[u]);
+        inside = begun = false;
+      }
+      if (flags & kStop) break;
     }
     if (!ok) {   // the products under way end before their TMEM is given back
-      umma_commit_w(&B->done);
-      wait_all(&B->done, 0, p.status, lim);
+      umma_commit_w(&B->done[u]);
+      wait_all(&B->done[u], 0, p.status, lim);
     }
   } else if (warp == 2) {
     // ---------------------------------------------------------------- the list
@@ -474,7 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
         mbar_arrive(&B->e_full[s]);
         ++n;
       };
-      Entry e = {};
+      Entry e = {}, held = {};   // an entry is held back until it is known whether it is a last
+      bool holds = false;
       for (unsigned item = blockIdx.x; item < tp.items && ok; item += gridDim.x) {
         const Item it = get_item(tp, item);
         e.b = it.b;
@@ -482,11 +500,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
         e.i0 = it.i0;
         const SubTile s0 = sub_tile(p, it.b, it.i0, it.i0 + kM);
         const SubTile s1 = sub_tile(p, it.b, it.i0 + kM, it.i0 + 2 * kM);
-        WinList<kM> w = win_list<kM>(p, it.b, it.i0, it.i0 + 2 * kM);
+        WinList<kKeys> w = win_list<kKeys>(p, it.b, it.i0, it.i0 + 2 * kM);
         WinTile t;
+        bool first = true;
         while (ok && win_next(p, w, t)) {
           const bool n0 = needs(s0, t), n1 = needs(s1, t);
           if (!n0 && !n1) continue;
+          if (holds) {
+            if (first) held.flags |= kLast;
+            put(held);
+          }
+          first = false;
           e.flags = kTileEntry | (n0 ? kNeed : 0) | (n1 ? kNeed << 1 : 0) |
                     (sees_whole(s0, t) ? kWhole : 0) | (sees_whole(s1, t) ? kWhole << 1 : 0);
           e.base = t.base;
@@ -499,13 +523,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
             e.past = t.c.past;
             e.head = t.c.head;
           }
-          put(e);
+          held = e;
+          holds = true;
         }
-        e.flags = 0;
-        put(e);
       }
-      e.flags = kStop;
-      put(e);
+      held.flags |= kLast | kStop;
+      put(held);
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -538,11 +561,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
         tmem_st16(O + 16 * x, ow);
       }
     };
-    Reader rd{0};
+    Reader<false> rd{0};
     Entry e;
     while (ok) {
-      ok = rd.next<false>(B, e, p.status, lim);
-      if (!ok || (e.flags & kStop)) break;
+      ok = rd.wait(B, p.status, lim);
+      if (!ok) break;
+      rd.part(B, e, 0);
+      if (!begun || (e.flags & kCache)) {
+        rd.part(B, e, 1);
+        rd.part(B, e, 2);
+      }
+      rd.done(B);
       if (e.flags & (kNeed << t)) {
         if (!begun) {
           ib = e.b;
@@ -557,14 +586,19 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
             row.lo = row.t0 = row.sink1 = 0;
           }
         }
-        ok = wait_all(&B->s_full[t], ns & 1, p.status, lim);
+        const int buf = ns & 1;
+        const uint32_t Sb = S + buf * kKeys;
+        ok = wait_all(&B->s_full[t][buf], (ns >> 1) & 1, p.status, lim);
         if (!ok) break;
-        ++ns;
         tc_fence_after();
-        const bool whole = e.flags & (kWhole << t);
-        // up to three spans of columns that the row sees
-        int a0 = 0, a1 = kM, b0 = 0, b1 = 0, c0 = 0, c1 = 0;
-        if (!whole) {
+        float s[2][32];
+        tmem_ld32(Sb, s[0]);
+        tmem_ld32(Sb + 32, s[1]);
+        tmem_wait32(s[0]);
+        tmem_wait32(s[1]);
+        if (!(e.flags & (kWhole << t))) {
+          // up to three spans of columns that the row sees
+          int a0, a1, b0, b1, c0 = 0, c1 = 0;
           if (!(e.flags & kCache)) {
             const int top = min(row.i + 1, e.end);
             a0 = row.lo - e.base;
@@ -583,67 +617,44 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
             c1 = e.count - e.base;
             if (row.seq != e.seq) a1 = b1 = c1 = -1;
           }
-        }
-        auto seen = [&](int x) {   // bits of the 32 columns of part x
-          return span_bits(a0, a1, 32 * x) | span_bits(b0, b1, 32 * x) | span_bits(c0, c1, 32 * x);
-        };
-        auto mask = [&](float (&s)[32], uint32_t bits) {
-          if (__all_sync(0xffffffffu, bits == 0xffffffffu)) return;
 #pragma unroll
-          for (int y = 0; y < 32; ++y) s[y] = bits & (1u << y) ? s[y] : -INFINITY;
-        };
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t bits = span_bits(a0, a1, 32 * x) | span_bits(b0, b1, 32 * x) |
+                                  span_bits(c0, c1, 32 * x);
+            if (!__all_sync(0xffffffffu, bits == 0xffffffffu)) {
+#pragma unroll
+              for (int y = 0; y < 32; ++y) s[x][y] = bits & (1u << y) ? s[x][y] : -INFINITY;
+            }
+          }
+        }
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto largest = [&](const float (&s)[32]) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int y = 0; y < 32; y += 8)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tops[i] = max3(tops[i], s[y + 2 * i], s[y + 2 * i + 1]);
-        };
-        if (whole) {
-          float s[4][32];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) tmem_ld32(S + 32 * x, s[x]);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) tmem_wait32(s[x]);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) largest(s[x]);
-        } else {
-#pragma unroll 1
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t bits = seen(x);
-            if (!__any_sync(0xffffffffu, bits)) continue;
-            float s[32];
-            tmem_ld32(S + 32 * x, s);
-            tmem_wait32(s);
-            mask(s, bits);
-            largest(s);
-          }
-        }
+            for (int i = 0; i < 4; ++i) tops[i] = max3(tops[i], s[x][y + 2 * i], s[x][y + 2 * i + 1]);
         const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
-        if (__any_sync(0xffffffffu, top > m + grow)) rescale(top > m + grow ? top : m);
+        if (__any_sync(0xffffffffu, top > m + grow)) {
+          // the outputs so far are those of all tiles before this one
+          if (begun) {
+            ok = wait_all(&B->pv_done[t], (ns - 1) & 1, p.status, lim);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          rescale(top > m + grow ? top : m);
+        }
+        ++ns;
         begun = true;
         float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
         const float mc = m == -INFINITY ? 0.f : m * c;
-#pragma unroll 1
-        for (int x = 0; x < 4; ++x) {   // the scores once more: 128 of them are not kept
-          float s[32];
-          uint32_t pw[16];
-          tmem_ld32(S + 32 * x, s);
-          tmem_wait32(s);
-          if (!whole) {
-            const uint32_t bits = seen(x);
-            if (!__any_sync(0xffffffffu, bits)) {
 #pragma unroll
-              for (int y = 0; y < 16; ++y) pw[y] = 0u;
-              tmem_st16(S + 16 * x, pw);
-              continue;
-            }
-            mask(s, bits);
-          }
+        for (int x = 0; x < 2; ++x) {
+          uint32_t pw[16];
 #pragma unroll
           for (int y = 0; y < 32; y += 4) {
-            const float v0 = ex2(fmaf(s[y], c, -mc)), v1 = ex2(fmaf(s[y + 1], c, -mc));
-            const float v2 = ex2(fmaf(s[y + 2], c, -mc)), v3 = ex2(fmaf(s[y + 3], c, -mc));
+            const float v0 = ex2(fmaf(s[x][y], c, -mc)), v1 = ex2(fmaf(s[x][y + 1], c, -mc));
+            const float v2 = ex2(fmaf(s[x][y + 2], c, -mc)), v3 = ex2(fmaf(s[x][y + 3], c, -mc));
             sum0 += v0;
             sum1 += v1;
             sum2 += v2;
@@ -651,14 +662,15 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
             pw[y / 2] = bf16_pair(v0, v1);
             pw[y / 2 + 1] = bf16_pair(v2, v3);
           }
-          tmem_st16(S + 16 * x, pw);
+          tmem_st16(Sb + 16 * x, pw);
         }
         l += (sum0 + sum1) + (sum2 + sum3);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B->p_full[t]);
-      } else if (!(e.flags & kTileEntry) && begun) {
+        if (lane == 0) mbar_arrive(&B->p_full[t][buf]);
+      }
+      if ((e.flags & kLast) && begun) {
         begun = false;
         ok = wait_all(&B->o_full[t], no & 1, p.status, lim);
         if (!ok) break;
@@ -726,6 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
           row_alone(tp, ib, ih, i0, first + x);
         }
       }
+      if (e.flags & kStop) break;
     }
   }
   __syncthreads();
@@ -753,10 +766,10 @@ int prepare() {
   return g_ready[dev] == 1 ? g_sms[dev] : 0;
 }
 
-// [B, H, N, d] with the given strides as a map of 64 x 128 boxes; false where TMA cannot
+// [B, H, N, d] with the given strides as a map of 64 x `rows` boxes; false where TMA cannot
 // take it.
 bool win_map(CUtensorMap* m, const void* ptr, const delta_rule_stride& s, long long B, long long H,
-             long long N, int d) {
+             long long N, int d, unsigned rows) {
   const unsigned long long dims[4] = {(unsigned long long)d, (unsigned long long)N,
                                       (unsigned long long)H, (unsigned long long)B};
   // the stride of a dimension of one element is never used: give a valid one
@@ -765,7 +778,7 @@ bool win_map(CUtensorMap* m, const void* ptr, const delta_rule_stride& s, long l
   for (unsigned long long x : st)
     if (x == 0 || x % 16 != 0 || x >= (1ull << 40)) return false;
   if ((reinterpret_cast<uintptr_t>(ptr) & 15) != 0 || d % 8 != 0) return false;
-  const unsigned box[4] = {64, kM, 1, 1};
+  const unsigned box[4] = {64, rows, 1, 1};
   return encode_bf16_4d(m, ptr, dims, st, box);
 }
 
@@ -774,15 +787,15 @@ bool win_map(CUtensorMap* m, const void* ptr, const delta_rule_stride& s, long l
 int window_attention_tc(const WindowArgs& a) {
   if (!a.bf16 || a.d > 128 || a.d % 8 != 0 || !(a.scale > 0.f)) return 1;
   TcParams p;
-  if (!win_map(&p.q, a.q, a.lay.q, a.B, a.Hq, a.N, a.d) ||
-      !win_map(&p.k, a.k, a.lay.k, a.B, a.Hk, a.N, a.d) ||
-      !win_map(&p.v, a.v, a.lay.v, a.B, a.Hk, a.N, a.d))
+  if (!win_map(&p.q, a.q, a.lay.q, a.B, a.Hq, a.N, a.d, kM) ||
+      !win_map(&p.k, a.k, a.lay.k, a.B, a.Hk, a.N, a.d, kKeys) ||
+      !win_map(&p.v, a.v, a.lay.v, a.B, a.Hk, a.N, a.d, kKeys))
     return 1;
   if (a.past) {
     const long long places = (long long)a.window + a.sinks;
     const delta_rule_stride s = {(long long)a.Hk * places * a.d, places * a.d, a.d};
-    if (!win_map(&p.ck, a.cache_k, s, a.n_slots, a.Hk, places, a.d) ||
-        !win_map(&p.cv, a.cache_v, s, a.n_slots, a.Hk, places, a.d))
+    if (!win_map(&p.ck, a.cache_k, s, a.n_slots, a.Hk, places, a.d, kKeys) ||
+        !win_map(&p.cv, a.cache_v, s, a.n_slots, a.Hk, places, a.d, kKeys))
       return 1;
   } else {
     p.ck = p.k;
