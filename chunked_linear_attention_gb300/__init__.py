@@ -1,6 +1,6 @@
 """GB300 (sm_103a) large-chunk TTT-KVB layer and chunked linear attention.
 
-Thin ctypes binding over the C ABI in ``include/ttt.h``: every step of the
+Thin ctypes binding over the C ABI in ``include/``: every step of the
 computation runs in the library's CUDA kernels; this module only marshals
 arguments (device pointers of torch tensors, the current CUDA stream) and
 allocates outputs and workspace with torch.  There is no CPU fallback: if the
@@ -40,6 +40,7 @@ EXPORTED = (
     "delta_rule_step", "block_norm_forward", "ttt_selftest_withhold_delta",
     "window_attention_forward", "window_attention_step", "selective_scan_workspace_size",
     "selective_scan_forward", "selective_scan_step", "short_conv_forward", "short_conv_step",
+    "ttt_selftest_withhold_window",
 )
 
 
@@ -162,6 +163,8 @@ def _declare(lib):
         call.restype, call.argtypes = i, [cp]
     lib.ttt_selftest_withhold_delta.restype = None
     lib.ttt_selftest_withhold_delta.argtypes = [i]
+    lib.ttt_selftest_withhold_window.restype = None
+    lib.ttt_selftest_withhold_window.argtypes = [i]
     lib.ttt_selftest_withhold_release.restype = None
     lib.ttt_selftest_withhold_release.argtypes = [i]
     lib.ttt_launch_count.restype = ctypes.c_ulonglong
@@ -1068,6 +1071,12 @@ def selftest_withhold_delta(kernel: int):
     """Test hook: from the next delta-rule call on, a wait of one of the chunk
     form's kernels runs out (0 turns it off).  See include/ttt_selftest.h."""
     library().ttt_selftest_withhold_delta(int(kernel))
+
+
+def selftest_withhold_window(what: int):
+    """Test hook: from the next call on, a wait of the window attention's tensor-core
+    kernel runs out (0 turns it off).  See include/ttt_selftest.h."""
+    library().ttt_selftest_withhold_window(int(what))
 
 
 def selftest_gemm(A, B, a_mn_major: bool, b_mn_major: bool, tile_n: int = 128, stream=None):

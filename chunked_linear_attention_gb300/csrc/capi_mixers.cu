@@ -7,6 +7,7 @@
 
 #include "capi_util.h"
 #include "mixers.h"
+#include "ttt_selftest.h"
 
 namespace {
 
@@ -338,6 +339,8 @@ int short_conv_step(const void* x, const float* w, const float* bias, void* stat
   a.stream = reinterpret_cast<cudaStream_t>(stream);
   return ttt::short_conv_step_launch(a);
 }
+
+void ttt_selftest_withhold_window(int what) { ttt::window_attention_withhold(what); }
 
 // The Python binding's forms of the calls: their arguments in one record each (a call with
 // 24 arguments through ctypes takes 7 us of the host's time, one with a record 1.5).  The

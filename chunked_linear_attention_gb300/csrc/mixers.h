@@ -32,6 +32,8 @@ int window_attention_simt(const WindowArgs& a);
 // On the tensor cores (bf16, d <= 128, aligned strides, scale > 0).  Returns 1 where it
 // does not apply, else a ttt_status.
 int window_attention_tc(const WindowArgs& a);
+// Test hook: see ttt_selftest_withhold_window.
+void window_attention_withhold(int what);
 // The new keys and values into the caches, behind the attention.
 int window_attention_store(const WindowArgs& a);
 

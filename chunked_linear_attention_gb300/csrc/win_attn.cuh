@@ -30,6 +30,7 @@ struct WinParams {
   float scale;          // of the scores, times log2(e)
   window_attention_layout lay;
   unsigned long long wait_ns;
+  int withhold;         // test hook, see ttt_selftest_withhold_window
 };
 
 // Slot and past of a sequence: no past without a slot of the pool.

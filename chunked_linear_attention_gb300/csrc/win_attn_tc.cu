@@ -24,6 +24,7 @@
 //   warp 2      the list of key tiles, for all others.
 //   warps 4-7   rows of the first tile, warps 8-11 of the second: softmax, rescaling,
 //               outputs.
+#include <atomic>
 #include <mutex>
 
 #include "builder.h"
@@ -339,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
         const bool c = e.flags & kCache;
         const CUtensorMap *mk = c ? &tp.ck : &tp.k, *mv = c ? &tp.cv : &tp.v;
         const int w = c ? e.slot : e.b;
+        if (p.withhold == 1 && blockIdx.x == 0 && fills == 1) break;
         ok = wait_one(&B->empty[s], ((fills / NS) & 1) ^ 1, p.status, lim);
         if (!ok) break;
         mbar_arrive_expect_tx(&B->full[s], 2 * TB);
@@ -668,7 +670,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B->p_full[t][buf]);
+        const bool kept = p.withhold == 2 && blockIdx.x == 0 && t == 0 && ns == 2;
+        if (lane == 0 && !kept) mbar_arrive(&B->p_full[t][buf]);
       }
       if ((e.flags & kLast) && begun) {
         begun = false;
@@ -745,6 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+std::atomic<int> g_withhold{0};
+
 int g_ready[64] = {0};   // 0 unknown, 1 usable, 2 not usable
 int g_sms[64] = {0};
 std::mutex g_mu;
@@ -784,6 +789,8 @@ bool win_map(CUtensorMap* m, const void* ptr, const delta_rule_stride& s, long l
 
 }  // namespace
 
+void window_attention_withhold(int what) { g_withhold.store(what); }
+
 int window_attention_tc(const WindowArgs& a) {
   if (!a.bf16 || a.d > 128 || a.d % 8 != 0 || !(a.scale > 0.f)) return 1;
   TcParams p;
@@ -804,6 +811,7 @@ int window_attention_tc(const WindowArgs& a) {
   const int sms = prepare();
   if (!sms) return TTT_ERR_CUDA;
   p.w = win_params(a);
+  p.w.withhold = g_withhold.load();
   p.tiles = (a.N + 2 * kM - 1) / (2 * kM);
   const long long items = (long long)a.B * p.tiles * a.Hq;
   if (items > 0x7fffffff) return 1;

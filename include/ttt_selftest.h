@@ -53,6 +53,18 @@ void ttt_selftest_withhold_release(int bh);
  * usual.  0 turns the hook off.  Process-wide; not for production use. */
 void ttt_selftest_withhold_delta(int kernel);
 
+/* Test hook for the bounded waits of window_attention_forward on the tensor
+ * cores.  From the next call on, in the first block
+ *   1  the second key tile is not loaded;
+ *   2  the first query tile's weights of its second key tile are not handed on.
+ * The block's roles run into their wait limits, record TTT_ERR_TIMEOUT in the
+ * device status word, wait for the copies and products that they have issued,
+ * and end.  The outputs of the first block's queries (the first 256 tokens of the
+ * first head, and every grid-th group of 256 after it) are undefined then;
+ * others are computed as usual.  0 turns the hook off.  Process-wide; not for
+ * production use. */
+void ttt_selftest_withhold_window(int what);
+
 #ifdef __cplusplus
 }
 #endif
