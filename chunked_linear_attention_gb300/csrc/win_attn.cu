@@ -8,50 +8,69 @@ namespace ttt {
 namespace {
 
 // ------------------------------------------------------------ prompts, fp32
-// One CTA: 64 queries of one head against key tiles of 64, 256 threads.  A thread
-// holds 4 x 4 scores and 4 rows x DP / 16 columns of the output; running maximum and
-// sum of the softmax per row, so that each score is made once.  Bound by the fp32 pipe
-// (16 products for 8 words of shared memory in the scores, 4 DP / 16 for 4 + DP / 16 in
-// the outputs).
-constexpr int kQT = 64, kKT = 64, kPad = 4;
+// One CTA: QT queries of one head against key tiles of 64, two threads a query.  A thread
+// holds 8 x 4 scores and 8 rows x DP / 16 columns of the output, with a running maximum and
+// sum of the softmax per row, so that each score is made once.  Bound by the shared memory's
+// words per product (12 for 32, in the scores and, at d 64, in the outputs): two thirds of
+// the fp32 pipe at best.  16384 tokens, 8 heads, window 1024: heads of 64 0.99 ms (35
+// TFLOP/s), of 128 1.93 ms; with 4 x 4 scores a thread (8 words for 16) and every score masked
+// by itself 1.36 and 3.21.  2048 tokens with a window of 512 are 256 blocks of few warps: 126
+// us, by 256 threads a block 116.
+constexpr int kKT = 64, kPad = 4;
 
-template <int DP>
+template <int DP, int QT>
 constexpr int simt_smem() {
-  return (DP * (kQT + kPad) * 2 + kKT * DP + kKT * (kQT + kPad)) * 4;
+  return (DP * (QT + kPad) + DP * (kKT + kPad) + kKT * DP + kKT * (QT + kPad)) * 4 +
+         QT * (int)sizeof(WinRow);
 }
 
-template <typename T, int DP>
-__global__ void __launch_bounds__(256) window_attention_kernel(const __grid_constant__ WinParams p) {
+template <typename T, int DP, int QT, bool VEC>
+__global__ void __launch_bounds__(2 * QT) window_attention_kernel(
+    const __grid_constant__ WinParams p) {
+  constexpr int NC = DP / 64;                  // 4 NC columns of the output a thread
+  constexpr int kQT = QT, kWarps = QT / 16;
   extern __shared__ __align__(16) float sm[];
   float* Qt = sm;                              // [DP][kQT + kPad]
   float* Kt = Qt + DP * (kQT + kPad);          // [DP][kKT + kPad]
   float* V = Kt + DP * (kKT + kPad);           // [kKT][DP]
   float* Pt = V + kKT * DP;                    // [kKT][kQT + kPad]
+  WinRow* rows = reinterpret_cast<WinRow*>(Pt + kKT * (kQT + kPad));
   pdl_launch_dependents();
   pdl_wait();
   const int b = blockIdx.z, h = blockIdx.y, i0 = blockIdx.x * kQT;
   const int hk = h / (p.Hq / p.Hk);
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int tid = threadIdx.x, lane = tid & 31, tx = tid & 15, ty = tid >> 4;
   if (blockIdx.x == 0 && h == 0 && p.starts) check_starts(p.starts, p.n_seq, p.N, p.status);
   const T* q = static_cast<const T*>(p.q) + b * p.lay.q.batch + h * p.lay.q.head;
   const T* k = static_cast<const T*>(p.k) + b * p.lay.k.batch + hk * p.lay.k.head;
   const T* v = static_cast<const T*>(p.v) + b * p.lay.v.batch + hk * p.lay.v.head;
-  for (int e = tid; e < kQT * DP; e += 256) {
-    const int r = e / DP, c = e % DP;
-    const bool in = i0 + r < p.N && c < p.d;
-    Qt[c * (kQT + kPad) + r] = in ? to_f<T>(q[(i0 + r) * p.lay.q.token + c]) * p.scale : 0.f;
+  // four numbers of a row of a tile to their places: lanes take 8 rows x 4 pieces, whose
+  // transposed places fall on different banks but for pairs
+  auto piece = [&](int e, int rows8, int& r, int& c) {
+    r = e % rows8 * 8 + (lane >> 2);
+    c = (e / rows8 * 4 + (lane & 3)) * 4;
+  };
+  for (int e = tid >> 5; e < DP / 16 * (kQT / 8); e += kWarps) {
+    int r, c;
+    piece(e, kQT / 8, r, c);
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
+    if (i0 + r < p.N && c < p.d) load_row<T, 4, VEC>(q + (i0 + r) * p.lay.q.token + c, p.d - c, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) Qt[(c + i) * (kQT + kPad) + r] = f[i] * p.scale;
   }
-  WinRow row[4];
+  if (tid < kQT) rows[tid] = win_row(p, b, i0 + tid);
+  float m[8], l[8], o[8][4 * NC];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) row[r] = win_row(p, b, i0 + ty * 4 + r);
-  float m[4], l[4], o[4][DP / 16];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
+  for (int r = 0; r < 8; ++r) {
     m[r] = -INFINITY;
     l[r] = 0.f;
 #pragma unroll
-    for (int c = 0; c < DP / 16; ++c) o[r][c] = 0.f;
+    for (int c = 0; c < 4 * NC; ++c) o[r][c] = 0.f;
   }
+  __syncthreads();
+  // windows begin one behind another: the last query's and the first query bound them all
+  const int last = min(kQT, p.N - i0) - 1;
+  const int lo_last = rows[last].lo;
   WinList<kKT> w = win_list<kKT>(p, b, i0, i0 + kQT);
   WinTile t;
   while (win_next(p, w, t)) {
@@ -67,39 +86,56 @@ __global__ void __launch_bounds__(256) window_attention_kernel(const __grid_cons
     }
     bool odd = false;
     __syncthreads();
-    for (int e = tid; e < kKT * DP; e += 256) {
-      const int r = e / DP, c = e % DP, j = t.base + r;
-      const bool in = j >= 0 && j < t.end && c < p.d;
-      Kt[c * (kKT + kPad) + r] = in ? to_f<T>(ks[j * sk + c]) : 0.f;
-      const float x = in ? to_f<T>(vs[j * sv + c]) : 0.f;
-      V[r * DP + c] = x;
-      odd |= !isfinite(x);
+#pragma unroll 4
+    for (int e = tid >> 5; e < DP / 16 * (kKT / 8); e += kWarps) {
+      int r, c;
+      piece(e, kKT / 8, r, c);
+      const int j = t.base + r;
+      float f[4] = {0.f, 0.f, 0.f, 0.f}, g[4] = {0.f, 0.f, 0.f, 0.f};
+      if (j >= 0 && j < t.end && c < p.d) {
+        load_row<T, 4, VEC>(ks + j * sk + c, p.d - c, f);
+        load_row<T, 4, VEC>(vs + j * sv + c, p.d - c, g);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        Kt[(c + i) * (kKT + kPad) + r] = f[i];
+        odd |= !isfinite(g[i]);
+      }
+      *reinterpret_cast<float4*>(V + r * DP + c) = make_float4(g[0], g[1], g[2], g[3]);
     }
     odd = __syncthreads_or(odd);
-    float s[4][4] = {};
+    float s[8][4] = {};
 #pragma unroll 4
     for (int c = 0; c < p.d; ++c) {
-      const float4 a = *reinterpret_cast<const float4*>(Qt + c * (kQT + kPad) + ty * 4);
+      const float4 a0 = *reinterpret_cast<const float4*>(Qt + c * (kQT + kPad) + ty * 8);
+      const float4 a1 = *reinterpret_cast<const float4*>(Qt + c * (kQT + kPad) + ty * 8 + 4);
       const float4 x = *reinterpret_cast<const float4*>(Kt + c * (kKT + kPad) + tx * 4);
-      const float aa[4] = {a.x, a.y, a.z, a.w}, xx[4] = {x.x, x.y, x.z, x.w};
+      const float aa[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+      const float xx[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < 8; ++r)
 #pragma unroll
         for (int n = 0; n < 4; ++n) s[r][n] = fmaf(aa[r], xx[n], s[r][n]);
     }
-    unsigned seen = 0;
+    unsigned seen = 0xffffffffu;
+    if (t.seq >= 0 || t.base < lo_last || t.base + kKT - 1 > i0 || t.base + kKT > t.end) {
+      seen = 0u;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      float top = -INFINITY;
+      for (int r = 0; r < 8; ++r) {
+        const WinRow row = rows[ty * 8 + r];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int j = t.base + tx * 4 + n;
-        const bool ok = t.seq < 0 ? sees_new(row[r], j, t.end)
-                                  : sees_cache(row[r], t.c, j, p.sinks, p.window);
-        seen |= (unsigned)ok << (r * 4 + n);
-        if (!ok) s[r][n] = -INFINITY;
-        top = fmaxf(top, s[r][n]);
+        for (int n = 0; n < 4; ++n) {
+          const int j = t.base + tx * 4 + n;
+          const bool ok = t.seq < 0 ? sees_new(row, j, t.end)
+                                    : sees_cache(row, t.c, j, p.sinks, p.window);
+          seen |= (unsigned)ok << (r * 4 + n);
+          if (!ok) s[r][n] = -INFINITY;
+        }
       }
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      float top = fmaxf(fmaxf(s[r][0], s[r][1]), fmaxf(s[r][2], s[r][3]));
 #pragma unroll
       for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
       const float mn = fmaxf(m[r], top);
@@ -111,68 +147,85 @@ __global__ void __launch_bounds__(256) window_attention_kernel(const __grid_cons
         s[r][n] = exp2f(s[r][n] - base);
         sum += s[r][n];
       }
-#pragma unroll
-      for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      // the sum over the 16 threads of a row waits until the end
       l[r] = fmaf(l[r], f, sum);
       m[r] = mn;
 #pragma unroll
-      for (int c = 0; c < DP / 16; ++c) o[r][c] *= f;
+      for (int c = 0; c < 4 * NC; ++c) o[r][c] *= f;
     }
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
-      *reinterpret_cast<float4*>(Pt + (tx * 4 + n) * (kQT + kPad) + ty * 4) =
-          make_float4(s[0][n], s[1][n], s[2][n], s[3][n]);
-    __syncthreads();
+    for (int n = 0; n < 4; ++n) {
+      float* to = Pt + (tx * 4 + n) * (kQT + kPad) + ty * 8;
+      *reinterpret_cast<float4*>(to) = make_float4(s[0][n], s[1][n], s[2][n], s[3][n]);
+      *reinterpret_cast<float4*>(to + 4) = make_float4(s[4][n], s[5][n], s[6][n], s[7][n]);
+    }
+    __syncwarp();   // a warp's rows are its own
     if (!odd) {
 #pragma unroll 4
       for (int n = 0; n < kKT; ++n) {
-        const float4 a = *reinterpret_cast<const float4*>(Pt + n * (kQT + kPad) + ty * 4);
-        const float aa[4] = {a.x, a.y, a.z, a.w};
+        const float4 a0 = *reinterpret_cast<const float4*>(Pt + n * (kQT + kPad) + ty * 8);
+        const float4 a1 = *reinterpret_cast<const float4*>(Pt + n * (kQT + kPad) + ty * 8 + 4);
+        const float aa[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
 #pragma unroll
-        for (int c = 0; c < DP / 16; ++c) {
-          const float x = V[n * DP + c * 16 + tx];
+        for (int c = 0; c < NC; ++c) {
+          const float4 x = *reinterpret_cast<const float4*>(V + n * DP + 64 * c + tx * 4);
+          const float xx[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int r = 0; r < 4; ++r) o[r][c] = fmaf(aa[r], x, o[r][c]);
+          for (int r = 0; r < 8; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[r][4 * c + i] = fmaf(aa[r], xx[i], o[r][4 * c + i]);
         }
       }
     } else {
       // a value that a query does not see must not reach it, not even times 0
+#pragma unroll 1
       for (int n = 0; n < kKT; ++n) {
-        const unsigned bits = __shfl_sync(0xffffffffu, seen, (tid & 16) | (n >> 2)) >> (n & 3);
-        const float4 a = *reinterpret_cast<const float4*>(Pt + n * (kQT + kPad) + ty * 4);
-        const float aa[4] = {a.x, a.y, a.z, a.w};
+        const unsigned bits = __shfl_sync(0xffffffffu, seen, (lane & 16) | (n >> 2)) >> (n & 3);
 #pragma unroll
-        for (int c = 0; c < DP / 16; ++c) {
-          const float x = V[n * DP + c * 16 + tx];
+        for (int r = 0; r < 8; ++r) {
+          const float a = Pt[n * (kQT + kPad) + ty * 8 + r];
+          if ((bits >> (r * 4)) & 1) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if ((bits >> (r * 4)) & 1) o[r][c] = fmaf(aa[r], x, o[r][c]);
+            for (int c = 0; c < 4 * NC; ++c)
+              o[r][c] = fmaf(a, V[n * DP + 64 * (c / 4) + tx * 4 + c % 4], o[r][c]);
+          }
         }
       }
     }
   }
   T* out = static_cast<T*>(p.out) + b * p.lay.out.batch + h * p.lay.out.head;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    if (row[r].i < 0) continue;
-    const float f = 1.f / l[r];
+  for (int r = 0; r < 8; ++r) {
+    float sum = l[r];
 #pragma unroll
-    for (int c = 0; c < DP / 16; ++c)
-      if (c * 16 + tx < p.d) out[row[r].i * p.lay.out.token + c * 16 + tx] = from_f<T>(o[r][c] * f);
+    for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    const int i = rows[ty * 8 + r].i;
+    if (i < 0) continue;
+    const float f = 1.f / sum;
+#pragma unroll
+    for (int c = 0; c < 4 * NC; ++c) {
+      const int at = 64 * (c / 4) + tx * 4 + c % 4;
+      if (at < p.d) out[i * p.lay.out.token + at] = from_f<T>(o[r][c] * f);
+    }
   }
 }
 
-template <typename T, int DP>
+template <typename T, int DP, int QT>
 int launch_simt(const WindowArgs& a, const WinParams& p) {
-  auto kern = window_attention_kernel<T, DP>;
-  constexpr int smem = simt_smem<DP>();
+  auto ok = [&](const void* x, const delta_rule_stride& s) {
+    return (reinterpret_cast<uintptr_t>(x) & (4 * sizeof(T) - 1)) == 0 && s.batch % 4 == 0 &&
+           s.head % 4 == 0 && s.token % 4 == 0;
+  };
+  const bool vec = a.d % 4 == 0 && ok(a.q, a.lay.q) && ok(a.k, a.lay.k) && ok(a.v, a.lay.v);
+  auto kern = vec ? window_attention_kernel<T, DP, QT, true> : window_attention_kernel<T, DP, QT, false>;
+  constexpr int smem = simt_smem<DP, QT>();
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return TTT_ERR_CUDA;
   const double tok = (double)a.B * a.N;
   ProfScope ps(PT_WIN_SIMT, a.stream, 4.0 * tok * a.Hq * a.d * fmin(a.N, (double)a.window + a.sinks),
                tok * (a.bf16 ? 2 : 4) * 2.0 * a.d * (a.Hq + a.Hk));
-  return launch_grid(kern, dim3((a.N + kQT - 1) / kQT, a.Hq, a.B), 256, smem, a.stream, p) ==
+  return launch_grid(kern, dim3((a.N + QT - 1) / QT, a.Hq, a.B), 2 * QT, smem, a.stream, p) ==
                  cudaSuccess
              ? TTT_OK
              : TTT_ERR_CUDA;
@@ -180,9 +233,13 @@ int launch_simt(const WindowArgs& a, const WinParams& p) {
 
 template <typename T>
 int simt_t(const WindowArgs& a, const WinParams& p) {
-  if (a.d <= 64) return launch_simt<T, 64>(a, p);
-  if (a.d <= 128) return launch_simt<T, 128>(a, p);
-  return launch_simt<T, 256>(a, p);
+  // Heads of more than 64 take most of the shared memory: 128 queries a block, where those
+  // fill the card twice, hold eight warps there and not four (16384 tokens, heads of 128: 1.93
+  // ms, 64 queries 2.50; of 64, with three blocks on an SM, 1.06 and 0.99).
+  const bool wide = (long long)((a.N + 127) / 128) * a.Hq * a.B >= 2 * 152;
+  if (a.d <= 64) return launch_simt<T, 64, 64>(a, p);
+  if (a.d <= 128) return wide ? launch_simt<T, 128, 128>(a, p) : launch_simt<T, 128, 64>(a, p);
+  return launch_simt<T, 256, 64>(a, p);
 }
 
 // ------------------------------------------------------------ the caches after a prompt

@@ -109,6 +109,14 @@ def test_attention_sizes(size, dtype):
 
 
 @TYPES
+@pytest.mark.parametrize("d", [128, 72])
+def test_attention_of_many_blocks(d, dtype):
+    """More blocks than the card takes at once, the last of them short."""
+    cla = lib()
+    attn(cla, qkv(14, 2, 16, 1, 1300, d, dtype), 70, 5, dtype)
+
+
+@TYPES
 @pytest.mark.parametrize("window,sinks", [(40, 4), (130, 0), (1, 1), (16, 200)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_attention_goes_on_from_a_cache(window, sinks, d, dtype):
