@@ -69,7 +69,7 @@ __device__ __forceinline__ bool step_row(const WinStepParams& p, int G, StepRowT
   if (slot < 0) {
     T* out = static_cast<T*>(p.out) + r.b * p.lay.out.batch + r.h0 * p.lay.out.head;
     if (r.split == 0)
-      for (int e = tid; e < r.heads * p.d; e += kWarps * 32)
+      for (int e = tid; e < r.heads * p.d; e += blockDim.x)
         out[e / p.d * p.lay.out.head + e % p.d] = from_f<T>(0.f);
     return false;
   }
@@ -82,7 +82,7 @@ __device__ __forceinline__ bool step_row(const WinStepParams& p, int G, StepRowT
   T* ck = static_cast<T*>(p.cache_k) + at;
   T* cv = static_cast<T*>(p.cache_v) + at;
   if (r.split == 0 && chunk == 0)
-    for (int e = tid; e < p.d; e += kWarps * 32) {
+    for (int e = tid; e < p.d; e += blockDim.x) {
       ck[(long long)r.own * p.d + e] = r.kn[e];
       cv[(long long)r.own * p.d + e] = r.vn[e];
     }
@@ -94,23 +94,23 @@ __device__ __forceinline__ bool step_row(const WinStepParams& p, int G, StepRowT
 }
 
 // The warps' sums, then the cluster's blocks' (a part of the outputs each).
-template <typename T, int DP, int G>
+template <typename T, int DP, int G, int NW>
 __device__ __forceinline__ void step_join(const WinStepParams& p, const StepRowT<T>& r,
-                                          float (&acc_s)[kWarps][G][DP], float (&m_s)[kWarps][G],
-                                          float (&l_s)[kWarps][G], float (&acc_b)[G][DP],
+                                          float (&acc_s)[NW][G][DP], float (&m_s)[NW][G],
+                                          float (&l_s)[NW][G], float (&acc_b)[G][DP],
                                           float (&m_b)[G], float (&l_b)[G]) {
   const int tid = threadIdx.x;
   T* out = static_cast<T*>(p.out) + r.b * p.lay.out.batch + r.h0 * p.lay.out.head;
   __syncthreads();
-  for (int e = tid; e < r.heads * DP; e += kWarps * 32) {
+  for (int e = tid; e < r.heads * DP; e += NW * 32) {
     const int g = e / DP, x = e % DP;
     float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_s[w][g]);
+    for (int w = 0; w < NW; ++w) top = fmaxf(top, m_s[w][g]);
     const float base = top == -INFINITY ? 0.f : top;
     float a = 0.f, sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < NW; ++w) {
       const float f = ex2(m_s[w][g] - base);
       a = fmaf(f, acc_s[w][g][x], a);
       sum = fmaf(f, l_s[w][g], sum);
@@ -128,7 +128,7 @@ __device__ __forceinline__ void step_join(const WinStepParams& p, const StepRowT
   if (p.splits == 1) return;
   cg::cluster_group cl = cg::this_cluster();
   cl.sync();
-  for (int e = r.split * kWarps * 32 + tid; e < r.heads * p.d; e += p.splits * kWarps * 32) {
+  for (int e = r.split * NW * 32 + tid; e < r.heads * p.d; e += p.splits * NW * 32) {
     const int g = e / p.d, x = e % p.d;
     float top = -INFINITY;
     for (int i = 0; i < p.splits; ++i) top = fmaxf(top, *cl.map_shared_rank(&m_b[g], i));
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kWarps * 32) window_step_kernel(
       }
     }
   }
-  step_join<T, DP, G>(p, row, acc_s, m_s, l_s, acc_b, m_b, l_b);
+  step_join<T, DP, G, kWarps>(p, row, acc_s, m_s, l_s, acc_b, m_b, l_b);
 }
 
 // ------------------------------------------------------------ bf16 on the tensor cores
@@ -281,13 +281,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int DP>
-__global__ void __launch_bounds__(kWarps * 32, 2) window_step_mma_kernel(
+template <int DP, int NW>
+__global__ void __launch_bounds__(NW * 32, 16 / NW) window_step_mma_kernel(
     const __grid_constant__ WinStepParams p) {
   using T = __nv_bfloat16;
   constexpr int G = 8, H = DP / 64;   // heads; halves of 64 dimensions
-  __shared__ float acc_s[kWarps][G][DP];
-  __shared__ float m_s[kWarps][G], l_s[kWarps][G];
+  __shared__ float acc_s[NW][G][DP];
+  __shared__ float m_s[NW][G], l_s[NW][G];
   __shared__ float acc_b[G][DP], m_b[G], l_b[G];   // of this block
   pdl_launch_dependents();
   pdl_wait();
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) window_step_mma_kernel(
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[y][n][e] = 0.f;
 
-  for (int j0 = r.from + warp * 16; j0 < r.to; j0 += kWarps * 16) {
+  for (int j0 = r.from + warp * 16; j0 < r.to; j0 += NW * 16) {
     uint4 k[2][2 * H], v[H][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {   // key j0 + 8 t + g
@@ -414,12 +414,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) window_step_mma_kernel(
     m_s[warp][g] = m;
     l_s[warp][g] = l;
   }
-  step_join<T, DP, G>(p, r, acc_s, m_s, l_s, acc_b, m_b, l_b);
+  step_join<T, DP, G, NW>(p, r, acc_s, m_s, l_s, acc_b, m_b, l_b);
 }
 
 // G: query heads that a block takes together.
 template <typename T>
-int win_step_go(const WindowStepArgs& a, WinStepParams p, int G, void (*kern)(WinStepParams)) {
+int win_step_go(const WindowStepArgs& a, WinStepParams p, int G, int warps,
+                void (*kern)(WinStepParams)) {
   p.chunks = (a.Hq / a.Hk + G - 1) / G;
   // two blocks a SM, and no block with less than 128 places
   const long long ctas = (long long)a.B * a.Hk * p.chunks, places = (long long)a.window + a.sinks;
@@ -429,7 +430,7 @@ int win_step_go(const WindowStepArgs& a, WinStepParams p, int G, void (*kern)(Wi
   const double pairs = (double)a.B * places;
   ProfScope ps(PT_WIN_STEP, a.stream, 4.0 * pairs * a.Hq * a.d, 2.0 * pairs * a.Hk * a.d * sizeof(T));
   const dim3 grid((unsigned)(a.Hk * p.chunks * p.splits), a.B);
-  return launch_grid(kern, grid, kWarps * 32, 0, a.stream, p, p.splits) == cudaSuccess ? TTT_OK
+  return launch_grid(kern, grid, warps * 32, 0, a.stream, p, p.splits) == cudaSuccess ? TTT_OK
                                                                                        : TTT_ERR_CUDA;
 }
 
@@ -445,7 +446,7 @@ bool rows_of_8(const WindowStepArgs& a) {
 
 template <typename T, int DP, int G>
 int launch_win_step(const WindowStepArgs& a, const WinStepParams& p) {
-  return win_step_go<T>(a, p, G, rows_of_8<T>(a) ? window_step_kernel<T, DP, G, true>
+  return win_step_go<T>(a, p, G, kWarps, rows_of_8<T>(a) ? window_step_kernel<T, DP, G, true>
                                                  : window_step_kernel<T, DP, G, false>);
 }
 
@@ -460,8 +461,20 @@ int step_g(const WindowStepArgs& a, const WinStepParams& p) {
 template <typename T>
 int step_d(const WindowStepArgs& a, const WinStepParams& p) {
   if constexpr (sizeof(T) == 2) {
-    if (a.d <= 128 && rows_of_8<T>(a))
-      return win_step_go<T>(a, p, 8, a.d <= 64 ? window_step_mma_kernel<64> : window_step_mma_kernel<128>);
+    if (a.d <= 128 && rows_of_8<T>(a)) {
+      // a warp takes 16 places at a time: no more warps than a small cache keeps busy (256
+      // rows, 8 key heads, 64 places: 44 us with eight warps a block, 25 with two; 300 places: 90 with eight, 78
+      // with four)
+      const long long places = (long long)a.window + a.sinks;
+      if (places <= 96)
+        return win_step_go<T>(a, p, 8, 2, a.d <= 64 ? window_step_mma_kernel<64, 2>
+                                                    : window_step_mma_kernel<128, 2>);
+      if (places <= 640)
+        return win_step_go<T>(a, p, 8, 4, a.d <= 64 ? window_step_mma_kernel<64, 4>
+                                                    : window_step_mma_kernel<128, 4>);
+      return win_step_go<T>(a, p, 8, 8, a.d <= 64 ? window_step_mma_kernel<64, 8>
+                                                  : window_step_mma_kernel<128, 8>);
+    }
   }
   if (a.d <= 64) return step_g<T, 64>(a, p);
   if (a.d <= 128) return step_g<T, 128>(a, p);
