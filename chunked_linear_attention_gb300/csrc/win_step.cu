@@ -3,12 +3,14 @@
 // What a token sees lies in the first min(t + 1, sinks + window) places of its slot, in
 // some order; a softmax does not mind the order.  So the step writes the token's key and
 // value to their place and takes the places as one list, split over the blocks of a
-// cluster: one warp reads several keys at once, DP / 8 lanes a key, 8 dimensions a lane,
-// for the G query heads of a key head together, with running maxima and sums; warps and
-// blocks join their sums at the end through (distributed) shared memory.  The new token's
+// cluster; a block takes several query heads of a key head together and keeps running
+// maxima and sums, which warps and blocks join at the end through (distributed) shared
+// memory.  In fp32 (and for rows that are not in 16-byte pieces) a warp reads several keys
+// at once, DP / 8 lanes a key, 8 dimensions a lane; bf16 goes to the tensor cores, below.  The new token's
 // row is taken from its inputs, never from the place that is being written.
 //
-// Bound by HBM: keys and values once.
+// Bound by HBM: keys and values once.  250 rows, 32 query heads on 8 key heads of 128,
+// 2048 + 4 places, bf16: 303 us, 6.9 TB/s; fp32 with 64 rows 217 us, 5.0 TB/s.
 #include <cooperative_groups.h>
 
 #include "mixers.cuh"
@@ -264,8 +266,8 @@ __global__ void __launch_bounds__(kWarps * 32) window_step_kernel(
 
 // ------------------------------------------------------------ bf16 on the tensor cores
 // With several query heads a key head the products above take longer than the keys and
-// values (8 FMA and their reduction for each number read): for bf16 they go through the
-// warp-wide matrix instruction, 16 keys at a time.
+// values (8 FMA and their reduction for each number read; the 250 rows above took 667 us):
+// for bf16 they go through the warp-wide matrix instruction, 16 keys at a time.
 //   S [heads x keys] = Q K^T: rows are the heads (8 at most; the other 8 rows are idle).  A
 //       lane reads 16 bytes of a key and uses them as the two operands' halves of two
 //       products: the dimensions of a product are those that its lanes have read.
@@ -281,12 +283,32 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
+               : "memory");
+}
+
+// Keys and values come to shared memory by asynchronous copies, kStepStages tiles of 16 a
+// warp, so that a warp has two on their way while it works on one (loaded into registers
+// where they are used, an iteration waited for memory: 16 rows of 8 key heads and 2052
+// places took 35 us, 27 with the copies).  A row's 16-byte pieces lie at their number xor the row's, so that the
+// lanes of a read fall on different banks.
+constexpr int kStepStages = 3;
+
 template <int DP, int NW>
-__global__ void __launch_bounds__(NW * 32, 16 / NW) window_step_mma_kernel(
+constexpr int step_smem() {
+  return NW * kStepStages * 2 * 16 * DP * 2;
+}
+
+template <int DP, int NW>
+__global__ void __launch_bounds__(NW * 32) window_step_mma_kernel(
     const __grid_constant__ WinStepParams p) {
   using T = __nv_bfloat16;
   constexpr int G = 8, H = DP / 64;   // heads; halves of 64 dimensions
-  __shared__ float acc_s[NW][G][DP];
+  constexpr int kTileB = 16 * DP * 2, kPer = DP / 8;   // bytes of a tile; pieces of a row
+  extern __shared__ __align__(128) uint8_t ring[];
+  static_assert(NW * kStepStages * 2 * kTileB >= NW * G * DP * 4, "the sums take the ring's place");
+  float(&acc_s)[NW][G][DP] = *reinterpret_cast<float(*)[NW][G][DP]>(ring);
   __shared__ float m_s[NW][G], l_s[NW][G];
   __shared__ float acc_b[G][DP], m_b[G], l_b[G];   // of this block
   pdl_launch_dependents();
@@ -294,8 +316,6 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW) window_step_mma_kernel(
   StepRowT<T> r;
   if (!step_row<T>(p, G, r)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
-  const T* ck = r.ck;
-  const T* cv = r.cv;
   // this lane's dimensions of head g: 32 i + 8 q4 ..
   uint4 q[2 * H];
 #pragma unroll
@@ -319,29 +339,50 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW) window_step_mma_kernel(
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[y][n][e] = 0.f;
 
-  for (int j0 = r.from + warp * 16; j0 < r.to; j0 += NW * 16) {
+  uint8_t* mine = ring + warp * kStepStages * 2 * kTileB;
+  const uint32_t mine_s = smem_u32(mine);
+  const int first = r.from + warp * 16, step = NW * 16;
+  // the tile of places j0 .. j0 + 15 to a stage; zeros behind the last place and dimension
+  auto fetch = [&](int j0, int stage) {
+    const uint32_t to = mine_s + stage * 2 * kTileB;
+    if (j0 < r.to) {
+#pragma unroll
+      for (int x = 0; x < 16 * kPer / 32; ++x) {
+        const int e = x * 32 + lane, row = e / kPer, c = e % kPer, j = j0 + row;
+        const bool in = j < r.to && c * 8 < p.d, own = j == r.own;
+        const long long at = in ? (long long)j * p.d + c * 8 : 0;
+        const uint32_t dst = to + row * (DP * 2) + ((c ^ (row & 7)) << 4);
+        copy16(dst, own && in ? r.kn + c * 8 : r.ck + at, in);
+        copy16(dst + kTileB, own && in ? r.vn + c * 8 : r.cv + at, in);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int x = 0; x < kStepStages - 1; ++x) fetch(first + x * step, x);
+  int stage = 0;
+  for (int j0 = first; j0 < r.to; j0 += step) {
+    int ahead = stage + kStepStages - 1;
+    if (ahead >= kStepStages) ahead -= kStepStages;
+    fetch(j0 + (kStepStages - 1) * step, ahead);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStepStages - 1) : "memory");
+    __syncwarp();
+    const uint32_t ks = mine_s + stage * 2 * kTileB, vs = ks + kTileB;
+    if (++stage == kStepStages) stage = 0;
     uint4 k[2][2 * H], v[H][4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {   // key j0 + 8 t + g
-      const int j = j0 + 8 * t + g;
-      const T* row = j == r.own ? r.kn : ck + (long long)(j < r.to ? j : r.from) * p.d;
+    for (int t = 0; t < 2; ++t)      // key j0 + 8 t + g
 #pragma unroll
-      for (int i = 0; i < 2 * H; ++i) {
-        const int c = 32 * i + 8 * q4;
-        k[t][i] = c < p.d ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
-      }
+      for (int i = 0; i < 2 * H; ++i)
+        k[t][i] = lds128(ks + (8 * t + g) * (DP * 2) + (((4 * i + q4) ^ g) << 4));
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {    // keys j0 + 2 q4, + 1, + 8, + 9
+      const int row = 2 * q4 + (t & 1) + 4 * (t & 2);
+#pragma unroll
+      for (int y = 0; y < H; ++y)
+        v[y][t] = lds128(vs + row * (DP * 2) + (((8 * y + g) ^ (row & 7)) << 4));
     }
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {   // keys j0 + 2 q4, + 1, + 8, + 9; zero behind the last
-      const int j = j0 + 2 * q4 + (t & 1) + 4 * (t & 2);
-      const T* row = j == r.own ? r.vn : cv + (long long)j * p.d;
-#pragma unroll
-      for (int y = 0; y < H; ++y) {
-        const int c = 64 * y + 8 * g;
-        v[y][t] = j < r.to && c < p.d ? *reinterpret_cast<const uint4*>(row + c)
-                                      : make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
+    __syncwarp();   // read before the stage is filled again
     float s[2][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -399,6 +440,8 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW) window_step_mma_kernel(
   }
   l += __shfl_xor_sync(0xffffffffu, l, 1);
   l += __shfl_xor_sync(0xffffffffu, l, 2);
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();   // the ring is done with
   // the sums of hi and of lo; column 2 q4 + e of the products with n has dimension
   // 64 y + 8 (2 q4 + e) + n
 #pragma unroll
@@ -419,10 +462,15 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW) window_step_mma_kernel(
 
 // G: query heads that a block takes together.
 template <typename T>
-int win_step_go(const WindowStepArgs& a, WinStepParams p, int G, int warps,
+int win_step_go(const WindowStepArgs& a, WinStepParams p, int G, int warps, int smem,
                 void (*kern)(WinStepParams)) {
+  // static arrays of up to 8 KB count towards the 48 KB that need no leave
+  if (smem > 40 * 1024 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return TTT_ERR_CUDA;
   p.chunks = (a.Hq / a.Hk + G - 1) / G;
-  // two blocks a SM, and no block with less than 128 places
+  // as many blocks as two a SM, and none with less than 128 places (up to four a SM: 8, 16
+  // and 32 rows of 8 key heads and 2052 places 20, 32 and 53 us, by this rule 15, 27 and 45)
   const long long ctas = (long long)a.B * a.Hk * p.chunks, places = (long long)a.window + a.sinks;
   p.splits = 1;
   while (p.splits < 8 && ctas * p.splits * 2 <= 2 * kStepSms && places / (p.splits * 2) >= 128)
@@ -430,8 +478,8 @@ int win_step_go(const WindowStepArgs& a, WinStepParams p, int G, int warps,
   const double pairs = (double)a.B * places;
   ProfScope ps(PT_WIN_STEP, a.stream, 4.0 * pairs * a.Hq * a.d, 2.0 * pairs * a.Hk * a.d * sizeof(T));
   const dim3 grid((unsigned)(a.Hk * p.chunks * p.splits), a.B);
-  return launch_grid(kern, grid, warps * 32, 0, a.stream, p, p.splits) == cudaSuccess ? TTT_OK
-                                                                                       : TTT_ERR_CUDA;
+  const cudaError_t e = launch_grid(kern, grid, warps * 32, smem, a.stream, p, p.splits);
+  return e == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 
 // Rows of 8 numbers, 16 bytes at a time: the caches are dense and 16-byte aligned.
@@ -446,8 +494,9 @@ bool rows_of_8(const WindowStepArgs& a) {
 
 template <typename T, int DP, int G>
 int launch_win_step(const WindowStepArgs& a, const WinStepParams& p) {
-  return win_step_go<T>(a, p, G, kWarps, rows_of_8<T>(a) ? window_step_kernel<T, DP, G, true>
-                                                 : window_step_kernel<T, DP, G, false>);
+  return win_step_go<T>(a, p, G, kWarps, 0,
+                        rows_of_8<T>(a) ? window_step_kernel<T, DP, G, true>
+                                        : window_step_kernel<T, DP, G, false>);
 }
 
 template <typename T, int DP>
@@ -462,18 +511,16 @@ template <typename T>
 int step_d(const WindowStepArgs& a, const WinStepParams& p) {
   if constexpr (sizeof(T) == 2) {
     if (a.d <= 128 && rows_of_8<T>(a)) {
-      // a warp takes 16 places at a time: no more warps than a small cache keeps busy (256
-      // rows, 8 key heads, 64 places: 44 us with eight warps a block, 25 with two; 300 places: 90 with eight, 78
-      // with four)
-      const long long places = (long long)a.window + a.sinks;
-      if (places <= 96)
-        return win_step_go<T>(a, p, 8, 2, a.d <= 64 ? window_step_mma_kernel<64, 2>
-                                                    : window_step_mma_kernel<128, 2>);
-      if (places <= 640)
-        return win_step_go<T>(a, p, 8, 4, a.d <= 64 ? window_step_mma_kernel<64, 4>
-                                                    : window_step_mma_kernel<128, 4>);
-      return win_step_go<T>(a, p, 8, 8, a.d <= 64 ? window_step_mma_kernel<64, 8>
-                                                  : window_step_mma_kernel<128, 8>);
+      // a warp takes 16 places at a time: four warps a block, or two where there are many
+      // blocks with few places (2048 blocks: 64 places 34 us with four, 26 with two; 200: 60
+      // and 53; 600: 112 and 111; 64 blocks with 128 places 5.4 and 6.9)
+      const long long ctas = (long long)a.B * a.Hk * ((a.Hq / a.Hk + 7) / 8);
+      const bool few = (long long)a.window + a.sinks <= 512 && ctas >= 4 * kStepSms;
+      if (a.d <= 64)
+        return few ? win_step_go<T>(a, p, 8, 2, step_smem<64, 2>(), window_step_mma_kernel<64, 2>)
+                   : win_step_go<T>(a, p, 8, 4, step_smem<64, 4>(), window_step_mma_kernel<64, 4>);
+      return few ? win_step_go<T>(a, p, 8, 2, step_smem<128, 2>(), window_step_mma_kernel<128, 2>)
+                 : win_step_go<T>(a, p, 8, 4, step_smem<128, 4>(), window_step_mma_kernel<128, 4>);
     }
   }
   if (a.d <= 64) return step_g<T, 64>(a, p);
