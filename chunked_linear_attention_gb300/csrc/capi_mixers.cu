@@ -32,11 +32,13 @@ bool not_negative(const mixer_stride& s) { return s.batch >= 0 && s.token >= 0; 
 int io_bytes(int io) { return io == TTT_BF16 ? 2 : 4; }
 
 // ---------------------------------------------------------------- attention
-int check_window(int B, int Hq, int Hk, int N, int d, int window, int sinks, int io) {
+int check_window(int B, int Hq, int Hk, int N, int d, int window, int sinks, int io, bool cache) {
   if (B <= 0 || Hq <= 0 || Hk <= 0 || N <= 0 || d <= 0 || Hq % Hk != 0) return TTT_ERR_SHAPE;
   if (window <= 0 || sinks < 0) return TTT_ERR_SHAPE;
   if (io != TTT_F32 && io != TTT_BF16) return TTT_ERR_ARG;
-  if (d > 256 || window > (1 << 30) || sinks > (1 << 30)) return TTT_ERR_UNSUPPORTED;
+  if (d > 256 || window > (1 << 30) || sinks > (1 << 30) ||
+      (cache && (long long)window + sinks > 1 << 30))
+    return TTT_ERR_UNSUPPORTED;
   return TTT_OK;
 }
 
@@ -72,7 +74,8 @@ int check_rows(int n_seq, int B, int N, int D, int io) {
   if (B <= 0 || N <= 0 || D <= 0 || n_seq <= 0) return TTT_ERR_SHAPE;
   if (B != 1 && n_seq != B) return TTT_ERR_SHAPE;
   if (io != TTT_F32 && io != TTT_BF16) return TTT_ERR_ARG;
-  if (B > 65535 || D > 32768 || n_seq > (1 << 20) || (long long)B * N > (1LL << 31) - 1)
+  if (B > 65535 || D > 32768 || n_seq > (1 << 20) || N > (1 << 30) ||
+      (long long)B * N > (1LL << 31) - 1)
     return TTT_ERR_UNSUPPORTED;
   return TTT_OK;
 }
@@ -117,7 +120,7 @@ int window_attention_forward(const void* q, const void* k, const void* v, void* 
   if (!q || !k || !v || !out) return TTT_ERR_NULL;
   if ((cache_k != nullptr) != (cache_v != nullptr)) return TTT_ERR_NULL;
   if (!cache_k && (past || slots)) return TTT_ERR_NULL;
-  int rc = check_window(B, Hq, Hk, N, d, window, sinks, io_dtype);
+  int rc = check_window(B, Hq, Hk, N, d, window, sinks, io_dtype, cache_k != nullptr);
   if (rc != TTT_OK) return rc;
   if (n_seq <= 0 || (seq_starts ? B != 1 : n_seq != B)) return TTT_ERR_SHAPE;
   if (cache_k && (n_slots <= 0 || (!slots && n_slots < n_seq))) return TTT_ERR_SHAPE;
@@ -156,7 +159,7 @@ int window_attention_step(const void* q, const void* k, const void* v, void* cac
                           float scale, const window_attention_layout* layout, void* out,
                           ttt_stream_t stream) {
   if (!q || !k || !v || !cache_k || !cache_v || !positions || !out) return TTT_ERR_NULL;
-  int rc = check_window(B, Hq, Hk, 1, d, window, sinks, io_dtype);
+  int rc = check_window(B, Hq, Hk, 1, d, window, sinks, io_dtype, true);
   if (rc != TTT_OK) return rc;
   if (n_slots <= 0 || (!slots && n_slots < B)) return TTT_ERR_SHAPE;
   if ((long long)Hq * B > (1 << 20) || B > 65535) return TTT_ERR_UNSUPPORTED;

@@ -80,7 +80,8 @@ typedef struct {
  * throughout.  What a token does not see does not reach it, NaN and infinity
  * included.
  * Supported: d <= 256, Hq * B and Hq * n_seq at most 65535, N at most 2^30, B * N
- * below 2^31, window and sinks at most 2^30.  The caches must be 16-byte aligned. */
+ * below 2^31, window and sinks at most 2^30, with caches together.  The caches must
+ * be 16-byte aligned. */
 int window_attention_forward(const void* q, const void* k, const void* v, void* cache_k,
                              void* cache_v, const int* slots, int n_slots, const int* past,
                              const int* seq_starts, int n_seq, int B, int Hq, int Hk, int N, int d,
@@ -98,8 +99,13 @@ int window_attention_forward(const void* q, const void* k, const void* v, void* 
  *   slots       see above.
  *   out         overlaps no other tensor.
  *
- * Computed in fp32 for both I/O types.  Supported: d <= 256, B <= 65535, Hq * B
- * at most 2^20.  The caches must be 16-byte aligned. */
+ * Scores, their softmax and the sums are fp32.  TTT_BF16 with d <= 128 and a
+ * multiple of 8, and k and v 16-byte aligned with strides that are multiples of
+ * 8 elements, takes the products through the tensor cores, with each weight as
+ * two bf16 numbers (off by 2^-17); where a value that the token sees is
+ * infinite, its column is NaN or infinite there.
+ * Supported: d <= 256, B <= 65535, Hq * B at most 2^20, window + sinks at most
+ * 2^30.  The caches must be 16-byte aligned. */
 int window_attention_step(const void* q, const void* k, const void* v, void* cache_k,
                           void* cache_v, const int* positions, const int* slots, int n_slots,
                           int B, int Hq, int Hk, int d, int window, int sinks, int io_dtype,
@@ -145,7 +151,7 @@ size_t selective_scan_workspace_size(int B, int N, int D, int S, int G, int n_se
  *               not shared with a concurrent call.
  *
  * Computed in fp32 for both I/O types.  Supported: S <= 128, D <= 32768,
- * B <= 65535, B * N below 2^31, n_seq at most 2^20. */
+ * B <= 65535, N at most 2^30, B * N below 2^31, n_seq at most 2^20. */
 int selective_scan_forward(const void* x, const void* dt, const float* A, const void* Bm,
                            const void* Cm, const float* Dx, const float* dt_bias, const void* z,
                            const float* state_in, const int* seq_starts, int n_seq, int B, int N,
@@ -190,8 +196,8 @@ typedef struct {
  *   state_out   [n_seq, W - 1, D] in io_dtype, the last inputs of each sequence
  *               with its state in front, or NULL.  Overlaps no other tensor.
  *
- * Computed in fp32.  Supported: 2 <= W <= 8, D <= 32768, B <= 65535,
- * B * N below 2^31, n_seq at most 2^20. */
+ * Computed in fp32.  Supported: 2 <= W <= 8, D <= 32768, B <= 65535, N at most
+ * 2^30, B * N below 2^31, n_seq at most 2^20. */
 int short_conv_forward(const void* x, const float* w, const float* bias, const void* state_in,
                        const int* seq_starts, int n_seq, int B, int N, int D, int W, int io_dtype,
                        int silu, const short_conv_layout* layout, void* out, void* state_out,

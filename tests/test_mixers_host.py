@@ -193,3 +193,19 @@ def test_bindings_refuse_tensors_of_the_host(cla):
                  lambda: cla.short_conv_step(x[0], w, torch.zeros(8, 3, 64))):
         with pytest.raises(ValueError, match="CUDA device"):
             call()
+
+
+def test_sizes_past_32_bit_arithmetic(cla):
+    """A cache of more than 2^30 places, and a token axis of more than 2^30."""
+    half = 1 << 29
+    for step in (window, window_step):
+        assert step(cla, window=half + 1, sinks=half) == TTT_ERR_UNSUPPORTED
+        assert step(cla, window=1 << 30, sinks=1) == TTT_ERR_UNSUPPORTED
+        assert step(cla, window=1 << 30, sinks=1 << 30) == TTT_ERR_UNSUPPORTED
+        if not torch.cuda.is_available():
+            assert step(cla, window=half, sinks=half) == TTT_ERR_CUDA
+    no_cache = dict(window=1 << 30, sinks=1 << 30, cache=False, slots=False, past=False)
+    if not torch.cuda.is_available():
+        assert window(cla, **no_cache) == TTT_ERR_CUDA
+    for call in (scan, conv):
+        assert call(cla, N=(1 << 30) + 1, B=1) == TTT_ERR_UNSUPPORTED
