@@ -4,10 +4,16 @@
 //
 // The channels are independent; so are the numbers of a state until y sums over them.
 // A thread holds CPT neighbouring channels x SPT numbers of the state, and L lanes one
-// channel's state; B and C of some tokens are in shared memory as fp32, for all channels
-// of a group.  With A' = A log2(e) each element of the state costs one base-2 exponential
-// and four fp32 operations, issued in pairs: the exponentials (32 a clock and SM) and
-// the fp32 pipe (128) are full at the same time.
+// channel's state.  Per token four warps run the recurrence on r, r x, B and C as fp32 in
+// shared memory; four others bring the next tile of them there and turn the last tile's sums
+// into outputs (one kind of warp for both, 1048 us where this takes 838).  With A' = A
+// log2(e) each element of the state costs one base-2 exponential and four fp32 operations,
+// issued in pairs.
+//
+// What bounds it: issue.  2 x 32768 tokens of 1536 x 16, bf16: 838 us, the carry 1/3 of them;
+// the exponentials of both passes alone would take 344 us (32 a clock and SM), the bytes of
+// the output pass 119.  A (token, channel) takes 84 lane-instructions of the carry and 124 of
+// the outputs, and 62% of the clocks issue one a scheduler.
 //
 // Few long sequences would leave most of the card idle (a token follows the one
 // before), so the token axis is cut into segments.  A segment maps the state that it
@@ -15,7 +21,7 @@
 // zero; the carry pass finds l and R for all segments at once, the join pass the states at
 // the segments' starts one after the other, and the output pass runs all segments at
 // once.  The carry makes every exponential twice; it is taken where the channels alone
-// do not fill the card.
+// do not fill the card (scan_shape).
 //
 // Packed sequences lie on the token axis as they are: a segment in which a sequence
 // begins ends with a state that knows nothing of what came before the segment.
@@ -527,7 +533,9 @@ ScanShape scan_shape(int B, int N, int D, int S, int G) {
   ScanShape s;
   // Many channels and tokens: four channels a thread, so that each number of B and C from
   // shared memory serves four.  Otherwise one channel over S / 4 lanes, so that a token takes
-  // little time.
+  // little time.  (S 16, 2048 tokens of 1536 channels: 60 us against 90; 1024 of 1024: 46
+  // and 39.  Groups of 64 channels leave half of the first kind's threads idle: 8192 tokens
+  // of 24 groups 401 us against 324.)
   const long long work = (long long)B * N * D;
   const bool wide = work >= 1 << 21 && D / G >= 128;
   s.cpt = wide ? 4 : 1;
@@ -536,12 +544,15 @@ ScanShape scan_shape(int B, int N, int D, int S, int G) {
   while (s.spt * s.lanes < S) s.lanes *= 2;
   const int ch = kScanThreads / s.lanes * s.cpt;
   s.blocks = (D / G + ch - 1) / ch;
-  // one round of CTAs, two on every SM; no segment shorter than 64 tokens
+  // One round of CTAs, two on every SM.  The carry costs 2/3 of an output pass, so that two
+  // segments of half the length pay already (25 sequences of 8000 x 1536: 2457 us, whole
+  // 2697).  No segment shorter than 32 tokens (1024 tokens of 2048 channels 49 us; 64: 59,
+  // 128: 95).
   const long long ctas = (long long)B * G * s.blocks, room = 2 * kScanSms;
   long long segs = room / ctas;
-  const long long most = (N + 63) / 64;
+  const long long most = (N + 31) / 32;
   if (segs > most) segs = most;
-  if (segs < 3) segs = 1;   // two segments carry as long as one runs
+  if (segs < 1) segs = 1;
   s.seg_tokens = (int)(((N + segs - 1) / segs + 15) / 16 * 16);   // whole tiles
   s.segs = (N + s.seg_tokens - 1) / s.seg_tokens;
   return s;
@@ -723,8 +734,9 @@ int launch_scan_step(const ScanStepArgs& a, const ScanStepParams& p) {
   const bool vec = a.S == 4 * L && a.D % per == 0 && ok(a.state, 16) && ok(a.A, 16) &&
                    ok(a.Bm, 4 * sizeof(T)) && ok(a.Cm, 4 * sizeof(T)) && a.lay.B.batch % 4 == 0 &&
                    a.lay.C.batch % 4 == 0;
-  // four rows a thread where that leaves every SM two blocks
-  const int R = (long long)((a.D + per - 1) / per) * ((a.B + 3) / 4) >= 2 * kScanSms ? 4 : 1;
+  // four rows a thread where that leaves every SM four blocks (states of 4096 x 16: 32 rows
+  // 6.4 us, one row a thread 7.4; 16 rows 5.8 and 5.0)
+  const int R = (long long)((a.D + per - 1) / per) * ((a.B + 3) / 4) >= 4 * kScanSms ? 4 : 1;
   const dim3 grid((a.D + per - 1) / per, (a.B + R - 1) / R);
   void (*kern)(ScanStepParams) =
       R == 4 ? (vec ? scan_step_kernel<T, L, 4, true> : scan_step_kernel<T, L, 4, false>)
