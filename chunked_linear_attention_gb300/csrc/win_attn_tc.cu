@@ -1,8 +1,8 @@
 // Window attention on the tensor cores: bf16, d <= 128.
 //
 // A block has 256 queries of one head, as two tiles of 128 rows that share the key tiles
-// of 128 (win_attn.cuh has the list).  Per key tile and query tile
-//     S = Q K^T      (128 x 128, fp32 in TMEM)
+// of 64 (win_attn.cuh has the list).  Per key tile and query tile
+//     S = Q K^T      (128 x 64, fp32 in TMEM)
 //     P = exp2(c S - c m),  l += sum P     (c = scale log2 e; one thread per row)
 //     O += P V       (P as bf16 in the TMEM columns that S had)
 // with m the row's largest score so far.  O and l are only rescaled, in TMEM, when that has
@@ -10,16 +10,25 @@
 // large, and so are their sums.  P is rounded to bf16 (2^-8 of each weight) as the operand
 // of the second product; l sums what was not rounded.
 //
-// What bounds it: per pair of tiles the products take 1024 clocks of the tensor core
-// (d 128) and the exponentials 1024 of the special-function units (32 a clock), so
-// the two tiles work in turn: while one's products run, the other's weights are made.
+// S lies in two buffers a query tile: while the rows make the weights of one, the products
+// fill the other.  Key tiles of 128 with one buffer leave a tile's products and rows waiting
+// for one another (2 x 32768 tokens of 12 heads of 128 on 4 key heads, window 2048: 800 us,
+// with a product warp for both query tiles 764); of 64 with one product warp 1080 (2780 clocks
+// an entry of its own instructions), with one a query tile 780 - 795, and the packed and
+// ragged prompts gain 9% from the smaller tiles.
+//
+// What bounds it: 2 x 32768 tokens as above run at 1.05 PFLOP/s, 54% of the tensor cores'
+// measured rate.  Per pair of query tiles and 64 keys the products take 1280 clocks (S 384
+// each, N 64 being bound by the operands' shared memory, and O 256) and the exponentials 512
+// (32 a clock); the rest are the hand-overs and the rows' other instructions: scores from TMEM
+// and weights into it, maxima, sums, conversions.
 //
 // A value that a query does not see still meets its weight 0 in P V, where NaN or
 // infinity would spoil the row.  So outputs that are not finite are computed again, from
 // the keys that the row sees alone (which leaves what is really NaN or infinite).
 //
 // Roles (384 threads, one block per SM, persistent over (tile pair, head)):
-//   warp 0      TMA: Q, and K and V through a ring of tiles.
+//   warp 0      TMA: Q, and K and V of a key tile together through a ring.
 //   warps 1, 3  the products of the first and of the second query tile.
 //   warp 2      the list of key tiles, for all others.
 //   warps 4-7   rows of the first tile, warps 8-11 of the second: softmax, rescaling,

@@ -73,7 +73,7 @@ typedef struct {
  *   layout      HOST pointer or NULL.
  *   out         overlaps no other tensor, nor its rows one another.
  *
- * io_dtype TTT_BF16 with d <= 128 and a multiple of 8, and q, k, v 16-byte
+ * io_dtype TTT_BF16 with scale > 0, d <= 128 and a multiple of 8, and q, k, v 16-byte
  * aligned with strides that are multiples of 8 elements (and not 0), runs on the
  * tensor cores: scores, their softmax and the sums are fp32, the weights are
  * rounded to bf16 for the product with v.  All other calls run in fp32
