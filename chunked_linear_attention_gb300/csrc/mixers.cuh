@@ -60,6 +60,38 @@ __device__ __forceinline__ int row_slot(const int* slots, int n_slots, int b, in
   return bad ? -1 : slot;
 }
 
+// The same for rows b0 .. b0 + R - 1 of one block, in two parts: what a thread reads from the
+// pool between them (of slots inside it) is on its way meanwhile.
+template <int R>
+__device__ __forceinline__ void read_slots(const int* slots, int b0, int B, int (&slot)[R]) {
+#pragma unroll
+  for (int i = 0; i < R; ++i) slot[i] = b0 + i < B ? (slots ? slots[b0 + i] : b0 + i) : -1;
+}
+template <int R>
+__device__ __forceinline__ void drop_bad_slots(const int* slots, int n_slots, int b0, int B,
+                                               int* status, int (&slot)[R]) {
+  if (!slots) return;
+  __shared__ unsigned taken;
+  if (threadIdx.x == 0) taken = 0u;
+  __syncthreads();
+  unsigned bad = 0u;
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (slot[i] >= n_slots) bad |= 1u << i;
+  for (int e = threadIdx.x; e < min(b0 + R - 1, B); e += blockDim.x) {
+    const int other = slots[e];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (slot[i] >= 0 && other == slot[i] && e < b0 + i) bad |= 1u << i;
+  }
+  if (bad) atomicOr(&taken, bad);
+  __syncthreads();
+  if (taken && threadIdx.x == 0) report_status(status, kStatusBadArg);
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if ((taken >> i) & 1) slot[i] = -1;
+}
+
 // e^x through the base-2 exponential: off by 2^-22 and |x| 2^-24 (the product's rounding).
 __device__ __forceinline__ float exp_f(float x) { return ex2(x * 1.44269504088896341f); }
 

@@ -644,44 +644,31 @@ template <typename T, int L, int R, bool VEC>
 __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ ScanStepParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ unsigned taken;
   const int b0 = blockIdx.y * R, l = threadIdx.x % L;
   const int c = blockIdx.x * (128 / L) + threadIdx.x / L;
   const bool in = c < p.D;
   int slot[R];
-#pragma unroll
-  for (int i = 0; i < R; ++i)
-    slot[i] = b0 + i < p.B ? (p.slots ? p.slots[b0 + i] : b0 + i) : -1;
-  if (p.slots) {   // slots outside the pool and ones that an earlier row uses
-    if (threadIdx.x == 0) taken = 0u;
-    __syncthreads();
-    unsigned bad = 0u;
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (slot[i] >= p.n_slots) bad |= 1u << i;
-    for (int e = threadIdx.x; e < min(b0 + R - 1, p.B); e += 128) {
-      const int other = p.slots[e];
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (slot[i] >= 0 && other == slot[i] && e < b0 + i) bad |= 1u << i;
-    }
-    if (bad) atomicOr(&taken, bad);
-    __syncthreads();
-    if (taken && threadIdx.x == 0) report_status(p.status, kStatusBadArg);
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-      if ((taken >> i) & 1) slot[i] = -1;
-  }
+  read_slots<R>(p.slots, b0, p.B, slot);
+  // everything is on its way before the slots are compared with other rows'
   const int g = in ? c / (p.D / p.G) : 0, s0 = l * 4;
   const int n = in ? max(0, min(4, p.S - s0)) : 0;
   float h[R][4], a[4];
   float xv[R], r[R], zv[R];
+  constexpr bool kEarly = R == 1;
+  Pack<T, 4> Bq[R], Cq[R];
+  auto load_bc = [&](int i) {
+    const T* Bm = static_cast<const T*>(p.Bm) + (b0 + i) * p.lay.B.batch + (long long)g * p.S;
+    const T* Cm = static_cast<const T*>(p.Cm) + (b0 + i) * p.lay.C.batch + (long long)g * p.S;
+    load_pack<T, 4, VEC>(Bm + s0, n, Bq[i]);
+    load_pack<T, 4, VEC>(Cm + s0, n, Cq[i]);
+  };
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int b = b0 + i;
     xv[i] = r[i] = zv[i] = 0.f;
-    if (slot[i] < 0) continue;
+    if (slot[i] < 0 || slot[i] >= p.n_slots) continue;
     load_row<float, 4, VEC>(p.state + ((long long)slot[i] * p.D + c) * p.S + s0, n, h[i]);
+    if (kEarly) load_bc(i);
     if (in) {
       xv[i] = to_f<T>(static_cast<const T*>(p.x)[b * p.lay.x.batch + c]);
       r[i] = to_f<T>(static_cast<const T*>(p.dt)[b * p.lay.dt.batch + c]);
@@ -690,6 +677,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ 
   }
   load_row<float, 4, VEC>(p.A + (long long)c * p.S + s0, n, a);
   const float bias = in && p.dt_bias ? p.dt_bias[c] : 0.f, dx = in && p.Dx ? p.Dx[c] : 0.f;
+  drop_bad_slots<R>(p.slots, p.n_slots, b0, p.B, p.status, slot);
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int b = b0 + i;
@@ -699,11 +687,10 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ 
       if (in && l == 0) *out = from_f<T>(0.f);
       continue;
     }
-    const T* Bm = static_cast<const T*>(p.Bm) + b * p.lay.B.batch + (long long)g * p.S;
-    const T* Cm = static_cast<const T*>(p.Cm) + b * p.lay.C.batch + (long long)g * p.S;
     float rr = r[i] + bias, acc = 0.f, Bv[4], Cv[4];
-    load_row<T, 4, VEC>(Bm + s0, n, Bv);
-    load_row<T, 4, VEC>(Cm + s0, n, Cv);
+    if (!kEarly) load_bc(i);
+    pack_f(Bq[i], Bv);
+    pack_f(Cq[i], Cv);
     if (p.softplus) {
       float none = 0.f;
       softplus2(rr, none);

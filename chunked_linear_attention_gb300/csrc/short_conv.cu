@@ -239,64 +239,119 @@ struct ConvStepParams {
   const int* slots;
   void* out;
   int* status;
-  int n_slots, D, W, silu;
+  int n_slots, B, D, silu;
   short_conv_layout lay;
 };
 
-// One CTA: 128 E channels of one row.
-template <typename T, int E, bool VEC>
+// One CTA: 128 E channels of R rows, whose states and inputs are on their way together; the
+// filters, in registers, serve all of them.
+template <typename T, int W, int E, int R, bool VEC>
 __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ ConvStepParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int b = blockIdx.y, c = (blockIdx.x * 128 + threadIdx.x) * E;
-  const int slot = row_slot(p.slots, p.n_slots, b, p.status);
-  if (c >= p.D) return;
-  const int n = VEC ? E : min(E, p.D - c);
-  T* out = static_cast<T*>(p.out) + b * p.lay.out.batch + c;
-  float y[E];
-  if (slot < 0) {
+  const int b0 = blockIdx.y * R, c = (blockIdx.x * 128 + threadIdx.x) * E;
+  const int n = VEC ? (c < p.D ? E : 0) : max(0, min(E, p.D - c));
+  int slot[R];
+  read_slots<R>(p.slots, b0, p.B, slot);
+  using V = Pack<T, E>;
+  V h[R][W - 1], x[R];
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = 0.f;
+  for (int i = 0; i < R; ++i) {
+    if (n == 0 || slot[i] < 0 || slot[i] >= p.n_slots) continue;
+    load_pack<T, E, VEC>(static_cast<const T*>(p.x) + (b0 + i) * p.lay.x.batch + c, n, x[i]);
+    const T* st = static_cast<const T*>(p.state) + (long long)slot[i] * (W - 1) * p.D + c;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) load_pack<T, E, VEC>(st + (long long)j * p.D, n, h[i][j]);
+  }
+  float w[E * W], bias[E];
+  const float* from = p.w + (long long)c * W;
+  if constexpr (VEC) {
+    constexpr int P = E * W % 4 == 0 ? 4 : 2;
+    using Q = Pack<float, P>;
+    if (n > 0) {
+#pragma unroll
+      for (int e = 0; e < E * W; e += P) {
+        const Q q = *reinterpret_cast<const Q*>(from + e);
+#pragma unroll
+        for (int k = 0; k < P; ++k) w[e + k] = q.v[k];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E * W; ++e) w[e] = e < n * W ? from[e] : 0.f;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) bias[e] = p.bias && e < n ? p.bias[c + e] : 0.f;
+  drop_bad_slots<R>(p.slots, p.n_slots, b0, p.B, p.status, slot);
+  if (n == 0) return;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (b0 + i >= p.B) return;
+    T* out = static_cast<T*>(p.out) + (b0 + i) * p.lay.out.batch + c;
+    float y[E], v[E];
+    if (slot[i] < 0) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = 0.f;
+      store_row<T, E, VEC>(out, n, y);
+      continue;
+    }
+    pack_f(x[i], v);
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] = fmaf(w[e * W + W - 1], v[e], bias[e]);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      pack_f(h[i][j], v);
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = fmaf(w[e * W + j], v[e], y[e]);
+    }
+    if (p.silu) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = silu_f(y[e]);
+    }
     store_row<T, E, VEC>(out, n, y);
-    return;
-  }
-  float v[E];
-  load_row<T, E, VEC>(static_cast<const T*>(p.x) + b * p.lay.x.batch + c, n, v);
-  const float* w = p.w + (long long)c * p.W;
+    T* st = static_cast<T*>(p.state) + (long long)slot[i] * (W - 1) * p.D + c;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    y[e] = p.bias && e < n ? p.bias[c + e] : 0.f;
-    if (e < n) y[e] = fmaf(w[e * p.W + p.W - 1], v[e], y[e]);
-  }
-  T* st = static_cast<T*>(p.state) + (long long)slot * (p.W - 1) * p.D + c;
-  for (int j = 0; j < p.W - 1; ++j) {
-    float h[E];
-    load_row<T, E, VEC>(st + (long long)j * p.D, n, h);
+    for (int j = 1; j < W; ++j) {
+      const V& q = j < W - 1 ? h[i][j] : x[i];
+      if constexpr (VEC) {
+        *reinterpret_cast<V*>(st + (long long)(j - 1) * p.D) = q;
+      } else {
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (e < n) y[e] = fmaf(w[e * p.W + j], h[e], y[e]);
-    if (j > 0) store_row<T, E, VEC>(st + (long long)(j - 1) * p.D, n, h);
+        for (int e = 0; e < E; ++e)
+          if (e < n) st[(long long)(j - 1) * p.D + e] = q.v[e];
+      }
+    }
   }
-  store_row<T, E, VEC>(st + (long long)(p.W - 2) * p.D, n, v);
-  if (p.silu) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = silu_f(y[e]);
-  }
-  store_row<T, E, VEC>(out, n, y);
+}
+
+template <typename T, int W>
+int conv_step_w(const ConvStepArgs& a, const ConvStepParams& p) {
+  constexpr int E = 8 / sizeof(T);
+  const bool vec = a.D % E == 0 && wide(a.x, 8) && wide(a.out, 8) && wide(a.state, 8) &&
+                   wide(a.w, 16) && a.lay.x.batch % E == 0 && a.lay.out.batch % E == 0;
+  const int per = 128 * (vec ? E : 1);
+  const unsigned blocks = (a.D + per - 1) / per;
+  const bool four = vec && (long long)blocks * ((a.B + 3) / 4) >= 152;
+  const dim3 grid(blocks, four ? (a.B + 3) / 4 : a.B);
+  const double n = (double)a.B * a.D;
+  ProfScope ps(PT_CONV_STEP, a.stream, 2.0 * n * W, 2.0 * n * W * sizeof(T));
+  void (*kern)(ConvStepParams) = four  ? conv_step_kernel<T, W, E, 4, true>
+                                 : vec ? conv_step_kernel<T, W, E, 1, true>
+                                       : conv_step_kernel<T, W, 1, 1, false>;
+  return launch_grid(kern, grid, 128, 0, a.stream, p) == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 
 template <typename T>
 int conv_step_t(const ConvStepArgs& a, const ConvStepParams& p) {
-  constexpr int E = 8 / sizeof(T);
-  const bool vec = a.D % E == 0 && wide(a.x, 8) && wide(a.out, 8) && wide(a.state, 8) &&
-                   a.lay.x.batch % E == 0 && a.lay.out.batch % E == 0;
-  const int per = 128 * (vec ? E : 1);
-  const dim3 grid((a.D + per - 1) / per, a.B);
-  const double n = (double)a.B * a.D;
-  ProfScope ps(PT_CONV_STEP, a.stream, 2.0 * n * a.W, 2.0 * n * a.W * sizeof(T));
-  const cudaError_t e = vec ? launch_grid(conv_step_kernel<T, E, true>, grid, 128, 0, a.stream, p)
-                            : launch_grid(conv_step_kernel<T, 1, false>, grid, 128, 0, a.stream, p);
-  return e == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
+  switch (a.W) {
+    case 2: return conv_step_w<T, 2>(a, p);
+    case 3: return conv_step_w<T, 3>(a, p);
+    case 4: return conv_step_w<T, 4>(a, p);
+    case 5: return conv_step_w<T, 5>(a, p);
+    case 6: return conv_step_w<T, 6>(a, p);
+    case 7: return conv_step_w<T, 7>(a, p);
+    default: return conv_step_w<T, 8>(a, p);
+  }
 }
 
 }  // namespace
@@ -320,7 +375,7 @@ int short_conv_step_launch(const ConvStepArgs& a) {
   p.slots = a.slots;
   p.out = a.out;
   p.status = a.status;
-  p.n_slots = a.n_slots; p.D = a.D; p.W = a.W; p.silu = a.silu;
+  p.n_slots = a.n_slots; p.B = a.B; p.D = a.D; p.silu = a.silu;
   p.lay = a.lay;
   return a.bf16 ? conv_step_t<__nv_bfloat16>(a, p) : conv_step_t<float>(a, p);
 }

@@ -1,5 +1,7 @@
 // Attention with a sliding window and sinks in fp32, for every type, size and stride, and
 // the writing of new keys and values into the caches.
+#include <algorithm>
+
 #include "prof.h"
 #include "win_attn.cuh"
 
@@ -352,10 +354,11 @@ int window_attention_store(const WindowArgs& a) {
   p.sk = a.lay.k; p.sv = a.lay.v;
   const int per = a.bf16 ? 8 : 4;
   const bool vec = rows_wide(a.k, p.sk, a.d, per) && rows_wide(a.v, p.sv, a.d, per);
-  // about eight rows of 16 bytes a thread for a full cache
+  // two pieces of 16 bytes a thread for a full cache, and some ten blocks a SM at most
   const long long most = a.N < (long long)a.window + a.sinks ? a.N : (long long)a.window + a.sinks;
-  long long parts = most * a.d / per / 2048 + 1;
-  p.parts = (int)(parts > 64 ? 64 : parts);
+  const long long parts = most * a.d / per / 512 + 1;
+  const long long room = std::max(64ll, 1536ll / ((long long)a.n_seq * a.Hk));
+  p.parts = (int)std::min(parts, room);
   const dim3 grid(p.parts, (unsigned)(a.n_seq * a.Hk));
   const double bytes = 4.0 * (double)a.n_seq * a.Hk * most * a.d * (a.bf16 ? 2 : 4);
   ProfScope ps(PT_WIN_STORE, a.stream, 0.0, bytes);
