@@ -636,11 +636,16 @@ struct ScanStepParams {
   selective_scan_layout lay;
 };
 
-// Four numbers of a state a thread, L lanes a channel, R rows of the batch; bound by HBM,
-// the states' bytes twice.  With four rows a thread has 64 bytes on their way, and A and the
-// check of the slots serve all four: 250 rows of 4096 x 16 take 34 us, one row a thread 44;
-// up to 32 rows a block, two at a time with the next two on their way, 55 (fewer blocks).
-template <typename T, int L, int R, bool VEC>
+// L lanes a channel, each K pieces of four numbers of its state, R rows of the batch a thread;
+// bound by HBM, the states' bytes twice.  250 rows of 4096 x 16: 25 us (131 MB there and
+// back, 5.3 TB/s); 1000 rows, whose states pass the L2, 122 us.  Both what is on its way and
+// the instructions count: the step, the gate, the skip and the sum over the lanes are for a
+// channel, so that one piece a lane (four rows a thread: 34 and 174 us) makes them twice as
+// often; two pieces and four rows 29 and 143, four pieces of one lane 32 and 132.  With 64
+// numbers four pieces and one row are ahead (1000 rows of 2048: 192 us, two pieces and two
+// rows 229).
+enum ScanPieces { kAnySize, kPieces, kAllPieces };   // S: any; a multiple of 4; 4 L K
+template <typename T, int L, int K, int R, ScanPieces P>
 __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ ScanStepParams p) {
   pdl_launch_dependents();
   pdl_wait();
@@ -650,32 +655,43 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ 
   int slot[R];
   read_slots<R>(p.slots, b0, p.B, slot);
   // everything is on its way before the slots are compared with other rows'
-  const int g = in ? c / (p.D / p.G) : 0, s0 = l * 4;
-  const int n = in ? max(0, min(4, p.S - s0)) : 0;
-  float h[R][4], a[4];
+  const int g = in ? c / (p.D / p.G) : 0;
+  constexpr bool VEC = P != kAnySize;
+  // numbers 4 (l + L k) .. + 3 of the state, `n` of them below S
+  auto first = [&](int k) { return 4 * (l + L * k); };
+  auto n = [&](int k) { return P == kAllPieces ? 4 : in ? max(0, min(4, p.S - first(k))) : 0; };
+  float h[R][K][4], a[K][4];
   float xv[R], r[R], zv[R];
-  constexpr bool kEarly = R == 1;
-  Pack<T, 4> Bq[R], Cq[R];
+  Pack<T, 4> Bq[R][K], Cq[R][K];
   auto load_bc = [&](int i) {
     const T* Bm = static_cast<const T*>(p.Bm) + (b0 + i) * p.lay.B.batch + (long long)g * p.S;
     const T* Cm = static_cast<const T*>(p.Cm) + (b0 + i) * p.lay.C.batch + (long long)g * p.S;
-    load_pack<T, 4, VEC>(Bm + s0, n, Bq[i]);
-    load_pack<T, 4, VEC>(Cm + s0, n, Cq[i]);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (n(k) == 0) continue;
+      load_pack<T, 4, VEC>(Bm + first(k), n(k), Bq[i][k]);
+      load_pack<T, 4, VEC>(Cm + first(k), n(k), Cq[i][k]);
+    }
   };
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int b = b0 + i;
     xv[i] = r[i] = zv[i] = 0.f;
     if (slot[i] < 0 || slot[i] >= p.n_slots) continue;
-    load_row<float, 4, VEC>(p.state + ((long long)slot[i] * p.D + c) * p.S + s0, n, h[i]);
-    if (kEarly) load_bc(i);
+    const float* st = p.state + ((long long)slot[i] * p.D + c) * p.S;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (n(k) > 0) load_row<float, 4, VEC>(st + first(k), n(k), h[i][k]);
+    load_bc(i);
     if (in) {
       xv[i] = to_f<T>(static_cast<const T*>(p.x)[b * p.lay.x.batch + c]);
       r[i] = to_f<T>(static_cast<const T*>(p.dt)[b * p.lay.dt.batch + c]);
       if (p.z) zv[i] = to_f<T>(static_cast<const T*>(p.z)[b * p.lay.z.batch + c]);
     }
   }
-  load_row<float, 4, VEC>(p.A + (long long)c * p.S + s0, n, a);
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    if (n(k) > 0) load_row<float, 4, VEC>(p.A + (long long)c * p.S + first(k), n(k), a[k]);
   const float bias = in && p.dt_bias ? p.dt_bias[c] : 0.f, dx = in && p.Dx ? p.Dx[c] : 0.f;
   drop_bad_slots<R>(p.slots, p.n_slots, b0, p.B, p.status, slot);
 #pragma unroll
@@ -687,21 +703,25 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ 
       if (in && l == 0) *out = from_f<T>(0.f);
       continue;
     }
-    float rr = r[i] + bias, acc = 0.f, Bv[4], Cv[4];
-    if (!kEarly) load_bc(i);
-    pack_f(Bq[i], Bv);
-    pack_f(Cq[i], Cv);
+    float rr = r[i] + bias, acc = 0.f;
     if (p.softplus) {
       float none = 0.f;
       softplus2(rr, none);
     }
+    float* st = p.state + ((long long)slot[i] * p.D + c) * p.S;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      h[i][e] = fmaf(ex2(rr * (a[e] * kLog2e)), h[i][e], rr * xv[i] * Bv[e]);
-      acc = fmaf(Cv[e], h[i][e], acc);
+    for (int k = 0; k < K; ++k) {
+      if (n(k) == 0) continue;
+      float Bv[4], Cv[4];
+      pack_f(Bq[i][k], Bv);
+      pack_f(Cq[i][k], Cv);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        h[i][k][e] = fmaf(ex2(rr * (a[k][e] * kLog2e)), h[i][k][e], rr * xv[i] * Bv[e]);
+        acc = fmaf(Cv[e], h[i][k][e], acc);
+      }
+      store_row<float, 4, VEC>(st + first(k), n(k), h[i][k]);
     }
-    if (n > 0)
-      store_row<float, 4, VEC>(p.state + ((long long)slot[i] * p.D + c) * p.S + s0, n, h[i]);
     acc = sum_over<L>(acc);
     if (in && l == 0) {
       acc = fmaf(dx, xv[i], acc);
@@ -711,34 +731,42 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ 
   }
 }
 
-template <typename T, int L>
+template <typename T, int L, int K>
 int launch_scan_step(const ScanStepArgs& a, const ScanStepParams& p) {
   const int per = 128 / L;
   const double n = (double)a.B * a.D * a.S;
   ProfScope ps(PT_SCAN_STEP, a.stream, 6.0 * n, 8.0 * n);
-  // the lanes' four numbers lie in one 16-byte piece where S is 4 L; those of B and C too
+  // four numbers lie in one 16-byte piece where S is a multiple of 4; those of B and C too
   auto ok = [](const void* x, unsigned bytes) { return (reinterpret_cast<uintptr_t>(x) & (bytes - 1)) == 0; };
-  const bool vec = a.S == 4 * L && a.D % per == 0 && ok(a.state, 16) && ok(a.A, 16) &&
+  const bool vec = a.S % 4 == 0 && ok(a.state, 16) && ok(a.A, 16) &&
                    ok(a.Bm, 4 * sizeof(T)) && ok(a.Cm, 4 * sizeof(T)) && a.lay.B.batch % 4 == 0 &&
                    a.lay.C.batch % 4 == 0;
-  // four rows a thread where that leaves every SM four blocks (states of 4096 x 16: 32 rows
-  // 6.4 us, one row a thread 7.4; 16 rows 5.8 and 5.0)
-  const int R = (long long)((a.D + per - 1) / per) * ((a.B + 3) / 4) >= 4 * kScanSms ? 4 : 1;
+  const bool all = vec && a.S == 4 * L * K && a.D % per == 0;
+  // several rows a thread where that leaves every SM four blocks (states of 4096 x 16: 32
+  // rows 4.4 us, one row a thread 5.2; 8 rows 3.4 and 2.9)
+  constexpr int M = K == 1 ? 4 : K == 2 ? 2 : 1;
+  const int R = (long long)((a.D + per - 1) / per) * ((a.B + M - 1) / M) >= 4 * kScanSms ? M : 1;
   const dim3 grid((a.D + per - 1) / per, (a.B + R - 1) / R);
-  void (*kern)(ScanStepParams) =
-      R == 4 ? (vec ? scan_step_kernel<T, L, 4, true> : scan_step_kernel<T, L, 4, false>)
-             : (vec ? scan_step_kernel<T, L, 1, true> : scan_step_kernel<T, L, 1, false>);
+  void (*kern)(ScanStepParams) = all   ? scan_step_kernel<T, L, K, 1, kAllPieces>
+                                 : vec ? scan_step_kernel<T, L, K, 1, kPieces>
+                                       : scan_step_kernel<T, L, K, 1, kAnySize>;
+  if constexpr (M > 1) {
+    if (R == M)
+      kern = all   ? scan_step_kernel<T, L, K, M, kAllPieces>
+             : vec ? scan_step_kernel<T, L, K, M, kPieces>
+                   : scan_step_kernel<T, L, K, M, kAnySize>;
+  }
   return launch_grid(kern, grid, 128, 0, a.stream, p) == cudaSuccess ? TTT_OK : TTT_ERR_CUDA;
 }
 
 template <typename T>
 int scan_step_t(const ScanStepArgs& a, const ScanStepParams& p) {
-  if (a.S <= 4) return launch_scan_step<T, 1>(a, p);
-  if (a.S <= 8) return launch_scan_step<T, 2>(a, p);
-  if (a.S <= 16) return launch_scan_step<T, 4>(a, p);
-  if (a.S <= 32) return launch_scan_step<T, 8>(a, p);
-  if (a.S <= 64) return launch_scan_step<T, 16>(a, p);
-  return launch_scan_step<T, 32>(a, p);
+  if (a.S <= 4) return launch_scan_step<T, 1, 1>(a, p);
+  if (a.S <= 8) return launch_scan_step<T, 1, 2>(a, p);
+  if (a.S <= 16) return launch_scan_step<T, 2, 2>(a, p);
+  if (a.S <= 32) return launch_scan_step<T, 4, 2>(a, p);
+  if (a.S <= 64) return launch_scan_step<T, 4, 4>(a, p);
+  return launch_scan_step<T, 8, 4>(a, p);
 }
 
 }  // namespace

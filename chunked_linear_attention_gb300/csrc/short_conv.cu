@@ -331,6 +331,8 @@ int conv_step_w(const ConvStepArgs& a, const ConvStepParams& p) {
                    wide(a.w, 16) && a.lay.x.batch % E == 0 && a.lay.out.batch % E == 0;
   const int per = 128 * (vec ? E : 1);
   const unsigned blocks = (a.D + per - 1) / per;
+  // four rows a thread where every SM gets a block all the same (512 rows of 4096 channels
+  // 7.4 us, one row a thread 9.1; 128 rows 3.8 and 4.0)
   const bool four = vec && (long long)blocks * ((a.B + 3) / 4) >= 152;
   const dim3 grid(blocks, four ? (a.B + 3) / 4 : a.B);
   const double n = (double)a.B * a.D;
