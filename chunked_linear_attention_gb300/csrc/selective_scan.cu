@@ -505,21 +505,33 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const __grid_constant__ 
   const float* sum = p.seg_sum + (long long)b * p.segs * p.D + i / p.S;
   const int* fresh = p.seg_new + (long long)b * p.segs;
   float h = 0.f;
-  constexpr int U = 8;   // segments whose numbers are on their way together
-  for (int j = 0; j < p.segs - 1; j += U) {
-    float l[U], f[U];
+  constexpr int U = 16;   // segments whose numbers are on their way together, behind U others
+  struct Part {
+    float l[U], r[U];
+    int fresh[U];
+  };
+  auto fetch = [&](int j, Part& q) {
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const bool in = j + k < p.segs - 1;
-      l[k] = in ? st[(j + k) * one] : 0.f;
-      f[k] = in && !fresh[j + k] ? ex2(A * sum[(long long)(j + k) * p.D]) : 0.f;
+      q.l[k] = in ? st[(j + k) * one] : 0.f;
+      q.r[k] = in ? sum[(long long)(j + k) * p.D] : 0.f;
+      q.fresh[k] = in ? fresh[j + k] : 1;
     }
+  };
+  Part q;
+  fetch(0, q);
+  for (int j = 0; j < p.segs - 1; j += U) {
+    Part next;
+    fetch(j + U, next);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       if (j + k >= p.segs - 1) break;
       if (j + k > 0) st[(j + k) * one] = h;
-      h = f[k] == 0.f ? l[k] : fmaf(f[k], h, l[k]);
+      const float f = q.fresh[k] ? 0.f : ex2(A * q.r[k]);
+      h = f == 0.f ? q.l[k] : fmaf(f, h, q.l[k]);
     }
+    q = next;
   }
   st[(p.segs - 1) * one] = h;
 }

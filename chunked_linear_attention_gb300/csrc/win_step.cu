@@ -10,7 +10,7 @@
 // row is taken from its inputs, never from the place that is being written.
 //
 // Bound by HBM: keys and values once.  250 rows, 32 query heads on 8 key heads of 128,
-// 2048 + 4 places, bf16: 303 us, 6.9 TB/s; fp32 with 64 rows 217 us, 5.0 TB/s.
+// 2048 + 4 places, bf16: 303 us, 6.9 TB/s; fp32 with 64 rows 195 us, 5.5 TB/s.
 #include <cooperative_groups.h>
 
 #include "mixers.cuh"
@@ -146,12 +146,14 @@ __device__ __forceinline__ void step_join(const WinStepParams& p, const StepRowT
   cl.sync();   // no block ends while another reads from it
 }
 
+// Two blocks on an SM: with four query heads and four keys of a lane on their way the registers
+// are for one, and 64 rows of fp32 as above take 217 us; two keys and two blocks 195.
 template <typename T, int DP, int G, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32) window_step_kernel(
+__global__ void __launch_bounds__(kWarps * 32, 2) window_step_kernel(
     const __grid_constant__ WinStepParams p) {
   constexpr int LPK = DP / 8;        // lanes per key
   constexpr int KPW = 32 / LPK;      // keys a warp reads at once
-  constexpr int U = 4;               // keys of a lane on their way together
+  constexpr int U = G == 4 ? 2 : 4;  // keys of a lane on their way together
   __shared__ float acc_s[kWarps][G][DP];
   __shared__ float m_s[kWarps][G], l_s[kWarps][G];
   __shared__ float acc_b[G][DP], m_b[G], l_b[G];   // of this block
