@@ -556,15 +556,16 @@ ScanShape scan_shape(int B, int N, int D, int S, int G) {
   while (s.spt * s.lanes < S) s.lanes *= 2;
   const int ch = kScanThreads / s.lanes * s.cpt;
   s.blocks = (D / G + ch - 1) / ch;
-  // One round of CTAs, two on every SM.  The carry costs 2/3 of an output pass, so that two
-  // segments of half the length pay already (25 sequences of 8000 x 1536: 2457 us, whole
-  // 2697).  No segment shorter than 32 tokens (1024 tokens of 2048 channels 49 us; 64: 59,
-  // 128: 95).
+  // One round of CTAs, two on every SM, and segments of whole tiles.  The carry costs 2/3 of an
+  // output pass, so that two segments of half the length pay already (25 sequences of 8000 x
+  // 1536: 2457 us, whole 2697), but for the launches and the join: 64 tokens of 512 channels
+  // 9.1 us in four segments, 8.9 whole and in one launch; 128 tokens 9.5 and 15.7; 192 tokens
+  // of 4096 channels 27.4 in two, 26.6 whole, 256 34.0 and 34.5.
   const long long ctas = (long long)B * G * s.blocks, room = 2 * kScanSms;
   long long segs = room / ctas;
-  const long long most = (N + 31) / 32;
+  const long long most = (N + 15) / 16;
   if (segs > most) segs = most;
-  if (segs < 1) segs = 1;
+  if (segs < 1 || N < 96 || (segs == 2 && N < 256)) segs = 1;
   s.seg_tokens = (int)(((N + segs - 1) / segs + 15) / 16 * 16);   // whole tiles
   s.segs = (N + s.seg_tokens - 1) / s.seg_tokens;
   return s;
