@@ -10,7 +10,7 @@
 // log2(e) each element of the state costs one base-2 exponential and four fp32 operations,
 // issued in pairs.
 //
-// What bounds it: issue.  2 x 32768 tokens of 1536 x 16, bf16: 838 us, the carry 1/3 of them;
+// What bounds it: issue.  2 x 32768 tokens of 1536 x 16, bf16: 828 us, the carry 330 of them;
 // the exponentials of both passes alone would take 344 us (32 a clock and SM), the bytes of
 // the output pass 119.  A (token, channel) takes 84 lane-instructions of the carry and 124 of
 // the outputs, and 62% of the clocks issue one a scheduler.
