@@ -180,8 +180,8 @@ __device__ __forceinline__ bool win_next(const WinParams& p, WinList<KT>& w, Win
     while (w.place < w.c.count) {
       const int base = w.place;
       w.place += KT;
-      // tiles that no query sees are left out (24 sequences of 20011 tokens, each with a past
-      // and a window of 1000: 244 us, all tiles of a ring that the first query sees 301)
+      // tiles that no query sees are left out (24 sequences of 20011 tokens, three quarters of
+      // them with a past, and a window of 1000: 219 us, all tiles of a seen ring 231)
       if (base < sinks || (base < head && base + KT > w.fresh) || base + KT > w.old) {
         t.seq = w.c.seq;
         t.base = base;

@@ -15,9 +15,10 @@
 // for one another (2 x 32768 tokens of 12 heads of 128 on 4 key heads, window 2048: 800 us,
 // with a product warp for both query tiles 764); of 64 with one product warp 1080 (2780 clocks
 // an entry of its own instructions), with one a query tile 780 - 795, and the packed and
-// ragged prompts gain 9% from the smaller tiles.
+// ragged prompts gain 9% from the smaller tiles.  With the rows' products and sums in the packed
+// fp32 instructions 761 (heads of 64: 615, without 662).
 //
-// What bounds it: 2 x 32768 tokens as above run at 1.05 PFLOP/s, 54% of the tensor cores'
+// What bounds it: 2 x 32768 tokens as above run at 1.09 PFLOP/s, 56% of the tensor cores'
 // measured rate.  Per pair of query tiles and 64 keys the products take 1280 clocks (S 384
 // each, N 64 being bound by the operands' shared memory, and O 256) and the exponentials 512
 // (32 a clock); the rest are the hand-overs and the rows' other instructions: scores from TMEM
@@ -657,25 +658,31 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
         }
         ++ns;
         begun = true;
-        float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
+        F2 sum0 = pack2(0.f, 0.f), sum1 = sum0;
         const float mc = m == -INFINITY ? 0.f : m * c;
+        const F2 cc = pack2(c, c), mm = pack2(-mc, -mc);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           uint32_t pw[16];
 #pragma unroll
           for (int y = 0; y < 32; y += 4) {
-            const float v0 = ex2(fmaf(s[x][y], c, -mc)), v1 = ex2(fmaf(s[x][y + 1], c, -mc));
-            const float v2 = ex2(fmaf(s[x][y + 2], c, -mc)), v3 = ex2(fmaf(s[x][y + 3], c, -mc));
-            sum0 += v0;
-            sum1 += v1;
-            sum2 += v2;
-            sum3 += v3;
+            float v0, v1, v2, v3;
+            unpack2(fma2(pack2(s[x][y], s[x][y + 1]), cc, mm), v0, v1);
+            unpack2(fma2(pack2(s[x][y + 2], s[x][y + 3]), cc, mm), v2, v3);
+            v0 = ex2(v0);
+            v1 = ex2(v1);
+            v2 = ex2(v2);
+            v3 = ex2(v3);
+            sum0 = add2(sum0, pack2(v0, v1));
+            sum1 = add2(sum1, pack2(v2, v3));
             pw[y / 2] = bf16_pair(v0, v1);
             pw[y / 2 + 1] = bf16_pair(v2, v3);
           }
           tmem_st16(Sb + 16 * x, pw);
         }
-        l += (sum0 + sum1) + (sum2 + sum3);
+        float l0, l1;
+        unpack2(add2(sum0, sum1), l0, l1);
+        l += l0 + l1;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
