@@ -112,3 +112,33 @@ def test_conv_step_bad_slots(dtype):
     assert (got[[b for b in range(n) if b not in good]] == 0).all()
     rest = [i for i in range(pool) if i not in at]
     assert torch.equal(st[rest].cpu(), state[rest])
+
+
+@TYPES
+@pytest.mark.parametrize("window, sinks", [(300, 5), (64, 0), (129, 70)], ids=str)
+def test_attention_ring_tiles(window, sinks, dtype):
+    """Sequences longer than the window behind pasts that end anywhere in the ring: which of
+    the cache's tiles a query tile leaves out."""
+    places = window + sinks
+    pasts = [1, max(1, sinks), sinks + 1, places - 1, places, places + 1, places + 70,
+             2 * window + sinks, 5 * places + 33, 0]
+    lengths = [90, 400, 1, 333, 260, 128, 257, 500, 64, 77]
+    starts = [0] + np.cumsum(lengths).tolist()
+    t = M.qkv(67, 1, 4, 2, starts[-1], 64, dtype)
+    r = M.gen(68)
+    caches = [r(len(pasts), 2, places, 64).to(dtype) for _ in range(2)]
+    for x in caches:   # what holds nothing yet
+        for s, past in enumerate(pasts):
+            x[s, :, min(past, places):] = float("nan")
+    cla, slots = lib(), list(range(len(pasts)))
+    dev, oracle = [x.to(M.DEV) for x in caches], [f64(x) for x in caches]
+    got = cla.window_attention_forward(*[x.to(M.DEV) for x in t], window, sinks, cache_k=dev[0],
+                                       cache_v=dev[1], slots=M.ints(slots), past=M.ints(pasts),
+                                       seq_starts=M.ints(starts))
+    torch.cuda.synchronize()
+    assert cla.device_status() == 0
+    ref, bound = MO.window_attention(*[f64(x) for x in t], window, sinks, None, oracle, slots, pasts,
+                                     starts, M.rounding(dtype, 64))
+    M.within(got, ref, bound, dtype)
+    for x, y in zip(dev, oracle):   # places that still hold nothing are NaN on both sides
+        assert np.array_equal(f64(x), y, equal_nan=True)
