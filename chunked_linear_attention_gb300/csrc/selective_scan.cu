@@ -492,6 +492,18 @@ __global__ void __launch_bounds__(2 * kScanThreads, CPT == 1 ? 3 : 2) selective_
   }
 }
 
+// A state h behind a segment that makes it 2^e h + l.  What is NaN or infinite stays, and 0 stays
+// 0 whatever the growth, as token by token.  Where 2^e is no normal number (|e| above 126), 2^e h
+// may be one: h then takes a quarter of e at a time, which covers all factors that lead from an
+// fp32 number to one (|e| up to 277).
+__device__ __forceinline__ float behind_segment(float h, float e, float l) {
+  if (fabsf(e) <= 126.f) return fmaf(ex2(e), h, l);
+  if (h == 0.f) return l;
+  if (isinf(h)) return h + l;
+  const float f = ex2(0.25f * e);
+  return fmaf(h * f * f * f, f, l);
+}
+
 // The start states of the segments 1, 2, ..: one thread per number of the state.
 __global__ void __launch_bounds__(256) scan_join_kernel(const __grid_constant__ ScanParams p) {
   pdl_launch_dependents();
@@ -528,8 +540,7 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const __grid_constant__ 
     for (int k = 0; k < U; ++k) {
       if (j + k >= p.segs - 1) break;
       if (j + k > 0) st[(j + k) * one] = h;
-      const float f = q.fresh[k] ? 0.f : ex2(A * q.r[k]);
-      h = f == 0.f ? q.l[k] : fmaf(f, h, q.l[k]);
+      h = q.fresh[k] ? q.l[k] : behind_segment(h, A * q.r[k], q.l[k]);
     }
     q = next;
   }

@@ -150,8 +150,12 @@ size_t selective_scan_workspace_size(int B, int N, int D, int S, int G, int n_se
  *   workspace   at least selective_scan_workspace_size() bytes, 256-byte aligned,
  *               not shared with a concurrent call.
  *
- * Computed in fp32 for both I/O types.  Supported: S <= 128, D <= 32768,
- * B <= 65535, N at most 2^30, B * N below 2^31, n_seq at most 2^20. */
+ * Computed in fp32 for both I/O types.  A state that is NaN or infinite stays so
+ * until its sequence ends.  The factor exp(r A) of one token is an fp32 number:
+ * positive r A above 88 makes it infinite, and a state of 0 NaN; over many
+ * tokens states may grow and shrink by more, as far as they are fp32 numbers.
+ * Supported: S <= 128, D <= 32768, B <= 65535, N at most 2^30, B * N below 2^31,
+ * n_seq at most 2^20. */
 int selective_scan_forward(const void* x, const void* dt, const float* A, const void* Bm,
                            const void* Cm, const float* Dx, const float* dt_bias, const void* z,
                            const float* state_in, const int* seq_starts, int n_seq, int B, int N,
