@@ -34,7 +34,8 @@ def alike(got, ref, bound, dtype):
     inf = np.isinf(ref)
     assert np.array_equal(np.isinf(got), inf) and np.array_equal(got[inf], ref[inf])
     held = np.isfinite(ref)
-    off = np.abs(got - ref)[held] - (bound + M.HALF[dtype] * (np.abs(ref) + bound))[held]
+    got, ref, bound = got[held], ref[held], bound[held]
+    off = np.abs(got - ref) - (bound + M.HALF[dtype] * (np.abs(ref) + bound))
     assert off.size == 0 or off.max() <= 1e-38, off.max()
 
 
