@@ -25,8 +25,9 @@
 // and weights into it, maxima, sums, conversions.
 //
 // A value that a query does not see still meets its weight 0 in P V, where NaN or
-// infinity would spoil the row.  So outputs that are not finite are computed again, from
-// the keys that the row sees alone (which leaves what is really NaN or infinite).
+// infinity would spoil the row.  So rows with outputs that are not finite are made again, in
+// fp32, from the keys that they see alone (which leaves what is really NaN or infinite): by all
+// the block's warps, behind its last item, when no role waits for another.
 //
 // Roles (384 threads, one block per SM, persistent over (tile pair, head)):
 //   warp 0      TMA: Q, and K and V of a key tile together through a ring.
@@ -39,7 +40,7 @@
 
 #include "builder.h"
 #include "prof.h"
-#include "win_attn.cuh"
+#include "win_rows.cuh"
 
 namespace ttt {
 
@@ -88,6 +89,8 @@ struct Bars {
   uint64_t pv_done[2], o_full[2], o_free[2];
   uint64_t done[2];
   uint32_t tmem;
+  int spoiled;   // a row has outputs that are not finite
+  int failed;    // a wait ran out
   alignas(16) Entry entry[kEntries];
 };
 static_assert(sizeof(Bars) <= 1024, "control region");
@@ -198,73 +201,6 @@ __device__ __forceinline__ uint32_t span_bits(int x0, int x1, int at) {
   return (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
 }
 
-// One row again, from what it sees alone, by a whole warp: lanes share the keys, then the
-// output's columns.
-__device__ __noinline__ void row_alone(const TcParams& tp, int b, int h, int i0, int i) {
-  const WinParams& p = tp.w;
-  const int lane = threadIdx.x & 31, hk = h / (p.Hq / p.Hk);
-  using T = __nv_bfloat16;
-  const T* q = static_cast<const T*>(p.q) + b * p.lay.q.batch + h * p.lay.q.head + i * p.lay.q.token;
-  const T* k = static_cast<const T*>(p.k) + b * p.lay.k.batch + hk * p.lay.k.head;
-  const T* v = static_cast<const T*>(p.v) + b * p.lay.v.batch + hk * p.lay.v.head;
-  T* out = static_cast<T*>(p.out) + b * p.lay.out.batch + h * p.lay.out.head + i * p.lay.out.token;
-  bool fine = true;
-  for (int c = lane; c < p.d; c += 32) fine = fine && isfinite(to_f<T>(q[c]));
-  if (!__all_sync(0xffffffffu, fine)) {   // every score is NaN or infinite
-    for (int c = lane; c < p.d; c += 32) out[c] = from_f<T>(NAN);
-    return;
-  }
-  const WinRow row = win_row(p, b, i);
-  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  WinList<kKeys> w = win_list<kKeys>(p, b, i0, i0 + 2 * kM);
-  WinTile t;
-  while (win_next(p, w, t)) {
-    const T *ks = k, *vs = v;
-    long long sk = p.lay.k.token, sv = p.lay.v.token;
-    if (t.seq >= 0) {
-      const long long at = ((long long)t.c.slot * p.Hk + hk) * (p.sinks + p.window) * p.d;
-      ks = static_cast<const T*>(p.cache_k) + at;
-      vs = static_cast<const T*>(p.cache_v) + at;
-      sk = sv = p.d;
-    }
-    for (int j0 = t.base; j0 < min(t.base + kKeys, t.end); j0 += 32) {
-      const int j = j0 + lane;
-      const bool in = j >= 0 && j < t.base + kKeys && j < t.end &&
-                      (t.seq < 0 ? sees_new(row, j, t.end)
-                                 : sees_cache(row, t.c, j, p.sinks, p.window));
-      float s = -INFINITY;
-      if (in) {
-        s = 0.f;
-        for (int c = 0; c < p.d; ++c) s = fmaf(to_f<T>(q[c]), to_f<T>(ks[j * sk + c]), s);
-        s *= p.scale;
-      }
-      float top = s;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn;
-      const float f = ex2(m - base);
-      m = mn;
-      l *= f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] *= f;
-      const float x = in ? ex2(s - base) : 0.f;
-      unsigned seen = __ballot_sync(0xffffffffu, in);
-      while (seen) {
-        const int n = __ffs(seen) - 1;
-        seen &= seen - 1;
-        const float xn = __shfl_sync(0xffffffffu, x, n);
-        l += xn;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (lane + 32 * e < p.d) acc[e] = fmaf(xn, to_f<T>(vs[(j0 + n) * sv + lane + 32 * e]), acc[e]);
-      }
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (lane + 32 * e < p.d) out[lane + 32 * e] = from_f<T>(acc[e] / l);
-}
-
 // The entries, read by a whole warp (by one thread: ALONE).
 template <bool ALONE>
 struct Reader {
@@ -284,6 +220,23 @@ struct Reader {
     ++n;
   }
 };
+
+// The spoiled rows of the block's items again.
+template <int DP>
+__device__ __noinline__ void mend_rows(const TcParams& tp, uint8_t* smem) {
+  static_assert(simt_smem<DP, kM>() <= 2 * Plan<DP>::kQ + 2 * Plan<DP>::kStages * Plan<DP>::kKv,
+                "in the place of the queries' and keys' tiles");
+  for (unsigned item = blockIdx.x; item < tp.items; item += gridDim.x) {
+    const Item it = get_item(tp, item);
+    for (int t = 0; t < 2; ++t) {
+      const int i0 = it.i0 + t * kM;
+      __syncthreads();
+      if (i0 < tp.w.N)
+        window_rows<__nv_bfloat16, DP, kM, true, kThreads / 32, true>(
+            tp.w, it.b, it.h, i0, reinterpret_cast<float*>(smem));
+    }
+  }
+}
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_constant__ TcParams tp) {
@@ -321,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
     }
     mbar_init(&B->done[0], 1);
     mbar_init(&B->done[1], 1);
+    B->spoiled = B->failed = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -376,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
         if (e.flags & kStop) break;
       }
       if (!ok) {   // what is on its way lands before the block ends
+        B->failed = 1;
         if (q_loads) wait_one(&B->q_full, (q_loads - 1) & 1, p.status, lim);
         for (int k = 1; k <= NS && k <= fills; ++k)
           wait_one(&B->full[(fills - k) % NS], ((fills - k) / NS) & 1, p.status, lim);
@@ -475,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
       if (flags & kStop) break;
     }
     if (!ok) {   // the products under way end before their TMEM is given back
+      B->failed = 1;
       umma_commit_w(&B->done[u]);
       wait_all(&B->done[u], 0, p.status, lim);
     }
@@ -541,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
       }
       held.flags |= kLast | kStop;
       put(held);
+      if (!ok) B->failed = 1;
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -749,19 +706,15 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
             }
           }
         }
-        __syncwarp();
-        unsigned again = __ballot_sync(0xffffffffu, live && !fine);
-        while (again) {
-          const int x = __ffs(again) - 1;
-          again &= again - 1;
-          row_alone(tp, ib, ih, i0, first + x);
-        }
+        if (live && !fine) B->spoiled = 1;
       }
       if (e.flags & kStop) break;
     }
+    if (!ok) B->failed = 1;
   }
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  if (B->spoiled && !B->failed) mend_rows<DP>(tp, smem);
 }
 
 std::atomic<int> g_withhold{0};

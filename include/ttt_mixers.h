@@ -78,7 +78,9 @@ typedef struct {
  * tensor cores: scores, their softmax and the sums are fp32, the weights are
  * rounded to bf16 for the product with v.  All other calls run in fp32
  * throughout.  What a token does not see does not reach it, NaN and infinity
- * included.
+ * included; on the tensor cores at the price that rows which share a key tile with
+ * NaN or infinite values are made again in fp32, some forty times as long (places
+ * of a cache that hold nothing are best zero).
  * Supported: d <= 256, Hq * B and Hq * n_seq at most 65535, N at most 2^30, B * N
  * below 2^31, window and sinks at most 2^30, with caches together.  The caches must
  * be 16-byte aligned. */
