@@ -85,17 +85,17 @@ __global__ void __launch_bounds__(256) window_store_kernel(const __grid_constant
     slot = -1;
   }
   if (slot < 0) return;
+  int past = p.past ? p.past[s] : 0;
+  if (past < 0) {
+    if (first && threadIdx.x == 0) report_status(p.status, kStatusBadArg);
+    past = 0;
+  }
   int t0 = 0, t1 = p.N, b = s;
   if (p.starts) {
     t0 = p.starts[s];
     t1 = p.starts[s + 1];
     b = 0;
     if (t0 < 0 || t1 <= t0 || t1 > p.N) return;
-  }
-  int past = p.past ? p.past[s] : 0;
-  if (past < 0) {
-    if (first && threadIdx.x == 0) report_status(p.status, kStatusBadArg);
-    past = 0;
   }
   const long long end = (long long)past + (t1 - t0);
   // positions: sinks among the new ones, then the last of the others
