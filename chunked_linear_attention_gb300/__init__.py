@@ -161,6 +161,10 @@ def _declare(lib):
                  "conv_step"):   # the same calls with their arguments as one packed record
         call = getattr(lib, "ttt_binding_" + name)
         call.restype, call.argtypes = i, [cp]
+    lib.ttt_binding_record_bytes.restype, lib.ttt_binding_record_bytes.argtypes = sz, [i]
+    for which, record in enumerate(_RECORDS):
+        if lib.ttt_binding_record_bytes(which) != record.size:
+            raise RuntimeError(f"{LIB_PATH} does not belong to this binding: build it again")
     lib.ttt_selftest_withhold_delta.restype = None
     lib.ttt_selftest_withhold_delta.argtypes = [i]
     lib.ttt_selftest_withhold_window.restype = None
@@ -698,9 +702,8 @@ def block_norm_forward(y, w: Optional[torch.Tensor] = None,
 
 # ---------------------------------------------------------------- fixed-state mixers
 # Made once per layer and decoded token too: arguments travel as one packed record.
-_pack_window = struct.Struct("@10P12q10if").pack
-_pack_scan = struct.Struct("@13PNP12q8i").pack
-_pack_conv = struct.Struct("@8P4q7i").pack
+_RECORDS = tuple(struct.Struct(x) for x in ("@10P12q10if", "@13PNP12q8i", "@8P4q7i"))
+_pack_window, _pack_scan, _pack_conv = (x.pack for x in _RECORDS)
 _I32 = torch.int32
 
 

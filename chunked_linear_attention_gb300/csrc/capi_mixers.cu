@@ -2,6 +2,7 @@
 // before anything is enqueued, and dispatch.
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 #include <utility>
 
@@ -347,7 +348,8 @@ void ttt_selftest_withhold_window(int what) { ttt::window_attention_withhold(wha
 
 // The Python binding's forms of the calls: their arguments in one record each (a call with
 // 24 arguments through ctypes takes 7 us of the host's time, one with a record 1.5).  The
-// records' fields lie as struct.pack puts them.
+// records' fields lie as struct.pack puts them; the binding compares their sizes when it loads
+// the library (ttt_binding_record_bytes).
 struct WindowRecord {
   const void *q, *k, *v;
   void *cache_k, *cache_v;
@@ -421,6 +423,14 @@ int ttt_binding_conv_forward(const ConvRecord* r) {
 int ttt_binding_conv_step(const ConvRecord* r) {
   return short_conv_step(r->x, r->w, r->bias, r->state_out, r->index, r->n, r->B, r->D, r->W, r->io,
                          r->silu, &r->lay, r->out, r->stream);
+}
+
+// Up to the end of the last field, as struct.pack makes them, of the window attention's (0), the
+// scan's (1) and the convolution's record (2).
+size_t ttt_binding_record_bytes(int which) {
+  if (which == 0) return offsetof(WindowRecord, scale) + sizeof(float);
+  if (which == 1) return offsetof(ScanRecord, softplus) + sizeof(int);
+  return offsetof(ConvRecord, silu) + sizeof(int);
 }
 
 }  // extern "C"
