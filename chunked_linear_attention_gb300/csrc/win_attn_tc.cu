@@ -706,7 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_tc_kernel(const __grid_con
             }
           }
         }
-        if (live && !fine) B->spoiled = 1;
+        // (a row whose weights are NaN, or all 0, is NaN by what it sees: nothing to mend)
+        if (live && !fine && l > 0.f) B->spoiled = 1;
       }
       if (e.flags & kStop) break;
     }
