@@ -663,10 +663,10 @@ struct ScanStepParams {
   selective_scan_layout lay;
 };
 
-// L lanes a channel, each K pieces of four numbers of its state, R rows of the batch a thread;
-// bound by HBM, the states' bytes twice.  250 rows of 4096 x 16: 25 us (131 MB there and
-// back, 5.3 TB/s); 1000 rows, whose states pass the L2, 122 us.  Both what is on its way and
-// the instructions count: the step, the gate, the skip and the sum over the lanes are for a
+// L lanes a channel, each K pieces of four numbers of its state, R rows of the batch a thread.
+// 245 rows of 4096 x 16 over states that pass the L2: 32.5 us, 4.2 TB/s of 6.8, bound by the loads'
+// latency and by issue (55%); with the states of one call in the L2 25 us, 1000 rows 122 us, as
+// below.  Both what is on its way and the instructions count: the step, the gate, the skip and the sum over the lanes are for a
 // channel, so that one piece a lane (four rows a thread: 34 and 174 us) makes them twice as
 // often; two pieces and four rows 29 and 143, four pieces of one lane 32 and 132.  With 64
 // numbers four pieces and one row are ahead (1000 rows of 2048: 192 us, two pieces and two

@@ -8,7 +8,9 @@
 // with m the row's largest score so far.  O and l are only rescaled, in TMEM, when that has
 // grown by more than 8 / c since the last time: until then the weights are at most 2^8 too
 // large, and so are their sums.  P is rounded to bf16 (2^-8 of each weight) as the operand
-// of the second product; l sums what was not rounded.
+// of the second product; l sums what was not rounded.  As pairs hi + lo of bf16 numbers, with
+// twice the second products, outputs are off by 1.7e-3 in the norm where they are by 1.8e-3 now
+// (the outputs' own rounding is 1.7e-3), and the case below takes 1013 us for 770.
 //
 // S lies in two buffers a query tile: while the rows make the weights of one, the products
 // fill the other.  Key tiles of 128 with one buffer leave a tile's products and rows waiting
@@ -16,10 +18,10 @@
 // with a product warp for both query tiles 764); of 64 with one product warp 1080 (2780 clocks
 // an entry of its own instructions), with one a query tile 780 - 795, and the packed and
 // ragged prompts gain 9% from the smaller tiles.  With the rows' products and sums in the packed
-// fp32 instructions 761 (heads of 64: 615, without 662).
+// fp32 instructions 761 (heads of 64: 615, without 662); over inputs that pass the L2 767.
 //
-// What bounds it: 2 x 32768 tokens as above run at 1.09 PFLOP/s, 56% of the tensor cores'
-// measured rate.  Per pair of query tiles and 64 keys the products take 1280 clocks (S 384
+// What bounds it: 2 x 32768 tokens as above run at 1.04 PFLOP/s of visible pairs, 54% of the
+// tensor cores' measured rate.  Per pair of query tiles and 64 keys the products take 1280 clocks (S 384
 // each, N 64 being bound by the operands' shared memory, and O 256) and the exponentials 512
 // (32 a clock); the rest are the hand-overs and the rows' other instructions: scores from TMEM
 // and weights into it, maxima, sums, conversions.

@@ -9,8 +9,8 @@ namespace ttt {
 // holds 8 x 4 scores and 8 rows x DP / 16 columns of the output, with a running maximum and
 // sum of the softmax per row, so that each score is made once.  Bound by the shared memory's
 // words per product (12 for 32, in the scores and, at d 64, in the outputs): two thirds of
-// the fp32 pipe at best.  16384 tokens, 8 heads, window 1024: heads of 64 0.99 ms (35
-// TFLOP/s), of 128 1.93 ms; with 4 x 4 scores a thread (8 words for 16) and every score masked
+// the fp32 pipe at best.  16384 tokens, 8 heads, window 1024: heads of 64 0.97 ms (34
+// TFLOP/s), of 128 1.89 ms; with 4 x 4 scores a thread (8 words for 16) and every score masked
 // by itself 1.36 and 3.21.  2048 tokens with a window of 512 are 256 blocks of few warps: 126
 // us, by 256 threads a block 116.
 constexpr int kKT = 64, kPad = 4;

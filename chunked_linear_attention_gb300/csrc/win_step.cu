@@ -9,8 +9,11 @@
 // at once, DP / 8 lanes a key, 8 dimensions a lane; bf16 goes to the tensor cores, below.  The new token's
 // row is taken from its inputs, never from the place that is being written.
 //
-// Bound by HBM: keys and values once.  250 rows, 32 query heads on 8 key heads of 128,
-// 2048 + 4 places, bf16: 303 us, 6.9 TB/s; fp32 with 64 rows 195 us, 5.5 TB/s.
+// Bound by HBM where a block takes all query heads of its key head, up to eight on the tensor
+// cores and four in fp32: keys and values once.  250 rows, 32 query heads on 8 key heads of 128,
+// 2048 + 4 places, bf16: 303 us, 6.9 TB/s; fp32 with 64 rows 192 us, 5.6 TB/s.  More heads are
+// taken in parts, by neighbouring blocks that each read the cache: fp32 with 64 heads on 8 324
+// us, with 128 565.
 #include <cooperative_groups.h>
 
 #include "mixers.cuh"
@@ -147,7 +150,7 @@ __device__ __forceinline__ void step_join(const WinStepParams& p, const StepRowT
 }
 
 // Two blocks on an SM: with four query heads and four keys of a lane on their way the registers
-// are for one, and 64 rows of fp32 as above take 217 us; two keys and two blocks 195.
+// are for one, and 64 rows of fp32 as above take 217 us; two keys and two blocks 192.
 template <typename T, int DP, int G, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32, 2) window_step_kernel(
     const __grid_constant__ WinStepParams p) {
